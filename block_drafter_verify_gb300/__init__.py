@@ -14,6 +14,9 @@ from .binding import (BF16, C, COMMIT_STATS, FP32, STAGES, DFlashError,
                       dflash_lmhead_topk_shard, dflash_topk_merge_shards,
                       dflash_verify_shard_stats, dflash_verify_shard_decide,
                       dflash_verify_shard_draw, SHARD_STATS, SHARD_PLAN,
+                      dflash_kv_append, dflash_paged_attn,
+                      dflash_paged_attn_workspace_bytes, dflash_sample,
+                      dflash_sample_workspace_bytes,
                       library_path, load)
 
 __all__ = ["BF16", "C", "COMMIT_STATS", "FP32", "STAGES", "DFlashError",
@@ -26,4 +29,6 @@ __all__ = ["BF16", "C", "COMMIT_STATS", "FP32", "STAGES", "DFlashError",
            "dflash_workspace_bytes", "dflash_lmhead_topk_shard",
            "dflash_topk_merge_shards", "dflash_verify_shard_stats",
            "dflash_verify_shard_decide", "dflash_verify_shard_draw",
-           "SHARD_STATS", "SHARD_PLAN", "library_path", "load"]
+           "dflash_kv_append", "dflash_paged_attn",
+           "dflash_paged_attn_workspace_bytes", "dflash_sample",
+           "dflash_sample_workspace_bytes", "SHARD_STATS", "SHARD_PLAN", "library_path", "load"]

@@ -27,7 +27,9 @@ EXPORTS = ("dflash_workspace_bytes", "dflash_lmhead_topk", "dflash_pair_score",
            "dflash_set_wait_limit_ns", "dflash_lmhead_topk_shard",
            "dflash_topk_merge_shards", "dflash_verify_shard_stats",
            "dflash_verify_shard_decide", "dflash_verify_shard_draw",
-           "dflash_check", "dflash_status_string")
+           "dflash_kv_append", "dflash_paged_attn_workspace_bytes",
+           "dflash_paged_attn", "dflash_sample_workspace_bytes",
+           "dflash_sample", "dflash_check", "dflash_status_string")
 STAGES = ("conv", "lmhead", "merge", "pair_score", "walk", "verify",
           "quant")
 
@@ -98,6 +100,14 @@ def load(path: str | None = None):
                                              vp]),
         "dflash_verify_shard_draw": (i32, [vp, vp, vp, vp, i32, i32, i32,
                                            i32, i32, f32, vp, vp, sz, vp]),
+        "dflash_kv_append": (i32, [vp, vp, vp, i64, i64, i64] + [vp] * 5 +
+                             [i32] * 12 + [vp] * 7),
+        "dflash_paged_attn_workspace_bytes": (sz, [i32] * 5),
+        "dflash_paged_attn": (i32, [vp] * 8 + [i32] * 9 +
+                              [f32, i32, vp, vp, vp, sz, vp]),
+        "dflash_sample_workspace_bytes": (sz, [i32, i32]),
+        "dflash_sample": (i32, [vp, i64, i32, vp, vp, vp, vp, vp, i32, i32,
+                                vp, vp, vp, vp, sz, vp]),
         "dflash_check": (i32, [vp]),
         "dflash_status_string": (ctypes.c_char_p, [i32]),
     }
@@ -404,6 +414,153 @@ def dflash_verify_shard_draw(target_shard, plan, topi, q, shard, v0, T,
     _call("dflash_verify_shard_draw", _ptr(target_shard), _ptr(plan),
           _ptr(topi), _ptr(q), int(shard), B, K1 - 1, Vs, int(v0), float(T),
           _ptr(out_tok), _ptr(ws), ws.numel(), _stream(stream))
+
+
+# --------------------------------------------------------------------------
+# the target's side of a cycle
+# --------------------------------------------------------------------------
+def _rows(t, dtype, tail, name):
+    """Pointer and row stride of a [rows, *tail] tensor whose rows are
+    contiguous but may lie apart (a slice of a projection's output)."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if tuple(t.shape[1:]) != tail:
+        raise ValueError(f"{name} must be [rows, {tail}], got "
+                         f"{tuple(t.shape)}")
+    step = 1
+    for n, st in zip(reversed(tail), reversed(t.stride()[1:])):
+        if n != 1 and st != step:
+            raise ValueError(f"rows of {name} must be contiguous")
+        step *= n
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else step
+
+
+def _ptr_of(t, dtype, name):
+    _want(t, dtype, name)
+    return _ptr(t)
+
+
+def _check_cache(k_codes, v_codes, k_scale, v_scale):
+    N, Hkv, page, D = k_codes.shape
+    if v_codes.shape != k_codes.shape:
+        raise ValueError("k_codes and v_codes must have one shape")
+    for t in (k_scale, v_scale):
+        if tuple(t.shape) != (N, Hkv):
+            raise ValueError("scales must be [num_pages, Hkv]")
+    return N, Hkv, page, D
+
+
+def dflash_kv_append(q, k, v, cos, sin, pos, n_new, page_table, k_codes,
+                     v_codes, k_scale, v_scale, q_out, kv_len,
+                     interleaved=False, stream=None):
+    """Rotate q and k by position and append k and v to the cache, in place.
+    q [B*Q,Hq,D] or None, k and v [B*Q,Hkv,D] (rows may lie apart, as parts
+    of one projection's output); cos, sin [max_pos,rot/2] f32 or None (no
+    rotation); pos [B] i32: tokens already committed; n_new [B] i32 or None
+    (Q each); page_table [B,max_pages] i32; k_codes, v_codes
+    [num_pages,Hkv,page,D] u8, k_scale, v_scale [num_pages,Hkv] f32 in/out;
+    q_out [B,Q,Hq,D] and kv_len [B] i32 outputs."""
+    N, Hkv, page, D = _check_cache(k_codes, v_codes, k_scale, v_scale)
+    B, max_pages = page_table.shape
+    rows = k.shape[0]
+    if rows % B or v.shape[0] != rows or pos.numel() != B or (
+            kv_len.numel() != B) or (n_new is not None and
+                                     n_new.numel() != B):
+        raise ValueError("k and v must have B * Q rows; pos, n_new and "
+                         "kv_len B entries")
+    kp, ld_k = _rows(k, k.dtype, (Hkv, D), "k")
+    vp, ld_v = _rows(v, k.dtype, (Hkv, D), "v")
+    qp, ld_q, Hq, qo = None, 0, Hkv, None
+    if q is not None:
+        Hq = q.shape[1]
+        qp, ld_q = _rows(q, k.dtype, (Hq, D), "q")
+        qo = _ptr_of(q_out, k.dtype, "q_out")
+        if q.shape[0] != rows or q_out.numel() != rows * Hq * D:
+            raise ValueError("q and q_out must have B * Q rows")
+    rot = max_pos = 0
+    if cos is not None:
+        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        if sin.shape != cos.shape:
+            raise ValueError("cos and sin must have one shape")
+    i32, f32, u8 = torch.int32, torch.float32, torch.uint8
+    _call("dflash_kv_append", qp, kp, vp, ld_q, ld_k, ld_v,
+          None if cos is None else _ptr_of(cos, f32, "cos"),
+          None if cos is None else _ptr_of(sin, f32, "sin"),
+          _ptr_of(pos, i32, "pos"),
+          None if n_new is None else _ptr_of(n_new, i32, "n_new"),
+          _ptr_of(page_table, i32, "page_table"), B, rows // B, Hq, Hkv, D,
+          rot, int(interleaved), max_pos, page, N, max_pages, _dtype(k), qo,
+          _ptr_of(k_codes, u8, "k_codes"), _ptr_of(v_codes, u8, "v_codes"),
+          _ptr_of(k_scale, f32, "k_scale"), _ptr_of(v_scale, f32, "v_scale"),
+          _ptr_of(kv_len, i32, "kv_len"), _stream(stream))
+
+
+def dflash_paged_attn_workspace_bytes(B, Q, Hq, Hkv, D) -> int:
+    return int(load().dflash_paged_attn_workspace_bytes(B, Q, Hq, Hkv, D))
+
+
+def dflash_paged_attn(q, k_codes, v_codes, k_scale, v_scale, page_table,
+                      kv_len, q_len, scale, out, lse, ws, causal=True,
+                      stream=None):
+    """Attention of q [B,Q,Hq,D] over the cache of dflash_kv_append (kv_len
+    [B] i32 tokens, the new ones included; q_len [B] i32 or None: Q new ones
+    each) into out [B,Q,Hq,D] and lse [B,Q,Hq] f32 (or None); ws uint8 of
+    dflash_paged_attn_workspace_bytes."""
+    N, Hkv, page, D = _check_cache(k_codes, v_codes, k_scale, v_scale)
+    B, Q, Hq, Dq = q.shape
+    if Dq != D or page_table.shape[0] != B or out.shape != q.shape or (
+            kv_len.numel() != B) or (q_len is not None and
+                                     q_len.numel() != B):
+        raise ValueError("q, out, page_table, kv_len, q_len and the cache "
+                         "must agree in B and D")
+    if lse is not None and lse.numel() != B * Q * Hq:
+        raise ValueError("lse must be [B, Q, Hq]")
+    i32, f32, u8 = torch.int32, torch.float32, torch.uint8
+    _call("dflash_paged_attn", _ptr(q), _ptr_of(k_codes, u8, "k_codes"),
+          _ptr_of(v_codes, u8, "v_codes"), _ptr_of(k_scale, f32, "k_scale"),
+          _ptr_of(v_scale, f32, "v_scale"),
+          _ptr_of(page_table, i32, "page_table"),
+          _ptr_of(kv_len, i32, "kv_len"),
+          None if q_len is None else _ptr_of(q_len, i32, "q_len"), B, Q, Hq,
+          Hkv, D, page, N, page_table.shape[1], int(causal), float(scale),
+          _dtype(q), _ptr_of(out, q.dtype, "out"),
+          None if lse is None else _ptr_of(lse, f32, "lse"), _ptr(ws),
+          ws.numel(), _stream(stream))
+
+
+def dflash_sample_workspace_bytes(R, V) -> int:
+    return int(load().dflash_sample_workspace_bytes(R, V))
+
+
+def dflash_sample(logits, temperature, top_k, top_p, min_p, u, token, n_kept,
+                  filtered, ws, stream=None):
+    """One token from each row of logits [R,V] (rows may lie apart), with
+    that row's temperature [R] f32, top_k [R] i32, top_p and min_p [R] f32
+    (each None: off) and uniform u [R] f32; token [R] i32, n_kept [R] i32
+    (or None) and filtered [R,V] f32 (or None) outputs; ws uint8 of
+    dflash_sample_workspace_bytes."""
+    R, V = logits.shape
+    lp, ld = _rows(logits, logits.dtype, (V,), "logits")
+    i32, f32 = torch.int32, torch.float32
+
+    def row(t, dtype, name):
+        if t is None:
+            return None
+        if t.numel() != R:
+            raise ValueError(f"{name} must have R entries")
+        return _ptr_of(t, dtype, name)
+
+    if filtered is not None and tuple(filtered.shape) != (R, V):
+        raise ValueError("filtered must be [R, V]")
+    _call("dflash_sample", lp, ld, _dtype(logits),
+          row(temperature, f32, "temperature"), row(top_k, i32, "top_k"),
+          row(top_p, f32, "top_p"), row(min_p, f32, "min_p"),
+          row(u, f32, "u"), R, V, row(token, i32, "token"),
+          row(n_kept, i32, "n_kept"),
+          None if filtered is None else _ptr_of(filtered, f32, "filtered"),
+          _ptr(ws), ws.numel(), _stream(stream))
 
 
 def dflash_check(stream=None):

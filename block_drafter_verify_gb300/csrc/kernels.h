@@ -173,6 +173,39 @@ cudaError_t launch_verify_shard_draw(const float* L, const float* plan,
                                      const VerifyWs& ws, int* err,
                                      cudaStream_t s);
 
+// kv_append.cu, paged_attn.cu ------------------------------------------------
+// Sizes of the paged 8-bit cache and of the rows that go to it.
+inline bool cache_sizes_ok(int B, int Q, int Hq, int Hkv, int D, int page,
+                           int num_pages, int max_pages) {
+  if (B < 1 || Q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq > 4096)
+    return false;
+  if (D < 16 || D > 256 || D % 16 != 0) return false;
+  if (page != 16 && page != 32 && page != 64 && page != 128) return false;
+  if (num_pages < 1 || max_pages < 1) return false;
+  // row counts and a sequence's positions stay within 32 bits
+  return (long long)B * Q <= (1 << 24) &&
+         (long long)max_pages * page <= (1LL << 30) &&
+         (long long)num_pages * Hkv * page <= (1LL << 31) - 1;
+}
+
+// Arguments of the attention kernels (dflash_paged_attn's).
+struct PagedAttnArgs {
+  const void* q;
+  const uint8_t *k_codes, *v_codes;
+  const float *k_scale, *v_scale;
+  const int *table, *kv_len, *q_len;  // q_len may be NULL
+  int B, Q, Hq, Hkv, D, page, num_pages, max_pages, causal;
+  float scale;
+  void* out;
+  float* lse;                         // may be NULL
+  int* err;
+};
+// A length from the device clamped to [0, most]; *bad if it was outside.
+__device__ __forceinline__ int attn_clamp(int x, long long most, bool* bad) {
+  if (x < 0 || x > most) *bad = true;
+  return x < 0 ? 0 : x > most ? (int)most : x;
+}
+
 // philox --------------------------------------------------------------------
 cudaError_t launch_philox(const uint32_t* ctr, uint64_t seed, uint32_t* out,
                           int64_t n, cudaStream_t s);

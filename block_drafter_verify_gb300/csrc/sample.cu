@@ -1,0 +1,609 @@
+// Sampling with temperature, top-k, top-p and min-p from given uniforms, and
+// the filtered logits for the lossless verify.
+//
+// Mathematics.  Tokens are ranked by (logit descending, id ascending); every
+// filter keeps a prefix of that ranking, so together they keep the tokens
+// not below one cut.  The cut is a 64-bit word: the logit's order-preserving
+// 32-bit key over the complement of the id.  Weights are 64-bit integers
+// floor(exp(.) 2^44): their sums are exact, so the cut, the totals and the
+// drawn token do not depend on how the row is split over threads and CTAs.
+//
+// A cluster of CTAs owns a row: each CTA reads its slice from HBM once and
+// keeps it in shared memory, where all later passes run; only histograms,
+// short lists and sums travel between the CTAs (distributed shared memory).
+//   1 load the slice, its largest (key, id); cluster maximum
+//   2 weights: total, and (filters on) a histogram of counts and weights over
+//     bins of (max - l) / T
+//   3 top-k: the bin of the k-th token; its members gathered and ranked
+//   4 top-p: the bin in which the weight passes p W; likewise
+//   5 kept weights by warp chunk, in id order; the draw; filtered logits
+// A bin with more members than the list holds (ties by the thousand, a tail
+// of weightless tokens) is resolved by radix selection on the 64-bit words
+// instead.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "kernels.h"
+
+namespace dflash {
+
+// SM count and device error word of the current device (api.cu).
+dflash_status current_device_info(int* sms, int** err);
+
+namespace {
+
+namespace cg = cooperative_groups;
+using u64 = unsigned long long;
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 1024;
+constexpr float kBinsPerUnit = 32.f;   // bins of 1/32 in (max - l) / T
+constexpr int kList = 512;             // members of one bin, over the cluster
+constexpr int kMaxCluster = 8;
+constexpr float kWeightOne = 17592186044416.f;  // 2^44
+
+struct SampleArgs {
+  const void* logits;
+  long long ld;
+  const float* temperature;
+  const int* top_k;
+  const float *top_p, *min_p, *u;
+  int R, V, slice;   // slice: tokens per CTA, a multiple of 8
+  int resident;      // the slice fits in shared memory
+  int* token;
+  int* n_kept;
+  float* filtered;
+  int* err;
+};
+
+// Order-preserving key of a logit (equal for -0 and 0); 0 is below -inf.
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t w = __float_as_uint(x + 0.f);
+  return w & 0x80000000u ? ~w : w | 0x80000000u;
+}
+__device__ __forceinline__ float of_key(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+constexpr uint32_t kKeyNegInf = 0x007fffffu;  // key_of(-inf)
+
+__device__ __forceinline__ u64 word_of(float x, int id) {
+  return (u64)key_of(x) << 32 | (uint32_t)~id;
+}
+
+template <typename U>
+__device__ __forceinline__ U warp_total(U v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ u64 warp_largest(u64 v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+    v = max(v, (u64)__shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+struct Shared {
+  // written by this CTA, read by the cluster
+  u64 top;               // largest word of the slice
+  u64 total;             // weight of the slice
+  u64 kept_w[kWarps];    // kept weight of each warp's chunk
+  uint32_t kept_n;
+  uint32_t bad;
+  uint32_t count[kBins];
+  uint32_t w_lo[kBins], w_hi[kBins];
+  u64 list[kList];
+  uint32_t listed;
+  // this CTA's own
+  uint32_t all_count[kBins];
+  u64 all_w[kBins];
+  u64 all_list[kList];
+  u64 scan_w[kWarps + 1];
+  uint32_t scan_n[kWarps + 1];
+  u64 warp_w[kWarps];
+  uint32_t warp_n[kWarps];
+  int found_bin;
+  u64 found_w;           // weight before the found bin
+  uint32_t found_n;      // tokens before it
+  u64 cut;
+  u64 kept_before;       // weight of the tokens down to the cut
+};
+
+// What a row's weights are made from.
+struct Row {
+  float top, inv_t;
+  bool greedy;
+};
+__device__ __forceinline__ float x_of(float l, const Row& r) {
+  if (l == r.top) return 1.f;
+  if (r.greedy) return 0.f;
+  return expf(__fmul_rn(__fsub_rn(l, r.top), r.inv_t));
+}
+__device__ __forceinline__ u64 weight_of(float x) {
+  return __float2ull_rz(__fmul_rn(x, kWeightOne));
+}
+// Bin of a logit: 0 at the maximum, rising as it falls; monotone in l.
+__device__ __forceinline__ int bin_of(float l, const Row& r) {
+  if (l == r.top) return 0;
+  const float z = __fmul_rn(__fmul_rn(__fsub_rn(r.top, l), r.inv_t),
+                            kBinsPerUnit);
+  return z < (float)(kBins - 1) ? (int)z : kBins - 1;
+}
+
+__device__ __forceinline__ void add_weight(Shared& S, int bin, u64 w) {
+  const uint32_t lo = (uint32_t)w, hi = (uint32_t)(w >> 32);
+  const uint32_t old = atomicAdd(&S.w_lo[bin], lo);
+  const uint32_t up = hi + (old + lo < old ? 1u : 0u);
+  if (up) atomicAdd(&S.w_hi[bin], up);
+}
+
+// Sums the cluster's histograms (first n bins) into all_count, all_w of
+// every CTA.  Cluster barriers on both sides: the histograms are complete
+// before, and may be cleared after.
+__device__ void reduce_bins(Shared& S, cg::cluster_group& cl, int n) {
+  cl.sync();
+  const int C = cl.num_blocks();
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    uint32_t c = 0;
+    u64 w = 0;
+    for (int r = 0; r < C; ++r) {
+      const Shared* o = cl.map_shared_rank(&S, r);
+      c += o->count[i];
+      w += (u64)o->w_hi[i] << 32 | 0u;
+      w += o->w_lo[i];
+    }
+    S.all_count[i] = c;
+    S.all_w[i] = w;
+  }
+  cl.sync();
+}
+
+// The first bin at which the running count reaches `need_n` (by_weight
+// false) or the running weight reaches `need_w`; its predecessors' sums.
+// found_bin = -1 if none does.  Whole CTA.
+__device__ void find_bin(Shared& S, int n, bool by_weight, uint32_t need_n,
+                         u64 need_w) {
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int per = (n + kThreads - 1) / kThreads;
+  uint32_t c = 0;
+  u64 w = 0;
+  for (int i = 0; i < per; ++i) {
+    const int bin = tid * per + i;
+    if (bin < n) { c += S.all_count[bin]; w += S.all_w[bin]; }
+  }
+  uint32_t pc = c;
+  u64 pw = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t oc = __shfl_up_sync(0xffffffffu, pc, o);
+    const u64 ow = __shfl_up_sync(0xffffffffu, pw, o);
+    if (lane >= o) { pc += oc; pw += ow; }
+  }
+  if (lane == 31) { S.warp_n[wid] = pc; S.warp_w[wid] = pw; }
+  if (tid == 0) S.found_bin = -1;
+  __syncthreads();
+  for (int i = 0; i < wid; ++i) { pc += S.warp_n[i]; pw += S.warp_w[i]; }
+  pc -= c;
+  pw -= w;
+  for (int i = 0; i < per; ++i) {
+    const int bin = tid * per + i;
+    if (bin >= n) break;
+    const uint32_t nc = pc + S.all_count[bin];
+    const u64 nw = pw + S.all_w[bin];
+    const bool here = by_weight ? pw < need_w && nw >= need_w
+                                : pc < need_n && nc >= need_n;
+    if (here) { S.found_bin = bin; S.found_n = pc; S.found_w = pw; }
+    pc = nc;
+    pw = nw;
+  }
+  __syncthreads();
+}
+
+template <typename T>
+__device__ __forceinline__ float logit_at(const T* data, int i) {
+  return to_f32(data[i]);
+}
+
+// Chunk of the slice that warp `wid` owns in id order: multiples of 128.
+__device__ __forceinline__ void warp_chunk(int n, int wid, int* a, int* b) {
+  const int per = ((n + kWarps - 1) / kWarps + 127) & ~127;
+  *a = min(n, wid * per);
+  *b = min(n, *a + per);
+}
+
+// Generic selection of the cut by radix on the 64-bit words, most
+// significant byte first: the word at which the count reaches need_n (or
+// the preceding weight has not yet reached need_w) over the whole cluster.
+template <typename T>
+__device__ void radix_cut(Shared& S, cg::cluster_group& cl, const T* data,
+                          int n, int id0, const Row& r, bool by_weight,
+                          uint32_t need_n, u64 need_w) {
+  u64 prefix = 0, mask = 0, before_w = 0;
+  uint32_t before_n = 0;
+  for (int shift = 56; shift >= 0; shift -= 8) {
+    for (int i = threadIdx.x; i < 256; i += kThreads)
+      S.count[i] = S.w_lo[i] = S.w_hi[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const float l = logit_at(data, i);
+      if (!(l > -INFINITY)) continue;
+      const u64 w = word_of(l, id0 + i);
+      if ((w & mask) != prefix) continue;
+      const int bin = 255 - (int)(w >> shift & 255);  // larger words first
+      atomicAdd(&S.count[bin], 1u);
+      add_weight(S, bin, weight_of(x_of(l, r)));
+    }
+    reduce_bins(S, cl, 256);
+    find_bin(S, 256, by_weight, by_weight ? 0 : need_n - before_n,
+             by_weight ? need_w - before_w : 0);
+    const int bin = S.found_bin;
+    before_n += S.found_n;
+    before_w += S.found_w;
+    prefix |= (u64)(255 - bin) << shift;
+    mask |= (u64)255 << shift;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    const float l = of_key((uint32_t)(prefix >> 32));
+    S.cut = prefix;
+    S.kept_before = before_w + weight_of(x_of(l, r));
+  }
+  __syncthreads();
+}
+
+// The cut in the found bin of the z histogram: its members gathered over
+// the cluster and ranked, or radix selection if there are too many.
+template <typename T>
+__device__ void bin_cut(Shared& S, cg::cluster_group& cl, const T* data, int n,
+                        int id0, const Row& r, bool by_weight, uint32_t need_n,
+                        u64 need_w) {
+  const int tid = threadIdx.x;
+  const int bin = S.found_bin;
+  const uint32_t members = S.all_count[bin];
+  const uint32_t before_n = S.found_n;
+  const u64 before_w = S.found_w;
+  if (members > kList) {  // uniform over the cluster
+    radix_cut(S, cl, data, n, id0, r, by_weight, need_n, need_w);
+    return;
+  }
+  if (tid == 0) S.listed = 0;
+  __syncthreads();
+  for (int i = tid; i < n; i += kThreads) {
+    const float l = logit_at(data, i);
+    if (l > -INFINITY && bin_of(l, r) == bin)
+      S.list[atomicAdd(&S.listed, 1u)] = word_of(l, id0 + i);
+  }
+  cl.sync();
+  const int C = cl.num_blocks();
+  uint32_t at = 0;
+  for (int c = 0; c < C; ++c) {
+    const Shared* o = cl.map_shared_rank(&S, c);
+    const uint32_t m = o->listed;
+    for (uint32_t i = tid; i < m; i += kThreads) S.all_list[at + i] = o->list[i];
+    at += m;
+  }
+  cl.sync();  // also a barrier of this CTA
+  for (uint32_t i = tid; i < members; i += kThreads) {
+    const u64 w = S.all_list[i];
+    uint32_t rank = before_n;
+    u64 sum = before_w;
+    for (uint32_t j = 0; j < members; ++j) {
+      const u64 o = S.all_list[j];
+      if (o > w) {
+        ++rank;
+        sum += weight_of(x_of(of_key((uint32_t)(o >> 32)), r));
+      }
+    }
+    const u64 own = weight_of(x_of(of_key((uint32_t)(w >> 32)), r));
+    const bool last = by_weight ? sum < need_w && sum + own >= need_w
+                                : rank + 1 == need_n;
+    if (last) { S.cut = w; S.kept_before = sum + own; }
+  }
+  __syncthreads();
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    sample_kernel(const __grid_constant__ SampleArgs a) {
+  cg::cluster_group cl = cg::this_cluster();
+  extern __shared__ uint4 smem16[];
+  Shared& S = *reinterpret_cast<Shared*>(smem16);
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int C = cl.num_blocks(), rank = cl.block_rank();
+  const int row = blockIdx.x / C;
+  const int id0 = rank * a.slice;
+  const int n = max(0, min(a.slice, a.V - id0));
+  const T* src = static_cast<const T*>(a.logits) + row * a.ld + id0;
+  T* own = reinterpret_cast<T*>(smem16 + (sizeof(Shared) + 15) / 16);
+  const T* data = a.resident ? own : src;
+
+  // ---- 1: the slice and the row's maximum --------------------------------
+  if (tid == 0) {
+    S.bad = 0;
+    S.kept_n = 0;
+  }
+  for (int i = tid; i < kBins; i += kThreads)
+    S.count[i] = S.w_lo[i] = S.w_hi[i] = 0;
+  u64 top = 0;
+  bool bad = false;
+  constexpr int E = 16 / sizeof(T);  // elements of a 16-byte load
+  const int off = (int)(reinterpret_cast<uintptr_t>(src) & 15) / (int)sizeof(T);
+  const int lead = min(n, (E - off) % E);  // elements before a 16-byte address
+  auto take = [&](int i, float l) {
+    if (l != l || l == INFINITY) bad = true;
+    if (l == l) top = max(top, word_of(l, id0 + i));
+  };
+  for (int i = tid; i < lead; i += kThreads) {
+    const T x = src[i];
+    if (a.resident) own[i] = x;
+    take(i, to_f32(x));
+  }
+  const int quads = (n - lead) / E;
+#pragma unroll 4
+  for (int v = tid; v < quads; v += kThreads) {
+    const uint4 w = reinterpret_cast<const uint4*>(src + lead)[v];
+    const T* x = reinterpret_cast<const T*>(&w);
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      if (a.resident) own[lead + v * E + k] = x[k];
+      take(lead + v * E + k, to_f32(x[k]));
+    }
+  }
+  for (int i = lead + quads * E + tid; i < n; i += kThreads) {
+    const T x = src[i];
+    if (a.resident) own[i] = x;
+    take(i, to_f32(x));
+  }
+  top = warp_largest(top);
+  if (lane == 0) S.warp_w[wid] = top;
+  __syncthreads();
+  if (bad) S.bad = 1;
+  if (tid == 0) {
+    for (int i = 1; i < kWarps; ++i) top = max(top, S.warp_w[i]);
+    S.top = top;
+  }
+  cl.sync();
+  for (int c = 0; c < C; ++c) top = max(top, cl.map_shared_rank(&S, c)->top);
+  top = warp_largest(top);
+
+  Row r;
+  const float t = a.temperature[row];
+  r.top = of_key((uint32_t)(top >> 32));
+  r.greedy = !(t > 0.f && t < INFINITY);
+  r.inv_t = r.greedy ? 0.f : __fdiv_rn(1.f, t);
+  const bool empty = top >> 32 <= kKeyNegInf;
+  if (tid == 0) {
+    if (S.bad || empty || !(t >= 0.f && t < INFINITY))
+      raise_error(a.err, kErrNonfinite);
+  }
+  const int k = a.top_k ? a.top_k[row] : 0;
+  const float p = a.top_p ? a.top_p[row] : 1.f;
+  const float mp = a.min_p ? a.min_p[row] : 0.f;
+  const bool by_k = !r.greedy && !empty && k > 0 && k < a.V;
+  const bool by_p = !r.greedy && !empty && p < 1.f;
+  u64 cut = empty ? ~0ull : r.greedy ? top : 0;
+
+  // ---- 2-4: the cut --------------------------------------------------------
+  if (by_k || by_p) {  // uniform over the cluster
+    auto fill = [&] {
+      u64 sum = 0;
+      for (int i = tid; i < n; i += kThreads) {
+        const float l = logit_at(data, i);
+        if (!(l > -INFINITY)) continue;
+        const u64 w = weight_of(x_of(l, r));
+        const int bin = bin_of(l, r);
+        sum += w;
+        atomicAdd(&S.count[bin], 1u);
+        add_weight(S, bin, w);
+      }
+      return sum;
+    };
+    bool redo = false;  // a radix selection has overwritten the histogram
+    u64 sum = warp_total(fill());
+    if (lane == 0) S.warp_w[wid] = sum;
+    __syncthreads();
+    if (tid == 0) {
+      for (int i = 1; i < kWarps; ++i) sum += S.warp_w[i];
+      S.total = sum;
+    }
+    reduce_bins(S, cl, kBins);
+    u64 total = 0;
+    for (int c = 0; c < C; ++c) total += cl.map_shared_rank(&S, c)->total;
+    if (by_k) {
+      find_bin(S, kBins, false, (uint32_t)k, 0);
+      if (S.found_bin >= 0) {  // fewer than k tokens above -inf: no cut
+        redo = S.all_count[S.found_bin] > kList;
+        bin_cut(S, cl, data, n, id0, r, false, (uint32_t)k, 0);
+        cut = S.cut;
+        total = S.kept_before;
+        __syncthreads();
+      }
+    }
+    if (by_p) {
+      double need = ceil((double)p * (double)total);
+      const u64 bound = need >= 1.0 ? (u64)need : 1;  // the first is kept
+      // The tokens past the top-k cut may stay in the histogram: bound is at
+      // most the weight before them.
+      if (redo) {
+        for (int i = tid; i < kBins; i += kThreads)
+          S.count[i] = S.w_lo[i] = S.w_hi[i] = 0;
+        __syncthreads();
+        fill();
+        reduce_bins(S, cl, kBins);
+      }
+      find_bin(S, kBins, true, 0, bound);
+      bin_cut(S, cl, data, n, id0, r, true, 0, bound);
+      cut = max(cut, S.cut);
+    }
+  }
+  const bool by_m = !r.greedy && mp > 0.f;
+  auto keeps = [&](float l, int i) {
+    return l > -INFINITY && word_of(l, id0 + i) >= cut &&
+           (!by_m || x_of(l, r) >= mp);
+  };
+
+  // ---- 5: kept weights in id order, the draw, the filtered logits ---------
+  int c0, c1;
+  warp_chunk(n, wid, &c0, &c1);
+  u64 sum = 0;
+  uint32_t cnt = 0;
+  for (int i = c0 + lane; i < c1; i += 32) {
+    const float l = logit_at(data, i);
+    if (keeps(l, i)) {
+      sum += weight_of(x_of(l, r));
+      ++cnt;
+    }
+  }
+  sum = warp_total(sum);
+  cnt = warp_total(cnt);
+  if (lane == 0) {
+    S.kept_w[wid] = sum;
+    if (cnt) atomicAdd(&S.kept_n, cnt);
+  }
+  cl.sync();
+  if (a.filtered) {
+    float* dst = a.filtered + (size_t)row * a.V + id0;
+    for (int i = tid; i < n; i += kThreads) {
+      const float l = logit_at(data, i);
+      dst[i] = keeps(l, i) ? l : -INFINITY;
+    }
+  }
+  if (wid == 0) {
+    // kept weight of every (CTA, warp) chunk in id order: lane handles four
+    constexpr int kPer = kMaxCluster * kWarps / 32;
+    u64 w[kPer], mine = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int at = lane * kPer + j;
+      w[j] = at < C * kWarps
+                 ? cl.map_shared_rank(&S, at / kWarps)->kept_w[at % kWarps]
+                 : 0;
+      mine += w[j];
+    }
+    u64 run = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 v = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += v;
+    }
+    const u64 total = __shfl_sync(0xffffffffu, run, 31);
+    if (rank == 0) {
+      uint32_t nk = lane < C ? cl.map_shared_rank(&S, lane)->kept_n : 0;
+      nk = warp_total(nk);
+      if (lane == 0 && a.n_kept) a.n_kept[row] = (int)nk;
+      if (lane == 0 && total == 0) a.token[row] = -1;
+    }
+    if (total > 0) {
+      const double f = floor((double)a.u[row] * (double)total);
+      u64 target = f > 0.0 ? (u64)f : 0;
+      if (target >= total) target = total - 1;
+      u64 before = run - mine;
+      int hit = -1;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        if (hit < 0 && target >= before && target < before + w[j])
+          hit = lane * kPer + j;
+        if (hit < 0) before += w[j];
+      }
+      const unsigned who = __ballot_sync(0xffffffffu, hit >= 0);
+      const int from = __ffs(who) - 1;
+      hit = __shfl_sync(0xffffffffu, hit, from);
+      before = __shfl_sync(0xffffffffu, before, from);
+      if (hit / kWarps == rank) {  // the chunk is in this CTA's slice
+        warp_chunk(n, hit % kWarps, &c0, &c1);
+        for (int base = c0; base < c1; base += 32) {
+          const int i = base + lane;
+          const float l = i < c1 ? logit_at(data, i) : -INFINITY;
+          u64 v = i < c1 && keeps(l, i) ? weight_of(x_of(l, r)) : 0;
+          const u64 one = v;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const u64 q = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += q;
+          }
+          const bool here = one > 0 && target >= before + v - one &&
+                            target < before + v;
+          if (here) a.token[row] = id0 + i;
+          if (__any_sync(0xffffffffu, here)) break;
+          before += __shfl_sync(0xffffffffu, v, 31);
+        }
+      }
+    }
+  }
+  cl.sync();  // no CTA leaves while another reads its sums
+}
+
+template <typename T>
+cudaError_t launch(SampleArgs a, cudaStream_t s) {
+  // The smallest cluster whose slices take at most 80 KB each, so that two
+  // CTAs fit an SM and one loads while the other works; wider rows take
+  // slices of up to 144 KB in a cluster of eight, still wider ones are read
+  // again from L2 and HBM in every pass.
+  int C = 1;
+  auto bytes = [&](int c) {
+    const long long sl = (((long long)a.V + c - 1) / c + 7) & ~7ll;
+    return sl * (long long)sizeof(T);
+  };
+  while (C < kMaxCluster && bytes(C) > 80 * 1024) C *= 2;
+  a.slice = (int)((((long long)a.V + C - 1) / C + 7) & ~7ll);
+  a.resident = bytes(C) <= 144 * 1024;
+  const size_t smem = (sizeof(Shared) + 15) / 16 * 16 +
+                      (a.resident ? (size_t)a.slice * sizeof(T) : 16);
+  auto* f = sample_kernel<T>;
+  cudaError_t e = cudaFuncSetAttribute(
+      f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  PdlLaunch L(dim3((unsigned)a.R * C), dim3(kThreads), smem, s, C);
+  return cudaLaunchKernelEx(&L.cfg, f, a);
+}
+
+}  // namespace
+}  // namespace dflash
+
+extern "C" {
+
+size_t dflash_sample_workspace_bytes(int R, int V) {
+  if (R < 1 || R > (1 << 24) || V < 1 || V > (1 << 30)) return 0;
+  return 256;
+}
+
+dflash_status dflash_sample(const void* logits, int64_t ld, dflash_dtype dt,
+                            const float* temperature, const int32_t* top_k,
+                            const float* top_p, const float* min_p,
+                            const float* u, int R, int V, int32_t* token,
+                            int32_t* n_kept, float* filtered, void* ws,
+                            size_t ws_bytes, dflash_stream_t stream) {
+  using namespace dflash;
+  if (!(logits && temperature && u && token && ws))
+    return DFLASH_ERR_INVALID_ARG;
+  if (dt != DFLASH_BF16 && dt != DFLASH_FP32) return DFLASH_ERR_INVALID_ARG;
+  const size_t need = dflash_sample_workspace_bytes(R, V);
+  if (need == 0 || ws_bytes < need || ld < V) return DFLASH_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(ws) & 255) return DFLASH_ERR_INVALID_ARG;
+  int sms = 0;
+  SampleArgs a;
+  const dflash_status st = current_device_info(&sms, &a.err);
+  if (st != DFLASH_OK) return st;
+  a.logits = logits;
+  a.ld = ld;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.u = u;
+  a.R = R;
+  a.V = V;
+  a.token = token;
+  a.n_kept = n_kept;
+  a.filtered = filtered;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = dt == DFLASH_FP32 ? launch<float>(a, s)
+                                          : launch<__nv_bfloat16>(a, s);
+  return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
+}
+
+}  // extern "C"

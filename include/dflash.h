@@ -10,7 +10,9 @@
  *   dflash_verify       rejection-sampling verify, residual / bonus draw
  *
  * or two: dflash_draft (the first three in one call, with the context gate
- * computed inside the conv launch) and dflash_verify.
+ * computed inside the conv launch) and dflash_verify.  Where the target model
+ * runs in the same program, dflash_kv_append, dflash_paged_attn and
+ * dflash_sample carry its share of the cycle.
  *
  * Sources (page title, section):
  *   "DFlash 2: Block diffusion, wearing a drafter's coat" — "Sixteen
@@ -500,6 +502,141 @@ dflash_status dflash_verify_shard_draw(const float* target_shard,
                                        int v0, float T, int32_t* out_tok,
                                        void* ws, size_t ws_bytes,
                                        dflash_stream_t s);
+
+/*
+ * The target's side of a cycle: the tokens that go through the target model
+ * before there are target logits.  The pages leave this part to the serving
+ * engine ("Running it" and "Caveats before you rebuild your serving stack",
+ * 2B-drafter page); these three calls are what a draft-verify loop needs
+ * from it: append the block's keys and values to the cache, attend over
+ * that cache with K+1 tokens per sequence, and filter or sample the logits.
+ *
+ * The cache holds keys and values in 8 bits (OCP FP8 E4M3, NaN never
+ * stored by dflash_kv_append) in pages of `page` tokens:
+ *   k_codes, v_codes [num_pages, Hkv, page, D] uint8
+ *   k_scale, v_scale [num_pages, Hkv] fp32: one scale for each page and
+ *                    head, a power of two of at least 2^-64; a cached value
+ *                    is code * scale
+ *   page_table       [B, max_pages] int32: token t of sequence b is slot
+ *                    t mod page of page page_table[b, t / page]
+ * page is 16, 32, 64 or 128; D is a multiple of 16 up to 256; Hq query heads
+ * share Hkv key heads in groups of Hq / Hkv (query head h reads key head
+ * h / (Hq / Hkv)).  Entries of page_table that no token needs are not read.
+ */
+
+/*
+ * dflash_kv_append: rotate q and k by their positions, append k and v to the
+ * cache.  Sequence b gets n = n_new[b] tokens (rows b*Q .. b*Q + n - 1 of q,
+ * k and v) at positions pos[b] .. pos[b] + n - 1; what the cache held from
+ * pos[b] on is overwritten, so the tokens that a verify rejected need no
+ * clearing: append at the committed length.
+ *   rotation of the first `rot` dimensions of every head by the angles whose
+ *   cosines and sines row p of cos_tab, sin_tab [max_pos, rot/2] fp32 holds:
+ *     (a, b) -> (a c - b s, b c + a s), the pairs (a, b) being dimensions
+ *     (j, j + rot/2), or (2j, 2j + 1) if interleaved; in fp32, each product
+ *     and sum rounded; rot = 0 (no tables) leaves q and k as they are
+ *   scale of a page and head: the least power of two s >= 2^-64 with
+ *     max |x| <= 448 s over the page's new tokens, and at least the old
+ *     scale if the page holds tokens before pos[b]; where that raises the
+ *     scale, the codes of those older tokens are rounded anew to it (exact
+ *     but for codes that become subnormal)
+ *   code = E4M3(x / s), nearest with ties to even; x is fp32 here, rounded
+ *     once.
+ *   q [B*Q, Hq, D], k, v [B*Q, Hkv, D] dtype, rows ld_q, ld_k, ld_v elements
+ *     apart (so they can be parts of one projection's output); q may be NULL
+ *     (then Hq and q_out are not used)
+ *   q_out [B, Q, Hq, D] dtype out: q rotated; rows without a token are 0
+ *   kv_len [B] int32 out: pos[b] + n, the length dflash_paged_attn takes;
+ *     must not be pos itself
+ *   n_new [B] int32, or NULL: Q tokens each
+ * Requirements: D % 16 == 0, rot % 8 == 0, rot <= D, rows and pointers of q,
+ * k, v, q_out aligned to four elements, the tables and codes to 16 bytes;
+ * ld >= heads * D; pages that this call writes belong to one sequence each.
+ * On the device: tokens beyond the page table or the angle tables, n_new
+ * outside [0, Q], a negative pos and a page id outside [0, num_pages) set
+ * DFLASH_ERR_BAD_INDEX; such tokens are left out (kv_len counts the tokens
+ * before them).  A NaN k or v sets DFLASH_ERR_NONFINITE and is stored as 0,
+ * an infinite one sets it and is stored as the largest code.
+ */
+dflash_status dflash_kv_append(
+    const void* q, const void* k, const void* v, int64_t ld_q, int64_t ld_k,
+    int64_t ld_v, const float* cos_tab, const float* sin_tab,
+    const int32_t* pos, const int32_t* n_new, const int32_t* page_table,
+    int B, int Q, int Hq, int Hkv, int D, int rot, int interleaved,
+    int max_pos, int page, int num_pages, int max_pages, dflash_dtype dt,
+    void* q_out, uint8_t* k_codes, uint8_t* v_codes, float* k_scale,
+    float* v_scale, int32_t* kv_len, dflash_stream_t s);
+
+/* Workspace of dflash_paged_attn for these sizes in bytes; 0 for invalid
+ * sizes. */
+size_t dflash_paged_attn_workspace_bytes(int B, int Q, int Hq, int Hkv, int D);
+
+/*
+ * dflash_paged_attn: softmax attention of each sequence's last tokens over
+ * its cache.  Query i < q_len[b] of sequence b stands at position
+ * kv_len[b] - q_len[b] + i and sees the cached tokens t
+ *   causal:     t <= its own position (the verify pass, a prompt's chunk)
+ *   not causal: t < kv_len[b] (a drafter's block, which sees all of itself)
+ *   s_t = scale * <q, k_t>,  out = sum_t softmax(s)_t v_t,
+ *   lse = ln sum_t exp(s_t).
+ * A query that sees nothing, and rows i >= q_len[b], give out = 0 and
+ * lse = -inf.
+ *   q, out [B, Q, Hq, D] dtype; lse [B, Q, Hq] fp32 or NULL
+ *   kv_len [B] int32; q_len [B] int32 or NULL (Q each)
+ *   ws >= dflash_paged_attn_workspace_bytes(B, Q, Hq, Hkv, D) bytes, 256-byte
+ *      aligned; its contents need no initialisation
+ * With bf16 storage and D <= 128 the products run on the tensor cores: q is
+ * split exactly into E4M3 parts, the softmax weights into three E4M3 parts
+ * (12 bits; sums and statistics in fp32).  Otherwise fp32 on the CUDA cores.
+ * Codes and slots past kv_len may hold anything.
+ * Requirements: Hq % Hkv == 0, Hq / Hkv <= 64, q, out and the codes 16-byte
+ * aligned; scale finite.  On the device: kv_len below 0 or beyond the page
+ * table, q_len outside [0, Q] and a page id outside [0, num_pages) set
+ * DFLASH_ERR_BAD_INDEX (lengths are clamped, such a page counts as zeros).
+ */
+dflash_status dflash_paged_attn(
+    const void* q, const uint8_t* k_codes, const uint8_t* v_codes,
+    const float* k_scale, const float* v_scale, const int32_t* page_table,
+    const int32_t* kv_len, const int32_t* q_len, int B, int Q, int Hq,
+    int Hkv, int D, int page, int num_pages, int max_pages, int causal,
+    float scale, dflash_dtype dt, void* out, float* lse, void* ws,
+    size_t ws_bytes, dflash_stream_t s);
+
+/* Workspace of dflash_sample for these sizes in bytes; 0 for invalid sizes. */
+size_t dflash_sample_workspace_bytes(int R, int V);
+
+/*
+ * dflash_sample: one token from each of R rows of logits l, with that row's
+ * temperature T, top-k, top-p and min-p, from a given uniform u; and the
+ * filtered logits, on which dflash_verify is lossless for the filtered
+ * target distribution ("Lossless, with conditions I did not used to state",
+ * drafter's coat page).  Tokens are ranked by l descending, id ascending:
+ *   x_v = exp((l_v - max l) * (1 / T)) in fp32 (1 at the maximum),
+ *   w_v = floor(x_v 2^44), a 64-bit integer: sums of weights are exact, so
+ *         neither their order nor the launch shape can change a result
+ *   top-k (0 < k): the first k tokens
+ *   top-p (p < 1): of those (total weight W), the tokens whose preceding
+ *         tokens weigh less than ceil(p W) (products in fp64); never none
+ *   min-p (0 < m): of those, the tokens with x_v >= m
+ *   token = the smallest id whose running kept weight, in id order, exceeds
+ *         floor(u W'), W' the kept tokens' weight.
+ * T = 0 keeps the first maximum only.
+ *   logits [R, V] dtype, rows ld elements apart; temperature [R] fp32;
+ *   top_k [R] int32, top_p, min_p [R] fp32: each may be NULL (filter off);
+ *   u [R] fp32 in [0, 1)
+ *   token [R] int32 out; n_kept [R] int32 out or NULL: tokens kept;
+ *   filtered [R, V] fp32 out or NULL: l_v if kept, else -inf
+ *   ws >= dflash_sample_workspace_bytes(R, V) bytes, 256-byte aligned
+ * Requirements: R >= 1, V >= 1, ld >= V.  A NaN (left out) or +inf logit
+ * sets DFLASH_ERR_NONFINITE, as does a row with no logit above -inf (token
+ * -1, n_kept 0) or a T that is negative or not finite (taken as 0).
+ */
+dflash_status dflash_sample(const void* logits, int64_t ld, dflash_dtype dt,
+                            const float* temperature, const int32_t* top_k,
+                            const float* top_p, const float* min_p,
+                            const float* u, int R, int V, int32_t* token,
+                            int32_t* n_kept, float* filtered, void* ws,
+                            size_t ws_bytes, dflash_stream_t s);
 
 /* Philox4x32-10 of n counters (ctr [n, 4] uint32, device) under key
  * (seed lo, seed hi) into out [n, 4] uint32 (device): the generator the

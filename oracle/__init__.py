@@ -4,7 +4,7 @@ Only tests/, ``__graft_entry__.smoke()`` and the CPU-baseline / reference
 legs of ``bench.py`` may import this package.  The product path (the CUDA
 library and its Python binding) never does.
 """
-from . import philox
+from . import philox, target_ops
 from .dflash_oracle import (C, E4M3_MAX, commit, conv2tap,
                             dequantize_e4m3_rows, dequantize_nvfp4_rows,
                             draft_verify_cycle, e2m1_decode, e2m1_encode,
@@ -16,7 +16,7 @@ from .dflash_oracle import (C, E4M3_MAX, commit, conv2tap,
                             round_bf16, to_storage,
                             top16_recall, verify)
 
-__all__ = ["philox", "C", "E4M3_MAX", "commit", "conv2tap",
+__all__ = ["philox", "target_ops", "C", "E4M3_MAX", "commit", "conv2tap",
            "dequantize_e4m3_rows", "dequantize_nvfp4_rows",
            "draft_verify_cycle", "e2m1_decode", "e2m1_encode", "e4m3_decode",
            "e4m3_encode", "gate", "lmhead_topk", "lmhead_topk_e4m3",
