@@ -200,6 +200,11 @@ struct PagedAttnArgs {
   float* lse;                         // may be NULL
   int* err;
 };
+// paged_attn_tc.cu: the tensor-core kernels.
+bool paged_attn_tc_takes(int D, dflash_dtype dt);
+size_t paged_attn_tc_ws(int B, int Q, int Hq, int Hkv);
+cudaError_t launch_paged_attn_tc(const PagedAttnArgs& a, int sms, float* part,
+                                 cudaStream_t s);
 // A length from the device clamped to [0, most]; *bad if it was outside.
 __device__ __forceinline__ int attn_clamp(int x, long long most, bool* bad) {
   if (x < 0 || x > most) *bad = true;

@@ -325,7 +325,11 @@ size_t dflash_paged_attn_workspace_bytes(int B, int Q, int Hq, int Hkv,
                                          int D) {
   using namespace dflash;
   if (!attn_sizes_ok(B, Q, Hq, Hkv, D)) return 0;
-  return (simt_ws(B, Q, Hq, Hkv, D) + 255) & ~(size_t)255;
+  // an upper bound over both dtypes
+  size_t need = simt_ws(B, Q, Hq, Hkv, D);
+  if (paged_attn_tc_takes(D, DFLASH_BF16))
+    need = std::max(need, paged_attn_tc_ws(B, Q, Hq, Hkv));
+  return (need + 255) & ~(size_t)255;
 }
 
 dflash_status dflash_paged_attn(
@@ -375,7 +379,9 @@ dflash_status dflash_paged_attn(
   a.lse = lse;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e =
-      dt == DFLASH_FP32
+      paged_attn_tc_takes(D, dt)
+          ? launch_paged_attn_tc(a, sms, static_cast<float*>(ws), s)
+      : dt == DFLASH_FP32
           ? launch_simt_d<float>(a, static_cast<float*>(ws), s)
           : launch_simt_d<__nv_bfloat16>(a, static_cast<float*>(ws), s);
   return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;

@@ -244,7 +244,7 @@ def _check_attn(dtype, D, n, out, lse, ref):
     tol = (2 * d + 8 * U + n * U + extra)[..., None] * absv + 1e-30
     if dtype == "bf16":
         tol = tol + 2.0 ** -8 * np.abs(o)
-    bad = np.abs(got - o) > tol
+    bad = ~(np.abs(got - o) <= tol)          # a NaN is bad
     assert not bad.any(), (np.abs(got - o)[bad].max(), int(bad.sum()))
     if lse is not None:
         g = np_(lse).astype(np.float64)
