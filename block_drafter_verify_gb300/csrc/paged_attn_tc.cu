@@ -7,10 +7,12 @@
 //   q    is scaled per row by a power of two and written as the sum of two
 //        E4M3 numbers (8 bits, all that bf16 has); both products accumulate
 //        into the same scores;
-//   P    the softmax weights, rounded to fp16 (11 bits), are written as three
-//        E4M3 numbers hi + mid / 16 + lo / 256, each with its own fp32
-//        accumulator, so small weights keep bits below the range of one
-//        E4M3 number.
+//   P    the softmax weights, rounded to fp16 (11 bits), are written as the
+//        sum of four E5M2 numbers.  E5M2 is the upper byte of fp16, so a part
+//        is cut off with a mask and the rest is an exact fp16 difference: no
+//        conversion instructions (four to a cycle and SM quarter; three E4M3
+//        parts made by them took 1200 cycles a tile of 80 rows), and no part
+//        needs a scale of its own.
 // Scores are computed transposed: S^T[token, row] = K q^T and
 // O^T[dim, row] = V^T P^T, so that the 128 lanes of an MMA are always full
 // (tokens, then dimensions) and the number of (query, head) rows, a multiple
@@ -23,7 +25,7 @@
 //   operand with N contiguous.
 // The running maximum is lazy: weights are taken against a reference that is
 // raised (and the accumulators rescaled, by an exact power of two) only when
-// a token beats it by more than 2^4.75; the pieces have room for that.
+// a token beats it by more than 2^5.75; fp16 has room for that.
 //
 // Work is split by tiles of 128 tokens: all tiles of all (sequence, key head,
 // row tile) units are numbered, and each CTA (one per SM) takes an equal run
@@ -31,8 +33,8 @@
 // sums that a second launch joins.
 //
 // Warps: 0 copies tiles (TMA, one box per page), 1 issues the MMAs, 2-3 lay
-// out q, 4-11 do the softmax (two warps per lane quarter, half of the rows
-// each) and write the output.  Every wait is bounded; on a timeout the CTA
+// out q, the others do the softmax (groups of four, one per lane quarter; a
+// group has 8 or 16 rows) and write the output.  Every wait is bounded; on a timeout the CTA
 // stops issuing, drains, frees TMEM and flags the error word.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -48,25 +50,36 @@ namespace {
 constexpr int kTile = 128;         // tokens of a tile, lanes of an MMA
 constexpr int kMaxRows = 96;       // (query, head) rows of a unit
 constexpr int kMaxCtas = 160;
-constexpr int kThreads = 384;
 constexpr int kUnitBytes = kTile * 128;  // a K or V tile in shared memory
-constexpr int kSoftWarps = 8;
+constexpr int kStages = 6;         // most stages of a K and a V tile
+constexpr int kLens = 128;         // sequences whose lengths are kept on chip
 constexpr uint64_t kWait = 2000000000ull;  // 2 s
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kHead = 4.f;       // weights are 2^(score - ref + kHead)
-constexpr float kRaise = 8.75f;    // 2^8.75 = 430 < 448
+constexpr float kHead = 10.f;      // weights are 2^(score - ref + kHead)
+constexpr float kRaise = 15.75f;   // 2^15.75 = 55109 < 57344, E5M2's largest
+constexpr int kParts = 4;          // E5M2 parts of a weight
 
 // Shared-memory plan for N rows.
 template <int N>
 struct Plan {
   static constexpr int Q = 2 * 2 * N * 128;       // two buffers, two parts
-  static constexpr int P = 2 * 3 * N * 128;       // two buffers, three parts
-  static constexpr int kFixed = 6 * 1024 + 1024;  // Meta, barriers, alignment
-  static constexpr int kUnits = (232448 - Q - P - kFixed) / kUnitBytes;
-  static constexpr int K = kUnits / 2 < 6 ? kUnits / 2 : 6;
-  static constexpr int V = kUnits - K < 6 ? kUnits - K : 6;
-  static constexpr int kBytes = kFixed + Q + P + (K + V) * kUnitBytes;
-  static constexpr int kCols = 5 * N <= 128 ? 128 : 5 * N <= 256 ? 256 : 512;
+  static constexpr int P = 2 * kParts * N * 128;  // two buffers
+  static constexpr int kGroups = N == 16 ? 2 : N / 16;  // softmax groups
+  static constexpr int kRowsOf = N / kGroups;           // rows of a group
+  static constexpr int kThreads = 128 + 128 * kGroups;
+  static constexpr int kFixed = 8 * 1024 + 1024;  // Meta, alignment
+  static constexpr int kFit = (232448 - Q - P - kFixed) / (2 * kUnitBytes);
+  static constexpr int S = kFit < kStages ? kFit : kStages;
+  static constexpr int kBytes = kFixed + Q + P + S * 2 * kUnitBytes;
+  // Up to 64 rows, the parts of an operand lie side by side in the MMA's N
+  // (half as many MMAs, whose time is that of reading the 128 lanes'
+  // operand); with more rows TMEM has room for fewer columns.
+  static constexpr bool kWide = N <= 64;
+  static constexpr int kScore = kWide ? 2 * N : N;      // columns of a tile
+  static constexpr int kAcc = kWide ? kParts * N : 2 * N;
+  static constexpr int kUse = 2 * kScore + kAcc;
+  static constexpr int kCols =
+      kUse <= 128 ? 128 : kUse <= 256 ? 256 : 512;
 };
 
 // One unit's part that a CTA works on, with what its rows need.
@@ -79,24 +92,27 @@ struct Segment {
   int min_lim;             // tokens that every live row sees
   alignas(16) int lim[kMaxRows];     // tokens each row sees
   alignas(16) float back[kMaxRows];  // undoes the row's scaling
+  int out_row[kMaxRows];             // row of out and lse, -1: none
+  int on[kMaxRows];                  // the row has a query
 };
 
 struct Meta {
   Segment seg[2];
   alignas(16) float neg_ref[kMaxRows], fac[kMaxRows], delta[kMaxRows];
   alignas(16) float warp_val[4][kMaxRows];
-  float ct[6][8], lv[6][8];  // per V stage and page: key factor, log2 scale
-  uint64_t kfull[6], kempty[6], vfull[6], vempty[6];
-  uint64_t sfull[2], sempty[2], pfull[2], pvdone[2], qfull[2], qempty[2];
+  float ct[kStages][8], lv[kStages][8];  // of a page: key factor, log2 scale
+  uint64_t full[kStages], empty[kStages];
+  uint64_t sfull[2], pfull[2], qfull[2], qempty[2];
   uint64_t drain;
   uint32_t tmem;
   int abort;
   long long start, count;    // first tile of this CTA's run and its length
   int b0;                    // its sequence, and the tiles before it there
   long long off0;
-  long long warp_sum[kThreads / 32];
+  long long warp_sum[32];
+  int2 lens[kLens];          // (cached tokens, queries)
 };
-static_assert(sizeof(Meta) <= 6 * 1024, "");
+static_assert(sizeof(Meta) <= 8 * 1024, "");
 
 // ---- the numbering of the tiles -------------------------------------------
 struct Shape {
@@ -111,6 +127,13 @@ __device__ __forceinline__ Lens lens_of(const PagedAttnArgs& a, int b,
   l.n = attn_clamp(a.kv_len[b], (long long)a.max_pages * a.page, bad);
   l.nq = attn_clamp(a.q_len ? a.q_len[b] : a.Q, a.Q, bad);
   return l;
+}
+// The same from the copy on chip, if the batch fits there.
+__device__ __forceinline__ Lens lens_of(const PagedAttnArgs& a, const Meta& m,
+                                        int b) {
+  if (a.B <= kLens) return Lens{m.lens[b].x, m.lens[b].y};
+  bool bad;
+  return lens_of(a, b, &bad);
 }
 // Tiles that row tile rt of a sequence needs (0: it sees nothing).
 __device__ __forceinline__ int tiles_of(const PagedAttnArgs& a, const Shape& s,
@@ -150,8 +173,7 @@ __device__ void walk_start(const PagedAttnArgs& a, const Shape& s,
   w.first = 1;
   w.hk = w.rt = w.tile = 0;
   if (w.left <= 0) return;
-  bool bad = false;
-  const Lens l = lens_of(a, w.b, &bad);
+  const Lens l = lens_of(a, m, w.b);
   const long long h = head_work(a, s, l);
   long long o = m.off0;
   w.hk = (int)(o / h);
@@ -168,11 +190,10 @@ struct Part {
   Lens l;
 };
 // The next segment; false at the end of the run.
-__device__ bool walk_next(const PagedAttnArgs& a, const Shape& s, Walk& w,
-                          Part& p) {
+__device__ bool walk_next(const PagedAttnArgs& a, const Shape& s,
+                          const Meta& m, Walk& w, Part& p) {
   if (w.left <= 0) return false;
-  bool bad = false;
-  p.l = lens_of(a, w.b, &bad);
+  p.l = lens_of(a, m, w.b);
   const int t = tiles_of(a, s, p.l, w.rt);
   const int work = max(1, t);
   const int take = (int)min((long long)(work - w.tile), w.left);
@@ -199,11 +220,34 @@ __device__ bool walk_next(const PagedAttnArgs& a, const Shape& s, Walk& w,
   return true;
 }
 
+// Position in a ring of S stages; `phase` flips on every lap.
+template <int S>
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == S) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+  // the stage k (<= S) uses back
+  __device__ __forceinline__ Ring back(int k) const {
+    Ring r = *this;
+    r.at -= k;
+    if (r.at < 0) {
+      r.at += S;
+      r.phase ^= 1;
+    }
+    return r;
+  }
+};
+
 // ---- PTX ------------------------------------------------------------------
-// Instruction descriptor: E4M3 x E4M3 -> fp32; both operands with M / N
-// contiguous (bits 15, 16) for the second product.
+// Instruction descriptor of the second product: E4M3 x E5M2 (format 1 in
+// bits 10-12) -> fp32, both operands with M / N contiguous (bits 15, 16).
 __host__ __device__ constexpr uint32_t idesc_mn(int N) {
-  return tc::idesc_e4m3_f32(128, N) | (1u << 15) | (1u << 16);
+  return tc::idesc_e4m3_f32(128, N) | (1u << 10) | (1u << 15) | (1u << 16);
 }
 // M contiguous in 128-byte rows with 128-byte swizzle (a V tile as TMA
 // writes it): groups of eight tokens 1024 bytes apart.
@@ -269,51 +313,92 @@ __device__ __forceinline__ void half_sync(int id) {
   asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(id) : "memory");
 }
 
-// Two weights (fp32, at most 430) as three pairs of codes.
-__device__ __forceinline__ void split3(float a, float b, uint32_t& hi,
-                                       uint32_t& mid, uint32_t& lo) {
-  const __half2 up = __float2half2_rn(16.f), dn = __float2half2_rn(-16.f);
-  const __half2 y = __floats2half2_rn(a, b);
-  hi = __nv_cvt_halfraw2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-  const __half2 h1(__nv_cvt_fp8x2_to_halfraw2(hi, __NV_E4M3));
-  const __half2 r1 = __hfma2(h1, dn, __hmul2(y, up));  // 16 (y - hi), exact
-  mid = __nv_cvt_halfraw2_to_fp8x2(r1, __NV_SATFINITE, __NV_E4M3);
-  const __half2 h2(__nv_cvt_fp8x2_to_halfraw2(mid, __NV_E4M3));
-  const __half2 r2 = __hfma2(h2, dn, __hmul2(r1, up));
-  lo = __nv_cvt_halfraw2_to_fp8x2(r2, __NV_SATFINITE, __NV_E4M3);
+// Largest of the warp's values.
+__device__ __forceinline__ float warp_top(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+// One thread of the warp (always the same one).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r));
+  return r != 0;
+}
+
+// Pairs of fp32 in one register pair.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Four weights (fp32 below 57344) as kParts words of four E5M2 numbers.
+__device__ __forceinline__ void split(float e0, float e1, float e2, float e3,
+                                      uint32_t (&w)[kParts]) {
+  __half2 a = __floats2half2_rn(e0, e1), b = __floats2half2_rn(e2, e3);
+#pragma unroll
+  for (int p = 0; p < kParts; ++p) {
+    const uint32_t ua = *reinterpret_cast<const uint32_t*>(&a);
+    const uint32_t ub = *reinterpret_cast<const uint32_t*>(&b);
+    w[p] = __byte_perm(ua, ub, 0x7531);  // the upper bytes
+    if (p + 1 < kParts) {
+      const uint32_t ta = ua & 0xff00ff00u, tb = ub & 0xff00ff00u;
+      a = __hsub2(a, *reinterpret_cast<const __half2*>(&ta));  // exact
+      b = __hsub2(b, *reinterpret_cast<const __half2*>(&tb));
+    }
+  }
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Plan<N>::kThreads, 1)
     paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k,
                          const __grid_constant__ CUtensorMap map_v,
                          const __grid_constant__ PagedAttnArgs a,
                          const Shape shape, float* __restrict__ part) {
   using PL = Plan<N>;
-  constexpr int HR = N / 2;  // rows of a softmax warp
+  constexpr int HR = PL::kRowsOf;  // rows of a softmax warp
+  constexpr int kThreads = PL::kThreads, kSoftWarps = 4 * PL::kGroups;
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sk = base;
-  uint8_t* sv = sk + PL::K * kUnitBytes;
-  uint8_t* sq = sv + PL::V * kUnitBytes;   // [2][2][N][128]
-  uint8_t* sp = sq + PL::Q;                // [2][3][N / 16][128][16]
+  uint8_t* skv = base;                     // [S][K tile, V tile]
+  uint8_t* sq = skv + PL::S * 2 * kUnitBytes;  // [2][2][N][128]
+  uint8_t* sp = sq + PL::Q;                // [2][4][N / 16][128][16]
   Meta& m = *reinterpret_cast<Meta*>(sp + PL::P);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort = &m.abort;
 
   if (tid == 0) {
-    for (int i = 0; i < 6; ++i) {
-      tc::mbar_init(&m.kfull[i], 1);
-      tc::mbar_init(&m.kempty[i], 1);
-      tc::mbar_init(&m.vfull[i], 1);
-      tc::mbar_init(&m.vempty[i], 1);
+    for (int i = 0; i < kStages; ++i) {
+      tc::mbar_init(&m.full[i], 1);
+      tc::mbar_init(&m.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&m.sfull[i], 1);
-      tc::mbar_init(&m.sempty[i], kSoftWarps);
+      tc::mbar_init(&m.sfull[i], 2);
       tc::mbar_init(&m.pfull[i], kSoftWarps);
-      tc::mbar_init(&m.pvdone[i], 1);
       tc::mbar_init(&m.qfull[i], 2);
       tc::mbar_init(&m.qempty[i], 1 + kSoftWarps);
     }
@@ -339,8 +424,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
     long long w = 0;
     bool bad = false;
-    for (int b = b0; b < b1; ++b)
-      w += a.Hkv * head_work(a, shape, lens_of(a, b, &bad));
+    for (int b = b0; b < b1; ++b) {
+      const Lens l = lens_of(a, b, &bad);
+      if (b < kLens) m.lens[b] = make_int2(l.n, l.nq);
+      w += a.Hkv * head_work(a, shape, l);
+    }
     if (bad && blockIdx.x == 0) raise_error(a.err, kErrBadIndex);
     long long run = w;
 #pragma unroll
@@ -366,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       long long o = p0 - (run - w);
       int b = b0;
       for (; b < b1; ++b) {
-        const long long v = a.Hkv * head_work(a, shape, lens_of(a, b, &bad));
+        const long long v = a.Hkv * head_work(a, shape, lens_of(a, m, b));
         if (o < v) break;
         o -= v;
       }
@@ -388,9 +476,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int oob = a.num_pages * a.Hkv * a.page;  // a row past the pool
     const uint32_t box = (uint32_t)a.page * 128;
     const float c = a.scale * kLog2e;
-    long long i = 0, nk = 0, nv = 0;       // tiles, K and V copies so far
+    Ring<PL::S> rs;
+    int copies = 0;                        // issued, up to the stages
     bool ok = true;
-    while (ok && walk_next(a, shape, w, p)) {
+    while (ok && walk_next(a, shape, m, w, p)) {
       const int pages = (p.l.n + a.page - 1) / a.page;
       // page ids two chunks of 32 ahead, their scales one ahead
       int at = p.t0 * pt;                  // first page of the chunk
@@ -408,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       float ks = load_scale(a.k_scale, id), vs = load_scale(a.v_scale, id);
       float ks1 = load_scale(a.k_scale, id1), vs1 = load_scale(a.v_scale, id1);
-      for (int t = p.t0; t < p.t1; ++t, ++i) {
+      for (int t = p.t0; t < p.t1; ++t) {
         if (t * pt - at == 32) {
           at += 32;
           id = id1; ks = ks1; vs = vs1;
@@ -426,104 +515,109 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (bad) raise_error(a.err, kErrBadIndex);
         const int row = bad ? oob : (pid * a.Hkv + p.hk) * a.page;
         const uint32_t bytes = box * __popc(__ballot_sync(0xffffffffu, have));
-        const int kst = (int)(i % PL::K), vst = (int)(i % PL::V);
-        ok = tc::mbar_wait_bounded(&m.kempty[kst],
-                                   (uint32_t)((i / PL::K) & 1) ^ 1, abort,
-                                   kWait);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (lane == 0) tc::mbar_arrive_expect_tx(&m.kfull[kst], bytes);
-        __syncwarp();
-        if (have)
-          tc::tma_load_2d(sk + kst * kUnitBytes + lane * box, &map_k,
-                          &m.kfull[kst], 0, row);
-        ++nk;
-        ok = tc::mbar_wait_bounded(&m.vempty[vst],
-                                   (uint32_t)((i / PL::V) & 1) ^ 1, abort,
-                                   kWait);
+        const int st = rs.at;
+        ok = tc::mbar_wait_bounded(&m.empty[st], rs.phase ^ 1, abort, kWait);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane < pt) {
-          m.ct[vst][lane] = have && !bad ? pk * c : 0.f;
-          m.lv[vst][lane] = have ? log2f(fmaxf(pv, 0x1p-100f)) : 0.f;
+          m.ct[st][lane] = have && !bad ? pk * c : 0.f;
+          m.lv[st][lane] = have ? log2f(fmaxf(pv, 0x1p-100f)) : 0.f;
         }
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive_expect_tx(&m.vfull[vst], bytes);
+        if (lane == 0) tc::mbar_arrive_expect_tx(&m.full[st], 2 * bytes);
         __syncwarp();
+        uint8_t* dst = skv + st * 2 * kUnitBytes + lane * box;
+        if (have) tc::tma_load_2d(dst, &map_k, &m.full[st], 0, row);
         if (have)
-          tc::tma_load_2d(sv + vst * kUnitBytes + lane * box, &map_v,
-                          &m.vfull[vst], 0, row);
-        ++nv;
+          tc::tma_load_2d(dst + kUnitBytes, &map_v, &m.full[st], 0, row);
+        rs.next();
+        copies = min(copies + 1, PL::S);
       }
     }
     // no copy is in flight when the CTA leaves, whatever the others did
     int never = 0;
-    for (long long j = max(0ll, nk - PL::K); j < nk; ++j)
-      tc::mbar_wait_bounded(&m.kfull[j % PL::K], (uint32_t)((j / PL::K) & 1),
-                            &never, kWait);
-    for (long long j = max(0ll, nv - PL::V); j < nv; ++j)
-      tc::mbar_wait_bounded(&m.vfull[j % PL::V], (uint32_t)((j / PL::V) & 1),
-                            &never, kWait);
+    for (; copies > 0; --copies) {
+      const Ring<PL::S> r = rs.back(copies);
+      tc::mbar_wait_bounded(&m.full[r.at], r.phase, &never, kWait);
+    }
   } else if (warp == 1) {
     // --------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t id_s = tc::idesc_e4m3_f32(128, N);
-      constexpr uint32_t id_o = idesc_mn(N);
-      const uint32_t o_col = tmem + 2 * N;
-      bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t par) {
-        ok = ok && tc::mbar_wait_bounded(bar, par, abort, kWait);
-        return ok;
-      };
-      long long i = 0;
-      for (int s = 0; ok; ++s) {
-        const int qb = s & 1;
-        if (!wait(&m.qfull[qb], (s >> 1) & 1)) break;
-        const Segment& g = m.seg[qb];
-        if (g.done) break;
-        const int T = g.t1 - g.t0;
-        const uint32_t q0 = tc::smem_u32(sq) + qb * 2 * N * 128;
-        auto scores = [&](long long j) {
-          const int st = (int)(j % PL::K), sb = (int)(j & 1);
-          if (!wait(&m.kfull[st], (uint32_t)((j / PL::K) & 1))) return;
-          if (!wait(&m.sempty[sb], (uint32_t)((j >> 1) & 1) ^ 1)) return;
-          tc::fence_after_sync();
-          const uint32_t k0 = tc::smem_u32(sk) + st * kUnitBytes;
+    // The whole warp waits, one elected thread issues: operands stay in
+    // uniform registers (issued by a lone lane, an MMA cost 90 cycles).
+    constexpr uint32_t id_s = tc::idesc_e4m3_f32(128, PL::kScore);
+    constexpr uint32_t id_o = idesc_mn(PL::kAcc);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t par) {
+      ok = ok && tc::mbar_wait_bounded(bar, par, abort, kWait);
+      ok = __all_sync(0xffffffffu, ok);
+      return ok;
+    };
+    Ring<PL::S> rk, rv;                    // of the first, second product
+    Ring<2> rs, rp;                        // scores, weights
+    for (int s = 0; ok; ++s) {
+      const int qb = s & 1;
+      if (!wait(&m.qfull[qb], (s >> 1) & 1)) break;
+      const Segment& g = m.seg[qb];
+      if (g.done) break;
+      const int T = __shfl_sync(0xffffffffu, g.t1 - g.t0, 0);
+      const uint32_t q0 = tc::smem_u32(sq) + qb * 2 * N * 128;
+      // The columns that tile t's scores go to were read by the softmax
+      // before it handed over the weights of tile t - 2, which the second
+      // product has waited for.  The softmax reads the tile's scales, which
+      // came with its copy: it acquires them through the arrival below.
+      auto scores = [&] {
+        if (!wait(&m.full[rk.at], rk.phase)) return;
+        tc::fence_after_sync();
+        const uint64_t dk =
+            tc::sdesc_k_sw128(tc::smem_u32(skv) + rk.at * 2 * kUnitBytes);
+        const uint64_t dq = tc::sdesc_k_sw128(q0);
+        if (elect_one()) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc::mma_e4m3(tmem + sb * N, tc::sdesc_k_sw128(k0 + 32 * k),
-                           tc::sdesc_k_sw128(q0 + h * N * 128 + 32 * k), id_s,
-                           (h | k) != 0);
-          tc::mma_commit(&m.kempty[st]);
-          tc::mma_commit(&m.sfull[sb]);
-        };
-        if (T > 0) scores(i);
-        for (int t = 0; ok && t < T; ++t, ++i) {
-          if (t + 1 < T) scores(i + 1);
-          const int st = (int)(i % PL::V), sb = (int)(i & 1);
-          if (!wait(&m.vfull[st], (uint32_t)((i / PL::V) & 1))) break;
-          if (!wait(&m.pfull[sb], (uint32_t)((i >> 1) & 1))) break;
-          tc::fence_after_sync();
-          const uint32_t v0 = tc::smem_u32(sv) + st * kUnitBytes;
-          const uint32_t p0 = tc::smem_u32(sp) + sb * 3 * N * 128;
-#pragma unroll
-          for (int h = 0; h < 3; ++h)
+          for (int h = 0; h < 2 * N / PL::kScore; ++h)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              tc::mma_e4m3(o_col + h * N, sdesc_mn_sw128(v0 + 4096 * k),
-                           sdesc_mn_plain(p0 + h * N * 128 + 512 * k), id_o,
-                           t > 0 || k > 0);
-          tc::mma_commit(&m.vempty[st]);
-          tc::mma_commit(&m.pvdone[sb]);
+              tc::mma_e4m3(tm + rs.at * PL::kScore, dk + 2 * k,
+                           dq + h * (N * 8) + 2 * k, id_s, (h | k) != 0);
+          tc::mma_commit(&m.sfull[rs.at]);
+          tc::mbar_arrive(&m.sfull[rs.at]);
         }
-        if (ok) tc::mma_commit(&m.qempty[qb]);
+        __syncwarp();
+        rk.next();
+        rs.next();
+      };
+      if (T > 0) scores();
+      for (int t = 0; ok && t < T; ++t) {
+        if (t + 1 < T) scores();
+        if (!wait(&m.pfull[rp.at], rp.phase)) break;
+        tc::fence_after_sync();
+        const uint64_t dv = sdesc_mn_sw128(
+            tc::smem_u32(skv) + rv.at * 2 * kUnitBytes + kUnitBytes);
+        const uint64_t dp =
+            sdesc_mn_plain(tc::smem_u32(sp) + rp.at * kParts * N * 128);
+        if (elect_one()) {
+          // all parts side by side, or 0 and 1, then 2 and 3 onto the same
+          // columns
+#pragma unroll
+          for (int h = 0; h < kParts * N / PL::kAcc; ++h)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tc::mma_e4m3(tm + 2 * PL::kScore, dv + 256 * k,
+                           dp + h * (N * 16) + 32 * k, id_o,
+                           t > 0 || h > 0 || k > 0);
+          tc::mma_commit(&m.empty[rv.at]);
+        }
+        __syncwarp();
+        rv.next();
+        rp.next();
       }
-      tc::mma_commit(&m.drain);
-      int never = 0;
-      tc::mbar_wait_bounded(&m.drain, 0, &never, kWait);
+      if (ok && elect_one()) tc::mma_commit(&m.qempty[qb]);
+      __syncwarp();
     }
+    if (elect_one()) tc::mma_commit(&m.drain);
+    __syncwarp();
+    int never = 0;
+    tc::mbar_wait_bounded(&m.drain, 0, &never, kWait);
   } else if (warp < 4) {
     // ------------------------------------------------------ layout of q
     Walk w;
@@ -538,35 +632,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!__all_sync(0xffffffffu, ok)) break;
       Segment& g = m.seg[qb];
       Part p;
-      const bool more = walk_next(a, shape, w, p);
+      const bool more = walk_next(a, shape, m, w, p);
       if (more) {
         const int row0 = p.rt * N;
         uint8_t* q0 = sq + qb * 2 * N * 128;
-        for (int r = qt >> 3; r < N; r += 8) {
-          const int row = row0 + r;
-          const int qi = row / shape.g;
-          const bool live = row < shape.rows && qi < p.l.nq;
+        constexpr int kBatch = 4;            // rows whose loads fly together
+#pragma unroll 1
+        for (int r0 = qt >> 3; r0 < N; r0 += 8 * kBatch) {
+         uint4 u[kBatch][2];
+         int out_row[kBatch], query[kBatch];
+#pragma unroll
+         for (int j = 0; j < kBatch; ++j) {
+           const int row = row0 + r0 + 8 * j;
+           const int qi = row / shape.g;
+           out_row[j] = row < shape.rows && r0 + 8 * j < N
+                            ? (p.b * a.Q + qi) * a.Hq + p.hk * shape.g +
+                                  (row - qi * shape.g)
+                            : -1;
+           query[j] = qi;
+           u[j][0] = u[j][1] = make_uint4(0, 0, 0, 0);
+           if (out_row[j] >= 0 && qi < p.l.nq && ch * 16 < a.D) {
+             const uint4* src = reinterpret_cast<const uint4*>(
+                 static_cast<const __nv_bfloat16*>(a.q) +
+                 (size_t)out_row[j] * a.D + ch * 16);
+             u[j][0] = src[0];
+             u[j][1] = src[1];
+           }
+         }
+#pragma unroll
+         for (int j = 0; j < kBatch; ++j) {
+          const int r = r0 + 8 * j;
+          if (r >= N) break;
+          const int qi = query[j];
+          const bool live = out_row[j] >= 0 && qi < p.l.nq;
           float x[16];
           float big = 0.f;
-          if (live && ch * 16 < a.D) {
-            const uint4* src = reinterpret_cast<const uint4*>(
-                static_cast<const __nv_bfloat16*>(a.q) +
-                (((size_t)p.b * a.Q + qi) * a.Hq + p.hk * shape.g +
-                 row % shape.g) * a.D + ch * 16);
-            const uint4 u[2] = {src[0], src[1]};
-            const uint32_t* v = reinterpret_cast<const uint32_t*>(u);
+          const uint32_t* v = reinterpret_cast<const uint32_t*>(u[j]);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              x[2 * k] = __uint_as_float(v[k] << 16);
-              x[2 * k + 1] = __uint_as_float(v[k] & 0xffff0000u);
-            }
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              big = x[k] == x[k] ? fmaxf(big, fabsf(x[k])) : INFINITY;
-          } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = 0.f;
+          for (int k = 0; k < 8; ++k) {
+            x[2 * k] = __uint_as_float(v[k] << 16);
+            x[2 * k + 1] = __uint_as_float(v[k] & 0xffff0000u);
           }
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            big = x[k] == x[k] ? fmaxf(big, fabsf(x[k])) : INFINITY;
 #pragma unroll
           for (int o = 4; o; o >>= 1)
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
@@ -602,7 +711,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             g.lim[r] = !live      ? 0x7fffffff
                        : a.causal ? min(p.l.n, p.l.n - p.l.nq + qi + 1)
                                   : p.l.n;
+            g.out_row[r] = out_row[j];
+            g.on[r] = live;
           }
+         }
         }
         if (qt == 0) {
           g.b = p.b;
@@ -627,14 +739,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const int half = (warp - 4) >> 2, quarter = warp & 3;
-    const int ht = tid - 128 - half * 128;  // thread of the half
+    const int half = (warp - 4) >> 2, quarter = warp & 3;  // half: the group
+    const int ht = tid - 128 - half * 128;  // thread of the group
     const int tok = quarter * 32 + lane;
     const int rb = half * HR;
     const int bar = 1 + half;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t o_col = lanes + 2 * N + rb;
-    long long i = 0;
+    const uint32_t o_col = lanes + 2 * PL::kScore + rb;
+    constexpr int OG = PL::kAcc / N;       // accumulators of a row
+    const int page_bits = __ffs(a.page) - 1;
+    Ring<2> rs;
+    Ring<PL::S> rv;
     bool live = true;
     for (int s = 0; live; ++s) {
       const int qb = s & 1;
@@ -650,41 +765,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ht < HR) m.neg_ref[rb + ht] = 0.f;
       half_sync(bar);
       float lv_ref = 0.f;
-      for (int t = 0; t < T; ++t, ++i) {
-        const int sb = (int)(i & 1), st = (int)(i % PL::V);
-        ok = tc::mbar_wait_bounded(&m.sfull[sb], (uint32_t)((i >> 1) & 1),
-                                   abort, kWait) &&
-             tc::mbar_wait_bounded(&m.vfull[st], (uint32_t)((i / PL::V) & 1),
-                                   abort, kWait);
+      for (int t = 0; t < T; ++t, rs.next(), rv.next()) {
+        const int sb = rs.at, st = rv.at;
+        // Also says that the weights' buffer is free: the scores' commit
+        // follows the second product of two tiles ago.
+        ok = tc::mbar_wait_bounded(&m.sfull[sb], rs.phase, abort, kWait);
         ok = __all_sync(0xffffffffu, ok);
         float y[HR];
         if (ok) {
           tc::fence_after_sync();
 #pragma unroll
           for (int r = 0; r < HR; r += 8)
-            tmem_ld8(lanes + sb * N + rb + r, y + r);
-          tmem_loaded(y);
+            tmem_ld8(lanes + sb * PL::kScore + rb + r, y + r);
+          if constexpr (PL::kWide) {
+            float z[HR];
+#pragma unroll
+            for (int r = 0; r < HR; r += 8)
+              tmem_ld8(lanes + sb * PL::kScore + N + rb + r, z + r);
+            tmem_loaded(z);
+            tmem_loaded(y);
+#pragma unroll
+            for (int r = 0; r < HR; r += 2)
+              unpack2(add2(pack2(y[r], y[r + 1]), pack2(z[r], z[r + 1])),
+                      y[r], y[r + 1]);
+          } else {
+            tmem_loaded(y);
+          }
           tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&m.sempty[sb]);
         } else {
 #pragma unroll
           for (int r = 0; r < HR; ++r) y[r] = 0.f;
         }
         const int pos = (g.t0 + t) * kTile + tok;
-        const float ct = m.ct[st][tok / a.page], lv = m.lv[st][tok / a.page];
+        const int pg = tok >> page_bits;
+        const float ct = m.ct[st][pg], lv = m.lv[st][pg];
         if (t == 0) lv_ref = m.lv[st][0];
         const float fl = tc::ex2_approx(fminf(lv_ref - lv, 100.f));
         float top = -INFINITY;
+        const uint64_t ct2 = pack2(ct, ct), lv2 = pack2(lv, lv);
 #pragma unroll
         for (int r = 0; r < HR; r += 4) {
-          const float4 bk = *reinterpret_cast<const float4*>(&g.back[rb + r]);
-          const float4 nr =
-              *reinterpret_cast<const float4*>(&m.neg_ref[rb + r]);
-          y[r] = fmaf(y[r] * bk.x, ct, lv) + nr.x;
-          y[r + 1] = fmaf(y[r + 1] * bk.y, ct, lv) + nr.y;
-          y[r + 2] = fmaf(y[r + 2] * bk.z, ct, lv) + nr.z;
-          y[r + 3] = fmaf(y[r + 3] * bk.w, ct, lv) + nr.w;
+          const ulonglong2 bk =
+              *reinterpret_cast<const ulonglong2*>(&g.back[rb + r]);
+          const ulonglong2 nr =
+              *reinterpret_cast<const ulonglong2*>(&m.neg_ref[rb + r]);
+          unpack2(add2(fma2(mul2(pack2(y[r], y[r + 1]), bk.x), ct2, lv2), nr.x),
+                  y[r], y[r + 1]);
+          unpack2(add2(fma2(mul2(pack2(y[r + 2], y[r + 3]), bk.y), ct2, lv2),
+                       nr.y),
+                  y[r + 2], y[r + 3]);
         }
         if ((g.t0 + t + 1) * kTile > g.min_lim) {
 #pragma unroll
@@ -698,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (half_any(bar, !ok)) { live = false; break; }
 #pragma unroll
           for (int r = 0; r < HR; ++r) {
-            const float z = warp_max(y[r]);
+            const float z = warp_top(y[r]);
             if (lane == 0) m.warp_val[quarter][rb + r] = z;
           }
           half_sync(bar);
@@ -716,9 +845,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           half_sync(bar);
           if (t > 0) {
-            ok = tc::mbar_wait_bounded(&m.pvdone[sb ^ 1],
-                                       (uint32_t)(((i - 1) >> 1) & 1), abort,
-                                       kWait);
+            const Ring<PL::S> before = rv.back(1);
+            ok = tc::mbar_wait_bounded(&m.empty[before.at], before.phase,
+                                       abort, kWait);
             ok = __all_sync(0xffffffffu, ok);
             tc::fence_after_sync();
 #pragma unroll
@@ -733,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               if (!one && ok) {
 #pragma unroll
-                for (int h = 0; h < 3; ++h) {
+                for (int h = 0; h < OG; ++h) {
                   float o[8];
                   tmem_ld8(o_col + h * N + r, o);
                   tmem_loaded(o);
@@ -749,34 +878,42 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int r = 0; r < HR; ++r) y[r] += m.delta[rb + r];
         }
-        // ---- the weights, in three parts -----------------------------------
-        ok = tc::mbar_wait_bounded(&m.pvdone[sb], (uint32_t)((i >> 1) & 1) ^ 1,
-                                   abort, kWait);
-        ok = __all_sync(0xffffffffu, ok);
-        uint8_t* dst = sp + sb * 3 * N * 128 + tok * 16;
+        // ---- the weights, in parts -----------------------------------------
+        uint8_t* dst = sp + sb * kParts * N * 128 + tok * 16;
+        const uint64_t fl2 = pack2(fl, fl);
+        constexpr int kRun = HR % 16 == 0 ? 16 : 8;  // rows of one store
 #pragma unroll
-        for (int r = 0; r < HR; r += 8) {
-          uint32_t c[3][4];
+        for (int r = 0; r < HR; r += kRun) {
+          uint32_t c[kRun / 4][kParts];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float e0 = tc::ex2_approx(y[r + 2 * k]);
-            const float e1 = tc::ex2_approx(y[r + 2 * k + 1]);
-            l[r + 2 * k] = fmaf(e0, fl, l[r + 2 * k]);
-            l[r + 2 * k + 1] = fmaf(e1, fl, l[r + 2 * k + 1]);
-            split3(e0, e1, c[0][k], c[1][k], c[2][k]);
+          for (int k = 0; k < kRun / 4; ++k) {
+            float e[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              e[j] = tc::ex2_approx(y[r + 4 * k + j]);
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+              float* lr = l + r + 4 * k + j;
+              unpack2(fma2(pack2(e[j], e[j + 1]), fl2, pack2(lr[0], lr[1])),
+                      lr[0], lr[1]);
+            }
+            split(e[0], e[1], e[2], e[3], c[k]);
           }
-          if (ok) {
-            const int row = rb + r;
+          const int row = rb + r;
 #pragma unroll
-            for (int h = 0; h < 3; ++h)
-              *reinterpret_cast<uint2*>(dst + h * N * 128 +
-                                        (row >> 4) * 2048 + (row & 8)) =
-                  make_uint2(c[h][0] | c[h][1] << 16, c[h][2] | c[h][3] << 16);
+          for (int h = 0; h < kParts; ++h) {
+            uint8_t* at = dst + h * N * 128 + (row >> 4) * 2048 + (row & 8);
+            if constexpr (kRun == 16)
+              *reinterpret_cast<uint4*>(at) =
+                  make_uint4(c[0][h], c[1][h], c[2][h], c[3][h]);
+            else
+              *reinterpret_cast<uint2*>(at) = make_uint2(c[0][h], c[1][h]);
           }
         }
         if (half == 0 && pos >= g.n && ok) {
           // values past the cache's end may be anything: their weight is 0
-          uint4* v = reinterpret_cast<uint4*>(sv + st * kUnitBytes + tok * 128);
+          uint4* v = reinterpret_cast<uint4*>(
+              skv + (2 * st + 1) * kUnitBytes + tok * 128);
 #pragma unroll
           for (int k = 0; k < 8; ++k) v[k] = make_uint4(0, 0, 0, 0);
         }
@@ -787,8 +924,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!live) break;
       // ---- the segment's result ------------------------------------------
       if (T > 0) {
-        ok = tc::mbar_wait_bounded(&m.pvdone[(i - 1) & 1],
-                                   (uint32_t)(((i - 1) >> 1) & 1), abort,
+        const Ring<PL::S> last = rv.back(1);
+        ok = tc::mbar_wait_bounded(&m.empty[last.at], last.phase, abort,
                                    kWait);
         if (half_any(bar, !ok)) break;
         tc::fence_after_sync();
@@ -801,18 +938,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       half_sync(bar);
       const float lift = exp2f(lv_ref);
       if (ht < HR) {
-        const int r = rb + ht, row = g.row0 + r;
+        const int r = rb + ht;
         const float sum = (m.warp_val[0][r] + m.warp_val[1][r]) +
                           (m.warp_val[2][r] + m.warp_val[3][r]);
         const float ref = -m.neg_ref[r] - lv_ref;   // log2 of what sum counts
-        const int qi = row / shape.g;
         const bool seen = sum > 0.f || sum != sum;  // a NaN stays one
         if (g.whole) {
-          const bool on = seen && row < shape.rows && qi < g.nq;
+          const bool on = seen && g.on[r];
           m.fac[r] = on ? lift / sum : 0.f;
-          if (row < shape.rows && a.lse)
-            a.lse[((size_t)g.b * a.Q + qi) * a.Hq + g.hk * shape.g +
-                  row % shape.g] =
+          if (g.out_row[r] >= 0 && a.lse)
+            a.lse[g.out_row[r]] =
                 on ? (log2f(sum) + ref) * 0.6931471805599453f : -INFINITY;
         } else {
           m.fac[r] = lift;
@@ -826,31 +961,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int d = tok;
 #pragma unroll
       for (int r = 0; r < HR; r += 8) {
-        float o[24];
+        float o[8 * OG];
         if (T > 0) {
 #pragma unroll
-          for (int h = 0; h < 3; ++h) tmem_ld8(o_col + h * N + r, o + 8 * h);
+          for (int h = 0; h < OG; ++h) tmem_ld8(o_col + h * N + r, o + 8 * h);
           tmem_loaded(o);
         } else {
 #pragma unroll
-          for (int k = 0; k < 24; ++k) o[k] = 0.f;
+          for (int k = 0; k < 8 * OG; ++k) o[k] = 0.f;
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float f = m.fac[rb + r + k];
-          const float v =
-              fmaf(o[16 + k], 0x1p-8f, fmaf(o[8 + k], 0x1p-4f, o[k])) * f;
-          const int row = g.row0 + rb + r + k;
+          const int row = rb + r + k;
+          const float f = m.fac[row];
+          float v = o[k];
+#pragma unroll
+          for (int h = 1; h < OG; ++h) v += o[8 * h + k];
+          v *= f;
           if (g.whole) {
-            if (row < shape.rows && d < a.D) {
-              const int qi = row / shape.g;
-              static_cast<__nv_bfloat16*>(a.out)[
-                  (((size_t)g.b * a.Q + qi) * a.Hq + g.hk * shape.g +
-                   row % shape.g) * a.D + d] =
+            const int at = g.out_row[row];
+            if (at >= 0 && d < a.D)
+              static_cast<__nv_bfloat16*>(a.out)[(size_t)at * a.D + d] =
                   __float2bfloat16_rn(f == 0.f ? 0.f : v);
-            }
           } else {
-            part[((size_t)g.slot * N + rb + r + k) * 128 + d] = v;
+            part[((size_t)g.slot * N + row) * 128 + d] = v;
           }
         }
       }
@@ -866,16 +1000,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && m.abort) raise_error(a.err, kErrTimeout);
 }
 
-// Joins the partial sums of the units that the runs cut: 128 threads (one
-// per dimension) for up to eight rows of a unit.
+// Joins the partial sums of the units that the runs cut: a warp per row,
+// eight rows of a unit to a CTA.
 constexpr int kJoinRows = 8;
-__global__ void __launch_bounds__(128)
+constexpr int kJoinThreads = 32 * kJoinRows;
+__global__ void __launch_bounds__(kJoinThreads)
     paged_attn_tc_join_kernel(const __grid_constant__ PagedAttnArgs a,
                               const Shape shape, int grid,
                               const float* __restrict__ part) {
+  __shared__ long long s_sum[2][kJoinRows];
+  __shared__ float s_w[kJoinRows][kMaxCtas];
   pdl_trigger();
   pdl_wait();
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int u = blockIdx.x;
   const int rt = u % shape.row_tiles;
   u /= shape.row_tiles;
@@ -883,24 +1020,26 @@ __global__ void __launch_bounds__(128)
   // tiles before this unit, and all tiles
   long long before = 0, total = 0;
   bool bad = false;
-  for (int i = tid; i < a.B; i += 128) {
+  for (int i = tid; i < a.B; i += kJoinThreads) {
     const long long w = a.Hkv * head_work(a, shape, lens_of(a, i, &bad));
     total += w;
     if (i < b) before += w;
   }
-  __shared__ long long s_sum[2][4];
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     before += __shfl_xor_sync(0xffffffffu, before, o);
     total += __shfl_xor_sync(0xffffffffu, total, o);
   }
   if (lane == 0) {
-    s_sum[0][tid >> 5] = before;
-    s_sum[1][tid >> 5] = total;
+    s_sum[0][warp] = before;
+    s_sum[1][warp] = total;
   }
   __syncthreads();
-  before = s_sum[0][0] + s_sum[0][1] + s_sum[0][2] + s_sum[0][3];
-  total = s_sum[1][0] + s_sum[1][1] + s_sum[1][2] + s_sum[1][3];
+  before = total = 0;
+  for (int i = 0; i < kJoinRows; ++i) {
+    before += s_sum[0][i];
+    total += s_sum[1][i];
+  }
   const int G = (int)min((long long)grid, total);
   const Lens l = lens_of(a, b, &bad);
   before += hk * head_work(a, shape, l);
@@ -909,50 +1048,55 @@ __global__ void __launch_bounds__(128)
   const int c0 = (int)(((before + 1) * G - 1) / total);
   const int c1 = (int)((end * G - 1) / total);  // of the last tile, end - 1
   if (c0 == c1) return;
+  const int r = blockIdx.y * kJoinRows + warp;
+  const int row = rt * shape.N + r;
+  if (r >= shape.N || row >= shape.rows) return;
   const int n = c1 - c0 + 1;
-  auto slot = [&](int i) {
-    const int c = c0 + i;
-    return 2 * c + (i == 0 && run_start(total, c, G) != before ? 1 : 0);
-  };
+  // a run's first segment is in its even slot; every part but the first
+  // starts its run
+  const int odd = run_start(total, c0, G) != before;
+  auto slot = [&](int i) { return 2 * (c0 + i) + (i == 0 ? odd : 0); };
   const float2* ml = reinterpret_cast<const float2*>(
       part + (size_t)2 * grid * shape.N * 128);
-  __shared__ float s_w[kMaxCtas];
-  const int r1 = min(shape.N, (int)(blockIdx.y + 1) * kJoinRows);
-  for (int r = blockIdx.y * kJoinRows; r < r1; ++r) {
-    const int row = rt * shape.N + r;
-    if (row >= shape.rows) break;
-    __syncthreads();
-    if (tid < 32) {
-      float top = -INFINITY;
-      for (int i = lane; i < n; i += 32)
-        top = fmaxf(top, ml[(size_t)slot(i) * shape.N + r].x);
-      top = warp_max(top);
-      float sum = 0.f;
-      for (int i = lane; i < n; i += 32) {
-        const float2 v = ml[(size_t)slot(i) * shape.N + r];
-        const float w = v.x == -INFINITY ? 0.f : exp2f(v.x - top);
-        s_w[i] = w;
-        sum += w * v.y;
-      }
-      sum = warp_sum(sum);
-      const int qi = row / shape.g;
-      const bool on = (sum > 0.f || sum != sum) && qi < l.nq;
-      const float inv = on ? 1.f / sum : 0.f;
-      for (int i = lane; i < n; i += 32) s_w[i] *= inv;
-      if (lane == 0 && a.lse)
-        a.lse[((size_t)b * a.Q + qi) * a.Hq + hk * shape.g + row % shape.g] =
-            on ? (log2f(sum) + top) * 0.6931471805599453f : -INFINITY;
-    }
-    __syncthreads();
-    if (tid < a.D) {
-      float o = 0.f;
+  float top = -INFINITY;
+  for (int i = lane; i < n; i += 32)
+    top = fmaxf(top, ml[(size_t)slot(i) * shape.N + r].x);
+  top = warp_max(top);
+  float sum = 0.f;
+  for (int i = lane; i < n; i += 32) {
+    const float2 v = ml[(size_t)slot(i) * shape.N + r];
+    const float w = v.x == -INFINITY ? 0.f : exp2f(v.x - top);
+    s_w[warp][i] = w;
+    sum += w * v.y;
+  }
+  sum = warp_sum(sum);
+  __syncwarp();
+  const int qi = row / shape.g;
+  const size_t at =
+      ((size_t)b * a.Q + qi) * a.Hq + hk * shape.g + row % shape.g;
+  const bool on = (sum > 0.f || sum != sum) && qi < l.nq;
+  const float inv = on ? 1.f / sum : 0.f;
+  if (lane == 0 && a.lse)
+    a.lse[at] = on ? (log2f(sum) + top) * 0.6931471805599453f : -INFINITY;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-      for (int i = 0; i < n; ++i)
-        o = fmaf(s_w[i], part[((size_t)slot(i) * shape.N + r) * 128 + tid], o);
-      static_cast<__nv_bfloat16*>(a.out)[
-          (((size_t)b * a.Q + row / shape.g) * a.Hq + hk * shape.g +
-           row % shape.g) * a.D + tid] = __float2bfloat16_rn(o);
-    }
+  for (int i = 0; i < n; ++i) {
+    const float w = s_w[warp][i];
+    const float4 v = *reinterpret_cast<const float4*>(
+        part + ((size_t)slot(i) * shape.N + r) * 128 + 4 * lane);
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+  }
+  if (4 * lane < a.D) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+    const __nv_bfloat162 y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    uint2 v;
+    v.x = *reinterpret_cast<const uint32_t*>(&x);
+    v.y = *reinterpret_cast<const uint32_t*>(&y);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) +
+                              at * a.D + 4 * lane) = v;
   }
 }
 
@@ -975,7 +1119,7 @@ cudaError_t launch_n(const CUtensorMap& mk, const CUtensorMap& mv,
   cudaError_t e = cudaFuncSetAttribute(
       f, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<N>::kBytes);
   if (e != cudaSuccess) return e;
-  PdlLaunch L(dim3(G), dim3(kThreads), Plan<N>::kBytes, stream);
+  PdlLaunch L(dim3(G), dim3(Plan<N>::kThreads), Plan<N>::kBytes, stream);
   return cudaLaunchKernelEx(&L.cfg, f, mk, mv, a, s, part);
 }
 
@@ -1014,7 +1158,7 @@ cudaError_t launch_paged_attn_tc(const PagedAttnArgs& a, int sms, float* part,
   if (units > 0x7fffffffll) return cudaErrorInvalidValue;
   const int most = std::min(s.N, s.rows);
   PdlLaunch J(dim3((unsigned)units, (most + kJoinRows - 1) / kJoinRows),
-              dim3(128), 0, stream);
+              dim3(kJoinThreads), 0, stream);
   return cudaLaunchKernelEx(&J.cfg, paged_attn_tc_join_kernel, a, s, G,
                             (const float*)part);
 }
