@@ -4,15 +4,16 @@
 // The cached codes go from HBM to the MMAs as they are: no kernel instruction
 // touches a key or a value.  What has to meet them in 8 bits is the small
 // side, split so that nothing is lost:
-//   q    is scaled per row by a power of two and written as the sum of two
-//        E4M3 numbers (8 bits, all that bf16 has); both products accumulate
-//        into the same scores;
+//   q    is scaled by a power of two and written as the sum of two E4M3
+//        numbers (8 bits, all that bf16 has), both products added.  The rows
+//        of a unit share the scale; a row more than 2^6 below the largest
+//        has its own (and costs the softmax one multiplication);
 //   P    the softmax weights, rounded to fp16 (11 bits), are written as the
-//        sum of four E5M2 numbers.  E5M2 is the upper byte of fp16, so a part
-//        is cut off with a mask and the rest is an exact fp16 difference: no
-//        conversion instructions (four to a cycle and SM quarter; three E4M3
-//        parts made by them took 1200 cycles a tile of 80 rows), and no part
-//        needs a scale of its own.
+//        sum of three E5M2 numbers.  E5M2 is the upper byte of fp16: a part
+//        is that byte after rounding, the rest an exact fp16 difference, and
+//        three parts of three bits and a sign hold eleven bits.  That takes
+//        no conversion instructions (parts made by those took 1200 cycles
+//        a tile of 80 rows), and no part needs a scale of its own.
 // Scores are computed transposed: S^T[token, row] = K q^T and
 // O^T[dim, row] = V^T P^T, so that the 128 lanes of an MMA are always full
 // (tokens, then dimensions) and the number of (query, head) rows, a multiple
@@ -51,32 +52,36 @@ constexpr int kTile = 128;         // tokens of a tile, lanes of an MMA
 constexpr int kMaxRows = 96;       // (query, head) rows of a unit
 constexpr int kMaxCtas = 160;
 constexpr int kUnitBytes = kTile * 128;  // a K or V tile in shared memory
-constexpr int kStages = 6;         // most stages of a K and a V tile
+constexpr int kStages = 7;         // most stages of K or V tiles
 constexpr int kLens = 128;         // sequences whose lengths are kept on chip
 constexpr uint64_t kWait = 2000000000ull;  // 2 s
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kHead = 10.f;      // weights are 2^(score - ref + kHead)
 constexpr float kRaise = 15.75f;   // 2^15.75 = 55109 < 57344, E5M2's largest
-constexpr int kParts = 4;          // E5M2 parts of a weight
+constexpr int kParts = 3;          // E5M2 parts of a weight
 
 // Shared-memory plan for N rows.
 template <int N>
 struct Plan {
-  static constexpr int Q = 2 * 2 * N * 128;       // two buffers, two parts
+  static constexpr int Q = 2 * N * 128;           // two parts of q
   static constexpr int P = 2 * kParts * N * 128;  // two buffers
-  static constexpr int kGroups = N == 16 ? 2 : N / 16;  // softmax groups
+  // softmax groups: as many as registers allow (a group's warp on each SM
+  // quarter hides the others' latencies), in whole rows of 16, eights or
+  // fours
+  static constexpr int kGroups = N >= 64 ? 4 : N == 48 ? 3 : 2;
   static constexpr int kRowsOf = N / kGroups;           // rows of a group
   static constexpr int kThreads = 128 + 128 * kGroups;
   static constexpr int kFixed = 8 * 1024 + 1024;  // Meta, alignment
-  static constexpr int kFit = (232448 - Q - P - kFixed) / (2 * kUnitBytes);
-  static constexpr int S = kFit < kStages ? kFit : kStages;
-  static constexpr int kBytes = kFixed + Q + P + S * 2 * kUnitBytes;
-  // Up to 64 rows, the parts of an operand lie side by side in the MMA's N
-  // (half as many MMAs, whose time is that of reading the 128 lanes'
-  // operand); with more rows TMEM has room for fewer columns.
-  static constexpr bool kWide = N <= 64;
-  static constexpr int kScore = kWide ? 2 * N : N;      // columns of a tile
-  static constexpr int kAcc = kWide ? kParts * N : 2 * N;
+  static constexpr int kFit = (232448 - Q - P - kFixed) / kUnitBytes;
+  // K is free again after the first product, V after the second
+  static constexpr int K = kFit / 2 - 1 < 5 ? kFit / 2 - 1 : 5;
+  static constexpr int V = kFit - K < kStages ? kFit - K : kStages;
+  static constexpr int kBytes = kFixed + Q + P + (K + V) * kUnitBytes;
+  // The parts of an operand lie side by side in the MMA's N where it (256)
+  // and TMEM (512 columns) allow: fewer MMAs, whose time is that of reading
+  // the 128 lanes' operand when N is small.
+  static constexpr int kScore = N <= 64 ? 2 * N : N;    // columns of a tile
+  static constexpr int kAcc = N <= 80 ? kParts * N : 2 * N;
   static constexpr int kUse = 2 * kScore + kAcc;
   static constexpr int kCols =
       kUse <= 128 ? 128 : kUse <= 256 ? 256 : 512;
@@ -91,25 +96,28 @@ struct Segment {
   int whole, slot;         // all of the unit's tiles / where partial sums go
   int min_lim;             // tokens that every live row sees
   alignas(16) int lim[kMaxRows];     // tokens each row sees
-  alignas(16) float back[kMaxRows];  // undoes the row's scaling
+  alignas(16) float rel[kMaxRows];   // undoes a row's own scaling
+  float back;                        // undoes the unit's
+  int uneven;                        // some row has its own scaling
   int out_row[kMaxRows];             // row of out and lse, -1: none
   int on[kMaxRows];                  // the row has a query
 };
 
 struct Meta {
   Segment seg[2];
-  alignas(16) float neg_ref[kMaxRows], fac[kMaxRows], delta[kMaxRows];
+  alignas(16) float neg_ref[kMaxRows], fac[kMaxRows];
+  float q_top[2];
   alignas(16) float warp_val[4][kMaxRows];
   float ct[kStages][8], lv[kStages][8];  // of a page: key factor, log2 scale
-  uint64_t full[kStages], empty[kStages];
-  uint64_t sfull[2], pfull[2], qfull[2], qempty[2];
+  uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
+  uint64_t sfull[2], pfull[2], qfull[2], qempty[2], qfree;
   uint64_t drain;
   uint32_t tmem;
   int abort;
-  long long start, count;    // first tile of this CTA's run and its length
+  int count;                 // tiles of this CTA's run
   int b0;                    // its sequence, and the tiles before it there
-  long long off0;
-  long long warp_sum[32];
+  int off0;
+  int warp_sum[32];
   int2 lens[kLens];          // (cached tokens, queries)
 };
 static_assert(sizeof(Meta) <= 8 * 1024, "");
@@ -148,22 +156,24 @@ __device__ __forceinline__ int tiles_of(const PagedAttnArgs& a, const Shape& s,
   return (seen + kTile - 1) / kTile;
 }
 // Work of one key head of a sequence: its tiles, at least one per row tile.
-__device__ __forceinline__ long long head_work(const PagedAttnArgs& a,
-                                               const Shape& s, const Lens& l) {
-  long long w = 0;
+// Fewer than 2^31 in all (checked on the host).
+__device__ __forceinline__ int head_work(const PagedAttnArgs& a,
+                                         const Shape& s, const Lens& l) {
+  int w = 0;
   for (int rt = 0; rt < s.row_tiles; ++rt) w += max(1, tiles_of(a, s, l, rt));
   return w;
 }
 // First tile of CTA c of the G that work (no more than there are tiles, so
 // that each of them has one).
-__device__ __forceinline__ long long run_start(long long total, int c, int G) {
-  return c >= G ? total : total * c / G;
+__device__ __forceinline__ int run_start(int total, int c, int G) {
+  const int q = total / G;
+  return c >= G ? total : q * c + (total - q * G) * c / G;
 }
 
 // Walks the units from a position in the numbering.
 struct Walk {
   int b, hk, rt, tile;       // tile: first one not yet handed out
-  long long left;            // tiles left in this CTA's run
+  int left;                  // tiles left in this CTA's run
   int first;                 // no segment handed out yet
 };
 __device__ void walk_start(const PagedAttnArgs& a, const Shape& s,
@@ -174,16 +184,16 @@ __device__ void walk_start(const PagedAttnArgs& a, const Shape& s,
   w.hk = w.rt = w.tile = 0;
   if (w.left <= 0) return;
   const Lens l = lens_of(a, m, w.b);
-  const long long h = head_work(a, s, l);
-  long long o = m.off0;
-  w.hk = (int)(o / h);
+  const int h = head_work(a, s, l);
+  int o = m.off0;
+  w.hk = o / h;
   o -= w.hk * h;
   for (;; ++w.rt) {
     const int t = max(1, tiles_of(a, s, l, w.rt));
     if (o < t) break;
     o -= t;
   }
-  w.tile = (int)o;
+  w.tile = o;
 }
 struct Part {
   int b, hk, rt, t0, t1, whole, first;
@@ -196,7 +206,7 @@ __device__ bool walk_next(const PagedAttnArgs& a, const Shape& s,
   p.l = lens_of(a, m, w.b);
   const int t = tiles_of(a, s, p.l, w.rt);
   const int work = max(1, t);
-  const int take = (int)min((long long)(work - w.tile), w.left);
+  const int take = min(work - w.tile, w.left);
   p.b = w.b;
   p.hk = w.hk;
   p.rt = w.rt;
@@ -218,6 +228,29 @@ __device__ bool walk_next(const PagedAttnArgs& a, const Shape& s,
     }
   }
   return true;
+}
+
+// Wait for phase `parity` of `bar`, at most kWait; false (and *abort set) if
+// it runs out or another role gave up.  Polls go to shared memory, whose
+// bandwidth the MMAs need: the clock and *abort are looked at seldom, and
+// roles that run ahead (kLazy) sleep between polls.
+template <bool kLazy = false>
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity,
+                                         volatile int* abort) {
+  if (tc::mbar_try_wait(bar, parity, 1000)) return true;
+  const uint64_t t0 = tc::globaltimer_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i) {
+      if (kLazy) __nanosleep(100);
+      if (tc::mbar_try_wait(bar, parity, 1000)) return true;
+    }
+    if (*abort) return false;
+    if (tc::globaltimer_ns() - t0 > kWait) {
+      *abort = 1;
+      return false;
+    }
+  }
 }
 
 // Position in a ring of S stages; `phase` flips on every lap.
@@ -262,25 +295,21 @@ __device__ __forceinline__ uint64_t sdesc_mn_plain(uint32_t saddr) {
          (static_cast<uint64_t>(2048 >> 4) << 32) |
          (static_cast<uint64_t>(1) << 46);
 }
-__device__ __forceinline__ void tmem_ld8(uint32_t addr, float* v) {
-  uint32_t r[8];
+__device__ __forceinline__ void tmem_ld4(uint32_t addr, float* v) {
+  uint32_t r[4];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}"
-      ", [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
-        "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
       : "r"(addr));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tmem_st8(uint32_t addr, const float* v) {
+__device__ __forceinline__ void tmem_st4(uint32_t addr, const float* v) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, "
-      "%7, %8};" ::"r"(addr),
+      "tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+          addr),
       "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])),
-      "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
-      "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-      "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+      "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3]))
       : "memory");
 }
 // Wait for this thread's TMEM loads; no use of v is scheduled before it.
@@ -293,21 +322,32 @@ __device__ __forceinline__ void tmem_loaded(float (&v)[M]) {
 __device__ __forceinline__ void tmem_stored() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(
+                   tc::smem_u32(bar)),
+               "r"(bytes)
+               : "memory");
+}
 __device__ __forceinline__ void fence_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
-// Barrier of 128 threads; true if `p` is true in any of them.
-__device__ __forceinline__ bool half_any(int id, bool p) {
+// Barrier `id` of T threads; true if `p` is true in any of them.
+template <int T>
+__device__ __forceinline__ bool any_of(int id, bool p) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred.aligned q, %2, 128, p;\n\t"
+      "barrier.cta.red.or.pred.aligned q, %2, %3, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}\n"
       : "=r"(r)
-      : "r"((uint32_t)p), "r"(id)
+      : "r"((uint32_t)p), "r"(id), "n"(T)
       : "memory");
   return r != 0;
+}
+constexpr int kQBar = 15;  // of the two warps that lay out q
+__device__ __forceinline__ bool half_any(int id, bool p) {
+  return any_of<128>(id, p);
 }
 __device__ __forceinline__ void half_sync(int id) {
   asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(id) : "memory");
@@ -363,9 +403,13 @@ __device__ __forceinline__ void split(float e0, float e1, float e2, float e3,
   for (int p = 0; p < kParts; ++p) {
     const uint32_t ua = *reinterpret_cast<const uint32_t*>(&a);
     const uint32_t ub = *reinterpret_cast<const uint32_t*>(&b);
-    w[p] = __byte_perm(ua, ub, 0x7531);  // the upper bytes
-    if (p + 1 < kParts) {
-      const uint32_t ta = ua & 0xff00ff00u, tb = ub & 0xff00ff00u;
+    // to the nearest upper byte, ties away; the last part fits one
+    if (p + 1 == kParts) {
+      w[p] = __byte_perm(ua, ub, 0x7531);
+    } else {
+      const uint32_t ta = (ua + 0x00800080u) & 0xff00ff00u;
+      const uint32_t tb = (ub + 0x00800080u) & 0xff00ff00u;
+      w[p] = __byte_perm(ta, tb, 0x7531);
       a = __hsub2(a, *reinterpret_cast<const __half2*>(&ta));  // exact
       b = __hsub2(b, *reinterpret_cast<const __half2*>(&tb));
     }
@@ -384,24 +428,28 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* skv = base;                     // [S][K tile, V tile]
-  uint8_t* sq = skv + PL::S * 2 * kUnitBytes;  // [2][2][N][128]
-  uint8_t* sp = sq + PL::Q;                // [2][4][N / 16][128][16]
+  uint8_t* sk = base;
+  uint8_t* sv = sk + PL::K * kUnitBytes;
+  uint8_t* sq = sv + PL::V * kUnitBytes;   // [2][N][128]
+  uint8_t* sp = sq + PL::Q;                // [2][kParts][N / 16][128][16]
   Meta& m = *reinterpret_cast<Meta*>(sp + PL::P);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort = &m.abort;
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      tc::mbar_init(&m.full[i], 1);
-      tc::mbar_init(&m.empty[i], 1);
+      tc::mbar_init(&m.kfull[i], 1);
+      tc::mbar_init(&m.kempty[i], 1);
+      tc::mbar_init(&m.vfull[i], 1);
+      tc::mbar_init(&m.vempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&m.sfull[i], 2);
       tc::mbar_init(&m.pfull[i], kSoftWarps);
       tc::mbar_init(&m.qfull[i], 2);
-      tc::mbar_init(&m.qempty[i], 1 + kSoftWarps);
+      tc::mbar_init(&m.qempty[i], kSoftWarps);
     }
+    tc::mbar_init(&m.qfree, 1);
     tc::mbar_init(&m.drain, 1);
     m.abort = 0;
     m.b0 = 0;
@@ -422,7 +470,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
   {
     const int per = (a.B + kThreads - 1) / kThreads;
     const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-    long long w = 0;
+    int w = 0;
     bool bad = false;
     for (int b = b0; b < b1; ++b) {
       const Lens l = lens_of(a, b, &bad);
@@ -430,31 +478,28 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
       w += a.Hkv * head_work(a, shape, l);
     }
     if (bad && blockIdx.x == 0) raise_error(a.err, kErrBadIndex);
-    long long run = w;
+    int run = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, run, o);
+      const int v = __shfl_up_sync(0xffffffffu, run, o);
       if (lane >= o) run += v;
     }
     if (lane == 31) m.warp_sum[warp] = run;
     __syncthreads();
-    long long total = 0;
+    int total = 0;
     for (int i = 0; i < kThreads / 32; ++i) {
       if (i < warp) run += m.warp_sum[i];
       total += m.warp_sum[i];
     }
-    const int G = (int)min((long long)gridDim.x, total);
-    const long long p0 = run_start(total, blockIdx.x, G);
-    const long long p1 = run_start(total, blockIdx.x + 1, G);
-    if (tid == 0) {
-      m.start = p0;
-      m.count = p1 - p0;
-    }
+    const int G = min((int)gridDim.x, total);
+    const int p0 = run_start(total, blockIdx.x, G);
+    const int p1 = run_start(total, blockIdx.x + 1, G);
+    if (tid == 0) m.count = p1 - p0;
     if (p1 > p0 && p0 >= run - w && p0 < run) {
-      long long o = p0 - (run - w);
+      int o = p0 - (run - w);
       int b = b0;
       for (; b < b1; ++b) {
-        const long long v = a.Hkv * head_work(a, shape, lens_of(a, m, b));
+        const int v = a.Hkv * head_work(a, shape, lens_of(a, m, b));
         if (o < v) break;
         o -= v;
       }
@@ -476,8 +521,9 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
     const int oob = a.num_pages * a.Hkv * a.page;  // a row past the pool
     const uint32_t box = (uint32_t)a.page * 128;
     const float c = a.scale * kLog2e;
-    Ring<PL::S> rs;
-    int copies = 0;                        // issued, up to the stages
+    Ring<PL::K> rk;
+    Ring<PL::V> rv;
+    int nk = 0, nv = 0;                    // copies issued, up to the stages
     bool ok = true;
     while (ok && walk_next(a, shape, m, w, p)) {
       const int pages = (p.l.n + a.page - 1) / a.page;
@@ -508,37 +554,51 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
         }
         const int from = t * pt - at + lane;  // lane < pt: its page
         const int pid = __shfl_sync(0xffffffffu, id, from & 31);
-        const float pk = __shfl_sync(0xffffffffu, ks, from & 31);
-        const float pv = __shfl_sync(0xffffffffu, vs, from & 31);
         const bool have = lane < pt && t * pt + lane < pages;
         const bool bad = have && (pid < 0 || pid >= a.num_pages);
         if (bad) raise_error(a.err, kErrBadIndex);
         const int row = bad ? oob : (pid * a.Hkv + p.hk) * a.page;
         const uint32_t bytes = box * __popc(__ballot_sync(0xffffffffu, have));
-        const int st = rs.at;
-        ok = tc::mbar_wait_bounded(&m.empty[st], rs.phase ^ 1, abort, kWait);
+        ok = wait_for<true>(&m.kempty[rk.at], rk.phase ^ 1, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        if (lane == 0) tc::mbar_arrive_expect_tx(&m.kfull[rk.at], bytes);
+        __syncwarp();
+        if (have)
+          tc::tma_load_2d(sk + rk.at * kUnitBytes + lane * box, &map_k,
+                          &m.kfull[rk.at], 0, row);
+        rk.next();
+        nk = min(nk + 1, PL::K);
+        ok = wait_for<true>(&m.vempty[rv.at], rv.phase ^ 1, abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        // the copy first: the scales may still be on their way here
+        if (lane == 0) expect_tx(&m.vfull[rv.at], bytes);
+        __syncwarp();
+        if (have)
+          tc::tma_load_2d(sv + rv.at * kUnitBytes + lane * box, &map_v,
+                          &m.vfull[rv.at], 0, row);
+        const float pk = __shfl_sync(0xffffffffu, ks, from & 31);
+        const float pv = __shfl_sync(0xffffffffu, vs, from & 31);
         if (lane < pt) {
-          m.ct[st][lane] = have && !bad ? pk * c : 0.f;
-          m.lv[st][lane] = have ? log2f(fmaxf(pv, 0x1p-100f)) : 0.f;
+          m.ct[rv.at][lane] = have && !bad ? pk * c : 0.f;
+          m.lv[rv.at][lane] = have ? log2f(fmaxf(pv, 0x1p-100f)) : 0.f;
         }
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive_expect_tx(&m.full[st], 2 * bytes);
-        __syncwarp();
-        uint8_t* dst = skv + st * 2 * kUnitBytes + lane * box;
-        if (have) tc::tma_load_2d(dst, &map_k, &m.full[st], 0, row);
-        if (have)
-          tc::tma_load_2d(dst + kUnitBytes, &map_v, &m.full[st], 0, row);
-        rs.next();
-        copies = min(copies + 1, PL::S);
+        if (lane == 0) tc::mbar_arrive(&m.vfull[rv.at]);
+        rv.next();
+        nv = min(nv + 1, PL::V);
       }
     }
     // no copy is in flight when the CTA leaves, whatever the others did
     int never = 0;
-    for (; copies > 0; --copies) {
-      const Ring<PL::S> r = rs.back(copies);
-      tc::mbar_wait_bounded(&m.full[r.at], r.phase, &never, kWait);
+    for (; nk > 0; --nk) {
+      const Ring<PL::K> r = rk.back(nk);
+      wait_for(&m.kfull[r.at], r.phase, &never);
+    }
+    for (; nv > 0; --nv) {
+      const Ring<PL::V> r = rv.back(nv);
+      wait_for(&m.vfull[r.at], r.phase, &never);
     }
   } else if (warp == 1) {
     // --------------------------------------------------------- MMA issuer
@@ -549,11 +609,12 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t par) {
-      ok = ok && tc::mbar_wait_bounded(bar, par, abort, kWait);
+      ok = ok && wait_for(bar, par, abort);
       ok = __all_sync(0xffffffffu, ok);
       return ok;
     };
-    Ring<PL::S> rk, rv;                    // of the first, second product
+    Ring<PL::K> rk;
+    Ring<PL::V> rv, rvs;                   // of the second, first product
     Ring<2> rs, rp;                        // scores, weights
     for (int s = 0; ok; ++s) {
       const int qb = s & 1;
@@ -561,17 +622,17 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
       const Segment& g = m.seg[qb];
       if (g.done) break;
       const int T = __shfl_sync(0xffffffffu, g.t1 - g.t0, 0);
-      const uint32_t q0 = tc::smem_u32(sq) + qb * 2 * N * 128;
       // The columns that tile t's scores go to were read by the softmax
       // before it handed over the weights of tile t - 2, which the second
       // product has waited for.  The softmax reads the tile's scales, which
       // came with its copy: it acquires them through the arrival below.
       auto scores = [&] {
-        if (!wait(&m.full[rk.at], rk.phase)) return;
+        if (!wait(&m.kfull[rk.at], rk.phase)) return;
+        if (!wait(&m.vfull[rvs.at], rvs.phase)) return;
         tc::fence_after_sync();
         const uint64_t dk =
-            tc::sdesc_k_sw128(tc::smem_u32(skv) + rk.at * 2 * kUnitBytes);
-        const uint64_t dq = tc::sdesc_k_sw128(q0);
+            tc::sdesc_k_sw128(tc::smem_u32(sk) + rk.at * kUnitBytes);
+        const uint64_t dq = tc::sdesc_k_sw128(tc::smem_u32(sq));
         if (elect_one()) {
 #pragma unroll
           for (int h = 0; h < 2 * N / PL::kScore; ++h)
@@ -579,45 +640,56 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
             for (int k = 0; k < 4; ++k)
               tc::mma_e4m3(tm + rs.at * PL::kScore, dk + 2 * k,
                            dq + h * (N * 8) + 2 * k, id_s, (h | k) != 0);
+          tc::mma_commit(&m.kempty[rk.at]);
           tc::mma_commit(&m.sfull[rs.at]);
           tc::mbar_arrive(&m.sfull[rs.at]);
         }
         __syncwarp();
         rk.next();
+        rvs.next();
         rs.next();
       };
       if (T > 0) scores();
       for (int t = 0; ok && t < T; ++t) {
-        if (t + 1 < T) scores();
+        if (t + 1 < T) {
+          scores();
+        } else {                           // q is not read any more
+          if (elect_one()) tc::mma_commit(&m.qfree);
+          __syncwarp();
+        }
         if (!wait(&m.pfull[rp.at], rp.phase)) break;
         tc::fence_after_sync();
-        const uint64_t dv = sdesc_mn_sw128(
-            tc::smem_u32(skv) + rv.at * 2 * kUnitBytes + kUnitBytes);
+        const uint64_t dv =
+            sdesc_mn_sw128(tc::smem_u32(sv) + rv.at * kUnitBytes);
         const uint64_t dp =
             sdesc_mn_plain(tc::smem_u32(sp) + rp.at * kParts * N * 128);
         if (elect_one()) {
-          // all parts side by side, or 0 and 1, then 2 and 3 onto the same
-          // columns
+          // all parts side by side, or 0 and 1, then 2 onto the columns of 0
 #pragma unroll
-          for (int h = 0; h < kParts * N / PL::kAcc; ++h)
+          for (int k = 0; k < 4; ++k)
+            tc::mma_e4m3(tm + 2 * PL::kScore, dv + 256 * k, dp + 32 * k, id_o,
+                         t > 0 || k > 0);
+          if constexpr (PL::kAcc < kParts * N) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               tc::mma_e4m3(tm + 2 * PL::kScore, dv + 256 * k,
-                           dp + h * (N * 16) + 32 * k, id_o,
-                           t > 0 || h > 0 || k > 0);
-          tc::mma_commit(&m.empty[rv.at]);
+                           dp + N * 16 + 32 * k, idesc_mn(N), 1);
+          }
+          tc::mma_commit(&m.vempty[rv.at]);
         }
         __syncwarp();
         rv.next();
         rp.next();
       }
-      if (ok && elect_one()) tc::mma_commit(&m.qempty[qb]);
-      __syncwarp();
+      if (T == 0) {
+        if (elect_one()) tc::mma_commit(&m.qfree);
+        __syncwarp();
+      }
     }
     if (elect_one()) tc::mma_commit(&m.drain);
     __syncwarp();
     int never = 0;
-    tc::mbar_wait_bounded(&m.drain, 0, &never, kWait);
+    wait_for(&m.drain, 0, &never);
   } else if (warp < 4) {
     // ------------------------------------------------------ layout of q
     Walk w;
@@ -626,95 +698,134 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
     const int ch = qt & 7;                 // 16 dimensions of a row
     for (int s = 0;; ++s) {
       const int qb = s & 1;
-      bool ok = tc::mbar_wait_bounded(&m.qempty[qb],
-                                      (uint32_t)((s >> 1) & 1) ^ 1, abort,
-                                      kWait);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      bool ok = wait_for<true>(&m.qempty[qb], (uint32_t)((s >> 1) & 1) ^ 1,
+                               abort);
+      if (s > 0)
+        ok = ok && wait_for<true>(&m.qfree, (uint32_t)(s - 1) & 1, abort);
+      if (any_of<64>(kQBar, !ok)) break;
       Segment& g = m.seg[qb];
       Part p;
       const bool more = walk_next(a, shape, m, w, p);
       if (more) {
         const int row0 = p.rt * N;
-        uint8_t* q0 = sq + qb * 2 * N * 128;
-        constexpr int kBatch = 4;            // rows whose loads fly together
-#pragma unroll 1
-        for (int r0 = qt >> 3; r0 < N; r0 += 8 * kBatch) {
-         uint4 u[kBatch][2];
-         int out_row[kBatch], query[kBatch];
-#pragma unroll
-         for (int j = 0; j < kBatch; ++j) {
-           const int row = row0 + r0 + 8 * j;
-           const int qi = row / shape.g;
-           out_row[j] = row < shape.rows && r0 + 8 * j < N
-                            ? (p.b * a.Q + qi) * a.Hq + p.hk * shape.g +
-                                  (row - qi * shape.g)
-                            : -1;
-           query[j] = qi;
-           u[j][0] = u[j][1] = make_uint4(0, 0, 0, 0);
-           if (out_row[j] >= 0 && qi < p.l.nq && ch * 16 < a.D) {
-             const uint4* src = reinterpret_cast<const uint4*>(
-                 static_cast<const __nv_bfloat16*>(a.q) +
-                 (size_t)out_row[j] * a.D + ch * 16);
-             u[j][0] = src[0];
-             u[j][1] = src[1];
-           }
-         }
-#pragma unroll
-         for (int j = 0; j < kBatch; ++j) {
-          const int r = r0 + 8 * j;
-          if (r >= N) break;
-          const int qi = query[j];
-          const bool live = out_row[j] >= 0 && qi < p.l.nq;
-          float x[16];
-          float big = 0.f;
-          const uint32_t* v = reinterpret_cast<const uint32_t*>(u[j]);
+        // two passes over this thread's rows, four loads in flight at a time
+        // (the second pass hits the caches)
+        constexpr int J = N / 8;             // rows of a thread
+        constexpr int JB = J % 4 == 0 ? 4 : 2;
+        auto load = [&](int j, uint32_t (&v)[8]) {  // returns the row of out
+          const int row = row0 + (qt >> 3) + 8 * j;
+          const int qi = row / shape.g;
+          const int out = row < shape.rows ? (p.b * a.Q + qi) * a.Hq +
+                                                 p.hk * shape.g +
+                                                 (row - qi * shape.g)
+                                           : -1;
+          uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
+          if (row < shape.rows && qi < p.l.nq && ch * 16 < a.D) {
+            const uint4* src = reinterpret_cast<const uint4*>(
+                static_cast<const __nv_bfloat16*>(a.q) + (size_t)out * a.D +
+                ch * 16);
+            u0 = src[0];
+            u1 = src[1];
+          }
+          v[0] = u0.x; v[1] = u0.y; v[2] = u0.z; v[3] = u0.w;
+          v[4] = u1.x; v[5] = u1.y; v[6] = u1.z; v[7] = u1.w;
+          return out;
+        };
+        auto largest = [&](const uint32_t (&v)[8]) {  // infinite: a NaN
+          float t = 0.f;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            x[2 * k] = __uint_as_float(v[k] << 16);
-            x[2 * k + 1] = __uint_as_float(v[k] & 0xffff0000u);
+            const float x0 = __uint_as_float(v[k] << 16);
+            const float x1 = __uint_as_float(v[k] & 0xffff0000u);
+            t = x0 == x0 ? fmaxf(t, fabsf(x0)) : INFINITY;
+            t = x1 == x1 ? fmaxf(t, fabsf(x1)) : INFINITY;
           }
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            big = x[k] == x[k] ? fmaxf(big, fabsf(x[k])) : INFINITY;
 #pragma unroll
           for (int o = 4; o; o >>= 1)
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-          // the row's largest value to [128, 256)
-          const int e = max((int)(__float_as_uint(big) >> 23) - 127, -100);
-          const float up = big < INFINITY ? __uint_as_float((134 - e) << 23)
-                                          : __uint_as_float(0x7fffffffu);
-          uint32_t hi[4], lo[4];
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+          return t;
+        };
+        float all = 0.f;
+#pragma unroll 1
+        for (int j0 = 0; j0 < J; j0 += JB) {
+          uint32_t v[JB][8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float2 y = make_float2(x[2 * k] * up, x[2 * k + 1] * up);
-            const uint32_t h =
-                __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-            const float2 f = __half22float2(
-                __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
-            const uint32_t l = __nv_cvt_float2_to_fp8x2(
-                make_float2(y.x - f.x, y.y - f.y), __NV_SATFINITE, __NV_E4M3);
-            if (k & 1) {
-              hi[k >> 1] |= h << 16;
-              lo[k >> 1] |= l << 16;
-            } else {
-              hi[k >> 1] = h;
-              lo[k >> 1] = l;
+          for (int j = 0; j < JB; ++j) load(j0 + j, v[j]);
+#pragma unroll
+          for (int j = 0; j < JB; ++j) {
+            const float t = largest(v[j]);
+            if (t < INFINITY) all = fmaxf(all, t);
+          }
+        }
+        all = warp_max(all);
+        if (lane == 0) m.q_top[warp - 2] = all;
+        any_of<64>(kQBar, false);
+        all = fmaxf(m.q_top[0], m.q_top[1]);
+        // the unit's largest value to [128, 256)
+        const int e_all = max((int)(__float_as_uint(all) >> 23) - 127, -100);
+        bool own = false;
+#pragma unroll 1
+        for (int j0 = 0; j0 < J; j0 += JB) {
+          uint32_t vv[JB][8];
+          int out_row[JB];
+#pragma unroll
+          for (int j = 0; j < JB; ++j) out_row[j] = load(j0 + j, vv[j]);
+#pragma unroll
+          for (int j = 0; j < JB; ++j) {
+            const uint32_t(&v)[8] = vv[j];
+            const float big = largest(v);
+            const int r = (qt >> 3) + 8 * (j0 + j);
+            const int e_row = (int)(__float_as_uint(big) >> 23) - 127;
+            int e = e_all;
+            if (big > 0.f && e_row < e_all - 6) {
+              e = max(e_row, max(-100, e_all - 100));
+              own = true;
+            }
+            const float up = big < INFINITY
+                                 ? __uint_as_float((134 - e) << 23)
+                                 : __uint_as_float(0x7fffffffu);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float2 y =
+                  make_float2(__uint_as_float(v[k] << 16) * up,
+                              __uint_as_float(v[k] & 0xffff0000u) * up);
+              const uint32_t h =
+                  __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+              const float2 f = __half22float2(
+                  __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+              const uint32_t l =
+                  __nv_cvt_float2_to_fp8x2(make_float2(y.x - f.x, y.y - f.y),
+                                           __NV_SATFINITE, __NV_E4M3);
+              if (k & 1) {
+                hi[k >> 1] |= h << 16;
+                lo[k >> 1] |= l << 16;
+              } else {
+                hi[k >> 1] = h;
+                lo[k >> 1] = l;
+              }
+            }
+            uint8_t* dst = sq + r * 128 + ((ch ^ (r & 7)) << 4);
+            *reinterpret_cast<uint4*>(dst) =
+                make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(dst + N * 128) =
+                make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if (ch == 0) {
+              const int qi = (row0 + r) / shape.g;
+              const bool live = out_row[j] >= 0 && qi < p.l.nq;
+              g.rel[r] = __uint_as_float((127 + e - e_all) << 23);
+              g.lim[r] = !live      ? 0x7fffffff
+                         : a.causal ? min(p.l.n, p.l.n - p.l.nq + qi + 1)
+                                    : p.l.n;
+              g.out_row[r] = out_row[j];
+              g.on[r] = live;
             }
           }
-          uint8_t* dst = q0 + r * 128 + ((ch ^ (r & 7)) << 4);
-          *reinterpret_cast<uint4*>(dst) =
-              make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(dst + N * 128) =
-              make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          if (ch == 0) {
-            g.back[r] = __uint_as_float((120 + e) << 23);  // 2^(e - 7)
-            g.lim[r] = !live      ? 0x7fffffff
-                       : a.causal ? min(p.l.n, p.l.n - p.l.nq + qi + 1)
-                                  : p.l.n;
-            g.out_row[r] = out_row[j];
-            g.on[r] = live;
-          }
-         }
+        }
+        own = any_of<64>(kQBar, own);
+        if (qt == 0) {
+          g.uneven = own;
+          g.back = __uint_as_float((120 + e_all) << 23);  // 2^(e_all - 7)
         }
         if (qt == 0) {
           g.b = p.b;
@@ -742,46 +853,56 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
     const int half = (warp - 4) >> 2, quarter = warp & 3;  // half: the group
     const int ht = tid - 128 - half * 128;  // thread of the group
     const int tok = quarter * 32 + lane;
-    const int rb = half * HR;
     const int bar = 1 + half;
+    // Row `row_of(r)` of the unit is row r (a multiple of 4) of the group.  A
+    // group holds whole units of 16 rows, whose bytes one store writes; the
+    // rest of the groups' rows share the last units.
+    constexpr int kFull = HR / 16 * 16, kRest = HR - kFull;
+    static_assert(PL::kGroups * kRest % 16 == 0 && kRest % 4 == 0, "");
+    auto row_of = [&](int r) {
+      return r < kFull ? half * kFull + r
+                       : PL::kGroups * kFull + half * kRest + r - kFull;
+    };
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t o_col = lanes + 2 * PL::kScore + rb;
-    constexpr int OG = PL::kAcc / N;       // accumulators of a row
+    const uint32_t o_col = lanes + 2 * PL::kScore;
+    const int my_row = ht < HR ? row_of(ht & ~3) + (ht & 3) : 0;
+    constexpr int SG = PL::kScore / N;     // columns of a row's score
+    constexpr int OG = PL::kAcc / N;       // and of its accumulator
     const int page_bits = __ffs(a.page) - 1;
     Ring<2> rs;
-    Ring<PL::S> rv;
+    Ring<PL::V> rv;
     bool live = true;
     for (int s = 0; live; ++s) {
       const int qb = s & 1;
-      bool ok = tc::mbar_wait_bounded(&m.qfull[qb], (s >> 1) & 1, abort,
-                                      kWait);
+      bool ok = wait_for(&m.qfull[qb], (s >> 1) & 1, abort);
       if (half_any(bar, !ok)) break;
       const Segment& g = m.seg[qb];
       if (g.done) break;
       const int T = g.t1 - g.t0;
-      float l[HR];
+      uint64_t l[HR / 2];   // sums of weights, by pairs of rows
 #pragma unroll
-      for (int r = 0; r < HR; ++r) l[r] = 0.f;
-      if (ht < HR) m.neg_ref[rb + ht] = 0.f;
+      for (int r = 0; r < HR / 2; ++r) l[r] = 0;
+      // kHead - reference; 0 before the first tile
+      if (ht < HR) m.neg_ref[my_row] = 0.f;
       half_sync(bar);
       float lv_ref = 0.f;
       for (int t = 0; t < T; ++t, rs.next(), rv.next()) {
         const int sb = rs.at, st = rv.at;
         // Also says that the weights' buffer is free: the scores' commit
         // follows the second product of two tiles ago.
-        ok = tc::mbar_wait_bounded(&m.sfull[sb], rs.phase, abort, kWait);
+        ok = wait_for(&m.sfull[sb], rs.phase, abort);
         ok = __all_sync(0xffffffffu, ok);
         float y[HR];
         if (ok) {
           tc::fence_after_sync();
+          const uint32_t s_col = lanes + sb * PL::kScore;
 #pragma unroll
-          for (int r = 0; r < HR; r += 8)
-            tmem_ld8(lanes + sb * PL::kScore + rb + r, y + r);
-          if constexpr (PL::kWide) {
+          for (int r = 0; r < HR; r += 4) tmem_ld4(s_col + row_of(r), y + r);
+          if constexpr (SG == 2) {
             float z[HR];
 #pragma unroll
-            for (int r = 0; r < HR; r += 8)
-              tmem_ld8(lanes + sb * PL::kScore + N + rb + r, z + r);
+            for (int r = 0; r < HR; r += 4)
+              tmem_ld4(s_col + N + row_of(r), z + r);
             tmem_loaded(z);
             tmem_loaded(y);
 #pragma unroll
@@ -798,28 +919,30 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
         }
         const int pos = (g.t0 + t) * kTile + tok;
         const int pg = tok >> page_bits;
-        const float ct = m.ct[st][pg], lv = m.lv[st][pg];
+        const float ct = m.ct[st][pg] * g.back, lv = m.lv[st][pg];
         if (t == 0) lv_ref = m.lv[st][0];
         const float fl = tc::ex2_approx(fminf(lv_ref - lv, 100.f));
-        float top = -INFINITY;
+        if (g.uneven) {
+#pragma unroll
+          for (int r = 0; r < HR; ++r) y[r] *= g.rel[row_of(r & ~3) + (r & 3)];
+        }
         const uint64_t ct2 = pack2(ct, ct), lv2 = pack2(lv, lv);
 #pragma unroll
         for (int r = 0; r < HR; r += 4) {
-          const ulonglong2 bk =
-              *reinterpret_cast<const ulonglong2*>(&g.back[rb + r]);
           const ulonglong2 nr =
-              *reinterpret_cast<const ulonglong2*>(&m.neg_ref[rb + r]);
-          unpack2(add2(fma2(mul2(pack2(y[r], y[r + 1]), bk.x), ct2, lv2), nr.x),
-                  y[r], y[r + 1]);
-          unpack2(add2(fma2(mul2(pack2(y[r + 2], y[r + 3]), bk.y), ct2, lv2),
-                       nr.y),
+              *reinterpret_cast<const ulonglong2*>(&m.neg_ref[row_of(r)]);
+          unpack2(add2(fma2(pack2(y[r], y[r + 1]), ct2, lv2), nr.x), y[r],
+                  y[r + 1]);
+          unpack2(add2(fma2(pack2(y[r + 2], y[r + 3]), ct2, lv2), nr.y),
                   y[r + 2], y[r + 3]);
         }
         if ((g.t0 + t + 1) * kTile > g.min_lim) {
 #pragma unroll
           for (int r = 0; r < HR; ++r)
-            y[r] = pos < min(g.lim[rb + r], g.n) ? y[r] : -INFINITY;
+            y[r] = pos < min(g.lim[row_of(r & ~3) + (r & 3)], g.n) ? y[r]
+                                                                 : -INFINITY;
         }
+        float top = -INFINITY;
 #pragma unroll
         for (int r = 0; r < HR; ++r) top = fmaxf(top, y[r]);
         if (half_any(bar, t == 0 || top > kRaise || !ok)) {
@@ -828,92 +951,96 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
 #pragma unroll
           for (int r = 0; r < HR; ++r) {
             const float z = warp_top(y[r]);
-            if (lane == 0) m.warp_val[quarter][rb + r] = z;
+            if (lane == 0) m.warp_val[quarter][row_of(r & ~3) + (r & 3)] = z;
           }
           half_sync(bar);
           if (ht < HR) {
-            const int r = rb + ht;
-            float z = fmaxf(fmaxf(m.warp_val[0][r], m.warp_val[1][r]),
-                            fmaxf(m.warp_val[2][r], m.warp_val[3][r]));
-            // y = score + neg_ref, neg_ref = kHead - ref (0 before the
-            // first tile and for a row that sees nothing)
-            float d = 0.f;
-            if (z > -INFINITY && (t == 0 || z > kHead)) d = kHead - ceilf(z);
-            m.delta[r] = d;
-            m.fac[r] = tc::ex2_approx(d);
+            const int r = my_row;
+            const float z =
+                fmaxf(fmaxf(m.warp_val[0][r], m.warp_val[1][r]),
+                      fmaxf(m.warp_val[2][r], m.warp_val[3][r]));
+            // nothing to raise for a row that sees nothing yet
+            const float d = z > -INFINITY && (t == 0 || z > kHead)
+                                ? kHead - ceilf(z) : 0.f;
+            m.fac[r] = d;
             m.neg_ref[r] += d;
           }
           half_sync(bar);
           if (t > 0) {
-            const Ring<PL::S> before = rv.back(1);
-            ok = tc::mbar_wait_bounded(&m.empty[before.at], before.phase,
-                                       abort, kWait);
+            const Ring<PL::V> before = rv.back(1);
+            ok = wait_for(&m.vempty[before.at], before.phase, abort);
             ok = __all_sync(0xffffffffu, ok);
             tc::fence_after_sync();
+          }
 #pragma unroll
-            for (int r = 0; r < HR; r += 8) {
-              float f[8];
-              bool one = true;
+          for (int r = 0; r < HR; r += 4) {
+            const float4 d =
+                *reinterpret_cast<const float4*>(&m.fac[row_of(r)]);
+            const float f[4] = {tc::ex2_approx(d.x), tc::ex2_approx(d.y),
+                                tc::ex2_approx(d.z), tc::ex2_approx(d.w)};
+            y[r] += d.x;
+            y[r + 1] += d.y;
+            y[r + 2] += d.z;
+            y[r + 3] += d.w;
+            l[r / 2] = mul2(l[r / 2], pack2(f[0], f[1]));
+            l[r / 2 + 1] = mul2(l[r / 2 + 1], pack2(f[2], f[3]));
+            const bool one = d.x == 0.f && d.y == 0.f && d.z == 0.f &&
+                             d.w == 0.f;
+            if (t > 0 && !one && ok) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                f[k] = m.fac[rb + r + k];
-                one &= f[k] == 1.f;
-                l[r + k] *= f[k];
-              }
-              if (!one && ok) {
+              for (int h = 0; h < OG; ++h) {
+                float o[4];
+                tmem_ld4(o_col + h * N + row_of(r), o);
+                tmem_loaded(o);
 #pragma unroll
-                for (int h = 0; h < OG; ++h) {
-                  float o[8];
-                  tmem_ld8(o_col + h * N + r, o);
-                  tmem_loaded(o);
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) o[k] *= f[k];
-                  tmem_st8(o_col + h * N + r, o);
-                }
+                for (int k = 0; k < 4; ++k) o[k] *= f[k];
+                tmem_st4(o_col + h * N + row_of(r), o);
               }
             }
+          }
+          if (t > 0) {
             tmem_stored();
             tc::fence_before_sync();
           }
-#pragma unroll
-          for (int r = 0; r < HR; ++r) y[r] += m.delta[rb + r];
         }
         // ---- the weights, in parts -----------------------------------------
         uint8_t* dst = sp + sb * kParts * N * 128 + tok * 16;
         const uint64_t fl2 = pack2(fl, fl);
-        constexpr int kRun = HR % 16 == 0 ? 16 : 8;  // rows of one store
 #pragma unroll
-        for (int r = 0; r < HR; r += kRun) {
-          uint32_t c[kRun / 4][kParts];
+        for (int r = 0; r < HR; r += 16) {
+          const int words = HR - r < 16 ? kRest / 4 : 4;  // of four rows
+          uint32_t c[4][kParts];
 #pragma unroll
-          for (int k = 0; k < kRun / 4; ++k) {
+          for (int k = 0; k < 4; ++k) {
+            if (k >= words) break;
             float e[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               e[j] = tc::ex2_approx(y[r + 4 * k + j]);
 #pragma unroll
             for (int j = 0; j < 4; j += 2) {
-              float* lr = l + r + 4 * k + j;
-              unpack2(fma2(pack2(e[j], e[j + 1]), fl2, pack2(lr[0], lr[1])),
-                      lr[0], lr[1]);
+              uint64_t& lr = l[(r + 4 * k + j) / 2];
+              lr = fma2(pack2(e[j], e[j + 1]), fl2, lr);
             }
             split(e[0], e[1], e[2], e[3], c[k]);
           }
-          const int row = rb + r;
+          const int row = row_of(r);
 #pragma unroll
           for (int h = 0; h < kParts; ++h) {
-            uint8_t* at = dst + h * N * 128 + (row >> 4) * 2048 + (row & 8);
-            if constexpr (kRun == 16)
+            uint8_t* at =
+                dst + h * N * 128 + (row >> 4) * 2048 + (row & 12);
+            if (words == 4)
               *reinterpret_cast<uint4*>(at) =
                   make_uint4(c[0][h], c[1][h], c[2][h], c[3][h]);
-            else
+            else if (words == 2)
               *reinterpret_cast<uint2*>(at) = make_uint2(c[0][h], c[1][h]);
+            else
+              *reinterpret_cast<uint32_t*>(at) = c[0][h];
           }
         }
         if (half == 0 && pos >= g.n && ok) {
           // values past the cache's end may be anything: their weight is 0
-          uint4* v = reinterpret_cast<uint4*>(
-              skv + (2 * st + 1) * kUnitBytes + tok * 128);
+          uint4* v = reinterpret_cast<uint4*>(sv + st * kUnitBytes + tok * 128);
 #pragma unroll
           for (int k = 0; k < 8; ++k) v[k] = make_uint4(0, 0, 0, 0);
         }
@@ -924,21 +1051,26 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
       if (!live) break;
       // ---- the segment's result ------------------------------------------
       if (T > 0) {
-        const Ring<PL::S> last = rv.back(1);
-        ok = tc::mbar_wait_bounded(&m.empty[last.at], last.phase, abort,
-                                   kWait);
+        const Ring<PL::V> last = rv.back(1);
+        ok = wait_for(&m.vempty[last.at], last.phase, abort);
         if (half_any(bar, !ok)) break;
         tc::fence_after_sync();
       }
 #pragma unroll
-      for (int r = 0; r < HR; ++r) {
-        const float v = warp_sum(l[r]);
-        if (lane == 0) m.warp_val[quarter][rb + r] = v;
+      for (int r = 0; r < HR; r += 2) {
+        float v0, v1;
+        unpack2(l[r / 2], v0, v1);
+        v0 = warp_sum(v0);
+        v1 = warp_sum(v1);
+        if (lane == 0)
+          *reinterpret_cast<float2*>(
+              &m.warp_val[quarter][row_of(r & ~3) + (r & 3)]) =
+              make_float2(v0, v1);
       }
       half_sync(bar);
       const float lift = exp2f(lv_ref);
       if (ht < HR) {
-        const int r = rb + ht;
+        const int r = my_row;
         const float sum = (m.warp_val[0][r] + m.warp_val[1][r]) +
                           (m.warp_val[2][r] + m.warp_val[3][r]);
         const float ref = -m.neg_ref[r] - lv_ref;   // log2 of what sum counts
@@ -960,23 +1092,24 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
       half_sync(bar);
       const int d = tok;
 #pragma unroll
-      for (int r = 0; r < HR; r += 8) {
-        float o[8 * OG];
+      for (int r = 0; r < HR; r += 4) {
+        float o[4 * OG];
         if (T > 0) {
 #pragma unroll
-          for (int h = 0; h < OG; ++h) tmem_ld8(o_col + h * N + r, o + 8 * h);
+          for (int h = 0; h < OG; ++h)
+            tmem_ld4(o_col + h * N + row_of(r), o + 4 * h);
           tmem_loaded(o);
         } else {
 #pragma unroll
-          for (int k = 0; k < 8 * OG; ++k) o[k] = 0.f;
+          for (int k = 0; k < 4 * OG; ++k) o[k] = 0.f;
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int row = rb + r + k;
+        for (int k = 0; k < 4; ++k) {
+          const int row = row_of(r) + k;
           const float f = m.fac[row];
           float v = o[k];
 #pragma unroll
-          for (int h = 1; h < OG; ++h) v += o[8 * h + k];
+          for (int h = 1; h < OG; ++h) v += o[4 * h + k];
           v *= f;
           if (g.whole) {
             const int at = g.out_row[row];
@@ -1008,7 +1141,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     paged_attn_tc_join_kernel(const __grid_constant__ PagedAttnArgs a,
                               const Shape shape, int grid,
                               const float* __restrict__ part) {
-  __shared__ long long s_sum[2][kJoinRows];
+  __shared__ int s_sum[2][kJoinRows];
   __shared__ float s_w[kJoinRows][kMaxCtas];
   pdl_trigger();
   pdl_wait();
@@ -1018,10 +1151,10 @@ __global__ void __launch_bounds__(kJoinThreads)
   u /= shape.row_tiles;
   const int hk = u % a.Hkv, b = u / a.Hkv;
   // tiles before this unit, and all tiles
-  long long before = 0, total = 0;
+  int before = 0, total = 0;
   bool bad = false;
   for (int i = tid; i < a.B; i += kJoinThreads) {
-    const long long w = a.Hkv * head_work(a, shape, lens_of(a, i, &bad));
+    const int w = a.Hkv * head_work(a, shape, lens_of(a, i, &bad));
     total += w;
     if (i < b) before += w;
   }
@@ -1040,13 +1173,13 @@ __global__ void __launch_bounds__(kJoinThreads)
     before += s_sum[0][i];
     total += s_sum[1][i];
   }
-  const int G = (int)min((long long)grid, total);
+  const int G = min(grid, total);
   const Lens l = lens_of(a, b, &bad);
   before += hk * head_work(a, shape, l);
   for (int i = 0; i < rt; ++i) before += max(1, tiles_of(a, shape, l, i));
-  const long long end = before + max(1, tiles_of(a, shape, l, rt));
-  const int c0 = (int)(((before + 1) * G - 1) / total);
-  const int c1 = (int)((end * G - 1) / total);  // of the last tile, end - 1
+  const int end = before + max(1, tiles_of(a, shape, l, rt));
+  const int c0 = (int)(((before + 1ll) * G - 1) / total);
+  const int c1 = (int)(((long long)end * G - 1) / total);  // of tile end - 1
   if (c0 == c1) return;
   const int r = blockIdx.y * kJoinRows + warp;
   const int row = rt * shape.N + r;
@@ -1138,6 +1271,10 @@ size_t paged_attn_tc_ws(int B, int Q, int Hq, int Hkv) {
 cudaError_t launch_paged_attn_tc(const PagedAttnArgs& a, int sms, float* part,
                                  cudaStream_t stream) {
   const Shape s = shape_of(a.Q, a.Hq, a.Hkv);
+  const long long most =
+      (long long)a.B * a.Hkv * s.row_tiles *
+      (((long long)a.max_pages * a.page + kTile - 1) / kTile + 1);
+  if (most > 0x7fffffffll) return cudaErrorInvalidValue;
   const int G = std::min(sms, kMaxCtas);
   CUtensorMap mk, mv;
   const uint64_t rows = (uint64_t)a.num_pages * a.Hkv * a.page;
@@ -1156,8 +1293,8 @@ cudaError_t launch_paged_attn_tc(const PagedAttnArgs& a, int sms, float* part,
   if (e != cudaSuccess) return e;
   const long long units = (long long)a.B * a.Hkv * s.row_tiles;
   if (units > 0x7fffffffll) return cudaErrorInvalidValue;
-  const int most = std::min(s.N, s.rows);
-  PdlLaunch J(dim3((unsigned)units, (most + kJoinRows - 1) / kJoinRows),
+  const int rows_of = std::min(s.N, s.rows);
+  PdlLaunch J(dim3((unsigned)units, (rows_of + kJoinRows - 1) / kJoinRows),
               dim3(kJoinThreads), 0, stream);
   return cudaLaunchKernelEx(&J.cfg, paged_attn_tc_join_kernel, a, s, G,
                             (const float*)part);
