@@ -58,6 +58,7 @@ constexpr uint64_t kWait = 2000000000ull;  // 2 s
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kHead = 10.f;      // weights are 2^(score - ref + kHead)
 constexpr float kRaise = 15.75f;   // 2^15.75 = 55109 < 57344, E5M2's largest
+constexpr int kUnitCost = 4;       // of a unit besides its tiles, in tiles
 constexpr int kParts = 3;          // E5M2 parts of a weight
 
 // Shared-memory plan for N rows.
@@ -155,25 +156,27 @@ __device__ __forceinline__ int tiles_of(const PagedAttnArgs& a, const Shape& s,
   }
   return (seen + kTile - 1) / kTile;
 }
-// Work of one key head of a sequence: its tiles, at least one per row tile.
+// Work of one key head of a sequence, in tiles: every unit counts kUnitCost
+// more than its tiles (its start and its output take about that long), so
+// that a run of short sequences does not fall to one CTA.
 // Fewer than 2^31 in all (checked on the host).
 __device__ __forceinline__ int head_work(const PagedAttnArgs& a,
                                          const Shape& s, const Lens& l) {
   int w = 0;
-  for (int rt = 0; rt < s.row_tiles; ++rt) w += max(1, tiles_of(a, s, l, rt));
+  for (int rt = 0; rt < s.row_tiles; ++rt) w += kUnitCost + tiles_of(a, s, l, rt);
   return w;
 }
-// First tile of CTA c of the G that work (no more than there are tiles, so
-// that each of them has one).
+// First position of CTA c of the G that work.
 __device__ __forceinline__ int run_start(int total, int c, int G) {
   const int q = total / G;
   return c >= G ? total : q * c + (total - q * G) * c / G;
 }
 
-// Walks the units from a position in the numbering.
+// Walks the units from a position in the numbering.  Position kUnitCost + t
+// of a unit is its tile t; a unit without tiles is at its last position.
 struct Walk {
-  int b, hk, rt, tile;       // tile: first one not yet handed out
-  int left;                  // tiles left in this CTA's run
+  int b, hk, rt, at;         // at: position in the unit
+  int left;                  // positions left in this CTA's run
   int first;                 // no segment handed out yet
 };
 __device__ void walk_start(const PagedAttnArgs& a, const Shape& s,
@@ -181,7 +184,7 @@ __device__ void walk_start(const PagedAttnArgs& a, const Shape& s,
   w.b = m.b0;
   w.left = m.count;
   w.first = 1;
-  w.hk = w.rt = w.tile = 0;
+  w.hk = w.rt = w.at = 0;
   if (w.left <= 0) return;
   const Lens l = lens_of(a, m, w.b);
   const int h = head_work(a, s, l);
@@ -189,11 +192,11 @@ __device__ void walk_start(const PagedAttnArgs& a, const Shape& s,
   w.hk = o / h;
   o -= w.hk * h;
   for (;; ++w.rt) {
-    const int t = max(1, tiles_of(a, s, l, w.rt));
+    const int t = kUnitCost + tiles_of(a, s, l, w.rt);
     if (o < t) break;
     o -= t;
   }
-  w.tile = o;
+  w.at = o;
 }
 struct Part {
   int b, hk, rt, t0, t1, whole, first;
@@ -202,32 +205,36 @@ struct Part {
 // The next segment; false at the end of the run.
 __device__ bool walk_next(const PagedAttnArgs& a, const Shape& s,
                           const Meta& m, Walk& w, Part& p) {
-  if (w.left <= 0) return false;
-  p.l = lens_of(a, m, w.b);
-  const int t = tiles_of(a, s, p.l, w.rt);
-  const int work = max(1, t);
-  const int take = min(work - w.tile, w.left);
-  p.b = w.b;
-  p.hk = w.hk;
-  p.rt = w.rt;
-  p.t0 = w.tile;
-  p.t1 = min(t, w.tile + take);
-  p.whole = take == work;
-  p.first = w.first;
-  w.first = 0;
-  w.left -= take;
-  w.tile += take;
-  if (w.tile == work) {
-    w.tile = 0;
-    if (++w.rt == s.row_tiles) {
-      w.rt = 0;
-      if (++w.hk == a.Hkv) {
-        w.hk = 0;
-        ++w.b;
+  while (w.left > 0) {
+    p.l = lens_of(a, m, w.b);
+    const int t = tiles_of(a, s, p.l, w.rt);
+    const int work = kUnitCost + t;
+    const int end = min(work, w.at + w.left);
+    p.b = w.b;
+    p.hk = w.hk;
+    p.rt = w.rt;
+    p.t0 = max(0, w.at - kUnitCost);
+    p.t1 = max(0, end - kUnitCost);
+    p.whole = p.t0 == 0 && p.t1 == t;
+    w.left -= end - w.at;
+    w.at = end;
+    if (end == work) {
+      w.at = 0;
+      if (++w.rt == s.row_tiles) {
+        w.rt = 0;
+        if (++w.hk == a.Hkv) {
+          w.hk = 0;
+          ++w.b;
+        }
       }
     }
+    if (p.t1 > p.t0 || (t == 0 && end == work)) {
+      p.first = w.first;
+      w.first = 0;
+      return true;
+    }
   }
-  return true;
+  return false;
 }
 
 // Wait for phase `parity` of `bar`, at most kWait; false (and *abort set) if
@@ -328,6 +335,13 @@ __device__ __forceinline__ void expect_tx(uint64_t* bar, uint32_t bytes) {
                "r"(bytes)
                : "memory");
 }
+// 16 bytes from global to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src,
+                                       bool read) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+               "l"(src), "r"(read ? 16 : 0)
+               : "memory");
+}
 __device__ __forceinline__ void fence_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -358,6 +372,34 @@ __device__ __forceinline__ float warp_top(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
+}
+// Sums over the warp's lanes of C values each, by halves: the lanes trade
+// half of what they hold as long as that is even.  Value i ends in v[0..] of
+// the lanes `slot`, the first value that this lane holds, says.
+template <int C, int O>
+__device__ __forceinline__ void lane_sums(float* v, int lane, int& slot) {
+  if constexpr (O > 0) {
+    if constexpr (C % 2 == 0) {
+      const bool up = lane & O;
+#pragma unroll
+      for (int i = 0; i < C / 2; ++i) {
+        const float give = up ? v[i] : v[i + C / 2];
+        const float keep = up ? v[i + C / 2] : v[i];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, O);
+      }
+      if (up) slot += C / 2;
+      lane_sums<C / 2, O / 2>(v, lane, slot);
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        v[i] += __shfl_xor_sync(0xffffffffu, v[i], O);
+      lane_sums<C, O / 2>(v, lane, slot);
+    }
+  }
+}
+// Values a lane holds in the end.
+constexpr int lane_share(int C, int O) {
+  return O == 0 ? C : lane_share(C % 2 ? C : C / 2, O / 2);
 }
 // One thread of the warp (always the same one).
 __device__ __forceinline__ bool elect_one() {
@@ -708,31 +750,45 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
       const bool more = walk_next(a, shape, m, w, p);
       if (more) {
         const int row0 = p.rt * N;
-        // two passes over this thread's rows, four loads in flight at a time
-        // (the second pass hits the caches)
+        // All rows' values fly at once, asynchronously, into the place their
+        // codes will take: the first 64 dimensions of a row where its upper
+        // parts go, the rest where its lower parts go.  A thread reads only
+        // what it copied itself.
         constexpr int J = N / 8;             // rows of a thread
-        constexpr int JB = J % 4 == 0 ? 4 : 2;
-        auto load = [&](int j, uint32_t (&v)[8]) {  // returns the row of out
-          const int row = row0 + (qt >> 3) + 8 * j;
+        auto raw = [&](int r) {              // this thread's 32 bytes
+          return sq + (ch >> 2) * N * 128 + r * 128 + (ch & 3) * 32;
+        };
+#pragma unroll 1
+        for (int j = 0; j < J; ++j) {
+          const int r = (qt >> 3) + 8 * j, row = row0 + r;
           const int qi = row / shape.g;
           const int out = row < shape.rows ? (p.b * a.Q + qi) * a.Hq +
                                                  p.hk * shape.g +
                                                  (row - qi * shape.g)
                                            : -1;
-          uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
-          if (row < shape.rows && qi < p.l.nq && ch * 16 < a.D) {
-            const uint4* src = reinterpret_cast<const uint4*>(
-                static_cast<const __nv_bfloat16*>(a.q) + (size_t)out * a.D +
-                ch * 16);
-            u0 = src[0];
-            u1 = src[1];
+          const bool live = row < shape.rows && qi < p.l.nq;
+          const bool read = live && ch * 16 < a.D;
+          const uint8_t* src =
+              static_cast<const uint8_t*>(a.q) +
+              (read ? ((size_t)out * a.D + ch * 16) * 2 : 0);
+          const uint32_t dst = tc::smem_u32(raw(r));
+          copy16(dst, src, read);
+          copy16(dst + 16, src + 16, read);
+          if (ch == 0) {
+            g.lim[r] = !live      ? 0x7fffffff
+                       : a.causal ? min(p.l.n, p.l.n - p.l.nq + qi + 1)
+                                  : p.l.n;
+            g.out_row[r] = out;
+            g.on[r] = live;
           }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        auto fetch = [&](int r, uint32_t (&v)[8]) {
+          const uint4 u0 = *reinterpret_cast<const uint4*>(raw(r));
+          const uint4 u1 = *reinterpret_cast<const uint4*>(raw(r) + 16);
           v[0] = u0.x; v[1] = u0.y; v[2] = u0.z; v[3] = u0.w;
           v[4] = u1.x; v[5] = u1.y; v[6] = u1.z; v[7] = u1.w;
-          return out;
-        };
-        auto largest = [&](const uint32_t (&v)[8]) {  // infinite: a NaN
-          float t = 0.f;
+          float t = 0.f;                     // infinite: a NaN
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const float x0 = __uint_as_float(v[k] << 16);
@@ -743,19 +799,14 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
 #pragma unroll
           for (int o = 4; o; o >>= 1)
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-          return t;
+          return t;                          // the row's largest value
         };
         float all = 0.f;
-#pragma unroll 1
-        for (int j0 = 0; j0 < J; j0 += JB) {
-          uint32_t v[JB][8];
-#pragma unroll
-          for (int j = 0; j < JB; ++j) load(j0 + j, v[j]);
-#pragma unroll
-          for (int j = 0; j < JB; ++j) {
-            const float t = largest(v[j]);
-            if (t < INFINITY) all = fmaxf(all, t);
-          }
+#pragma unroll 2
+        for (int j = 0; j < J; ++j) {
+          uint32_t v[8];
+          const float t = fetch((qt >> 3) + 8 * j, v);
+          if (t < INFINITY) all = fmaxf(all, t);
         }
         all = warp_max(all);
         if (lane == 0) m.q_top[warp - 2] = all;
@@ -765,62 +816,47 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
         const int e_all = max((int)(__float_as_uint(all) >> 23) - 127, -100);
         bool own = false;
 #pragma unroll 1
-        for (int j0 = 0; j0 < J; j0 += JB) {
-          uint32_t vv[JB][8];
-          int out_row[JB];
+        for (int j = 0; j < J; ++j) {
+          const int r = (qt >> 3) + 8 * j;
+          uint32_t v[8];
+          const float big = fetch(r, v);  // the whole row has been read now
+          const int e_row = (int)(__float_as_uint(big) >> 23) - 127;
+          int e = e_all;
+          if (big > 0.f && e_row < e_all - 6) {
+            e = max(e_row, max(-100, e_all - 100));
+            own = true;
+          }
+          const float up = big < INFINITY
+                               ? __uint_as_float((134 - e) << 23)
+                               : __uint_as_float(0x7fffffffu);
+          uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int j = 0; j < JB; ++j) out_row[j] = load(j0 + j, vv[j]);
-#pragma unroll
-          for (int j = 0; j < JB; ++j) {
-            const uint32_t(&v)[8] = vv[j];
-            const float big = largest(v);
-            const int r = (qt >> 3) + 8 * (j0 + j);
-            const int e_row = (int)(__float_as_uint(big) >> 23) - 127;
-            int e = e_all;
-            if (big > 0.f && e_row < e_all - 6) {
-              e = max(e_row, max(-100, e_all - 100));
-              own = true;
-            }
-            const float up = big < INFINITY
-                                 ? __uint_as_float((134 - e) << 23)
-                                 : __uint_as_float(0x7fffffffu);
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float2 y =
-                  make_float2(__uint_as_float(v[k] << 16) * up,
-                              __uint_as_float(v[k] & 0xffff0000u) * up);
-              const uint32_t h =
-                  __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-              const float2 f = __half22float2(
-                  __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
-              const uint32_t l =
-                  __nv_cvt_float2_to_fp8x2(make_float2(y.x - f.x, y.y - f.y),
-                                           __NV_SATFINITE, __NV_E4M3);
-              if (k & 1) {
-                hi[k >> 1] |= h << 16;
-                lo[k >> 1] |= l << 16;
-              } else {
-                hi[k >> 1] = h;
-                lo[k >> 1] = l;
-              }
-            }
-            uint8_t* dst = sq + r * 128 + ((ch ^ (r & 7)) << 4);
-            *reinterpret_cast<uint4*>(dst) =
-                make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(dst + N * 128) =
-                make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            if (ch == 0) {
-              const int qi = (row0 + r) / shape.g;
-              const bool live = out_row[j] >= 0 && qi < p.l.nq;
-              g.rel[r] = __uint_as_float((127 + e - e_all) << 23);
-              g.lim[r] = !live      ? 0x7fffffff
-                         : a.causal ? min(p.l.n, p.l.n - p.l.nq + qi + 1)
-                                    : p.l.n;
-              g.out_row[r] = out_row[j];
-              g.on[r] = live;
+          for (int k = 0; k < 8; ++k) {
+            const float2 y =
+                make_float2(__uint_as_float(v[k] << 16) * up,
+                            __uint_as_float(v[k] & 0xffff0000u) * up);
+            const uint32_t h =
+                __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+            const float2 f = __half22float2(
+                __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+            const uint32_t l =
+                __nv_cvt_float2_to_fp8x2(make_float2(y.x - f.x, y.y - f.y),
+                                         __NV_SATFINITE, __NV_E4M3);
+            if (k & 1) {
+              hi[k >> 1] |= h << 16;
+              lo[k >> 1] |= l << 16;
+            } else {
+              hi[k >> 1] = h;
+              lo[k >> 1] = l;
             }
           }
+          uint8_t* dst = sq + r * 128 + ((ch ^ (r & 7)) << 4);
+          __syncwarp();
+          *reinterpret_cast<uint4*>(dst) =
+              make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(dst + N * 128) =
+              make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          if (ch == 0) g.rel[r] = __uint_as_float((127 + e - e_all) << 23);
         }
         own = any_of<64>(kQBar, own);
         if (qt == 0) {
@@ -893,6 +929,8 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
         ok = wait_for(&m.sfull[sb], rs.phase, abort);
         ok = __all_sync(0xffffffffu, ok);
         float y[HR];
+        const int pg = tok >> page_bits;
+        const float ct = m.ct[st][pg] * g.back, lv = m.lv[st][pg];
         if (ok) {
           tc::fence_after_sync();
           const uint32_t s_col = lanes + sb * PL::kScore;
@@ -918,8 +956,6 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
           for (int r = 0; r < HR; ++r) y[r] = 0.f;
         }
         const int pos = (g.t0 + t) * kTile + tok;
-        const int pg = tok >> page_bits;
-        const float ct = m.ct[st][pg] * g.back, lv = m.lv[st][pg];
         if (t == 0) lv_ref = m.lv[st][0];
         const float fl = tc::ex2_approx(fminf(lv_ref - lv, 100.f));
         if (g.uneven) {
@@ -1056,16 +1092,17 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
         if (half_any(bar, !ok)) break;
         tc::fence_after_sync();
       }
+      {
+        float v[HR];
 #pragma unroll
-      for (int r = 0; r < HR; r += 2) {
-        float v0, v1;
-        unpack2(l[r / 2], v0, v1);
-        v0 = warp_sum(v0);
-        v1 = warp_sum(v1);
-        if (lane == 0)
-          *reinterpret_cast<float2*>(
-              &m.warp_val[quarter][row_of(r & ~3) + (r & 3)]) =
-              make_float2(v0, v1);
+        for (int r = 0; r < HR; r += 2) unpack2(l[r / 2], v[r], v[r + 1]);
+        int from = 0;
+        lane_sums<HR, 16>(v, lane, from);
+#pragma unroll
+        for (int i = 0; i < lane_share(HR, 16); ++i) {
+          const int r = from + i;  // some lanes hold the same sums
+          m.warp_val[quarter][row_of(r & ~3) + (r & 3)] = v[i];
+        }
       }
       half_sync(bar);
       const float lift = exp2f(lv_ref);
@@ -1176,9 +1213,13 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int G = min(grid, total);
   const Lens l = lens_of(a, b, &bad);
   before += hk * head_work(a, shape, l);
-  for (int i = 0; i < rt; ++i) before += max(1, tiles_of(a, shape, l, i));
-  const int end = before + max(1, tiles_of(a, shape, l, rt));
-  const int c0 = (int)(((before + 1ll) * G - 1) / total);
+  for (int i = 0; i < rt; ++i)
+    before += kUnitCost + tiles_of(a, shape, l, i);
+  const int tiles = tiles_of(a, shape, l, rt);
+  if (tiles < 2) return;
+  const int head = before + kUnitCost;  // of its first tile
+  const int end = head + tiles;
+  const int c0 = (int)(((head + 1ll) * G - 1) / total);
   const int c1 = (int)(((long long)end * G - 1) / total);  // of tile end - 1
   if (c0 == c1) return;
   const int r = blockIdx.y * kJoinRows + warp;
@@ -1186,8 +1227,8 @@ __global__ void __launch_bounds__(kJoinThreads)
   if (r >= shape.N || row >= shape.rows) return;
   const int n = c1 - c0 + 1;
   // a run's first segment is in its even slot; every part but the first
-  // starts its run
-  const int odd = run_start(total, c0, G) != before;
+  // starts its run, and the first does if no unit before it ends there
+  const int odd = run_start(total, c0, G) < before;
   auto slot = [&](int i) { return 2 * (c0 + i) + (i == 0 ? odd : 0); };
   const float2* ml = reinterpret_cast<const float2*>(
       part + (size_t)2 * grid * shape.N * 128);
@@ -1273,7 +1314,7 @@ cudaError_t launch_paged_attn_tc(const PagedAttnArgs& a, int sms, float* part,
   const Shape s = shape_of(a.Q, a.Hq, a.Hkv);
   const long long most =
       (long long)a.B * a.Hkv * s.row_tiles *
-      (((long long)a.max_pages * a.page + kTile - 1) / kTile + 1);
+      (((long long)a.max_pages * a.page + kTile - 1) / kTile + kUnitCost);
   if (most > 0x7fffffffll) return cudaErrorInvalidValue;
   const int G = std::min(sms, kMaxCtas);
   CUtensorMap mk, mv;
