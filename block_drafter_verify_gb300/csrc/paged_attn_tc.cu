@@ -324,7 +324,7 @@ template <int M>
 __device__ __forceinline__ void tmem_loaded(float (&v)[M]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < M; ++i) asm volatile("" : "+f"(v[i])::"memory");
+  for (int i = 0; i < M; ++i) asm volatile("" : "+f"(v[i]));
 }
 __device__ __forceinline__ void tmem_stored() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -899,8 +899,17 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
       return r < kFull ? half * kFull + r
                        : PL::kGroups * kFull + half * kRest + r - kFull;
     };
+    // The same as offsets from the group's first and first shared row.
+    const int full0 = half * kFull, rest0 = PL::kGroups * kFull + half * kRest;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    auto col_of = [&](uint32_t base, int r) {
+      return r < kFull ? base + full0 + r : base + rest0 + (r - kFull);
+    };
     const uint32_t o_col = lanes + 2 * PL::kScore;
+    const float* ref_full = m.neg_ref + full0;
+    const float* ref_rest = m.neg_ref + rest0;
+    uint8_t* p_full = sp + tok * 16 + full0 * 128;  // 2048 bytes to 16 rows
+    uint8_t* p_rest = sp + tok * 16 + (rest0 >> 4) * 2048 + (rest0 & 12);
     const int my_row = ht < HR ? row_of(ht & ~3) + (ht & 3) : 0;
     constexpr int SG = PL::kScore / N;     // columns of a row's score
     constexpr int OG = PL::kAcc / N;       // and of its accumulator
@@ -914,7 +923,11 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
       if (half_any(bar, !ok)) break;
       const Segment& g = m.seg[qb];
       if (g.done) break;
-      const int T = g.t1 - g.t0;
+      const int T = g.t1 - g.t0, n = g.n;
+      const int mask_from = g.min_lim - g.t0 * kTile;  // tokens from the start
+      const bool uneven = g.uneven;
+      const float back = g.back;
+      int pos = g.t0 * kTile + tok;          // this thread's token
       uint64_t l[HR / 2];   // sums of weights, by pairs of rows
 #pragma unroll
       for (int r = 0; r < HR / 2; ++r) l[r] = 0;
@@ -922,7 +935,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
       if (ht < HR) m.neg_ref[my_row] = 0.f;
       half_sync(bar);
       float lv_ref = 0.f;
-      for (int t = 0; t < T; ++t, rs.next(), rv.next()) {
+      for (int t = 0; t < T; ++t, rs.next(), rv.next(), pos += kTile) {
         const int sb = rs.at, st = rv.at;
         // Also says that the weights' buffer is free: the scores' commit
         // follows the second product of two tiles ago.
@@ -930,17 +943,17 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         float y[HR];
         const int pg = tok >> page_bits;
-        const float ct = m.ct[st][pg] * g.back, lv = m.lv[st][pg];
+        const float ct = m.ct[st][pg] * back, lv = m.lv[st][pg];
         if (ok) {
           tc::fence_after_sync();
           const uint32_t s_col = lanes + sb * PL::kScore;
 #pragma unroll
-          for (int r = 0; r < HR; r += 4) tmem_ld4(s_col + row_of(r), y + r);
+          for (int r = 0; r < HR; r += 4) tmem_ld4(col_of(s_col, r), y + r);
           if constexpr (SG == 2) {
             float z[HR];
 #pragma unroll
             for (int r = 0; r < HR; r += 4)
-              tmem_ld4(s_col + N + row_of(r), z + r);
+              tmem_ld4(col_of(s_col + N, r), z + r);
             tmem_loaded(z);
             tmem_loaded(y);
 #pragma unroll
@@ -955,10 +968,9 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
 #pragma unroll
           for (int r = 0; r < HR; ++r) y[r] = 0.f;
         }
-        const int pos = (g.t0 + t) * kTile + tok;
         if (t == 0) lv_ref = m.lv[st][0];
         const float fl = tc::ex2_approx(fminf(lv_ref - lv, 100.f));
-        if (g.uneven) {
+        if (uneven) {
 #pragma unroll
           for (int r = 0; r < HR; ++r) y[r] *= g.rel[row_of(r & ~3) + (r & 3)];
         }
@@ -966,21 +978,22 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
 #pragma unroll
         for (int r = 0; r < HR; r += 4) {
           const ulonglong2 nr =
-              *reinterpret_cast<const ulonglong2*>(&m.neg_ref[row_of(r)]);
+              *reinterpret_cast<const ulonglong2*>(
+                  r < kFull ? ref_full + r : ref_rest + (r - kFull));
           unpack2(add2(fma2(pack2(y[r], y[r + 1]), ct2, lv2), nr.x), y[r],
                   y[r + 1]);
           unpack2(add2(fma2(pack2(y[r + 2], y[r + 3]), ct2, lv2), nr.y),
                   y[r + 2], y[r + 3]);
         }
-        if ((g.t0 + t + 1) * kTile > g.min_lim) {
+        if ((t + 1) * kTile > mask_from) {
 #pragma unroll
           for (int r = 0; r < HR; ++r)
-            y[r] = pos < min(g.lim[row_of(r & ~3) + (r & 3)], g.n) ? y[r]
-                                                                 : -INFINITY;
+            y[r] = pos < min(g.lim[row_of(r & ~3) + (r & 3)], n) ? y[r]
+                                                               : -INFINITY;
         }
-        float top = -INFINITY;
+        float top = fmaxf(y[0], y[1]);
 #pragma unroll
-        for (int r = 0; r < HR; ++r) top = fmaxf(top, y[r]);
+        for (int r = 2; r < HR; r += 2) top = fmaxf(fmaxf(y[r], y[r + 1]), top);
         if (half_any(bar, t == 0 || top > kRaise || !ok)) {
           // ---- raise the references -------------------------------------
           if (half_any(bar, !ok)) { live = false; break; }
@@ -1040,7 +1053,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
           }
         }
         // ---- the weights, in parts -----------------------------------------
-        uint8_t* dst = sp + sb * kParts * N * 128 + tok * 16;
+        const int p_buf = sb * kParts * N * 128;
         const uint64_t fl2 = pack2(fl, fl);
 #pragma unroll
         for (int r = 0; r < HR; r += 16) {
@@ -1060,11 +1073,10 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
             }
             split(e[0], e[1], e[2], e[3], c[k]);
           }
-          const int row = row_of(r);
 #pragma unroll
           for (int h = 0; h < kParts; ++h) {
             uint8_t* at =
-                dst + h * N * 128 + (row >> 4) * 2048 + (row & 12);
+                (r < kFull ? p_full + r * 128 : p_rest) + p_buf + h * N * 128;
             if (words == 4)
               *reinterpret_cast<uint4*>(at) =
                   make_uint4(c[0][h], c[1][h], c[2][h], c[3][h]);
@@ -1074,7 +1086,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
               *reinterpret_cast<uint32_t*>(at) = c[0][h];
           }
         }
-        if (half == 0 && pos >= g.n && ok) {
+        if (half == 0 && pos >= n && ok) {
           // values past the cache's end may be anything: their weight is 0
           uint4* v = reinterpret_cast<uint4*>(sv + st * kUnitBytes + tok * 128);
 #pragma unroll
