@@ -158,6 +158,29 @@ def _call(name, *args):
         raise DFlashError(name, st)
 
 
+# The target-side calls are made once per layer, so their marshalling is kept
+# short: plain integers for pointers (the declared argument types convert
+# them) and one test per tensor.
+def _at(t, dtype, name):
+    """Address of a contiguous CUDA tensor of `dtype`."""
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    _want(t, dtype, name)
+    return _ptr(t).value
+
+
+def _on(stream):
+    """Handle of a stream, of the current one if None."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
+
+
+def _run(name, st):
+    if st != 0:
+        raise DFlashError(name, st)
+
+
 # --------------------------------------------------------------------------
 # the ABI, one function per entry point
 # --------------------------------------------------------------------------
@@ -420,36 +443,45 @@ def dflash_verify_shard_draw(target_shard, plan, topi, q, shard, v0, T,
 # the target's side of a cycle
 # --------------------------------------------------------------------------
 def _rows(t, dtype, tail, name):
-    """Pointer and row stride of a [rows, *tail] tensor whose rows are
+    """Address and row stride of a [rows, *tail] tensor whose rows are
     contiguous but may lie apart (a slice of a projection's output)."""
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dtype is not dtype:
+        _want(t, dtype, name)
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
-    if tuple(t.shape[1:]) != tail:
-        raise ValueError(f"{name} must be [rows, {tail}], got "
-                         f"{tuple(t.shape)}")
+    if t.dim() != len(tail) + 1:
+        raise ValueError(f"{name} must be [rows, {tail}]")
     step = 1
-    for n, st in zip(reversed(tail), reversed(t.stride()[1:])):
-        if n != 1 and st != step:
+    for i in range(len(tail), 0, -1):
+        n = t.size(i)
+        if n != tail[i - 1]:
+            raise ValueError(f"{name} must be [rows, {tail}], got "
+                             f"{tuple(t.shape)}")
+        if n != 1 and t.stride(i) != step:
             raise ValueError(f"rows of {name} must be contiguous")
         step *= n
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else step
+    return t.data_ptr(), t.stride(0) if t.size(0) > 1 else step
 
 
-def _ptr_of(t, dtype, name):
-    _want(t, dtype, name)
-    return _ptr(t)
+def _heads(t, dtype, H, D, name):
+    """_rows of [rows, H, D], the usual case first."""
+    if (t.dtype is dtype and t.is_cuda and t.dim() == 3 and
+            t.stride(2) == 1 and t.stride(1) == D and t.size(2) == D and
+            t.size(1) == H and t.size(0) > 1):
+        return t.data_ptr(), t.stride(0)
+    return _rows(t, dtype, (H, D), name)
 
 
 def _check_cache(k_codes, v_codes, k_scale, v_scale):
     N, Hkv, page, D = k_codes.shape
     if v_codes.shape != k_codes.shape:
         raise ValueError("k_codes and v_codes must have one shape")
-    for t in (k_scale, v_scale):
-        if tuple(t.shape) != (N, Hkv):
-            raise ValueError("scales must be [num_pages, Hkv]")
+    if k_scale.numel() != N * Hkv or v_scale.numel() != N * Hkv:
+        raise ValueError("scales must be [num_pages, Hkv]")
     return N, Hkv, page, D
+
+
+_F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
 
 
 def dflash_kv_append(q, k, v, cos, sin, pos, n_new, page_table, k_codes,
@@ -464,37 +496,36 @@ def dflash_kv_append(q, k, v, cos, sin, pos, n_new, page_table, k_codes,
     q_out [B,Q,Hq,D] and kv_len [B] i32 outputs."""
     N, Hkv, page, D = _check_cache(k_codes, v_codes, k_scale, v_scale)
     B, max_pages = page_table.shape
-    rows = k.shape[0]
-    if rows % B or v.shape[0] != rows or pos.numel() != B or (
+    rows, dt = k.size(0), k.dtype
+    if rows % B or v.size(0) != rows or pos.numel() != B or (
             kv_len.numel() != B) or (n_new is not None and
                                      n_new.numel() != B):
         raise ValueError("k and v must have B * Q rows; pos, n_new and "
                          "kv_len B entries")
-    kp, ld_k = _rows(k, k.dtype, (Hkv, D), "k")
-    vp, ld_v = _rows(v, k.dtype, (Hkv, D), "v")
+    kp, ld_k = _heads(k, dt, Hkv, D, "k")
+    vp, ld_v = _heads(v, dt, Hkv, D, "v")
     qp, ld_q, Hq, qo = None, 0, Hkv, None
     if q is not None:
-        Hq = q.shape[1]
-        qp, ld_q = _rows(q, k.dtype, (Hq, D), "q")
-        qo = _ptr_of(q_out, k.dtype, "q_out")
-        if q.shape[0] != rows or q_out.numel() != rows * Hq * D:
+        Hq = q.size(1)
+        qp, ld_q = _heads(q, dt, Hq, D, "q")
+        qo = _at(q_out, dt, "q_out")
+        if q.size(0) != rows or q_out.numel() != rows * Hq * D:
             raise ValueError("q and q_out must have B * Q rows")
     rot = max_pos = 0
+    cp = sp = None
     if cos is not None:
-        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
-        if sin.shape != cos.shape:
+        max_pos, rot = cos.size(0), 2 * cos.size(1)
+        if sin.numel() != cos.numel() or 2 * sin.size(1) != rot:
             raise ValueError("cos and sin must have one shape")
-    i32, f32, u8 = torch.int32, torch.float32, torch.uint8
-    _call("dflash_kv_append", qp, kp, vp, ld_q, ld_k, ld_v,
-          None if cos is None else _ptr_of(cos, f32, "cos"),
-          None if cos is None else _ptr_of(sin, f32, "sin"),
-          _ptr_of(pos, i32, "pos"),
-          None if n_new is None else _ptr_of(n_new, i32, "n_new"),
-          _ptr_of(page_table, i32, "page_table"), B, rows // B, Hq, Hkv, D,
-          rot, int(interleaved), max_pos, page, N, max_pages, _dtype(k), qo,
-          _ptr_of(k_codes, u8, "k_codes"), _ptr_of(v_codes, u8, "v_codes"),
-          _ptr_of(k_scale, f32, "k_scale"), _ptr_of(v_scale, f32, "v_scale"),
-          _ptr_of(kv_len, i32, "kv_len"), _stream(stream))
+        cp, sp = _at(cos, _F32, "cos"), _at(sin, _F32, "sin")
+    _run("dflash_kv_append", load().dflash_kv_append(
+        qp, kp, vp, ld_q, ld_k, ld_v, cp, sp, _at(pos, _I32, "pos"),
+        None if n_new is None else _at(n_new, _I32, "n_new"),
+        _at(page_table, _I32, "page_table"), B, rows // B, Hq, Hkv, D, rot,
+        1 if interleaved else 0, max_pos, page, N, max_pages, _dtype(k), qo,
+        _at(k_codes, _U8, "k_codes"), _at(v_codes, _U8, "v_codes"),
+        _at(k_scale, _F32, "k_scale"), _at(v_scale, _F32, "v_scale"),
+        _at(kv_len, _I32, "kv_len"), _on(stream)))
 
 
 def dflash_paged_attn_workspace_bytes(B, Q, Hq, Hkv, D) -> int:
@@ -510,24 +541,24 @@ def dflash_paged_attn(q, k_codes, v_codes, k_scale, v_scale, page_table,
     dflash_paged_attn_workspace_bytes."""
     N, Hkv, page, D = _check_cache(k_codes, v_codes, k_scale, v_scale)
     B, Q, Hq, Dq = q.shape
-    if Dq != D or page_table.shape[0] != B or out.shape != q.shape or (
+    tB, max_pages = page_table.shape
+    if Dq != D or tB != B or out.shape != q.shape or (
             kv_len.numel() != B) or (q_len is not None and
                                      q_len.numel() != B):
         raise ValueError("q, out, page_table, kv_len, q_len and the cache "
                          "must agree in B and D")
     if lse is not None and lse.numel() != B * Q * Hq:
         raise ValueError("lse must be [B, Q, Hq]")
-    i32, f32, u8 = torch.int32, torch.float32, torch.uint8
-    _call("dflash_paged_attn", _ptr(q), _ptr_of(k_codes, u8, "k_codes"),
-          _ptr_of(v_codes, u8, "v_codes"), _ptr_of(k_scale, f32, "k_scale"),
-          _ptr_of(v_scale, f32, "v_scale"),
-          _ptr_of(page_table, i32, "page_table"),
-          _ptr_of(kv_len, i32, "kv_len"),
-          None if q_len is None else _ptr_of(q_len, i32, "q_len"), B, Q, Hq,
-          Hkv, D, page, N, page_table.shape[1], int(causal), float(scale),
-          _dtype(q), _ptr_of(out, q.dtype, "out"),
-          None if lse is None else _ptr_of(lse, f32, "lse"), _ptr(ws),
-          ws.numel(), _stream(stream))
+    dt = q.dtype
+    _run("dflash_paged_attn", load().dflash_paged_attn(
+        _at(q, dt, "q"), _at(k_codes, _U8, "k_codes"),
+        _at(v_codes, _U8, "v_codes"), _at(k_scale, _F32, "k_scale"),
+        _at(v_scale, _F32, "v_scale"), _at(page_table, _I32, "page_table"),
+        _at(kv_len, _I32, "kv_len"),
+        None if q_len is None else _at(q_len, _I32, "q_len"), B, Q, Hq, Hkv,
+        D, page, N, max_pages, 1 if causal else 0, scale, _dtype(q),
+        _at(out, dt, "out"), None if lse is None else _at(lse, _F32, "lse"),
+        _at(ws, _U8, "ws"), ws.numel(), _on(stream)))
 
 
 def dflash_sample_workspace_bytes(R, V) -> int:
@@ -543,24 +574,23 @@ def dflash_sample(logits, temperature, top_k, top_p, min_p, u, token, n_kept,
     dflash_sample_workspace_bytes."""
     R, V = logits.shape
     lp, ld = _rows(logits, logits.dtype, (V,), "logits")
-    i32, f32 = torch.int32, torch.float32
 
     def row(t, dtype, name):
         if t is None:
             return None
         if t.numel() != R:
             raise ValueError(f"{name} must have R entries")
-        return _ptr_of(t, dtype, name)
+        return _at(t, dtype, name)
 
-    if filtered is not None and tuple(filtered.shape) != (R, V):
+    if filtered is not None and filtered.shape != logits.shape:
         raise ValueError("filtered must be [R, V]")
-    _call("dflash_sample", lp, ld, _dtype(logits),
-          row(temperature, f32, "temperature"), row(top_k, i32, "top_k"),
-          row(top_p, f32, "top_p"), row(min_p, f32, "min_p"),
-          row(u, f32, "u"), R, V, row(token, i32, "token"),
-          row(n_kept, i32, "n_kept"),
-          None if filtered is None else _ptr_of(filtered, f32, "filtered"),
-          _ptr(ws), ws.numel(), _stream(stream))
+    _run("dflash_sample", load().dflash_sample(
+        lp, ld, _dtype(logits), row(temperature, _F32, "temperature"),
+        row(top_k, _I32, "top_k"), row(top_p, _F32, "top_p"),
+        row(min_p, _F32, "min_p"), row(u, _F32, "u"), R, V,
+        row(token, _I32, "token"), row(n_kept, _I32, "n_kept"),
+        None if filtered is None else _at(filtered, _F32, "filtered"),
+        _at(ws, _U8, "ws"), ws.numel(), _on(stream)))
 
 
 def dflash_check(stream=None):

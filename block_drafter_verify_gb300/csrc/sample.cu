@@ -9,17 +9,20 @@
 // drawn token do not depend on how the row is split over threads and CTAs.
 //
 // A cluster of CTAs owns a row: each CTA reads its slice from HBM once and
-// keeps it in shared memory, where all later passes run; only histograms,
-// short lists and sums travel between the CTAs (distributed shared memory).
-//   1 load the slice, its largest (key, id); cluster maximum
-//   2 weights: total, and (filters on) a histogram of counts and weights over
-//     bins of (max - l) / T
-//   3 top-k: the bin of the k-th token; its members gathered and ranked
-//   4 top-p: the bin in which the weight passes p W; likewise
-//   5 kept weights by warp chunk, in id order; the draw; filtered logits
-// A bin with more members than the list holds (ties by the thousand, a tail
-// of weightless tokens) is resolved by radix selection on the 64-bit words
-// instead.
+// keeps it in shared memory, where all later passes run; only maxima,
+// histograms, short lists and sums travel between the CTAs (distributed
+// shared memory).  What happens then is the row's own:
+//   T = 0           the first maximum;
+//   top-k           the k-th largest of the threads' own maxima bounds the
+//                   k-th largest token from below, so one comparison per
+//                   token gathers few more than k candidates; one CTA sorts
+//                   them, applies top-p and min-p, and draws among them;
+//   top-p only      a histogram of weights over bins of (max - l) / T finds
+//                   the bin in which the weight passes p W, whose members are
+//                   gathered and ranked; kept weights by warp chunk, the draw;
+//   neither         kept weights by warp chunk, the draw.
+// What overflows a list (ties by the thousand, a tail of weightless tokens)
+// is resolved by radix selection on the 64-bit words instead.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -41,6 +44,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
 constexpr float kBinsPerUnit = 32.f;   // bins of 1/32 in (max - l) / T
 constexpr int kList = 512;             // members of one bin, over the cluster
+constexpr int kCand = 2048;            // top-k candidates, over the cluster
+constexpr int kCandBins = 512;         // bins of 1/16 for their bound
 constexpr int kMaxCluster = 8;
 constexpr float kWeightOne = 17592186044416.f;  // 2^44
 
@@ -87,21 +92,14 @@ __device__ __forceinline__ u64 warp_largest(u64 v) {
 
 struct Shared {
   // written by this CTA, read by the cluster
-  u64 top;               // largest word of the slice
+  float top;             // largest logit of the slice
+  int first;             // T = 0: first token of the slice that has it
   u64 total;             // weight of the slice
   u64 kept_w[kWarps];    // kept weight of each warp's chunk
   uint32_t kept_n;
   uint32_t bad;
-  uint32_t count[kBins];
-  uint32_t w_lo[kBins], w_hi[kBins];
-  u64 list[kList];
   uint32_t listed;
   // this CTA's own
-  uint32_t all_count[kBins];
-  u64 all_w[kBins];
-  u64 all_list[kList];
-  u64 scan_w[kWarps + 1];
-  uint32_t scan_n[kWarps + 1];
   u64 warp_w[kWarps];
   uint32_t warp_n[kWarps];
   int found_bin;
@@ -109,6 +107,21 @@ struct Shared {
   uint32_t found_n;      // tokens before it
   u64 cut;
   u64 kept_before;       // weight of the tokens down to the cut
+  int kept;
+  union {
+    struct {
+      uint32_t count[kBins];              // read by the cluster
+      uint32_t w_lo[kBins], w_hi[kBins];  // read by the cluster
+      u64 list[kList];                    // read by the cluster
+      uint32_t all_count[kBins];
+      u64 all_w[kBins];
+      u64 all_list[kList];
+    };
+    struct {
+      u64 cand[kCand];      // this CTA's candidates
+      u64 all_cand[kCand];  // the row's, in the first CTA
+    };
+  };
 };
 
 // What a row's weights are made from.
@@ -304,6 +317,156 @@ __device__ void bin_cut(Shared& S, cg::cluster_group& cl, const T* data, int n,
   __syncthreads();
 }
 
+// Elements of a 16-byte word.
+template <typename T>
+struct Vec {
+  static constexpr int E = 16 / sizeof(T);
+  uint4 w;
+  __device__ __forceinline__ float at(int k) const {
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(k == 0 ? w.x : k == 1 ? w.y : k == 2 ? w.z : w.w);
+    } else {
+      const uint32_t v = k < 2 ? w.x : k < 4 ? w.y : k < 6 ? w.z : w.w;
+      return __uint_as_float(k & 1 ? v & 0xffff0000u : v << 16);
+    }
+  }
+};
+
+// f(i, logit) over elements [from, to) of the slice for T threads of index t,
+// words of 16 bytes where the data is aligned to them (from always is).
+template <typename T, typename F>
+__device__ __forceinline__ void each(const T* data, bool wide, int from,
+                                     int to, int t, int threads, F f) {
+  constexpr int E = Vec<T>::E;
+  int done = from;
+  if (wide) {
+    const int words = (to - from) / E;
+    const uint4* p = reinterpret_cast<const uint4*>(data + from);
+#pragma unroll 2
+    for (int v = t; v < words; v += threads) {
+      const Vec<T> x{p[v]};
+#pragma unroll
+      for (int k = 0; k < E; ++k) f(from + v * E + k, x.at(k));
+    }
+    done = from + words * E;
+  }
+  for (int i = done + t; i < to; i += threads) f(i, to_f32(data[i]));
+}
+
+// Sorts key[0, n) descending; n at most kCand, entries up to the next power
+// of two are overwritten with 0.  Whole CTA.
+__device__ void sort_down(u64* key, int n) {
+  int P = 2;
+  while (P < n) P *= 2;
+  for (int i = n + threadIdx.x; i < P; i += kThreads) key[i] = 0;
+  __syncthreads();
+  for (int k = 2; k <= P; k *= 2) {
+    for (int j = k / 2; j > 0; j /= 2) {
+      for (int i = threadIdx.x; i < P / 2; i += kThreads) {
+        const int a = 2 * i - (i & (j - 1)), b = a + j;
+        const u64 x = key[a], y = key[b];
+        const bool down = (a & k) == 0;
+        if ((x < y) == down) {
+          key[a] = y;
+          key[b] = x;
+        }
+      }
+      // steps within 64 entries stay within a warp's own entries
+      if (j > 32 || P / 2 > kThreads) __syncthreads();
+      else __syncwarp();
+    }
+    __syncthreads();
+  }
+}
+
+// Exclusive sum over the CTA of v (thread order); *all: the total.
+__device__ u64 cta_scan(Shared& S, u64 v, u64* all) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  u64 run = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 q = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += q;
+  }
+  __syncthreads();
+  if (lane == 31) S.warp_w[wid] = run;
+  __syncthreads();
+  u64 before = 0, total = 0;
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < wid) before += S.warp_w[i];
+    total += S.warp_w[i];
+  }
+  *all = total;
+  return before + run - v;
+}
+
+__device__ __forceinline__ u64 draw_target(float u, u64 total) {
+  const double f = floor((double)u * (double)total);
+  const u64 t = f > 0.0 ? (u64)f : 0;
+  return t >= total ? total - 1 : t;
+}
+__device__ __forceinline__ u64 top_p_bound(float p, u64 total) {
+  const double need = ceil((double)p * (double)total);
+  return need >= 1.0 ? (u64)need : 1;  // the first token is kept
+}
+
+// The row's n candidates (S.all_cand, at least k of its tokens, the largest
+// ones among them) to the kept set's cut, size and weight, and the token.
+// Whole CTA; scratch: S.cand.
+__device__ void pick(Shared& S, const Row& r, int n, int k, float p, float mp,
+                     float u, int* token) {
+  const int tid = threadIdx.x;
+  sort_down(S.all_cand, n);
+  constexpr int kPer = kCand / kThreads;
+  auto x_at = [&](u64 w) { return x_of(of_key((uint32_t)(w >> 32)), r); };
+  float x[kPer];
+  u64 w[kPer], mine = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int i = tid * kPer + j;
+    x[j] = i < k ? x_at(S.all_cand[i]) : 0.f;
+    w[j] = i < k ? weight_of(x[j]) : 0;
+    mine += w[j];
+  }
+  u64 total, before = cta_scan(S, mine, &total);
+  const u64 bound = p < 1.f ? top_p_bound(p, total) : ~0ull;
+  int kept = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int i = tid * kPer + j;
+    if (i < k && (i == 0 || before < bound) && x[j] >= mp) ++kept;
+    before += w[j];
+  }
+  u64 all;
+  cta_scan(S, (u64)kept, &all);
+  kept = (int)all;  // a prefix of the order
+  if (tid == 0) {
+    S.cut = S.all_cand[kept - 1];
+    S.kept = kept;
+  }
+  // the kept tokens by id: the word's lower half is the id's complement
+  for (int i = tid; i < kept; i += kThreads)
+    S.cand[i] = S.all_cand[i] << 32 | (uint32_t)i;
+  __syncthreads();
+  sort_down(S.cand, kept);
+  mine = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int i = tid * kPer + j;
+    w[j] = i < kept ? weight_of(x_at(S.all_cand[(uint32_t)S.cand[i]])) : 0;
+    mine += w[j];
+  }
+  before = cta_scan(S, mine, &total);
+  const u64 target = draw_target(u, total);
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int i = tid * kPer + j;
+    if (w[j] > 0 && target >= before && target < before + w[j])
+      *token = (int)~(uint32_t)(S.cand[i] >> 32);
+    before += w[j];
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     sample_kernel(const __grid_constant__ SampleArgs a) {
@@ -320,86 +483,216 @@ __global__ void __launch_bounds__(kThreads)
   const T* src = static_cast<const T*>(a.logits) + row * a.ld + id0;
   T* own = reinterpret_cast<T*>(smem16 + (sizeof(Shared) + 15) / 16);
   const T* data = a.resident ? own : src;
+  const bool src_wide = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
+  const bool wide = a.resident || src_wide;
 
-  // ---- 1: the slice and the row's maximum --------------------------------
+  // ---- the slice and the row's maximum -------------------------------------
   if (tid == 0) {
     S.bad = 0;
     S.kept_n = 0;
+    S.listed = 0;
+    S.first = 0x7fffffff;
   }
-  for (int i = tid; i < kBins; i += kThreads)
-    S.count[i] = S.w_lo[i] = S.w_hi[i] = 0;
-  u64 top = 0;
+  float top = -INFINITY;
   bool bad = false;
-  constexpr int E = 16 / sizeof(T);  // elements of a 16-byte load
-  const int off = (int)(reinterpret_cast<uintptr_t>(src) & 15) / (int)sizeof(T);
-  const int lead = min(n, (E - off) % E);  // elements before a 16-byte address
-  auto take = [&](int i, float l) {
-    if (l != l || l == INFINITY) bad = true;
-    if (l == l) top = max(top, word_of(l, id0 + i));
+  auto take = [&](float l) {
+    bad |= !(l < INFINITY);  // NaN, too
+    top = fmaxf(top, l);     // passes over a NaN
   };
-  for (int i = tid; i < lead; i += kThreads) {
-    const T x = src[i];
-    if (a.resident) own[i] = x;
-    take(i, to_f32(x));
-  }
-  const int quads = (n - lead) / E;
+  if (src_wide) {
+    constexpr int E = Vec<T>::E;
+    const int words = n / E;
+    const uint4* p = reinterpret_cast<const uint4*>(src);
 #pragma unroll 4
-  for (int v = tid; v < quads; v += kThreads) {
-    const uint4 w = reinterpret_cast<const uint4*>(src + lead)[v];
-    const T* x = reinterpret_cast<const T*>(&w);
+    for (int v = tid; v < words; v += kThreads) {
+      const Vec<T> x{p[v]};
+      if (a.resident) reinterpret_cast<uint4*>(own)[v] = x.w;
 #pragma unroll
-    for (int k = 0; k < E; ++k) {
-      if (a.resident) own[lead + v * E + k] = x[k];
-      take(lead + v * E + k, to_f32(x[k]));
+      for (int k = 0; k < E; ++k) take(x.at(k));
+    }
+    for (int i = words * E + tid; i < n; i += kThreads) {
+      const T x = src[i];
+      if (a.resident) own[i] = x;
+      take(to_f32(x));
+    }
+  } else {
+#pragma unroll 8
+    for (int i = tid; i < n; i += kThreads) {
+      const T x = src[i];
+      if (a.resident) own[i] = x;
+      take(to_f32(x));
     }
   }
-  for (int i = lead + quads * E + tid; i < n; i += kThreads) {
-    const T x = src[i];
-    if (a.resident) own[i] = x;
-    take(i, to_f32(x));
-  }
-  top = warp_largest(top);
-  if (lane == 0) S.warp_w[wid] = top;
+  const float my_top = top;  // of this thread's tokens
+  top = warp_max(top);
+  if (lane == 0) S.warp_w[wid] = __float_as_uint(top);
   __syncthreads();
   if (bad) S.bad = 1;
   if (tid == 0) {
-    for (int i = 1; i < kWarps; ++i) top = max(top, S.warp_w[i]);
+    for (int i = 1; i < kWarps; ++i)
+      top = fmaxf(top, __uint_as_float((uint32_t)S.warp_w[i]));
     S.top = top;
   }
   cl.sync();
-  for (int c = 0; c < C; ++c) top = max(top, cl.map_shared_rank(&S, c)->top);
-  top = warp_largest(top);
+  top = lane < C ? cl.map_shared_rank(&S, lane)->top : -INFINITY;
+  top = warp_max(top);
 
   Row r;
   const float t = a.temperature[row];
-  r.top = of_key((uint32_t)(top >> 32));
+  r.top = top;
   r.greedy = !(t > 0.f && t < INFINITY);
   r.inv_t = r.greedy ? 0.f : __fdiv_rn(1.f, t);
-  const bool empty = top >> 32 <= kKeyNegInf;
-  if (tid == 0) {
-    if (S.bad || empty || !(t >= 0.f && t < INFINITY))
-      raise_error(a.err, kErrNonfinite);
-  }
+  const bool empty = top == -INFINITY;
+  if (tid == 0 && (S.bad || empty || !(t >= 0.f && t < INFINITY)))
+    raise_error(a.err, kErrNonfinite);
   const int k = a.top_k ? a.top_k[row] : 0;
   const float p = a.top_p ? a.top_p[row] : 1.f;
-  const float mp = a.min_p ? a.min_p[row] : 0.f;
+  // at most 1 (which keeps the maximum), 0 for what is no number
+  const float mp = a.min_p && a.min_p[row] > 0.f ? fminf(a.min_p[row], 1.f)
+                                                 : 0.f;
+  const float u = a.u[row];
   const bool by_k = !r.greedy && !empty && k > 0 && k < a.V;
   const bool by_p = !r.greedy && !empty && p < 1.f;
-  u64 cut = empty ? ~0ull : r.greedy ? top : 0;
+  float* dst = a.filtered ? a.filtered + (size_t)row * a.V + id0 : nullptr;
+  // the slice's filtered logits: those not below the cut, given as a word
+  auto filter = [&](u64 cut) {
+    const float lc = of_key((uint32_t)(cut >> 32));
+    const int last = (int)~(uint32_t)cut;  // of the tokens with that logit
+    if (a.resident && (reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
+      const int words = n / 4;
+#pragma unroll 2
+      for (int v = tid; v < words; v += kThreads) {
+        float f[4];
+        if constexpr (sizeof(T) == 4) {
+          const float4 x = reinterpret_cast<const float4*>(own)[v];
+          f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+        } else {
+          const uint2 x = reinterpret_cast<const uint2*>(own)[v];
+          f[0] = __uint_as_float(x.x << 16);
+          f[1] = __uint_as_float(x.x & 0xffff0000u);
+          f[2] = __uint_as_float(x.y << 16);
+          f[3] = __uint_as_float(x.y & 0xffff0000u);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          f[j] = f[j] > lc || (f[j] == lc && id0 + 4 * v + j <= last)
+                     ? f[j] : -INFINITY;
+        reinterpret_cast<float4*>(dst)[v] =
+            make_float4(f[0], f[1], f[2], f[3]);
+      }
+      for (int i = words * 4 + tid; i < n; i += kThreads) {
+        const float l = to_f32(own[i]);
+        dst[i] = l > lc || (l == lc && id0 + i <= last) ? l : -INFINITY;
+      }
+    } else {
+      for (int i = tid; i < n; i += kThreads) {
+        const float l = to_f32(data[i]);
+        dst[i] = l > lc || (l == lc && id0 + i <= last) ? l : -INFINITY;
+      }
+    }
+  };
 
-  // ---- 2-4: the cut --------------------------------------------------------
-  if (by_k || by_p) {  // uniform over the cluster
+  // ---- T = 0, or nothing to draw from --------------------------------------
+  if (r.greedy || empty) {  // uniform over the cluster
+    int first = 0x7fffffff;
+    if (!empty)
+      each(data, wide, 0, n, tid, kThreads, [&](int i, float l) {
+        if (l == top) first = min(first, id0 + i);
+      });
+    if (first != 0x7fffffff) atomicMin(&S.first, first);
+    cl.sync();
+    first = lane < C ? cl.map_shared_rank(&S, lane)->first : 0x7fffffff;
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+      first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
+    if (rank == 0 && tid == 0) {
+      a.token[row] = empty ? -1 : first;
+      if (a.n_kept) a.n_kept[row] = empty ? 0 : 1;
+    }
+    if (dst) filter(empty ? ~0ull : word_of(top, first));
+    cl.sync();  // no CTA leaves while another reads its maximum
+    return;
+  }
+
+  // ---- top-k: candidates, sorted and drawn from by the first CTA -----------
+  if (by_k && k <= kCand) {
+    for (int i = tid; i < kCandBins; i += kThreads) S.count[i] = 0;
+    __syncthreads();
+    // bins of the threads' maxima, half as fine as the weights' bins
+    if (my_top > -INFINITY) {
+      const int bin = bin_of(my_top, r) / (kBins / kCandBins);
+      atomicAdd(&S.count[bin], 1u);
+    }
+    cl.sync();
+    for (int i = tid; i < kCandBins; i += kThreads) {
+      uint32_t c = 0;
+      for (int q = 0; q < C; ++q) c += cl.map_shared_rank(&S, q)->count[i];
+      S.all_count[i] = c;
+      S.all_w[i] = 0;
+    }
+    __syncthreads();
+    find_bin(S, kCandBins, false, (uint32_t)k, 0);
+    const int bin = S.found_bin;
+    cl.sync();  // the counts have been read; the lists take their place
+    bool fits = bin >= 0 && bin < kCandBins - 1;
+    if (fits) {
+      // a logit below every one of the bins up to `bin`: their z is less
+      // than (bin + 1) / 16, with room for the roundings of z
+      const float z = (float)(bin + 1) * (kBins / kCandBins) / kBinsPerUnit;
+      const float low = r.top - z * t * 1.0001f - fabsf(r.top) * 1e-6f;
+      each(data, wide, 0, n, tid, kThreads, [&](int i, float l) {
+        if (l >= low && l > -INFINITY) {
+          const uint32_t at = atomicAdd(&S.listed, 1u);
+          if (at < kCand) S.cand[at] = word_of(l, id0 + i);
+        }
+      });
+      __syncthreads();
+      cl.sync();
+      uint32_t at = 0, all = 0;
+      for (int q = 0; q < C; ++q) {
+        const uint32_t c = cl.map_shared_rank(&S, q)->listed;
+        if (q < rank) at += c;
+        all += c;
+      }
+      fits = all <= kCand;  // the same in every CTA
+      if (fits) {
+        u64* to = cl.map_shared_rank(S.all_cand, 0);
+        for (uint32_t i = tid; i < S.listed; i += kThreads)
+          to[at + i] = S.cand[i];
+        cl.sync();
+        if (rank == 0) {
+          // top-k of fewer tokens than k keeps them all
+          pick(S, r, (int)all, min(k, (int)all), p, mp, u, a.token + row);
+          if (tid == 0 && a.n_kept) a.n_kept[row] = S.kept;
+          __syncthreads();
+          if (dst && tid < C) cl.map_shared_rank(&S, tid)->cut = S.cut;
+        }
+        if (dst) {
+          cl.sync();
+          filter(S.cut);
+        }
+        return;  // nothing of another CTA is read any more
+      }
+    }
+    cl.sync();
+  }
+
+  // ---- the cut by histogram of weights --------------------------------------
+  u64 cut = 0;
+  if (by_k || by_p) {
+    for (int i = tid; i < kBins; i += kThreads)
+      S.count[i] = S.w_lo[i] = S.w_hi[i] = 0;
+    __syncthreads();
     auto fill = [&] {
       u64 sum = 0;
-      for (int i = tid; i < n; i += kThreads) {
-        const float l = logit_at(data, i);
-        if (!(l > -INFINITY)) continue;
+      each(data, wide, 0, n, tid, kThreads, [&](int i, float l) {
+        if (!(l > -INFINITY)) return;
         const u64 w = weight_of(x_of(l, r));
         const int bin = bin_of(l, r);
         sum += w;
         atomicAdd(&S.count[bin], 1u);
         add_weight(S, bin, w);
-      }
+      });
       return sum;
     };
     bool redo = false;  // a radix selection has overwritten the histogram
@@ -424,8 +717,7 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
     if (by_p) {
-      double need = ceil((double)p * (double)total);
-      const u64 bound = need >= 1.0 ? (u64)need : 1;  // the first is kept
+      const u64 bound = top_p_bound(p, total);
       // The tokens past the top-k cut may stay in the histogram: bound is at
       // most the weight before them.
       if (redo) {
@@ -440,24 +732,24 @@ __global__ void __launch_bounds__(kThreads)
       cut = max(cut, S.cut);
     }
   }
-  const bool by_m = !r.greedy && mp > 0.f;
-  auto keeps = [&](float l, int i) {
-    return l > -INFINITY && word_of(l, id0 + i) >= cut &&
-           (!by_m || x_of(l, r) >= mp);
+  const bool by_m = mp > 0.f;
+  auto keeps = [&](float l, int i, float x) {
+    return l > -INFINITY && (cut == 0 || word_of(l, id0 + i) >= cut) &&
+           (!by_m || x >= mp);
   };
 
-  // ---- 5: kept weights in id order, the draw, the filtered logits ---------
+  // ---- kept weights in id order, the draw, the filtered logits -------------
   int c0, c1;
   warp_chunk(n, wid, &c0, &c1);
   u64 sum = 0;
   uint32_t cnt = 0;
-  for (int i = c0 + lane; i < c1; i += 32) {
-    const float l = logit_at(data, i);
-    if (keeps(l, i)) {
-      sum += weight_of(x_of(l, r));
+  each(data, wide, c0, c1, lane, 32, [&](int i, float l) {
+    const float x = x_of(l, r);
+    if (keeps(l, i, x)) {
+      sum += weight_of(x);
       ++cnt;
     }
-  }
+  });
   sum = warp_total(sum);
   cnt = warp_total(cnt);
   if (lane == 0) {
@@ -465,13 +757,11 @@ __global__ void __launch_bounds__(kThreads)
     if (cnt) atomicAdd(&S.kept_n, cnt);
   }
   cl.sync();
-  if (a.filtered) {
-    float* dst = a.filtered + (size_t)row * a.V + id0;
+  if (dst)
     for (int i = tid; i < n; i += kThreads) {
-      const float l = logit_at(data, i);
-      dst[i] = keeps(l, i) ? l : -INFINITY;
+      const float l = to_f32(data[i]);
+      dst[i] = keeps(l, i, by_m ? x_of(l, r) : 1.f) ? l : -INFINITY;
     }
-  }
   if (wid == 0) {
     // kept weight of every (CTA, warp) chunk in id order: lane handles four
     constexpr int kPer = kMaxCluster * kWarps / 32;
@@ -495,42 +785,38 @@ __global__ void __launch_bounds__(kThreads)
       uint32_t nk = lane < C ? cl.map_shared_rank(&S, lane)->kept_n : 0;
       nk = warp_total(nk);
       if (lane == 0 && a.n_kept) a.n_kept[row] = (int)nk;
-      if (lane == 0 && total == 0) a.token[row] = -1;
     }
-    if (total > 0) {
-      const double f = floor((double)a.u[row] * (double)total);
-      u64 target = f > 0.0 ? (u64)f : 0;
-      if (target >= total) target = total - 1;
-      u64 before = run - mine;
-      int hit = -1;
+    const u64 target = draw_target(u, total);
+    u64 before = run - mine;
+    int hit = -1;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        if (hit < 0 && target >= before && target < before + w[j])
-          hit = lane * kPer + j;
-        if (hit < 0) before += w[j];
-      }
-      const unsigned who = __ballot_sync(0xffffffffu, hit >= 0);
-      const int from = __ffs(who) - 1;
-      hit = __shfl_sync(0xffffffffu, hit, from);
-      before = __shfl_sync(0xffffffffu, before, from);
-      if (hit / kWarps == rank) {  // the chunk is in this CTA's slice
-        warp_chunk(n, hit % kWarps, &c0, &c1);
-        for (int base = c0; base < c1; base += 32) {
-          const int i = base + lane;
-          const float l = i < c1 ? logit_at(data, i) : -INFINITY;
-          u64 v = i < c1 && keeps(l, i) ? weight_of(x_of(l, r)) : 0;
-          const u64 one = v;
+    for (int j = 0; j < kPer; ++j) {
+      if (hit < 0 && target >= before && target < before + w[j])
+        hit = lane * kPer + j;
+      if (hit < 0) before += w[j];
+    }
+    const unsigned who = __ballot_sync(0xffffffffu, hit >= 0);
+    const int from = __ffs(who) - 1;
+    hit = __shfl_sync(0xffffffffu, hit, from);
+    before = __shfl_sync(0xffffffffu, before, from);
+    if (hit / kWarps == rank) {  // the chunk is in this CTA's slice
+      warp_chunk(n, hit % kWarps, &c0, &c1);
+      for (int base = c0; base < c1; base += 32) {
+        const int i = base + lane;
+        const float l = i < c1 ? to_f32(data[i]) : -INFINITY;
+        const float x = x_of(l, r);
+        u64 v = i < c1 && keeps(l, i, x) ? weight_of(x) : 0;
+        const u64 one = v;
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const u64 q = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += q;
-          }
-          const bool here = one > 0 && target >= before + v - one &&
-                            target < before + v;
-          if (here) a.token[row] = id0 + i;
-          if (__any_sync(0xffffffffu, here)) break;
-          before += __shfl_sync(0xffffffffu, v, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+          const u64 q = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += q;
         }
+        const bool here = one > 0 && target >= before + v - one &&
+                          target < before + v;
+        if (here) a.token[row] = id0 + i;
+        if (__any_sync(0xffffffffu, here)) break;
+        before += __shfl_sync(0xffffffffu, v, 31);
       }
     }
   }

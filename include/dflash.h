@@ -617,7 +617,7 @@ size_t dflash_sample_workspace_bytes(int R, int V);
  *   top-k (0 < k): the first k tokens
  *   top-p (p < 1): of those (total weight W), the tokens whose preceding
  *         tokens weigh less than ceil(p W) (products in fp64); never none
- *   min-p (0 < m): of those, the tokens with x_v >= m
+ *   min-p (0 < m, at most 1): of those, the tokens with x_v >= m
  *   token = the smallest id whose running kept weight, in id order, exceeds
  *         floor(u W'), W' the kept tokens' weight.
  * T = 0 keeps the first maximum only.
