@@ -9,17 +9,20 @@
 // drawn token do not depend on how the row is split over threads and CTAs.
 //
 // A cluster of CTAs owns a row: each CTA reads its slice from HBM once and
-// keeps it in shared memory, where all later passes run; only maxima,
-// histograms, short lists and sums travel between the CTAs (distributed
-// shared memory).  What happens then is the row's own:
+// keeps it in shared memory (by bulk copies: more bytes in flight than its
+// threads could have), where all later passes run; only maxima, histograms,
+// short lists and sums travel between the CTAs (distributed shared memory).
+// What happens then is the row's own:
 //   T = 0           the first maximum;
 //   top-k           the k-th largest of the threads' own maxima bounds the
 //                   k-th largest token from below, so one comparison per
-//                   token gathers few more than k candidates; one CTA sorts
-//                   them, applies top-p and min-p, and draws among them;
+//                   token gathers few more than k candidates (with small k
+//                   each CTA takes its own bound, which spares two cluster
+//                   barriers); one CTA sorts them, applies top-p and min-p,
+//                   and draws among them;
 //   top-p only      a histogram of weights over bins of (max - l) / T finds
 //                   the bin in which the weight passes p W, whose members are
-//                   gathered and ranked; kept weights by warp chunk, the draw;
+//                   gathered and sorted; kept weights by warp chunk, the draw;
 //   neither         kept weights by warp chunk, the draw.
 // What overflows a list (ties by the thousand, a tail of weightless tokens)
 // is resolved by radix selection on the 64-bit words instead.
@@ -28,6 +31,7 @@
 #include <algorithm>
 
 #include "kernels.h"
+#include "tc_ptx.cuh"
 
 namespace dflash {
 
@@ -43,8 +47,10 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
 constexpr float kBinsPerUnit = 32.f;   // bins of 1/32 in (max - l) / T
-constexpr int kList = 512;             // members of one bin, over the cluster
-constexpr int kCand = 2048;            // top-k candidates, over the cluster
+constexpr int kCand = 2048;            // candidates, over the cluster
+constexpr int kOwnBound = 128;         // largest k for a bound of each CTA
+constexpr int kChunks = 4;             // copies of a slice
+constexpr uint64_t kWait = 2000000000ull;  // 2 s
 constexpr int kCandBins = 512;         // bins of 1/16 for their bound
 constexpr int kMaxCluster = 8;
 constexpr float kWeightOne = 17592186044416.f;  // 2^44
@@ -99,6 +105,7 @@ struct Shared {
   uint32_t kept_n;
   uint32_t bad;
   uint32_t listed;
+  uint64_t landed[kChunks];  // barriers of the slice's copies
   // this CTA's own
   u64 warp_w[kWarps];
   uint32_t warp_n[kWarps];
@@ -112,10 +119,8 @@ struct Shared {
     struct {
       uint32_t count[kBins];              // read by the cluster
       uint32_t w_lo[kBins], w_hi[kBins];  // read by the cluster
-      u64 list[kList];                    // read by the cluster
       uint32_t all_count[kBins];
       u64 all_w[kBins];
-      u64 all_list[kList];
     };
     struct {
       u64 cand[kCand];      // this CTA's candidates
@@ -266,57 +271,6 @@ __device__ void radix_cut(Shared& S, cg::cluster_group& cl, const T* data,
   __syncthreads();
 }
 
-// The cut in the found bin of the z histogram: its members gathered over
-// the cluster and ranked, or radix selection if there are too many.
-template <typename T>
-__device__ void bin_cut(Shared& S, cg::cluster_group& cl, const T* data, int n,
-                        int id0, const Row& r, bool by_weight, uint32_t need_n,
-                        u64 need_w) {
-  const int tid = threadIdx.x;
-  const int bin = S.found_bin;
-  const uint32_t members = S.all_count[bin];
-  const uint32_t before_n = S.found_n;
-  const u64 before_w = S.found_w;
-  if (members > kList) {  // uniform over the cluster
-    radix_cut(S, cl, data, n, id0, r, by_weight, need_n, need_w);
-    return;
-  }
-  if (tid == 0) S.listed = 0;
-  __syncthreads();
-  for (int i = tid; i < n; i += kThreads) {
-    const float l = logit_at(data, i);
-    if (l > -INFINITY && bin_of(l, r) == bin)
-      S.list[atomicAdd(&S.listed, 1u)] = word_of(l, id0 + i);
-  }
-  cl.sync();
-  const int C = cl.num_blocks();
-  uint32_t at = 0;
-  for (int c = 0; c < C; ++c) {
-    const Shared* o = cl.map_shared_rank(&S, c);
-    const uint32_t m = o->listed;
-    for (uint32_t i = tid; i < m; i += kThreads) S.all_list[at + i] = o->list[i];
-    at += m;
-  }
-  cl.sync();  // also a barrier of this CTA
-  for (uint32_t i = tid; i < members; i += kThreads) {
-    const u64 w = S.all_list[i];
-    uint32_t rank = before_n;
-    u64 sum = before_w;
-    for (uint32_t j = 0; j < members; ++j) {
-      const u64 o = S.all_list[j];
-      if (o > w) {
-        ++rank;
-        sum += weight_of(x_of(of_key((uint32_t)(o >> 32)), r));
-      }
-    }
-    const u64 own = weight_of(x_of(of_key((uint32_t)(w >> 32)), r));
-    const bool last = by_weight ? sum < need_w && sum + own >= need_w
-                                : rank + 1 == need_n;
-    if (last) { S.cut = w; S.kept_before = sum + own; }
-  }
-  __syncthreads();
-}
-
 // Elements of a 16-byte word.
 template <typename T>
 struct Vec {
@@ -410,6 +364,87 @@ __device__ __forceinline__ u64 top_p_bound(float p, u64 total) {
   return need >= 1.0 ? (u64)need : 1;  // the first token is kept
 }
 
+// Gathers this CTA's S.cand[0, S.listed) of every CTA into S.all_cand of
+// the first; *all: how many, over the cluster.  False (and nothing moved) if
+// that is more than kCand.  Barriers: the lists are complete before, and
+// everything of other CTAs has been read after.
+__device__ bool collect(Shared& S, cg::cluster_group& cl, int* all) {
+  cl.sync();
+  const int C = cl.num_blocks(), rank = cl.block_rank();
+  uint32_t at = 0, n = 0;
+  for (int q = 0; q < C; ++q) {
+    const uint32_t c = cl.map_shared_rank(&S, q)->listed;
+    if (q < rank) at += c;
+    n += c;
+  }
+  *all = (int)n;
+  const bool fits = n <= kCand;  // the same in every CTA
+  if (fits) {
+    u64* to = cl.map_shared_rank(S.all_cand, 0);
+    for (uint32_t i = threadIdx.x; i < S.listed; i += kThreads)
+      to[at + i] = S.cand[i];
+  }
+  cl.sync();
+  return fits;
+}
+
+// The cut in the found bin of the histogram: its members gathered in the
+// first CTA and sorted, or radix selection if there are too many.  The
+// histogram is lost.
+template <typename T>
+__device__ void bin_cut(Shared& S, cg::cluster_group& cl, const T* data,
+                        bool wide, int n, int id0, const Row& r, bool by_weight,
+                        uint32_t need_n, u64 need_w) {
+  const int tid = threadIdx.x;
+  const int bin = S.found_bin;
+  const uint32_t before_n = S.found_n;
+  const u64 before_w = S.found_w;
+  if (tid == 0) S.listed = 0;
+  __syncthreads();
+  each(data, wide, 0, n, tid, kThreads, [&](int i, float l) {
+    if (l > -INFINITY && bin_of(l, r) == bin) {
+      const uint32_t at = atomicAdd(&S.listed, 1u);
+      if (at < kCand) S.cand[at] = word_of(l, id0 + i);
+    }
+  });
+  __syncthreads();
+  int all;
+  if (!collect(S, cl, &all)) {
+    radix_cut(S, cl, data, n, id0, r, by_weight, need_n, need_w);
+    return;
+  }
+  if (cl.block_rank() == 0) {
+    sort_down(S.all_cand, all);
+    constexpr int kPer = kCand / kThreads;
+    u64 w[kPer], mine = 0, total;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = tid * kPer + j;
+      w[j] = i < all ? weight_of(x_of(of_key((uint32_t)(S.all_cand[i] >> 32)),
+                                      r))
+                     : 0;
+      mine += w[j];
+    }
+    u64 before = before_w + cta_scan(S, mine, &total);
+    const int C = cl.num_blocks();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = tid * kPer + j;
+      const bool last =
+          i < all && (by_weight ? before < need_w && before + w[j] >= need_w
+                                : before_n + i + 1 == need_n);
+      if (last)
+        for (int q = 0; q < C; ++q) {
+          Shared* o = cl.map_shared_rank(&S, q);
+          o->cut = S.all_cand[i];
+          o->kept_before = before + w[j];
+        }
+      before += w[j];
+    }
+  }
+  cl.sync();
+}
+
 // The row's n candidates (S.all_cand, at least k of its tokens, the largest
 // ones among them) to the kept set's cut, size and weight, and the token.
 // Whole CTA; scratch: S.cand.
@@ -492,29 +527,56 @@ __global__ void __launch_bounds__(kThreads)
     S.kept_n = 0;
     S.listed = 0;
     S.first = 0x7fffffff;
+    for (int i = 0; i < kChunks; ++i) tc::mbar_init(&S.landed[i], 1);
+    tc::fence_mbar_init();
   }
+  __syncthreads();
   float top = -INFINITY;
   bool bad = false;
   auto take = [&](float l) {
     bad |= !(l < INFINITY);  // NaN, too
     top = fmaxf(top, l);     // passes over a NaN
   };
-  if (src_wide) {
+  if (src_wide && a.resident) {
+    constexpr int E = Vec<T>::E;
+    const int words = n / E, per = (words + kChunks - 1) / kChunks;
+    if (tid == 0)
+      for (int c = 0; c < kChunks; ++c) {
+        const int v0 = min(words, c * per), v1 = min(words, v0 + per);
+        tc::mbar_arrive_expect_tx(&S.landed[c], (v1 - v0) * 16);
+        if (v1 > v0)
+          tc::bulk_load(reinterpret_cast<uint4*>(own) + v0,
+                        reinterpret_cast<const uint4*>(src) + v0,
+                        (v1 - v0) * 16, &S.landed[c]);
+      }
+    int give_up = 0;
+    for (int c = 0; c < kChunks; ++c) {
+      if (!tc::mbar_wait_bounded(&S.landed[c], 0, &give_up, kWait))
+        raise_error(a.err, kErrTimeout);
+      const int v1 = min(words, (c + 1) * per);
+#pragma unroll 4
+      for (int v = min(words, c * per) + tid; v < v1; v += kThreads) {
+        const Vec<T> x{reinterpret_cast<const uint4*>(own)[v]};
+#pragma unroll
+        for (int k = 0; k < E; ++k) take(x.at(k));
+      }
+    }
+    for (int i = words * E + tid; i < n; i += kThreads) {
+      const T x = src[i];
+      own[i] = x;
+      take(to_f32(x));
+    }
+  } else if (src_wide) {
     constexpr int E = Vec<T>::E;
     const int words = n / E;
     const uint4* p = reinterpret_cast<const uint4*>(src);
 #pragma unroll 4
     for (int v = tid; v < words; v += kThreads) {
       const Vec<T> x{p[v]};
-      if (a.resident) reinterpret_cast<uint4*>(own)[v] = x.w;
 #pragma unroll
       for (int k = 0; k < E; ++k) take(x.at(k));
     }
-    for (int i = words * E + tid; i < n; i += kThreads) {
-      const T x = src[i];
-      if (a.resident) own[i] = x;
-      take(to_f32(x));
-    }
+    for (int i = words * E + tid; i < n; i += kThreads) take(to_f32(src[i]));
   } else {
 #pragma unroll 8
     for (int i = tid; i < n; i += kThreads) {
@@ -616,65 +678,66 @@ __global__ void __launch_bounds__(kThreads)
 
   // ---- top-k: candidates, sorted and drawn from by the first CTA -----------
   if (by_k && k <= kCand) {
-    for (int i = tid; i < kCandBins; i += kThreads) S.count[i] = 0;
+    // bins of the threads' maxima, half as fine as the weights' bins; below
+    // the slice's own maximum where each CTA takes its own bound
+    const bool own_bound = k <= kOwnBound;
+    Row b = r;
+    if (own_bound) b.top = S.top;
+    for (int i = tid; i < kCandBins; i += kThreads) {
+      S.count[i] = 0;
+      S.all_w[i] = 0;
+    }
     __syncthreads();
-    // bins of the threads' maxima, half as fine as the weights' bins
     if (my_top > -INFINITY) {
-      const int bin = bin_of(my_top, r) / (kBins / kCandBins);
+      const int bin = bin_of(my_top, b) / (kBins / kCandBins);
       atomicAdd(&S.count[bin], 1u);
     }
-    cl.sync();
-    for (int i = tid; i < kCandBins; i += kThreads) {
-      uint32_t c = 0;
-      for (int q = 0; q < C; ++q) c += cl.map_shared_rank(&S, q)->count[i];
-      S.all_count[i] = c;
-      S.all_w[i] = 0;
+    if (own_bound) {
+      __syncthreads();
+      for (int i = tid; i < kCandBins; i += kThreads)
+        S.all_count[i] = S.count[i];
+    } else {
+      cl.sync();
+      for (int i = tid; i < kCandBins; i += kThreads) {
+        uint32_t c = 0;
+        for (int q = 0; q < C; ++q) c += cl.map_shared_rank(&S, q)->count[i];
+        S.all_count[i] = c;
+      }
     }
     __syncthreads();
     find_bin(S, kCandBins, false, (uint32_t)k, 0);
     const int bin = S.found_bin;
-    cl.sync();  // the counts have been read; the lists take their place
-    bool fits = bin >= 0 && bin < kCandBins - 1;
-    if (fits) {
-      // a logit below every one of the bins up to `bin`: their z is less
-      // than (bin + 1) / 16, with room for the roundings of z
-      const float z = (float)(bin + 1) * (kBins / kCandBins) / kBinsPerUnit;
-      const float low = r.top - z * t * 1.0001f - fabsf(r.top) * 1e-6f;
-      each(data, wide, 0, n, tid, kThreads, [&](int i, float l) {
-        if (l >= low && l > -INFINITY) {
-          const uint32_t at = atomicAdd(&S.listed, 1u);
-          if (at < kCand) S.cand[at] = word_of(l, id0 + i);
-        }
-      });
-      __syncthreads();
-      cl.sync();
-      uint32_t at = 0, all = 0;
-      for (int q = 0; q < C; ++q) {
-        const uint32_t c = cl.map_shared_rank(&S, q)->listed;
-        if (q < rank) at += c;
-        all += c;
+    // the counts have been read; the lists take their place
+    if (own_bound) __syncthreads();
+    else cl.sync();
+    // A logit below every one of the bins up to `bin`: their z is less than
+    // (bin + 1) / 16, with room for the roundings of z.  No such bin: all.
+    const float z = (float)(bin + 1) * (kBins / kCandBins) / kBinsPerUnit;
+    const float low = bin < 0 || bin == kCandBins - 1
+                          ? -INFINITY
+                          : b.top - z * t * 1.0001f - fabsf(b.top) * 1e-6f;
+    each(data, wide, 0, n, tid, kThreads, [&](int i, float l) {
+      if (l >= low && l > -INFINITY) {
+        const uint32_t at = atomicAdd(&S.listed, 1u);
+        if (at < kCand) S.cand[at] = word_of(l, id0 + i);
       }
-      fits = all <= kCand;  // the same in every CTA
-      if (fits) {
-        u64* to = cl.map_shared_rank(S.all_cand, 0);
-        for (uint32_t i = tid; i < S.listed; i += kThreads)
-          to[at + i] = S.cand[i];
+    });
+    __syncthreads();
+    int all;
+    if (collect(S, cl, &all)) {
+      if (rank == 0) {
+        // top-k of fewer tokens than k keeps them all
+        pick(S, r, all, min(k, all), p, mp, u, a.token + row);
+        if (tid == 0 && a.n_kept) a.n_kept[row] = S.kept;
+        __syncthreads();
+        if (dst && tid < C) cl.map_shared_rank(&S, tid)->cut = S.cut;
+      }
+      if (dst) {
         cl.sync();
-        if (rank == 0) {
-          // top-k of fewer tokens than k keeps them all
-          pick(S, r, (int)all, min(k, (int)all), p, mp, u, a.token + row);
-          if (tid == 0 && a.n_kept) a.n_kept[row] = S.kept;
-          __syncthreads();
-          if (dst && tid < C) cl.map_shared_rank(&S, tid)->cut = S.cut;
-        }
-        if (dst) {
-          cl.sync();
-          filter(S.cut);
-        }
-        return;  // nothing of another CTA is read any more
+        filter(S.cut);
       }
+      return;  // nothing of another CTA is read any more
     }
-    cl.sync();
   }
 
   // ---- the cut by histogram of weights --------------------------------------
@@ -690,12 +753,12 @@ __global__ void __launch_bounds__(kThreads)
         const u64 w = weight_of(x_of(l, r));
         const int bin = bin_of(l, r);
         sum += w;
-        atomicAdd(&S.count[bin], 1u);
-        add_weight(S, bin, w);
+        if (by_k) atomicAdd(&S.count[bin], 1u);
+        if (by_p) add_weight(S, bin, w);
       });
       return sum;
     };
-    bool redo = false;  // a radix selection has overwritten the histogram
+    bool redo = false;  // the top-k cut has overwritten the histogram
     u64 sum = warp_total(fill());
     if (lane == 0) S.warp_w[wid] = sum;
     __syncthreads();
@@ -709,8 +772,9 @@ __global__ void __launch_bounds__(kThreads)
     if (by_k) {
       find_bin(S, kBins, false, (uint32_t)k, 0);
       if (S.found_bin >= 0) {  // fewer than k tokens above -inf: no cut
-        redo = S.all_count[S.found_bin] > kList;
-        bin_cut(S, cl, data, n, id0, r, false, (uint32_t)k, 0);
+        redo = true;
+        bin_cut(S, cl, data, wide, n, id0, r, false, (uint32_t)k,
+                S.found_w);
         cut = S.cut;
         total = S.kept_before;
         __syncthreads();
@@ -728,7 +792,7 @@ __global__ void __launch_bounds__(kThreads)
         reduce_bins(S, cl, kBins);
       }
       find_bin(S, kBins, true, 0, bound);
-      bin_cut(S, cl, data, n, id0, r, true, 0, bound);
+      bin_cut(S, cl, data, wide, n, id0, r, true, 0, bound);
       cut = max(cut, S.cut);
     }
   }
@@ -743,13 +807,27 @@ __global__ void __launch_bounds__(kThreads)
   warp_chunk(n, wid, &c0, &c1);
   u64 sum = 0;
   uint32_t cnt = 0;
-  each(data, wide, c0, c1, lane, 32, [&](int i, float l) {
-    const float x = x_of(l, r);
-    if (keeps(l, i, x)) {
-      sum += weight_of(x);
-      ++cnt;
-    }
-  });
+  if (cut == 0 && !by_m) {
+    each(data, wide, c0, c1, lane, 32, [&](int, float l) {
+      const bool on = l > -INFINITY;  // not a NaN, either
+      sum += weight_of(on ? x_of(l, r) : 0.f);
+      cnt += on;
+    });
+  } else {
+    // no weight is needed of what lies surely below the filters
+    const float low =
+        fmaxf(cut ? of_key((uint32_t)(cut >> 32)) : -INFINITY,
+              by_m ? r.top + logf(mp) * t * 1.0001f - fabsf(r.top) * 1e-6f
+                   : -INFINITY);
+    each(data, wide, c0, c1, lane, 32, [&](int i, float l) {
+      if (!(l >= low)) return;
+      const float x = x_of(l, r);
+      if (keeps(l, i, x)) {
+        sum += weight_of(x);
+        ++cnt;
+      }
+    });
+  }
   sum = warp_total(sum);
   cnt = warp_total(cnt);
   if (lane == 0) {
