@@ -53,7 +53,6 @@ constexpr int kChunks = 4;             // copies of a slice
 constexpr uint64_t kWait = 2000000000ull;  // 2 s
 constexpr int kCandBins = 512;         // bins of 1/16 for their bound
 constexpr int kMaxCluster = 8;
-constexpr float kWeightOne = 17592186044416.f;  // 2^44
 
 struct SampleArgs {
   const void* logits;
@@ -89,19 +88,13 @@ __device__ __forceinline__ U warp_total(U v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ u64 warp_largest(u64 v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1)
-    v = max(v, (u64)__shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-
 struct Shared {
   // written by this CTA, read by the cluster
   float top;             // largest logit of the slice
   int first;             // T = 0: first token of the slice that has it
   u64 total;             // weight of the slice
   u64 kept_w[kWarps];    // kept weight of each warp's chunk
+  float kept_least[kWarps];  // and its smallest kept logit
   uint32_t kept_n;
   uint32_t bad;
   uint32_t listed;
@@ -135,12 +128,23 @@ struct Row {
   bool greedy;
 };
 __device__ __forceinline__ float x_of(float l, const Row& r) {
-  if (l == r.top) return 1.f;
-  if (r.greedy) return 0.f;
+  if (l == r.top) return 1.f;  // also where the difference is no number
   return expf(__fmul_rn(__fsub_rn(l, r.top), r.inv_t));
 }
+// The same where the maximum and 1 / T are finite and l is a number.
+__device__ __forceinline__ float x_plain(float l, const Row& r) {
+  return expf(__fmul_rn(__fsub_rn(l, r.top), r.inv_t));
+}
+// floor(x 2^44) for 0 <= x <= 1, as 21 and 23 bits that additions to 2^23
+// (whose last place is 1) round off towards zero: the conversion to a 64-bit
+// integer has a sixteenth of their rate.
 __device__ __forceinline__ u64 weight_of(float x) {
-  return __float2ull_rz(__fmul_rn(x, kWeightOne));
+  const float xs = __fmul_rn(x, 0x1p21f);
+  const float hi = __fadd_rz(xs, 0x1p23f);
+  const float rest = __fsub_rn(xs, __fsub_rn(hi, 0x1p23f));  // exact
+  const float lo = __fmaf_rz(rest, 0x1p23f, 0x1p23f);
+  return (u64)(__float_as_uint(hi) - 0x4b000000u) * (1u << 23) +
+         (__float_as_uint(lo) - 0x4b000000u);
 }
 // Bin of a logit: 0 at the maximum, rising as it falls; monotone in l.
 __device__ __forceinline__ int bin_of(float l, const Row& r) {
@@ -531,11 +535,13 @@ __global__ void __launch_bounds__(kThreads)
     tc::fence_mbar_init();
   }
   __syncthreads();
-  float top = -INFINITY;
+  float tops[kChunks];  // of this thread's tokens, by quarters
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) tops[c] = -INFINITY;
   bool bad = false;
-  auto take = [&](float l) {
-    bad |= !(l < INFINITY);  // NaN, too
-    top = fmaxf(top, l);     // passes over a NaN
+  auto take = [&](int c, float l) {
+    bad |= !(l < INFINITY);         // NaN, too
+    tops[c] = fmaxf(tops[c], l);    // passes over a NaN
   };
   if (src_wide && a.resident) {
     constexpr int E = Vec<T>::E;
@@ -550,6 +556,7 @@ __global__ void __launch_bounds__(kThreads)
                         (v1 - v0) * 16, &S.landed[c]);
       }
     int give_up = 0;
+#pragma unroll
     for (int c = 0; c < kChunks; ++c) {
       if (!tc::mbar_wait_bounded(&S.landed[c], 0, &give_up, kWait))
         raise_error(a.err, kErrTimeout);
@@ -558,34 +565,48 @@ __global__ void __launch_bounds__(kThreads)
       for (int v = min(words, c * per) + tid; v < v1; v += kThreads) {
         const Vec<T> x{reinterpret_cast<const uint4*>(own)[v]};
 #pragma unroll
-        for (int k = 0; k < E; ++k) take(x.at(k));
+        for (int k = 0; k < E; ++k) take(c, x.at(k));
       }
     }
     for (int i = words * E + tid; i < n; i += kThreads) {
       const T x = src[i];
       own[i] = x;
-      take(to_f32(x));
+      take(0, to_f32(x));
     }
   } else if (src_wide) {
     constexpr int E = Vec<T>::E;
     const int words = n / E;
     const uint4* p = reinterpret_cast<const uint4*>(src);
-#pragma unroll 4
-    for (int v = tid; v < words; v += kThreads) {
-      const Vec<T> x{p[v]};
+    for (int v = tid; v < words; v += kChunks * kThreads) {
+      Vec<T> x[kChunks];
 #pragma unroll
-      for (int k = 0; k < E; ++k) take(x.at(k));
+      for (int c = 0; c < kChunks; ++c)
+        if (v + c * kThreads < words) x[c].w = p[v + c * kThreads];
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+        if (v + c * kThreads < words) {
+#pragma unroll
+          for (int k = 0; k < E; ++k) take(c, x[c].at(k));
+        }
     }
-    for (int i = words * E + tid; i < n; i += kThreads) take(to_f32(src[i]));
+    for (int i = words * E + tid; i < n; i += kThreads)
+      take(0, to_f32(src[i]));
   } else {
-#pragma unroll 8
-    for (int i = tid; i < n; i += kThreads) {
-      const T x = src[i];
-      if (a.resident) own[i] = x;
-      take(to_f32(x));
+    for (int i0 = tid; i0 < n; i0 += kChunks * kThreads) {
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) {
+        const int i = i0 + c * kThreads;
+        if (i < n) {
+          const T x = src[i];
+          if (a.resident) own[i] = x;
+          take(c, to_f32(x));
+        }
+      }
     }
   }
-  const float my_top = top;  // of this thread's tokens
+  float top = tops[0];
+#pragma unroll
+  for (int c = 1; c < kChunks; ++c) top = fmaxf(top, tops[c]);
   top = warp_max(top);
   if (lane == 0) S.warp_w[wid] = __float_as_uint(top);
   __syncthreads();
@@ -620,16 +641,16 @@ __global__ void __launch_bounds__(kThreads)
   auto filter = [&](u64 cut) {
     const float lc = of_key((uint32_t)(cut >> 32));
     const int last = (int)~(uint32_t)cut;  // of the tokens with that logit
-    if (a.resident && (reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
+    if (wide && (reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
       const int words = n / 4;
 #pragma unroll 2
       for (int v = tid; v < words; v += kThreads) {
         float f[4];
         if constexpr (sizeof(T) == 4) {
-          const float4 x = reinterpret_cast<const float4*>(own)[v];
+          const float4 x = reinterpret_cast<const float4*>(data)[v];
           f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
         } else {
-          const uint2 x = reinterpret_cast<const uint2*>(own)[v];
+          const uint2 x = reinterpret_cast<const uint2*>(data)[v];
           f[0] = __uint_as_float(x.x << 16);
           f[1] = __uint_as_float(x.x & 0xffff0000u);
           f[2] = __uint_as_float(x.y << 16);
@@ -643,7 +664,7 @@ __global__ void __launch_bounds__(kThreads)
             make_float4(f[0], f[1], f[2], f[3]);
       }
       for (int i = words * 4 + tid; i < n; i += kThreads) {
-        const float l = to_f32(own[i]);
+        const float l = to_f32(data[i]);
         dst[i] = l > lc || (l == lc && id0 + i <= last) ? l : -INFINITY;
       }
     } else {
@@ -688,10 +709,10 @@ __global__ void __launch_bounds__(kThreads)
       S.all_w[i] = 0;
     }
     __syncthreads();
-    if (my_top > -INFINITY) {
-      const int bin = bin_of(my_top, b) / (kBins / kCandBins);
-      atomicAdd(&S.count[bin], 1u);
-    }
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+      if (tops[c] > -INFINITY)
+        atomicAdd(&S.count[bin_of(tops[c], b) / (kBins / kCandBins)], 1u);
     if (own_bound) {
       __syncthreads();
       for (int i = tid; i < kCandBins; i += kThreads)
@@ -746,13 +767,33 @@ __global__ void __launch_bounds__(kThreads)
     for (int i = tid; i < kBins; i += kThreads)
       S.count[i] = S.w_lo[i] = S.w_hi[i] = 0;
     __syncthreads();
+    // Top-p only: tokens of less than (1 - p) W / V weigh less than (1 - p) W
+    // together, so they are past the cut and need no bin.  The weight of this
+    // CTA's threads' maxima, times 0.9 for roundings, stands for W from below.
+    float low = -INFINITY;
+    if (!by_k) {
+      float sum = 0.f;
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+        if (tops[c] > -INFINITY) sum += x_of(tops[c], r);
+      sum = warp_sum(sum);
+      if (lane == 0) S.warp_n[wid] = __float_as_uint(sum);
+      __syncthreads();
+      sum = 0.f;
+      for (int i = 0; i < kWarps; ++i) sum += __uint_as_float(S.warp_n[i]);
+      __syncthreads();
+      const float least = 0.9f * (1.f - p) * sum / (float)a.V;
+      if (least > 0.f && least < 1.f)
+        low = r.top + logf(least) * t * 1.0001f - fabsf(r.top) * 1e-6f;
+    }
     auto fill = [&] {
       u64 sum = 0;
       each(data, wide, 0, n, tid, kThreads, [&](int i, float l) {
         if (!(l > -INFINITY)) return;
         const u64 w = weight_of(x_of(l, r));
-        const int bin = bin_of(l, r);
         sum += w;
+        if (l < low) return;
+        const int bin = bin_of(l, r);
         if (by_k) atomicAdd(&S.count[bin], 1u);
         if (by_p) add_weight(S, bin, w);
       });
@@ -807,12 +848,19 @@ __global__ void __launch_bounds__(kThreads)
   warp_chunk(n, wid, &c0, &c1);
   u64 sum = 0;
   uint32_t cnt = 0;
+  float least = INFINITY;  // smallest kept logit, where min-p has a say
   if (cut == 0 && !by_m) {
-    each(data, wide, c0, c1, lane, 32, [&](int, float l) {
-      const bool on = l > -INFINITY;  // not a NaN, either
-      sum += weight_of(on ? x_of(l, r) : 0.f);
-      cnt += on;
-    });
+    if (S.bad || !(r.inv_t < INFINITY))
+      each(data, wide, c0, c1, lane, 32, [&](int, float l) {
+        const bool on = l > -INFINITY;  // not a NaN, either
+        sum += weight_of(on ? x_of(l, r) : 0.f);
+        cnt += on;
+      });
+    else
+      each(data, wide, c0, c1, lane, 32, [&](int, float l) {
+        sum += weight_of(x_plain(l, r));
+        cnt += l > -INFINITY;
+      });
   } else {
     // no weight is needed of what lies surely below the filters
     const float low =
@@ -825,21 +873,33 @@ __global__ void __launch_bounds__(kThreads)
       if (keeps(l, i, x)) {
         sum += weight_of(x);
         ++cnt;
+        least = fminf(least, l);
       }
     });
   }
+  least = -warp_max(-least);
   sum = warp_total(sum);
   cnt = warp_total(cnt);
   if (lane == 0) {
     S.kept_w[wid] = sum;
+    S.kept_least[wid] = least;
     if (cnt) atomicAdd(&S.kept_n, cnt);
   }
   cl.sync();
-  if (dst)
-    for (int i = tid; i < n; i += kThreads) {
-      const float l = to_f32(data[i]);
-      dst[i] = keeps(l, i, by_m ? x_of(l, r) : 1.f) ? l : -INFINITY;
+  if (dst) {
+    // what is kept, as one cut: all tokens of the smallest kept logit if
+    // min-p decided, all above -inf if nothing did
+    u64 at = cut ? cut : (u64)kKeyNegInf << 32;
+    if (by_m) {
+      least = INFINITY;
+      for (int i = lane; i < C * kWarps; i += 32)
+        least = fminf(least, cl.map_shared_rank(&S, i / kWarps)
+                                 ->kept_least[i % kWarps]);
+      least = -warp_max(-least);
+      at = max(at, word_of(least, 0x7fffffff));  // up to the last id
     }
+    filter(at);
+  }
   if (wid == 0) {
     // kept weight of every (CTA, warp) chunk in id order: lane handles four
     constexpr int kPer = kMaxCluster * kWarps / 32;
@@ -879,22 +939,35 @@ __global__ void __launch_bounds__(kThreads)
     before = __shfl_sync(0xffffffffu, before, from);
     if (hit / kWarps == rank) {  // the chunk is in this CTA's slice
       warp_chunk(n, hit % kWarps, &c0, &c1);
-      for (int base = c0; base < c1; base += 32) {
-        const int i = base + lane;
-        const float l = i < c1 ? to_f32(data[i]) : -INFINITY;
-        const float x = x_of(l, r);
-        u64 v = i < c1 && keeps(l, i, x) ? weight_of(x) : 0;
-        const u64 one = v;
+      // eight tokens to a lane at a time
+      for (int base = c0; base < c1; base += 256) {
+        u64 v[8], one = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int i = base + lane * 8 + j;
+          const float l = i < c1 ? to_f32(data[i]) : -INFINITY;
+          const float x = x_of(l, r);
+          v[j] = i < c1 && keeps(l, i, x) ? weight_of(x) : 0;
+          one += v[j];
+        }
+        u64 sum8 = one;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const u64 q = __shfl_up_sync(0xffffffffu, v, o);
-          if (lane >= o) v += q;
+          const u64 q = __shfl_up_sync(0xffffffffu, sum8, o);
+          if (lane >= o) sum8 += q;
         }
-        const bool here = one > 0 && target >= before + v - one &&
-                          target < before + v;
-        if (here) a.token[row] = id0 + i;
+        u64 at = before + sum8 - one;
+        const bool here = one > 0 && target >= at && target < at + one;
+        if (here) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (target >= at && target < at + v[j])
+              a.token[row] = id0 + base + lane * 8 + j;
+            at += v[j];
+          }
+        }
         if (__any_sync(0xffffffffu, here)) break;
-        before += __shfl_sync(0xffffffffu, v, 31);
+        before += __shfl_sync(0xffffffffu, sum8, 31);
       }
     }
   }
@@ -903,18 +976,19 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename T>
 cudaError_t launch(SampleArgs a, cudaStream_t s) {
-  // The smallest cluster whose slices take at most 80 KB each, so that two
-  // CTAs fit an SM and one loads while the other works; wider rows take
-  // slices of up to 144 KB in a cluster of eight, still wider ones are read
-  // again from L2 and HBM in every pass.
-  int C = 1;
-  auto bytes = [&](int c) {
-    const long long sl = (((long long)a.V + c - 1) / c + 7) & ~7ll;
-    return sl * (long long)sizeof(T);
-  };
-  while (C < kMaxCluster && bytes(C) > 80 * 1024) C *= 2;
+  // One wave of CTAs, four to an SM, if that takes at most eight to a row:
+  // fewer to a row cost less in barriers between them (288 rows of 151936
+  // fp32 logits, top-k 50: 126 us with eight, 84 us with two), more of them
+  // shorten a lone row (20 us with eight, 28 us with two).  Never more than
+  // slices of 4096 tokens need.
+  int C = kMaxCluster;
+  while (C > 1 && ((long long)a.R * C > 4 * 152 ||
+                   (long long)(C / 2) * 4096 >= a.V))
+    C /= 2;
+  // A slice stays in shared memory where two CTAs fit an SM so; the rest is
+  // read again, from L2 for the most part.
   a.slice = (int)((((long long)a.V + C - 1) / C + 7) & ~7ll);
-  a.resident = bytes(C) <= 144 * 1024;
+  a.resident = (long long)a.slice * (long long)sizeof(T) <= 76 * 1024;
   const size_t smem = (sizeof(Shared) + 15) / 16 * 16 +
                       (a.resident ? (size_t)a.slice * sizeof(T) : 16);
   auto* f = sample_kernel<T>;
