@@ -154,6 +154,20 @@ __device__ __forceinline__ int bin_of(float l, const Row& r) {
   return z < (float)(kBins - 1) ? (int)z : kBins - 1;
 }
 
+// A logit below all of bins 0 .. bin (-inf after the last): z is less than
+// (bin + 1) / kBinsPerUnit there, with room for its roundings.
+__device__ __forceinline__ float bin_floor(int bin, const Row& r, float t) {
+  if (bin >= kBins - 1) return -INFINITY;
+  const float z = (float)(bin + 1) / kBinsPerUnit;
+  return r.top - z * t * 1.0001f - fabsf(r.top) * 1e-6f;
+}
+
+// A logit above all of bins bin, bin + 1, ...
+__device__ __forceinline__ float bin_ceil(int bin, const Row& r, float t) {
+  const float z = (float)bin / kBinsPerUnit;
+  return r.top - z * t * 0.9999f + fabsf(r.top) * 1e-6f;
+}
+
 __device__ __forceinline__ void add_weight(Shared& S, int bin, u64 w) {
   const uint32_t lo = (uint32_t)w, hi = (uint32_t)(w >> 32);
   const uint32_t old = atomicAdd(&S.w_lo[bin], lo);
@@ -397,16 +411,19 @@ __device__ bool collect(Shared& S, cg::cluster_group& cl, int* all) {
 // histogram is lost.
 template <typename T>
 __device__ void bin_cut(Shared& S, cg::cluster_group& cl, const T* data,
-                        bool wide, int n, int id0, const Row& r, bool by_weight,
-                        uint32_t need_n, u64 need_w) {
+                        bool wide, int n, int id0, const Row& r, float t,
+                        bool by_weight, uint32_t need_n, u64 need_w) {
   const int tid = threadIdx.x;
   const int bin = S.found_bin;
   const uint32_t before_n = S.found_n;
   const u64 before_w = S.found_w;
   if (tid == 0) S.listed = 0;
   __syncthreads();
+  // one comparison on each side decides for most tokens
+  const float below = bin_floor(bin, r, t);
+  const float above = bin_ceil(bin, r, t);
   each(data, wide, 0, n, tid, kThreads, [&](int i, float l) {
-    if (l > -INFINITY && bin_of(l, r) == bin) {
+    if (l >= below && l <= above && l > -INFINITY && bin_of(l, r) == bin) {
       const uint32_t at = atomicAdd(&S.listed, 1u);
       if (at < kCand) S.cand[at] = word_of(l, id0 + i);
     }
@@ -449,11 +466,12 @@ __device__ void bin_cut(Shared& S, cg::cluster_group& cl, const T* data,
   cl.sync();
 }
 
-// The row's n candidates (S.all_cand, at least k of its tokens, the largest
-// ones among them) to the kept set's cut, size and weight, and the token.
-// Whole CTA; scratch: S.cand.
-__device__ void pick(Shared& S, const Row& r, int n, int k, float p, float mp,
-                     float u, int* token) {
+// The row's n candidates (S.all_cand: its largest tokens, at least k of them)
+// to the kept set's cut and size, and the token.  The first k are kept, of
+// those the ones whose predecessors weigh less than `bound` (0: p of the k
+// tokens' weight).  Whole CTA; scratch: S.cand.
+__device__ void pick(Shared& S, const Row& r, int n, int k, u64 bound, float p,
+                     float mp, float u, int* token) {
   const int tid = threadIdx.x;
   sort_down(S.all_cand, n);
   constexpr int kPer = kCand / kThreads;
@@ -468,7 +486,7 @@ __device__ void pick(Shared& S, const Row& r, int n, int k, float p, float mp,
     mine += w[j];
   }
   u64 total, before = cta_scan(S, mine, &total);
-  const u64 bound = p < 1.f ? top_p_bound(p, total) : ~0ull;
+  if (bound == 0) bound = p < 1.f ? top_p_bound(p, total) : ~0ull;
   int kept = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
@@ -697,7 +715,32 @@ __global__ void __launch_bounds__(kThreads)
     return;
   }
 
-  // ---- top-k: candidates, sorted and drawn from by the first CTA -----------
+  // The tokens from `low` up as candidates, sorted and drawn from by the first
+  // CTA; false if they are too many.
+  auto finish = [&](float low, int most, u64 bound) {
+    each(data, wide, 0, n, tid, kThreads, [&](int i, float l) {
+      if (l >= low && l > -INFINITY) {
+        const uint32_t at = atomicAdd(&S.listed, 1u);
+        if (at < kCand) S.cand[at] = word_of(l, id0 + i);
+      }
+    });
+    __syncthreads();
+    int all;
+    if (!collect(S, cl, &all)) return false;
+    if (rank == 0) {
+      pick(S, r, all, min(most, all), bound, p, mp, u, a.token + row);
+      if (tid == 0 && a.n_kept) a.n_kept[row] = S.kept;
+      __syncthreads();
+      if (dst && tid < C) cl.map_shared_rank(&S, tid)->cut = S.cut;
+    }
+    if (dst) {
+      cl.sync();
+      filter(S.cut);
+    }
+    return true;  // nothing of another CTA is read any more
+  };
+
+  // ---- top-k: candidates from the threads' maxima -----------------------------
   if (by_k && k <= kCand) {
     // bins of the threads' maxima, half as fine as the weights' bins; below
     // the slice's own maximum where each CTA takes its own bound
@@ -731,34 +774,11 @@ __global__ void __launch_bounds__(kThreads)
     // the counts have been read; the lists take their place
     if (own_bound) __syncthreads();
     else cl.sync();
-    // A logit below every one of the bins up to `bin`: their z is less than
-    // (bin + 1) / 16, with room for the roundings of z.  No such bin: all.
-    const float z = (float)(bin + 1) * (kBins / kCandBins) / kBinsPerUnit;
-    const float low = bin < 0 || bin == kCandBins - 1
-                          ? -INFINITY
-                          : b.top - z * t * 1.0001f - fabsf(b.top) * 1e-6f;
-    each(data, wide, 0, n, tid, kThreads, [&](int i, float l) {
-      if (l >= low && l > -INFINITY) {
-        const uint32_t at = atomicAdd(&S.listed, 1u);
-        if (at < kCand) S.cand[at] = word_of(l, id0 + i);
-      }
-    });
-    __syncthreads();
-    int all;
-    if (collect(S, cl, &all)) {
-      if (rank == 0) {
-        // top-k of fewer tokens than k keeps them all
-        pick(S, r, all, min(k, all), p, mp, u, a.token + row);
-        if (tid == 0 && a.n_kept) a.n_kept[row] = S.kept;
-        __syncthreads();
-        if (dst && tid < C) cl.map_shared_rank(&S, tid)->cut = S.cut;
-      }
-      if (dst) {
-        cl.sync();
-        filter(S.cut);
-      }
-      return;  // nothing of another CTA is read any more
-    }
+    const float low =
+        bin < 0 ? -INFINITY
+                : bin_floor((bin + 1) * (kBins / kCandBins) - 1, b, t);
+    // top-k of fewer tokens than k keeps them all
+    if (finish(low, k, 0)) return;
   }
 
   // ---- the cut by histogram of weights --------------------------------------
@@ -794,7 +814,7 @@ __global__ void __launch_bounds__(kThreads)
         sum += w;
         if (l < low) return;
         const int bin = bin_of(l, r);
-        if (by_k) atomicAdd(&S.count[bin], 1u);
+        atomicAdd(&S.count[bin], 1u);
         if (by_p) add_weight(S, bin, w);
       });
       return sum;
@@ -814,8 +834,7 @@ __global__ void __launch_bounds__(kThreads)
       find_bin(S, kBins, false, (uint32_t)k, 0);
       if (S.found_bin >= 0) {  // fewer than k tokens above -inf: no cut
         redo = true;
-        bin_cut(S, cl, data, wide, n, id0, r, false, (uint32_t)k,
-                S.found_w);
+        bin_cut(S, cl, data, wide, n, id0, r, t, false, (uint32_t)k, 0);
         cut = S.cut;
         total = S.kept_before;
         __syncthreads();
@@ -833,7 +852,22 @@ __global__ void __launch_bounds__(kThreads)
         reduce_bins(S, cl, kBins);
       }
       find_bin(S, kBins, true, 0, bound);
-      bin_cut(S, cl, data, wide, n, id0, r, true, 0, bound);
+      // few tokens up to the cut's bin: they are all that is left to look at
+      const int bin = S.found_bin;
+      if (!redo && bin < kBins - 1 &&
+          S.found_n + S.all_count[bin] <= kCand / 2) {
+        if (tid == 0) S.listed = 0;
+        __syncthreads();
+        if (finish(bin_floor(bin, r, t), kCand, bound)) return;
+        // (not so few: the bins have been overwritten)
+        for (int i = tid; i < kBins; i += kThreads)
+          S.count[i] = S.w_lo[i] = S.w_hi[i] = 0;
+        __syncthreads();
+        fill();
+        reduce_bins(S, cl, kBins);
+        find_bin(S, kBins, true, 0, bound);
+      }
+      bin_cut(S, cl, data, wide, n, id0, r, t, true, 0, bound);
       cut = max(cut, S.cut);
     }
   }
