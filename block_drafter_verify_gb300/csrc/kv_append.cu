@@ -32,7 +32,7 @@ namespace {
 constexpr float kE4m3Max = 448.f;
 constexpr int kMinExp = -64;   // smallest exponent of a block scale
 constexpr int kThreads = 256;  // most threads of a CTA
-constexpr int kKeep = 4;       // units a thread keeps in registers
+constexpr int kKeep = 2;       // units a thread keeps in registers
 constexpr int kHeads = 8;      // q heads per rotation thread
 
 struct AppendArgs {
@@ -52,30 +52,42 @@ struct AppendArgs {
   int* err;
 };
 
+// N values of type T (4 or 8) as loaded.
 template <typename T, int N>
-__device__ __forceinline__ void load_n(const T* p, float (&f)[N]) {
+struct Raw {
   static_assert(N == 4 || N == 8, "");
-  if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p + i);
-      f[i] = v.x; f[i + 1] = v.y; f[i + 2] = v.z; f[i + 3] = v.w;
-    }
-  } else {
-    uint32_t w[N / 2];
-    if constexpr (N == 8) {
-      const uint4 v = *reinterpret_cast<const uint4*>(p);
-      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-    } else {
+  static constexpr int W = N * sizeof(T) / 4;  // 32-bit words
+  uint32_t w[W];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (W == 2) {
       const uint2 v = *reinterpret_cast<const uint2*>(p);
       w[0] = v.x; w[1] = v.y;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      for (int i = 0; i < W; i += 4) {
+        const uint4 v = reinterpret_cast<const uint4*>(p)[i / 4];
+        w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+      }
     }
   }
+  __device__ __forceinline__ void get(float (&f)[N]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[i] = __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  }
+};
+template <typename T, int N>
+__device__ __forceinline__ void load_n(const T* p, float (&f)[N]) {
+  Raw<T, N> r;
+  r.load(p);
+  r.get(f);
 }
 
 template <typename T, int N>
@@ -214,7 +226,7 @@ __device__ __forceinline__ int live_tokens(const AppendArgs& a, int b,
 }
 
 template <typename T, int VEC, bool kInter>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
     kv_append_kernel(const __grid_constant__ AppendArgs a) {
   pdl_trigger();
   pdl_wait();
@@ -244,16 +256,26 @@ __global__ void __launch_bounds__(kThreads)
     const T* src = static_cast<const T*>(a.q) + row * a.ld_q;
     T* dst = static_cast<T*>(a.q_out) + row * a.Hq * a.D;
     const int h1 = min(a.Hq, (hg + 1) * kHeads);
-#pragma unroll 4
-    for (int h = hg * kHeads; h < h1; ++h) {
-      float x[VEC] = {}, y[VEC] = {};
-      if (live) {
-        load_n<T, VEC>(src + (size_t)h * a.D + un.d0, x);
-        load_n<T, VEC>(src + (size_t)h * a.D + un.d1, y);
-        if (un.angle >= 0) rotate<VEC, kInter>(x, y, c, s);
+    for (int h0 = hg * kHeads; h0 < h1; h0 += 4) {  // four heads in flight
+      Raw<T, VEC> x[4], y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (live && h0 + i < h1) {
+          x[i].load(src + (size_t)(h0 + i) * a.D + un.d0);
+          y[i].load(src + (size_t)(h0 + i) * a.D + un.d1);
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (h0 + i >= h1) break;
+        float u[VEC] = {}, v[VEC] = {};
+        if (live) {
+          x[i].get(u);
+          y[i].get(v);
+          if (un.angle >= 0) rotate<VEC, kInter>(u, v, c, s);
+        }
+        store_n<T, VEC>(dst + (size_t)(h0 + i) * a.D + un.d0, u);
+        store_n<T, VEC>(dst + (size_t)(h0 + i) * a.D + un.d1, v);
       }
-      store_n<T, VEC>(dst + (size_t)h * a.D + un.d0, x);
-      store_n<T, VEC>(dst + (size_t)h * a.D + un.d1, y);
     }
     return;
   }
@@ -333,7 +355,7 @@ __global__ void __launch_bounds__(kThreads)
       fold(y[k]);
     }
   }
-  for (int i = tid + kKeep * nt; i < work; i += nt) {  // pages beyond 16 KB
+  for (int i = tid + kKeep * nt; i < work; i += nt) {  // larger pages
     float p[VEC], r[VEC];
     fetch(i, p, r);
     fold(p);
