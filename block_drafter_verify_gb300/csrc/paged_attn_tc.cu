@@ -53,7 +53,6 @@ constexpr int kMaxRows = 96;       // (query, head) rows of a unit
 constexpr int kMaxCtas = 160;
 constexpr int kUnitBytes = kTile * 128;  // a K or V tile in shared memory
 constexpr int kStages = 7;         // most stages of K or V tiles
-constexpr int kLens = 128;         // sequences whose lengths are kept on chip
 constexpr uint64_t kWait = 2000000000ull;  // 2 s
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kHead = 10.f;      // weights are 2^(score - ref + kHead)
@@ -72,7 +71,7 @@ struct Plan {
   static constexpr int kGroups = N >= 64 ? 4 : N == 48 ? 3 : 2;
   static constexpr int kRowsOf = N / kGroups;           // rows of a group
   static constexpr int kThreads = 128 + 128 * kGroups;
-  static constexpr int kFixed = 8 * 1024 + 1024;  // Meta, alignment
+  static constexpr int kFixed = 7 * 1024 + 1024;  // Meta, alignment
   static constexpr int kFit = (232448 - Q - P - kFixed) / kUnitBytes;
   // K is free again after the first product, V after the second
   static constexpr int K = kFit / 2 - 1 < 5 ? kFit / 2 - 1 : 5;
@@ -115,13 +114,8 @@ struct Meta {
   uint64_t drain;
   uint32_t tmem;
   int abort;
-  int count;                 // tiles of this CTA's run
-  int b0;                    // its sequence, and the tiles before it there
-  int off0;
-  int warp_sum[32];
-  int2 lens[kLens];          // (cached tokens, queries)
 };
-static_assert(sizeof(Meta) <= 8 * 1024, "");
+static_assert(sizeof(Meta) <= 7 * 1024, "");
 
 // ---- the numbering of the tiles -------------------------------------------
 struct Shape {
@@ -137,16 +131,10 @@ __device__ __forceinline__ Lens lens_of(const PagedAttnArgs& a, int b,
   l.nq = attn_clamp(a.q_len ? a.q_len[b] : a.Q, a.Q, bad);
   return l;
 }
-// The same from the copy on chip, if the batch fits there.
-__device__ __forceinline__ Lens lens_of(const PagedAttnArgs& a, const Meta& m,
-                                        int b) {
-  if (a.B <= kLens) return Lens{m.lens[b].x, m.lens[b].y};
-  bool bad;
-  return lens_of(a, b, &bad);
-}
 // Tiles that row tile rt of a sequence needs (0: it sees nothing).
 __device__ __forceinline__ int tiles_of(const PagedAttnArgs& a, const Shape& s,
                                         const Lens& l, int rt) {
+  if (s.row_tiles == 1) return l.nq > 0 ? (l.n + kTile - 1) / kTile : 0;
   const int q0 = rt * s.N / s.g;
   if (q0 >= l.nq) return 0;
   int seen = l.n;
@@ -179,34 +167,62 @@ struct Walk {
   int left;                  // positions left in this CTA's run
   int first;                 // no segment handed out yet
 };
-__device__ void walk_start(const PagedAttnArgs& a, const Shape& s,
-                           const Meta& m, Walk& w) {
-  w.b = m.b0;
-  w.left = m.count;
-  w.first = 1;
-  w.hk = w.rt = w.at = 0;
-  if (w.left <= 0) return;
-  const Lens l = lens_of(a, m, w.b);
-  const int h = head_work(a, s, l);
-  int o = m.off0;
-  w.hk = o / h;
-  o -= w.hk * h;
-  for (;; ++w.rt) {
-    const int t = kUnitCost + tiles_of(a, s, l, w.rt);
-    if (o < t) break;
-    o -= t;
+// Where the run of CTA `cta` of `grid` starts.  A whole warp, each lane with
+// a stretch of the sequences; *bad: some length was out of range.
+__device__ void walk_start(const PagedAttnArgs& a, const Shape& s, int cta,
+                           int grid, Walk& w, bool* bad) {
+  const int lane = threadIdx.x & 31;
+  const int per = (a.B + 31) / 32;
+  const int b0 = min(a.B, lane * per), b1 = min(a.B, b0 + per);
+  int work = 0;
+  for (int b = b0; b < b1; ++b)
+    work += a.Hkv * head_work(a, s, lens_of(a, b, bad));
+  int run = work;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += v;
   }
-  w.at = o;
+  const int total = __shfl_sync(0xffffffffu, run, 31);
+  const int G = min(grid, total);
+  const int p0 = run_start(total, cta, G), p1 = run_start(total, cta + 1, G);
+  w.left = p1 - p0;
+  w.first = 1;
+  w.b = w.hk = w.rt = w.at = 0;
+  if (w.left <= 0) return;                 // the same in every lane
+  const bool mine = p0 >= run - work && p0 < run;
+  int o = p0 - (run - work), h = 1;
+  if (mine) {
+    for (w.b = b0; w.b < b1; ++w.b) {
+      h = head_work(a, s, lens_of(a, w.b, bad));
+      if (o < a.Hkv * h) break;
+      o -= a.Hkv * h;
+    }
+    w.hk = o / h;
+    o -= w.hk * h;
+    const Lens l = lens_of(a, w.b, bad);
+    for (;; ++w.rt) {
+      const int t = kUnitCost + tiles_of(a, s, l, w.rt);
+      if (o < t) break;
+      o -= t;
+    }
+  }
+  const int from = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+  w.b = __shfl_sync(0xffffffffu, w.b, from);
+  w.hk = __shfl_sync(0xffffffffu, w.hk, from);
+  w.rt = __shfl_sync(0xffffffffu, w.rt, from);
+  w.at = __shfl_sync(0xffffffffu, o, from);
 }
 struct Part {
   int b, hk, rt, t0, t1, whole, first;
   Lens l;
 };
 // The next segment; false at the end of the run.
-__device__ bool walk_next(const PagedAttnArgs& a, const Shape& s,
-                          const Meta& m, Walk& w, Part& p) {
+__device__ bool walk_next(const PagedAttnArgs& a, const Shape& s, Walk& w,
+                          Part& p) {
+  bool bad = false;
   while (w.left > 0) {
-    p.l = lens_of(a, m, w.b);
+    p.l = lens_of(a, w.b, &bad);
     const int t = tiles_of(a, s, p.l, w.rt);
     const int work = kUnitCost + t;
     const int end = min(work, w.at + w.left);
@@ -494,8 +510,6 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
     tc::mbar_init(&m.qfree, 1);
     tc::mbar_init(&m.drain, 1);
     m.abort = 0;
-    m.b0 = 0;
-    m.off0 = 0;
     tc::fence_mbar_init();
   }
   if (warp == 1) {
@@ -506,49 +520,6 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
     tc::tma_prefetch_map(&map_k);
     tc::tma_prefetch_map(&map_v);
   }
-  pdl_trigger();
-  pdl_wait();
-  // ---- where this CTA's run of tiles starts ------------------------------
-  {
-    const int per = (a.B + kThreads - 1) / kThreads;
-    const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-    int w = 0;
-    bool bad = false;
-    for (int b = b0; b < b1; ++b) {
-      const Lens l = lens_of(a, b, &bad);
-      if (b < kLens) m.lens[b] = make_int2(l.n, l.nq);
-      w += a.Hkv * head_work(a, shape, l);
-    }
-    if (bad && blockIdx.x == 0) raise_error(a.err, kErrBadIndex);
-    int run = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, run, o);
-      if (lane >= o) run += v;
-    }
-    if (lane == 31) m.warp_sum[warp] = run;
-    __syncthreads();
-    int total = 0;
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < warp) run += m.warp_sum[i];
-      total += m.warp_sum[i];
-    }
-    const int G = min((int)gridDim.x, total);
-    const int p0 = run_start(total, blockIdx.x, G);
-    const int p1 = run_start(total, blockIdx.x + 1, G);
-    if (tid == 0) m.count = p1 - p0;
-    if (p1 > p0 && p0 >= run - w && p0 < run) {
-      int o = p0 - (run - w);
-      int b = b0;
-      for (; b < b1; ++b) {
-        const int v = a.Hkv * head_work(a, shape, lens_of(a, m, b));
-        if (o < v) break;
-        o -= v;
-      }
-      m.b0 = b;
-      m.off0 = o;
-    }
-  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -556,8 +527,14 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
 
   if (warp == 0) {
     // ---------------------------------------------------------- producer
+    pdl_wait();
+    pdl_trigger();  // after the wait: the join may read the lengths at once
     Walk w;
-    walk_start(a, shape, m, w);
+    {
+      bool bad = false;
+      walk_start(a, shape, blockIdx.x, gridDim.x, w, &bad);
+      if (bad && blockIdx.x == 0) raise_error(a.err, kErrBadIndex);
+    }
     Part p;
     const int pt = kTile / a.page;         // pages of a tile
     const int oob = a.num_pages * a.Hkv * a.page;  // a row past the pool
@@ -567,7 +544,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
     Ring<PL::V> rv;
     int nk = 0, nv = 0;                    // copies issued, up to the stages
     bool ok = true;
-    while (ok && walk_next(a, shape, m, w, p)) {
+    while (ok && walk_next(a, shape, w, p)) {
       const int pages = (p.l.n + a.page - 1) / a.page;
       // page ids two chunks of 32 ahead, their scales one ahead
       int at = p.t0 * pt;                  // first page of the chunk
@@ -649,6 +626,8 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
     constexpr uint32_t id_s = tc::idesc_e4m3_f32(128, PL::kScore);
     constexpr uint32_t id_o = idesc_mn(PL::kAcc);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    pdl_wait();
+    pdl_trigger();
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t par) {
       ok = ok && wait_for(bar, par, abort);
@@ -734,8 +713,15 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
     wait_for(&m.drain, 0, &never);
   } else if (warp < 4) {
     // ------------------------------------------------------ layout of q
+    pdl_wait();
+    pdl_trigger();
     Walk w;
-    walk_start(a, shape, m, w);
+    {
+      bool bad = false;
+      walk_start(a, shape, blockIdx.x, gridDim.x, w, &bad);
+    }
+    // row / g for the rows of a tile, x < kMaxRows + 64, exactly
+    const uint32_t by_g = (65536 + shape.g - 1) / shape.g;
     const int qt = tid - 64;               // 0..63
     const int ch = qt & 7;                 // 16 dimensions of a row
     for (int s = 0;; ++s) {
@@ -747,9 +733,10 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
       if (any_of<64>(kQBar, !ok)) break;
       Segment& g = m.seg[qb];
       Part p;
-      const bool more = walk_next(a, shape, m, w, p);
+      const bool more = walk_next(a, shape, w, p);
       if (more) {
         const int row0 = p.rt * N;
+        const int q_first = row0 / shape.g, q_rest = row0 - q_first * shape.g;
         // All rows' values fly at once, asynchronously, into the place their
         // codes will take: the first 64 dimensions of a row where its upper
         // parts go, the rest where its lower parts go.  A thread reads only
@@ -761,11 +748,12 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
 #pragma unroll 1
         for (int j = 0; j < J; ++j) {
           const int r = (qt >> 3) + 8 * j, row = row0 + r;
-          const int qi = row / shape.g;
-          const int out = row < shape.rows ? (p.b * a.Q + qi) * a.Hq +
-                                                 p.hk * shape.g +
-                                                 (row - qi * shape.g)
-                                           : -1;
+          const int dq = (int)((uint32_t)(q_rest + r) * by_g >> 16);
+          const int qi = q_first + dq;
+          const int out = row < shape.rows
+                              ? (p.b * a.Q + qi) * a.Hq + p.hk * shape.g +
+                                    (q_rest + r - dq * shape.g)
+                              : -1;
           const bool live = row < shape.rows && qi < p.l.nq;
           const bool read = live && ch * 16 < a.D;
           const uint8_t* src =
@@ -873,9 +861,8 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
           g.nq = p.l.nq;
           g.whole = p.whole;
           g.slot = 2 * blockIdx.x + (p.first ? 0 : 1);
-          g.min_lim = a.causal ? min(p.l.n, p.l.n - p.l.nq +
-                                                row0 / shape.g + 1)
-                               : p.l.n;
+          g.min_lim =
+              a.causal ? min(p.l.n, p.l.n - p.l.nq + q_first + 1) : p.l.n;
         }
       }
       if (qt == 0) g.done = !more;
@@ -917,17 +904,29 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
     Ring<2> rs;
     Ring<PL::V> rv;
     bool live = true;
-    for (int s = 0; live; ++s) {
+    // s = -1: one tile of a segment that is not there.  It waits for nothing,
+    // signals nothing and writes nothing that is read, but brings the code of
+    // the tile, of the raised reference and of the output (first executions
+    // of which took 6000 to 10000 cycles) into the instruction caches while
+    // the lengths, q and the first tile are on their way.
+    for (int s = -1; live; ++s) {
+      const bool dry = s < 0;
       const int qb = s & 1;
-      bool ok = wait_for(&m.qfull[qb], (s >> 1) & 1, abort);
+      if (s == 0) {  // the outputs may still be read by the launch before
+        pdl_wait();
+        pdl_trigger();
+      }
+      bool ok = dry || wait_for(&m.qfull[qb], (s >> 1) & 1, abort);
       if (half_any(bar, !ok)) break;
       const Segment& g = m.seg[qb];
-      if (g.done) break;
-      const int T = g.t1 - g.t0, n = g.n;
-      const int mask_from = g.min_lim - g.t0 * kTile;  // tokens from the start
-      const bool uneven = g.uneven;
-      const float back = g.back;
-      int pos = g.t0 * kTile + tok;          // this thread's token
+      if (!dry && g.done) break;
+      const int T = dry ? 1 : g.t1 - g.t0, n = dry ? 0x7fffffff : g.n;
+      // tokens from the segment's start
+      const int mask_from = dry ? 0x7fffffff : g.min_lim - g.t0 * kTile;
+      const bool uneven = !dry && g.uneven;
+      const bool whole = dry || g.whole;
+      const float back = dry ? 0.f : g.back;
+      int pos = dry ? tok : g.t0 * kTile + tok;  // this thread's token
       uint64_t l[HR / 2];   // sums of weights, by pairs of rows
 #pragma unroll
       for (int r = 0; r < HR / 2; ++r) l[r] = 0;
@@ -935,11 +934,11 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
       if (ht < HR) m.neg_ref[my_row] = 0.f;
       half_sync(bar);
       float lv_ref = 0.f;
-      for (int t = 0; t < T; ++t, rs.next(), rv.next(), pos += kTile) {
+      for (int t = 0; t < T; ++t, pos += kTile) {
         const int sb = rs.at, st = rv.at;
         // Also says that the weights' buffer is free: the scores' commit
         // follows the second product of two tiles ago.
-        ok = wait_for(&m.sfull[sb], rs.phase, abort);
+        ok = dry || wait_for(&m.sfull[sb], rs.phase, abort);
         ok = __all_sync(0xffffffffu, ok);
         float y[HR];
         const int pg = tok >> page_bits;
@@ -1094,13 +1093,17 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
         }
         fence_async();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&m.pfull[sb]);
+        if (!dry) {
+          if (lane == 0) tc::mbar_arrive(&m.pfull[sb]);
+          rs.next();
+          rv.next();
+        }
       }
       if (!live) break;
       // ---- the segment's result ------------------------------------------
       if (T > 0) {
         const Ring<PL::V> last = rv.back(1);
-        ok = wait_for(&m.vempty[last.at], last.phase, abort);
+        ok = dry || wait_for(&m.vempty[last.at], last.phase, abort);
         if (half_any(bar, !ok)) break;
         tc::fence_after_sync();
       }
@@ -1124,10 +1127,10 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
                           (m.warp_val[2][r] + m.warp_val[3][r]);
         const float ref = -m.neg_ref[r] - lv_ref;   // log2 of what sum counts
         const bool seen = sum > 0.f || sum != sum;  // a NaN stays one
-        if (g.whole) {
+        if (whole) {
           const bool on = seen && g.on[r];
           m.fac[r] = on ? lift / sum : 0.f;
-          if (g.out_row[r] >= 0 && a.lse)
+          if (!dry && g.out_row[r] >= 0 && a.lse)
             a.lse[g.out_row[r]] =
                 on ? (log2f(sum) + ref) * 0.6931471805599453f : -INFINITY;
         } else {
@@ -1160,8 +1163,8 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
 #pragma unroll
           for (int h = 1; h < OG; ++h) v += o[4 * h + k];
           v *= f;
-          if (g.whole) {
-            const int at = g.out_row[row];
+          if (whole) {
+            const int at = dry ? -1 : g.out_row[row];
             if (at >= 0 && d < a.D)
               static_cast<__nv_bfloat16*>(a.out)[(size_t)at * a.D + d] =
                   __float2bfloat16_rn(f == 0.f ? 0.f : v);
@@ -1172,7 +1175,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&m.qempty[qb]);
+      if (!dry && lane == 0) tc::mbar_arrive(&m.qempty[qb]);
     }
   }
   tc::fence_before_sync();
@@ -1192,8 +1195,8 @@ __global__ void __launch_bounds__(kJoinThreads)
                               const float* __restrict__ part) {
   __shared__ int s_sum[2][kJoinRows];
   __shared__ float s_w[kJoinRows][kMaxCtas];
-  pdl_trigger();
-  pdl_wait();
+  // The launch before lets this one start once it has waited for what wrote
+  // the lengths: only the partial sums are to be waited for.
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int u = blockIdx.x;
   const int rt = u % shape.row_tiles;
@@ -1228,11 +1231,16 @@ __global__ void __launch_bounds__(kJoinThreads)
   for (int i = 0; i < rt; ++i)
     before += kUnitCost + tiles_of(a, shape, l, i);
   const int tiles = tiles_of(a, shape, l, rt);
-  if (tiles < 2) return;
+  if (tiles < 2) {
+    pdl_wait();
+    return;
+  }
   const int head = before + kUnitCost;  // of its first tile
   const int end = head + tiles;
   const int c0 = (int)(((head + 1ll) * G - 1) / total);
   const int c1 = (int)(((long long)end * G - 1) / total);  // of tile end - 1
+  pdl_trigger();
+  pdl_wait();
   if (c0 == c1) return;
   const int r = blockIdx.y * kJoinRows + warp;
   const int row = rt * shape.N + r;
