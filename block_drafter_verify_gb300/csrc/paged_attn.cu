@@ -10,10 +10,13 @@
 // parts that run at the same time.
 //
 // A row is a (query, head) pair; the Hq / Hkv heads that share a key head
-// read its tokens together.  The CUDA-core kernel takes 16 rows of one key
-// head and a part of the tokens: tiles of 32 tokens go through registers
-// (loaded one tile ahead) to shared memory as fp32; lane = token for the
-// scores, lane = dimension for the sum of values.
+// read its tokens together.  The CUDA-core kernel takes up to eight rows of
+// one key head and a part of the tokens; its warps take tiles of 32 tokens
+// in turn, each with sums of its own (joined in shared memory at the end),
+// so that few rows still make many independent warps.  For the scores
+// lane = token, which reads its key's codes 16 at a time (the tile's lines
+// are used whole, over the steps); for the sum of values lane = four
+// dimensions, one line per token.  No tile passes through shared memory.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -27,12 +30,11 @@ dflash_status current_device_info(int* sms, int** err);
 
 namespace {
 
-constexpr int kRows = 16;     // rows of a CTA
+constexpr int kRows = 8;      // rows of a CTA
 constexpr int kTok = 32;      // tokens of a tile
-constexpr int kWarps = 4;
-constexpr int kRowsWarp = kRows / kWarps;
+constexpr int kWarps = 8;
 constexpr int kMaxSplits = 32;
-constexpr int kTargetCtas = 608;  // four to an SM
+constexpr int kTargetCtas = 456;  // three to an SM
 
 // Parts each sequence is cut into, from the sizes the host knows.
 int simt_splits(long long B, long long Q, int Hq, int Hkv) {
@@ -62,18 +64,17 @@ __device__ __forceinline__ void decode16(const uint4& w, float s,
   }
 }
 
-// KD = 32-dimension slices of the widest head this instance takes.
-template <typename T, int KD>
+// W = words of four dimensions that a lane holds; with G = 2 the halves of a
+// warp take two tokens' values at a time (heads of up to 64 dimensions).
+template <typename T, int W, int G>
 __global__ void __launch_bounds__(kWarps * 32)
     paged_attn_simt_kernel(const __grid_constant__ PagedAttnArgs a, int splits,
                            int row_tiles, float* __restrict__ part) {
-  constexpr int DM = 32 * KD;
-  constexpr int kChunks = kTok * DM / 16 / (kWarps * 32);  // per thread
   extern __shared__ float4 smem4[];
-  float* sk = reinterpret_cast<float*>(smem4);      // [kTok][D + 4]
-  const int D = a.D, SK = D + 4;
-  float* sv = sk + kTok * SK;                       // [kTok][D]
-  float* sq = sv + kTok * D;                        // [kRows][D]
+  const int D = a.D;
+  float* sq = reinterpret_cast<float*>(smem4);  // [kRows][D]
+  float* so = sq + kRows * D;                   // [kWarps][kRows][D]
+  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -84,159 +85,174 @@ __global__ void __launch_bounds__(kWarps * 32)
   item /= row_tiles;
   const int hk = item % a.Hkv, b = item / a.Hkv;
   const int g = a.Hq / a.Hkv;
+  const int row0 = tile * kRows, rows_here = min(kRows, a.Q * g - row0);
   bool bad = false;
   const int n = attn_clamp(a.kv_len[b], a.max_pages * (long long)a.page, &bad);
   const int nq = attn_clamp(a.q_len ? a.q_len[b] : a.Q, a.Q, &bad);
   if (bad && tid == 0) raise_error(a.err, kErrBadIndex);
-
   for (int i = tid; i < kRows * D; i += kWarps * 32) {
-    const int r = tile * kRows + i / D;
-    const int qi = r / g, h = hk * g + r % g;
-    sq[i] = qi < nq ? to_f32(static_cast<const T*>(a.q)[
-                          (((size_t)b * a.Q + qi) * a.Hq + h) * D + i % D]) *
-                          a.scale
-                    : 0.f;
+    const int r = i / D, row = row0 + r;
+    const int qi = row / g, h = hk * g + row % g;
+    sq[i] = r < rows_here && qi < nq
+                ? to_f32(static_cast<const T*>(
+                      a.q)[(((size_t)b * a.Q + qi) * a.Hq + h) * D + i % D]) *
+                      a.scale
+                : 0.f;
   }
-  // tokens each of this warp's rows sees: t < lim
-  int lim[kRowsWarp];
-  int most = 0;
+  // tokens each row sees: t < lim (none for a row without a query)
+  int lim[kRows], most = 0;
 #pragma unroll
-  for (int k = 0; k < kRowsWarp; ++k) {
-    const int r = tile * kRows + wid * kRowsWarp + k;
-    const int qi = r / g;
-    lim[k] = qi >= nq ? 0 : a.causal ? max(0, min(n, n - nq + qi + 1)) : n;
-  }
-  {
-    const int r_last = min((tile + 1) * kRows, a.Q * g) - 1;
-    const int qi = min(r_last / g, nq - 1);
-    most = nq == 0 ? 0 : a.causal ? max(0, min(n, n - nq + qi + 1)) : n;
+  for (int r = 0; r < kRows; ++r) {
+    const int qi = (row0 + r) / g;
+    lim[r] = r >= rows_here || qi >= nq
+                 ? 0
+                 : a.causal ? max(0, min(n, n - nq + qi + 1)) : n;
+    most = max(most, lim[r]);
   }
   int chunk = (most + splits - 1) / splits;
   chunk = max((chunk + kTok - 1) / kTok * kTok, 2 * kTok);
   const int t0 = (int)min((long long)sp * chunk, (long long)most);
   const int t1 = (int)min((long long)t0 + chunk, (long long)most);
+  __syncthreads();
 
-  uint4 kr[kChunks], vr[kChunks];
-  float ks[kChunks], vs[kChunks];
-  const int row_chunks = D / 16;
-  auto fetch = [&](int base) {
+  const int part_lane = G == 2 ? lane & 15 : lane;  // words of a value
+  float m[kRows], l[kRows], o[kRows][4 * W];
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const int i = tid + c * kWarps * 32;
-      const int t = base + i / row_chunks;
-      kr[c] = vr[c] = make_uint4(0, 0, 0, 0);
-      ks[c] = vs[c] = 0.f;
-      if (i < kTok * row_chunks && t < t1) {
-        const int id = a.table[(size_t)b * a.max_pages + t / a.page];
-        if (id >= 0 && id < a.num_pages) {
-          const size_t ph = (size_t)id * a.Hkv + hk;
-          const size_t at = (ph * a.page + t % a.page) * D +
-                            (i % row_chunks) * 16;
-          kr[c] = *reinterpret_cast<const uint4*>(a.k_codes + at);
-          vr[c] = *reinterpret_cast<const uint4*>(a.v_codes + at);
-          ks[c] = a.k_scale[ph];
-          vs[c] = a.v_scale[ph];
-        } else {
-          raise_error(a.err, kErrBadIndex);
+  for (int r = 0; r < kRows; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+#pragma unroll
+    for (int d = 0; d < 4 * W; ++d) o[r][d] = 0.f;
+  }
+  for (int base = t0 + wid * kTok; base < t1; base += kWarps * kTok) {
+    // this lane's token: where its codes are, its scales
+    const int t = base + lane;
+    int id = -1;
+    if (t < t1) {
+      id = a.table[(size_t)b * a.max_pages + t / a.page];
+      if (id < 0 || id >= a.num_pages) {
+        raise_error(a.err, kErrBadIndex);
+        id = -1;
+      }
+    }
+    const size_t ph = id >= 0 ? (size_t)id * a.Hkv + hk : 0;
+    const size_t at = (ph * a.page + t % a.page) * D;
+    const float ks = id >= 0 ? a.k_scale[ph] : 0.f;
+    const float vs = id >= 0 ? a.v_scale[ph] : 0.f;
+    float s[kRows] = {};
+#pragma unroll 2
+    for (int d = 0; d < D; d += 16) {
+      uint4 kc = make_uint4(0, 0, 0, 0);
+      if (id >= 0) kc = *reinterpret_cast<const uint4*>(a.k_codes + at + d);
+      float k[16];
+      decode16(kc, ks, k);
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        if (r >= rows_here) break;  // uniform
+        const float4* q4 = reinterpret_cast<const float4*>(sq + r * D + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 q = q4[i];
+          s[r] = fmaf(q.x, k[4 * i], fmaf(q.y, k[4 * i + 1],
+                 fmaf(q.z, k[4 * i + 2], fmaf(q.w, k[4 * i + 3], s[r]))));
         }
       }
     }
-  };
-  float m[kRowsWarp], l[kRowsWarp], o[kRowsWarp][KD];
+    float w[kRows];  // this lane's token's weights, times its values' scale
 #pragma unroll
-  for (int k = 0; k < kRowsWarp; ++k) {
-    m[k] = -INFINITY;
-    l[k] = 0.f;
+    for (int r = 0; r < kRows; ++r) {
+      w[r] = 0.f;
+      if (r >= rows_here) break;
+      const float x = t < min(lim[r], t1) ? s[r] : -INFINITY;
+      const float mn = fmaxf(m[r], warp_max(x));
+      const float f = mn == -INFINITY ? 1.f : expf(m[r] - mn);
+      const float p = x == -INFINITY ? 0.f : expf(x - mn);
+      l[r] = l[r] * f + p;
+      m[r] = mn;
+      w[r] = p * vs;
 #pragma unroll
-    for (int d = 0; d < KD; ++d) o[k][d] = 0.f;
-  }
-  if (t0 < t1) fetch(t0);
-  for (int base = t0; base < t1; base += kTok) {
-    __syncthreads();  // the previous tile has been read
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      const int i = tid + c * kWarps * 32;
-      if (i < kTok * row_chunks) {
-        const int t = i / row_chunks, d = (i % row_chunks) * 16;
-        float f[16];
-        decode16(kr[c], ks[c], f);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          *reinterpret_cast<float4*>(sk + t * SK + d + 4 * k) =
-              make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
-        decode16(vr[c], vs[c], f);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          *reinterpret_cast<float4*>(sv + t * D + d + 4 * k) =
-              make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
-      }
+      for (int d = 0; d < 4 * W; ++d) o[r][d] *= f;
     }
-    __syncthreads();
-    if (base + kTok < t1) fetch(base + kTok);
-    float s[kRowsWarp] = {};
-    const float* kt = sk + lane * SK;
-    const float* qr = sq + wid * kRowsWarp * D;
+    const long long mine = id >= 0 ? (long long)at : -1;
 #pragma unroll 4
-    for (int d = 0; d < D; d += 4) {
-      const float4 kv = *reinterpret_cast<const float4*>(kt + d);
+    for (int i = 0; i < kTok; i += G) {
+      const int from = G == 2 ? i + (lane >> 4) : i;
+      const long long src = __shfl_sync(0xffffffffu, mine, from);
+      uint32_t v[W];
 #pragma unroll
-      for (int k = 0; k < kRowsWarp; ++k) {
-        const float4 qv = *reinterpret_cast<const float4*>(qr + k * D + d);
-        s[k] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y,
-                    fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, s[k]))));
+      for (int c = 0; c < W; ++c) {
+        const int d = 4 * (part_lane + 32 * c);
+        v[c] = src >= 0 && d < D
+                   ? *reinterpret_cast<const uint32_t*>(a.v_codes + src + d)
+                   : 0;
       }
-    }
-    float p[kRowsWarp];
+      float x[4 * W];
 #pragma unroll
-    for (int k = 0; k < kRowsWarp; ++k) {
-      const bool sees = base + lane < min(lim[k], t1);
-      const float x = sees ? s[k] : -INFINITY;
-      const float mn = fmaxf(m[k], warp_max(x));
-      const float f = mn == -INFINITY ? 1.f : expf(m[k] - mn);
-      p[k] = x == -INFINITY ? 0.f : expf(x - mn);
-      l[k] = l[k] * f + p[k];
-      m[k] = mn;
+      for (int c = 0; c < W; ++c)
 #pragma unroll
-      for (int d = 0; d < KD; ++d) o[k][d] *= f;
-    }
-#pragma unroll 4
-    for (int t = 0; t < kTok; ++t) {
-      float v[KD];
+        for (int j = 0; j < 2; ++j) {
+          const float2 f2 = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
+              (__nv_fp8x2_storage_t)(v[c] >> (16 * j)), __NV_E4M3)));
+          x[4 * c + 2 * j] = f2.x;
+          x[4 * c + 2 * j + 1] = f2.y;
+        }
 #pragma unroll
-      for (int d = 0; d < KD; ++d)
-        v[d] = lane + 32 * d < D ? sv[t * D + lane + 32 * d] : 0.f;
+      for (int r = 0; r < kRows; ++r) {
+        if (r >= rows_here) break;
+        const float wr = __shfl_sync(0xffffffffu, w[r], from);
 #pragma unroll
-      for (int k = 0; k < kRowsWarp; ++k) {
-        const float w = __shfl_sync(0xffffffffu, p[k], t);
-#pragma unroll
-        for (int d = 0; d < KD; ++d) o[k][d] = fmaf(w, v[d], o[k][d]);
+        for (int d = 0; d < 4 * W; ++d) o[r][d] = fmaf(wr, x[d], o[r][d]);
       }
     }
   }
+  // ---- the warps' sums ------------------------------------------------------
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    if (r >= rows_here) break;
+    const float sum = warp_sum(l[r]);
+    if (lane == 0) {
+      s_m[wid][r] = m[r];
+      s_l[wid][r] = sum;
+    }
+#pragma unroll
+    for (int d = 0; d < 4 * W; ++d)
+      if (G == 2) o[r][d] += __shfl_xor_sync(0xffffffffu, o[r][d], 16);
+#pragma unroll
+    for (int c = 0; c < W; ++c) {
+      const int d = 4 * (part_lane + 32 * c);
+      if (d < D && (G == 1 || lane < 16))
+        *reinterpret_cast<float4*>(so + ((size_t)wid * kRows + r) * D + d) =
+            make_float4(o[r][4 * c], o[r][4 * c + 1], o[r][4 * c + 2],
+                        o[r][4 * c + 3]);
+    }
+  }
+  __syncthreads();
   const long long rows = (long long)a.B * a.Q * a.Hq;
+  for (int i = tid; i < rows_here * D; i += kWarps * 32) {
+    const int r = i / D, d = i % D, rr = row0 + r;
+    const long long row =
+        ((long long)b * a.Q + rr / g) * a.Hq + hk * g + rr % g;
+    float top = -INFINITY;
 #pragma unroll
-  for (int k = 0; k < kRowsWarp; ++k) {
-    const int r = tile * kRows + wid * kRowsWarp + k;
-    const float sum = warp_sum(l[k]);
-    if (r >= a.Q * g) continue;
-    const long long row = ((long long)b * a.Q + r / g) * a.Hq + hk * g + r % g;
+    for (int v = 0; v < kWarps; ++v) top = fmaxf(top, s_m[v][r]);
+    float sum = 0.f, acc = 0.f;
+#pragma unroll
+    for (int v = 0; v < kWarps; ++v) {
+      const float f = s_m[v][r] == -INFINITY ? 0.f : expf(s_m[v][r] - top);
+      sum = fmaf(f, s_l[v][r], sum);
+      if (f != 0.f) acc = fmaf(f, so[((size_t)v * kRows + r) * D + d], acc);
+    }
+    const bool seen = sum > 0.f || sum != sum;  // a NaN stays one
     if (splits == 1) {
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-      for (int d = 0; d < KD; ++d)
-        if (lane + 32 * d < D)
-          static_cast<T*>(a.out)[row * D + lane + 32 * d] =
-              from_f32<T>(o[k][d] * inv);
-      if (lane == 0 && a.lse)
-        a.lse[row] = sum > 0.f ? m[k] + logf(sum) : -INFINITY;
+      static_cast<T*>(a.out)[row * D + d] =
+          from_f32<T>(seen ? acc / sum : 0.f);
+      if (d == 0 && a.lse) a.lse[row] = seen ? top + logf(sum) : -INFINITY;
     } else {
-      float* po = part + ((size_t)sp * rows + row) * D;
-      float* pm = part + (size_t)splits * rows * D + ((size_t)sp * rows + row) * 2;
-#pragma unroll
-      for (int d = 0; d < KD; ++d)
-        if (lane + 32 * d < D) po[lane + 32 * d] = o[k][d];
-      if (lane == 0) {
-        pm[0] = m[k];
+      part[((size_t)sp * rows + row) * D + d] = acc;
+      if (d == 0) {
+        float* pm = part + (size_t)splits * rows * D +
+                    ((size_t)sp * rows + row) * 2;
+        pm[0] = top;
         pm[1] = sum;
       }
     }
@@ -263,7 +279,8 @@ __global__ void __launch_bounds__(128)
   const float m = warp_max(mi);
   const float w = mi == -INFINITY ? 0.f : expf(mi - m);
   const float l = warp_sum(w * li);
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const bool seen = l > 0.f || l != l;  // a NaN stays one
+  const float inv = seen ? 1.f / l : 0.f;
   for (int base = 0; base < D; base += 32) {  // whole warps shuffle
     const int d = base + lane;
     float o = 0.f;
@@ -274,19 +291,18 @@ __global__ void __launch_bounds__(128)
     }
     if (d < D) out[row * D + d] = from_f32<T>(o * inv);
   }
-  if (lane == 0 && lse) lse[row] = l > 0.f ? m + logf(l) : -INFINITY;
+  if (lane == 0 && lse) lse[row] = seen ? m + logf(l) : -INFINITY;
 }
 
-template <typename T, int KD>
+template <typename T, int W, int G>
 cudaError_t launch_simt(const PagedAttnArgs& a, float* part, cudaStream_t s) {
   const int g = a.Hq / a.Hkv;
   const int tiles = (a.Q * g + kRows - 1) / kRows;
   const int ns = simt_splits(a.B, a.Q, a.Hq, a.Hkv);
   const long long ctas = (long long)a.B * a.Hkv * tiles * ns;
   if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
-  const size_t smem = (size_t)(kTok * (a.D + 4) + kTok * a.D + kRows * a.D) *
-                      sizeof(float);
-  auto* f = paged_attn_simt_kernel<T, KD>;
+  const size_t smem = (size_t)(1 + kWarps) * kRows * a.D * sizeof(float);
+  auto* f = paged_attn_simt_kernel<T, W, G>;
   cudaError_t e = cudaFuncSetAttribute(
       f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -303,9 +319,9 @@ cudaError_t launch_simt(const PagedAttnArgs& a, float* part, cudaStream_t s) {
 template <typename T>
 cudaError_t launch_simt_d(const PagedAttnArgs& a, float* part,
                           cudaStream_t s) {
-  if (a.D <= 64) return launch_simt<T, 2>(a, part, s);
-  if (a.D <= 128) return launch_simt<T, 4>(a, part, s);
-  return launch_simt<T, 8>(a, part, s);
+  if (a.D <= 64) return launch_simt<T, 1, 2>(a, part, s);
+  if (a.D <= 128) return launch_simt<T, 1, 1>(a, part, s);
+  return launch_simt<T, 2, 1>(a, part, s);
 }
 
 inline bool aligned_to(const void* p, uintptr_t a) {
