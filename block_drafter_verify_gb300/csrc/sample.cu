@@ -96,7 +96,7 @@ struct Shared {
   u64 kept_w[kWarps];    // kept weight of each warp's chunk
   float kept_least[kWarps];  // and its smallest kept logit
   uint32_t kept_n;
-  uint32_t bad;
+  uint32_t odd;          // a logit of the slice is not finite
   uint32_t listed;
   uint64_t landed[kChunks];  // barriers of the slice's copies
   // this CTA's own
@@ -138,13 +138,19 @@ __device__ __forceinline__ float x_plain(float l, const Row& r) {
 // floor(x 2^44) for 0 <= x <= 1, as 21 and 23 bits that additions to 2^23
 // (whose last place is 1) round off towards zero: the conversion to a 64-bit
 // integer has a sixteenth of their rate.
-__device__ __forceinline__ u64 weight_of(float x) {
+struct WeightBits {
+  uint32_t hi, lo;  // 0x4b000000 (the bits of 2^23) above the halves
+};
+__device__ __forceinline__ WeightBits weight_bits(float x) {
   const float xs = __fmul_rn(x, 0x1p21f);
   const float hi = __fadd_rz(xs, 0x1p23f);
   const float rest = __fsub_rn(xs, __fsub_rn(hi, 0x1p23f));  // exact
   const float lo = __fmaf_rz(rest, 0x1p23f, 0x1p23f);
-  return (u64)(__float_as_uint(hi) - 0x4b000000u) * (1u << 23) +
-         (__float_as_uint(lo) - 0x4b000000u);
+  return WeightBits{__float_as_uint(hi), __float_as_uint(lo)};
+}
+__device__ __forceinline__ u64 weight_of(float x) {
+  const WeightBits w = weight_bits(x);
+  return (u64)(w.hi - 0x4b000000u) * (1u << 23) + (w.lo - 0x4b000000u);
 }
 // Bin of a logit: 0 at the maximum, rising as it falls; monotone in l.
 __device__ __forceinline__ int bin_of(float l, const Row& r) {
@@ -545,7 +551,7 @@ __global__ void __launch_bounds__(kThreads)
 
   // ---- the slice and the row's maximum -------------------------------------
   if (tid == 0) {
-    S.bad = 0;
+    S.odd = 0;
     S.kept_n = 0;
     S.listed = 0;
     S.first = 0x7fffffff;
@@ -556,10 +562,33 @@ __global__ void __launch_bounds__(kThreads)
   float tops[kChunks];  // of this thread's tokens, by quarters
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) tops[c] = -INFINITY;
-  bool bad = false;
+  bool odd = false;  // a logit that is not finite
   auto take = [&](int c, float l) {
-    bad |= !(l < INFINITY);         // NaN, too
+    odd |= !(fabsf(l) < INFINITY);
     tops[c] = fmaxf(tops[c], l);    // passes over a NaN
+  };
+  // A word of them; bf16 in pairs: what is not finite survives one of the
+  // largest of the pairs and the smallest.
+  auto take_word = [&](int c, const Vec<T>& x) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int k = 0; k < Vec<T>::E; ++k) take(c, x.at(k));
+    } else {
+      const __nv_bfloat162* v =
+          reinterpret_cast<const __nv_bfloat162*>(&x.w);
+      const __nv_bfloat162 hi = __hmax2_nan(__hmax2_nan(v[0], v[1]),
+                                            __hmax2_nan(v[2], v[3]));
+      const __nv_bfloat162 lo = __hmin2_nan(__hmin2_nan(v[0], v[1]),
+                                            __hmin2_nan(v[2], v[3]));
+      const float2 h = __bfloat1622float2(hi), l = __bfloat1622float2(lo);
+      if (fabsf(h.x) < INFINITY && fabsf(h.y) < INFINITY &&
+          l.x > -INFINITY && l.y > -INFINITY) {
+        tops[c] = fmaxf(tops[c], fmaxf(h.x, h.y));
+      } else {
+#pragma unroll
+        for (int k = 0; k < Vec<T>::E; ++k) take(c, x.at(k));
+      }
+    }
   };
   if (src_wide && a.resident) {
     constexpr int E = Vec<T>::E;
@@ -582,8 +611,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll 4
       for (int v = min(words, c * per) + tid; v < v1; v += kThreads) {
         const Vec<T> x{reinterpret_cast<const uint4*>(own)[v]};
-#pragma unroll
-        for (int k = 0; k < E; ++k) take(c, x.at(k));
+        take_word(c, x);
       }
     }
     for (int i = words * E + tid; i < n; i += kThreads) {
@@ -602,10 +630,7 @@ __global__ void __launch_bounds__(kThreads)
         if (v + c * kThreads < words) x[c].w = p[v + c * kThreads];
 #pragma unroll
       for (int c = 0; c < kChunks; ++c)
-        if (v + c * kThreads < words) {
-#pragma unroll
-          for (int k = 0; k < E; ++k) take(c, x[c].at(k));
-        }
+        if (v + c * kThreads < words) take_word(c, x[c]);
     }
     for (int i = words * E + tid; i < n; i += kThreads)
       take(0, to_f32(src[i]));
@@ -628,7 +653,7 @@ __global__ void __launch_bounds__(kThreads)
   top = warp_max(top);
   if (lane == 0) S.warp_w[wid] = __float_as_uint(top);
   __syncthreads();
-  if (bad) S.bad = 1;
+  if (odd) S.odd = 1;
   if (tid == 0) {
     for (int i = 1; i < kWarps; ++i)
       top = fmaxf(top, __uint_as_float((uint32_t)S.warp_w[i]));
@@ -644,8 +669,14 @@ __global__ void __launch_bounds__(kThreads)
   r.greedy = !(t > 0.f && t < INFINITY);
   r.inv_t = r.greedy ? 0.f : __fdiv_rn(1.f, t);
   const bool empty = top == -INFINITY;
-  if (tid == 0 && (S.bad || empty || !(t >= 0.f && t < INFINITY)))
+  if (tid == 0 && (empty || !(t >= 0.f && t < INFINITY)))
     raise_error(a.err, kErrNonfinite);
+  if (S.odd) {  // -inf is a masked token, the others are errors
+    bool bad = false;
+    each(data, wide, 0, n, tid, kThreads,
+         [&](int, float l) { bad |= !(l < INFINITY); });
+    if (bad) raise_error(a.err, kErrNonfinite);
+  }
   const int k = a.top_k ? a.top_k[row] : 0;
   const float p = a.top_p ? a.top_p[row] : 1.f;
   // at most 1 (which keeps the maximum), 0 for what is no number
@@ -806,8 +837,31 @@ __global__ void __launch_bounds__(kThreads)
       if (least > 0.f && least < 1.f)
         low = r.top + logf(least) * t * 1.0001f - fabsf(r.top) * 1e-6f;
     }
+    const bool plain = !S.odd && r.inv_t < INFINITY;
     auto fill = [&] {
       u64 sum = 0;
+      if (plain) {  // as in the sum of all weights below
+        for (int b = 0; b < n; b += kThreads * 512) {
+          uint32_t hi = 0, lo = 0, m = 0;
+          each(data, wide, b, min(n, b + kThreads * 512), tid, kThreads,
+               [&](int, float l) {
+                 const WeightBits w = weight_bits(x_plain(l, r));
+                 hi += w.hi;
+                 lo += w.lo;
+                 ++m;
+                 if (l < low) return;
+                 const int bin = bin_of(l, r);
+                 atomicAdd(&S.count[bin], 1u);
+                 if (by_p)
+                   add_weight(S, bin,
+                              (u64)(w.hi - 0x4b000000u) * (1u << 23) +
+                                  (w.lo - 0x4b000000u));
+               });
+          sum += (u64)(hi - m * 0x4b000000u) * (1u << 23) +
+                 (lo - m * 0x4b000000u);
+        }
+        return sum;
+      }
       each(data, wide, 0, n, tid, kThreads, [&](int i, float l) {
         if (!(l > -INFINITY)) return;
         const u64 w = weight_of(x_of(l, r));
@@ -884,17 +938,30 @@ __global__ void __launch_bounds__(kThreads)
   uint32_t cnt = 0;
   float least = INFINITY;  // smallest kept logit, where min-p has a say
   if (cut == 0 && !by_m) {
-    if (S.bad || !(r.inv_t < INFINITY))
+    if (S.odd || !(r.inv_t < INFINITY)) {  // uniform in the CTA
       each(data, wide, c0, c1, lane, 32, [&](int, float l) {
         const bool on = l > -INFINITY;  // not a NaN, either
         sum += weight_of(on ? x_of(l, r) : 0.f);
         cnt += on;
       });
-    else
-      each(data, wide, c0, c1, lane, 32, [&](int, float l) {
-        sum += weight_of(x_plain(l, r));
-        cnt += l > -INFINITY;
-      });
+    } else {
+      // All weights are wanted and all logits finite.  The halves of up to
+      // 512 weights fit 32 bits each; the 0x4b000000 of every float comes
+      // off at the end.
+      for (int b = c0; b < c1; b += 32 * 512) {
+        const int e = min(c1, b + 32 * 512);
+        uint32_t hi = 0, lo = 0, m = 0;
+        each(data, wide, b, e, lane, 32, [&](int, float l) {
+          const WeightBits w = weight_bits(x_plain(l, r));
+          hi += w.hi;
+          lo += w.lo;
+          ++m;
+        });
+        sum += (u64)(hi - m * 0x4b000000u) * (1u << 23) +
+               (lo - m * 0x4b000000u);
+        cnt += m;
+      }
+    }
   } else {
     // no weight is needed of what lies surely below the filters
     const float low =
@@ -1010,13 +1077,15 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename T>
 cudaError_t launch(SampleArgs a, cudaStream_t s) {
-  // One wave of CTAs, four to an SM, if that takes at most eight to a row:
-  // fewer to a row cost less in barriers between them (288 rows of 151936
+  // Two waves of CTAs, four to an SM, if that takes at most eight to a row.
+  // Fewer to a row cost less in barriers between them (288 rows of 151936
   // fp32 logits, top-k 50: 126 us with eight, 84 us with two), more of them
-  // shorten a lone row (20 us with eight, 28 us with two).  Never more than
-  // slices of 4096 tokens need.
+  // shorten rows that need several passes (the same rows with mixed filters:
+  // 249 us with two, 219 us with four, 248 us with eight; a lone row of
+  // top-k 50: 28 us with two, 20 us with eight).  Never more than slices of
+  // 4096 tokens need.
   int C = kMaxCluster;
-  while (C > 1 && ((long long)a.R * C > 4 * 152 ||
+  while (C > 1 && ((long long)a.R * C > 8 * 152 ||
                    (long long)(C / 2) * 4096 >= a.V))
     C /= 2;
   // A slice stays in shared memory where two CTAs fit an SM so; the rest is
