@@ -409,7 +409,7 @@ cudaError_t launch(const AppendArgs& a, bool inter, cudaStream_t s) {
   if (a.q)
     rot = (((long long)a.B * a.Q * units + nt - 1) / nt) *
           ((a.Hq + kHeads - 1) / kHeads);
-  if (cache + rot > 0x7fffffffll) return cudaErrorInvalidValue;
+  if (cache + rot > 0x7fffffffll) return cudaErrorNotSupported;
   args.cache_ctas = (int)cache;
   PdlLaunch L(dim3((unsigned)(cache + rot)), dim3(nt), 0, s);
   return inter ? cudaLaunchKernelEx(&L.cfg, kv_append_kernel<T, VEC, true>, args)
@@ -499,5 +499,7 @@ extern "C" dflash_status dflash_kv_append(
     e = launch<__nv_bfloat16, 8>(a, interleaved != 0, s);
   else
     e = launch<__nv_bfloat16, 4>(a, interleaved != 0, s);
-  return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
+  return e == cudaSuccess            ? DFLASH_OK
+         : e == cudaErrorNotSupported ? DFLASH_ERR_UNSUPPORTED
+                                      : DFLASH_ERR_CUDA;
 }

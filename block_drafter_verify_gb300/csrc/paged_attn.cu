@@ -300,7 +300,7 @@ cudaError_t launch_simt(const PagedAttnArgs& a, float* part, cudaStream_t s) {
   const int tiles = (a.Q * g + kRows - 1) / kRows;
   const int ns = simt_splits(a.B, a.Q, a.Hq, a.Hkv);
   const long long ctas = (long long)a.B * a.Hkv * tiles * ns;
-  if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
+  if (ctas > 0x7fffffffll) return cudaErrorNotSupported;
   const size_t smem = (size_t)(1 + kWarps) * kRows * a.D * sizeof(float);
   auto* f = paged_attn_simt_kernel<T, W, G>;
   cudaError_t e = cudaFuncSetAttribute(
@@ -400,7 +400,9 @@ dflash_status dflash_paged_attn(
       : dt == DFLASH_FP32
           ? launch_simt_d<float>(a, static_cast<float*>(ws), s)
           : launch_simt_d<__nv_bfloat16>(a, static_cast<float*>(ws), s);
-  return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
+  return e == cudaSuccess            ? DFLASH_OK
+         : e == cudaErrorNotSupported ? DFLASH_ERR_UNSUPPORTED
+                                      : DFLASH_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -8,12 +8,14 @@
 //        numbers (8 bits, all that bf16 has), both products added.  The rows
 //        of a unit share the scale; a row more than 2^6 below the largest
 //        has its own (and costs the softmax one multiplication);
-//   P    the softmax weights, rounded to fp16 (11 bits), are written as the
-//        sum of three E5M2 numbers.  E5M2 is the upper byte of fp16: a part
-//        is that byte after rounding, the rest an exact fp16 difference, and
-//        three parts of three bits and a sign hold eleven bits.  That takes
-//        no conversion instructions (parts made by those took 1200 cycles
-//        a tile of 80 rows), and no part needs a scale of its own.
+//   P    the softmax weights are written as the sum of four E5M2 numbers, in
+//        all exact to 2^-13.  E5M2 is the upper byte of fp16: of the weight
+//        rounded to fp16 a part is that byte after rounding, the rest an
+//        exact fp16 difference, and three parts of three bits and a sign hold
+//        its eleven bits; the fourth is the upper byte of what fp16 rounded
+//        off.  That takes no conversion to 8 bits (parts made by those took
+//        1200 cycles a tile of 80 rows), and no part needs a scale of its
+//        own.  Without the fourth part: 2^-11, and 2 to 7 % less time.
 // Scores are computed transposed: S^T[token, row] = K q^T and
 // O^T[dim, row] = V^T P^T, so that the 128 lanes of an MMA are always full
 // (tokens, then dimensions) and the number of (query, head) rows, a multiple
@@ -58,7 +60,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kHead = 10.f;      // weights are 2^(score - ref + kHead)
 constexpr float kRaise = 15.75f;   // 2^15.75 = 55109 < 57344, E5M2's largest
 constexpr int kUnitCost = 4;       // of a unit besides its tiles, in tiles
-constexpr int kParts = 3;          // E5M2 parts of a weight
+constexpr int kParts = 4;          // E5M2 parts of a weight
 
 // Shared-memory plan for N rows.
 template <int N>
@@ -81,7 +83,7 @@ struct Plan {
   // and TMEM (512 columns) allow: fewer MMAs, whose time is that of reading
   // the 128 lanes' operand when N is small.
   static constexpr int kScore = N <= 64 ? 2 * N : N;    // columns of a tile
-  static constexpr int kAcc = N <= 80 ? kParts * N : 2 * N;
+  static constexpr int kAcc = N <= 64 ? kParts * N : 2 * N;
   static constexpr int kUse = 2 * kScore + kAcc;
   static constexpr int kCols =
       kUse <= 128 ? 128 : kUse <= 256 ? 256 : 512;
@@ -453,16 +455,24 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Four weights (fp32 below 57344) as kParts words of four E5M2 numbers.
+// Four weights (fp32 below 57344) as kParts words of four E5M2 numbers:
+// three for the weight rounded to fp16, one for what that rounded off.
 __device__ __forceinline__ void split(float e0, float e1, float e2, float e3,
                                       uint32_t (&w)[kParts]) {
   __half2 a = __floats2half2_rn(e0, e1), b = __floats2half2_rn(e2, e3);
+  {
+    const float2 fa = __half22float2(a), fb = __half22float2(b);
+    const __half2 ra = __floats2half2_rn(e0 - fa.x, e1 - fa.y);  // exact
+    const __half2 rb = __floats2half2_rn(e2 - fb.x, e3 - fb.y);
+    w[3] = __byte_perm(*reinterpret_cast<const uint32_t*>(&ra),
+                       *reinterpret_cast<const uint32_t*>(&rb), 0x7531);
+  }
 #pragma unroll
-  for (int p = 0; p < kParts; ++p) {
+  for (int p = 0; p < 3; ++p) {
     const uint32_t ua = *reinterpret_cast<const uint32_t*>(&a);
     const uint32_t ub = *reinterpret_cast<const uint32_t*>(&b);
-    // to the nearest upper byte, ties away; the last part fits one
-    if (p + 1 == kParts) {
+    // to the nearest upper byte, ties away; the third part fits one
+    if (p == 2) {
       w[p] = __byte_perm(ua, ub, 0x7531);
     } else {
       const uint32_t ta = (ua + 0x00800080u) & 0xff00ff00u;
@@ -685,7 +695,8 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
         const uint64_t dp =
             sdesc_mn_plain(tc::smem_u32(sp) + rp.at * kParts * N * 128);
         if (elect_one()) {
-          // all parts side by side, or 0 and 1, then 2 onto the columns of 0
+          // all parts side by side, or 0 and 1, then 2 and 3 onto the same
+          // columns
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             tc::mma_e4m3(tm + 2 * PL::kScore, dv + 256 * k, dp + 32 * k, id_o,
@@ -694,7 +705,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               tc::mma_e4m3(tm + 2 * PL::kScore, dv + 256 * k,
-                           dp + N * 16 + 32 * k, idesc_mn(N), 1);
+                           dp + N * 16 + 32 * k, id_o, 1);
           }
           tc::mma_commit(&m.vempty[rv.at]);
         }
@@ -1335,7 +1346,7 @@ cudaError_t launch_paged_attn_tc(const PagedAttnArgs& a, int sms, float* part,
   const long long most =
       (long long)a.B * a.Hkv * s.row_tiles *
       (((long long)a.max_pages * a.page + kTile - 1) / kTile + kUnitCost);
-  if (most > 0x7fffffffll) return cudaErrorInvalidValue;
+  if (most > 0x7fffffffll) return cudaErrorNotSupported;
   const int G = std::min(sms, kMaxCtas);
   CUtensorMap mk, mv;
   const uint64_t rows = (uint64_t)a.num_pages * a.Hkv * a.page;
@@ -1353,7 +1364,7 @@ cudaError_t launch_paged_attn_tc(const PagedAttnArgs& a, int sms, float* part,
   }
   if (e != cudaSuccess) return e;
   const long long units = (long long)a.B * a.Hkv * s.row_tiles;
-  if (units > 0x7fffffffll) return cudaErrorInvalidValue;
+  if (units > 0x7fffffffll) return cudaErrorNotSupported;
   const int rows_of = std::min(s.N, s.rows);
   PdlLaunch J(dim3((unsigned)units, (rows_of + kJoinRows - 1) / kJoinRows),
               dim3(kJoinThreads), 0, stream);

@@ -585,12 +585,15 @@ size_t dflash_paged_attn_workspace_bytes(int B, int Q, int Hq, int Hkv, int D);
  *   kv_len [B] int32; q_len [B] int32 or NULL (Q each)
  *   ws >= dflash_paged_attn_workspace_bytes(B, Q, Hq, Hkv, D) bytes, 256-byte
  *      aligned; its contents need no initialisation
- * With bf16 storage and D <= 128 the products run on the tensor cores: q is
- * split exactly into E4M3 parts, the softmax weights into three E4M3 parts
- * (12 bits; sums and statistics in fp32).  Otherwise fp32 on the CUDA cores.
- * Codes and slots past kv_len may hold anything.
+ * With bf16 storage and D <= 128 the products run on the tensor cores: q as
+ * the sum of two E4M3 numbers (all its bits, down to 2^-17 of its row's
+ * largest value), the softmax weights as the sum of four E5M2 numbers (to
+ * 2^-13); sums and statistics in fp32.  Otherwise fp32 on the CUDA cores.
+ * Codes and slots past kv_len may hold anything.  Scales are powers of two
+ * between 2^-100 and 2^120, as dflash_kv_append writes them.
  * Requirements: Hq % Hkv == 0, Hq / Hkv <= 64, q, out and the codes 16-byte
- * aligned; scale finite.  On the device: kv_len below 0 or beyond the page
+ * aligned; scale finite; fewer than 2^31 tiles of 128 tokens over all
+ * sequences' page tables and key heads (with bf16).  On the device: kv_len below 0 or beyond the page
  * table, q_len outside [0, Q] and a page id outside [0, num_pages) set
  * DFLASH_ERR_BAD_INDEX (lengths are clamped, such a page counts as zeros).
  */
