@@ -945,39 +945,54 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
       if (ht < HR) m.neg_ref[my_row] = 0.f;
       half_sync(bar);
       float lv_ref = 0.f;
+      // The scores of buffer `at` into y: asked for by ask(), there after
+      // got().  With more than 32 rows the softmax sets the pace, and the
+      // next tile's scores, if ready, are asked for while this tile's weights
+      // are handed over: 36 rows 78 -> 74 us, 72 rows 99 -> 96 us (eight
+      // sequences of 16,384); with fewer the cache does, and one row of
+      // 131,072 tokens went from 58 to 60 us.
+      float y[HR], z[SG == 2 ? HR : 1];
+      auto ask = [&](int at) {
+        tc::fence_after_sync();
+        const uint32_t s_col = lanes + at * PL::kScore;
+#pragma unroll
+        for (int r = 0; r < HR; r += 4) tmem_ld4(col_of(s_col, r), y + r);
+        if constexpr (SG == 2) {
+#pragma unroll
+          for (int r = 0; r < HR; r += 4) tmem_ld4(col_of(s_col + N, r), z + r);
+        }
+      };
+      auto got = [&] {
+        if constexpr (SG == 2) {
+          tmem_loaded(z);
+          tmem_loaded(y);
+#pragma unroll
+          for (int r = 0; r < HR; r += 2)
+            unpack2(add2(pack2(y[r], y[r + 1]), pack2(z[r], z[r + 1])), y[r],
+                    y[r + 1]);
+        } else {
+          tmem_loaded(y);
+        }
+        tc::fence_before_sync();
+      };
+      bool early = false;  // y holds this tile's scores already
       for (int t = 0; t < T; ++t, pos += kTile) {
         const int sb = rs.at, st = rv.at;
         // Also says that the weights' buffer is free: the scores' commit
         // follows the second product of two tiles ago.
-        ok = dry || wait_for(&m.sfull[sb], rs.phase, abort);
-        ok = __all_sync(0xffffffffu, ok);
-        float y[HR];
+        if (!early) {
+          ok = dry || wait_for(&m.sfull[sb], rs.phase, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+            ask(sb);
+            got();
+          } else {
+#pragma unroll
+            for (int r = 0; r < HR; ++r) y[r] = 0.f;
+          }
+        }
         const int pg = tok >> page_bits;
         const float ct = m.ct[st][pg] * back, lv = m.lv[st][pg];
-        if (ok) {
-          tc::fence_after_sync();
-          const uint32_t s_col = lanes + sb * PL::kScore;
-#pragma unroll
-          for (int r = 0; r < HR; r += 4) tmem_ld4(col_of(s_col, r), y + r);
-          if constexpr (SG == 2) {
-            float z[HR];
-#pragma unroll
-            for (int r = 0; r < HR; r += 4)
-              tmem_ld4(col_of(s_col + N, r), z + r);
-            tmem_loaded(z);
-            tmem_loaded(y);
-#pragma unroll
-            for (int r = 0; r < HR; r += 2)
-              unpack2(add2(pack2(y[r], y[r + 1]), pack2(z[r], z[r + 1])),
-                      y[r], y[r + 1]);
-          } else {
-            tmem_loaded(y);
-          }
-          tc::fence_before_sync();
-        } else {
-#pragma unroll
-          for (int r = 0; r < HR; ++r) y[r] = 0.f;
-        }
         if (t == 0) lv_ref = m.lv[st][0];
         const float fl = tc::ex2_approx(fminf(lv_ref - lv, 100.f));
         if (uneven) {
@@ -1102,12 +1117,25 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 8; ++k) v[k] = make_uint4(0, 0, 0, 0);
         }
-        fence_async();
-        __syncwarp();
+        early = false;
         if (!dry) {
-          if (lane == 0) tc::mbar_arrive(&m.pfull[sb]);
           rs.next();
           rv.next();
+          if (N > 32 && t + 1 < T)
+            early = tc::mbar_try_wait(&m.sfull[rs.at], rs.phase, 0);
+        }
+        early = __all_sync(0xffffffffu, early);
+        // No branch between ask() and got(): the registers are in flight.
+        if (early) {
+          ask(rs.at);
+          fence_async();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&m.pfull[sb]);
+          got();
+        } else {
+          fence_async();
+          __syncwarp();
+          if (!dry && lane == 0) tc::mbar_arrive(&m.pfull[sb]);
         }
       }
       if (!live) break;
