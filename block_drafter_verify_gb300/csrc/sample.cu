@@ -530,8 +530,11 @@ __device__ void pick(Shared& S, const Row& r, int n, int k, u64 bound, float p,
   }
 }
 
+// Three CTAs to an SM (40 registers) hide each other's barriers: 288 rows with
+// mixed filters 217 us with two (64 registers), 193 us with three, 191 us with
+// four, where 128 rows without filters go from 73 us to 78 us.
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
     sample_kernel(const __grid_constant__ SampleArgs a) {
   cg::cluster_group cl = cg::this_cluster();
   extern __shared__ uint4 smem16[];
@@ -1077,13 +1080,13 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename T>
 cudaError_t launch(SampleArgs a, cudaStream_t s) {
-  // Two waves of CTAs, four to an SM, if that takes at most eight to a row.
-  // Fewer to a row cost less in barriers between them (288 rows of 151936
-  // fp32 logits, top-k 50: 126 us with eight, 84 us with two), more of them
-  // shorten rows that need several passes (the same rows with mixed filters:
-  // 249 us with two, 219 us with four, 248 us with eight; a lone row of
-  // top-k 50: 28 us with two, 20 us with eight).  Never more than slices of
-  // 4096 tokens need.
+  // Up to eight CTAs for each SM, three of them resident, if that takes at
+  // most eight to a row.  Fewer to a row cost less in barriers between them,
+  // more of them shorten rows that need several passes (288 rows of 151936
+  // fp32 logits with mixed filters: 235 us with two, 193 us with four; a lone
+  // row of top-k 50: 28 us with two, 20 us with eight; against that 128 rows
+  // of 262144 without filters: 68 us with four, 73 us with eight).  Never
+  // more than slices of 4096 tokens need.
   int C = kMaxCluster;
   while (C > 1 && ((long long)a.R * C > 8 * 152 ||
                    (long long)(C / 2) * 4096 >= a.V))
