@@ -52,6 +52,8 @@ constexpr int kOwnBound = 128;         // largest k for a bound of each CTA
 constexpr int kChunks = 4;             // copies of a slice
 constexpr uint64_t kWait = 2000000000ull;  // 2 s
 constexpr int kCandBins = 512;         // bins of 1/16 for their bound
+constexpr int kList = 256;             // members of one bin
+constexpr int kCollects = 3;           // lists that a row may gather
 constexpr int kMaxCluster = 8;
 
 struct SampleArgs {
@@ -97,9 +99,17 @@ struct Shared {
   float kept_least[kWarps];  // and its smallest kept logit
   uint32_t kept_n;
   uint32_t odd;          // a logit of the slice is not finite
-  uint32_t listed;
+  uint32_t lists[kCollects][kMaxCluster];  // lengths of every CTA's lists
+  uint32_t row_listed[kCollects];  // the first CTA's: places taken in all_cand
   uint64_t landed[kChunks];  // barriers of the slice's copies
   // this CTA's own
+  uint32_t listed;
+  uint32_t list_at;      // place of its list among the row's
+  uint32_t n_list;       // members of a bin
+  uint32_t least_key;
+  u64 target;            // what the weight in found_bin reaches
+  float t, top_p, min_p, u;
+  int top_k;
   u64 warp_w[kWarps];
   uint32_t warp_n[kWarps];
   int found_bin;
@@ -112,7 +122,12 @@ struct Shared {
     struct {
       uint32_t count[kBins];              // read by the cluster
       uint32_t w_lo[kBins], w_hi[kBins];  // read by the cluster
-      uint32_t all_count[kBins];
+      union {
+        uint32_t all_count[kBins];
+        struct {
+          u64 list[kList], list_w[kList];
+        };
+      };
       u64 all_w[kBins];
     };
     struct {
@@ -202,18 +217,21 @@ __device__ void reduce_bins(Shared& S, cg::cluster_group& cl, int n) {
   cl.sync();
 }
 
-// The first bin at which the running count reaches `need_n` (by_weight
-// false) or the running weight reaches `need_w`; its predecessors' sums.
-// found_bin = -1 if none does.  Whole CTA.
-__device__ void find_bin(Shared& S, int n, bool by_weight, uint32_t need_n,
-                         u64 need_w) {
+// The first of n bins at which the running count reaches `need_n` (by_weight
+// false) or the running weight reaches need_w(weight of all bins); its
+// predecessors' sums.  found_bin = -1 if none does.  Whole CTA, which has left
+// the last call's results behind.
+template <typename Count, typename Weight, typename Need>
+__device__ __forceinline__ void find_bin(Shared& S, int n, Count count,
+                                         Weight weight, bool by_weight,
+                                         uint32_t need_n, Need need_w) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int per = (n + kThreads - 1) / kThreads;
   uint32_t c = 0;
   u64 w = 0;
   for (int i = 0; i < per; ++i) {
     const int bin = tid * per + i;
-    if (bin < n) { c += S.all_count[bin]; w += S.all_w[bin]; }
+    if (bin < n) { c += count(bin); w += weight(bin); }
   }
   uint32_t pc = c;
   u64 pw = w;
@@ -226,21 +244,36 @@ __device__ void find_bin(Shared& S, int n, bool by_weight, uint32_t need_n,
   if (lane == 31) { S.warp_n[wid] = pc; S.warp_w[wid] = pw; }
   if (tid == 0) S.found_bin = -1;
   __syncthreads();
-  for (int i = 0; i < wid; ++i) { pc += S.warp_n[i]; pw += S.warp_w[i]; }
+  u64 total = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    const u64 v = S.warp_w[i];
+    if (i < wid) { pc += S.warp_n[i]; pw += v; }
+    total += v;
+  }
   pc -= c;
   pw -= w;
+  const u64 need = by_weight ? need_w(total) : 0;
+  if (tid == 0) S.target = need;
   for (int i = 0; i < per; ++i) {
     const int bin = tid * per + i;
     if (bin >= n) break;
-    const uint32_t nc = pc + S.all_count[bin];
-    const u64 nw = pw + S.all_w[bin];
-    const bool here = by_weight ? pw < need_w && nw >= need_w
+    const uint32_t nc = pc + count(bin);
+    const u64 nw = pw + weight(bin);
+    const bool here = by_weight ? pw < need && nw >= need
                                 : pc < need_n && nc >= need_n;
     if (here) { S.found_bin = bin; S.found_n = pc; S.found_w = pw; }
     pc = nc;
     pw = nw;
   }
   __syncthreads();
+}
+// The same of the cluster's bins, as reduce_bins left them.
+__device__ void find_bin(Shared& S, int n, bool by_weight, uint32_t need_n,
+                         u64 need_w) {
+  find_bin(S, n, [&](int i) { return S.all_count[i]; },
+           [&](int i) { return S.all_w[i]; }, by_weight, need_n,
+           [&](u64) { return need_w; });
 }
 
 template <typename T>
@@ -388,28 +421,32 @@ __device__ __forceinline__ u64 top_p_bound(float p, u64 total) {
   return need >= 1.0 ? (u64)need : 1;  // the first token is kept
 }
 
-// Gathers this CTA's S.cand[0, S.listed) of every CTA into S.all_cand of
-// the first; *all: how many, over the cluster.  False (and nothing moved) if
-// that is more than kCand.  Barriers: the lists are complete before, and
-// everything of other CTAs has been read after.
-__device__ bool collect(Shared& S, cg::cluster_group& cl, int* all) {
-  cl.sync();
+// Gathers S.cand[0, S.listed) of every CTA into S.all_cand of the first, in
+// no order; *all: how many, over the cluster.  False, and nothing to use, if
+// that is more than kCand.  `call`: a number not used before.  `free`: the
+// first CTA's all_cand is not in use.  What it wrote is there after it, and
+// nothing of another CTA is read any more.
+__device__ bool collect(Shared& S, cg::cluster_group& cl, int call, bool free,
+                        int* all) {
+  if (free) __syncthreads();
+  else cl.sync();
   const int C = cl.num_blocks(), rank = cl.block_rank();
-  uint32_t at = 0, n = 0;
-  for (int q = 0; q < C; ++q) {
-    const uint32_t c = cl.map_shared_rank(&S, q)->listed;
-    if (q < rank) at += c;
-    n += c;
-  }
-  *all = (int)n;
-  const bool fits = n <= kCand;  // the same in every CTA
-  if (fits) {
+  const int tid = threadIdx.x;
+  const uint32_t mine = S.listed;
+  if (tid == 0)
+    S.list_at = atomicAdd(&cl.map_shared_rank(&S, 0)->row_listed[call], mine);
+  if (tid < C) cl.map_shared_rank(&S, tid)->lists[call][rank] = mine;
+  __syncthreads();
+  const uint32_t at = S.list_at;
+  if (at + mine <= kCand) {
     u64* to = cl.map_shared_rank(S.all_cand, 0);
-    for (uint32_t i = threadIdx.x; i < S.listed; i += kThreads)
-      to[at + i] = S.cand[i];
+    for (uint32_t i = tid; i < mine; i += kThreads) to[at + i] = S.cand[i];
   }
   cl.sync();
-  return fits;
+  uint32_t n = 0;
+  for (int q = 0; q < C; ++q) n += S.lists[call][q];
+  *all = (int)n;
+  return n <= kCand;  // the same in every CTA
 }
 
 // The cut in the found bin of the histogram: its members gathered in the
@@ -418,7 +455,8 @@ __device__ bool collect(Shared& S, cg::cluster_group& cl, int* all) {
 template <typename T>
 __device__ void bin_cut(Shared& S, cg::cluster_group& cl, const T* data,
                         bool wide, int n, int id0, const Row& r, float t,
-                        bool by_weight, uint32_t need_n, u64 need_w) {
+                        int call, bool by_weight, uint32_t need_n,
+                        u64 need_w) {
   const int tid = threadIdx.x;
   const int bin = S.found_bin;
   const uint32_t before_n = S.found_n;
@@ -434,9 +472,8 @@ __device__ void bin_cut(Shared& S, cg::cluster_group& cl, const T* data,
       if (at < kCand) S.cand[at] = word_of(l, id0 + i);
     }
   });
-  __syncthreads();
   int all;
-  if (!collect(S, cl, &all)) {
+  if (!collect(S, cl, call, false, &all)) {
     radix_cut(S, cl, data, n, id0, r, by_weight, need_n, need_w);
     return;
   }
@@ -475,9 +512,10 @@ __device__ void bin_cut(Shared& S, cg::cluster_group& cl, const T* data,
 // The row's n candidates (S.all_cand: its largest tokens, at least k of them)
 // to the kept set's cut and size, and the token.  The first k are kept, of
 // those the ones whose predecessors weigh less than `bound` (0: p of the k
-// tokens' weight).  Whole CTA; scratch: S.cand.
-__device__ void pick(Shared& S, const Row& r, int n, int k, u64 bound, float p,
-                     float mp, float u, int* token) {
+// tokens' weight).  By sorting them: for ties beyond pick()'s lists.  Whole
+// CTA; scratch: S.cand.
+__device__ void pick_sorted(Shared& S, const Row& r, int n, int k, u64 bound,
+                            float p, float mp, float u, int* token) {
   const int tid = threadIdx.x;
   sort_down(S.all_cand, n);
   constexpr int kPer = kCand / kThreads;
@@ -530,6 +568,139 @@ __device__ void pick(Shared& S, const Row& r, int n, int k, u64 bound, float p,
   }
 }
 
+// The same without a sort.  Bins of equal width from the maximum to `low`
+// (which no candidate is below) hold the candidates' numbers and weights: the
+// bin of the k-th token, or of the one whose weight passes the bound, is found
+// by a scan, and its few members by comparing each with each.  The token is
+// found likewise, in bins of ids.  1053 candidates, k = 1000, p = 0.9: sorting
+// them by rank, then those kept by id, took 33 us of a lone row's 41 us.
+__device__ void pick(Shared& S, const Row& r, float t, float low, int V, int n,
+                     int k, u64 bound, float p, float mp, float u,
+                     int* token) {
+  const int tid = threadIdx.x;
+  const u64 given = bound;
+  const float span = low > -INFINITY ? r.top - low : 32.f * t;
+  const float scale = (float)(kBins - 1) / span;
+  int shift = 0;
+  while (V - 1 >> shift >= kBins) ++shift;
+  auto clear = [&] {
+    for (int i = tid; i < kBins; i += kThreads)
+      S.count[i] = S.w_lo[i] = S.w_hi[i] = 0;
+    if (tid == 0) S.n_list = 0;
+    __syncthreads();
+  };
+  auto logit = [&](u64 w) { return of_key((uint32_t)(w >> 32)); };
+  auto bin_at = [&](u64 w) {  // monotone; what is no number counts as 0
+    return min((int)__fmul_rn(__fsub_rn(r.top, logit(w)), scale), kBins - 1);
+  };
+  auto id_bin = [&](u64 w) { return (int)(~(uint32_t)w >> shift); };
+  auto count = [&](int i) { return S.count[i]; };
+  auto weight = [&](int i) { return (u64)S.w_hi[i] << 32 | S.w_lo[i]; };
+  auto list = [&](u64 key, float x) {
+    const uint32_t at = atomicAdd(&S.n_list, 1u);
+    if (at < kList) {
+      S.list[at] = key;
+      S.list_w[at] = weight_of(x);
+    }
+  };
+  // The cut in the found bin; false if it has too many members.
+  auto edge = [&](bool by_weight) {
+    const int bin = S.found_bin;
+    for (int i = tid; i < n; i += kThreads) {
+      const u64 c = S.all_cand[i];
+      if (bin_at(c) == bin) list(c, x_of(logit(c), r));
+    }
+    __syncthreads();
+    const int m = (int)S.n_list;
+    if (m > kList) return false;
+    if (tid < m) {
+      const u64 mine = S.list[tid], w = S.list_w[tid], need = S.target;
+      int rank = (int)S.found_n;
+      u64 before = S.found_w;
+      for (int j = 0; j < m; ++j)
+        if (S.list[j] > mine) {
+          ++rank;
+          before += S.list_w[j];
+        }
+      if (by_weight ? before < need && before + w >= need : rank + 1 == k) {
+        S.cut = mine;
+        S.kept_before = before + w;
+      }
+    }
+    __syncthreads();
+    if (tid == 0) S.n_list = 0;
+    return true;
+  };
+
+  if (tid == 0) {
+    S.kept = 0;
+    S.least_key = ~0u;
+  }
+  clear();
+  for (int i = tid; i < n; i += kThreads) {
+    const u64 c = S.all_cand[i];
+    const int b = bin_at(c);
+    atomicAdd(&S.count[b], 1u);
+    add_weight(S, b, weight_of(x_of(logit(c), r)));
+  }
+  __syncthreads();
+  bool found = false, ok = true;
+  if (bound) {
+    find_bin(S, kBins, count, weight, true, 0, [&](u64) { return bound; });
+    found = S.found_bin >= 0;
+    if (found) ok = edge(true);
+    else __syncthreads();  // all of them are lighter: all are kept
+  }
+  if (!found) {
+    find_bin(S, kBins, count, weight, false, (uint32_t)k,
+             [](u64) { return 0ull; });
+    ok = edge(false);
+    if (ok && bound == 0 && p < 1.f) {
+      bound = top_p_bound(p, S.kept_before);
+      find_bin(S, kBins, count, weight, true, 0, [&](u64) { return bound; });
+      ok = edge(true);
+    }
+  }
+  if (ok) {
+    const u64 cut = S.cut;
+    auto keeps = [&](u64 c, float x) { return c >= cut && x >= mp; };
+    clear();
+    for (int i = tid; i < n; i += kThreads) {
+      const u64 c = S.all_cand[i];
+      const float x = x_of(logit(c), r);
+      if (!keeps(c, x)) continue;
+      add_weight(S, id_bin(c), weight_of(x));
+      atomicAdd(&S.kept, 1);
+      if (mp > 0.f) atomicMin(&S.least_key, (uint32_t)(c >> 32));
+    }
+    __syncthreads();
+    find_bin(S, kBins, count, weight, true, 0,
+             [&](u64 total) { return draw_target(u, total) + 1; });
+    const int bin = S.found_bin;
+    for (int i = tid; i < n; i += kThreads) {
+      const u64 c = S.all_cand[i];
+      if (id_bin(c) != bin) continue;
+      const float x = x_of(logit(c), r);
+      if (keeps(c, x)) list(~(uint32_t)c, x);
+    }
+    // what is kept, as one cut: all of the smallest logit if min-p decided
+    if (tid == 0 && mp > 0.f)
+      S.cut = max(cut, (u64)S.least_key << 32 | 0x80000000u);
+    __syncthreads();
+    const int m = (int)S.n_list;
+    ok = m <= kList;
+    if (ok && tid < m) {
+      const u64 mine = S.list[tid], target = S.target - 1;
+      u64 before = S.found_w;
+      for (int j = 0; j < m; ++j)
+        if (S.list[j] < mine) before += S.list_w[j];
+      if (target >= before && target < before + S.list_w[tid])
+        *token = (int)mine;
+    }
+  }
+  if (!ok) pick_sorted(S, r, n, k, given, p, mp, u, token);
+}
+
 // Three CTAs to an SM (40 registers) hide each other's barriers: 288 rows with
 // mixed filters 217 us with two (64 registers), 193 us with three, 191 us with
 // four, where 128 rows without filters go from 73 us to 78 us.
@@ -557,7 +728,13 @@ __global__ void __launch_bounds__(kThreads, 3)
     S.odd = 0;
     S.kept_n = 0;
     S.listed = 0;
+    for (int i = 0; i < kCollects; ++i) S.row_listed[i] = 0;
     S.first = 0x7fffffff;
+    S.t = a.temperature[row];
+    S.top_k = a.top_k ? a.top_k[row] : 0;
+    S.top_p = a.top_p ? a.top_p[row] : 1.f;
+    S.min_p = a.min_p ? a.min_p[row] : 0.f;
+    S.u = a.u[row];
     for (int i = 0; i < kChunks; ++i) tc::mbar_init(&S.landed[i], 1);
     tc::fence_mbar_init();
   }
@@ -667,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   top = warp_max(top);
 
   Row r;
-  const float t = a.temperature[row];
+  const float t = S.t;
   r.top = top;
   r.greedy = !(t > 0.f && t < INFINITY);
   r.inv_t = r.greedy ? 0.f : __fdiv_rn(1.f, t);
@@ -680,12 +857,11 @@ __global__ void __launch_bounds__(kThreads, 3)
          [&](int, float l) { bad |= !(l < INFINITY); });
     if (bad) raise_error(a.err, kErrNonfinite);
   }
-  const int k = a.top_k ? a.top_k[row] : 0;
-  const float p = a.top_p ? a.top_p[row] : 1.f;
+  const int k = S.top_k;
+  const float p = S.top_p;
   // at most 1 (which keeps the maximum), 0 for what is no number
-  const float mp = a.min_p && a.min_p[row] > 0.f ? fminf(a.min_p[row], 1.f)
-                                                 : 0.f;
-  const float u = a.u[row];
+  const float mp = S.min_p > 0.f ? fminf(S.min_p, 1.f) : 0.f;
+  const float u = S.u;
   const bool by_k = !r.greedy && !empty && k > 0 && k < a.V;
   const bool by_p = !r.greedy && !empty && p < 1.f;
   float* dst = a.filtered ? a.filtered + (size_t)row * a.V + id0 : nullptr;
@@ -749,20 +925,20 @@ __global__ void __launch_bounds__(kThreads, 3)
     return;
   }
 
-  // The tokens from `low` up as candidates, sorted and drawn from by the first
+  // The tokens from `low` up as candidates, cut and drawn from by the first
   // CTA; false if they are too many.
-  auto finish = [&](float low, int most, u64 bound) {
+  auto finish = [&](float low, bool free, int most, u64 bound) {
     each(data, wide, 0, n, tid, kThreads, [&](int i, float l) {
       if (l >= low && l > -INFINITY) {
         const uint32_t at = atomicAdd(&S.listed, 1u);
         if (at < kCand) S.cand[at] = word_of(l, id0 + i);
       }
     });
-    __syncthreads();
     int all;
-    if (!collect(S, cl, &all)) return false;
+    if (!collect(S, cl, 0, free, &all)) return false;
     if (rank == 0) {
-      pick(S, r, all, min(most, all), bound, p, mp, u, a.token + row);
+      pick(S, r, t, low, a.V, all, min(most, all), bound, p, mp, u,
+           a.token + row);
       if (tid == 0 && a.n_kept) a.n_kept[row] = S.kept;
       __syncthreads();
       if (dst && tid < C) cl.map_shared_rank(&S, tid)->cut = S.cut;
@@ -781,10 +957,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     const bool own_bound = k <= kOwnBound;
     Row b = r;
     if (own_bound) b.top = S.top;
-    for (int i = tid; i < kCandBins; i += kThreads) {
-      S.count[i] = 0;
-      S.all_w[i] = 0;
-    }
+    for (int i = tid; i < kCandBins; i += kThreads) S.count[i] = 0;
     __syncthreads();
 #pragma unroll
     for (int c = 0; c < kChunks; ++c)
@@ -792,8 +965,6 @@ __global__ void __launch_bounds__(kThreads, 3)
         atomicAdd(&S.count[bin_of(tops[c], b) / (kBins / kCandBins)], 1u);
     if (own_bound) {
       __syncthreads();
-      for (int i = tid; i < kCandBins; i += kThreads)
-        S.all_count[i] = S.count[i];
     } else {
       cl.sync();
       for (int i = tid; i < kCandBins; i += kThreads) {
@@ -801,9 +972,12 @@ __global__ void __launch_bounds__(kThreads, 3)
         for (int q = 0; q < C; ++q) c += cl.map_shared_rank(&S, q)->count[i];
         S.all_count[i] = c;
       }
+      __syncthreads();
     }
-    __syncthreads();
-    find_bin(S, kCandBins, false, (uint32_t)k, 0);
+    const uint32_t* of = own_bound ? S.count : S.all_count;
+    find_bin(S, kCandBins, [&](int i) { return of[i]; },
+             [](int) { return 0ull; }, false, (uint32_t)k,
+             [](u64) { return 0ull; });
     const int bin = S.found_bin;
     // the counts have been read; the lists take their place
     if (own_bound) __syncthreads();
@@ -812,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         bin < 0 ? -INFINITY
                 : bin_floor((bin + 1) * (kBins / kCandBins) - 1, b, t);
     // top-k of fewer tokens than k keeps them all
-    if (finish(low, k, 0)) return;
+    if (finish(low, true, k, 0)) return;
   }
 
   // ---- the cut by histogram of weights --------------------------------------
@@ -891,7 +1065,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       find_bin(S, kBins, false, (uint32_t)k, 0);
       if (S.found_bin >= 0) {  // fewer than k tokens above -inf: no cut
         redo = true;
-        bin_cut(S, cl, data, wide, n, id0, r, t, false, (uint32_t)k, 0);
+        bin_cut(S, cl, data, wide, n, id0, r, t, 1, false, (uint32_t)k, 0);
         cut = S.cut;
         total = S.kept_before;
         __syncthreads();
@@ -915,7 +1089,7 @@ __global__ void __launch_bounds__(kThreads, 3)
           S.found_n + S.all_count[bin] <= kCand / 2) {
         if (tid == 0) S.listed = 0;
         __syncthreads();
-        if (finish(bin_floor(bin, r, t), kCand, bound)) return;
+        if (finish(bin_floor(bin, r, t), false, kCand, bound)) return;
         // (not so few: the bins have been overwritten)
         for (int i = tid; i < kBins; i += kThreads)
           S.count[i] = S.w_lo[i] = S.w_hi[i] = 0;
@@ -924,7 +1098,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         reduce_bins(S, cl, kBins);
         find_bin(S, kBins, true, 0, bound);
       }
-      bin_cut(S, cl, data, wide, n, id0, r, t, true, 0, bound);
+      bin_cut(S, cl, data, wide, n, id0, r, t, 2, true, 0, bound);
       cut = max(cut, S.cut);
     }
   }
