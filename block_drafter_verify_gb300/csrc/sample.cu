@@ -8,24 +8,37 @@
 // floor(exp(.) 2^44): their sums are exact, so the cut, the totals and the
 // drawn token do not depend on how the row is split over threads and CTAs.
 //
-// A cluster of CTAs owns a row: each CTA reads its slice from HBM once and
-// keeps it in shared memory (by bulk copies: more bytes in flight than its
-// threads could have), where all later passes run; only maxima, histograms,
-// short lists and sums travel between the CTAs (distributed shared memory).
+// A cluster of CTAs owns a row: each CTA reads its slice from HBM once, and
+// later passes from L2, or from shared memory where few CTAs leave room for
+// the slice (by bulk copies: more bytes in flight than its threads could
+// have); only maxima, histograms, short lists and sums travel between the CTAs
+// (distributed shared memory).
 // What happens then is the row's own:
 //   T = 0           the first maximum;
 //   top-k           the k-th largest of the threads' own maxima bounds the
-//                   k-th largest token from below, so one comparison per
-//                   token gathers few more than k candidates (with small k
-//                   each CTA takes its own bound, which spares two cluster
-//                   barriers); one CTA sorts them, applies top-p and min-p,
-//                   and draws among them;
-//   top-p only      a histogram of weights over bins of (max - l) / T finds
-//                   the bin in which the weight passes p W, whose members are
-//                   gathered and sorted; kept weights by warp chunk, the draw;
+//                   k-th largest token from below, and only the threads'
+//                   parts whose maximum reaches it are read again for the few
+//                   more than k candidates (with small k each CTA takes its
+//                   own bound, which spares two cluster barriers); one CTA
+//                   finds the cut in them, with top-p and min-p, and draws
+//                   among them;
+//   min-p only      likewise from its bound, if the tokens are few;
+//   top-p only      the weights' sum, and the tokens' numbers in bins of
+//                   (max - l) / T, from which any prefix's weight is known to
+//                   a part in 64: a short prefix is gathered and cut as above;
+//                   of a long one the weight before a range of bins around the
+//                   cut is summed and the range's members gathered and cut;
 //   neither         kept weights by warp chunk, the draw.
 // What overflows a list (ties by the thousand, a tail of weightless tokens)
-// is resolved by radix selection on the 64-bit words instead.
+// is resolved by a histogram of the 64-bit words instead, refined until the
+// rest fits one.
+//
+// What bounds it.  288 rows of 151936 fp32 logits, 26 us of HBM: T = 0 44 us,
+// top-k 50 61 us, no filter 74 us, top-k 1000 with top-p 88 us, top-p 0.9 of
+// 17000 tokens 196 us: instruction issue (about 20 for each token's maximum
+// and weight, 20 more for a bin, of the tokens that may be kept) and the
+// barriers of each row's chain, which other rows' CTAs hide in part.  A lone
+// row: 10 us, 13 us, 12 us, 20 us and 32 us, the chain alone.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -45,15 +58,18 @@ using u64 = unsigned long long;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 1024;
-constexpr float kBinsPerUnit = 32.f;   // bins of 1/32 in (max - l) / T
+constexpr int kBins = 2048;
+constexpr float kBinsPerUnit = 64.f;   // bins of 1/64 in (max - l) / T
+constexpr int kTopBins = 192;          // bins whose weight is summed
+constexpr int kSlots = 1024;           // bins of candidates
 constexpr int kCand = 2048;            // candidates, over the cluster
+constexpr int kOwn = 1536;             // of one CTA
 constexpr int kOwnBound = 128;         // largest k for a bound of each CTA
 constexpr int kChunks = 4;             // copies of a slice
 constexpr uint64_t kWait = 2000000000ull;  // 2 s
-constexpr int kCandBins = 512;         // bins of 1/16 for their bound
+constexpr int kCandBins = 512;         // bins of 1/16 for a bound of them
 constexpr int kList = 256;             // members of one bin
-constexpr int kCollects = 3;           // lists that a row may gather
+constexpr int kCollects = 5;           // lists that a row may gather
 constexpr int kMaxCluster = 8;
 
 struct SampleArgs {
@@ -95,15 +111,17 @@ struct Shared {
   float top;             // largest logit of the slice
   int first;             // T = 0: first token of the slice that has it
   u64 total;             // weight of the slice
+  u64 top_w;             // and of its tokens in the first kTopBins bins
   u64 kept_w[kWarps];    // kept weight of each warp's chunk
   float kept_least[kWarps];  // and its smallest kept logit
   uint32_t kept_n;
   uint32_t odd;          // a logit of the slice is not finite
+  uint32_t fine;         // one has more bits than bf16
   uint32_t lists[kCollects][kMaxCluster];  // lengths of every CTA's lists
   uint32_t row_listed[kCollects];  // the first CTA's: places taken in all_cand
   uint64_t landed[kChunks];  // barriers of the slice's copies
   // this CTA's own
-  uint32_t listed;
+  uint32_t listed, n_quarters;
   uint32_t list_at;      // place of its list among the row's
   uint32_t n_list;       // members of a bin
   uint32_t least_key;
@@ -120,18 +138,25 @@ struct Shared {
   int kept;
   union {
     struct {
-      uint32_t count[kBins];              // read by the cluster
-      uint32_t w_lo[kBins], w_hi[kBins];  // read by the cluster
       union {
-        uint32_t all_count[kBins];
+        uint32_t count[kBins];  // read by the cluster
         struct {
+          uint32_t slots[kSlots];
           u64 list[kList], list_w[kList];
         };
       };
-      u64 all_w[kBins];
+      union {
+        struct {
+          uint32_t w_lo[kSlots], w_hi[kSlots];  // read by the cluster
+        };
+        uint32_t all_count[kBins];
+      };
+      uint32_t all_n[kSlots];
+      u64 all_w[kSlots];
     };
     struct {
-      u64 cand[kCand];      // this CTA's candidates
+      u64 cand[kOwn];       // this CTA's candidates
+      uint16_t quarters[kChunks * kThreads];  // that may have some
       u64 all_cand[kCand];  // the row's, in the first CTA
     };
   };
@@ -196,45 +221,42 @@ __device__ __forceinline__ void add_weight(Shared& S, int bin, u64 w) {
   if (up) atomicAdd(&S.w_hi[bin], up);
 }
 
-// Sums the cluster's histograms (first n bins) into all_count, all_w of
-// every CTA.  Cluster barriers on both sides: the histograms are complete
-// before, and may be cleared after.
-__device__ void reduce_bins(Shared& S, cg::cluster_group& cl, int n) {
+// Sums the cluster's counts (first n bins) into all_count of every CTA.
+// Cluster barriers on both sides: the counts are complete before, and may be
+// overwritten after.
+__device__ void reduce_counts(Shared& S, cg::cluster_group& cl, int n) {
   cl.sync();
   const int C = cl.num_blocks();
   for (int i = threadIdx.x; i < n; i += kThreads) {
     uint32_t c = 0;
-    u64 w = 0;
-    for (int r = 0; r < C; ++r) {
-      const Shared* o = cl.map_shared_rank(&S, r);
-      c += o->count[i];
-      w += (u64)o->w_hi[i] << 32 | 0u;
-      w += o->w_lo[i];
-    }
+    for (int q = 0; q < C; ++q) c += cl.map_shared_rank(&S, q)->count[i];
     S.all_count[i] = c;
-    S.all_w[i] = w;
   }
   cl.sync();
 }
 
-// The first of n bins at which the running count reaches `need_n` (by_weight
-// false) or the running weight reaches need_w(weight of all bins); its
-// predecessors' sums.  found_bin = -1 if none does.  Whole CTA, which has left
-// the last call's results behind.
-template <typename Count, typename Weight, typename Need>
+// The first of n bins (N at most) at which the running count reaches `need_n`
+// (by_weight false) or the running weight reaches need_w(weight of all bins);
+// its predecessors' sums.  found_bin = -1 if none does.  Whole CTA, which has
+// left the last call's results behind.
+template <int N, typename Count, typename Weight, typename Need>
 __device__ __forceinline__ void find_bin(Shared& S, int n, Count count,
                                          Weight weight, bool by_weight,
                                          uint32_t need_n, Need need_w) {
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int per = (n + kThreads - 1) / kThreads;
-  uint32_t c = 0;
-  u64 w = 0;
-  for (int i = 0; i < per; ++i) {
-    const int bin = tid * per + i;
-    if (bin < n) { c += count(bin); w += weight(bin); }
+  constexpr int kPer = (N + kThreads - 1) / kThreads;
+  uint32_t c[kPer], pc = 0;
+  u64 w[kPer], pw = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int bin = tid * kPer + i;
+    c[i] = bin < n ? count(bin) : 0;
+    w[i] = bin < n ? weight(bin) : 0;
+    pc += c[i];
+    pw += w[i];
   }
-  uint32_t pc = c;
-  u64 pw = w;
+  const uint32_t own_c = pc;
+  const u64 own_w = pw;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t oc = __shfl_up_sync(0xffffffffu, pc, o);
@@ -251,29 +273,23 @@ __device__ __forceinline__ void find_bin(Shared& S, int n, Count count,
     if (i < wid) { pc += S.warp_n[i]; pw += v; }
     total += v;
   }
-  pc -= c;
-  pw -= w;
+  pc -= own_c;
+  pw -= own_w;
   const u64 need = by_weight ? need_w(total) : 0;
   if (tid == 0) S.target = need;
-  for (int i = 0; i < per; ++i) {
-    const int bin = tid * per + i;
-    if (bin >= n) break;
-    const uint32_t nc = pc + count(bin);
-    const u64 nw = pw + weight(bin);
-    const bool here = by_weight ? pw < need && nw >= need
-                                : pc < need_n && nc >= need_n;
-    if (here) { S.found_bin = bin; S.found_n = pc; S.found_w = pw; }
-    pc = nc;
-    pw = nw;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const bool here = by_weight ? pw < need && pw + w[i] >= need
+                                : pc < need_n && pc + c[i] >= need_n;
+    if (here) {
+      S.found_bin = tid * kPer + i;
+      S.found_n = pc;
+      S.found_w = pw;
+    }
+    pc += c[i];
+    pw += w[i];
   }
   __syncthreads();
-}
-// The same of the cluster's bins, as reduce_bins left them.
-__device__ void find_bin(Shared& S, int n, bool by_weight, uint32_t need_n,
-                         u64 need_w) {
-  find_bin(S, n, [&](int i) { return S.all_count[i]; },
-           [&](int i) { return S.all_w[i]; }, by_weight, need_n,
-           [&](u64) { return need_w; });
 }
 
 template <typename T>
@@ -286,46 +302,6 @@ __device__ __forceinline__ void warp_chunk(int n, int wid, int* a, int* b) {
   const int per = ((n + kWarps - 1) / kWarps + 127) & ~127;
   *a = min(n, wid * per);
   *b = min(n, *a + per);
-}
-
-// Generic selection of the cut by radix on the 64-bit words, most
-// significant byte first: the word at which the count reaches need_n (or
-// the preceding weight has not yet reached need_w) over the whole cluster.
-template <typename T>
-__device__ void radix_cut(Shared& S, cg::cluster_group& cl, const T* data,
-                          int n, int id0, const Row& r, bool by_weight,
-                          uint32_t need_n, u64 need_w) {
-  u64 prefix = 0, mask = 0, before_w = 0;
-  uint32_t before_n = 0;
-  for (int shift = 56; shift >= 0; shift -= 8) {
-    for (int i = threadIdx.x; i < 256; i += kThreads)
-      S.count[i] = S.w_lo[i] = S.w_hi[i] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      const float l = logit_at(data, i);
-      if (!(l > -INFINITY)) continue;
-      const u64 w = word_of(l, id0 + i);
-      if ((w & mask) != prefix) continue;
-      const int bin = 255 - (int)(w >> shift & 255);  // larger words first
-      atomicAdd(&S.count[bin], 1u);
-      add_weight(S, bin, weight_of(x_of(l, r)));
-    }
-    reduce_bins(S, cl, 256);
-    find_bin(S, 256, by_weight, by_weight ? 0 : need_n - before_n,
-             by_weight ? need_w - before_w : 0);
-    const int bin = S.found_bin;
-    before_n += S.found_n;
-    before_w += S.found_w;
-    prefix |= (u64)(255 - bin) << shift;
-    mask |= (u64)255 << shift;
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) {
-    const float l = of_key((uint32_t)(prefix >> 32));
-    S.cut = prefix;
-    S.kept_before = before_w + weight_of(x_of(l, r));
-  }
-  __syncthreads();
 }
 
 // Elements of a 16-byte word.
@@ -364,32 +340,6 @@ __device__ __forceinline__ void each(const T* data, bool wide, int from,
   for (int i = done + t; i < to; i += threads) f(i, to_f32(data[i]));
 }
 
-// Sorts key[0, n) descending; n at most kCand, entries up to the next power
-// of two are overwritten with 0.  Whole CTA.
-__device__ void sort_down(u64* key, int n) {
-  int P = 2;
-  while (P < n) P *= 2;
-  for (int i = n + threadIdx.x; i < P; i += kThreads) key[i] = 0;
-  __syncthreads();
-  for (int k = 2; k <= P; k *= 2) {
-    for (int j = k / 2; j > 0; j /= 2) {
-      for (int i = threadIdx.x; i < P / 2; i += kThreads) {
-        const int a = 2 * i - (i & (j - 1)), b = a + j;
-        const u64 x = key[a], y = key[b];
-        const bool down = (a & k) == 0;
-        if ((x < y) == down) {
-          key[a] = y;
-          key[b] = x;
-        }
-      }
-      // steps within 64 entries stay within a warp's own entries
-      if (j > 32 || P / 2 > kThreads) __syncthreads();
-      else __syncwarp();
-    }
-    __syncthreads();
-  }
-}
-
 // Exclusive sum over the CTA of v (thread order); *all: the total.
 __device__ u64 cta_scan(Shared& S, u64 v, u64* all) {
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
@@ -423,16 +373,14 @@ __device__ __forceinline__ u64 top_p_bound(float p, u64 total) {
 
 // Gathers S.cand[0, S.listed) of every CTA into S.all_cand of the first, in
 // no order; *all: how many, over the cluster.  False, and nothing to use, if
-// that is more than kCand.  `call`: a number not used before.  `free`: the
-// first CTA's all_cand is not in use.  What it wrote is there after it, and
-// nothing of another CTA is read any more.
-__device__ bool collect(Shared& S, cg::cluster_group& cl, int call, bool free,
-                        int* all) {
-  if (free) __syncthreads();
-  else cl.sync();
+// that is more than kCand, or more than kOwn of one.  `call`: a number not used before; a cluster
+// barrier lies between the last use of all_cand and this.  What it wrote is
+// there after it, and nothing of another CTA is read any more.
+__device__ bool collect(Shared& S, cg::cluster_group& cl, int call, int* all) {
+  __syncthreads();
   const int C = cl.num_blocks(), rank = cl.block_rank();
   const int tid = threadIdx.x;
-  const uint32_t mine = S.listed;
+  const uint32_t mine = S.listed <= kOwn ? S.listed : kCand + 1;
   if (tid == 0)
     S.list_at = atomicAdd(&cl.map_shared_rank(&S, 0)->row_listed[call], mine);
   if (tid < C) cl.map_shared_rank(&S, tid)->lists[call][rank] = mine;
@@ -449,263 +397,260 @@ __device__ bool collect(Shared& S, cg::cluster_group& cl, int call, bool free,
   return n <= kCand;  // the same in every CTA
 }
 
-// The cut in the found bin of the histogram: its members gathered in the
-// first CTA and sorted, or radix selection if there are too many.  The
-// histogram is lost.
-template <typename T>
-__device__ void bin_cut(Shared& S, cg::cluster_group& cl, const T* data,
-                        bool wide, int n, int id0, const Row& r, float t,
-                        int call, bool by_weight, uint32_t need_n,
-                        u64 need_w) {
-  const int tid = threadIdx.x;
-  const int bin = S.found_bin;
-  const uint32_t before_n = S.found_n;
-  const u64 before_w = S.found_w;
-  if (tid == 0) S.listed = 0;
+__device__ __forceinline__ float x_of_word(u64 w, const Row& r) {
+  return x_of(of_key((uint32_t)(w >> 32)), r);
+}
+
+// A range of words, in slots of equal width from the largest down.
+struct Slots {
+  u64 hi, lo;
+  int shift;
+  __device__ __forceinline__ Slots(u64 hi_, u64 lo_)
+      : hi(hi_), lo(lo_) {
+    // kSlots is 2^10; the float's exponent may be one more than the integer's
+    const int e = (int)(__float_as_uint(__ull2float_rn(hi - lo)) >> 23) - 127;
+    shift = max(0, e - 9);
+  }
+  __device__ __forceinline__ bool has(u64 w) const { return w >= lo && w <= hi; }
+  __device__ __forceinline__ int of(u64 w) const {
+    return (int)((hi - w) >> shift);
+  }
+  __device__ __forceinline__ Slots within(int slot) const {
+    const u64 top = hi - ((u64)slot << shift);
+    const u64 width = (1ull << shift) - 1;
+    return Slots(top, top - lo > width ? top - width : lo);
+  }
+};
+__device__ __forceinline__ void clear_slots(Shared& S) {
+  for (int i = threadIdx.x; i < kSlots; i += kThreads)
+    S.slots[i] = S.w_lo[i] = S.w_hi[i] = 0;
+  if (threadIdx.x == 0) S.n_list = 0;
   __syncthreads();
-  // one comparison on each side decides for most tokens
-  const float below = bin_floor(bin, r, t);
-  const float above = bin_ceil(bin, r, t);
-  each(data, wide, 0, n, tid, kThreads, [&](int i, float l) {
-    if (l >= below && l <= above && l > -INFINITY && bin_of(l, r) == bin) {
-      const uint32_t at = atomicAdd(&S.listed, 1u);
-      if (at < kCand) S.cand[at] = word_of(l, id0 + i);
+}
+
+// The cut among the n candidates (S.all_cand): of those with a key other than
+// 0, in [lo, hi], by falling key the k-th, or the one whose weight makes the
+// sum reach need_w(weight of all); S.cut is its key, S.kept_before the weight
+// down to it.  Slots hold the candidates' numbers and weights; a scan finds
+// the cut's slot, and comparing each with each finds it among the slot's few
+// members (ties by the hundred make a range of their own, in finer slots).
+// Returns 0 if the weight is not reached, 1 if the slots are those of [lo, hi]
+// still (which `filled` tells the next call), else 2.  Whole CTA.
+template <typename Key, typename Need>
+__device__ int cut_in(Shared& S, const Row& r, int n, u64 hi, u64 lo,
+                      bool filled, bool by_weight, uint32_t k, Key key,
+                      Need need_w) {
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  Slots at(hi, lo);
+  uint32_t n0 = 0;       // before the range
+  u64 w0 = 0, need = 0;
+  for (bool first = true;; first = false) {
+    if (first && filled) {
+      if (tid == 0) S.n_list = 0;
+    } else {
+      clear_slots(S);
+      for (int i = tid; i < n; i += kThreads) {
+        const u64 c = S.all_cand[i], w = key(c);
+        if (w == 0 || !at.has(w)) continue;
+        const int b = at.of(w);
+        atomicAdd(&S.slots[b], 1u);
+        add_weight(S, b, weight_of(x_of_word(c, r)));
+      }
+      __syncthreads();
     }
+    find_bin<kSlots>(
+        S, kSlots, [&](int i) { return S.slots[i]; },
+        [&](int i) { return ((u64)S.w_hi[i] << 32) + S.w_lo[i]; }, by_weight,
+        k - n0, [&](u64 all) { return first ? need_w(all) : need - w0; });
+    const int slot = S.found_bin;
+    if (first) need = S.target;
+    if (slot < 0) {
+      __syncthreads();
+      return 0;
+    }
+    n0 += S.found_n;
+    w0 += S.found_w;
+    at = at.within(slot);
+    u64 most = 0, least = ~0ull;
+    for (int i = tid; i < n; i += kThreads) {
+      const u64 c = S.all_cand[i], w = key(c);
+      if (w == 0 || !at.has(w)) continue;
+      const uint32_t to = atomicAdd(&S.n_list, 1u);
+      if (to < kList) {
+        S.list[to] = w;
+        S.list_w[to] = weight_of(x_of_word(c, r));
+      }
+      most = max(most, w);
+      least = min(least, w);
+    }
+    __syncthreads();
+    const int m = (int)S.n_list;
+    if (m <= kList) {
+      if (tid < m) {
+        const u64 mine = S.list[tid], w = S.list_w[tid];
+        uint32_t rank = n0;
+        u64 before = w0;
+        for (int j = 0; j < m; ++j)
+          if (S.list[j] > mine) {
+            ++rank;
+            before += S.list_w[j];
+          }
+        if (by_weight ? before < need && before + w >= need : rank + 1 == k) {
+          S.cut = mine;
+          S.kept_before = before + w;
+        }
+      }
+      __syncthreads();
+      return first ? 1 : 2;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+      least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+    }
+    if (lane == 0) {
+      S.list[wid] = most;
+      S.list[kWarps + wid] = least;
+    }
+    __syncthreads();
+    for (int i = 0; i < kWarps; ++i) {
+      most = max(most, S.list[i]);
+      least = min(least, S.list[kWarps + i]);
+    }
+    at = Slots(most, least);
+  }
+}
+
+// The row's n candidates (its largest tokens, none below `low`, at least k of
+// them) to the kept set's cut and size, and the token.  The first k are kept,
+// of those the ones whose predecessors weigh less than `bound` (0: p of the k
+// tokens' weight).  Whole CTA.  A lone row of 151936 logits: k = 1000, p = 0.9
+// (1053 candidates) 18 us, k = 50 13 us; with two sorts of the candidates (by
+// rank, then by id) 41 us and 21 us.
+__device__ void pick(Shared& S, const Row& r, float low, int V, int n, int k,
+                     u64 bound, float p, float mp, float u, int* token) {
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    S.kept = 0;
+    S.least_key = ~0u;
+  }
+  const u64 hi = (u64)key_of(r.top) << 32 | 0xffffffffu;
+  const u64 lo = (u64)key_of(low) << 32;
+  auto whole = [](u64 c) { return c; };
+  const bool found =
+      bound && cut_in(S, r, n, hi, lo, false, true, 0, whole,
+                      [&](u64) { return bound; });
+  if (!found) {  // all are lighter, if there is a bound
+    const int filled = cut_in(S, r, n, hi, lo, bound != 0, false, (uint32_t)k,
+                              whole, [](u64) { return 0ull; });
+    if (bound == 0 && p < 1.f) {
+      const u64 need = top_p_bound(p, S.kept_before);
+      cut_in(S, r, n, hi, lo, filled == 1, true, 0, whole,
+             [&](u64) { return need; });
+    }
+  }
+  const u64 cut = S.cut;
+  auto keeps = [&](u64 c) {
+    return c >= cut && (mp == 0.f || x_of_word(c, r) >= mp);
+  };
+  for (int i = tid; i < n; i += kThreads) {
+    const u64 c = S.all_cand[i];
+    if (!keeps(c)) continue;
+    atomicAdd(&S.kept, 1);
+    if (mp > 0.f) atomicMin(&S.least_key, (uint32_t)(c >> 32));
+  }
+  // the kept tokens by id: the word's lower half is the id's complement
+  cut_in(S, r, n, 0xffffffffu, (uint32_t)~(uint32_t)(V - 1), false, true, 0,
+         [&](u64 c) { return keeps(c) ? (u64)(uint32_t)c : 0ull; },
+         [&](u64 all) { return draw_target(u, all) + 1; });
+  if (tid == 0) {
+    *token = (int)~(uint32_t)S.cut;
+    // what is kept, as one cut: all of the smallest logit if min-p decided
+    S.cut = mp > 0.f ? max(cut, (u64)S.least_key << 32 | 0x80000000u) : cut;
+  }
+}
+
+// The row's cut where nothing narrows it: slots over the words of all tokens,
+// then over the cut's slot, until its members fit a list.
+template <typename T>
+__device__ void refine_cut(Shared& S, cg::cluster_group& cl, const T* data,
+                           bool wide, int n, int id0, const Row& r, int call,
+                           bool by_weight, uint32_t need_n, u64 need_w) {
+  const int tid = threadIdx.x;
+  Slots at(~0ull, 0);
+  uint32_t n0 = 0;  // before the range
+  u64 w0 = 0;
+  for (;;) {
+    clear_slots(S);
+    each(data, wide, 0, n, tid, kThreads, [&](int i, float l) {
+      const u64 w = word_of(l, id0 + i);
+      if (!(l > -INFINITY) || !at.has(w)) return;
+      const int b = at.of(w);
+      atomicAdd(&S.slots[b], 1u);
+      add_weight(S, b, weight_of(x_of(l, r)));
+    });
+    cl.sync();
+    for (int i = tid; i < kSlots; i += kThreads) {
+      uint32_t c = 0;
+      u64 w = 0;
+      for (int q = 0; q < cl.num_blocks(); ++q) {
+        const Shared* o = cl.map_shared_rank(&S, q);
+        c += o->slots[i];
+        w += ((u64)o->w_hi[i] << 32) + o->w_lo[i];
+      }
+      S.all_n[i] = c;
+      S.all_w[i] = w;
+    }
+    cl.sync();
+    find_bin<kSlots>(S, kSlots, [&](int i) { return S.all_n[i]; },
+                     [&](int i) { return S.all_w[i]; }, by_weight,
+                     need_n - n0, [&](u64) { return need_w - w0; });
+    const int slot = S.found_bin;
+    if (slot < 0) {  // no cut (the caller has counted: this does not happen)
+      __syncthreads();
+      if (tid == 0) {
+        S.cut = 0;
+        S.kept_before = w0;
+      }
+      __syncthreads();
+      return;
+    }
+    n0 += S.found_n;
+    w0 += S.found_w;
+    at = at.within(slot);
+    if (S.all_n[slot] <= kOwn) break;
+    __syncthreads();
+  }
+  if (tid == 0) S.listed = 0;
+  cl.sync();  // the first CTA's sums are where the list will be
+  each(data, wide, 0, n, tid, kThreads, [&](int i, float l) {
+    const u64 w = word_of(l, id0 + i);
+    if (!(l > -INFINITY) || !at.has(w)) return;
+    const uint32_t to = atomicAdd(&S.listed, 1u);
+    if (to < kOwn) S.cand[to] = w;
   });
   int all;
-  if (!collect(S, cl, call, false, &all)) {
-    radix_cut(S, cl, data, n, id0, r, by_weight, need_n, need_w);
-    return;
-  }
+  collect(S, cl, call, &all);
   if (cl.block_rank() == 0) {
-    sort_down(S.all_cand, all);
-    constexpr int kPer = kCand / kThreads;
-    u64 w[kPer], mine = 0, total;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int i = tid * kPer + j;
-      w[j] = i < all ? weight_of(x_of(of_key((uint32_t)(S.all_cand[i] >> 32)),
-                                      r))
-                     : 0;
-      mine += w[j];
-    }
-    u64 before = before_w + cta_scan(S, mine, &total);
-    const int C = cl.num_blocks();
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int i = tid * kPer + j;
-      const bool last =
-          i < all && (by_weight ? before < need_w && before + w[j] >= need_w
-                                : before_n + i + 1 == need_n);
-      if (last)
-        for (int q = 0; q < C; ++q) {
-          Shared* o = cl.map_shared_rank(&S, q);
-          o->cut = S.all_cand[i];
-          o->kept_before = before + w[j];
-        }
-      before += w[j];
+    cut_in(S, r, min(all, kCand), at.hi, at.lo, false, by_weight, need_n - n0,
+           [](u64 c) { return c; }, [&](u64) { return need_w - w0; });
+    const u64 cut = S.cut, before = w0 + S.kept_before;
+    __syncthreads();
+    if (tid < cl.num_blocks()) {
+      Shared* o = cl.map_shared_rank(&S, tid);
+      o->cut = cut;
+      o->kept_before = before;
     }
   }
   cl.sync();
 }
 
-// The row's n candidates (S.all_cand: its largest tokens, at least k of them)
-// to the kept set's cut and size, and the token.  The first k are kept, of
-// those the ones whose predecessors weigh less than `bound` (0: p of the k
-// tokens' weight).  By sorting them: for ties beyond pick()'s lists.  Whole
-// CTA; scratch: S.cand.
-__device__ void pick_sorted(Shared& S, const Row& r, int n, int k, u64 bound,
-                            float p, float mp, float u, int* token) {
-  const int tid = threadIdx.x;
-  sort_down(S.all_cand, n);
-  constexpr int kPer = kCand / kThreads;
-  auto x_at = [&](u64 w) { return x_of(of_key((uint32_t)(w >> 32)), r); };
-  float x[kPer];
-  u64 w[kPer], mine = 0;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int i = tid * kPer + j;
-    x[j] = i < k ? x_at(S.all_cand[i]) : 0.f;
-    w[j] = i < k ? weight_of(x[j]) : 0;
-    mine += w[j];
-  }
-  u64 total, before = cta_scan(S, mine, &total);
-  if (bound == 0) bound = p < 1.f ? top_p_bound(p, total) : ~0ull;
-  int kept = 0;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int i = tid * kPer + j;
-    if (i < k && (i == 0 || before < bound) && x[j] >= mp) ++kept;
-    before += w[j];
-  }
-  u64 all;
-  cta_scan(S, (u64)kept, &all);
-  kept = (int)all;  // a prefix of the order
-  if (tid == 0) {
-    S.cut = S.all_cand[kept - 1];
-    S.kept = kept;
-  }
-  // the kept tokens by id: the word's lower half is the id's complement
-  for (int i = tid; i < kept; i += kThreads)
-    S.cand[i] = S.all_cand[i] << 32 | (uint32_t)i;
-  __syncthreads();
-  sort_down(S.cand, kept);
-  mine = 0;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int i = tid * kPer + j;
-    w[j] = i < kept ? weight_of(x_at(S.all_cand[(uint32_t)S.cand[i]])) : 0;
-    mine += w[j];
-  }
-  before = cta_scan(S, mine, &total);
-  const u64 target = draw_target(u, total);
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int i = tid * kPer + j;
-    if (w[j] > 0 && target >= before && target < before + w[j])
-      *token = (int)~(uint32_t)(S.cand[i] >> 32);
-    before += w[j];
-  }
-}
-
-// The same without a sort.  Bins of equal width from the maximum to `low`
-// (which no candidate is below) hold the candidates' numbers and weights: the
-// bin of the k-th token, or of the one whose weight passes the bound, is found
-// by a scan, and its few members by comparing each with each.  The token is
-// found likewise, in bins of ids.  1053 candidates, k = 1000, p = 0.9: sorting
-// them by rank, then those kept by id, took 33 us of a lone row's 41 us.
-__device__ void pick(Shared& S, const Row& r, float t, float low, int V, int n,
-                     int k, u64 bound, float p, float mp, float u,
-                     int* token) {
-  const int tid = threadIdx.x;
-  const u64 given = bound;
-  const float span = low > -INFINITY ? r.top - low : 32.f * t;
-  const float scale = (float)(kBins - 1) / span;
-  int shift = 0;
-  while (V - 1 >> shift >= kBins) ++shift;
-  auto clear = [&] {
-    for (int i = tid; i < kBins; i += kThreads)
-      S.count[i] = S.w_lo[i] = S.w_hi[i] = 0;
-    if (tid == 0) S.n_list = 0;
-    __syncthreads();
-  };
-  auto logit = [&](u64 w) { return of_key((uint32_t)(w >> 32)); };
-  auto bin_at = [&](u64 w) {  // monotone; what is no number counts as 0
-    return min((int)__fmul_rn(__fsub_rn(r.top, logit(w)), scale), kBins - 1);
-  };
-  auto id_bin = [&](u64 w) { return (int)(~(uint32_t)w >> shift); };
-  auto count = [&](int i) { return S.count[i]; };
-  auto weight = [&](int i) { return (u64)S.w_hi[i] << 32 | S.w_lo[i]; };
-  auto list = [&](u64 key, float x) {
-    const uint32_t at = atomicAdd(&S.n_list, 1u);
-    if (at < kList) {
-      S.list[at] = key;
-      S.list_w[at] = weight_of(x);
-    }
-  };
-  // The cut in the found bin; false if it has too many members.
-  auto edge = [&](bool by_weight) {
-    const int bin = S.found_bin;
-    for (int i = tid; i < n; i += kThreads) {
-      const u64 c = S.all_cand[i];
-      if (bin_at(c) == bin) list(c, x_of(logit(c), r));
-    }
-    __syncthreads();
-    const int m = (int)S.n_list;
-    if (m > kList) return false;
-    if (tid < m) {
-      const u64 mine = S.list[tid], w = S.list_w[tid], need = S.target;
-      int rank = (int)S.found_n;
-      u64 before = S.found_w;
-      for (int j = 0; j < m; ++j)
-        if (S.list[j] > mine) {
-          ++rank;
-          before += S.list_w[j];
-        }
-      if (by_weight ? before < need && before + w >= need : rank + 1 == k) {
-        S.cut = mine;
-        S.kept_before = before + w;
-      }
-    }
-    __syncthreads();
-    if (tid == 0) S.n_list = 0;
-    return true;
-  };
-
-  if (tid == 0) {
-    S.kept = 0;
-    S.least_key = ~0u;
-  }
-  clear();
-  for (int i = tid; i < n; i += kThreads) {
-    const u64 c = S.all_cand[i];
-    const int b = bin_at(c);
-    atomicAdd(&S.count[b], 1u);
-    add_weight(S, b, weight_of(x_of(logit(c), r)));
-  }
-  __syncthreads();
-  bool found = false, ok = true;
-  if (bound) {
-    find_bin(S, kBins, count, weight, true, 0, [&](u64) { return bound; });
-    found = S.found_bin >= 0;
-    if (found) ok = edge(true);
-    else __syncthreads();  // all of them are lighter: all are kept
-  }
-  if (!found) {
-    find_bin(S, kBins, count, weight, false, (uint32_t)k,
-             [](u64) { return 0ull; });
-    ok = edge(false);
-    if (ok && bound == 0 && p < 1.f) {
-      bound = top_p_bound(p, S.kept_before);
-      find_bin(S, kBins, count, weight, true, 0, [&](u64) { return bound; });
-      ok = edge(true);
-    }
-  }
-  if (ok) {
-    const u64 cut = S.cut;
-    auto keeps = [&](u64 c, float x) { return c >= cut && x >= mp; };
-    clear();
-    for (int i = tid; i < n; i += kThreads) {
-      const u64 c = S.all_cand[i];
-      const float x = x_of(logit(c), r);
-      if (!keeps(c, x)) continue;
-      add_weight(S, id_bin(c), weight_of(x));
-      atomicAdd(&S.kept, 1);
-      if (mp > 0.f) atomicMin(&S.least_key, (uint32_t)(c >> 32));
-    }
-    __syncthreads();
-    find_bin(S, kBins, count, weight, true, 0,
-             [&](u64 total) { return draw_target(u, total) + 1; });
-    const int bin = S.found_bin;
-    for (int i = tid; i < n; i += kThreads) {
-      const u64 c = S.all_cand[i];
-      if (id_bin(c) != bin) continue;
-      const float x = x_of(logit(c), r);
-      if (keeps(c, x)) list(~(uint32_t)c, x);
-    }
-    // what is kept, as one cut: all of the smallest logit if min-p decided
-    if (tid == 0 && mp > 0.f)
-      S.cut = max(cut, (u64)S.least_key << 32 | 0x80000000u);
-    __syncthreads();
-    const int m = (int)S.n_list;
-    ok = m <= kList;
-    if (ok && tid < m) {
-      const u64 mine = S.list[tid], target = S.target - 1;
-      u64 before = S.found_w;
-      for (int j = 0; j < m; ++j)
-        if (S.list[j] < mine) before += S.list_w[j];
-      if (target >= before && target < before + S.list_w[tid])
-        *token = (int)mine;
-    }
-  }
-  if (!ok) pick_sorted(S, r, n, k, given, p, mp, u, token);
-}
-
-// Three CTAs to an SM (40 registers) hide each other's barriers: 288 rows with
-// mixed filters 217 us with two (64 registers), 193 us with three, 191 us with
-// four, where 128 rows without filters go from 73 us to 78 us.
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 3)
+// Three CTAs to an SM (40 registers each thread) hide each other's barriers:
+// 288 rows with mixed filters 193 us, 217 us with two (64 registers).  Where
+// there are no more than two to an SM, 64 registers spare the spills: 64 rows
+// with top-p 0.9 54 us, 71 us with 40 registers.
+template <typename T, int kPerSm>
+__global__ void __launch_bounds__(kThreads, kPerSm)
     sample_kernel(const __grid_constant__ SampleArgs a) {
   cg::cluster_group cl = cg::this_cluster();
   extern __shared__ uint4 smem16[];
@@ -722,12 +667,16 @@ __global__ void __launch_bounds__(kThreads, 3)
   const T* data = a.resident ? own : src;
   const bool src_wide = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
   const bool wide = a.resident || src_wide;
+  // A thread's tokens are four quarters: of a slice that is copied, a quarter
+  // of each copy's words, else every fourth of its words (or tokens).
+  constexpr int E = Vec<T>::E;
+  const int words = n / E, per = (words + kChunks - 1) / kChunks;
 
   // ---- the slice and the row's maximum -------------------------------------
   if (tid == 0) {
-    S.odd = 0;
+    S.odd = S.fine = 0;
     S.kept_n = 0;
-    S.listed = 0;
+    S.listed = S.n_quarters = 0;
     for (int i = 0; i < kCollects; ++i) S.row_listed[i] = 0;
     S.first = 0x7fffffff;
     S.t = a.temperature[row];
@@ -743,8 +692,10 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
   for (int c = 0; c < kChunks; ++c) tops[c] = -INFINITY;
   bool odd = false;  // a logit that is not finite
+  uint32_t bits = 0;
   auto take = [&](int c, float l) {
     odd |= !(fabsf(l) < INFINITY);
+    bits |= __float_as_uint(l);
     tops[c] = fmaxf(tops[c], l);    // passes over a NaN
   };
   // A word of them; bf16 in pairs: what is not finite survives one of the
@@ -771,8 +722,6 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
   };
   if (src_wide && a.resident) {
-    constexpr int E = Vec<T>::E;
-    const int words = n / E, per = (words + kChunks - 1) / kChunks;
     if (tid == 0)
       for (int c = 0; c < kChunks; ++c) {
         const int v0 = min(words, c * per), v1 = min(words, v0 + per);
@@ -800,8 +749,6 @@ __global__ void __launch_bounds__(kThreads, 3)
       take(0, to_f32(x));
     }
   } else if (src_wide) {
-    constexpr int E = Vec<T>::E;
-    const int words = n / E;
     const uint4* p = reinterpret_cast<const uint4*>(src);
     for (int v = tid; v < words; v += kChunks * kThreads) {
       Vec<T> x[kChunks];
@@ -834,6 +781,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   if (lane == 0) S.warp_w[wid] = __float_as_uint(top);
   __syncthreads();
   if (odd) S.odd = 1;
+  if (bits & 0xffffu) S.fine = 1;
   if (tid == 0) {
     for (int i = 1; i < kWarps; ++i)
       top = fmaxf(top, __uint_as_float((uint32_t)S.warp_w[i]));
@@ -858,12 +806,50 @@ __global__ void __launch_bounds__(kThreads, 3)
     if (bad) raise_error(a.err, kErrNonfinite);
   }
   const int k = S.top_k;
-  const float p = S.top_p;
+  const float p = S.top_p < 0.f ? 0.f : S.top_p;
   // at most 1 (which keeps the maximum), 0 for what is no number
   const float mp = S.min_p > 0.f ? fminf(S.min_p, 1.f) : 0.f;
   const float u = S.u;
   const bool by_k = !r.greedy && !empty && k > 0 && k < a.V;
   const bool by_p = !r.greedy && !empty && p < 1.f;
+  // f(i, logit) over the slice's tokens from `low` up: those of the threads'
+  // quarters whose maximum is not below it, a word to a thread.  Once a row.
+  auto from = [&](float low, auto f) {
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+      if (tops[c] >= low && tops[c] > -INFINITY)
+        S.quarters[atomicAdd(&S.n_quarters, 1u)] = c * kThreads + tid;
+    __syncthreads();
+    const bool copied = a.resident && src_wide;
+    const int step = copied ? kThreads : kChunks * kThreads;
+    const int units = src_wide ? words : n;  // words, or tokens
+    const uint32_t q = (copied ? per + step - 1 : units + step - 1) / step;
+    const uint32_t items = S.n_quarters * q;
+    auto test = [&](int i, float l) {
+      if (l >= low && l > -INFINITY) f(i, l);
+    };
+#pragma unroll 2
+    for (uint32_t it = tid; it < items; it += kThreads) {
+      const uint32_t at = it / q;
+      const int of = S.quarters[at], c = of / kThreads;
+      int v = of + (int)(it - at * q) * step, to = units;
+      if (copied) {
+        v += c * (per - kThreads);
+        to = min(words, (c + 1) * per);
+      }
+      if (v >= to) continue;
+      if (src_wide) {
+        const Vec<T> x{reinterpret_cast<const uint4*>(data)[v]};
+#pragma unroll
+        for (int k = 0; k < E; ++k) test(v * E + k, x.at(k));
+      } else {
+        test(v, to_f32(data[v]));
+      }
+    }
+    if (src_wide)
+      for (int i = words * E + tid; i < n; i += kThreads)
+        test(i, to_f32(data[i]));
+  };
   float* dst = a.filtered ? a.filtered + (size_t)row * a.V + id0 : nullptr;
   // the slice's filtered logits: those not below the cut, given as a word
   auto filter = [&](u64 cut) {
@@ -888,8 +874,8 @@ __global__ void __launch_bounds__(kThreads, 3)
         for (int j = 0; j < 4; ++j)
           f[j] = f[j] > lc || (f[j] == lc && id0 + 4 * v + j <= last)
                      ? f[j] : -INFINITY;
-        reinterpret_cast<float4*>(dst)[v] =
-            make_float4(f[0], f[1], f[2], f[3]);
+        __stcs(reinterpret_cast<float4*>(dst) + v,
+               make_float4(f[0], f[1], f[2], f[3]));
       }
       for (int i = words * 4 + tid; i < n; i += kThreads) {
         const float l = to_f32(data[i]);
@@ -907,9 +893,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   if (r.greedy || empty) {  // uniform over the cluster
     int first = 0x7fffffff;
     if (!empty)
-      each(data, wide, 0, n, tid, kThreads, [&](int i, float l) {
-        if (l == top) first = min(first, id0 + i);
-      });
+      from(top, [&](int i, float) { first = min(first, id0 + i); });
     if (first != 0x7fffffff) atomicMin(&S.first, first);
     cl.sync();
     first = lane < C ? cl.map_shared_rank(&S, lane)->first : 0x7fffffff;
@@ -927,17 +911,15 @@ __global__ void __launch_bounds__(kThreads, 3)
 
   // The tokens from `low` up as candidates, cut and drawn from by the first
   // CTA; false if they are too many.
-  auto finish = [&](float low, bool free, int most, u64 bound) {
-    each(data, wide, 0, n, tid, kThreads, [&](int i, float l) {
-      if (l >= low && l > -INFINITY) {
-        const uint32_t at = atomicAdd(&S.listed, 1u);
-        if (at < kCand) S.cand[at] = word_of(l, id0 + i);
-      }
+  auto finish = [&](float low, int most, u64 bound) {
+    from(low, [&](int i, float l) {
+      const uint32_t at = atomicAdd(&S.listed, 1u);
+      if (at < kOwn) S.cand[at] = word_of(l, id0 + i);
     });
     int all;
-    if (!collect(S, cl, 0, free, &all)) return false;
+    if (!collect(S, cl, 0, &all)) return false;
     if (rank == 0) {
-      pick(S, r, t, low, a.V, all, min(most, all), bound, p, mp, u,
+      pick(S, r, low, a.V, all, min(most, all), bound, p, mp, u,
            a.token + row);
       if (tid == 0 && a.n_kept) a.n_kept[row] = S.kept;
       __syncthreads();
@@ -975,7 +957,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       __syncthreads();
     }
     const uint32_t* of = own_bound ? S.count : S.all_count;
-    find_bin(S, kCandBins, [&](int i) { return of[i]; },
+    find_bin<kCandBins>(S, kCandBins, [&](int i) { return of[i]; },
              [](int) { return 0ull; }, false, (uint32_t)k,
              [](u64) { return 0ull; });
     const int bin = S.found_bin;
@@ -986,21 +968,183 @@ __global__ void __launch_bounds__(kThreads, 3)
         bin < 0 ? -INFINITY
                 : bin_floor((bin + 1) * (kBins / kCandBins) - 1, b, t);
     // top-k of fewer tokens than k keeps them all
-    if (finish(low, true, k, 0)) return;
+    if (finish(low, k, 0)) return;
   }
 
-  // ---- the cut by histogram of weights --------------------------------------
+  // ---- the cut by counts in bins ----------------------------------------------
+  const bool by_m = mp > 0.f;
+  const float low_m =  // no token kept by min-p is below
+      by_m ? r.top + logf(mp) * t * 1.0001f - fabsf(r.top) * 1e-6f
+           : -INFINITY;
+  // min-p alone: its tokens, if they are few, are candidates of no other bound
+  if (by_m && !by_k && !by_p && finish(low_m, kCand, ~0ull)) return;
   u64 cut = 0;
-  if (by_k || by_p) {
-    for (int i = tid; i < kBins; i += kThreads)
-      S.count[i] = S.w_lo[i] = S.w_hi[i] = 0;
+  bool done = false;  // kept_w and kept_n are those of the cut
+
+  // The tokens of bins [0, bins) from `low` up into the bins, over the
+  // cluster; the weight of all tokens, and of those in the first kTopBins.
+  auto fill = [&](float low, int bins, u64* top_w) {
+    for (int i = tid; i < bins; i += kThreads) S.count[i] = 0;
+    if (tid < 32) S.w_lo[tid] = S.w_hi[tid] = 0;
     __syncthreads();
-    // Top-p only: tokens of less than (1 - p) W / V weigh less than (1 - p) W
-    // together, so they are past the cut and need no bin.  The weight of this
-    // CTA's threads' maxima, times 0.9 for roundings, stands for W from below.
-    float low = -INFINITY;
+    u64 sum = 0;
+    if (!S.odd && r.inv_t < INFINITY) {  // as in the sum of all weights below
+      for (int b = 0; b < n; b += kThreads * 512) {
+        uint32_t hi = 0, lo = 0, m = 0;
+        each(data, wide, b, min(n, b + kThreads * 512), tid, kThreads,
+             [&](int, float l) {
+               const float z = __fmul_rn(__fsub_rn(l, r.top), r.inv_t);
+               const WeightBits w = weight_bits(expf(z));
+               hi += w.hi;
+               lo += w.lo;
+               ++m;
+               // (the integer part by an addition to 2^23, as in weight_bits)
+               const float b = __fmaf_rz(z, -kBinsPerUnit, 0x1p23f);
+               const uint32_t bin = __float_as_uint(b) - 0x4b000000u;
+               if (l >= low) atomicAdd(&S.count[min(bin, bins - 1u)], 1u);
+               if (bin < kTopBins)
+                 add_weight(S, lane,
+                            (u64)(w.hi - 0x4b000000u) * (1u << 23) +
+                                (w.lo - 0x4b000000u));
+             });
+        sum += (u64)(hi - m * 0x4b000000u) * (1u << 23) +
+               (lo - m * 0x4b000000u);
+      }
+    } else {
+      each(data, wide, 0, n, tid, kThreads, [&](int, float l) {
+        if (!(l > -INFINITY)) return;
+        const u64 w = weight_of(x_of(l, r));
+        const int bin = bin_of(l, r);
+        sum += w;
+        if (l >= low) atomicAdd(&S.count[min(bin, bins - 1)], 1u);
+        if (bin < kTopBins) add_weight(S, lane, w);
+      });
+    }
+    sum = warp_total(sum);
+    if (lane == 0) S.warp_w[wid] = sum;
+    __syncthreads();
+    if (wid == 0) {
+      sum = warp_total(lane < kWarps ? S.warp_w[lane] : 0ull);
+      const u64 tw = warp_total(((u64)S.w_hi[lane] << 32) + S.w_lo[lane]);
+      if (lane == 0) {
+        S.total = sum;
+        S.top_w = tw;
+      }
+    }
+    reduce_counts(S, cl, bins);
+    u64 total = 0;
+    *top_w = 0;
+    for (int c = 0; c < C; ++c) {
+      total += cl.map_shared_rank(&S, c)->total;
+      *top_w += cl.map_shared_rank(&S, c)->top_w;
+    }
+    return total;
+  };
+
+  // The cut if it lies in [lo, hi]: kept_w and kept_n of the tokens above, the
+  // others listed, cut, and counted if kept.  False if it does not, or if
+  // there are too many of them.
+  auto narrow = [&](int call, float lo, float hi, bool by_weight,
+                    uint32_t need_n, u64 need_w) {
+    if (tid == 0) {
+      S.listed = 0;
+      S.kept_n = 0;
+      S.cut = 0;
+    }
+    __syncthreads();
+    int c0, c1;
+    warp_chunk(n, wid, &c0, &c1);
+    u64 sum = 0;
+    uint32_t cnt = 0;
+    for (int b = c0; b < c1; b += 32 * 512) {  // as in the sum of all weights
+      uint32_t w_hi = 0, w_lo = 0, m = 0;
+      each(data, wide, b, min(c1, b + 32 * 512), lane, 32,
+           [&](int i, float l) {
+             const bool on = l > hi;
+             const WeightBits w = weight_bits(on ? x_of(l, r) : 0.f);
+             w_hi += w.hi;
+             w_lo += w.lo;
+             ++m;
+             cnt += on;
+             if (l >= lo && !on && l > -INFINITY) {
+               const uint32_t at = atomicAdd(&S.listed, 1u);
+               if (at < kOwn) S.cand[at] = word_of(l, id0 + i);
+             }
+           });
+      sum += (u64)(w_hi - m * 0x4b000000u) * (1u << 23) +
+             (w_lo - m * 0x4b000000u);
+    }
+    sum = warp_total(sum);
+    cnt = warp_total(cnt);
+    if (lane == 0) {
+      S.kept_w[wid] = sum;
+      if (cnt) atomicAdd(&S.kept_n, cnt);
+    }
+    int all;
+    if (!collect(S, cl, call, &all)) return false;
+    if (rank == 0) {
+      sum = 0;
+      for (int i = lane; i < C * kWarps; i += 32)
+        sum += cl.map_shared_rank(&S, i / kWarps)->kept_w[i % kWarps];
+      sum = warp_total(sum);
+      cnt = warp_total(lane < C ? cl.map_shared_rank(&S, lane)->kept_n : 0u);
+      if (by_weight ? sum < need_w : cnt < need_n) {  // uniform
+        cut_in(S, r, all, (u64)key_of(hi) << 32 | 0xffffffffu,
+               (u64)key_of(lo) << 32, false, by_weight, need_n - cnt,
+               [](u64 c) { return c; }, [&](u64) { return need_w - sum; });
+        const u64 at_cut = S.cut, before = sum + S.kept_before;
+        __syncthreads();
+        if (tid < C) {
+          Shared* o = cl.map_shared_rank(&S, tid);
+          o->cut = at_cut;
+          o->kept_before = before;
+        }
+      }
+    }
+    cl.sync();
+    const u64 at_cut = S.cut;
+    if (at_cut == 0) return false;
+    // (the first CTA's slots have overwritten its list)
+    const u64* mine = rank == 0 ? S.all_cand + S.list_at : S.cand;
+    const int per = ((n + kWarps - 1) / kWarps + 127) & ~127;
+    for (uint32_t i = tid; i < S.listed; i += kThreads) {
+      const u64 c = mine[i];
+      if (c < at_cut) continue;
+      atomicAdd(&S.kept_w[((int)~(uint32_t)c - id0) / per],
+                weight_of(x_of_word(c, r)));
+      atomicAdd(&S.kept_n, 1u);
+    }
+    __syncthreads();
+    return true;
+  };
+
+  u64 total = 0, top_w;
+  bool have_total = false;
+  if (by_k) {
+    fill(-INFINITY, kBins, &top_w);
+    find_bin<kBins>(S, kBins, [&](int i) { return S.all_count[i]; },
+             [](int) { return 0ull; }, false, (uint32_t)k,
+             [](u64) { return 0ull; });
+    const int bin = S.found_bin;
+    __syncthreads();
+    if (bin >= 0) {  // fewer than k tokens above -inf: no cut
+      done = narrow(1, bin_floor(bin, r, t), bin_ceil(bin, r, t), false,
+                    (uint32_t)k, 0);
+      if (!done)
+        refine_cut(S, cl, data, wide, n, id0, r, 3, false, (uint32_t)k, 0);
+      cut = S.cut;
+      total = S.kept_before;
+      have_total = true;
+      __syncthreads();
+    }
+  }
+  if (by_p) {
+    // Tokens of less than (1 - p) W / V weigh less than (1 - p) W together, so
+    // they are past the cut and need no bin.  The weight of this CTA's
+    // threads' maxima, times 0.9 for roundings, stands for W from below where
+    // no top-k has a say; 1 does for all CTAs, and for how many bins they use.
+    float sum = 0.f;
     if (!by_k) {
-      float sum = 0.f;
 #pragma unroll
       for (int c = 0; c < kChunks; ++c)
         if (tops[c] > -INFINITY) sum += x_of(tops[c], r);
@@ -1010,99 +1154,88 @@ __global__ void __launch_bounds__(kThreads, 3)
       sum = 0.f;
       for (int i = 0; i < kWarps; ++i) sum += __uint_as_float(S.warp_n[i]);
       __syncthreads();
-      const float least = 0.9f * (1.f - p) * sum / (float)a.V;
-      if (least > 0.f && least < 1.f)
-        low = r.top + logf(least) * t * 1.0001f - fabsf(r.top) * 1e-6f;
     }
-    const bool plain = !S.odd && r.inv_t < INFINITY;
-    auto fill = [&] {
-      u64 sum = 0;
-      if (plain) {  // as in the sum of all weights below
-        for (int b = 0; b < n; b += kThreads * 512) {
-          uint32_t hi = 0, lo = 0, m = 0;
-          each(data, wide, b, min(n, b + kThreads * 512), tid, kThreads,
-               [&](int, float l) {
-                 const WeightBits w = weight_bits(x_plain(l, r));
-                 hi += w.hi;
-                 lo += w.lo;
-                 ++m;
-                 if (l < low) return;
-                 const int bin = bin_of(l, r);
-                 atomicAdd(&S.count[bin], 1u);
-                 if (by_p)
-                   add_weight(S, bin,
-                              (u64)(w.hi - 0x4b000000u) * (1u << 23) +
-                                  (w.lo - 0x4b000000u));
-               });
-          sum += (u64)(hi - m * 0x4b000000u) * (1u << 23) +
-                 (lo - m * 0x4b000000u);
-        }
-        return sum;
-      }
-      each(data, wide, 0, n, tid, kThreads, [&](int i, float l) {
-        if (!(l > -INFINITY)) return;
-        const u64 w = weight_of(x_of(l, r));
-        sum += w;
-        if (l < low) return;
-        const int bin = bin_of(l, r);
-        atomicAdd(&S.count[bin], 1u);
-        if (by_p) add_weight(S, bin, w);
-      });
-      return sum;
+    const float share = 0.9f * (1.f - p) / (float)a.V;
+    auto logit_of = [&](float x) {  // a little below
+      return x > 0.f && x < 1.f
+                 ? r.top + logf(x) * t * 1.0001f - fabsf(r.top) * 1e-6f
+                 : -INFINITY;
     };
-    bool redo = false;  // the top-k cut has overwritten the histogram
-    u64 sum = warp_total(fill());
-    if (lane == 0) S.warp_w[wid] = sum;
-    __syncthreads();
-    if (tid == 0) {
-      for (int i = 1; i < kWarps; ++i) sum += S.warp_w[i];
-      S.total = sum;
-    }
-    reduce_bins(S, cl, kBins);
-    u64 total = 0;
-    for (int c = 0; c < C; ++c) total += cl.map_shared_rank(&S, c)->total;
-    if (by_k) {
-      find_bin(S, kBins, false, (uint32_t)k, 0);
-      if (S.found_bin >= 0) {  // fewer than k tokens above -inf: no cut
-        redo = true;
-        bin_cut(S, cl, data, wide, n, id0, r, t, 1, false, (uint32_t)k, 0);
-        cut = S.cut;
-        total = S.kept_before;
-        __syncthreads();
-      }
-    }
-    if (by_p) {
-      const u64 bound = top_p_bound(p, total);
-      // The tokens past the top-k cut may stay in the histogram: bound is at
-      // most the weight before them.
-      if (redo) {
-        for (int i = tid; i < kBins; i += kThreads)
-          S.count[i] = S.w_lo[i] = S.w_hi[i] = 0;
-        __syncthreads();
-        fill();
-        reduce_bins(S, cl, kBins);
-      }
-      find_bin(S, kBins, true, 0, bound);
-      // few tokens up to the cut's bin: they are all that is left to look at
-      const int bin = S.found_bin;
-      if (!redo && bin < kBins - 1 &&
-          S.found_n + S.all_count[bin] <= kCand / 2) {
+    const float low = fmaxf(logit_of(share * fmaxf(sum, 1.f)), low_m);
+    const int bins =
+        share > 0.f
+            ? min(kBins, (int)(-logf(share) * kBinsPerUnit * 1.001f) + 3)
+            : kBins;
+    const u64 weight = fill(low, bins, &top_w);
+    const u64 bound = top_p_bound(p, have_total ? total : weight);
+    auto count = [&](int i) { return S.all_count[i]; };
+    // The bin of the cut.  A bin's tokens all weigh that of its place `at`;
+    // the first bins, whose tokens are few and heavy, weigh what they do if
+    // the cut is past them: a token of weight w puts the sum off by w / 128 at
+    // most, of which the cut's own bin may hold less.  (The last may hold
+    // tokens of beyond it: nothing, from below.)
+    // Logits that are bf16 numbers do not fill a bin evenly: they all stand at
+    // the one that is next to its middle.
+    const u64 off = bound > top_w ? top_w : 0;
+    bool coarse = true;
+    for (int c = 0; c < C; ++c) coarse &= !cl.map_shared_rank(&S, c)->fine;
+    auto find = [&](float at, float slack) {
+      find_bin<kBins>(S, bins, count,
+               [&](int i) {
+                 float x = expf(((float)i + at) * (-1.f / kBinsPerUnit));
+                 if (coarse && slack == 0.f) {
+                   const float l = __bfloat162float(__float2bfloat16_rn(
+                       r.top - ((float)i + at) * t * (1.f / kBinsPerUnit)));
+                   if (l <= r.top && bin_of(l, r) == i) x = x_of(l, r);
+                 }
+                 const float w = floorf(x * 0x1p44f * (1.f + slack)) +
+                                 (slack < 0.f ? -1.f : 1.f);
+                 return (slack < 0.f && i == bins - 1) || (off && i < kTopBins)
+                            ? 0ull
+                            : S.all_count[i] * (u64)fmaxf(w, 0.f);
+               },
+               true, 0, [&](u64) { return bound - off; });
+      return S.found_bin;
+    };
+    int bin = find(0.5f, 0.f);
+    if (!have_total && bin >= 0 &&
+        S.found_n + S.all_count[bin] <= kOwn * 3 / 4) {
+      __syncthreads();
+      const int last = find(1.f, -1e-4f);  // from below: the cut is not past it
+      if (last >= 0 && S.found_n + S.all_count[last] <= kOwn * 7 / 8) {
         if (tid == 0) S.listed = 0;
         __syncthreads();
-        if (finish(bin_floor(bin, r, t), false, kCand, bound)) return;
-        // (not so few: the bins have been overwritten)
-        for (int i = tid; i < kBins; i += kThreads)
-          S.count[i] = S.w_lo[i] = S.w_hi[i] = 0;
-        __syncthreads();
-        fill();
-        reduce_bins(S, cl, kBins);
-        find_bin(S, kBins, true, 0, bound);
+        if (finish(bin_floor(last, r, t), kCand, bound)) return;
+        fill(low, bins, &top_w);  // the list has overwritten the bins
       }
-      bin_cut(S, cl, data, wide, n, id0, r, t, 2, true, 0, bound);
+    }
+    __syncthreads();
+    bool past = false;  // the cut is past all tokens that min-p keeps
+    if (by_m && bin < 0) {
+      past = find(0.f, 1e-4f) < 0;
+      __syncthreads();
+    }
+    if (!past) {
+      if (bin < 0) bin = bins - 1;
+      // one bin on each side of it, more while they hold few tokens
+      int b0 = bin, b1 = bin;
+      uint32_t c = S.all_count[bin];
+      for (int i = 0; i < 16 && (i < 2 || c < 512); ++i) {
+        const int b = i & 1 ? b0 - 1 : b1 + 1;
+        if (b < 0 || b >= bins || c + S.all_count[b] > kOwn - 128) continue;
+        c += S.all_count[b];
+        b0 = min(b0, b);
+        b1 = max(b1, b);
+      }
+      __syncthreads();
+      done = narrow(2, bin_floor(b1, r, t), bin_ceil(b0, r, t), true, 0, bound);
+      if (!done)
+        refine_cut(S, cl, data, wide, n, id0, r, 4, true, 0, bound);
       cut = max(cut, S.cut);
+      __syncthreads();
     }
   }
-  const bool by_m = mp > 0.f;
+  done = done && !by_m;
   auto keeps = [&](float l, int i, float x) {
     return l > -INFINITY && (cut == 0 || word_of(l, id0 + i) >= cut) &&
            (!by_m || x >= mp);
@@ -1114,7 +1247,9 @@ __global__ void __launch_bounds__(kThreads, 3)
   u64 sum = 0;
   uint32_t cnt = 0;
   float least = INFINITY;  // smallest kept logit, where min-p has a say
-  if (cut == 0 && !by_m) {
+  if (done) {
+    // (there already)
+  } else if (cut == 0 && !by_m) {
     if (S.odd || !(r.inv_t < INFINITY)) {  // uniform in the CTA
       each(data, wide, c0, c1, lane, 32, [&](int, float l) {
         const bool on = l > -INFINITY;  // not a NaN, either
@@ -1142,9 +1277,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   } else {
     // no weight is needed of what lies surely below the filters
     const float low =
-        fmaxf(cut ? of_key((uint32_t)(cut >> 32)) : -INFINITY,
-              by_m ? r.top + logf(mp) * t * 1.0001f - fabsf(r.top) * 1e-6f
-                   : -INFINITY);
+        fmaxf(cut ? of_key((uint32_t)(cut >> 32)) : -INFINITY, low_m);
     each(data, wide, c0, c1, lane, 32, [&](int i, float l) {
       if (!(l >= low)) return;
       const float x = x_of(l, r);
@@ -1158,10 +1291,14 @@ __global__ void __launch_bounds__(kThreads, 3)
   least = -warp_max(-least);
   sum = warp_total(sum);
   cnt = warp_total(cnt);
-  if (lane == 0) {
-    S.kept_w[wid] = sum;
-    S.kept_least[wid] = least;
-    if (cnt) atomicAdd(&S.kept_n, cnt);
+  if (!done) {
+    if (tid == 0) S.kept_n = 0;
+    __syncthreads();
+    if (lane == 0) {
+      S.kept_w[wid] = sum;
+      S.kept_least[wid] = least;
+      if (cnt) atomicAdd(&S.kept_n, cnt);
+    }
   }
   cl.sync();
   if (dst) {
@@ -1196,82 +1333,75 @@ __global__ void __launch_bounds__(kThreads, 3)
       const u64 v = __shfl_up_sync(0xffffffffu, run, o);
       if (lane >= o) run += v;
     }
-    const u64 total = __shfl_sync(0xffffffffu, run, 31);
+    const u64 all = __shfl_sync(0xffffffffu, run, 31);
     if (rank == 0) {
       uint32_t nk = lane < C ? cl.map_shared_rank(&S, lane)->kept_n : 0;
       nk = warp_total(nk);
       if (lane == 0 && a.n_kept) a.n_kept[row] = (int)nk;
     }
-    const u64 target = draw_target(u, total);
+    const u64 target = draw_target(u, all);
     u64 before = run - mine;
-    int hit = -1;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      if (hit < 0 && target >= before && target < before + w[j])
-        hit = lane * kPer + j;
-      if (hit < 0) before += w[j];
-    }
-    const unsigned who = __ballot_sync(0xffffffffu, hit >= 0);
-    const int from = __ffs(who) - 1;
-    hit = __shfl_sync(0xffffffffu, hit, from);
-    before = __shfl_sync(0xffffffffu, before, from);
-    if (hit / kWarps == rank) {  // the chunk is in this CTA's slice
-      warp_chunk(n, hit % kWarps, &c0, &c1);
-      // eight tokens to a lane at a time
-      for (int base = c0; base < c1; base += 256) {
-        u64 v[8], one = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int i = base + lane * 8 + j;
-          const float l = i < c1 ? to_f32(data[i]) : -INFINITY;
-          const float x = x_of(l, r);
-          v[j] = i < c1 && keeps(l, i, x) ? weight_of(x) : 0;
-          one += v[j];
-        }
-        u64 sum8 = one;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const u64 q = __shfl_up_sync(0xffffffffu, sum8, o);
-          if (lane >= o) sum8 += q;
-        }
-        u64 at = before + sum8 - one;
-        const bool here = one > 0 && target >= at && target < at + one;
-        if (here) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (target >= at && target < at + v[j])
-              a.token[row] = id0 + base + lane * 8 + j;
-            at += v[j];
-          }
-        }
-        if (__any_sync(0xffffffffu, here)) break;
-        before += __shfl_sync(0xffffffffu, sum8, 31);
+      if (target >= before && target < before + w[j]) {
+        S.found_bin = lane * kPer + j;
+        S.target = target - before;  // within the chunk
       }
+      before += w[j];
     }
+  }
+  __syncthreads();
+  const int chunk = S.found_bin;
+  if (chunk / kWarps == rank) {  // it is in this CTA's slice
+    u64 target = S.target;
+    warp_chunk(n, chunk % kWarps, &c0, &c1);
+    auto weight_at = [&](int i) {
+      const float l = to_f32(data[i]);
+      const float x = x_of(l, r);
+      return keeps(l, i, x) ? weight_of(x) : 0;
+    };
+    const int each_n = (c1 - c0 + kThreads - 1) / kThreads;
+    const int i0 = c0 + tid * each_n, i1 = min(c1, i0 + each_n);
+    u64 mine = 0, all;
+    for (int i = i0; i < i1; ++i) mine += weight_at(i);
+    u64 at = cta_scan(S, mine, &all);
+    if (target >= at && target < at + mine)
+      for (int i = i0; i < i1; ++i) {
+        const u64 w = weight_at(i);
+        if (target >= at && target < at + w) a.token[row] = id0 + i;
+        at += w;
+      }
   }
   cl.sync();  // no CTA leaves while another reads its sums
 }
 
 template <typename T>
 cudaError_t launch(SampleArgs a, cudaStream_t s) {
-  // Up to eight CTAs for each SM, three of them resident, if that takes at
-  // most eight to a row.  Fewer to a row cost less in barriers between them,
-  // more of them shorten rows that need several passes (288 rows of 151936
-  // fp32 logits with mixed filters: 235 us with two, 193 us with four; a lone
-  // row of top-k 50: 28 us with two, 20 us with eight; against that 128 rows
-  // of 262144 without filters: 68 us with four, 73 us with eight).  Never
-  // more than slices of 4096 tokens need.
+  // One wave of CTAs, three to an SM: fewer to a row cost less in barriers
+  // between them (64 rows of 262144 bf16 logits, top-k 50: 27 us with four, 38
+  // us with eight; a lone row 17 us with eight, 28 us with two).  But
+  // no slices of more than 65536 tokens, up to eight CTAs for each SM: rows
+  // differ in how long they take, and in several waves the short ones fill
+  // what the long ones leave (288 rows of 151936 with mixed filters: 156 us
+  // with four, 267 us with one; with top-k 50 in all of them 69 us and 53 us).
+  // Never more than slices of 4096 tokens need.
   int C = kMaxCluster;
-  while (C > 1 && ((long long)a.R * C > 8 * 152 ||
+  while (C > 1 && ((long long)a.R * C > 3 * 152 ||
                    (long long)(C / 2) * 4096 >= a.V))
     C /= 2;
-  // A slice stays in shared memory where two CTAs fit an SM so; the rest is
-  // read again, from L2 for the most part.
+  while (C < kMaxCluster && (long long)C * 65536 < a.V &&
+         (long long)a.R * C * 2 <= 8 * 152)
+    C *= 2;
+  // A slice stays in shared memory where that takes no CTA's place on an SM
+  // (100 rows of 151936 logits, top-k 50: 40 us, with slices of 76 KB held 45
+  // us); the rest is read again, from L2 for the most part.
+  const bool two = (long long)a.R * C <= 2 * 152;
   a.slice = (int)((((long long)a.V + C - 1) / C + 7) & ~7ll);
-  a.resident = (long long)a.slice * (long long)sizeof(T) <= 76 * 1024;
+  a.resident =
+      (long long)a.slice * (long long)sizeof(T) <= (two ? 76 : 36) * 1024;
   const size_t smem = (sizeof(Shared) + 15) / 16 * 16 +
                       (a.resident ? (size_t)a.slice * sizeof(T) : 16);
-  auto* f = sample_kernel<T>;
+  auto* f = two ? sample_kernel<T, 2> : sample_kernel<T, 3>;
   cudaError_t e = cudaFuncSetAttribute(
       f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -1285,7 +1415,7 @@ cudaError_t launch(SampleArgs a, cudaStream_t s) {
 extern "C" {
 
 size_t dflash_sample_workspace_bytes(int R, int V) {
-  if (R < 1 || R > (1 << 24) || V < 1 || V > (1 << 30)) return 0;
+  if (R < 1 || R > (1 << 24) || V < 1 || V >= (1 << 20)) return 0;
   return 256;
 }
 

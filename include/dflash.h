@@ -630,7 +630,8 @@ size_t dflash_sample_workspace_bytes(int R, int V);
  *   token [R] int32 out; n_kept [R] int32 out or NULL: tokens kept;
  *   filtered [R, V] fp32 out or NULL: l_v if kept, else -inf
  *   ws >= dflash_sample_workspace_bytes(R, V) bytes, 256-byte aligned
- * Requirements: R >= 1, V >= 1, ld >= V.  A NaN (left out) or +inf logit
+ * Requirements: R >= 1, 1 <= V < 2^20 (their weights add up in 64 bits),
+ * ld >= V.  A NaN (left out) or +inf logit
  * sets DFLASH_ERR_NONFINITE, as does a row with no logit above -inf (token
  * -1, n_kept 0) or a T that is negative or not finite (taken as 0).
  */

@@ -735,6 +735,68 @@ def test_sample_does_not_depend_on_the_split(lib):
     lib.dflash_check()
 
 
+def _wide_row(V, kind):
+    rng = np.random.default_rng(V)
+    l = (2.5 * rng.standard_normal(V)).astype(np.float32)
+    l[rng.integers(0, V, 30)] += 6
+    if kind == "bf16 values":      # values tie by the hundred
+        l = torch.from_numpy(l).bfloat16().float().numpy()
+    elif kind == "eighths":        # and by the thousand
+        l = np.round(l * 8) / 8
+    elif kind == "flat":
+        l = (l * 0.02).astype(np.float32)
+    elif kind == "one tie":        # 700 equal tokens around the cuts
+        l[rng.permutation(V)[:700]] = np.partition(l, -650)[-650]
+    elif kind == "masked":
+        l[rng.random(V) < 0.7] = -np.inf
+    return l[None]
+
+
+@pytest.mark.parametrize("kind", ["spread", "bf16 values", "eighths", "flat",
+                                  "one tie", "masked"])
+@pytest.mark.parametrize("T,k,p,m", [
+    (1.3, 0, 0.95, 0.0), (0.6, 0, 0.9, 0.0), (1.0, 0, 0.5, 0.001),
+    (1.0, 0, 0.999, 0.05), (1.0, 900, 1.0, 0.0), (1.0, 1200, 0.8, 0.01),
+    (0.02, 1500, 0.9, 0.0), (1.0, 2040, 1.0, 0.0), (1.0, 9000, 0.97, 0.0),
+    (40.0, 0, 0.3, 0.0), (1.0, 0, 1.0, 0.0004)])
+def test_sample_large_kept_sets(lib, kind, T, k, p, m):
+    """Kept sets of a hundred to tens of thousands, ties inside and across
+    every list's size, from one row (eight CTAs) and among many (one to four
+    CTAs, other registers, logits not held): the oracle's, and all the same."""
+    V = 60001 if kind == "masked" else 131072
+    l = _wide_row(V, kind)
+    x = torch.from_numpy(l).cuda()
+    if kind == "bf16 values":
+        y = x.bfloat16()
+    us = np.array([0.0, 0.37, 0.9999], np.float32)
+    for u in us:
+        a = _run_sample(lib, x, [T], [k], [p], [m], [u])
+        _check_sample(l, [T], [k], [p], [m], [u], a)
+        for n in (3, 300, 1300):
+            wide = (y if kind == "bf16 values" and n == 3 else x).repeat(n, 1)
+            b = _run_sample(lib, wide, [T] * n, [k] * n, [p] * n, [m] * n,
+                            [u] * n, filtered=n == 3)
+            assert np.all(b[0] == a[0]) and np.all(b[1] == a[1])
+            if n == 3:
+                assert np.array_equal(b[2], np.repeat(a[2], n, 0))
+            del wide
+    lib.dflash_check()
+
+
+def test_sample_largest_vocabulary(lib):
+    """Weights of 2^20 - 1 equal tokens add up in 64 bits; one more token is
+    refused."""
+    V = (1 << 20) - 1
+    l = np.full((2, V), -3.25, np.float32)
+    x = torch.from_numpy(l).cuda()
+    for k, p in ((None, None), (None, [0.75, 0.125]), ([1000, 700000], None)):
+        u = np.array([0.6, 0.3], np.float32)
+        got = _run_sample(lib, x, [1.0, 0.5], k, p, None, u)
+        lib.dflash_check()
+        _check_sample(l, [1.0, 0.5], k, p, None, u, got)
+    assert lib.dflash_sample_workspace_bytes(2, V + 1) == 0
+
+
 def test_filtered_logits_make_the_verify_lossless(lib):
     """dflash_verify on the filtered logits draws from the filtered target
     distribution: with no draft accepted by design, the emitted token's

@@ -171,6 +171,8 @@ def test_sample_refuses_on_the_host(so):
         {"ws": ctypes.c_void_p(0x100010)}, {"ws_bytes": size - 1}])
     assert so.dflash_sample_workspace_bytes(0, 100) == 0
     assert so.dflash_sample_workspace_bytes(4, 0) == 0
+    assert so.dflash_sample_workspace_bytes(4, (1 << 20) - 1) > 0
+    assert so.dflash_sample_workspace_bytes(4, 1 << 20) == 0
 
 
 def test_binding_refuses_wrong_tensors():
