@@ -321,6 +321,7 @@ struct Vec {
 
 // f(i, logit) over elements [from, to) of the slice for T threads of index t,
 // words of 16 bytes where the data is aligned to them (from always is).
+// Not unrolled: other warps hide the loads, and registers are short.
 template <typename T, typename F>
 __device__ __forceinline__ void each(const T* data, bool wide, int from,
                                      int to, int t, int threads, F f) {
@@ -329,7 +330,7 @@ __device__ __forceinline__ void each(const T* data, bool wide, int from,
   if (wide) {
     const int words = (to - from) / E;
     const uint4* p = reinterpret_cast<const uint4*>(data + from);
-#pragma unroll 2
+#pragma unroll 1
     for (int v = t; v < words; v += threads) {
       const Vec<T> x{p[v]};
 #pragma unroll
