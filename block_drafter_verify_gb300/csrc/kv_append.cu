@@ -29,7 +29,6 @@ dflash_status current_device_info(int* sms, int** err);
 
 namespace {
 
-constexpr float kE4m3Max = 448.f;
 constexpr int kMinExp = -64;   // smallest exponent of a block scale
 constexpr int kThreads = 256;  // most threads of a CTA
 constexpr int kKeep = 2;       // units a thread keeps in registers

@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
                          const Shape shape, float* __restrict__ part) {
   using PL = Plan<N>;
   constexpr int HR = PL::kRowsOf;  // rows of a softmax warp
-  constexpr int kThreads = PL::kThreads, kSoftWarps = 4 * PL::kGroups;
+  constexpr int kSoftWarps = 4 * PL::kGroups;
   extern __shared__ uint8_t raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
