@@ -442,33 +442,34 @@ def dflash_verify_shard_draw(target_shard, plan, topi, q, shard, v0, T,
 # --------------------------------------------------------------------------
 # the target's side of a cycle
 # --------------------------------------------------------------------------
+# (shape and stride() as a whole: size(i) and stride(i) take twice as long,
+# and at decode sizes a call costs the host more than the GPU)
 def _rows(t, dtype, tail, name):
-    """Address and row stride of a [rows, *tail] tensor whose rows are
+    """Address, row stride and rows of a [rows, *tail] tensor whose rows are
     contiguous but may lie apart (a slice of a projection's output)."""
     if t.dtype is not dtype:
         _want(t, dtype, name)
     if not t.is_cuda:
         raise ValueError("expected a CUDA tensor")
-    if t.dim() != len(tail) + 1:
-        raise ValueError(f"{name} must be [rows, {tail}]")
+    shape, stride = t.shape, t.stride()
+    if shape[1:] != tail:
+        raise ValueError(f"{name} must be [rows, {tail}], got {tuple(shape)}")
     step = 1
-    for i in range(len(tail), 0, -1):
-        n = t.size(i)
-        if n != tail[i - 1]:
-            raise ValueError(f"{name} must be [rows, {tail}], got "
-                             f"{tuple(t.shape)}")
-        if n != 1 and t.stride(i) != step:
+    for n, at in zip(reversed(tail), reversed(stride)):
+        if n != 1 and at != step:
             raise ValueError(f"rows of {name} must be contiguous")
         step *= n
-    return t.data_ptr(), t.stride(0) if t.size(0) > 1 else step
+    return t.data_ptr(), stride[0] if shape[0] > 1 else step, shape[0]
 
 
 def _heads(t, dtype, H, D, name):
     """_rows of [rows, H, D], the usual case first."""
-    if (t.dtype is dtype and t.is_cuda and t.dim() == 3 and
-            t.stride(2) == 1 and t.stride(1) == D and t.size(2) == D and
-            t.size(1) == H and t.size(0) > 1):
-        return t.data_ptr(), t.stride(0)
+    shape, stride = t.shape, t.stride()
+    if (len(shape) == 3 and stride[2] == 1 and stride[1] == D and
+            shape[2] == D and shape[1] == H and t.dtype is dtype and
+            t.is_cuda):
+        rows = shape[0]
+        return t.data_ptr(), stride[0] if rows > 1 else H * D, rows
     return _rows(t, dtype, (H, D), name)
 
 
@@ -496,27 +497,28 @@ def dflash_kv_append(q, k, v, cos, sin, pos, n_new, page_table, k_codes,
     q_out [B,Q,Hq,D] and kv_len [B] i32 outputs."""
     N, Hkv, page, D = _check_cache(k_codes, v_codes, k_scale, v_scale)
     B, max_pages = page_table.shape
-    rows, dt = k.size(0), k.dtype
-    if rows % B or v.size(0) != rows or pos.numel() != B or (
+    dt = k.dtype
+    kp, ld_k, rows = _heads(k, dt, Hkv, D, "k")
+    vp, ld_v, v_rows = _heads(v, dt, Hkv, D, "v")
+    if rows % B or v_rows != rows or pos.numel() != B or (
             kv_len.numel() != B) or (n_new is not None and
                                      n_new.numel() != B):
         raise ValueError("k and v must have B * Q rows; pos, n_new and "
                          "kv_len B entries")
-    kp, ld_k = _heads(k, dt, Hkv, D, "k")
-    vp, ld_v = _heads(v, dt, Hkv, D, "v")
     qp, ld_q, Hq, qo = None, 0, Hkv, None
     if q is not None:
-        Hq = q.size(1)
-        qp, ld_q = _heads(q, dt, Hq, D, "q")
+        Hq = q.shape[-2]
+        qp, ld_q, q_rows = _heads(q, dt, Hq, D, "q")
         qo = _at(q_out, dt, "q_out")
-        if q.size(0) != rows or q_out.numel() != rows * Hq * D:
+        if q_rows != rows or q_out.numel() != rows * Hq * D:
             raise ValueError("q and q_out must have B * Q rows")
     rot = max_pos = 0
     cp = sp = None
     if cos is not None:
-        max_pos, rot = cos.size(0), 2 * cos.size(1)
-        if sin.numel() != cos.numel() or 2 * sin.size(1) != rot:
+        max_pos, rot = cos.shape
+        if sin.shape != cos.shape:
             raise ValueError("cos and sin must have one shape")
+        rot *= 2
         cp, sp = _at(cos, _F32, "cos"), _at(sin, _F32, "sin")
     _run("dflash_kv_append", load().dflash_kv_append(
         qp, kp, vp, ld_q, ld_k, ld_v, cp, sp, _at(pos, _I32, "pos"),
@@ -573,7 +575,11 @@ def dflash_sample(logits, temperature, top_k, top_p, min_p, u, token, n_kept,
     (or None) and filtered [R,V] f32 (or None) outputs; ws uint8 of
     dflash_sample_workspace_bytes."""
     R, V = logits.shape
-    lp, ld = _rows(logits, logits.dtype, (V,), "logits")
+    ld, step = logits.stride()
+    if (step != 1 and V > 1) or not logits.is_cuda:
+        _rows(logits, logits.dtype, (V,), "logits")  # raises
+    if R == 1:
+        ld = V
 
     def row(t, dtype, name):
         if t is None:
@@ -585,7 +591,7 @@ def dflash_sample(logits, temperature, top_k, top_p, min_p, u, token, n_kept,
     if filtered is not None and filtered.shape != logits.shape:
         raise ValueError("filtered must be [R, V]")
     _run("dflash_sample", load().dflash_sample(
-        lp, ld, _dtype(logits), row(temperature, _F32, "temperature"),
+        logits.data_ptr(), ld, _dtype(logits), row(temperature, _F32, "temperature"),
         row(top_k, _I32, "top_k"), row(top_p, _F32, "top_p"),
         row(min_p, _F32, "min_p"), row(u, _F32, "u"), R, V,
         row(token, _I32, "token"), row(n_kept, _I32, "n_kept"),
