@@ -47,7 +47,8 @@ struct AppendArgs {
   float* scale[2];
   int* kv_len;
   int touched;                // most pages a sequence's tokens fall into
-  int cache_ctas;             // CTAs of the first kind
+  uint32_t share;  // of the grid, the CTAs of the cache
+  int rotates;     // there are others
   int* err;
 };
 
@@ -166,7 +167,7 @@ __device__ __forceinline__ float pow2(int e) {  // -126 <= e <= 127
 
 template <int VEC>
 __device__ __forceinline__ void store_codes(uint8_t* p, const float (&f)[VEC],
-                                            float inv) {
+                                            float inv, bool odd) {
   uint32_t w[VEC / 4];
 #pragma unroll
   for (int i = 0; i < VEC / 4; ++i) {
@@ -174,7 +175,8 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float (&f)[VEC],
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float x = f[4 * i + k];
-      t[k] = x == x ? x * inv : 0.f;  // a NaN is stored as 0
+      t[k] = x * inv;
+      if (odd && x != x) t[k] = 0.f;  // a NaN is stored as 0
     }
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(t[0], t[1]),
                                                  __NV_SATFINITE, __NV_E4M3);
@@ -232,16 +234,19 @@ __global__ void __launch_bounds__(kThreads, 3)
   const int tid = threadIdx.x, nt = blockDim.x;
   const int units = a.D / (2 * VEC);
   const int r2 = a.rot / 2;
-  if ((int)blockIdx.x >= a.cache_ctas) {
+  // The CTAs of both kinds alternate evenly, so that the rotation's traffic
+  // fills the waits of the cache's: of the first x, x share / 2^32 are the
+  // cache's (share: the part of 2^32, rounded up, that they are of the grid).
+  const uint32_t x = blockIdx.x, before = __umulhi(x, a.share);
+  if (a.rotates && __umulhi(x + 1, a.share) == before) {
     // ---- rotation of q ---------------------------------------------------
     const int groups = (a.Hq + kHeads - 1) / kHeads;
-    const int item = blockIdx.x - a.cache_ctas;
+    const int item = (int)(x - before);
     const int hg = item % groups;
-    const long long i = (long long)(item / groups) * nt + tid;
-    if (i >= (long long)a.B * a.Q * units) return;
-    const int u = (int)(i % units);
+    const int i = item / groups * nt + tid;
+    if (i >= a.B * a.Q * units) return;
+    const int u = i % units, b = i / units / a.Q, j = i / units - b * a.Q;
     const long long row = i / units;
-    const int b = (int)(row / a.Q), j = (int)(row - (long long)b * a.Q);
     int pos;
     bool bad;
     const bool live = j < live_tokens(a, b, &pos, &bad);
@@ -279,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     return;
   }
   // ---- one page and head of k or v ---------------------------------------
-  int item = blockIdx.x;
+  int item = a.rotates ? (int)before : (int)x;
   const int kv = item & 1;
   item >>= 1;
   const int h = item % a.Hkv;
@@ -298,10 +303,6 @@ __global__ void __launch_bounds__(kThreads, 3)
   const long long end = (long long)pos + n;
   if (start >= end) return;
   const int id = a.table[(size_t)b * a.max_pages + pg];
-  if (id < 0 || id >= a.num_pages) {
-    if (tid == 0) raise_error(a.err, kErrBadIndex);
-    return;
-  }
   const int first = pos > start ? (int)(pos - start) : 0;  // older tokens
   const int last = (int)(end - start < a.page ? end - start : a.page);
   const int work = (last - first) * units;
@@ -309,9 +310,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   const T* src = static_cast<const T*>(a.x[kv]) +
                  ((long long)b * a.Q + (start + first - pos)) * a.ld[kv] +
                  (size_t)h * a.D;
-  uint8_t* dst = a.codes[kv] + ((size_t)id * a.Hkv + h) * a.page * a.D;
-  float* scale = a.scale[kv] + (size_t)id * a.Hkv + h;
-
+  uint8_t* dst = nullptr;
   auto fetch = [&](int i, float (&x)[VEC], float (&y)[VEC]) {
     const int j = i / units, u = i - j * units;
     const Unit un = unit_at<VEC, kInter>(u, a.rot);
@@ -326,32 +325,36 @@ __global__ void __launch_bounds__(kThreads, 3)
       rotate<VEC, kInter>(x, y, c, s);
     }
   };
+  bool odd = false;  // a value of this thread's is not finite
   auto put = [&](int i, const float (&x)[VEC], const float (&y)[VEC],
                  float inv) {
     const int j = i / units, u = i - j * units;
     const Unit un = unit_at<VEC, kInter>(u, a.rot);
     uint8_t* p = dst + (size_t)(first + j) * a.D;
-    store_codes<VEC>(p + un.d0, x, inv);
-    store_codes<VEC>(p + un.d1, y, inv);
+    store_codes<VEC>(p + un.d0, x, inv, odd);
+    store_codes<VEC>(p + un.d1, y, inv, odd);
   };
-  float amax = 0.f;
-  bool odd = false;  // a value that is not finite
+  // the bits of a magnitude grow with it; infinity and NaN are the largest
+  uint32_t top = 0;
   auto fold = [&](const float (&x)[VEC]) {
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      const float m = fabsf(x[k]);
-      if (m < INFINITY) amax = fmaxf(amax, m);
-      else odd = true;
-    }
+    for (int k = 0; k < VEC; ++k)
+      top = max(top, __float_as_uint(x[k]) & 0x7fffffffu);
   };
-  float x[kKeep][VEC], y[kKeep][VEC];
+  float amax = 0.f;
+  auto fold_finite = [&](const float (&x)[VEC]) {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k)
+      if (fabsf(x[k]) < INFINITY) amax = fmaxf(amax, fabsf(x[k]));
+  };
+  float xs[kKeep][VEC], ys[kKeep][VEC];
 #pragma unroll
   for (int k = 0; k < kKeep; ++k) {
     const int i = tid + k * nt;
     if (i < work) {
-      fetch(i, x[k], y[k]);
-      fold(x[k]);
-      fold(y[k]);
+      fetch(i, xs[k], ys[k]);
+      fold(xs[k]);
+      fold(ys[k]);
     }
   }
   for (int i = tid + kKeep * nt; i < work; i += nt) {  // larger pages
@@ -360,9 +363,33 @@ __global__ void __launch_bounds__(kThreads, 3)
     fold(p);
     fold(r);
   }
+  if (top < 0x7f800000u) {
+    amax = __uint_as_float(top);
+  } else {
+    odd = true;
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k)
+      if (tid + k * nt < work) {
+        fold_finite(xs[k]);
+        fold_finite(ys[k]);
+      }
+    for (int i = tid + kKeep * nt; i < work; i += nt) {
+      float p[VEC], r[VEC];
+      fetch(i, p, r);
+      fold_finite(p);
+      fold_finite(r);
+    }
+  }
   __shared__ float s_max[kThreads / 32];
   amax = warp_max(amax);
   if ((tid & 31) == 0) s_max[tid >> 5] = amax;
+  // only now: the values travelled meanwhile
+  if (id < 0 || id >= a.num_pages) {  // uniform
+    if (tid == 0) raise_error(a.err, kErrBadIndex);
+    return;
+  }
+  dst = a.codes[kv] + ((size_t)id * a.Hkv + h) * a.page * a.D;
+  float* scale = a.scale[kv] + (size_t)id * a.Hkv + h;
   if (odd) raise_error(a.err, kErrNonfinite);
   const float was = first > 0 ? *scale : 0.f;
   __syncthreads();  // every thread has read the old scale, too
@@ -375,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
   for (int k = 0; k < kKeep; ++k) {
     const int i = tid + k * nt;
-    if (i < work) put(i, x[k], y[k], inv);
+    if (i < work) put(i, xs[k], ys[k], inv);
   }
   for (int i = tid + kKeep * nt; i < work; i += nt) {
     float p[VEC], r[VEC];
@@ -408,8 +435,13 @@ cudaError_t launch(const AppendArgs& a, bool inter, cudaStream_t s) {
   if (a.q)
     rot = (((long long)a.B * a.Q * units + nt - 1) / nt) *
           ((a.Hq + kHeads - 1) / kHeads);
-  if (cache + rot > 0x7fffffffll) return cudaErrorNotSupported;
-  args.cache_ctas = (int)cache;
+  if (cache + rot > 0x7fffffffll ||
+      (a.q && (long long)a.B * a.Q * units > 0x7fffffffll - kThreads))
+    return cudaErrorNotSupported;
+  // (cache + rot is below 2^31: the rounding up adds less than a half)
+  args.rotates = rot > 0;
+  args.share = (uint32_t)((((unsigned long long)cache << 32) + cache + rot - 1) /
+                          (unsigned long long)(cache + rot));
   PdlLaunch L(dim3((unsigned)(cache + rot)), dim3(nt), 0, s);
   return inter ? cudaLaunchKernelEx(&L.cfg, kv_append_kernel<T, VEC, true>, args)
                : cudaLaunchKernelEx(&L.cfg, kv_append_kernel<T, VEC, false>, args);
