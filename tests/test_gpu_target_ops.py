@@ -212,6 +212,43 @@ def test_append_non_finite_inputs(lib):
     assert np.all(rest == 0x78)
 
 
+@pytest.mark.parametrize("dtype,D,page,Q", [
+    ("fp32", 256, 128, 200), ("bf16", 256, 128, 131), ("bf16", 64, 16, 3)])
+def test_append_non_finite_anywhere(lib, dtype, D, page, Q):
+    """NaN and infinities at any token of a page, those a thread reads twice
+    among them: stored as 0 and the largest codes, no part of the scale."""
+    rng = np.random.default_rng(Q)
+    Hkv = 2
+    cache = Cache(np.array([Q]), page, Hkv, D, rng)
+    (kc, vc, ks, vs), table = cache.cuda()
+    x = [torch.from_numpy(rng.standard_normal((Q, Hkv, D)).astype(
+        np.float32)).to(DT[dtype]).float().numpy() for _ in range(2)]
+    clean, top = [a.copy() for a in x], []
+    for a, c in zip(x, clean):
+        for bad in (np.nan, np.inf, -np.inf):
+            a[rng.random(a.shape) < 0.003] = bad
+        a[-1, 0, -1] = np.nan
+        c[~np.isfinite(a)] = 0
+        top.append(np.isinf(a))
+    k, v = (torch.from_numpy(a).to(DT[dtype]).cuda() for a in x)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    lib.dflash_kv_append(None, k, v, None, None, i32(0), None, table, kc, vc,
+                         ks, vs, None, i32(0))
+    with pytest.raises(lib.DFlashError) as e:
+        lib.dflash_check()
+    assert e.value.status == 4
+    o = [c.copy() for c in cache.codes] + [s.copy() for s in cache.scale]
+    to.kv_append(None, clean[0][None], clean[1][None], None, None, [0], [Q],
+                 cache.table, page, *o)
+    for a, hit, want in zip(x, top, o[:2]):
+        for t, h, d in zip(*np.nonzero(hit)):
+            want[cache.table[0, t // page], h, t % page, d] = (
+                0x7E if a[t, h, d] > 0 else 0xFE)
+    assert np.array_equal(np_(kc), o[0]) and np.array_equal(np_(vc), o[1])
+    assert np.array_equal(np_(ks), o[2], equal_nan=True)
+    assert np.array_equal(np_(vs), o[3], equal_nan=True)
+
+
 # --------------------------------------------------------------------------
 # attention
 # --------------------------------------------------------------------------
