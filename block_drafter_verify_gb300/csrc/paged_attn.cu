@@ -17,6 +17,12 @@
 // lane = token, which reads its key's codes 16 at a time (the tile's lines
 // are used whole, over the steps); for the sum of values lane = four
 // dimensions, one line per token.  No tile passes through shared memory.
+//
+// What bounds it: the latency of the codes' loads and of each warp's chain of
+// fp32 products; 16 warps fit an SM.  fp32, heads of 128: one row of 60000
+// tokens and 8 key heads 184 us (123 MB), 60 such rows of 3000 tokens 473 us
+// (368 MB); without asking for the next tile's lines 230 us and 605 us.  32 x 9
+// queries of 4000 tokens, 36 rows a head: 1.8 ms.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -34,7 +40,7 @@ constexpr int kRows = 8;      // rows of a CTA
 constexpr int kTok = 32;      // tokens of a tile
 constexpr int kWarps = 8;
 constexpr int kMaxSplits = 32;
-constexpr int kTargetCtas = 456;  // three to an SM
+constexpr int kTargetCtas = 304;  // two to an SM
 
 // Parts each sequence is cut into, from the sizes the host knows.
 int simt_splits(long long B, long long Q, int Hq, int Hkv) {
@@ -64,10 +70,17 @@ __device__ __forceinline__ void decode16(const uint4& w, float s,
   }
 }
 
+__device__ __forceinline__ void prefetch(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 // W = words of four dimensions that a lane holds; with G = 2 the halves of a
 // warp take two tokens' values at a time (heads of up to 64 dimensions).
+// Two CTAs to an SM (128 registers): with three (80, some spilt) 32 x 9
+// queries of 4000 tokens take 1.5 instead of 1.9 ms, but 60 rows of 3000 683
+// instead of 605 us; heads of 256 with one 181 instead of 134 us.
 template <typename T, int W, int G>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, 2)
     paged_attn_simt_kernel(const __grid_constant__ PagedAttnArgs a, int splits,
                            int row_tiles, float* __restrict__ part) {
   extern __shared__ float4 smem4[];
@@ -124,9 +137,9 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
     for (int d = 0; d < 4 * W; ++d) o[r][d] = 0.f;
   }
-  for (int base = t0 + wid * kTok; base < t1; base += kWarps * kTok) {
-    // this lane's token: where its codes are, its scales
-    const int t = base + lane;
+  // The page of a lane's token is looked up, and its lines asked for, a tile
+  // ahead: they take longer than the tile.
+  auto page_of = [&](int t) {
     int id = -1;
     if (t < t1) {
       id = a.table[(size_t)b * a.max_pages + t / a.page];
@@ -135,6 +148,23 @@ __global__ void __launch_bounds__(kWarps * 32)
         id = -1;
       }
     }
+    return id;
+  };
+  auto ask = [&](int id, int t) {
+    if (id < 0) return;
+    const size_t at = (((size_t)id * a.Hkv + hk) * a.page + t % a.page) * D;
+    for (int d = 0; d < D; d += 128) {
+      prefetch(a.k_codes + at + d);
+      prefetch(a.v_codes + at + d);
+    }
+  };
+  const int t_first = t0 + wid * kTok + lane;
+  int id = page_of(t_first);
+  ask(id, t_first);
+  for (int base = t0 + wid * kTok; base < t1; base += kWarps * kTok) {
+    // this lane's token: where its codes are, its scales
+    const int t = base + lane;
+    const int next = page_of(t + kWarps * kTok);
     const size_t ph = id >= 0 ? (size_t)id * a.Hkv + hk : 0;
     const size_t at = (ph * a.page + t % a.page) * D;
     const float ks = id >= 0 ? a.k_scale[ph] : 0.f;
@@ -158,6 +188,7 @@ __global__ void __launch_bounds__(kWarps * 32)
         }
       }
     }
+    ask(next, t + kWarps * kTok);
     float w[kRows];  // this lane's token's weights, times its values' scale
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
@@ -204,6 +235,7 @@ __global__ void __launch_bounds__(kWarps * 32)
         for (int d = 0; d < 4 * W; ++d) o[r][d] = fmaf(wr, x[d], o[r][d]);
       }
     }
+    id = next;
   }
   // ---- the warps' sums ------------------------------------------------------
 #pragma unroll
@@ -281,15 +313,36 @@ __global__ void __launch_bounds__(128)
   const float l = warp_sum(w * li);
   const bool seen = l > 0.f || l != l;  // a NaN stays one
   const float inv = seen ? 1.f / l : 0.f;
-  for (int base = 0; base < D; base += 32) {  // whole warps shuffle
-    const int d = base + lane;
-    float o = 0.f;
-    for (int s = 0; s < splits; ++s) {
-      const float ws = __shfl_sync(0xffffffffu, w, s);
-      if (d < D && ws != 0.f)
-        o = fmaf(ws, part[((size_t)s * rows + row) * D + d], o);
+  constexpr int kAt = 8;  // parts on their way at once
+  for (int base = 0; base < D; base += 128) {  // whole warps shuffle
+    const int d = base + 4 * lane;  // D % 16 == 0
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < splits; s0 += kAt) {
+      float4 x[kAt];
+      float ws[kAt];
+#pragma unroll
+      for (int s = 0; s < kAt; ++s) {
+        ws[s] = __shfl_sync(0xffffffffu, w, s0 + s);  // 0 past the splits
+        x[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (d < D && ws[s] != 0.f)
+          x[s] = *reinterpret_cast<const float4*>(
+              part + ((size_t)(s0 + s) * rows + row) * D + d);
+      }
+#pragma unroll
+      for (int s = 0; s < kAt; ++s) {
+        o.x = fmaf(ws[s], x[s].x, o.x);
+        o.y = fmaf(ws[s], x[s].y, o.y);
+        o.z = fmaf(ws[s], x[s].z, o.z);
+        o.w = fmaf(ws[s], x[s].w, o.w);
+      }
     }
-    if (d < D) out[row * D + d] = from_f32<T>(o * inv);
+    if (d < D) {
+      T* to = out + row * D + d;
+      to[0] = from_f32<T>(o.x * inv);
+      to[1] = from_f32<T>(o.y * inv);
+      to[2] = from_f32<T>(o.z * inv);
+      to[3] = from_f32<T>(o.w * inv);
+    }
   }
   if (lane == 0 && lse) lse[row] = seen ? m + logf(l) : -INFINITY;
 }
