@@ -35,10 +35,10 @@
 //
 // What bounds it.  288 rows of 151936 fp32 logits, 26 us of HBM: T = 0 44 us,
 // top-k 50 61 us, no filter 74 us, top-k 1000 with top-p 88 us, top-p 0.9 of
-// 17000 tokens 196 us: instruction issue (about 20 for each token's maximum
-// and weight, 20 more for a bin, of the tokens that may be kept) and the
-// barriers of each row's chain, which other rows' CTAs hide in part.  A lone
-// row: 10 us, 13 us, 12 us, 20 us and 32 us, the chain alone.
+// 17000 tokens 196 us: the loads' latency (the second reading from L2 among
+// them) and the barriers of each row's chain, which other rows' CTAs hide in
+// part (issue slots are used to 30 to 55 %).  A lone row: 10 us, 13 us, 12 us,
+// 20 us and 32 us, the chain alone.
 #include <cooperative_groups.h>
 
 #include <algorithm>
