@@ -22,7 +22,7 @@
 // fp32 products; 16 warps fit an SM.  fp32, heads of 128: one row of 60000
 // tokens and 8 key heads 184 us (123 MB), 60 such rows of 3000 tokens 473 us
 // (368 MB); without asking for the next tile's lines 230 us and 605 us.  32 x 9
-// queries of 4000 tokens, 36 rows a head: 1.8 ms.
+// queries of 4000 tokens, 36 rows a head: 1.6 ms.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -76,11 +76,13 @@ __device__ __forceinline__ void prefetch(const void* p) {
 
 // W = words of four dimensions that a lane holds; with G = 2 the halves of a
 // warp take two tokens' values at a time (heads of up to 64 dimensions).
-// Two CTAs to an SM (128 registers): with three (80, some spilt) 32 x 9
-// queries of 4000 tokens take 1.5 instead of 1.9 ms, but 60 rows of 3000 683
-// instead of 605 us; heads of 256 with one 181 instead of 134 us.
-template <typename T, int W, int G>
-__global__ void __launch_bounds__(kWarps * 32, 2)
+// Two CTAs to an SM (128 registers).  Three (80, some spilt) where heads of 80
+// to 128 have full row tiles and sequences are not cut: 32 x 9 queries of 4000
+// tokens, 36 rows a head, 1.57 instead of 1.79 ms; cut sequences, four rows and
+// narrow heads lose (one row of 60000 tokens 267 instead of 223 us, 60 such
+// rows of 3000 683 instead of 605 us, D = 64 150 instead of 126 us).
+template <typename T, int W, int G, int kPerSm>
+__global__ void __launch_bounds__(kWarps * 32, kPerSm)
     paged_attn_simt_kernel(const __grid_constant__ PagedAttnArgs a, int splits,
                            int row_tiles, float* __restrict__ part) {
   extern __shared__ float4 smem4[];
@@ -355,7 +357,9 @@ cudaError_t launch_simt(const PagedAttnArgs& a, float* part, cudaStream_t s) {
   const long long ctas = (long long)a.B * a.Hkv * tiles * ns;
   if (ctas > 0x7fffffffll) return cudaErrorNotSupported;
   const size_t smem = (size_t)(1 + kWarps) * kRows * a.D * sizeof(float);
-  auto* f = paged_attn_simt_kernel<T, W, G>;
+  auto* f = paged_attn_simt_kernel<T, W, G, 2>;  // (the rule is the kernel's)
+  if constexpr (W == 1 && G == 1)
+    if (ns == 1 && a.Q * g >= kRows) f = paged_attn_simt_kernel<T, W, G, 3>;
   cudaError_t e = cudaFuncSetAttribute(
       f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
