@@ -518,6 +518,15 @@ __device__ int cut_in(Shared& S, const Row& r, int n, u64 hi, u64 lo,
       most = max(most, S.list[i]);
       least = min(least, S.list[kWarps + i]);
     }
+    if (most == least) {  // no finer slots part them (no two tokens' keys are
+      __syncthreads();    // equal: this bounds the loop whatever is there)
+      if (tid == 0) {
+        S.cut = most;
+        S.kept_before = w0;
+      }
+      __syncthreads();
+      return 2;
+    }
     at = Slots(most, least);
   }
 }
@@ -911,7 +920,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
   }
 
   // The tokens from `low` up as candidates, cut and drawn from by the first
-  // CTA; false if they are too many.
+  // CTA; false if they are too many.  At most once a row: neither the places
+  // that collect() gave out nor the quarters of from() are taken back.
   auto finish = [&](float low, int most, u64 bound) {
     from(low, [&](int i, float l) {
       const uint32_t at = atomicAdd(&S.listed, 1u);
@@ -1199,8 +1209,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
       return S.found_bin;
     };
     int bin = find(0.5f, 0.f);
-    if (!have_total && bin >= 0 &&
-        S.found_n + S.all_count[bin] <= kOwn * 3 / 4) {
+    // (with a top-k, whose tokens finish() may have listed already: no second
+    // time)
+    if (!by_k && bin >= 0 && S.found_n + S.all_count[bin] <= kOwn * 3 / 4) {
       __syncthreads();
       const int last = find(1.f, -1e-4f);  // from below: the cut is not past it
       if (last >= 0 && S.found_n + S.all_count[last] <= kOwn * 7 / 8) {
