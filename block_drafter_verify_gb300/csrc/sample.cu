@@ -200,18 +200,30 @@ __device__ __forceinline__ int bin_of(float l, const Row& r) {
   return z < (float)(kBins - 1) ? (int)z : kBins - 1;
 }
 
+// The three bounds below are differences from the maximum.  Under an infinite
+// one there are its own tokens, in bin 0, and all others, weightless and in the
+// last bin; the bounds are then these tokens' own logits.
+
 // A logit below all of bins 0 .. bin (-inf after the last): z is less than
 // (bin + 1) / kBinsPerUnit there, with room for its roundings.
 __device__ __forceinline__ float bin_floor(int bin, const Row& r, float t) {
   if (bin >= kBins - 1) return -INFINITY;
+  if (r.top == INFINITY) return r.top;
   const float z = (float)(bin + 1) / kBinsPerUnit;
   return r.top - z * t * 1.0001f - fabsf(r.top) * 1e-6f;
 }
 
 // A logit above all of bins bin, bin + 1, ...
 __device__ __forceinline__ float bin_ceil(int bin, const Row& r, float t) {
+  if (r.top == INFINITY) return bin > 0 ? 0x1.fffffep127f : r.top;
   const float z = (float)bin / kBinsPerUnit;
   return r.top - z * t * 0.9999f + fabsf(r.top) * 1e-6f;
+}
+
+// A logit below all that weigh x or more (0 < x <= 1).
+__device__ __forceinline__ float weight_floor(float x, const Row& r, float t) {
+  if (r.top == INFINITY) return r.top;
+  return r.top + logf(x) * t * 1.0001f - fabsf(r.top) * 1e-6f;
 }
 
 __device__ __forceinline__ void add_weight(Shared& S, int bin, u64 w) {
@@ -686,6 +698,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
   if (tid == 0) {
     S.odd = S.fine = 0;
     S.kept_n = 0;
+    S.cut = 0;
     S.listed = S.n_quarters = 0;
     for (int i = 0; i < kCollects; ++i) S.row_listed[i] = 0;
     S.first = 0x7fffffff;
@@ -985,8 +998,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
   // ---- the cut by counts in bins ----------------------------------------------
   const bool by_m = mp > 0.f;
   const float low_m =  // no token kept by min-p is below
-      by_m ? r.top + logf(mp) * t * 1.0001f - fabsf(r.top) * 1e-6f
-           : -INFINITY;
+      by_m ? weight_floor(mp, r, t) : -INFINITY;
   // min-p alone: its tokens, if they are few, are candidates of no other bound
   if (by_m && !by_k && !by_p && finish(low_m, kCand, ~0ull)) return;
   u64 cut = 0;
@@ -1167,12 +1179,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
       __syncthreads();
     }
     const float share = 0.9f * (1.f - p) / (float)a.V;
-    auto logit_of = [&](float x) {  // a little below
-      return x > 0.f && x < 1.f
-                 ? r.top + logf(x) * t * 1.0001f - fabsf(r.top) * 1e-6f
-                 : -INFINITY;
-    };
-    const float low = fmaxf(logit_of(share * fmaxf(sum, 1.f)), low_m);
+    const float least_x = share * fmaxf(sum, 1.f);
+    const float low =
+        fmaxf(least_x > 0.f && least_x < 1.f ? weight_floor(least_x, r, t)
+                                             : -INFINITY, low_m);
     const int bins =
         share > 0.f
             ? min(kBins, (int)(-logf(share) * kBinsPerUnit * 1.001f) + 3)

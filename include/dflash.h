@@ -631,7 +631,7 @@ size_t dflash_sample_workspace_bytes(int R, int V);
  *   filtered [R, V] fp32 out or NULL: l_v if kept, else -inf
  *   ws >= dflash_sample_workspace_bytes(R, V) bytes, 256-byte aligned
  * Requirements: R >= 1, 1 <= V < 2^20 (their weights add up in 64 bits),
- * ld >= V.  A NaN (left out) or +inf logit
+ * ld >= V.  A NaN (left out) or +inf logit (weight 1, every other token's 0)
  * sets DFLASH_ERR_NONFINITE, as does a row with no logit above -inf (token
  * -1, n_kept 0) or a T that is negative or not finite (taken as 0).
  */

@@ -137,7 +137,9 @@ def sample_row(l, T, k=0, p=1.0, m=0.0, u=0.0):
         kept[order[0]] = True
         return int(order[0]), kept, np.inf, np.inf
     inv = np.float32(1) / np.float32(T)
-    x = np.exp((l - l.max()) * np.float64(inv))
+    # (an infinite maximum weighs 1, everything else beside it 0)
+    x = np.exp(np.subtract(l, l.max(), out=np.zeros(V), where=l != l.max()) *
+               np.float64(inv))
     if 0 < k < V:
         order = order[:k]
     w = np.floor(x[order] * WEIGHT_ONE)

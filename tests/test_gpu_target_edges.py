@@ -37,3 +37,32 @@ def test_sample_fewer_unmasked_tokens_than_k(lib, R, V, first, n, p, m):
                   [p] * len(rows), [m] * len(rows), u[rows],
                   [g[rows] for g in got])
     assert np.all(np.isin(got[0], at)) and np.all(got[1] == got[1][0])
+
+
+@pytest.mark.parametrize("R", [1, 300])
+@pytest.mark.parametrize("count", [1, 2])
+@pytest.mark.parametrize("V", [300, 50000])
+@pytest.mark.parametrize("k,p,m", [
+    (0, 1.0, 0.0), (1, 1.0, 0.0), (5, 1.0, 0.0), (1000, 1.0, 0.0),
+    (0, 0.9, 0.0), (0, 0.4, 0.0), (0, 1.0, 0.1), (0, 1.0, 1.0),
+    (5, 0.9, 0.1), (0, 0.9, 0.1)])
+def test_sample_infinite_logit(lib, R, count, V, k, p, m):
+    """An infinite logit weighs 1, every other token 0: flagged, and the
+    definition's token, kept set and filtered logits all the same."""
+    rng = np.random.default_rng(V + count)
+    l = (2.5 * rng.standard_normal((1, V))).astype(np.float32)
+    at = rng.choice(V, count, replace=False)
+    l[0, at] = np.inf
+    l = np.repeat(l, R, 0)
+    for T in (0.7, 0.0):
+        u = rng.random(R).astype(np.float32)
+        got = _run_sample(lib, torch.from_numpy(l).cuda(), [T] * R, [k] * R,
+                          [p] * R, [m] * R, u)
+        with pytest.raises(lib.DFlashError) as e:
+            lib.dflash_check()
+        assert e.value.status == 4
+        assert np.all(np.isin(got[0], at))
+        rows = [0] if R == 1 else [0, 1, 150, R - 1]
+        _check_sample(l[rows], [T] * len(rows), [k] * len(rows),
+                      [p] * len(rows), [m] * len(rows), u[rows],
+                      [g[rows] for g in got])
