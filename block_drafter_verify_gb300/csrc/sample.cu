@@ -66,6 +66,10 @@ constexpr int kCand = 2048;            // candidates, over the cluster
 constexpr int kOwn = 1536;             // of one CTA
 constexpr int kOwnBound = 128;         // largest k for a bound of each CTA
 constexpr int kChunks = 4;             // copies of a slice
+// Weights whose halves a thread adds up in 32 bits: 512 halves of 23 bits fit.
+// In a block of this many tokens to a thread, each() gives it one more where
+// the last word is not full.
+constexpr int kBlock = 504;            // (words of eight)
 constexpr uint64_t kWait = 2000000000ull;  // 2 s
 constexpr int kCandBins = 512;         // bins of 1/16 for a bound of them
 constexpr int kList = 256;             // members of one bin
@@ -1012,9 +1016,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     __syncthreads();
     u64 sum = 0;
     if (!S.odd && r.inv_t < INFINITY) {  // as in the sum of all weights below
-      for (int b = 0; b < n; b += kThreads * 512) {
+      for (int b = 0; b < n; b += kThreads * kBlock) {
         uint32_t hi = 0, lo = 0, m = 0;
-        each(data, wide, b, min(n, b + kThreads * 512), tid, kThreads,
+        each(data, wide, b, min(n, b + kThreads * kBlock), tid, kThreads,
              [&](int, float l) {
                const float z = __fmul_rn(__fsub_rn(l, r.top), r.inv_t);
                const WeightBits w = weight_bits(expf(z));
@@ -1079,9 +1083,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     warp_chunk(n, wid, &c0, &c1);
     u64 sum = 0;
     uint32_t cnt = 0;
-    for (int b = c0; b < c1; b += 32 * 512) {  // as in the sum of all weights
+    for (int b = c0; b < c1; b += 32 * kBlock) {  // as in all weights' sum
       uint32_t w_hi = 0, w_lo = 0, m = 0;
-      each(data, wide, b, min(c1, b + 32 * 512), lane, 32,
+      each(data, wide, b, min(c1, b + 32 * kBlock), lane, 32,
            [&](int i, float l) {
              const bool on = l > hi;
              const WeightBits w = weight_bits(on ? x_of(l, r) : 0.f);
@@ -1279,11 +1283,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
         cnt += on;
       });
     } else {
-      // All weights are wanted and all logits finite.  The halves of up to
-      // 512 weights fit 32 bits each; the 0x4b000000 of every float comes
-      // off at the end.
-      for (int b = c0; b < c1; b += 32 * 512) {
-        const int e = min(c1, b + 32 * 512);
+      // All weights are wanted and all logits finite.  The 0x4b000000 of
+      // every float comes off at the end.
+      for (int b = c0; b < c1; b += 32 * kBlock) {
+        const int e = min(c1, b + 32 * kBlock);
         uint32_t hi = 0, lo = 0, m = 0;
         each(data, wide, b, e, lane, 32, [&](int, float l) {
           const WeightBits w = weight_bits(x_plain(l, r));

@@ -66,3 +66,47 @@ def test_sample_infinite_logit(lib, R, count, V, k, p, m):
         _check_sample(l[rows], [T] * len(rows), [k] * len(rows),
                       [p] * len(rows), [m] * len(rows), u[rows],
                       [g[rows] for g in got])
+
+
+def _ones_below():
+    """A logit whose weight against a maximum of 0 ends in (nearly) 23 ones,
+    and that weight: 513 of its low halves exceed 32 bits."""
+    d = torch.linspace(-6.0, -4.5, 1 << 18, device="cuda")
+    w = (torch.exp(d).double() * 2.0 ** 44).long()
+    low = w & ((1 << 23) - 1)
+    i = int(low.argmax())
+    assert 513 * int(low[i]) >= 1 << 32
+    return float(d[i]), int(w[i])
+
+
+def test_sample_sums_of_full_low_halves(lib):
+    """All tokens but the first tie at a weight whose low half is nearly all
+    ones, in rows of one CTA whose last block is one token short: sums of 512
+    and one tokens to a thread.  Integer sums are exact, so uniforms and
+    nuclei next to a boundary decide as the integers do."""
+    R, V = 609, (1 << 18) - 1                  # one CTA to a row
+    d, w = _ones_below()
+    big = torch.full((R, V + 1), d, device="cuda")
+    big[:, 0] = 0.0
+    x = big[:, :V]                             # rows aligned to 16 bytes
+    one, total = 1 << 44, (1 << 44) + (V - 1) * w
+    # uniforms (and nuclei) whose target lies less than 2^32 above the first
+    # weight of a token, so that a lost carry would show
+    f = np.arange(1 << 23, 1 << 24).astype(np.float64) / (1 << 24)
+    t = np.floor(f * float(total)).astype(np.int64)
+    near = f[(t - one) % w < 1 << 32]
+    assert near.size >= 2 * R
+    pick = near[np.linspace(0, near.size - 1, R).astype(int)]
+    u = pick.astype(np.float32)
+    tok, nk, _ = _run_sample(lib, x, [1.0] * R, None, None, None, u, False)
+    lib.dflash_check()
+    t = np.floor(pick * float(total)).astype(np.int64)
+    assert np.array_equal(tok, 1 + (t - one) // w)
+    assert np.all(nk == V)
+    tok, nk, _ = _run_sample(lib, x, [1.0] * R, None, u, None, [0.0] * R,
+                             False)
+    lib.dflash_check()
+    need = np.ceil(pick * float(total)).astype(np.int64)
+    # the first token, then as many as have less than `need` before them
+    assert np.array_equal(nk, 1 + -(-(need - one) // w))
+    assert np.all(tok == 0)
