@@ -296,6 +296,8 @@ dflash_status current_device_info(int* sms, int** err) {
   return DFLASH_OK;
 }
 
+uint64_t wait_limit_ns() { return g_wait_ns.load(); }
+
 // The checks dflash_verify and dflash_verify_noalloc share (everything but
 // the scratch memory): pointers, sizes, temperature, alignment.
 bool verify_args_ok(const float* target_logits, const int32_t* draft,

@@ -12,8 +12,9 @@ namespace dflash {
 
 // Default limit of the tensor-core kernels' bounded waits (2 s, far beyond
 // any real wait); dflash_set_wait_limit_ns changes it for later launches of
-// the conv and of the single-CTA LM head.
+// the conv, of the single-CTA LM head and of the sampling.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
+uint64_t wait_limit_ns();  // the present one (api.cu)
 
 // conv.cu -----------------------------------------------------------------
 template <typename T>

@@ -70,7 +70,6 @@ constexpr int kChunks = 4;             // copies of a slice
 // In a block of this many tokens to a thread, each() gives it one more where
 // the last word is not full.
 constexpr int kBlock = 504;            // (words of eight)
-constexpr uint64_t kWait = 2000000000ull;  // 2 s
 constexpr int kCandBins = 512;         // bins of 1/16 for a bound of them
 constexpr int kList = 256;             // members of one bin
 constexpr int kCollects = 5;           // lists that a row may gather
@@ -88,6 +87,7 @@ struct SampleArgs {
   int* n_kept;
   float* filtered;
   int* err;
+  uint64_t wait_ns;  // limit of the waits for the slice's copies
 };
 
 // Order-preserving key of a logit (equal for -0 and 0); 0 is below -inf.
@@ -112,7 +112,7 @@ __device__ __forceinline__ U warp_total(U v) {
 }
 struct Shared {
   // written by this CTA, read by the cluster
-  float top;             // largest logit of the slice
+  float top;             // largest logit of the slice; NaN: it did not come
   int first;             // T = 0: first token of the slice that has it
   u64 total;             // weight of the slice
   u64 top_w;             // and of its tokens in the first kTopBins bins
@@ -121,6 +121,7 @@ struct Shared {
   uint32_t kept_n;
   uint32_t odd;          // a logit of the slice is not finite
   uint32_t fine;         // one has more bits than bf16
+  uint32_t late;         // a copy of the slice did not come in time
   uint32_t lists[kCollects][kMaxCluster];  // lengths of every CTA's lists
   uint32_t row_listed[kCollects];  // the first CTA's: places taken in all_cand
   uint64_t landed[kChunks];  // barriers of the slice's copies
@@ -700,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
 
   // ---- the slice and the row's maximum -------------------------------------
   if (tid == 0) {
-    S.odd = S.fine = 0;
+    S.odd = S.fine = S.late = 0;
     S.kept_n = 0;
     S.cut = 0;
     S.listed = S.n_quarters = 0;
@@ -761,8 +762,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     int give_up = 0;
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-      if (!tc::mbar_wait_bounded(&S.landed[c], 0, &give_up, kWait))
-        raise_error(a.err, kErrTimeout);
+      if (!tc::mbar_wait_bounded(&S.landed[c], 0, &give_up, a.wait_ns)) {
+        // The row is given up, but not while a copy is in flight.
+        S.late = 1;
+        int never = 0;
+        tc::mbar_wait_bounded(&S.landed[c], 0, &never, kWaitLimitNs);
+      }
       const int v1 = min(words, (c + 1) * per);
 #pragma unroll 4
       for (int v = min(words, c * per) + tid; v < v1; v += kThreads) {
@@ -812,10 +817,22 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
   if (tid == 0) {
     for (int i = 1; i < kWarps; ++i)
       top = fmaxf(top, __uint_as_float((uint32_t)S.warp_w[i]));
+    if (S.late) {
+      raise_error(a.err, kErrTimeout);
+      top = NAN;
+    }
     S.top = top;
   }
   cl.sync();
   top = lane < C ? cl.map_shared_rank(&S, lane)->top : -INFINITY;
+  if (__any_sync(0xffffffffu, top != top)) {  // uniform over the cluster
+    if (rank == 0 && tid == 0) {
+      a.token[row] = -1;
+      if (a.n_kept) a.n_kept[row] = 0;
+    }
+    cl.sync();  // no CTA leaves while another reads its maximum
+    return;
+  }
   top = warp_max(top);
 
   Row r;
@@ -1473,6 +1490,7 @@ dflash_status dflash_sample(const void* logits, int64_t ld, dflash_dtype dt,
   a.token = token;
   a.n_kept = n_kept;
   a.filtered = filtered;
+  a.wait_ns = wait_limit_ns();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = dt == DFLASH_FP32 ? launch<float>(a, s)
                                           : launch<__nv_bfloat16>(a, s);

@@ -110,3 +110,32 @@ def test_sample_sums_of_full_low_halves(lib):
     # the first token, then as many as have less than `need` before them
     assert np.array_equal(nk, 1 + -(-(need - one) // w))
     assert np.all(tok == 0)
+
+
+def test_sample_gives_up_on_a_copy_and_recovers(lib):
+    """So many slices are copied at once that some outlast a limit of a
+    nanosecond: flagged, no token for their rows, and the next call is
+    right."""
+    R, V = 4000, 9000
+    rng = np.random.default_rng(3)
+    l = np.repeat((2.5 * rng.standard_normal((1, V))).astype(np.float32), R, 0)
+    x = torch.from_numpy(l).cuda()
+    u = rng.random(R).astype(np.float32)
+    args = ([1.0] * R, [50] * R, [0.9] * R, None, u)
+    lib.dflash_check()                         # nothing pending
+    try:
+        lib.dflash_set_wait_limit_ns(1)
+        torch.empty(1 << 28, dtype=torch.uint8, device="cuda").zero_()
+        tok, nk, _ = _run_sample(lib, x, *args, filtered=False)
+        with pytest.raises(lib.DFlashError) as e:
+            lib.dflash_check()
+        assert e.value.status == 5             # DFLASH_ERR_DEVICE_TIMEOUT
+    finally:
+        lib.dflash_set_wait_limit_ns(0)        # back to the default (2 s)
+    late = tok == -1
+    assert late.any() and np.all(nk[late] == 0)
+    got = _run_sample(lib, x, *args, filtered=False)
+    lib.dflash_check()
+    rows = [0, 1, R // 2, R - 1]
+    _check_sample(l[rows], *([a[0]] * 4 for a in args[:3]), None, u[rows],
+                  [None if g is None else g[rows] for g in got])
