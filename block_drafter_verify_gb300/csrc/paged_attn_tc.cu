@@ -58,6 +58,14 @@ constexpr int kStages = 7;         // most stages of K or V tiles
 constexpr uint64_t kWait = 2000000000ull;  // 2 s
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kHead = 10.f;      // weights are 2^(score - ref + kHead)
+// A row's sum counts its weights without their value scales (2^lv), times
+// 2^kSumRef: with scales from 2^kLeastLv to 2^kMostLv and 2^30 tokens it stays
+// between 2^-95 and 2^126, whichever of them the reference has come from.
+constexpr float kSumRef = 16.f;
+constexpr float kLeastLv = -64.f, kMostLv = 120.f;
+// Weights of pages whose value scale is that much (in bits) below the largest
+// of the run so far may underflow: their terms of the sum are computed apart.
+constexpr float kFarLv = 90.f;
 constexpr float kRaise = 15.75f;   // 2^15.75 = 55109 < 57344, E5M2's largest
 constexpr int kUnitCost = 4;       // of a unit besides its tiles, in tiles
 constexpr int kParts = 4;          // E5M2 parts of a weight
@@ -110,7 +118,8 @@ struct Meta {
   alignas(16) float neg_ref[kMaxRows], fac[kMaxRows];
   float q_top[2];
   alignas(16) float warp_val[4][kMaxRows];
-  float ct[kStages][8], lv[kStages][8];  // of a page: key factor, log2 scale
+  // of a page: key factor, log2 of the value scale, 2^(kSumRef - that) or 0
+  float ct[kStages][8], lv[kStages][8], fl[kStages][8];
   uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
   uint64_t sfull[2], pfull[2], qfull[2], qempty[2], qfree;
   uint64_t drain;
@@ -570,6 +579,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
                    ? s[(size_t)pid * a.Hkv + p.hk]
                    : 1.f;
       };
+      float top_lv = -INFINITY;            // of the pages so far
       float ks = load_scale(a.k_scale, id), vs = load_scale(a.v_scale, id);
       float ks1 = load_scale(a.k_scale, id1), vs1 = load_scale(a.v_scale, id1);
       for (int t = p.t0; t < p.t1; ++t) {
@@ -609,9 +619,13 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
                           &m.vfull[rv.at], 0, row);
         const float pk = __shfl_sync(0xffffffffu, ks, from & 31);
         const float pv = __shfl_sync(0xffffffffu, vs, from & 31);
+        const float lv = fminf(fmaxf(log2f(pv), kLeastLv), kMostLv);
+        top_lv = fmaxf(top_lv, warp_top(have ? lv : -INFINITY));
         if (lane < pt) {
           m.ct[rv.at][lane] = have && !bad ? pk * c : 0.f;
-          m.lv[rv.at][lane] = have ? log2f(fmaxf(pv, 0x1p-100f)) : 0.f;
+          m.lv[rv.at][lane] = have ? lv : 0.f;
+          m.fl[rv.at][lane] =
+              lv < top_lv - kFarLv ? 0.f : tc::ex2_approx(kSumRef - lv);
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&m.vfull[rv.at]);
@@ -944,7 +958,6 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
       // kHead - reference; 0 before the first tile
       if (ht < HR) m.neg_ref[my_row] = 0.f;
       half_sync(bar);
-      float lv_ref = 0.f;
       // The scores of buffer `at` into y: asked for by ask(), there after
       // got().  With more than 32 rows the softmax sets the pace, and the
       // next tile's scores, if ready, are asked for while this tile's weights
@@ -993,8 +1006,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
         }
         const int pg = tok >> page_bits;
         const float ct = m.ct[st][pg] * back, lv = m.lv[st][pg];
-        if (t == 0) lv_ref = m.lv[st][0];
-        const float fl = tc::ex2_approx(fminf(lv_ref - lv, 100.f));
+        const float fl = m.fl[st][pg];
         if (uneven) {
 #pragma unroll
           for (int r = 0; r < HR; ++r) y[r] *= g.rel[row_of(r & ~3) + (r & 3)];
@@ -1050,14 +1062,21 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
           for (int r = 0; r < HR; r += 4) {
             const float4 d =
                 *reinterpret_cast<const float4*>(&m.fac[row_of(r)]);
-            const float f[4] = {tc::ex2_approx(d.x), tc::ex2_approx(d.y),
-                                tc::ex2_approx(d.z), tc::ex2_approx(d.w)};
-            y[r] += d.x;
-            y[r + 1] += d.y;
-            y[r + 2] += d.z;
-            y[r + 3] += d.w;
-            l[r / 2] = mul2(l[r / 2], pack2(f[0], f[1]));
-            l[r / 2 + 1] = mul2(l[r / 2 + 1], pack2(f[2], f[3]));
+            // in two factors: the sums may hold what the weights do not
+            const float e[4] = {d.x, d.y, d.z, d.w};
+            float f[4], f2[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              y[r + k] += e[k];
+              f[k] = tc::ex2_approx(fmaxf(e[k], -100.f));
+              f2[k] = tc::ex2_approx(fminf(e[k] + 100.f, 0.f));
+            }
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+              uint64_t& lr = l[(r + k) / 2];
+              lr = mul2(mul2(lr, pack2(f[k], f[k + 1])),
+                        pack2(f2[k], f2[k + 1]));
+            }
             const bool one = d.x == 0.f && d.y == 0.f && d.z == 0.f &&
                              d.w == 0.f;
             if (t > 0 && !one && ok) {
@@ -1067,7 +1086,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
                 tmem_ld4(o_col + h * N + row_of(r), o);
                 tmem_loaded(o);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[k] *= f[k];
+                for (int k = 0; k < 4; ++k) o[k] *= f[k] * f2[k];
                 tmem_st4(o_col + h * N + row_of(r), o);
               }
             }
@@ -1076,6 +1095,13 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
             tmem_stored();
             tc::fence_before_sync();
           }
+        }
+        if (fl == 0.f) {
+#pragma unroll
+          for (int r = 0; r < HR; r += 2)
+            l[r / 2] = add2(l[r / 2],
+                            pack2(tc::ex2_approx(y[r] + (kSumRef - lv)),
+                                  tc::ex2_approx(y[r + 1] + (kSumRef - lv))));
         }
         // ---- the weights, in parts -----------------------------------------
         const int p_buf = sb * kParts * N * 128;
@@ -1159,25 +1185,29 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
         }
       }
       half_sync(bar);
-      const float lift = exp2f(lv_ref);
       if (ht < HR) {
         const int r = my_row;
         const float sum = (m.warp_val[0][r] + m.warp_val[1][r]) +
                           (m.warp_val[2][r] + m.warp_val[3][r]);
-        const float ref = -m.neg_ref[r] - lv_ref;   // log2 of what sum counts
         const bool seen = sum > 0.f || sum != sum;  // a NaN stays one
+        // sum = frac 2^ex; 2^ref: what frac counts.  (Parts of runs whose
+        // value scales lie far apart join by that.)
+        const int ex =
+            min(max((int)(__float_as_uint(sum) >> 23) - 127, -100), 120);
+        const float frac = sum * __uint_as_float((127 - ex) << 23);
+        const float ref = (float)ex - m.neg_ref[r] - kSumRef;
         if (whole) {
           const bool on = seen && g.on[r];
-          m.fac[r] = on ? lift / sum : 0.f;
+          m.fac[r] = on ? exp2f(kSumRef) / sum : 0.f;
           if (!dry && g.out_row[r] >= 0 && a.lse)
             a.lse[g.out_row[r]] =
-                on ? (log2f(sum) + ref) * 0.6931471805599453f : -INFINITY;
+                on ? (log2f(frac) + ref) * 0.6931471805599453f : -INFINITY;
         } else {
-          m.fac[r] = lift;
+          m.fac[r] = __uint_as_float((127 + (int)kSumRef - ex) << 23);
           float2* ml = reinterpret_cast<float2*>(
               part + (size_t)2 * gridDim.x * N * 128);
           ml[(size_t)g.slot * N + r] =
-              make_float2(seen ? ref : -INFINITY, seen ? sum : 0.f);
+              make_float2(seen ? ref : -INFINITY, seen ? frac : 0.f);
         }
       }
       half_sync(bar);

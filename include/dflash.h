@@ -590,7 +590,7 @@ size_t dflash_paged_attn_workspace_bytes(int B, int Q, int Hq, int Hkv, int D);
  * largest value), the softmax weights as the sum of four E5M2 numbers (to
  * 2^-13); sums and statistics in fp32.  Otherwise fp32 on the CUDA cores.
  * Codes and slots past kv_len may hold anything.  Scales are powers of two
- * between 2^-100 and 2^120, as dflash_kv_append writes them.
+ * between 2^-64 and 2^120, as dflash_kv_append writes them.
  * Requirements: Hq % Hkv == 0, Hq / Hkv <= 64, q, out and the codes 16-byte
  * aligned; scale finite; fewer than 2^31 tiles of 128 tokens over all
  * sequences' page tables and key heads (with bf16).  On the device: kv_len below 0 or beyond the page

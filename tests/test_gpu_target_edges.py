@@ -5,7 +5,10 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_target_ops import _check_sample, _run_sample
+import oracle
+from oracle import target_ops as to
+from test_gpu_target_ops import (DT, Cache, _attend, _check_attn,
+                                 _check_sample, _run_sample)
 
 pytestmark = pytest.mark.gpu
 
@@ -139,3 +142,49 @@ def test_sample_gives_up_on_a_copy_and_recovers(lib):
     rows = [0, 1, R // 2, R - 1]
     _check_sample(l[rows], *([a[0]] * 4 for a in args[:3]), None, u[rows],
                   [None if g is None else g[rows] for g in got])
+
+
+# --------------------------------------------------------------------------
+# attention
+# --------------------------------------------------------------------------
+SCALES = [(-64, 63), (-64, 120), (63, -64), (120, -64), (100, -20),
+          (-10, 90), (2, 2)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16"])
+@pytest.mark.parametrize("first,rest", SCALES)
+@pytest.mark.parametrize("zero", [True, False])
+@pytest.mark.parametrize("g,n,B", [(4, 500, 1), (36, 700, 1), (4, 20000, 1),
+                                   (20, 1500, 90)])
+@pytest.mark.parametrize("scale", [0.02, 3.0])
+def test_attention_value_scales_over_their_range(lib, dtype, first, rest,
+                                                 zero, g, n, B, scale):
+    """Pages whose values lie up to 2^184 apart, among them pages of zeros
+    (which carry the smallest scale), first or later, in runs that hold
+    whole sequences and in parts that are joined: a token's share of the
+    softmax's sum does not depend on its value."""
+    rng = np.random.default_rng(g + n)
+    D, page = 64, 32
+    cache = Cache([n], page, 1, D, rng, spread=0)
+    ids = cache.table[0]
+    # values of at most 2^7 times a scale of 2^120: bf16 holds them
+    cache.codes[1][:] = oracle.e4m3_encode(
+        (rng.standard_normal(cache.codes[1].shape) * 8).astype(np.float32))
+    cut = len(ids) // 3
+    cache.scale[1][ids[:cut]] = 2.0 ** first
+    cache.scale[1][ids[cut:]] = 2.0 ** rest
+    cache.scale[1][ids[-2]] = 2.0 ** first     # and a late one
+    if zero:
+        small = ids[cache.scale[1][ids, 0] == 2.0 ** min(first, rest)]
+        cache.codes[1][small] = 0
+    q = torch.tensor(rng.standard_normal((1, 1, g, D)) * 2,
+                     dtype=torch.float32).to(DT[dtype]).cuda()
+    ref = to.paged_attn(q.float().cpu().numpy().astype(np.float64),
+                        *cache.codes, *cache.scale, cache.table, [n], [1],
+                        scale)
+    cache.table = np.repeat(cache.table, B, 0)
+    out, lse = _attend(lib, dtype, cache, q.repeat(B, 1, 1, 1), [n] * B,
+                       None, True, scale)
+    lib.dflash_check()
+    for b in {0, B // 2, B - 1}:
+        _check_attn(dtype, D, n, out[b:b + 1], lse[b:b + 1], ref)
