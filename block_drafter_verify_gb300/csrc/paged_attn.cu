@@ -40,6 +40,9 @@ constexpr int kRows = 8;      // rows of a CTA
 constexpr int kTok = 32;      // tokens of a tile
 constexpr int kWarps = 8;
 constexpr int kMaxSplits = 32;
+// Values are added up times 2^-32, exactly: of the largest scale (2^120) some
+// hundred would pass fp32's range before they are divided by their weights.
+constexpr float kDown = 0x1p-32f, kUp = 0x1p32f;
 constexpr int kTargetCtas = 304;  // two to an SM
 
 // Parts each sequence is cut into, from the sizes the host knows.
@@ -170,7 +173,7 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm)
     const size_t ph = id >= 0 ? (size_t)id * a.Hkv + hk : 0;
     const size_t at = (ph * a.page + t % a.page) * D;
     const float ks = id >= 0 ? a.k_scale[ph] : 0.f;
-    const float vs = id >= 0 ? a.v_scale[ph] : 0.f;
+    const float vs = id >= 0 ? a.v_scale[ph] * kDown : 0.f;
     float s[kRows] = {};
 #pragma unroll 2
     for (int d = 0; d < D; d += 16) {
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm)
     const bool seen = sum > 0.f || sum != sum;  // a NaN stays one
     if (splits == 1) {
       static_cast<T*>(a.out)[row * D + d] =
-          from_f32<T>(seen ? acc / sum : 0.f);
+          from_f32<T>(seen ? acc / sum * kUp : 0.f);
       if (d == 0 && a.lse) a.lse[row] = seen ? top + logf(sum) : -INFINITY;
     } else {
       part[((size_t)sp * rows + row) * D + d] = acc;
@@ -314,7 +317,7 @@ __global__ void __launch_bounds__(128)
   const float w = mi == -INFINITY ? 0.f : expf(mi - m);
   const float l = warp_sum(w * li);
   const bool seen = l > 0.f || l != l;  // a NaN stays one
-  const float inv = seen ? 1.f / l : 0.f;
+  const float inv = seen ? kUp / l : 0.f;
   constexpr int kAt = 8;  // parts on their way at once
   for (int base = 0; base < D; base += 128) {  // whole warps shuffle
     const int d = base + 4 * lane;  // D % 16 == 0

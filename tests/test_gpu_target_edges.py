@@ -151,7 +151,7 @@ SCALES = [(-64, 63), (-64, 120), (63, -64), (120, -64), (100, -20),
           (-10, 90), (2, 2)]
 
 
-@pytest.mark.parametrize("dtype", ["bf16"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("first,rest", SCALES)
 @pytest.mark.parametrize("zero", [True, False])
 @pytest.mark.parametrize("g,n,B", [(4, 500, 1), (36, 700, 1), (4, 20000, 1),
