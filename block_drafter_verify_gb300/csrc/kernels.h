@@ -183,7 +183,7 @@ inline bool cache_sizes_ok(int B, int Q, int Hq, int Hkv, int D, int page,
   if (D < 16 || D > 256 || D % 16 != 0) return false;
   if (page != 16 && page != 32 && page != 64 && page != 128) return false;
   if (num_pages < 1 || max_pages < 1) return false;
-  // row counts and a sequence's positions stay within 32 bits
+  // tokens and a sequence's positions stay within 32 bits
   return (long long)B * Q <= (1 << 24) &&
          (long long)max_pages * page <= (1LL << 30) &&
          (long long)num_pages * Hkv * page <= (1LL << 31) - 1;

@@ -388,8 +388,10 @@ inline bool aligned_to(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
 
+// (the tensor-core kernel counts the rows of out in 32 bits)
 bool attn_sizes_ok(int B, int Q, int Hq, int Hkv, int D) {
-  return cache_sizes_ok(B, Q, Hq, Hkv, D, 16, 1, 1) && Hq / Hkv <= 64;
+  return cache_sizes_ok(B, Q, Hq, Hkv, D, 16, 1, 1) && Hq / Hkv <= 64 &&
+         (long long)B * Q * Hq <= 0x7fffffffll;
 }
 
 }  // namespace

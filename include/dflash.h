@@ -591,11 +591,12 @@ size_t dflash_paged_attn_workspace_bytes(int B, int Q, int Hq, int Hkv, int D);
  * 2^-13); sums and statistics in fp32.  Otherwise fp32 on the CUDA cores.
  * Codes and slots past kv_len may hold anything.  Scales are powers of two
  * between 2^-64 and 2^120, as dflash_kv_append writes them.
- * Requirements: Hq % Hkv == 0, Hq / Hkv <= 64, q, out and the codes 16-byte
- * aligned; scale finite; fewer than 2^31 tiles of 128 tokens over all
- * sequences' page tables and key heads (with bf16).  On the device: kv_len below 0 or beyond the page
- * table, q_len outside [0, Q] and a page id outside [0, num_pages) set
- * DFLASH_ERR_BAD_INDEX (lengths are clamped, such a page counts as zeros).
+ * Requirements: Hq % Hkv == 0, Hq / Hkv <= 64, B * Q * Hq < 2^31; q, out and
+ * the codes 16-byte aligned; scale finite; fewer than 2^31 tiles of 128 tokens
+ * over all sequences' page tables and key heads (with bf16).  On the device:
+ * kv_len below 0 or beyond the page table, q_len outside [0, Q] and a page id
+ * outside [0, num_pages) set DFLASH_ERR_BAD_INDEX (lengths are clamped, such a
+ * page counts as zeros).
  */
 dflash_status dflash_paged_attn(
     const void* q, const uint8_t* k_codes, const uint8_t* v_codes,
