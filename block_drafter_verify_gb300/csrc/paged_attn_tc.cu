@@ -4,10 +4,17 @@
 // The cached codes go from HBM to the MMAs as they are: no kernel instruction
 // touches a key or a value.  What has to meet them in 8 bits is the small
 // side, split so that nothing is lost:
-//   q    is scaled by a power of two and written as the sum of two E4M3
-//        numbers (8 bits, all that bf16 has), both products added.  The rows
-//        of a unit share the scale; a row more than 2^6 below the largest
-//        has its own (and costs the softmax one multiplication);
+//   q    is scaled by a power of two and written as the sum of two 8-bit
+//        numbers (8 bits, all that bf16 has), both products added: E4M3 and,
+//        of what that leaves, E4M3 again of 2^5 times it where the two scores
+//        stand side by side, E5M2 where they fall onto the same columns.  (In
+//        E4M3 as it is, which ends at 2^-9, small values would lose all below
+//        2^-10.)  So a value is exact to 2^-21 of the largest of the rows that
+//        share a scale.  The rows of a unit do; a row more than 2^4 below the
+//        largest has its own, so that every row has 2^-17 of its own largest
+//        (one more multiplication a score: 36 rows 75.8 -> 79.7 us, 72 rows
+//        98.6 -> 108.7 us, 96 rows 110.9 -> 122.9 us, eight sequences of
+//        16,384, which is why not all rows do);
 //   P    the softmax weights are written as the sum of four E5M2 numbers, in
 //        all exact to 2^-13.  E5M2 is the upper byte of fp16: of the weight
 //        rounded to fp16 a part is that byte after rounding, the rest an
@@ -69,6 +76,7 @@ constexpr float kFarLv = 90.f;
 constexpr float kRaise = 15.75f;   // 2^15.75 = 55109 < 57344, E5M2's largest
 constexpr int kUnitCost = 4;       // of a unit besides its tiles, in tiles
 constexpr int kParts = 4;          // E5M2 parts of a weight
+constexpr int kRowsApart = 4;      // bits below the unit's for a scale of its own
 
 // Shared-memory plan for N rows.
 template <int N>
@@ -92,6 +100,10 @@ struct Plan {
   // the 128 lanes' operand when N is small.
   static constexpr int kScore = N <= 64 ? 2 * N : N;    // columns of a tile
   static constexpr int kAcc = N <= 64 ? kParts * N : 2 * N;
+  // Of q's second part: its factor (undone where the scores are added) and type
+  static constexpr float kRestUp = kScore == 2 * N ? 32.f : 1.f;
+  static constexpr __nv_fp8_interpretation_t kRestType =
+      kScore == 2 * N ? __NV_E4M3 : __NV_E5M2;
   static constexpr int kUse = 2 * kScore + kAcc;
   static constexpr int kCols =
       kUse <= 128 ? 128 : kUse <= 256 ? 256 : 512;
@@ -648,6 +660,8 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
     // The whole warp waits, one elected thread issues: operands stay in
     // uniform registers (issued by a lone lane, an MMA cost 90 cycles).
     constexpr uint32_t id_s = tc::idesc_e4m3_f32(128, PL::kScore);
+    // (of q's second part on the same columns: format 1, as in idesc_mn)
+    constexpr uint32_t id_rest = id_s | (1u << 10);
     constexpr uint32_t id_o = idesc_mn(PL::kAcc);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     pdl_wait();
@@ -684,7 +698,8 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               tc::mma_e4m3(tm + rs.at * PL::kScore, dk + 2 * k,
-                           dq + h * (N * 8) + 2 * k, id_s, (h | k) != 0);
+                           dq + h * (N * 8) + 2 * k, h ? id_rest : id_s,
+                           (h | k) != 0);
           tc::mma_commit(&m.kempty[rk.at]);
           tc::mma_commit(&m.sfull[rs.at]);
           tc::mbar_arrive(&m.sfull[rs.at]);
@@ -835,7 +850,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
           const float big = fetch(r, v);  // the whole row has been read now
           const int e_row = (int)(__float_as_uint(big) >> 23) - 127;
           int e = e_all;
-          if (big > 0.f && e_row < e_all - 6) {
+          if (big > 0.f && e_row < e_all - kRowsApart) {
             e = max(e_row, max(-100, e_all - 100));
             own = true;
           }
@@ -852,9 +867,10 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
                 __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
             const float2 f = __half22float2(
                 __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+            const float2 rest = make_float2((y.x - f.x) * PL::kRestUp,
+                                            (y.y - f.y) * PL::kRestUp);
             const uint32_t l =
-                __nv_cvt_float2_to_fp8x2(make_float2(y.x - f.x, y.y - f.y),
-                                         __NV_SATFINITE, __NV_E4M3);
+                __nv_cvt_float2_to_fp8x2(rest, __NV_SATFINITE, PL::kRestType);
             if (k & 1) {
               hi[k >> 1] |= h << 16;
               lo[k >> 1] |= l << 16;
@@ -981,8 +997,9 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
           tmem_loaded(y);
 #pragma unroll
           for (int r = 0; r < HR; r += 2)
-            unpack2(add2(pack2(y[r], y[r + 1]), pack2(z[r], z[r + 1])), y[r],
-                    y[r + 1]);
+            unpack2(fma2(pack2(z[r], z[r + 1]),
+                         pack2(1.f / PL::kRestUp, 1.f / PL::kRestUp),
+                         pack2(y[r], y[r + 1])), y[r], y[r + 1]);
         } else {
           tmem_loaded(y);
         }

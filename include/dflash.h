@@ -586,7 +586,7 @@ size_t dflash_paged_attn_workspace_bytes(int B, int Q, int Hq, int Hkv, int D);
  *   ws >= dflash_paged_attn_workspace_bytes(B, Q, Hq, Hkv, D) bytes, 256-byte
  *      aligned; its contents need no initialisation
  * With bf16 storage and D <= 128 the products run on the tensor cores: q as
- * the sum of two E4M3 numbers (all its bits, down to 2^-17 of its row's
+ * the sum of two 8-bit numbers (all its bits, down to 2^-17 of its row's
  * largest value), the softmax weights as the sum of four E5M2 numbers (to
  * 2^-13); sums and statistics in fp32.  Otherwise fp32 on the CUDA cores.
  * Codes and slots past kv_len may hold anything.  Scales are powers of two

@@ -7,7 +7,7 @@ import torch
 
 import oracle
 from oracle import target_ops as to
-from test_gpu_target_ops import (DT, Cache, _attend, _check_attn,
+from test_gpu_target_ops import (DT, U, Cache, _attend, _check_attn,
                                  _check_sample, _run_sample)
 
 pytestmark = pytest.mark.gpu
@@ -188,3 +188,43 @@ def test_attention_value_scales_over_their_range(lib, dtype, first, rest,
     lib.dflash_check()
     for b in {0, B // 2, B - 1}:
         _check_attn(dtype, D, n, out[b:b + 1], lse[b:b + 1], ref)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("below", [1, 2, 3, 5, 6, 7, 12])
+@pytest.mark.parametrize("g", [4, 20])
+def test_attention_small_row_beside_a_large_one(lib, dtype, below, g):
+    """A row 2^below under the largest of its unit, most of it 2^11 under its
+    own largest value: every query value keeps 2^-17 of its own row's largest,
+    so that a score is off by that times the sum of |k| at most (fp32: by the
+    sum's roundings)."""
+    n, D, page, Q = 300, 128, 32, 4
+    rng = np.random.default_rng(below)
+    cache = Cache([n], page, 1, D, rng, spread=0)
+    ids = cache.table[0]
+    sign = rng.integers(0, 2, (len(ids), 1, page, 1))
+    cache.codes[0][ids] = np.where(sign, 0x38, 0xB8)   # 1 or -1 throughout
+    cache.codes[0][ids, :, :, 0] = 0
+    cache.scale[0][ids] = 1.0
+    for c, s in zip(cache.codes, cache.scale):
+        c[ids[-1], :, n % page:] = 0x7F
+    x = rng.standard_normal((1, Q, g, D))
+    x *= 200 / np.abs(x).max(-1, keepdims=True)        # in [128, 256)
+    low = 2.0 ** -below
+    x[0, 1, 2] = 0.99 * 2.0 ** -11 * 128 * low
+    x[0, 1, 2, 0] = 128 * low
+    q = torch.tensor(x, dtype=torch.float32).to(DT[dtype])
+    scale = 5 / (127 * float(q[0, 1, 2, 1]))           # scores of 5 and -5
+    out, lse = _attend(lib, dtype, cache, q.cuda(), [n], None, True, scale)
+    lib.dflash_check()
+    ref = to.paged_attn(q.float().numpy().astype(np.float64), *cache.codes,
+                        *cache.scale, cache.table, [n], [Q], scale)
+    o, z = ref[0][0, 1, 2], ref[1][0, 1, 2]
+    part = 2.0 ** -17 if dtype == "bf16" else (D + 3) * U
+    d = part * 128 * low * 127 * scale
+    assert abs(float(lse[0, 1, 2]) - z) <= d + (n + 16) * U
+    tol = (2 * d + (n + 8) * U + (2.0 ** -14 if dtype == "bf16" else 0)
+           ) * ref[3][0, 1, 2]
+    if dtype == "bf16":
+        tol = tol + 2.0 ** -8 * np.abs(o)
+    assert np.all(np.abs(out[0, 1, 2].double().cpu().numpy() - o) <= tol)
