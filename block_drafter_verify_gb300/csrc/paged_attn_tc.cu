@@ -16,11 +16,16 @@
 //        98.6 -> 108.7 us, 96 rows 110.9 -> 122.9 us, eight sequences of
 //        16,384, which is why not all rows do);
 //   P    the softmax weights are written as the sum of four E5M2 numbers, in
-//        all exact to 2^-13.  E5M2 is the upper byte of fp16: of the weight
-//        rounded to fp16 a part is that byte after rounding, the rest an
-//        exact fp16 difference, and three parts of three bits and a sign hold
-//        its eleven bits; the fourth is the upper byte of what fp16 rounded
-//        off.  That takes no conversion to 8 bits (parts made by those took
+//        all exact to 2^-13 of themselves or 2^-16, whichever is more: E5M2
+//        has nothing below 2^-16, which is 2^-25 of the row's largest weight in
+//        this run at worst (that one lies above 2^9).  The sum of the weights
+//        counts them as they are in fp32, so n weights of less than 2^-26 of
+//        the largest, which the products drop, pull the output towards 0 by n
+//        2^-26 of the values' size at most.  E5M2 is the upper byte of fp16:
+//        of the weight rounded to fp16 a part is that byte after rounding, the
+//        rest an exact fp16 difference, and three parts of three bits and a
+//        sign hold its eleven bits; the fourth is the upper byte of what fp16
+//        rounded off.  That takes no conversion to 8 bits (parts made by those took
 //        1200 cycles a tile of 80 rows), and no part needs a scale of its
 //        own.  Without the fourth part: 2^-11, and 2 to 7 % less time.
 // Scores are computed transposed: S^T[token, row] = K q^T and

@@ -588,7 +588,9 @@ size_t dflash_paged_attn_workspace_bytes(int B, int Q, int Hq, int Hkv, int D);
  * With bf16 storage and D <= 128 the products run on the tensor cores: q as
  * the sum of two 8-bit numbers (all its bits, down to 2^-17 of its row's
  * largest value), the softmax weights as the sum of four E5M2 numbers (to
- * 2^-13); sums and statistics in fp32.  Otherwise fp32 on the CUDA cores.
+ * 2^-13 of themselves or 2^-25 of their row's largest, whichever is more; a
+ * weight counts with its value's scale here); sums and statistics in fp32.
+ * Otherwise fp32 on the CUDA cores.
  * Codes and slots past kv_len may hold anything.  Scales are powers of two
  * between 2^-64 and 2^120, as dflash_kv_append writes them.
  * Requirements: Hq % Hkv == 0, Hq / Hkv <= 64, B * Q * Hq < 2^31; q, out and

@@ -1,6 +1,8 @@
 """The target's calls at the ends of their stated ranges.  Tolerances are those
 of test_gpu_target_ops; where a test has its own, its docstring derives it.
 """
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -228,3 +230,38 @@ def test_attention_small_row_beside_a_large_one(lib, dtype, below, g):
     if dtype == "bf16":
         tol = tol + 2.0 ** -8 * np.abs(o)
     assert np.all(np.abs(out[0, 1, 2].double().cpu().numpy() - o) <= tol)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("bits", [12, 16, 20, 24, 26, 30])
+def test_attention_small_weights_of_a_long_run(lib, dtype, bits):
+    """One token of weight 1 and value 0, thousands of weight 2^-bits behind
+    it in the same run (enough sequences that none is cut more than once).
+    With bf16 a weight w keeps 2^-13 of itself and 2^-25 of the largest, so
+    that n of them sum to within n (2^-13 w + 2^-25)."""
+    n, D, page, B = 6000, 64, 32, 304
+    rng = np.random.default_rng(bits)
+    cache = Cache([n], page, 1, D, rng, spread=0)
+    kc, vc = cache.codes
+    ids = cache.table[0]
+    kc[ids] = 0
+    kc[ids[0], 0, 0, 0] = 0x38                # 1.0: only token 0 scores
+    vc[ids] = 0x78                            # 256
+    vc[ids[0], 0, 0] = 0
+    cache.scale[0][:] = 1
+    cache.scale[1][:] = 2.0 ** -8             # every value is 1
+    s = bits * math.log(2)
+    q = torch.full((B, 1, 1, D), 1.0, dtype=DT[dtype], device="cuda")
+    ref = to.paged_attn(np.ones((1, 1, 1, D)), *cache.codes, *cache.scale,
+                        cache.table, [n], [1], s)
+    cache.table = np.repeat(cache.table, B, 0)
+    out, lse = _attend(lib, dtype, cache, q, [n] * B, None, True, s)
+    lib.dflash_check()
+    o, z = ref[0][0, 0, 0], float(ref[1][0, 0, 0])
+    w = 2.0 ** -bits
+    tol = (4 * (D + 3) * U * s + 2 * n * U) * o    # scores, sums
+    if dtype == "bf16":
+        tol = tol + n * (2.0 ** -13 * w + 2.0 ** -25) + 2.0 ** -9 * o
+    for b in (0, 1, 150, B - 1):
+        assert np.all(np.abs(out[b, 0, 0].double().cpu().numpy() - o) <= tol)
+        assert abs(float(lse[b]) - z) <= 4 * (D + 3) * U * s + 2 * n * U
