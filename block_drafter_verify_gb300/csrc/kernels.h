@@ -12,7 +12,7 @@ namespace dflash {
 
 // Default limit of the tensor-core kernels' bounded waits (2 s, far beyond
 // any real wait); dflash_set_wait_limit_ns changes it for later launches of
-// the conv, of the single-CTA LM head and of the sampling.
+// the conv, of the single-CTA LM head, of the attention and of the sampling.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 uint64_t wait_limit_ns();  // the present one (api.cu)
 
@@ -200,6 +200,7 @@ struct PagedAttnArgs {
   void* out;
   float* lse;                         // may be NULL
   int* err;
+  uint64_t wait_ns;                   // limit of the tensor-core kernel's waits
 };
 // paged_attn_tc.cu: the tensor-core kernels.
 bool paged_attn_tc_takes(int D, dflash_dtype dt);

@@ -455,6 +455,7 @@ dflash_status dflash_paged_attn(
   a.scale = scale;
   a.out = out;
   a.lse = lse;
+  a.wait_ns = wait_limit_ns();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e =
       paged_attn_tc_takes(D, dt)

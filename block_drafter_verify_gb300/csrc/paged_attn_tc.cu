@@ -67,7 +67,6 @@ constexpr int kMaxRows = 96;       // (query, head) rows of a unit
 constexpr int kMaxCtas = 160;
 constexpr int kUnitBytes = kTile * 128;  // a K or V tile in shared memory
 constexpr int kStages = 7;         // most stages of K or V tiles
-constexpr uint64_t kWait = 2000000000ull;  // 2 s
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kHead = 10.f;      // weights are 2^(score - ref + kHead)
 // A row's sum counts its weights without their value scales (2^lv), times
@@ -281,23 +280,26 @@ __device__ bool walk_next(const PagedAttnArgs& a, const Shape& s, Walk& w,
   return false;
 }
 
-// Wait for phase `parity` of `bar`, at most kWait; false (and *abort set) if
-// it runs out or another role gave up.  Polls go to shared memory, whose
-// bandwidth the MMAs need: the clock and *abort are looked at seldom, and
-// roles that run ahead (kLazy) sleep between polls.
+// Wait for phase `parity` of `bar`, at most `limit` ns; false (and *abort set)
+// if it runs out or another role gave up.  Polls go to shared memory, whose
+// bandwidth the MMAs need: the clock and *abort are looked at every 64 polls
+// (some 100 us; every poll with a limit below a millisecond), and roles that
+// run ahead (kLazy) sleep between polls.
 template <bool kLazy = false>
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity,
-                                         volatile int* abort) {
+                                         volatile int* abort,
+                                         uint64_t limit) {
   if (tc::mbar_try_wait(bar, parity, 1000)) return true;
   const uint64_t t0 = tc::globaltimer_ns();
+  const int polls = limit < 1000000ull ? 1 : 64;
   for (;;) {
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i) {
+    for (int i = 0; i < polls; ++i) {
       if (kLazy) __nanosleep(100);
       if (tc::mbar_try_wait(bar, parity, 1000)) return true;
     }
     if (*abort) return false;
-    if (tc::globaltimer_ns() - t0 > kWait) {
+    if (tc::globaltimer_ns() - t0 > limit) {
       *abort = 1;
       return false;
     }
@@ -615,7 +617,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
         if (bad) raise_error(a.err, kErrBadIndex);
         const int row = bad ? oob : (pid * a.Hkv + p.hk) * a.page;
         const uint32_t bytes = box * __popc(__ballot_sync(0xffffffffu, have));
-        ok = wait_for<true>(&m.kempty[rk.at], rk.phase ^ 1, abort);
+        ok = wait_for<true>(&m.kempty[rk.at], rk.phase ^ 1, abort, a.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0) tc::mbar_arrive_expect_tx(&m.kfull[rk.at], bytes);
@@ -625,7 +627,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
                           &m.kfull[rk.at], 0, row);
         rk.next();
         nk = min(nk + 1, PL::K);
-        ok = wait_for<true>(&m.vempty[rv.at], rv.phase ^ 1, abort);
+        ok = wait_for<true>(&m.vempty[rv.at], rv.phase ^ 1, abort, a.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         // the copy first: the scales may still be on their way here
@@ -654,11 +656,11 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
     int never = 0;
     for (; nk > 0; --nk) {
       const Ring<PL::K> r = rk.back(nk);
-      wait_for(&m.kfull[r.at], r.phase, &never);
+      wait_for(&m.kfull[r.at], r.phase, &never, kWaitLimitNs);
     }
     for (; nv > 0; --nv) {
       const Ring<PL::V> r = rv.back(nv);
-      wait_for(&m.vfull[r.at], r.phase, &never);
+      wait_for(&m.vfull[r.at], r.phase, &never, kWaitLimitNs);
     }
   } else if (warp == 1) {
     // --------------------------------------------------------- MMA issuer
@@ -673,7 +675,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
     pdl_trigger();
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t par) {
-      ok = ok && wait_for(bar, par, abort);
+      ok = ok && wait_for(bar, par, abort, a.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       return ok;
     };
@@ -755,7 +757,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
     if (elect_one()) tc::mma_commit(&m.drain);
     __syncwarp();
     int never = 0;
-    wait_for(&m.drain, 0, &never);
+    wait_for(&m.drain, 0, &never, kWaitLimitNs);
   } else if (warp < 4) {
     // ------------------------------------------------------ layout of q
     pdl_wait();
@@ -772,9 +774,10 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
     for (int s = 0;; ++s) {
       const int qb = s & 1;
       bool ok = wait_for<true>(&m.qempty[qb], (uint32_t)((s >> 1) & 1) ^ 1,
-                               abort);
+                               abort, a.wait_ns);
       if (s > 0)
-        ok = ok && wait_for<true>(&m.qfree, (uint32_t)(s - 1) & 1, abort);
+        ok = ok && wait_for<true>(&m.qfree, (uint32_t)(s - 1) & 1, abort,
+                                  a.wait_ns);
       if (any_of<64>(kQBar, !ok)) break;
       Segment& g = m.seg[qb];
       Part p;
@@ -962,7 +965,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
         pdl_wait();
         pdl_trigger();
       }
-      bool ok = dry || wait_for(&m.qfull[qb], (s >> 1) & 1, abort);
+      bool ok = dry || wait_for(&m.qfull[qb], (s >> 1) & 1, abort, a.wait_ns);
       if (half_any(bar, !ok)) break;
       const Segment& g = m.seg[qb];
       if (!dry && g.done) break;
@@ -1016,7 +1019,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
         // Also says that the weights' buffer is free: the scores' commit
         // follows the second product of two tiles ago.
         if (!early) {
-          ok = dry || wait_for(&m.sfull[sb], rs.phase, abort);
+          ok = dry || wait_for(&m.sfull[sb], rs.phase, abort, a.wait_ns);
           ok = __all_sync(0xffffffffu, ok);
           if (ok) {
             ask(sb);
@@ -1076,7 +1079,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
           half_sync(bar);
           if (t > 0) {
             const Ring<PL::V> before = rv.back(1);
-            ok = wait_for(&m.vempty[before.at], before.phase, abort);
+            ok = wait_for(&m.vempty[before.at], before.phase, abort, a.wait_ns);
             ok = __all_sync(0xffffffffu, ok);
             tc::fence_after_sync();
           }
@@ -1190,7 +1193,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
       // ---- the segment's result ------------------------------------------
       if (T > 0) {
         const Ring<PL::V> last = rv.back(1);
-        ok = dry || wait_for(&m.vempty[last.at], last.phase, abort);
+        ok = dry || wait_for(&m.vempty[last.at], last.phase, abort, a.wait_ns);
         if (half_any(bar, !ok)) break;
         tc::fence_after_sync();
       }

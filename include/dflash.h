@@ -669,11 +669,11 @@ dflash_status dflash_philox4x32(const uint32_t* ctr, uint64_t seed,
 dflash_status dflash_profile_stage(int stage, void* begin, void* end);
 
 /* Limit, in nanoseconds, of the bounded waits inside the tensor-core
- * kernels of later launches: the conv and the single-CTA LM head (one row
- * tile, B*K <= 128) give up on a wait that runs longer, stop issuing work,
- * let their copies and MMAs in flight complete, free their TMEM and set
- * DFLASH_ERR_DEVICE_TIMEOUT in the device error word (their results are
- * then invalid).  dflash_sample's waits for the copies of a row do so too
+ * kernels of later launches: the conv, the single-CTA LM head (one row tile,
+ * B*K <= 128) and dflash_paged_attn give up on a wait that runs longer, stop
+ * issuing work, let their copies and MMAs in flight complete, free their TMEM
+ * and set DFLASH_ERR_DEVICE_TIMEOUT in the device error word (their results
+ * are then invalid).  dflash_sample's waits for the copies of a row do so too
  * (that row's token is then -1).  0 restores the default of 2 s, far beyond
  * any real wait; the CTA-pair LM head always uses it.  Process-wide host state,
  * meant for tests of that failure path ("Failure detection": a wait that

@@ -265,3 +265,32 @@ def test_attention_small_weights_of_a_long_run(lib, dtype, bits):
     for b in (0, 1, 150, B - 1):
         assert np.all(np.abs(out[b, 0, 0].double().cpu().numpy() - o) <= tol)
         assert abs(float(lse[b]) - z) <= 4 * (D + 3) * U * s + 2 * n * U
+
+
+def test_attention_gives_up_on_a_wait_and_recovers(lib):
+    """Every CTA has three sequences of 200 tiles, so that the warps that lay
+    out q wait a hundred microseconds and more for the softmax: with a limit
+    of a nanosecond they give up, the kernel drains, and the next call is
+    right."""
+    rng = np.random.default_rng(31)
+    n, B, Q, Hq, D = 200 * 128, 456, 9, 8, 128
+    cache = Cache([n], 128, 1, D, rng)
+    q = torch.tensor(rng.standard_normal((1, Q, Hq, D)),
+                     dtype=torch.float32).to(torch.bfloat16)
+    ref = to.paged_attn(q.float().numpy().astype(np.float64), *cache.codes,
+                        *cache.scale, cache.table, [n], [Q], 0.1)
+    cache.table = np.repeat(cache.table, B, 0)
+    q = q.cuda().repeat(B, 1, 1, 1)
+    lib.dflash_check()                         # nothing pending
+    try:
+        lib.dflash_set_wait_limit_ns(1)
+        _attend(lib, "bf16", cache, q, [n] * B, None, True, 0.1)
+        with pytest.raises(lib.DFlashError) as e:
+            lib.dflash_check()
+        assert e.value.status == 5             # DFLASH_ERR_DEVICE_TIMEOUT
+    finally:
+        lib.dflash_set_wait_limit_ns(0)        # back to the default (2 s)
+    out, lse = _attend(lib, "bf16", cache, q, [n] * B, None, True, 0.1)
+    lib.dflash_check()
+    for b in (0, 200, B - 1):
+        _check_attn("bf16", D, n, out[b:b + 1], lse[b:b + 1], ref)
