@@ -12,8 +12,8 @@
 //        2^-10.)  So a value is exact to 2^-21 of the largest of the rows that
 //        share a scale.  The rows of a unit do; a row more than 2^4 below the
 //        largest has its own, so that every row has 2^-17 of its own largest
-//        (one more multiplication a score: 36 rows 75.8 -> 79.7 us, 72 rows
-//        98.6 -> 108.7 us, 96 rows 110.9 -> 122.9 us, eight sequences of
+//        (one more multiplication a score: 36 rows 73.5 -> 77.7 us, 72 rows
+//        97.1 -> 107.0 us, 96 rows 111.5 -> 124.2 us, eight sequences of
 //        16,384, which is why not all rows do);
 //   P    the softmax weights are written as the sum of four E5M2 numbers, in
 //        all exact to 2^-13 of themselves or 2^-16, whichever is more: E5M2
@@ -193,7 +193,18 @@ struct Walk {
   int b, hk, rt, at;         // at: position in the unit
   int left;                  // positions left in this CTA's run
   int first;                 // no segment handed out yet
+  int total, G;              // all positions, and the CTAs that work
 };
+// A unit that is cut, for the join: CTA c leaves it here if the unit's first
+// tile is CTA c - 1's and its next is c's own.
+struct alignas(16) Cut {
+  int b, hk, rt;
+  int parts;  // 0: no such unit; 2 n + odd: n parts, the first in the odd slot
+};
+// Words of partial sums, before the CTAs' Cuts.
+__host__ __device__ constexpr size_t part_words(int grid, int N) {
+  return (size_t)2 * grid * N * (128 + 2);
+}
 // Where the run of CTA `cta` of `grid` starts.  A whole warp, each lane with
 // a stretch of the sequences; *bad: some length was out of range.
 __device__ void walk_start(const PagedAttnArgs& a, const Shape& s, int cta,
@@ -215,6 +226,8 @@ __device__ void walk_start(const PagedAttnArgs& a, const Shape& s, int cta,
   const int p0 = run_start(total, cta, G), p1 = run_start(total, cta + 1, G);
   w.left = p1 - p0;
   w.first = 1;
+  w.total = total;
+  w.G = G;
   w.b = w.hk = w.rt = w.at = 0;
   if (w.left <= 0) return;                 // the same in every lane
   const bool mine = p0 >= run - work && p0 < run;
@@ -239,6 +252,23 @@ __device__ void walk_start(const PagedAttnArgs& a, const Shape& s, int cta,
   w.hk = __shfl_sync(0xffffffffu, w.hk, from);
   w.rt = __shfl_sync(0xffffffffu, w.rt, from);
   w.at = __shfl_sync(0xffffffffu, o, from);
+}
+// What CTA `cta` leaves for the join, from the start of its walk.
+__device__ __forceinline__ Cut cut_at(const PagedAttnArgs& a, const Shape& s,
+                                      const Walk& w, int cta) {
+  Cut c{w.b, w.hk, w.rt, 0};
+  if (w.left <= 0 || w.at <= kUnitCost) return c;  // no tile lies before
+  bool bad = false;
+  const int before = run_start(w.total, cta, w.G) - w.at;  // first position
+  const int head = before + kUnitCost;                     // its first tile's
+  const int end = head + tiles_of(a, s, lens_of(a, w.b, &bad), w.rt);
+  const int c0 = (int)(((head + 1ll) * w.G - 1) / w.total);
+  if (c0 != cta - 1) return c;
+  const int c1 = (int)(((long long)end * w.G - 1) / w.total);
+  // a run's first segment is in its even slot; every part but the first
+  // starts its run, and the first does if no unit before it ends there
+  c.parts = 2 * (c1 - c0 + 1) + (run_start(w.total, c0, w.G) < before);
+  return c;
 }
 struct Part {
   int b, hk, rt, t0, t1, whole, first;
@@ -566,12 +596,15 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
   if (warp == 0) {
     // ---------------------------------------------------------- producer
     pdl_wait();
-    pdl_trigger();  // after the wait: the join may read the lengths at once
+    pdl_trigger();
     Walk w;
     {
       bool bad = false;
       walk_start(a, shape, blockIdx.x, gridDim.x, w, &bad);
       if (bad && blockIdx.x == 0) raise_error(a.err, kErrBadIndex);
+      if (lane == 0)
+        reinterpret_cast<Cut*>(part + part_words(gridDim.x, N))[blockIdx.x] =
+            cut_at(a, shape, w, blockIdx.x);
     }
     Part p;
     const int pt = kTile / a.page;         // pages of a tile
@@ -1279,70 +1312,29 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
   if (tid == 0 && m.abort) raise_error(a.err, kErrTimeout);
 }
 
-// Joins the partial sums of the units that the runs cut: a warp per row,
-// eight rows of a unit to a CTA.
+// Joins the partial sums of the units that the runs cut: a CTA for each that
+// may have left one, a warp per row, eight rows of the unit to a CTA.  (With a
+// CTA for every unit that counted the work before it, the join took 27 ms of
+// 30 for a prompt of 8192 tokens and 64 heads.)
 constexpr int kJoinRows = 8;
 constexpr int kJoinThreads = 32 * kJoinRows;
 __global__ void __launch_bounds__(kJoinThreads)
     paged_attn_tc_join_kernel(const __grid_constant__ PagedAttnArgs a,
                               const Shape shape, int grid,
                               const float* __restrict__ part) {
-  __shared__ int s_sum[2][kJoinRows];
   __shared__ float s_w[kJoinRows][kMaxCtas];
-  // The launch before lets this one start once it has waited for what wrote
-  // the lengths: only the partial sums are to be waited for.
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int u = blockIdx.x;
-  const int rt = u % shape.row_tiles;
-  u /= shape.row_tiles;
-  const int hk = u % a.Hkv, b = u / a.Hkv;
-  // tiles before this unit, and all tiles
-  int before = 0, total = 0;
-  bool bad = false;
-  for (int i = tid; i < a.B; i += kJoinThreads) {
-    const int w = a.Hkv * head_work(a, shape, lens_of(a, i, &bad));
-    total += w;
-    if (i < b) before += w;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-  }
-  if (lane == 0) {
-    s_sum[0][warp] = before;
-    s_sum[1][warp] = total;
-  }
-  __syncthreads();
-  before = total = 0;
-  for (int i = 0; i < kJoinRows; ++i) {
-    before += s_sum[0][i];
-    total += s_sum[1][i];
-  }
-  const int G = min(grid, total);
-  const Lens l = lens_of(a, b, &bad);
-  before += hk * head_work(a, shape, l);
-  for (int i = 0; i < rt; ++i)
-    before += kUnitCost + tiles_of(a, shape, l, i);
-  const int tiles = tiles_of(a, shape, l, rt);
-  if (tiles < 2) {
-    pdl_wait();
-    return;
-  }
-  const int head = before + kUnitCost;  // of its first tile
-  const int end = head + tiles;
-  const int c0 = (int)(((head + 1ll) * G - 1) / total);
-  const int c1 = (int)(((long long)end * G - 1) / total);  // of tile end - 1
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_trigger();
   pdl_wait();
-  if (c0 == c1) return;
+  const int cta = blockIdx.x + 1;
+  const Cut cut =
+      reinterpret_cast<const Cut*>(part + part_words(grid, shape.N))[cta];
+  if (cut.parts == 0) return;
   const int r = blockIdx.y * kJoinRows + warp;
-  const int row = rt * shape.N + r;
+  const int row = cut.rt * shape.N + r;
   if (r >= shape.N || row >= shape.rows) return;
-  const int n = c1 - c0 + 1;
-  // a run's first segment is in its even slot; every part but the first
-  // starts its run, and the first does if no unit before it ends there
-  const int odd = run_start(total, c0, G) < before;
+  const int n = cut.parts >> 1, odd = cut.parts & 1, c0 = cta - 1;
+  const int b = cut.b, hk = cut.hk;
   auto slot = [&](int i) { return 2 * (c0 + i) + (i == 0 ? odd : 0); };
   const float2* ml = reinterpret_cast<const float2*>(
       part + (size_t)2 * grid * shape.N * 128);
@@ -1362,7 +1354,9 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int qi = row / shape.g;
   const size_t at =
       ((size_t)b * a.Q + qi) * a.Hq + hk * shape.g + row % shape.g;
-  const bool on = (sum > 0.f || sum != sum) && qi < l.nq;
+  bool bad = false;
+  const bool on =
+      (sum > 0.f || sum != sum) && qi < lens_of(a, b, &bad).nq;
   const float inv = on ? 1.f / sum : 0.f;
   if (lane == 0 && a.lse)
     a.lse[at] = on ? (log2f(sum) + top) * 0.6931471805599453f : -INFINITY;
@@ -1420,7 +1414,7 @@ bool paged_attn_tc_takes(int D, dflash_dtype dt) {
 size_t paged_attn_tc_ws(int B, int Q, int Hq, int Hkv) {
   (void)B;
   const Shape s = shape_of(Q, Hq, Hkv);
-  return (size_t)2 * kMaxCtas * s.N * (128 + 2) * sizeof(float);
+  return part_words(kMaxCtas, s.N) * sizeof(float) + kMaxCtas * sizeof(Cut);
 }
 
 cudaError_t launch_paged_attn_tc(const PagedAttnArgs& a, int sms, float* part,
@@ -1446,10 +1440,9 @@ cudaError_t launch_paged_attn_tc(const PagedAttnArgs& a, int sms, float* part,
     default: e = launch_n<96>(mk, mv, a, s, G, part, stream); break;
   }
   if (e != cudaSuccess) return e;
-  const long long units = (long long)a.B * a.Hkv * s.row_tiles;
-  if (units > 0x7fffffffll) return cudaErrorNotSupported;
+  if (G < 2) return e;
   const int rows_of = std::min(s.N, s.rows);
-  PdlLaunch J(dim3((unsigned)units, (rows_of + kJoinRows - 1) / kJoinRows),
+  PdlLaunch J(dim3(G - 1, (rows_of + kJoinRows - 1) / kJoinRows),
               dim3(kJoinThreads), 0, stream);
   return cudaLaunchKernelEx(&J.cfg, paged_attn_tc_join_kernel, a, s, G,
                             (const float*)part);

@@ -294,3 +294,27 @@ def test_attention_gives_up_on_a_wait_and_recovers(lib):
     lib.dflash_check()
     for b in (0, 200, B - 1):
         _check_attn("bf16", D, n, out[b:b + 1], lse[b:b + 1], ref)
+
+
+@pytest.mark.parametrize("Q,kv,g,Hkv,B", [(700, 700, 8, 1, 1),
+                                          (1000, 1900, 3, 2, 2),
+                                          (4096, 4096, 8, 2, 1)])
+def test_attention_of_a_prompt_chunk(lib, Q, kv, g, Hkv, B):
+    """Prompts of many row tiles, most of them whole in one CTA, some cut:
+    rows at every place against the oracle's."""
+    rng = np.random.default_rng(Q)
+    D = 64
+    cache = Cache([kv] * B, 64, Hkv, D, rng)
+    q = torch.tensor(rng.standard_normal((B, Q, g * Hkv, D)),
+                     dtype=torch.float32).to(torch.bfloat16)
+    out, lse = _attend(lib, "bf16", cache, q.cuda(), [kv] * B, None, True,
+                       0.125)
+    lib.dflash_check()
+    assert torch.isfinite(lse).all()
+    at = rng.choice(Q, 40, replace=False)
+    for i in at:                               # one query's rows each
+        n = kv - Q + int(i) + 1
+        ref = to.paged_attn(q[:, i:i + 1].float().numpy().astype(np.float64),
+                            *cache.codes, *cache.scale, cache.table, [n] * B,
+                            [1] * B, 0.125)
+        _check_attn("bf16", D, n, out[:, i:i + 1], lse[:, i:i + 1], ref)
