@@ -43,7 +43,8 @@ constexpr int kMaxSplits = 32;
 // Values are added up times 2^-32, exactly: of the largest scale (2^120) some
 // hundred would pass fp32's range before they are divided by their weights.
 constexpr float kDown = 0x1p-32f, kUp = 0x1p32f;
-constexpr int kTargetCtas = 304;  // two to an SM
+// Two to an SM of 152.  Not the device's count: the workspace query has none.
+constexpr int kTargetCtas = 304;
 
 // Parts each sequence is cut into, from the sizes the host knows.
 int simt_splits(long long B, long long Q, int Hq, int Hkv) {

@@ -1418,7 +1418,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
 }
 
 template <typename T>
-cudaError_t launch(SampleArgs a, cudaStream_t s) {
+cudaError_t launch(SampleArgs a, int sms, cudaStream_t s) {
   // One wave of CTAs, three to an SM: fewer to a row cost less in barriers
   // between them (64 rows of 262144 bf16 logits, top-k 50: 27 us with four, 38
   // us with eight; a lone row 17 us with eight, 28 us with two).  But
@@ -1428,16 +1428,16 @@ cudaError_t launch(SampleArgs a, cudaStream_t s) {
   // with four, 267 us with one; with top-k 50 in all of them 69 us and 53 us).
   // Never more than slices of 4096 tokens need.
   int C = kMaxCluster;
-  while (C > 1 && ((long long)a.R * C > 3 * 152 ||
+  while (C > 1 && ((long long)a.R * C > 3 * sms ||
                    (long long)(C / 2) * 4096 >= a.V))
     C /= 2;
   while (C < kMaxCluster && (long long)C * 65536 < a.V &&
-         (long long)a.R * C * 2 <= 8 * 152)
+         (long long)a.R * C * 2 <= 8 * sms)
     C *= 2;
   // A slice stays in shared memory where that takes no CTA's place on an SM
   // (100 rows of 151936 logits, top-k 50: 40 us, with slices of 76 KB held 45
   // us); the rest is read again, from L2 for the most part.
-  const bool two = (long long)a.R * C <= 2 * 152;
+  const bool two = (long long)a.R * C <= 2 * sms;
   a.slice = (int)((((long long)a.V + C - 1) / C + 7) & ~7ll);
   a.resident =
       (long long)a.slice * (long long)sizeof(T) <= (two ? 76 : 36) * 1024;
@@ -1492,8 +1492,9 @@ dflash_status dflash_sample(const void* logits, int64_t ld, dflash_dtype dt,
   a.filtered = filtered;
   a.wait_ns = wait_limit_ns();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = dt == DFLASH_FP32 ? launch<float>(a, s)
-                                          : launch<__nv_bfloat16>(a, s);
+  const cudaError_t e = dt == DFLASH_FP32
+                            ? launch<float>(a, sms, s)
+                            : launch<__nv_bfloat16>(a, sms, s);
   return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 
