@@ -34,11 +34,11 @@
 // rest fits one.
 //
 // What bounds it.  288 rows of 151936 fp32 logits, 26 us of HBM: T = 0 44 us,
-// top-k 50 61 us, no filter 74 us, top-k 1000 with top-p 88 us, top-p 0.9 of
-// 17000 tokens 196 us: the loads' latency (the second reading from L2 among
-// them) and the barriers of each row's chain, which other rows' CTAs hide in
-// part (issue slots are used to 30 to 55 %).  A lone row: 10 us, 13 us, 12 us,
-// 20 us and 32 us, the chain alone.
+// top-k 50 61 us, no filter 77 us, top-k 1000 with top-p 87 us, min-p 0.001
+// (6600 tokens) 153 us, top-p 0.9 (16600 tokens) 195 us: the loads' latency
+// (the second reading from L2 among them) and the barriers of each row's chain,
+// which other rows' CTAs hide in part (issue slots are used to 30 to 55 %).  A
+// lone row that L2 holds: 8, 13, 10, 19, 16 and 30 us, the chain alone.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -121,7 +121,6 @@ struct Shared {
   uint32_t kept_n;
   uint32_t odd;          // a logit of the slice is not finite
   uint32_t fine;         // one has more bits than bf16
-  uint32_t late;         // a copy of the slice did not come in time
   uint32_t lists[kCollects][kMaxCluster];  // lengths of every CTA's lists
   uint32_t row_listed[kCollects];  // the first CTA's: places taken in all_cand
   uint64_t landed[kChunks];  // barriers of the slice's copies
@@ -141,7 +140,9 @@ struct Shared {
   u64 cut;
   u64 kept_before;       // weight of the tokens down to the cut
   int kept;
-  union {
+  uint32_t late;         // a copy of the slice did not come in time
+  // (at 8 bytes beside a multiple of 16 a lone row took 11.5 us, not 11.1)
+  union alignas(16) {
     struct {
       union {
         uint32_t count[kBins];  // read by the cluster
@@ -552,7 +553,7 @@ __device__ int cut_in(Shared& S, const Row& r, int n, u64 hi, u64 lo,
 // them) to the kept set's cut and size, and the token.  The first k are kept,
 // of those the ones whose predecessors weigh less than `bound` (0: p of the k
 // tokens' weight).  Whole CTA.  A lone row of 151936 logits: k = 1000, p = 0.9
-// (1053 candidates) 18 us, k = 50 13 us; with two sorts of the candidates (by
+// (1053 candidates) 19 us, k = 50 13 us; with two sorts of the candidates (by
 // rank, then by id) 41 us and 21 us.
 __device__ void pick(Shared& S, const Row& r, float low, int V, int n, int k,
                      u64 bound, float p, float mp, float u, int* token) {
@@ -673,9 +674,9 @@ __device__ void refine_cut(Shared& S, cg::cluster_group& cl, const T* data,
 }
 
 // Three CTAs to an SM (40 registers each thread) hide each other's barriers:
-// 288 rows with mixed filters 193 us, 217 us with two (64 registers).  Where
-// there are no more than two to an SM, 64 registers spare the spills: 64 rows
-// with top-p 0.9 54 us, 71 us with 40 registers.
+// 288 rows with mixed filters and filtered logits 160 us, 169 us with two (64
+// registers).  Where there are no more than two to an SM, 64 registers spare the
+// spills: 64 rows with top-p 0.9 54 us, 71 us with 40 registers.
 template <typename T, int kPerSm>
 __global__ void __launch_bounds__(kThreads, kPerSm)
     sample_kernel(const __grid_constant__ SampleArgs a) {
@@ -762,12 +763,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     int give_up = 0;
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
-      if (!tc::mbar_wait_bounded(&S.landed[c], 0, &give_up, a.wait_ns)) {
-        // The row is given up, but not while a copy is in flight.
-        S.late = 1;
-        int never = 0;
-        tc::mbar_wait_bounded(&S.landed[c], 0, &never, kWaitLimitNs);
-      }
+      tc::mbar_wait_bounded(&S.landed[c], 0, &give_up, a.wait_ns);
       const int v1 = min(words, (c + 1) * per);
 #pragma unroll 4
       for (int v = min(words, c * per) + tid; v < v1; v += kThreads) {
@@ -779,6 +775,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
       const T x = src[i];
       own[i] = x;
       take(0, to_f32(x));
+    }
+    if (give_up) {  // the row is, but not while a copy is in flight
+      S.late = 1;
+      int never = 0;
+#pragma unroll 1
+      for (int c = 0; c < kChunks; ++c)
+        tc::mbar_wait_bounded(&S.landed[c], 0, &never, kWaitLimitNs);
     }
   } else if (src_wide) {
     const uint4* p = reinterpret_cast<const uint4*>(src);
@@ -1420,13 +1423,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
 template <typename T>
 cudaError_t launch(SampleArgs a, int sms, cudaStream_t s) {
   // One wave of CTAs, three to an SM: fewer to a row cost less in barriers
-  // between them (64 rows of 262144 bf16 logits, top-k 50: 27 us with four, 38
-  // us with eight; a lone row 17 us with eight, 28 us with two).  But
-  // no slices of more than 65536 tokens, up to eight CTAs for each SM: rows
-  // differ in how long they take, and in several waves the short ones fill
-  // what the long ones leave (288 rows of 151936 with mixed filters: 156 us
-  // with four, 267 us with one; with top-k 50 in all of them 69 us and 53 us).
-  // Never more than slices of 4096 tokens need.
+  // between them (64 rows of 262144 bf16 logits in L2, top-k 50: 17 us with
+  // four, 27 us with eight; a lone row without filters 10 us with eight, 24 us
+  // with two).  But no slices of more than 65536 tokens, up to eight CTAs for
+  // each SM: rows differ in how long they take, and in several waves the short
+  // ones fill what the long ones leave (288 rows of 151936 with mixed filters:
+  // 160 us with four, 261 us with one; with top-k 50 in all of them 60 us and 43
+  // us).  Never more than slices of 4096 tokens need.
   int C = kMaxCluster;
   while (C > 1 && ((long long)a.R * C > 3 * sms ||
                    (long long)(C / 2) * 4096 >= a.V))
@@ -1435,8 +1438,9 @@ cudaError_t launch(SampleArgs a, int sms, cudaStream_t s) {
          (long long)a.R * C * 2 <= 8 * sms)
     C *= 2;
   // A slice stays in shared memory where that takes no CTA's place on an SM
-  // (100 rows of 151936 logits, top-k 50: 40 us, with slices of 76 KB held 45
-  // us); the rest is read again, from L2 for the most part.
+  // (100 rows of 151936 logits in L2, top-k 50: 23 us, with slices of 148 KB
+  // held, one CTA to an SM, 35 us); the rest is read again, from L2 for the most
+  // part.
   const bool two = (long long)a.R * C <= 2 * sms;
   a.slice = (int)((((long long)a.V + C - 1) / C + 7) & ~7ll);
   a.resident =
