@@ -553,10 +553,14 @@ dflash_status dflash_verify_shard_draw(const float* target_shard,
  * k, v, q_out aligned to four elements, the tables and codes to 16 bytes;
  * ld >= heads * D; pages that this call writes belong to one sequence each.
  * On the device: tokens beyond the page table or the angle tables, n_new
- * outside [0, Q], a negative pos and a page id outside [0, num_pages) set
- * DFLASH_ERR_BAD_INDEX; such tokens are left out (kv_len counts the tokens
- * before them).  A NaN k or v sets DFLASH_ERR_NONFINITE and is stored as 0,
- * an infinite one sets it and is stored as the largest code.
+ * outside [0, Q] (all of the sequence's tokens), a negative pos (likewise) and
+ * a page id outside [0, num_pages) set DFLASH_ERR_BAD_INDEX; such tokens are
+ * left out.  kv_len counts none of them but those of a bad page id, which
+ * dflash_paged_attn counts as zeros and flags again.  A NaN k (after its
+ * rotation) or v sets DFLASH_ERR_NONFINITE and is stored as 0, an infinite one
+ * sets it and is stored as the largest code.  (An infinite k is turned with its
+ * partner: times a cosine or sine of 0, or against another infinity, it makes a
+ * NaN.)
  */
 dflash_status dflash_kv_append(
     const void* q, const void* k, const void* v, int64_t ld_q, int64_t ld_k,

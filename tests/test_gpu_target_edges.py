@@ -147,6 +147,39 @@ def test_sample_gives_up_on_a_copy_and_recovers(lib):
 
 
 # --------------------------------------------------------------------------
+# append
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("inter", [False, True])
+def test_append_infinite_key_is_turned(lib, dtype, inter):
+    """At position 0 (cosine 1, sine 0) an infinite key stays infinite, stored
+    as the largest code, and makes a NaN of its partner, stored as 0; at
+    position 1 both are infinite."""
+    D, page = 16, 16
+    k = torch.ones(2, 1, D, dtype=DT[dtype], device="cuda")
+    k[:, 0, 0] = float("inf")
+    v = torch.ones_like(k)
+    ang = torch.arange(2, device="cuda")[:, None] * torch.ones(
+        D // 2, device="cuda")
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    kc, vc = (torch.zeros(1, 1, page, D, dtype=torch.uint8, device="cuda")
+              for _ in range(2))
+    ks, vs = (torch.zeros(1, 1, device="cuda") for _ in range(2))
+    lib.dflash_kv_append(None, k, v, ang.cos(), ang.sin(), i32(0), None,
+                         i32(0).view(1, 1), kc, vc, ks, vs, None, i32(0),
+                         interleaved=inter)
+    with pytest.raises(lib.DFlashError) as e:
+        lib.dflash_check()
+    assert e.value.status == 4
+    other = 1 if inter else D // 2
+    got = kc[0, 0, :2].cpu().numpy()
+    assert got[:, [0, other]].tolist() == [[0x7E, 0], [0x7E, 0x7E]]
+    rest = np.delete(got, [0, other], 1)
+    assert np.all(rest != 0x7E) and np.all(rest[0] == 0x78)   # 1 = 256 / 256
+    assert float(ks) == 2.0 ** -8
+
+
+# --------------------------------------------------------------------------
 # attention
 # --------------------------------------------------------------------------
 SCALES = [(-64, 63), (-64, 120), (63, -64), (120, -64), (100, -20),
@@ -318,3 +351,28 @@ def test_attention_of_a_prompt_chunk(lib, Q, kv, g, Hkv, B):
                             *cache.codes, *cache.scale, cache.table, [n] * B,
                             [1] * B, 0.125)
         _check_attn("bf16", D, n, out[:, i:i + 1], lse[:, i:i + 1], ref)
+
+
+@pytest.mark.parametrize("dtype,g", [("bf16", 2), ("bf16", 30), ("fp32", 2)])
+def test_attention_counts_a_bad_page_as_zeros(lib, dtype, g):
+    """A page id outside the pool: flagged, and its tokens have keys and
+    values of 0 (a score of 0, a share of the sum)."""
+    rng = np.random.default_rng(41)
+    n, D, page = 200, 64, 16
+    cache = Cache([n], page, 1, D, rng)
+    q = torch.tensor(rng.standard_normal((1, 2, g, D)),
+                     dtype=torch.float32).to(DT[dtype])
+    ids = cache.table[0]
+    for c, s in zip(cache.codes, cache.scale):
+        c[ids[3]] = 0
+        s[ids[3]] = 1.0
+    ref = to.paged_attn(q.float().numpy().astype(np.float64), *cache.codes,
+                        *cache.scale, cache.table, [n], [2], 0.1)
+    for bad in (-1, len(cache.scale[0]), 1 << 30):
+        cache.table = cache.table.copy()
+        cache.table[0, 3] = bad
+        out, lse = _attend(lib, dtype, cache, q.cuda(), [n], None, True, 0.1)
+        with pytest.raises(lib.DFlashError) as e:
+            lib.dflash_check()
+        assert e.value.status == 6             # DFLASH_ERR_BAD_INDEX
+        _check_attn(dtype, D, n, out, lse, ref)
