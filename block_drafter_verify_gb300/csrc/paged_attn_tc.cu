@@ -1120,13 +1120,15 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
           for (int r = 0; r < HR; r += 4) {
             const float4 d =
                 *reinterpret_cast<const float4*>(&m.fac[row_of(r)]);
-            // in two factors: the sums may hold what the weights do not
+            // In two factors: the sums may hold what the weights do not.  A
+            // reference falls only in the first tile, where there is nothing
+            // to scale yet (2^d may pass fp32's range).
             const float e[4] = {d.x, d.y, d.z, d.w};
             float f[4], f2[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               y[r + k] += e[k];
-              f[k] = tc::ex2_approx(fmaxf(e[k], -100.f));
+              f[k] = tc::ex2_approx(fminf(fmaxf(e[k], -100.f), 0.f));
               f2[k] = tc::ex2_approx(fminf(e[k] + 100.f, 0.f));
             }
 #pragma unroll

@@ -376,3 +376,31 @@ def test_attention_counts_a_bad_page_as_zeros(lib, dtype, g):
             lib.dflash_check()
         assert e.value.status == 6             # DFLASH_ERR_BAD_INDEX
         _check_attn(dtype, D, n, out, lse, ref)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("g,n,B", [(4, 1, 1), (4, 300, 1), (20, 300, 3),
+                                   (4, 20000, 1), (40, 900, 2)])
+@pytest.mark.parametrize("size", [-5000.0, -300.0, -85.0, 85.0, 300.0, 5000.0])
+def test_attention_far_scores(lib, dtype, g, n, B, size):
+    """Rows whose scores all lie far below 0, or far above: 2^-score and
+    2^score pass fp32's range, the softmax does not."""
+    rng = np.random.default_rng(n + g)
+    D, page = 64, 32
+    cache = Cache([n] * B, page, 1, D, rng, spread=0)
+    keys = cache.table[:, :-(-n // page)].ravel()
+    x = np.full(cache.codes[0][keys].shape, 100.0)     # all keys alike but
+    x[..., 0] += 8 * rng.integers(-3, 4, x.shape[:-1])  # for one dimension
+    bits = oracle.e4m3_encode(x.astype(np.float32))
+    tail = cache.codes[0][keys] == 0x7F                # past the lengths
+    cache.codes[0][keys] = np.where(tail, 0x7F, bits)
+    cache.scale[0][keys] = 2.0 ** -6
+    q = torch.tensor(rng.uniform(1, 2, (B, 1, g, D)), dtype=torch.float32).to(
+        DT[dtype])
+    scale = size / float(q[0, 0, 0].double().sum() * 100 / 64)
+    out, lse = _attend(lib, dtype, cache, q.cuda(), [n] * B, None, True, scale)
+    lib.dflash_check()
+    ref = to.paged_attn(q.float().numpy().astype(np.float64), *cache.codes,
+                        *cache.scale, cache.table, [n] * B, [1] * B, scale)
+    assert np.all(np.isfinite(ref[1])) and np.abs(ref[1]).max() > 60
+    _check_attn(dtype, D, n, out, lse, ref)
