@@ -25,8 +25,8 @@
 //        of the weight rounded to fp16 a part is that byte after rounding, the
 //        rest an exact fp16 difference, and three parts of three bits and a
 //        sign hold its eleven bits; the fourth is the upper byte of what fp16
-//        rounded off.  That takes no conversion to 8 bits (parts made by those took
-//        1200 cycles a tile of 80 rows), and no part needs a scale of its
+//        rounded off.  That takes no conversion to 8 bits (parts made by those
+//        took 1200 cycles a tile of 80 rows), and no part needs a scale of its
 //        own.  Without the fourth part: 2^-11, and 2 to 7 % less time.
 // Scores are computed transposed: S^T[token, row] = K q^T and
 // O^T[dim, row] = V^T P^T, so that the 128 lanes of an MMA are always full
@@ -83,7 +83,7 @@ constexpr float kFarLv = 90.f;
 constexpr float kRaise = 15.75f;   // 2^15.75 = 55109 < 57344, E5M2's largest
 constexpr int kUnitCost = 4;       // of a unit besides its tiles, in tiles
 constexpr int kParts = 4;          // E5M2 parts of a weight
-constexpr int kRowsApart = 4;      // bits below the unit's for a scale of its own
+constexpr int kRowsApart = 4;      // bits below the unit's: a scale of its own
 
 // Shared-memory plan for N rows.
 template <int N>
