@@ -16,7 +16,10 @@ from .binding import (BF16, C, COMMIT_STATS, FP32, STAGES, DFlashError,
                       dflash_verify_shard_draw, SHARD_STATS, SHARD_PLAN,
                       dflash_kv_append, dflash_paged_attn,
                       dflash_paged_attn_workspace_bytes, dflash_sample,
-                      dflash_sample_workspace_bytes,
+                      dflash_sample_workspace_bytes, dflash_kv_append_axes,
+                      dflash_shared_attn, dflash_shared_attn_workspace_bytes,
+                      dflash_attn_mass, dflash_kv_evict,
+                      dflash_kv_evict_workspace_bytes, dflash_logprobs,
                       library_path, load)
 
 __all__ = ["BF16", "C", "COMMIT_STATS", "FP32", "STAGES", "DFlashError",
@@ -31,4 +34,8 @@ __all__ = ["BF16", "C", "COMMIT_STATS", "FP32", "STAGES", "DFlashError",
            "dflash_verify_shard_decide", "dflash_verify_shard_draw",
            "dflash_kv_append", "dflash_paged_attn",
            "dflash_paged_attn_workspace_bytes", "dflash_sample",
-           "dflash_sample_workspace_bytes", "SHARD_STATS", "SHARD_PLAN", "library_path", "load"]
+           "dflash_sample_workspace_bytes", "dflash_kv_append_axes",
+           "dflash_shared_attn", "dflash_shared_attn_workspace_bytes",
+           "dflash_attn_mass", "dflash_kv_evict",
+           "dflash_kv_evict_workspace_bytes", "dflash_logprobs",
+           "SHARD_STATS", "SHARD_PLAN", "library_path", "load"]

@@ -29,7 +29,11 @@ EXPORTS = ("dflash_workspace_bytes", "dflash_lmhead_topk", "dflash_pair_score",
            "dflash_verify_shard_decide", "dflash_verify_shard_draw",
            "dflash_kv_append", "dflash_paged_attn_workspace_bytes",
            "dflash_paged_attn", "dflash_sample_workspace_bytes",
-           "dflash_sample", "dflash_check", "dflash_status_string")
+           "dflash_sample", "dflash_kv_append_axes",
+           "dflash_shared_attn_workspace_bytes", "dflash_shared_attn",
+           "dflash_attn_mass", "dflash_kv_evict_workspace_bytes",
+           "dflash_kv_evict", "dflash_logprobs", "dflash_check",
+           "dflash_status_string")
 STAGES = ("conv", "lmhead", "merge", "pair_score", "walk", "verify",
           "quant")
 
@@ -108,6 +112,19 @@ def load(path: str | None = None):
         "dflash_sample_workspace_bytes": (sz, [i32, i32]),
         "dflash_sample": (i32, [vp, i64, i32, vp, vp, vp, vp, vp, i32, i32,
                                 vp, vp, vp, vp, sz, vp]),
+        "dflash_kv_append_axes": (i32, [vp, vp, vp, i64, i64, i64] +
+                                  [vp] * 4 + [i32] + [vp] * 3 + [i32] * 12 +
+                                  [vp] * 7),
+        "dflash_shared_attn_workspace_bytes": (sz, [i32] * 5),
+        "dflash_shared_attn": (i32, [vp] * 8 + [i32] * 10 +
+                               [f32, i32, vp, vp, vp, sz, vp]),
+        "dflash_attn_mass": (i32, [vp] * 8 + [i32] * 10 +
+                             [f32, f32, i32, vp, i64, vp]),
+        "dflash_kv_evict_workspace_bytes": (sz, [i32] * 4),
+        "dflash_kv_evict": (i32, [vp, i64] + [vp] * 6 + [i32] * 9 +
+                            [vp, i64, vp, vp, vp, sz, vp]),
+        "dflash_logprobs": (i32, [vp, i64, i32, vp, vp, i32, i32, i32] +
+                            [vp] * 7),
         "dflash_check": (i32, [vp]),
         "dflash_status_string": (ctypes.c_char_p, [i32]),
     }
@@ -485,16 +502,10 @@ def _check_cache(k_codes, v_codes, k_scale, v_scale):
 _F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
 
 
-def dflash_kv_append(q, k, v, cos, sin, pos, n_new, page_table, k_codes,
-                     v_codes, k_scale, v_scale, q_out, kv_len,
-                     interleaved=False, stream=None):
-    """Rotate q and k by position and append k and v to the cache, in place.
-    q [B*Q,Hq,D] or None, k and v [B*Q,Hkv,D] (rows may lie apart, as parts
-    of one projection's output); cos, sin [max_pos,rot/2] f32 or None (no
-    rotation); pos [B] i32: tokens already committed; n_new [B] i32 or None
-    (Q each); page_table [B,max_pages] i32; k_codes, v_codes
-    [num_pages,Hkv,page,D] u8, k_scale, v_scale [num_pages,Hkv] f32 in/out;
-    q_out [B,Q,Hq,D] and kv_len [B] i32 outputs."""
+def _append(name, axes, q, k, v, cos, sin, pos, n_new, page_table, k_codes,
+            v_codes, k_scale, v_scale, q_out, kv_len, interleaved, stream):
+    """Both appends; axes: what dflash_kv_append_axes has besides, given the
+    number of rows."""
     N, Hkv, page, D = _check_cache(k_codes, v_codes, k_scale, v_scale)
     B, max_pages = page_table.shape
     dt = k.dtype
@@ -520,14 +531,51 @@ def dflash_kv_append(q, k, v, cos, sin, pos, n_new, page_table, k_codes,
             raise ValueError("cos and sin must have one shape")
         rot *= 2
         cp, sp = _at(cos, _F32, "cos"), _at(sin, _F32, "sin")
-    _run("dflash_kv_append", load().dflash_kv_append(
-        qp, kp, vp, ld_q, ld_k, ld_v, cp, sp, _at(pos, _I32, "pos"),
+    _run(name, getattr(load(), name)(
+        qp, kp, vp, ld_q, ld_k, ld_v, cp, sp,
+        *(axes(rows, rot) if axes else ()), _at(pos, _I32, "pos"),
         None if n_new is None else _at(n_new, _I32, "n_new"),
         _at(page_table, _I32, "page_table"), B, rows // B, Hq, Hkv, D, rot,
         1 if interleaved else 0, max_pos, page, N, max_pages, _dtype(k), qo,
         _at(k_codes, _U8, "k_codes"), _at(v_codes, _U8, "v_codes"),
         _at(k_scale, _F32, "k_scale"), _at(v_scale, _F32, "v_scale"),
         _at(kv_len, _I32, "kv_len"), _on(stream)))
+
+
+def dflash_kv_append(q, k, v, cos, sin, pos, n_new, page_table, k_codes,
+                     v_codes, k_scale, v_scale, q_out, kv_len,
+                     interleaved=False, stream=None):
+    """Rotate q and k by position and append k and v to the cache, in place.
+    q [B*Q,Hq,D] or None, k and v [B*Q,Hkv,D] (rows may lie apart, as parts
+    of one projection's output); cos, sin [max_pos,rot/2] f32 or None (no
+    rotation); pos [B] i32: tokens already committed; n_new [B] i32 or None
+    (Q each); page_table [B,max_pages] i32; k_codes, v_codes
+    [num_pages,Hkv,page,D] u8, k_scale, v_scale [num_pages,Hkv] f32 in/out;
+    q_out [B,Q,Hq,D] and kv_len [B] i32 outputs."""
+    _append("dflash_kv_append", None, q, k, v, cos, sin, pos, n_new,
+            page_table, k_codes, v_codes, k_scale, v_scale, q_out, kv_len,
+            interleaved, stream)
+
+
+def dflash_kv_append_axes(q, k, v, cos, sin, axis_pos, axis_of, pos, n_new,
+                          page_table, k_codes, v_codes, k_scale, v_scale,
+                          q_out, kv_len, interleaved=False, stream=None):
+    """dflash_kv_append with positions of their own: axis_pos [axes,B*Q] i32,
+    axis_of [rot/2] u8 the axis of each angle (None with one axis); pos [B]
+    i32 is the slot of a sequence's first new token only."""
+    A = axis_pos.shape[0]
+
+    def axes(rows, rot):
+        if axis_pos.numel() != A * rows:
+            raise ValueError("axis_pos must be [axes, B * Q]")
+        if axis_of is not None and axis_of.numel() != rot // 2:
+            raise ValueError("axis_of must be [rot / 2]")
+        return (_at(axis_pos, _I32, "axis_pos"),
+                None if axis_of is None else _at(axis_of, _U8, "axis_of"), A)
+
+    _append("dflash_kv_append_axes", axes, q, k, v, cos, sin, pos, n_new,
+            page_table, k_codes, v_codes, k_scale, v_scale, q_out, kv_len,
+            interleaved, stream)
 
 
 def dflash_paged_attn_workspace_bytes(B, Q, Hq, Hkv, D) -> int:
@@ -597,6 +645,144 @@ def dflash_sample(logits, temperature, top_k, top_p, min_p, u, token, n_kept,
         row(token, _I32, "token"), row(n_kept, _I32, "n_kept"),
         None if filtered is None else _at(filtered, _F32, "filtered"),
         _at(ws, _U8, "ws"), ws.numel(), _on(stream)))
+
+
+def dflash_shared_attn_workspace_bytes(B, Q, Hq, Hkv, D) -> int:
+    return int(load().dflash_shared_attn_workspace_bytes(B, Q, Hq, Hkv, D))
+
+
+def dflash_shared_attn(q, k_codes, v_codes, k_scale, v_scale, page_table,
+                       kv_len, q_len, shared, scale, out, lse, ws,
+                       causal=True, stream=None):
+    """dflash_paged_attn for sequences whose first `shared` tokens (whole
+    pages) are the first sequence's, read once for all; ws uint8 of
+    dflash_shared_attn_workspace_bytes."""
+    N, Hkv, page, D = _check_cache(k_codes, v_codes, k_scale, v_scale)
+    B, Q, Hq, Dq = q.shape
+    tB, max_pages = page_table.shape
+    if Dq != D or tB != B or out.shape != q.shape or (
+            kv_len.numel() != B) or (q_len is not None and
+                                     q_len.numel() != B):
+        raise ValueError("q, out, page_table, kv_len, q_len and the cache "
+                         "must agree in B and D")
+    if lse is not None and lse.numel() != B * Q * Hq:
+        raise ValueError("lse must be [B, Q, Hq]")
+    dt = q.dtype
+    _run("dflash_shared_attn", load().dflash_shared_attn(
+        _at(q, dt, "q"), _at(k_codes, _U8, "k_codes"),
+        _at(v_codes, _U8, "v_codes"), _at(k_scale, _F32, "k_scale"),
+        _at(v_scale, _F32, "v_scale"), _at(page_table, _I32, "page_table"),
+        _at(kv_len, _I32, "kv_len"),
+        None if q_len is None else _at(q_len, _I32, "q_len"), shared, B, Q,
+        Hq, Hkv, D, page, N, max_pages, 1 if causal else 0, scale, _dtype(q),
+        _at(out, dt, "out"), None if lse is None else _at(lse, _F32, "lse"),
+        _at(ws, _U8, "ws"), ws.numel(), _on(stream)))
+
+
+def _mass_rows(t, B, Hkv, name):
+    """Address and slots of a [B,Hkv,slots] f32 tensor."""
+    if len(t.shape) != 3 or t.shape[0] != B or t.shape[1] != Hkv:
+        raise ValueError(f"{name} must be [B, Hkv, slots]")
+    return _at(t, _F32, name), t.shape[2]
+
+
+def dflash_attn_mass(q, k_codes, k_scale, page_table, kv_len, q_len, lse,
+                     fresh, first, scale, decay, mass, causal=True,
+                     stream=None):
+    """Add the attention weights of q [B,Q,Hq,D] over the cached tokens to
+    mass [B,Hkv,slots] f32, in place; lse [B,Q,Hq] f32 from the attention of
+    these queries; fresh [B] i32 or None: slots from there on start at 0,
+    those below are multiplied by `decay` first; slots below `first` are left
+    as they are.  kv_len, q_len and causal as in dflash_paged_attn."""
+    N, Hkv, page, D = k_codes.shape
+    if k_scale.numel() != N * Hkv:
+        raise ValueError("scales must be [num_pages, Hkv]")
+    B, Q, Hq, Dq = q.shape
+    tB, max_pages = page_table.shape
+    if Dq != D or tB != B or kv_len.numel() != B or (
+            q_len is not None and q_len.numel() != B) or (
+            fresh is not None and fresh.numel() != B):
+        raise ValueError("q, page_table, kv_len, q_len, fresh and the cache "
+                         "must agree in B and D")
+    if lse.numel() != B * Q * Hq:
+        raise ValueError("lse must be [B, Q, Hq]")
+    mp, ld = _mass_rows(mass, B, Hkv, "mass")
+    _run("dflash_attn_mass", load().dflash_attn_mass(
+        _at(q, q.dtype, "q"), _at(k_codes, _U8, "k_codes"),
+        _at(k_scale, _F32, "k_scale"), _at(page_table, _I32, "page_table"),
+        _at(kv_len, _I32, "kv_len"),
+        None if q_len is None else _at(q_len, _I32, "q_len"),
+        _at(lse, _F32, "lse"),
+        None if fresh is None else _at(fresh, _I32, "fresh"), first, B, Q,
+        Hq, Hkv, D, page, N, max_pages, 1 if causal else 0, scale, decay,
+        _dtype(q), mp, ld, _on(stream)))
+
+
+def dflash_kv_evict_workspace_bytes(B, Hkv, page, budget) -> int:
+    return int(load().dflash_kv_evict_workspace_bytes(B, Hkv, page, budget))
+
+
+def dflash_kv_evict(mass, k_codes, v_codes, k_scale, v_scale, page_table,
+                    kv_len, budget, sink, recent, mass_out, new_len, kept,
+                    ws, stream=None):
+    """Bound every sequence's cache to `budget` tokens, in place: the first
+    `sink`, the last `recent` and those of largest mass [B,Hkv,slots] f32 of
+    each key head.  mass_out [B,Hkv,slots] f32 or None: the kept slots' mass
+    in their new places; new_len [B] i32 and kept [B,Hkv,budget] i32 (or
+    None) outputs; ws uint8 of dflash_kv_evict_workspace_bytes."""
+    N, Hkv, page, D = _check_cache(k_codes, v_codes, k_scale, v_scale)
+    B, max_pages = page_table.shape
+    if kv_len.numel() != B or new_len.numel() != B:
+        raise ValueError("kv_len and new_len must have B entries")
+    if kept is not None and kept.numel() != B * Hkv * budget:
+        raise ValueError("kept must be [B, Hkv, budget]")
+    mp, ld = _mass_rows(mass, B, Hkv, "mass")
+    op, ld_out = (None, 0) if mass_out is None else _mass_rows(
+        mass_out, B, Hkv, "mass_out")
+    _run("dflash_kv_evict", load().dflash_kv_evict(
+        mp, ld, _at(k_codes, _U8, "k_codes"),
+        _at(v_codes, _U8, "v_codes"), _at(k_scale, _F32, "k_scale"),
+        _at(v_scale, _F32, "v_scale"), _at(page_table, _I32, "page_table"),
+        _at(kv_len, _I32, "kv_len"), B, Hkv, D, page, N, max_pages, budget,
+        sink, recent, op, ld_out, _at(new_len, _I32, "new_len"),
+        None if kept is None else _at(kept, _I32, "kept"),
+        _at(ws, _U8, "ws"), ws.numel(), _on(stream)))
+
+
+def dflash_logprobs(logits, temperature, token, logprob, rank, lse, entropy,
+                    top, top_id, stream=None):
+    """Log probability and rank of the given token [R] i32 (-1: none) of each
+    row of logits [R,V] (rows may lie apart), the rows' logsumexp and
+    entropy, and the K most likely tokens: logprob, lse, entropy [R] f32, rank
+    [R] i32, top [R,K] f32, top_id [R,K] i32 outputs, each may be None;
+    temperature [R] f32 or None."""
+    R, V = logits.shape
+    ld, step = logits.stride()
+    if (step != 1 and V > 1) or not logits.is_cuda:
+        _rows(logits, logits.dtype, (V,), "logits")  # raises
+    if R == 1:
+        ld = V
+
+    def row(t, dtype, name):
+        if t is None:
+            return None
+        if t.numel() != R:
+            raise ValueError(f"{name} must have R entries")
+        return _at(t, dtype, name)
+
+    K = 0
+    if top is not None or top_id is not None:
+        if top is None or top_id is None or top.shape != top_id.shape or (
+                top.shape[:1] != (R,) or top.dim() != 2):
+            raise ValueError("top and top_id must both be [R, K]")
+        K = top.shape[1]
+    _run("dflash_logprobs", load().dflash_logprobs(
+        logits.data_ptr(), ld, _dtype(logits),
+        row(temperature, _F32, "temperature"), row(token, _I32, "token"), R,
+        V, K, row(logprob, _F32, "logprob"), row(rank, _I32, "rank"),
+        row(lse, _F32, "lse"), row(entropy, _F32, "entropy"),
+        _at(top, _F32, "top") if K else None,
+        _at(top_id, _I32, "top_id") if K else None, _on(stream)))
 
 
 def dflash_check(stream=None):

@@ -213,6 +213,40 @@ __device__ __forceinline__ int attn_clamp(int x, long long most, bool* bad) {
   return x < 0 ? 0 : x > most ? (int)most : x;
 }
 
+// attn_mass.cu ---------------------------------------------------------------
+// Arguments of the kernels that gather attention weight (dflash_attn_mass's).
+struct AttnMassArgs {
+  const void* q;
+  const uint8_t* k_codes;
+  const float* k_scale;
+  const int *table, *kv_len, *q_len;  // q_len may be NULL
+  const float* lse;
+  const int* fresh;                   // may be NULL
+  int first;
+  int B, Q, Hq, Hkv, D, page, num_pages, max_pages, causal;
+  float scale, decay;
+  float* mass;
+  long long ld_mass;
+  int* err;
+  uint64_t wait_ns;
+};
+// Tokens that a sequence can have: those of its pages, and of a row of mass.
+__host__ __device__ inline long long mass_most(const AttnMassArgs& a) {
+  const long long most = (long long)a.max_pages * a.page;
+  return most < a.ld_mass ? most : a.ld_mass;
+}
+__device__ __forceinline__ int mass_length(const AttnMassArgs& a, int b,
+                                           bool* bad) {
+  return attn_clamp(a.kv_len[b], mass_most(a), bad);
+}
+// The weight that token t of sequence b and key head hk got from this call.
+__device__ __forceinline__ void mass_store(const AttnMassArgs& a, int b,
+                                           int hk, int t, float sum) {
+  float* to = a.mass + ((long long)b * a.Hkv + hk) * a.ld_mass + t;
+  const bool old = !a.fresh || t < a.fresh[b];
+  *to = old ? fmaf(a.decay, *to, sum) : sum;
+}
+
 // philox --------------------------------------------------------------------
 cudaError_t launch_philox(const uint32_t* ctr, uint64_t seed, uint32_t* out,
                           int64_t n, cudaStream_t s);

@@ -23,6 +23,10 @@
 // bytes: they wait for lengths, page ids, values and each other), which the
 // rotation's traffic fills where both alternate; one kind after the other took
 // 69 us.  Three CTAs to an SM: two 80 us, four (64 registers) 72 us.
+//
+// With positions of several axes a token's angles come from a row of the tables
+// for each axis; a thread's four or eight angles lie in one section, which costs
+// it one more load, or (axes in turn) are gathered one by one.
 #include <cuda_fp8.h>
 
 #include "kernels.h"
@@ -67,6 +71,9 @@ struct AppendArgs {
   const void* q;
   long long ld_q;
   const float *cos_tab, *sin_tab;
+  const int* axis_pos;        // [axes, B * Q] positions, or NULL: the slots
+  const uint8_t* axis_of;     // [rot / 2] the angles' axes, or NULL: all 0
+  int axes;
   const int *pos, *n_new, *table;
   int B, Q, Hq, Hkv, D, rot, max_pos, page, num_pages, max_pages;
   void* q_out;
@@ -229,7 +236,51 @@ __device__ __forceinline__ uint32_t requant4(uint32_t w, float ratio) {
   return out;
 }
 
+// Angles [first, first + VEC) of the token in row `row` of q, k and v that
+// goes to slot `slot`.
+template <int VEC, bool kAxes>
+__device__ __forceinline__ void load_angles(const AppendArgs& a, long long row,
+                                            long long slot, int first,
+                                            float (&c)[VEC], float (&s)[VEC]) {
+  const int r2 = a.rot / 2;
+  if constexpr (!kAxes) {
+    const size_t at = (size_t)slot * r2 + first;
+    load_n<float, VEC>(a.cos_tab + at, c);
+    load_n<float, VEC>(a.sin_tab + at, s);
+  } else {
+    uint32_t w[VEC / 4];                 // the angles' axes, a byte each
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i)
+      w[i] = a.axis_of ? reinterpret_cast<const uint32_t*>(a.axis_of +
+                                                           first)[i]
+                       : 0;
+    auto row_of = [&](uint32_t axis) {   // of the tables
+      bool bad = axis >= (uint32_t)a.axes;
+      const long long p =
+          a.axis_pos[(bad ? 0ll : (long long)axis) * a.B * a.Q + row];
+      bad = bad || p < 0 || p >= a.max_pos;
+      if (bad) raise_error(a.err, kErrBadIndex);
+      return p < 0 ? 0ll : p >= a.max_pos ? a.max_pos - 1ll : p;
+    };
+    const uint32_t axis = w[0] & 0xff;
+    if (w[0] == axis * 0x01010101u && w[VEC / 4 - 1] == w[0]) {
+      const size_t at = (size_t)row_of(axis) * r2 + first;
+      load_n<float, VEC>(a.cos_tab + at, c);
+      load_n<float, VEC>(a.sin_tab + at, s);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const size_t at =
+            (size_t)row_of(w[i / 4] >> (8 * (i % 4)) & 0xff) * r2 + first + i;
+        c[i] = a.cos_tab[at];
+        s[i] = a.sin_tab[at];
+      }
+    }
+  }
+}
+
 // New tokens of sequence b that fit: clamped to the tables; *bad if not all.
+template <bool kAxes>
 __device__ __forceinline__ int live_tokens(const AppendArgs& a, int b,
                                            int* pos_out, bool* bad) {
   const int pos = a.pos[b];
@@ -241,7 +292,7 @@ __device__ __forceinline__ int live_tokens(const AppendArgs& a, int b,
     return 0;
   }
   long long most = (long long)a.max_pages * a.page;
-  if (a.rot > 0 && a.max_pos < most) most = a.max_pos;
+  if (!kAxes && a.rot > 0 && a.max_pos < most) most = a.max_pos;
   const long long room = most - pos;
   if (n > room) {
     *bad = true;
@@ -250,14 +301,13 @@ __device__ __forceinline__ int live_tokens(const AppendArgs& a, int b,
   return n;
 }
 
-template <typename T, int VEC, bool kInter>
+template <typename T, int VEC, bool kInter, bool kAxes>
 __global__ void __launch_bounds__(kThreads, 3)
     kv_append_kernel(const __grid_constant__ AppendArgs a) {
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, nt = blockDim.x;
   const int units = a.D / (2 * VEC);
-  const int r2 = a.rot / 2;
   // The CTAs of both kinds alternate evenly, so that the rotation's traffic
   // fills the waits of the cache's: of the first x, x share / 2^32 are the
   // cache's (share: the part of 2^32, rounded up, that they are of the grid).
@@ -274,14 +324,11 @@ __global__ void __launch_bounds__(kThreads, 3)
     const long long row = row_of;
     int pos;
     bool bad;
-    const bool live = j < live_tokens(a, b, &pos, &bad);
+    const bool live = j < live_tokens<kAxes>(a, b, &pos, &bad);
     const Unit un = unit_at<VEC, kInter>(u, a.rot);
     float c[VEC], s[VEC];
-    if (live && un.angle >= 0) {
-      const size_t at = (size_t)(pos + j) * r2 + un.angle;
-      load_n<float, VEC>(a.cos_tab + at, c);
-      load_n<float, VEC>(a.sin_tab + at, s);
-    }
+    if (live && un.angle >= 0)
+      load_angles<VEC, kAxes>(a, row, pos + j, un.angle, c, s);
     const T* src = static_cast<const T*>(a.q) + row * a.ld_q;
     T* dst = static_cast<T*>(a.q_out) + row * a.Hq * a.D;
     const int h1 = min(a.Hq, (hg + 1) * kHeads);
@@ -316,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   const int t = a.seqs.split(b);
   int pos;
   bool bad;
-  const int n = live_tokens(a, b, &pos, &bad);
+  const int n = live_tokens<kAxes>(a, b, &pos, &bad);
   if (t == 0 && h == 0 && kv == 0 && tid == 0) {
     a.kv_len[b] = pos + n;
     if (bad) raise_error(a.err, kErrBadIndex);
@@ -344,9 +391,9 @@ __global__ void __launch_bounds__(kThreads, 3)
     load_n<T, VEC>(p + un.d1, y);
     if (turn && un.angle >= 0) {
       float c[VEC], s[VEC];
-      const size_t at = (size_t)(start + first + j) * r2 + un.angle;
-      load_n<float, VEC>(a.cos_tab + at, c);
-      load_n<float, VEC>(a.sin_tab + at, s);
+      const long long slot = start + first + j;
+      load_angles<VEC, kAxes>(a, (long long)b * a.Q + (slot - pos), slot,
+                              un.angle, c, s);
       rotate<VEC, kInter>(x, y, c, s);
     }
   };
@@ -485,26 +532,27 @@ cudaError_t launch(const AppendArgs& a, bool inter, cudaStream_t s) {
   args.share = (uint32_t)((((unsigned long long)cache << 32) + cache + rot - 1) /
                           (unsigned long long)(cache + rot));
   PdlLaunch L(dim3((unsigned)(cache + rot)), dim3(nt), 0, s);
-  return inter ? cudaLaunchKernelEx(&L.cfg, kv_append_kernel<T, VEC, true>, args)
-               : cudaLaunchKernelEx(&L.cfg, kv_append_kernel<T, VEC, false>, args);
+  auto* f = a.axis_pos ? inter ? kv_append_kernel<T, VEC, true, true>
+                               : kv_append_kernel<T, VEC, false, true>
+            : inter    ? kv_append_kernel<T, VEC, true, false>
+                       : kv_append_kernel<T, VEC, false, false>;
+  return cudaLaunchKernelEx(&L.cfg, f, args);
 }
 
 inline bool aligned_to(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
 }
 
-}  // namespace
-}  // namespace dflash
-
-extern "C" dflash_status dflash_kv_append(
+// Both entry points; axis_pos NULL: positions are the slots.
+dflash_status append(
     const void* q, const void* k, const void* v, int64_t ld_q, int64_t ld_k,
     int64_t ld_v, const float* cos_tab, const float* sin_tab,
+    const int32_t* axis_pos, const uint8_t* axis_of, int axes,
     const int32_t* pos, const int32_t* n_new, const int32_t* page_table,
     int B, int Q, int Hq, int Hkv, int D, int rot, int interleaved,
     int max_pos, int page, int num_pages, int max_pages, dflash_dtype dt,
     void* q_out, uint8_t* k_codes, uint8_t* v_codes, float* k_scale,
     float* v_scale, int32_t* kv_len, dflash_stream_t stream) {
-  using namespace dflash;
   if (!(k && v && pos && page_table && k_codes && v_codes && k_scale &&
         v_scale && kv_len) || kv_len == pos)
     return DFLASH_ERR_INVALID_ARG;
@@ -537,6 +585,9 @@ extern "C" dflash_status dflash_kv_append(
   a.ld_q = ld_q;
   a.cos_tab = cos_tab;
   a.sin_tab = sin_tab;
+  a.axis_pos = axis_pos;
+  a.axis_of = axis_of;
+  a.axes = axes;
   a.pos = pos;
   a.n_new = n_new;
   a.table = page_table;
@@ -575,4 +626,41 @@ extern "C" dflash_status dflash_kv_append(
   return e == cudaSuccess            ? DFLASH_OK
          : e == cudaErrorNotSupported ? DFLASH_ERR_UNSUPPORTED
                                       : DFLASH_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace dflash
+
+extern "C" dflash_status dflash_kv_append(
+    const void* q, const void* k, const void* v, int64_t ld_q, int64_t ld_k,
+    int64_t ld_v, const float* cos_tab, const float* sin_tab,
+    const int32_t* pos, const int32_t* n_new, const int32_t* page_table,
+    int B, int Q, int Hq, int Hkv, int D, int rot, int interleaved,
+    int max_pos, int page, int num_pages, int max_pages, dflash_dtype dt,
+    void* q_out, uint8_t* k_codes, uint8_t* v_codes, float* k_scale,
+    float* v_scale, int32_t* kv_len, dflash_stream_t stream) {
+  return dflash::append(q, k, v, ld_q, ld_k, ld_v, cos_tab, sin_tab, nullptr,
+                        nullptr, 0, pos, n_new, page_table, B, Q, Hq, Hkv, D,
+                        rot, interleaved, max_pos, page, num_pages, max_pages,
+                        dt, q_out, k_codes, v_codes, k_scale, v_scale, kv_len,
+                        stream);
+}
+
+extern "C" dflash_status dflash_kv_append_axes(
+    const void* q, const void* k, const void* v, int64_t ld_q, int64_t ld_k,
+    int64_t ld_v, const float* cos_tab, const float* sin_tab,
+    const int32_t* axis_pos, const uint8_t* axis_of, int axes,
+    const int32_t* pos, const int32_t* n_new, const int32_t* page_table,
+    int B, int Q, int Hq, int Hkv, int D, int rot, int interleaved,
+    int max_pos, int page, int num_pages, int max_pages, dflash_dtype dt,
+    void* q_out, uint8_t* k_codes, uint8_t* v_codes, float* k_scale,
+    float* v_scale, int32_t* kv_len, dflash_stream_t stream) {
+  if (!axis_pos || axes < 1 || axes > DFLASH_MAX_AXES || rot < 8 ||
+      (axes > 1 && !axis_of) || !dflash::aligned_to(axis_of, 8))
+    return DFLASH_ERR_INVALID_ARG;
+  return dflash::append(q, k, v, ld_q, ld_k, ld_v, cos_tab, sin_tab, axis_pos,
+                        axis_of, axes, pos, n_new, page_table, B, Q, Hq, Hkv,
+                        D, rot, interleaved, max_pos, page, num_pages,
+                        max_pages, dt, q_out, k_codes, v_codes, k_scale,
+                        v_scale, kv_len, stream);
 }

@@ -1,0 +1,494 @@
+// Log probabilities of given tokens, their ranks, the rows' entropies and
+// their most likely tokens.
+//
+// Mathematics.  With x = l / T, m = max l, d = (l - m) / T, w = exp(d):
+//   lse = m / T + ln S,  S = sum w;   ln p_v = d_v - ln S;
+//   entropy = ln S - (sum w d) / S.
+// One pass keeps m, S and U = sum w d of what a thread has seen; when m grows
+// by h / T, U becomes f (U - S h / T) and S f S with f = exp(-h / T), and two
+// threads' sums join likewise.  A token's rank is the number of tokens before it
+// in the order (logit descending, id ascending), so its logit is fetched first
+// and the pass counts.
+//
+// The K most likely: the K-th largest maximum of 64 groups of threads bounds
+// the K-th largest logit of the slice from below; only the groups that reach it
+// read their parts again, from L2, for the few more than K candidates, which are
+// ranked by counting.  A cluster of CTAs owns a row; the first of them joins the
+// CTAs' sums and lists.  What overflows the list (ties by the thousand) is found
+// by K searches for the next largest instead.
+//
+// What bounds it: bytes in batches, the chain of dependent steps for one row.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "kernels.h"
+#include "tc_ptx.cuh"
+
+namespace dflash {
+
+// SM count and device error word of the current device (api.cu).
+dflash_status current_device_info(int* sms, int** err);
+
+namespace {
+
+namespace cg = cooperative_groups;
+using u64 = unsigned long long;
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kGroups = 64;     // of threads, for the bound of the top K
+constexpr int kGroupOf = kThreads / kGroups;
+constexpr int kMost = DFLASH_MAX_ALTERNATIVES;
+constexpr int kList = 1024;     // candidates of a CTA
+constexpr int kMaxCluster = 8;
+constexpr float kLog2e = 1.4426950408889634f;
+static_assert(kMost <= kGroups, "");
+
+struct Args {
+  const void* logits;
+  long long ld;
+  const float* temperature;
+  const int* token;
+  int R, V, K, slice;   // slice: tokens per CTA
+  float *logprob, *lse, *entropy, *top;
+  int *rank, *top_id;
+  int* err;
+};
+
+// m: largest logit; s, u: sums of w and of w (l - m), not yet over T.
+struct Sums {
+  float m, s, u;
+};
+__device__ __forceinline__ Sums join(const Sums& a, const Sums& b, float c) {
+  if (a.m == -INFINITY) return b;
+  if (b.m == -INFINITY) return a;
+  const Sums& x = a.m >= b.m ? a : b;
+  const Sums& y = a.m >= b.m ? b : a;
+  const float h = y.m - x.m;
+  if (!(h > -INFINITY)) return x;  // x.m is infinite
+  const float f = tc::ex2_approx(h * c);
+  return Sums{x.m, x.s + f * y.s, x.u + f * (y.u + h * y.s)};
+}
+
+// What the CTAs of a row hand to the first of them.
+struct Shared {
+  Sums sums[kMaxCluster];
+  int before[kMaxCluster];
+  int odd[kMaxCluster];
+  u64 top[kMaxCluster][kMost];
+  int n_top[kMaxCluster];
+  // this CTA's own
+  Sums warp_sums[kWarps];
+  int warp_before[kWarps], warp_odd[kWarps];
+  float group_max[kGroups];
+  float bound;
+  int listed;
+  u64 list[kList];
+  u64 warp_best[kWarps];
+};
+
+// Order-preserving key of a logit that is no NaN (equal for -0 and 0).
+__device__ __forceinline__ u64 word_of(float x, int id) {
+  const uint32_t w = __float_as_uint(x + 0.f);
+  return (u64)(w & 0x80000000u ? ~w : w | 0x80000000u) << 32 | (uint32_t)~id;
+}
+__device__ __forceinline__ float value_of(u64 word) {
+  const uint32_t k = (uint32_t)(word >> 32);
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+// A 16-byte word of logits, as fp32.
+template <typename T>
+struct Words {
+  static constexpr int N = 16 / sizeof(T);
+  __device__ static __forceinline__ void get(const uint4& w, float (&f)[N]) {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(x[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(x[i] << 16);
+        f[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
+      }
+    }
+  }
+};
+
+// max of two numbers; a NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+template <typename T, bool kTop, bool kRank>
+__global__ void __launch_bounds__(kThreads)
+    logprobs_kernel(const __grid_constant__ Args a) {
+  constexpr int N = Words<T>::N;
+  constexpr int kAhead = 4;          // words in flight
+  extern __shared__ uint4 smem16[];
+  Shared& sh = *reinterpret_cast<Shared*>(smem16);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), me = (int)cluster.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  pdl_trigger();
+  pdl_wait();
+  const int r = blockIdx.x / C;
+  const T* row = static_cast<const T*>(a.logits) + (long long)r * a.ld;
+  float t = a.temperature ? a.temperature[r] : 1.f;
+  bool odd = false;
+  if (!(t >= 0x1p-126f && t < INFINITY)) {
+    odd = true;
+    t = 1.f;
+  }
+  const float c = kLog2e / t;
+  const int token = a.token ? a.token[r] : -1;
+  const bool given = token >= 0 && token < a.V;
+  const float mine = given ? to_f32(row[token]) : 0.f;
+
+  // Words of 16 bytes that start on a 16-byte boundary: word i holds tokens
+  // i N - skew .. of the row.  This CTA's are [w0, w1).
+  const int skew = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+  const T* base = row - skew;
+  const int words = (int)(((long long)a.V + skew + N - 1) / N);
+  const int per = a.slice / N;
+  const int w0 = min(words, me * per), w1 = min(words, w0 + per);
+  // whole words only; the others are read by token
+  const int full0 = skew ? 1 : 0, full1 = (int)(((long long)a.V + skew) / N);
+  auto whole = [&](int i) { return i >= full0 && i < full1; };
+  auto fetch = [&](int i) {
+    uint4 w;
+    if (whole(i)) {
+      w = __ldg(reinterpret_cast<const uint4*>(base) + i);
+    } else {                       // the row's ends, filled up with -inf
+      uint32_t x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 4) {
+          const long long v = (long long)i * 4 + j - skew;
+          x[j] = v >= 0 && v < a.V
+                     ? reinterpret_cast<const uint32_t*>(row)[v] : 0xff800000u;
+        } else {
+          x[j] = 0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const long long v = (long long)i * 8 + 2 * j + h - skew;
+            x[j] |= (uint32_t)(v >= 0 && v < a.V
+                                   ? reinterpret_cast<const uint16_t*>(row)[v]
+                                   : 0xff80u)
+                    << (16 * h);
+          }
+        }
+      }
+      w = make_uint4(x[0], x[1], x[2], x[3]);
+    }
+    return w;
+  };
+
+  Sums acc{-INFINITY, 0.f, 0.f};
+  int before = 0;
+  auto take = [&](const uint4 (&raw)[kAhead], int first, int n) {
+    float f[kAhead][N];
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (k >= n) break;
+      Words<T>::get(raw[k], f[k]);
+#pragma unroll
+      for (int j = 0; j < N; ++j) top = max_nan(top, f[k][j]);
+    }
+    if (top != top) {                // a NaN: left out
+      odd = true;
+      top = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (k >= n) break;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          if (f[k][j] != f[k][j]) f[k][j] = -INFINITY;
+          top = fmaxf(top, f[k][j]);
+        }
+      }
+    }
+    if (top > acc.m) {
+      const float h = acc.m - top;   // -inf at first, and before +inf
+      const float g = tc::ex2_approx(h * c);
+      acc.u = h > -INFINITY ? g * fmaf(h, acc.s, acc.u) : 0.f;
+      acc.s *= g;
+      acc.m = top;
+    }
+    const float ref = acc.m == -INFINITY ? 0.f : acc.m;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (k >= n) break;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        // (-inf: a weight of 0 times a number)
+        const float d = fmaxf(f[k][j] - ref, -1e30f);
+        const float w = tc::ex2_approx(d * c);
+        acc.s += w;
+        acc.u = fmaf(w, d, acc.u);
+      }
+      if constexpr (kRank) {
+        const long long at = ((long long)first + k * kThreads) * N - skew;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          before += f[k][j] > mine ||
+                    (f[k][j] == mine && at + j < token && at + j >= 0);
+      }
+    }
+  };
+  for (int i = w0 + tid; i < w1; i += kAhead * kThreads) {
+    uint4 raw[kAhead];
+    const int n = min(kAhead, (w1 - i + kThreads - 1) / kThreads);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (k < n) raw[k] = fetch(i + k * kThreads);
+    take(raw, i, n);
+  }
+
+  // ---- the CTA's sums ------------------------------------------------------
+  const float my_max = acc.m;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const Sums x{__shfl_xor_sync(0xffffffffu, acc.m, o),
+                 __shfl_xor_sync(0xffffffffu, acc.s, o),
+                 __shfl_xor_sync(0xffffffffu, acc.u, o)};
+    // the lower lane's first in both, so that both lanes get the same bits
+    acc = lane & o ? join(x, acc, c) : join(acc, x, c);
+    if (kRank) before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  odd = __any_sync(0xffffffffu, odd);
+  if (lane == 0) {
+    sh.warp_sums[warp] = acc;
+    sh.warp_before[warp] = before;
+    sh.warp_odd[warp] = odd;
+  }
+  if (kTop) {
+    float g = my_max;
+#pragma unroll
+    for (int o = kGroupOf / 2; o; o >>= 1)
+      g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+    if (tid % kGroupOf == 0) sh.group_max[tid / kGroupOf] = g;
+    if (tid == 0) sh.listed = 0;
+  }
+  __syncthreads();
+  Shared* first = cluster.map_shared_rank(&sh, 0);
+  if (tid < 32) {
+    Sums x = tid < kWarps ? sh.warp_sums[tid] : Sums{-INFINITY, 0.f, 0.f};
+    int b = tid < kWarps ? sh.warp_before[tid] : 0;
+    int o = tid < kWarps ? sh.warp_odd[tid] : 0;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+      const Sums y{__shfl_xor_sync(0xffffffffu, x.m, d),
+                   __shfl_xor_sync(0xffffffffu, x.s, d),
+                   __shfl_xor_sync(0xffffffffu, x.u, d)};
+      x = tid & d ? join(y, x, c) : join(x, y, c);
+      b += __shfl_xor_sync(0xffffffffu, b, d);
+      o |= __shfl_xor_sync(0xffffffffu, o, d);
+    }
+    // every CTA of the cluster has started
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    if (tid == 0) {
+      first->sums[me] = x;
+      first->before[me] = b;
+      first->odd[me] = o;
+    }
+  } else {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  }
+
+  // ---- the CTA's K most likely ------------------------------------------------
+  if (kTop) {
+    if (tid < kGroups) {             // the K-th largest maximum
+      const float g = sh.group_max[tid];
+      int above = 0;
+#pragma unroll 8
+      for (int i = 0; i < kGroups; ++i) {
+        const float x = sh.group_max[i];
+        above += x > g || (x == g && i < tid);
+      }
+      if (above == a.K - 1) sh.bound = g;
+    }
+    __syncthreads();
+    const float bound = sh.bound;
+    // -inf: fewer than K groups hold any token, so every token above -inf is
+    // a candidate
+    if (sh.group_max[tid / kGroupOf] >= bound && my_max >= bound &&
+        my_max > -INFINITY)
+      for (int i = w0 + tid; i < w1; i += kThreads) {
+        float f[N];
+        Words<T>::get(fetch(i), f);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (f[j] >= bound && f[j] > -INFINITY) {
+            const int at = atomicAdd(&sh.listed, 1);
+            if (at < kList)
+              sh.list[at] = word_of(f[j], (int)((long long)i * N + j - skew));
+          }
+      }
+    __syncthreads();
+    int n = sh.listed;
+    if (n <= kList) {
+      for (int i = tid; i < n; i += kThreads) {
+        const u64 x = sh.list[i];
+        int above = 0;
+        for (int j = 0; j < n; ++j) above += sh.list[j] > x;
+        if (above < a.K) first->top[me][above] = x;
+      }
+      n = min(n, a.K);
+    } else {                         // the next largest, K times
+      u64 last = ~0ull;
+      n = a.K;                       // there are more than kList
+      for (int k = 0; k < a.K; ++k) {
+        u64 best = 0;
+        for (int i = w0 + tid; i < w1; i += kThreads) {
+          float f[N];
+          Words<T>::get(fetch(i), f);
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if (f[j] > -INFINITY) {
+              const u64 x = word_of(f[j], (int)((long long)i * N + j - skew));
+              if (x < last && x > best) best = x;
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+          best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+        if (lane == 0) sh.warp_best[warp] = best;
+        __syncthreads();
+        for (int i = 0; i < kWarps; ++i) best = max(best, sh.warp_best[i]);
+        __syncthreads();
+        last = best;
+        if (tid == 0) first->top[me][k] = best;
+      }
+    }
+    if (tid == 0) first->n_top[me] = n;
+  }
+  cluster.sync();
+  if (me != 0) return;
+
+  // ---- the row -----------------------------------------------------------------
+  Sums x{-INFINITY, 0.f, 0.f};
+  int rank = 0, any_odd = 0;
+  for (int i = 0; i < C; ++i) {
+    x = join(x, sh.sums[i], c);
+    rank += sh.before[i];
+    any_odd |= sh.odd[i];
+  }
+  const bool empty = x.m == -INFINITY, infinite = x.m == INFINITY;
+  const float inv_t = 1.f / t;
+  const float log_s = logf(x.s);
+  const float nan = __int_as_float(0x7fffffff);
+  if (tid == 0) {
+    if (any_odd || empty || infinite) raise_error(a.err, kErrNonfinite);
+    if (token >= a.V || token < -1) raise_error(a.err, kErrBadIndex);
+    if (a.lse)
+      a.lse[r] = empty || infinite ? x.m : fmaf(x.m, inv_t, log_s);
+    if (a.entropy)
+      a.entropy[r] =
+          empty || infinite ? nan : fmaxf(log_s - x.u / x.s * inv_t, 0.f);
+    if (a.logprob)
+      a.logprob[r] = token == -1                    ? 0.f
+                     : !given || empty || infinite ? nan
+                                                   : (mine - x.m) / t - log_s;
+    if (kRank) a.rank[r] = given && mine == mine ? rank : -1;
+  }
+  if (kTop) {
+    const int lists = C * kMost;
+    for (int i = tid; i < a.K; i += kThreads) {
+      a.top[(long long)r * a.K + i] = -INFINITY;
+      a.top_id[(long long)r * a.K + i] = -1;
+    }
+    __syncthreads();
+    for (int i = tid; i < lists; i += kThreads) {
+      const int from = i / kMost, k = i % kMost;
+      if (k >= sh.n_top[from]) continue;
+      const u64 w = sh.top[from][k];
+      int above = k;                 // its own list is sorted
+      for (int j = 0; j < C; ++j)
+        if (j != from)
+          for (int q = 0; q < sh.n_top[j] && above < a.K; ++q) {
+            if (sh.top[j][q] < w) break;
+            ++above;
+          }
+      if (above < a.K) {
+        const float v = value_of(w);
+        a.top[(long long)r * a.K + above] =
+            infinite ? nan : (v - x.m) / t - log_s;
+        a.top_id[(long long)r * a.K + above] = (int)~(uint32_t)w;
+      }
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch(const Args& args, int sms, cudaStream_t s) {
+  Args a = args;
+  // CTAs of a row: as many as two an SM leave room for, with 4096 tokens each
+  int C = 1;
+  while (C < kMaxCluster && (long long)a.R * C < 2 * sms &&
+         a.V > 4096 * C)
+    C *= 2;
+  const int N = 16 / sizeof(T);
+  // (a row may start anywhere in its first word)
+  const long long words = ((long long)a.V + 2 * N - 2) / N;
+  a.slice = (int)((words + C - 1) / C * N);
+  if ((long long)a.R * C > 0x7fffffffll) return cudaErrorNotSupported;
+  const bool top = a.K > 0, rank = a.rank != nullptr;
+  auto* f = top ? rank ? logprobs_kernel<T, true, true>
+                       : logprobs_kernel<T, true, false>
+            : rank ? logprobs_kernel<T, false, true>
+                   : logprobs_kernel<T, false, false>;
+  PdlLaunch L(dim3((unsigned)(a.R * C)), dim3(kThreads), sizeof(Shared), s, C);
+  return cudaLaunchKernelEx(&L.cfg, f, a);
+}
+static_assert(sizeof(Shared) <= 48 * 1024, "");
+
+}  // namespace
+}  // namespace dflash
+
+extern "C" dflash_status dflash_logprobs(
+    const void* logits, int64_t ld, dflash_dtype dt, const float* temperature,
+    const int32_t* token, int R, int V, int K, float* logprob, int32_t* rank,
+    float* lse, float* entropy, float* top, int32_t* top_id,
+    dflash_stream_t stream) {
+  using namespace dflash;
+  if (!logits || (dt != DFLASH_BF16 && dt != DFLASH_FP32))
+    return DFLASH_ERR_INVALID_ARG;
+  if (R < 1 || V < 1 || V > 0x7fffff00 || ld < V || K < 0 || K > kMost)
+    return DFLASH_ERR_INVALID_ARG;
+  if ((logprob || rank) && !token) return DFLASH_ERR_INVALID_ARG;
+  if ((K > 0) != (top != nullptr) || (K > 0) != (top_id != nullptr))
+    return DFLASH_ERR_INVALID_ARG;
+  const uintptr_t size = dt == DFLASH_FP32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(logits) % size)
+    return DFLASH_ERR_INVALID_ARG;
+  int sms = 0;
+  Args a;
+  const dflash_status st = current_device_info(&sms, &a.err);
+  if (st != DFLASH_OK) return st;
+  a.logits = logits;
+  a.ld = ld;
+  a.temperature = temperature;
+  a.token = token;
+  a.R = R;
+  a.V = V;
+  a.K = K;
+  a.logprob = logprob;
+  a.lse = lse;
+  a.entropy = entropy;
+  a.top = top;
+  a.rank = rank;
+  a.top_id = top_id;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = dt == DFLASH_FP32 ? launch<float>(a, sms, s)
+                                          : launch<__nv_bfloat16>(a, sms, s);
+  return e == cudaSuccess            ? DFLASH_OK
+         : e == cudaErrorNotSupported ? DFLASH_ERR_UNSUPPORTED
+                                      : DFLASH_ERR_CUDA;
+}

@@ -12,7 +12,10 @@
  * or two: dflash_draft (the first three in one call, with the context gate
  * computed inside the conv launch) and dflash_verify.  Where the target model
  * runs in the same program, dflash_kv_append, dflash_paged_attn and
- * dflash_sample carry its share of the cycle.
+ * dflash_sample carry its share of the cycle; dflash_kv_append_axes,
+ * dflash_shared_attn, dflash_attn_mass, dflash_kv_evict and dflash_logprobs
+ * do so for targets with several position axes, batches under one prompt,
+ * caches of a bounded size, and answers with their probabilities.
  *
  * Sources (page title, section):
  *   "DFlash 2: Block diffusion, wearing a drafter's coat" — "Sixteen
@@ -87,6 +90,8 @@ typedef enum { DFLASH_BF16 = 0, DFLASH_FP32 = 1 } dflash_dtype;
 #define DFLASH_MAX_SHARDS 64   /* vocabulary shards of one merge / decide */
 #define DFLASH_SHARD_STATS 20  /* words per target row of shard statistics */
 #define DFLASH_SHARD_PLAN 8    /* words per sequence of a shard draw plan */
+#define DFLASH_MAX_AXES 4      /* position axes of dflash_kv_append_axes */
+#define DFLASH_MAX_ALTERNATIVES 32  /* most likely tokens of dflash_logprobs */
 
 /* Workspace needed by dflash_lmhead_topk (which = 0), dflash_verify
  * (which = 1), dflash_draft (which = 2) or dflash_draft_e4m3 (which = 3)
@@ -648,6 +653,168 @@ dflash_status dflash_sample(const void* logits, int64_t ld, dflash_dtype dt,
                             const float* u, int R, int V, int32_t* token,
                             int32_t* n_kept, float* filtered, void* ws,
                             size_t ws_bytes, dflash_stream_t s);
+
+/*
+ * dflash_kv_append_axes: dflash_kv_append with positions of their own, one to
+ * DFLASH_MAX_AXES of them for each token (time, height and width of images and
+ * video; with one axis, the true positions of a sequence whose cache was
+ * evicted, where slots are no positions any more).  Angle j of the token in row
+ * r of q and k is that of row axis_pos[axis_of[j], r] of the tables:
+ *   axis_pos [axes, B*Q] int32: the positions of every row (rows without a
+ *            token are not read)
+ *   axis_of  [rot/2] uint8: each angle's axis, in sections or in any other
+ *            order; NULL with one axis
+ *   pos      [B] int32: as in dflash_kv_append the slot of the first new token,
+ *            but not its position; the slots are not bounded by max_pos
+ * Everything else, results included, is as there.
+ * Requirements: as dflash_kv_append; rot >= 8, 1 <= axes <= DFLASH_MAX_AXES,
+ * axis_of 8-byte aligned.  On the device: a position outside [0, max_pos) (the
+ * nearest row is taken) and an axis_of entry of `axes` or more (axis 0 is
+ * taken) set DFLASH_ERR_BAD_INDEX.
+ */
+dflash_status dflash_kv_append_axes(
+    const void* q, const void* k, const void* v, int64_t ld_q, int64_t ld_k,
+    int64_t ld_v, const float* cos_tab, const float* sin_tab,
+    const int32_t* axis_pos, const uint8_t* axis_of, int axes,
+    const int32_t* pos, const int32_t* n_new, const int32_t* page_table,
+    int B, int Q, int Hq, int Hkv, int D, int rot, int interleaved,
+    int max_pos, int page, int num_pages, int max_pages, dflash_dtype dt,
+    void* q_out, uint8_t* k_codes, uint8_t* v_codes, float* k_scale,
+    float* v_scale, int32_t* kv_len, dflash_stream_t s);
+
+/* Workspace of dflash_shared_attn for these sizes in bytes; 0 for invalid
+ * sizes. */
+size_t dflash_shared_attn_workspace_bytes(int B, int Q, int Hq, int Hkv,
+                                          int D);
+
+/*
+ * dflash_shared_attn: dflash_paged_attn for a batch whose sequences all begin
+ * with the same `shared` tokens, in the same pages (one system prompt, several
+ * continuations of one request).  These are read once for the rows of all
+ * sequences together, each sequence's own tokens as before.  Same arguments,
+ * limits and results as dflash_paged_attn, up to the roundings of another
+ * order: kv_len, q_len and the positions count the shared tokens, and a query
+ * sees those of them at or before its own position (all of them below
+ * kv_len[b] if not causal).
+ *   shared      a whole number of pages, 0 for none; the first shared / page
+ *               entries of page_table are read from the first sequence's row
+ *               only, whatever the other rows hold there
+ *   ws >= dflash_shared_attn_workspace_bytes(B, Q, Hq, Hkv, D) bytes, 256-byte
+ *      aligned; its contents need no initialisation
+ * Requirements, and what is flagged on the device: as dflash_paged_attn;
+ * 0 <= shared <= max_pages * page, shared % page == 0.
+ */
+dflash_status dflash_shared_attn(
+    const void* q, const uint8_t* k_codes, const uint8_t* v_codes,
+    const float* k_scale, const float* v_scale, const int32_t* page_table,
+    const int32_t* kv_len, const int32_t* q_len, int shared, int B, int Q,
+    int Hq, int Hkv, int D, int page, int num_pages, int max_pages,
+    int causal, float scale, dflash_dtype dt, void* out, float* lse, void* ws,
+    size_t ws_bytes, dflash_stream_t s);
+
+/*
+ * dflash_attn_mass: the attention weight that each cached token gets from a
+ * block of queries, added to what it has gathered before.  For every sequence
+ * b, key head h and slot t with first <= t < kv_len[b]:
+ *     mass[b, h, t] = (t < fresh[b] ? decay * mass[b, h, t] : 0) +
+ *         sum exp(scale * <q_ij, k_t> - lse[b, i, j])
+ * over the queries i < q_len[b] that see t (causal or not, as in
+ * dflash_paged_attn) and the heads j of the group that reads key head h.  lse
+ * is what dflash_paged_attn or dflash_shared_attn gave for these queries, so
+ * the weights are the softmax's own; a query that saw nothing (lse = -inf)
+ * adds nothing.  Other slots of mass are left as they are.  Called after a
+ * verify with the committed lengths and q_len = n + 1, it counts the accepted
+ * queries only.
+ *   lse   [B, Q, Hq] fp32;  fresh [B] int32: the slots from which on there is
+ *         no weight yet (the length before the block), or NULL: kv_len
+ *   first slots below it are not looked at (those that an eviction keeps
+ *         anyway, for example a prefix that sequences share)
+ *   mass  [B, Hkv] rows of fp32, ld_mass elements apart, in/out
+ * Sums and weights are fp32; their order is fixed, and nothing is added
+ * atomically.
+ * Requirements: as dflash_paged_attn; first >= 0, ld_mass >= 1, decay finite.
+ * On the device: as dflash_paged_attn; a kv_len beyond ld_mass sets
+ * DFLASH_ERR_BAD_INDEX too (the length is clamped).
+ */
+dflash_status dflash_attn_mass(
+    const void* q, const uint8_t* k_codes, const float* k_scale,
+    const int32_t* page_table, const int32_t* kv_len, const int32_t* q_len,
+    const float* lse, const int32_t* fresh, int first, int B, int Q, int Hq,
+    int Hkv, int D, int page, int num_pages, int max_pages, int causal,
+    float scale, float decay, dflash_dtype dt, float* mass, int64_t ld_mass,
+    dflash_stream_t s);
+
+/* Workspace of dflash_kv_evict for these sizes in bytes; 0 for invalid
+ * sizes. */
+size_t dflash_kv_evict_workspace_bytes(int B, int Hkv, int page, int budget);
+
+/*
+ * dflash_kv_evict: bounds each sequence's cache to `budget` tokens, in place.
+ * A sequence with n = kv_len[b] > budget keeps, in every key head for itself,
+ * the slots below `sink`, those from n - recent on, and of the others the
+ * budget - sink - recent of largest mass (ties: the lower slot; a NaN is below
+ * all numbers and sets DFLASH_ERR_NONFINITE).  The kept tokens move to slots
+ * 0 .. budget - 1 in their order; keys stay turned by the positions that they
+ * were appended with, so append to such a sequence with
+ * dflash_kv_append_axes.  A sequence with n <= budget stays as it is.
+ *   mass     [B, Hkv] rows of fp32, ld_mass elements apart
+ *   mass_out [B, Hkv] rows, ld_out apart, or NULL: the kept slots' mass in
+ *            their new places [0, new_len[b]); must not overlap mass
+ *   new_len  [B] int32 out: min(n, budget); must not be kv_len itself
+ *   kept     [B, Hkv, budget] int32 out or NULL: the old slot of every new
+ *            one, -1 from new_len[b] on
+ *   codes and scales as in dflash_kv_append, in/out.  A page of which any slot
+ *   changes gets the least scale that its kept tokens need (a power of two
+ *   s >= 2^-64 with max |x| <= 448 s) and their codes rounded to it (exact but
+ *   for codes that become subnormal); other pages, and slots from new_len[b]
+ *   on, are left as they are (the latter's scale may change).
+ *   ws >= dflash_kv_evict_workspace_bytes(B, Hkv, page, budget) bytes, 256-byte
+ *      aligned; its contents need no initialisation
+ * Pages that this call changes belong to one sequence each: with a prefix that
+ * sequences share, sink covers it.  Whole pages past new_len[b] are free.
+ * Requirements: sink, recent >= 0, sink + recent <= budget, 1 <= budget <=
+ * 2^30, ld_mass >= 1, ld_out at least what the new lengths can be; codes
+ * 16-byte aligned; scales powers of two as dflash_kv_append writes them.  On
+ * the device: kv_len below 0 or beyond the page table or ld_mass sets
+ * DFLASH_ERR_BAD_INDEX (clamped), as does a page id outside [0, num_pages) (its
+ * tokens count as zeros; such a page is not written).
+ */
+dflash_status dflash_kv_evict(
+    const float* mass, int64_t ld_mass, uint8_t* k_codes, uint8_t* v_codes,
+    float* k_scale, float* v_scale, const int32_t* page_table,
+    const int32_t* kv_len, int B, int Hkv, int D, int page, int num_pages,
+    int max_pages, int budget, int sink, int recent, float* mass_out,
+    int64_t ld_out, int32_t* new_len, int32_t* kept, void* ws,
+    size_t ws_bytes, dflash_stream_t s);
+
+/*
+ * dflash_logprobs: what R rows of logits l say about given tokens and about
+ * themselves, with x = l / T:
+ *   lse     [R] ln sum_v exp(x_v)
+ *   logprob [R] x_token - lse, the token's log probability
+ *   rank    [R] int32: the tokens before it in the order (l descending, id
+ *           ascending); 0 is the most likely
+ *   entropy [R] -sum_v p_v ln p_v, p = exp(x - lse)
+ *   top, top_id [R, K]: log probabilities and ids of the first K tokens in that
+ *           order; where fewer than K have a logit above -inf, -inf and -1
+ *   logits [R, V] dtype, rows ld elements apart; temperature [R] fp32 or NULL
+ *   (1); token [R] int32 or NULL; each output may be NULL, logprob and rank
+ *   are without token, top and top_id with K = 0.  A token of -1 is none: its
+ *   logprob is 0, its rank -1 (so rows of dflash_verify's out_tok can be given
+ *   as they are).
+ * Requirements: R >= 1, 1 <= V < 2^31 - 256, ld >= V, 0 <= K <=
+ * DFLASH_MAX_ALTERNATIVES.  No workspace.
+ * A NaN logit counts as -inf (as a given token: logprob NaN, rank -1).  A row
+ * with a +inf logit has lse = +inf, one without any logit above -inf lse =
+ * -inf; both have NaN for entropy and log probabilities.  Those three, and a T
+ * that is below 2^-126 or not finite (taken as 1), set DFLASH_ERR_NONFINITE; a
+ * token outside [-1, V) sets DFLASH_ERR_BAD_INDEX (logprob NaN, rank -1).
+ */
+dflash_status dflash_logprobs(
+    const void* logits, int64_t ld, dflash_dtype dt, const float* temperature,
+    const int32_t* token, int R, int V, int K, float* logprob, int32_t* rank,
+    float* lse, float* entropy, float* top, int32_t* top_id,
+    dflash_stream_t s);
 
 /* Philox4x32-10 of n counters (ctr [n, 4] uint32, device) under key
  * (seed lo, seed hi) into out [n, 4] uint32 (device): the generator the
