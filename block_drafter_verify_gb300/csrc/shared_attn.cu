@@ -99,7 +99,10 @@ size_t dflash_shared_attn_workspace_bytes(int B, int Q, int Hq, int Hkv,
                                           int D) {
   using namespace dflash;
   if (!shared_sizes_ok(B, Q, Hq, Hkv, D)) return 0;
-  const size_t need = simt_ws(B, Q, Hq, Hkv, D);
+  // an upper bound over both dtypes
+  size_t need = simt_ws(B, Q, Hq, Hkv, D);
+  if (paged_attn_tc_takes(D, DFLASH_BF16))
+    need = std::max(need, shared_attn_tc_ws(B, Q, Hq, D));
   return (need + 255) & ~(size_t)255;
 }
 
@@ -153,7 +156,9 @@ dflash_status dflash_shared_attn(
   a.wait_ns = wait_limit_ns();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e =
-      dt == DFLASH_FP32
+      paged_attn_tc_takes(D, dt)
+          ? launch_shared_attn_tc(a, shared, sms, ws, s)
+      : dt == DFLASH_FP32
           ? launch_simt_d<float>(a, shared, static_cast<float*>(ws), s)
           : launch_simt_d<__nv_bfloat16>(a, shared, static_cast<float*>(ws), s);
   return e == cudaSuccess            ? DFLASH_OK

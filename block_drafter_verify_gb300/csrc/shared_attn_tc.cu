@@ -1,0 +1,1127 @@
+// Attention of a batch whose sequences share their first tokens, on the tensor
+// cores (tcgen05), for bf16 queries and heads of up to 128 dimensions.
+//
+// The rows (query, head) of all sequences that read a key head are numbered
+// through.  A unit is up to 256 of them, in two halves of 128, with the tokens
+// that they see: of all sequences with the shared tokens, of one sequence with
+// its own.  Both are tiles of 128 tokens: S = Q K^T (a row to a TMEM lane, so a
+// thread owns a row and its sums), P = weights, O += P V.
+//   K and V  are taken to fp16 on their way (four warps, from the tile that TMA
+//            brought to two operands as the MMA reads them): E4M3 codes are
+//            exact there.  That costs the 8-bit MMA's rate, but then one product
+//            does where the codes as they are need q in two and the weights in
+//            four 8-bit parts, and with 128 and 256 rows to a tile the products
+//            are what counts.
+//   q        is scaled by a power of two for each row, its largest value to
+//            [2^14, 2^15): fp16 then holds all of bf16's bits down to 2^-28 of
+//            that value.
+//   P        fp16: 2^-12 of a weight, or 2^-35 of the row's largest.  The sum
+//            counts weights as they are in fp32.
+// The page's scales are one factor and one addend of the exponent for 16 columns:
+// weights carry their value's scale, the row's sum is taken without it (see
+// kSumRef).  The running maximum is lazy: weights are taken against a reference
+// that is raised (sum and accumulator rescaled, by an exact power of two) only
+// when a token beats it by more than 2^5.75.
+//
+// All tiles of all units are numbered, and every CTA (one per SM) takes an equal
+// run of them by cost.  A run's parts of units go to the workspace, and a second
+// launch joins each row's: of the shared tokens and of its sequence's own.
+//
+// Warps: 0 copies tiles (TMA, one box per page), 1 issues the MMAs, 2 hands out
+// the segments of the run, 4-7 convert, 8-15 (a group of four to a half) lay out
+// q, do the softmax and write the parts.  While one half's softmax runs, the
+// tensor cores have the other's products.  Every wait is bounded; on a timeout
+// the CTA stops issuing, drains, frees TMEM and flags the error word.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "kernels.h"
+#include "tc_ptx.cuh"
+
+namespace dflash {
+namespace {
+
+constexpr int kTile = 128;          // tokens of a tile
+constexpr int kHalf = 128;          // rows of a half
+constexpr int kRows = 2 * kHalf;    // most rows of a unit
+constexpr int kMaxCtas = 160;
+constexpr int kThreads = 512;
+constexpr int kRawBytes = kTile * 128;      // a tile of codes
+constexpr int kWideBytes = 2 * kRawBytes;   // and as fp16
+constexpr int kRaw = 4, kWide = 3;          // stages: K and V by turns
+constexpr int kInfo = 8;                    // tiles' scales in flight
+constexpr int kSegs = 4;                    // segments handed out ahead
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kHead = 10.f;       // weights are 2^(score - ref + kHead)
+constexpr float kRaise = 15.75f;    // 2^15.75 = 55109 < 65504
+// A row's sum counts its weights without their value scales (2^lv), times
+// 2^kSumRef: with scales from 2^kLeastLv to 2^kMostLv and 2^30 tokens it stays
+// between 2^-95 and 2^126, whichever of them the reference has come from.
+constexpr float kSumRef = 16.f;
+constexpr float kLeastLv = -64.f, kMostLv = 120.f;
+// Weights of pages whose value scale is that much (in bits) below the largest
+// of the run so far may underflow: their terms of the sum are computed apart.
+constexpr float kFarLv = 90.f;
+// Work is counted in tiles of one half; a unit's start and end take kUnitCost.
+constexpr int kUnitCost = 4;
+
+// Part of a unit that a CTA works on.
+struct Segment {
+  int done;               // no more work
+  int prefix;             // the shared tokens' (of all sequences)
+  int b, hk;              // row of the page table, key head
+  int row0, rows;         // rows of the head
+  int tok0, T, end;       // first token, tiles, end of the tokens
+  int slot;               // where the part goes; -1: the whole unit, by row
+};
+
+struct Meta {
+  Segment seg[kSegs];
+  // of 16 tokens: key factor, log2 of the value scale, 2^(kSumRef - that) or 0
+  alignas(16) float4 info[kInfo][kTile / 16];
+  uint64_t raw_full[kRaw], raw_empty[kRaw], wide_full[kWide], wide_empty[kWide];
+  uint64_t s_full[2], p_full[2], q_full[2], o_full[2];
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t drain;
+  uint32_t tmem;
+  int abort;
+};
+constexpr int kQBytes = kRows * 128 * 2;
+constexpr int kSmem = 1024 + kQBytes + kWide * kWideBytes + kRaw * kRawBytes +
+                      ((int)sizeof(Meta) + 15) / 16 * 16;
+static_assert(kSmem <= 232448, "");
+
+// ---- the numbering of the work ---------------------------------------------
+struct Shape {
+  int g;                  // query heads of a key head
+  int own, all;           // rows of a head: a sequence's, all sequences'
+  int own_units, all_units;
+  int shared, tiles;      // shared tokens, their tiles
+};
+__host__ __device__ __forceinline__ int cost_of(int rows, int unit) {
+  return rows - unit * kRows > kHalf ? 2 : 1;
+}
+__host__ __device__ __forceinline__ int work_of(int T, int cost) {
+  return T > 0 ? kUnitCost + T * cost : 0;
+}
+struct Lens {
+  int n, nq;
+};
+__device__ __forceinline__ Lens lens_of(const PagedAttnArgs& a, int b,
+                                        bool* bad) {
+  Lens l;
+  l.n = attn_clamp(a.kv_len[b], (long long)a.max_pages * a.page, bad);
+  l.nq = attn_clamp(a.q_len ? a.q_len[b] : a.Q, a.Q, bad);
+  return l;
+}
+// Own tokens' tiles of unit u of a sequence.
+__device__ __forceinline__ int tiles_of(const PagedAttnArgs& a, const Shape& s,
+                                        const Lens& l, int u) {
+  const int q0 = u * kRows / s.g;
+  if (q0 >= l.nq) return 0;
+  int seen = l.n;
+  if (a.causal) {
+    const int q1 = min((min((u + 1) * kRows, s.own) - 1) / s.g, l.nq - 1);
+    seen = max(0, min(l.n, l.n - l.nq + q1 + 1));
+  }
+  return (max(0, seen - s.shared) + kTile - 1) / kTile;
+}
+// Work of one key head: the shared tokens', a sequence's own.
+__host__ __device__ __forceinline__ int shared_work(const Shape& s) {
+  return (s.all_units - 1) * work_of(s.tiles, 2) +
+         work_of(s.tiles, cost_of(s.all, s.all_units - 1));
+}
+__device__ __forceinline__ int own_work(const PagedAttnArgs& a, const Shape& s,
+                                        const Lens& l) {
+  int w = 0;
+  for (int u = 0; u < s.own_units; ++u)
+    w += work_of(tiles_of(a, s, l, u), cost_of(s.own, u));
+  return w;
+}
+// First position of CTA c of the G that work.
+__device__ __forceinline__ int run_start(int total, int c, int G) {
+  return (int)((long long)total * c / G);
+}
+__device__ __forceinline__ int cta_of(int total, int at, int G) {
+  return (int)(((at + 1ll) * G - 1) / total);
+}
+// Tiles of a unit before position `at` of it.
+__device__ __forceinline__ int tiles_before(int at, int T, int cost) {
+  return at <= kUnitCost ? 0 : min(T, (at - kUnitCost + cost - 1) / cost);
+}
+
+// Walks the units from a position in the numbering.
+struct Walk {
+  int b, hk, u, at;       // b = -1: the shared tokens; at: position in the unit
+  int left;               // positions left in this CTA's run
+};
+// Where the run of CTA `cta` of `grid` starts.  A whole warp, each lane with a
+// stretch of the sequences; *bad: some length was out of range.  where [B + 2]
+// (or NULL) gets every sequence's first position, all of them, and G.
+__device__ void walk_start(const PagedAttnArgs& a, const Shape& s, int cta,
+                           int grid, Walk& w, int* where, bool* bad) {
+  const int lane = threadIdx.x & 31;
+  const int per = (a.B + 31) / 32;
+  const int b0 = min(a.B, lane * per), b1 = min(a.B, b0 + per);
+  int work = 0;
+  for (int b = b0; b < b1; ++b)
+    work += a.Hkv * own_work(a, s, lens_of(a, b, bad));
+  int run = work;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += v;
+  }
+  const int head = shared_work(s), first = a.Hkv * head;
+  run += first;
+  const int total = __shfl_sync(0xffffffffu, run, 31);
+  const int G = min(grid, total);
+  if (where) {
+    int at = run - work;
+    for (int b = b0; b < b1; ++b) {
+      where[b] = at;
+      at += a.Hkv * own_work(a, s, lens_of(a, b, bad));
+    }
+    if (lane == 31) {
+      where[a.B] = total;
+      where[a.B + 1] = G;
+    }
+  }
+  w = Walk{0, 0, 0, 0, 0};
+  if (cta >= G) return;                    // the same in every lane
+  const int p0 = run_start(total, cta, G);
+  w.left = run_start(total, cta + 1, G) - p0;
+  if (p0 < first) {
+    w.b = -1;
+    w.hk = p0 / head;
+    w.at = p0 - w.hk * head;
+    const int full = work_of(s.tiles, 2);
+    w.u = min(w.at / full, s.all_units - 1);
+    w.at -= w.u * full;
+    return;
+  }
+  const bool mine = p0 >= run - work && p0 < run;
+  int o = p0 - (run - work);
+  if (mine) {
+    int h = 1;
+    for (w.b = b0; w.b < b1; ++w.b) {
+      h = own_work(a, s, lens_of(a, w.b, bad));
+      if (o < a.Hkv * h) break;
+      o -= a.Hkv * h;
+    }
+    w.hk = o / h;
+    o -= w.hk * h;
+    const Lens l = lens_of(a, w.b, bad);
+    for (;; ++w.u) {
+      const int t = work_of(tiles_of(a, s, l, w.u), cost_of(s.own, w.u));
+      if (o < t) break;
+      o -= t;
+    }
+  }
+  const int from = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+  w.b = __shfl_sync(0xffffffffu, w.b, from);
+  w.hk = __shfl_sync(0xffffffffu, w.hk, from);
+  w.u = __shfl_sync(0xffffffffu, w.u, from);
+  w.at = __shfl_sync(0xffffffffu, o, from);
+}
+// The next segment; false at the end of the run.
+__device__ bool walk_next(const PagedAttnArgs& a, const Shape& s, Walk& w,
+                          int cta, Segment& g) {
+  bool bad = false;
+  while (w.left > 0) {
+    const bool prefix = w.b < 0;
+    const Lens l = prefix ? Lens{0, 0} : lens_of(a, w.b, &bad);
+    const int T = prefix ? s.tiles : tiles_of(a, s, l, w.u);
+    const int cost = cost_of(prefix ? s.all : s.own, w.u);
+    const int work = work_of(T, cost);
+    const int from = w.at, end = min(work, from + w.left);
+    const int t0 = tiles_before(from, T, cost), t1 = tiles_before(end, T, cost);
+    const int b = w.b, hk = w.hk, u = w.u;
+    w.left -= end - from;
+    w.at = end;
+    if (end == work) {
+      w.at = 0;
+      if (++w.u == (prefix ? s.all_units : s.own_units)) {
+        w.u = 0;
+        if (++w.hk == a.Hkv) {
+          w.hk = 0;
+          ++w.b;
+        }
+      }
+    }
+    if (t1 > t0) {
+      const int tok = prefix ? 0 : s.shared;
+      g.done = 0;
+      g.prefix = prefix;
+      g.b = prefix ? 0 : b;
+      g.hk = hk;
+      g.row0 = (prefix ? 0 : b * s.own) + u * kRows;
+      g.rows = min(kRows, (prefix ? s.all : s.own) - u * kRows);
+      g.tok0 = tok + t0 * kTile;
+      g.T = t1 - t0;
+      g.end = prefix ? s.shared : l.n;
+      g.slot = t1 - t0 == T ? -1 : 2 * cta + (from > 0 ? 0 : 1);
+      return true;
+    }
+  }
+  g.done = 1;
+  return false;
+}
+
+// ---- the workspace -----------------------------------------------------------
+// Parts of rows: D sums of weights times values, and {reference, sum of
+// weights}: of the runs' cut units by slot, then of whole units by row (index
+// of out's row), of the shared tokens and of the own.
+struct Parts {
+  float* o;
+  float2* ml;
+  int* where;
+  size_t by_row;           // first of the parts by row
+};
+__host__ __device__ inline Parts parts_of(void* ws, size_t rows, int D) {
+  Parts p;
+  p.by_row = (size_t)2 * kMaxCtas * kRows;
+  const size_t n = p.by_row + 2 * rows;
+  p.o = static_cast<float*>(ws);
+  p.ml = reinterpret_cast<float2*>(p.o + n * D);
+  p.where = reinterpret_cast<int*>(p.ml + n);
+  return p;
+}
+
+// Wait for phase `parity` of `bar`, at most `limit` ns; false (and *abort set)
+// if it runs out or another role gave up.  The clock and *abort are looked at
+// every 64 polls (every poll with a limit below a millisecond).
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity,
+                                         volatile int* abort, uint64_t limit) {
+  if (tc::mbar_try_wait(bar, parity, 1000)) return true;
+  const uint64_t t0 = tc::globaltimer_ns();
+  const int polls = limit < 1000000ull ? 1 : 64;
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < polls; ++i)
+      if (tc::mbar_try_wait(bar, parity, 1000)) return true;
+    if (*abort) return false;
+    if (tc::globaltimer_ns() - t0 > limit) {
+      *abort = 1;
+      return false;
+    }
+  }
+}
+
+// Position in a ring of S stages; `phase` flips on every lap.
+template <int S>
+struct Ring {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == S) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// ---- PTX -----------------------------------------------------------------------
+// kind::f16 with fp16 operands (format 0), fp32 D.
+__host__ __device__ constexpr uint32_t idesc_f16(int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(kHalf >> 4) << 24);
+}
+// B with N contiguous (bit 16).
+__host__ __device__ constexpr uint32_t idesc_f16_mn(int N) {
+  return idesc_f16(N) | (1u << 16);
+}
+// N contiguous in 128-byte rows (64 values of a token) with 128-byte swizzle:
+// groups of eight tokens 1024 bytes apart (stride), blocks of 64 values 16 KB
+// apart (leading offset).
+__device__ __forceinline__ uint64_t sdesc_mn_wide(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |
+         (static_cast<uint64_t>(kRawBytes >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) |
+         (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+// D[tmem] (+)= A[tmem] * B[smem].
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a,
+                                           uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(
+          d),
+      "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_x16(uint32_t addr,
+                                            const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, "
+      "%7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+      "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_x16(uint32_t addr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, "
+      "%7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
+        "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15])
+      : "r"(addr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld_x32(uint32_t addr, float (&v)[32]) {
+  tmem_ld_x16(addr, *reinterpret_cast<float (*)[16]>(v));
+  tmem_ld_x16(addr + 16, *reinterpret_cast<float (*)[16]>(v + 16));
+}
+// Wait for this thread's TMEM loads; no use of v is scheduled before it.
+template <int M>
+__device__ __forceinline__ void tmem_loaded(float (&v)[M]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < M; ++i) asm volatile("" : "+f"(v[i]));
+}
+__device__ __forceinline__ void tmem_stored() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// One thread of the warp (always the same one).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ float warp_top(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// A row of the segment as its thread sees it.
+struct Row {
+  int out;        // row of out and lse, -1: none
+  int lim;        // tokens it sees
+};
+__device__ __forceinline__ Row row_at(const PagedAttnArgs& a, const Shape& s,
+                                      const Segment& g, int r) {
+  if (r >= g.rows) return Row{-1, 0};
+  const int query = (g.row0 + r) / s.g;       // of all sequences
+  const int b = query / a.Q, i = query - b * a.Q;
+  bool bad = false;
+  const Lens l = lens_of(a, b, &bad);
+  if (i >= l.nq) return Row{-1, 0};
+  const int lim = a.causal ? min(l.n, l.n - l.nq + i + 1) : l.n;
+  return Row{query * a.Hq + g.hk * s.g + (g.row0 + r) - query * s.g,
+             min(lim, g.end)};
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    shared_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k,
+                          const __grid_constant__ CUtensorMap map_v,
+                          const __grid_constant__ PagedAttnArgs a,
+                          const Shape shape, void* ws) {
+  extern __shared__ uint8_t raw_smem[];
+  uint8_t* base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
+  uint8_t* sq = base;                         // [2 halves][2][128][128]
+  uint8_t* wide = sq + kQBytes;               // [kWide][2][128][128]
+  uint8_t* raw = wide + kWide * kWideBytes;   // [kRaw][128][128]
+  Meta& m = *reinterpret_cast<Meta*>(raw + kRaw * kRawBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort = &m.abort;
+
+  if (tid == 0) {
+    for (int i = 0; i < kRaw; ++i) {
+      tc::mbar_init(&m.raw_full[i], 1);
+      tc::mbar_init(&m.raw_empty[i], 4);
+    }
+    for (int i = 0; i < kWide; ++i) {
+      tc::mbar_init(&m.wide_full[i], 4);
+      tc::mbar_init(&m.wide_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&m.s_full[i], 2);
+      tc::mbar_init(&m.p_full[i], 4);
+      tc::mbar_init(&m.q_full[i], 4);
+      tc::mbar_init(&m.o_full[i], 1);
+    }
+    for (int i = 0; i < kSegs; ++i) {
+      tc::mbar_init(&m.seg_full[i], 1);
+      tc::mbar_init(&m.seg_empty[i], 1 + 1 + 4 + 8);
+    }
+    tc::mbar_init(&m.drain, 1);
+    m.abort = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(&m.tmem, 512);
+    tc::tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tc::tma_prefetch_map(&map_k);
+    tc::tma_prefetch_map(&map_v);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = m.tmem;
+  const int steps = a.D / 16;                 // 16 dimensions
+  pdl_wait();
+  pdl_trigger();
+
+  Ring<kSegs> rg;
+  // the next segment; false: something gave up
+  auto next_segment = [&] {
+    const bool ok = wait_for(&m.seg_full[rg.at], rg.phase, abort, a.wait_ns);
+    return __all_sync(0xffffffffu, ok) != 0;
+  };
+  auto done_segment = [&] {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&m.seg_empty[rg.at]);
+    rg.next();
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const int pt = kTile / a.page;            // pages of a tile
+    const int oob = a.num_pages * a.Hkv * a.page;  // a row past the pool
+    const uint32_t box = (uint32_t)a.page * 128;
+    const float c = fabsf(a.scale) * kLog2e;
+    Ring<kRaw> rr;
+    int in_flight = 0, tile = 0;
+    bool ok = true;
+    while (ok) {
+      if (!next_segment()) break;
+      const Segment g = m.seg[rg.at];
+      done_segment();
+      if (g.done) break;
+      const int pages = (g.end + a.page - 1) / a.page;
+      const int last = min(pages, g.tok0 / a.page + g.T * pt);
+      // page ids two chunks of 32 ahead, their scales one ahead
+      int at = g.tok0 / a.page;
+      auto load_id = [&](int first) {
+        const int pg = first + lane;
+        return pg < last ? a.table[(size_t)g.b * a.max_pages + pg] : -1;
+      };
+      auto load_scale = [&](const float* s, int pid) {
+        return pid >= 0 && pid < a.num_pages
+                   ? s[(size_t)pid * a.Hkv + g.hk] : 1.f;
+      };
+      int id = load_id(at), id1 = load_id(at + 32), id2 = load_id(at + 64);
+      float ks = load_scale(a.k_scale, id), vs = load_scale(a.v_scale, id);
+      float ks1 = load_scale(a.k_scale, id1), vs1 = load_scale(a.v_scale, id1);
+      float top_lv = -INFINITY;               // of the pages so far
+      for (int t = 0; t < g.T && ok; ++t) {
+        const int pg = g.tok0 / a.page + t * pt;  // first page of the tile
+        if (pg - at == 32) {
+          at += 32;
+          id = id1; ks = ks1; vs = vs1;
+          id1 = id2;
+          ks1 = load_scale(a.k_scale, id1);
+          vs1 = load_scale(a.v_scale, id1);
+          id2 = load_id(at + 64);
+        }
+        const int from = pg - at + lane;      // lane < pt: its page
+        const int pid = __shfl_sync(0xffffffffu, id, from & 31);
+        const float pk = __shfl_sync(0xffffffffu, ks, from & 31);
+        const float pv = __shfl_sync(0xffffffffu, vs, from & 31);
+        const bool have = lane < pt && pg + lane < last;
+        const bool bad = have && (pid < 0 || pid >= a.num_pages);
+        if (bad) raise_error(a.err, kErrBadIndex);
+        const int row = bad ? oob : (pid * a.Hkv + g.hk) * a.page;
+        const uint32_t bytes = box * __popc(__ballot_sync(0xffffffffu, have));
+        const float lv = fminf(fmaxf(log2f(pv), kLeastLv), kMostLv);
+        top_lv = fmaxf(top_lv, warp_top(have ? lv : -INFINITY));
+        // every 16 tokens have their page's (lanes 0 to 7)
+        {
+          const int page_of = lane * 16 / a.page;  // (below pt, lane < 8)
+          const float k16 = __shfl_sync(
+              0xffffffffu, have && !bad ? pk * c : 0.f, page_of & 31);
+          const float l16 =
+              __shfl_sync(0xffffffffu, have ? lv : 0.f, page_of & 31);
+          if (lane < kTile / 16)
+            m.info[tile % kInfo][lane] = make_float4(
+                k16, l16,
+                l16 < top_lv - kFarLv ? 0.f : tc::ex2_approx(kSumRef - l16),
+                0.f);
+        }
+        ++tile;
+        __syncwarp();
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          ok = ok && wait_for(&m.raw_empty[rr.at], rr.phase ^ 1, abort,
+                              a.wait_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) tc::mbar_arrive_expect_tx(&m.raw_full[rr.at], bytes);
+          __syncwarp();
+          if (have)
+            tc::tma_load_2d(raw + rr.at * kRawBytes + lane * box,
+                            kv ? &map_v : &map_k, &m.raw_full[rr.at], 0, row);
+          rr.next();
+          in_flight = min(in_flight + 1, kRaw);
+        }
+      }
+    }
+    // no copy is in flight when the CTA leaves, whatever the others did
+    int never = 0;
+    for (; in_flight > 0; --in_flight) {
+      Ring<kRaw> r = rr;
+      r.at -= in_flight;
+      if (r.at < 0) {
+        r.at += kRaw;
+        r.phase ^= 1;
+      }
+      wait_for(&m.raw_full[r.at], r.phase, &never, kWaitLimitNs);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    constexpr uint32_t id_s = idesc_f16(kTile);
+    const uint32_t id_o = idesc_f16_mn(a.D);
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t par) {
+      ok = ok && wait_for(bar, par, abort, a.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      return ok;
+    };
+    Ring<kWide> rw;
+    uint32_t q_par[2] = {0, 0}, p_par[2] = {0, 0};
+    while (ok) {
+      if (!next_segment()) break;
+      const bool done = m.seg[rg.at].done;
+      const int T = __shfl_sync(0xffffffffu, m.seg[rg.at].T, 0);
+      const int halves =
+          __shfl_sync(0xffffffffu, m.seg[rg.at].rows, 0) > kHalf ? 2 : 1;
+      done_segment();
+      if (done) break;
+      // scores of half h with the keys in stage `at`
+      auto scores = [&](int h, int at, bool last) {
+        tc::fence_after_sync();
+        if (elect_one()) {
+          const uint64_t dq =
+              tc::sdesc_k_sw128(tc::smem_u32(sq) + h * (kQBytes / 2));
+          const uint64_t dk =
+              tc::sdesc_k_sw128(tc::smem_u32(wide) + at * kWideBytes);
+          for (int k = 0; k < steps; ++k) {
+            const int off = (k >> 2) * (kRawBytes >> 4) + (k & 3) * 2;
+            tc::mma_bf16(tm + h * kTile, dq + off, dk + off, id_s, k > 0);
+          }
+          if (last) tc::mma_commit(&m.wide_empty[at]);
+          tc::mma_commit(&m.s_full[h]);
+          tc::mbar_arrive(&m.s_full[h]);  // (releases the tile's scales)
+        }
+        __syncwarp();
+      };
+      for (int h = 0; h < halves; ++h) {
+        if (!wait(&m.q_full[h], q_par[h])) break;
+        q_par[h] ^= 1;
+        if (h == 0 && !wait(&m.wide_full[rw.at], rw.phase)) break;
+        scores(h, rw.at, h == halves - 1);
+      }
+      rw.next();
+      for (int t = 0; t < T && ok; ++t) {
+        const Ring<kWide> rv = rw;
+        rw.next();
+        const bool more = t + 1 < T;
+        for (int h = 0; h < halves; ++h) {
+          if (!wait(&m.p_full[h], p_par[h])) break;
+          p_par[h] ^= 1;
+          if (h == 0 && !wait(&m.wide_full[rv.at], rv.phase)) break;
+          tc::fence_after_sync();
+          if (elect_one()) {
+            const uint64_t dv =
+                sdesc_mn_wide(tc::smem_u32(wide) + rv.at * kWideBytes);
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              mma_f16_ts(tm + kRows + h * kTile, tm + h * kTile + 8 * k,
+                         dv + k * (2048 >> 4), id_o, t > 0 || k > 0);
+            if (h == halves - 1) tc::mma_commit(&m.wide_empty[rv.at]);
+            if (!more) tc::mma_commit(&m.o_full[h]);
+          }
+          __syncwarp();
+          if (more) {
+            if (h == 0 && !wait(&m.wide_full[rw.at], rw.phase)) break;
+            scores(h, rw.at, h == halves - 1);
+          }
+        }
+        if (more) rw.next();
+      }
+    }
+    if (elect_one()) tc::mma_commit(&m.drain);
+    __syncwarp();
+    int never = 0;
+    wait_for(&m.drain, 0, &never, kWaitLimitNs);
+  } else if (warp == 2) {
+    // ----------------------------------------------------------- the run
+    Walk w;
+    {
+      bool bad = false;
+      const size_t rows = (size_t)a.B * a.Q * a.Hq;
+      walk_start(a, shape, blockIdx.x, gridDim.x, w,
+                 blockIdx.x == 0 ? parts_of(ws, rows, a.D).where : nullptr,
+                 &bad);
+      if (bad && blockIdx.x == 0) raise_error(a.err, kErrBadIndex);
+    }
+    for (bool more = true; more;) {
+      const bool ok = wait_for(&m.seg_empty[rg.at], rg.phase ^ 1, abort,
+                               a.wait_ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      Segment g;
+      more = walk_next(a, shape, w, blockIdx.x, g);
+      if (lane == 0) {
+        m.seg[rg.at] = g;
+        tc::mbar_arrive(&m.seg_full[rg.at]);
+      }
+      __syncwarp();
+      rg.next();
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ---------------------------------------------------------- converters
+    const int tok = tid - 128;                // row of the tile
+    Ring<kRaw> rr;
+    Ring<kWide> rw;
+    bool ok = true;
+    while (ok) {
+      if (!next_segment()) break;
+      const int done = m.seg[rg.at].done, T = m.seg[rg.at].T;
+      int left = m.seg[rg.at].end - m.seg[rg.at].tok0 - tok;
+      done_segment();
+      if (done) break;
+      for (int t = 0; t < T && ok; ++t, left -= kTile) {
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          ok = ok && wait_for(&m.raw_full[rr.at], rr.phase, abort, a.wait_ns) &&
+               wait_for(&m.wide_empty[rw.at], rw.phase ^ 1, abort, a.wait_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint8_t* src = raw + rr.at * kRawBytes + tok * 128;
+          uint8_t* dst = wide + rw.at * kWideBytes + tok * 128;
+          // values past the cache's end may be anything: they are 0
+          const bool live = left > 0;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            if (c >= steps) break;
+            uint4 w = *reinterpret_cast<const uint4*>(
+                src + ((c ^ (tok & 7)) << 4));
+            if (!live) w = make_uint4(0, 0, 0, 0);
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            uint32_t y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                  (__nv_fp8x2_storage_t)(x[i >> 1] >> (16 * (i & 1))),
+                  __NV_E4M3);
+              y[i] = (uint32_t)h.x | (uint32_t)h.y << 16;
+            }
+            uint8_t* to = dst + (c >> 2) * kRawBytes;
+            const int c0 = (c & 3) * 2;
+            *reinterpret_cast<uint4*>(to + ((c0 ^ (tok & 7)) << 4)) =
+                make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(to + (((c0 + 1) ^ (tok & 7)) << 4)) =
+                make_uint4(y[4], y[5], y[6], y[7]);
+          }
+          fence_async();
+          __syncwarp();
+          if (lane == 0) {
+            tc::mbar_arrive(&m.raw_empty[rr.at]);
+            tc::mbar_arrive(&m.wide_full[rw.at]);
+          }
+          rr.next();
+          rw.next();
+        }
+      }
+    }
+  } else if (warp >= 8) {
+    // -------------------------------------------------------------- softmax
+    const int half = (warp - 8) >> 2, quarter = warp & 3;
+    const int r_half = quarter * 32 + lane, r_unit = half * kHalf + r_half;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t s_col = lanes + half * kTile;
+    const uint32_t o_col = lanes + kRows + half * kTile;
+    uint8_t* qh = sq + half * (kQBytes / 2);
+    const Parts parts = parts_of(ws, (size_t)a.B * a.Q * a.Hq, a.D);
+    uint32_t s_par = 0, o_par = 0;
+    int tile = 0;                             // of all segments
+    bool ok = true;
+    while (ok) {
+      if (!next_segment()) break;
+      const Segment g = m.seg[rg.at];
+      done_segment();
+      if (g.done) break;
+      if (half * kHalf >= g.rows) {
+        tile += g.T;
+        continue;
+      }
+      const Row row = row_at(a, shape, g, r_unit);
+      float back = 0.f;                       // undoes the row's scaling
+      // ---- q: eight lanes to a row, 16 dimensions each --------------------
+      {
+        const int ch = lane & 7;
+#pragma unroll 1
+        for (int j0 = 0; j0 < 8; j0 += 4) {
+          uint4 u[4][2];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int from = (j0 + j) * 4 + (lane >> 3);
+            const int out = __shfl_sync(0xffffffffu, row.out, from);
+            u[j][0] = u[j][1] = make_uint4(0, 0, 0, 0);
+            if (out >= 0 && ch < steps) {
+              const uint4* src = reinterpret_cast<const uint4*>(
+                  static_cast<const uint8_t*>(a.q) +
+                  ((size_t)out * a.D + ch * 16) * 2);
+              u[j][0] = __ldg(src);
+              u[j][1] = __ldg(src + 1);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t v[8] = {u[j][0].x, u[j][0].y, u[j][0].z, u[j][0].w,
+                                   u[j][1].x, u[j][1].y, u[j][1].z, u[j][1].w};
+            float top = 0.f;                  // infinite: a NaN
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float x0 = __uint_as_float(v[k] << 16);
+              const float x1 = __uint_as_float(v[k] & 0xffff0000u);
+              top = x0 == x0 ? fmaxf(top, fabsf(x0)) : INFINITY;
+              top = x1 == x1 ? fmaxf(top, fabsf(x1)) : INFINITY;
+            }
+#pragma unroll
+            for (int o = 4; o; o >>= 1)
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int e =
+                max((int)(__float_as_uint(top) >> 23) - 127, -100);
+            float up = top < INFINITY ? __uint_as_float((141 - e) << 23)
+                                      : __uint_as_float(0x7fffffffu);
+            if (a.scale < 0.f) up = -up;
+            uint32_t y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const __half2 h = __floats2half2_rn(
+                  __uint_as_float(v[k] << 16) * up,
+                  __uint_as_float(v[k] & 0xffff0000u) * up);
+              y[k] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            const int r = quarter * 32 + (j0 + j) * 4 + (lane >> 3);
+            if (ch < steps) {
+              uint8_t* to = qh + (ch >> 2) * kRawBytes + r * 128;
+              const int c0 = (ch & 3) * 2;
+              *reinterpret_cast<uint4*>(to + ((c0 ^ (r & 7)) << 4)) =
+                  make_uint4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4*>(to + (((c0 + 1) ^ (r & 7)) << 4)) =
+                  make_uint4(y[4], y[5], y[6], y[7]);
+            }
+            // the row's own thread keeps what undoes its scaling
+            const float of = __shfl_sync(
+                0xffffffffu, __uint_as_float((113 + e) << 23), (lane & 3) * 8);
+            if ((lane >> 2) == j0 + j) back = of;
+          }
+        }
+      }
+      tc::fence_before_sync();                // (the last segment's O is read)
+      fence_async();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&m.q_full[half]);
+      const int lim = row.out >= 0 ? row.lim : 0x7fffffff;
+      float l = 0.f, nr = 0.f;                // nr: -reference
+      for (int t = 0; t < g.T; ++t, ++tile) {
+        ok = wait_for(&m.s_full[half], s_par, abort, a.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        s_par ^= 1;
+        tc::fence_after_sync();
+        const float4* info = m.info[tile % kInfo];
+        const int seen = lim - (g.tok0 + t * kTile);  // columns [0, seen)
+        const bool masked = __any_sync(0xffffffffu, seen < kTile);
+        // ---- the largest exponent ------------------------------------------
+        float top = -INFINITY;
+        float x[2][32];
+        tmem_ld_x32(s_col, x[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_loaded(x[c & 1]);
+          if (c < 3) tmem_ld_x32(s_col + 32 * (c + 1), x[(c + 1) & 1]);
+          float (&y)[32] = x[c & 1];
+          if (masked) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (32 * c + j >= seen) y[j] = -INFINITY;
+          }
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const float4 i = info[2 * c + b];
+            float big = y[16 * b];
+#pragma unroll
+            for (int j = 1; j < 16; ++j) big = fmaxf(big, y[16 * b + j]);
+            if (big > -INFINITY) top = fmaxf(top, fmaf(big, i.x * back, i.y));
+          }
+        }
+        if (__any_sync(0xffffffffu, t == 0 || top + nr > kRaise)) {
+          // ---- raise the reference: nothing to raise for a row that sees
+          // nothing, and in the first tile nothing to scale
+          float d = 0.f;
+          if (top > -INFINITY && (t == 0 || top + nr > kHead))
+            d = kHead - ceilf(top + nr);
+          nr += d;
+          if (t > 0) {
+            // in two factors: the sum may hold what the weights do not
+            const float f = tc::ex2_approx(fmaxf(d, -100.f));
+            const float f2 = tc::ex2_approx(fminf(d + 100.f, 0.f));
+            l = l * f * f2;
+            for (int c = 0; c < steps; ++c) {
+              float o[16];
+              tmem_ld_x16(o_col + 16 * c, o);
+              tmem_loaded(o);
+              uint32_t w[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                w[j] = __float_as_uint(o[j] * f * f2);
+              tmem_st_x16(o_col + 16 * c, w);
+            }
+          }
+        }
+        // ---- the weights ---------------------------------------------------
+        tmem_ld_x32(s_col, x[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_loaded(x[c & 1]);
+          if (c < 3) tmem_ld_x32(s_col + 32 * (c + 1), x[(c + 1) & 1]);
+          float (&y)[32] = x[c & 1];
+          uint32_t w[16];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const float4 i = info[2 * c + b];
+            const float f = i.x * back, add = i.y + nr;
+            if (i.z == 0.f) {
+              float sum = 0.f;
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if (!masked || 32 * c + 16 * b + j < seen)
+                  sum += tc::ex2_approx(
+                      fmaf(y[16 * b + j], f, nr + kSumRef));
+              l += sum;
+            }
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float e = tc::ex2_approx(fmaf(y[16 * b + j], f, add));
+              if (masked && 32 * c + 16 * b + j >= seen) e = 0.f;
+              y[16 * b + j] = e;
+              sum += e;
+            }
+            l = fmaf(i.z, sum, l);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const __half2 h = __floats2half2_rn(y[16 * b + 2 * j],
+                                                  y[16 * b + 2 * j + 1]);
+              w[8 * b + j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+          }
+          // (onto scores that have been read)
+          tmem_st_x16(s_col + 16 * c, w);
+        }
+        tmem_stored();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&m.p_full[half]);
+      }
+      if (!ok) break;
+      // ---- the part ----------------------------------------------------------
+      ok = wait_for(&m.o_full[half], o_par, abort, a.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      o_par ^= 1;
+      tc::fence_after_sync();
+      const bool any = l > 0.f || l != l;     // a NaN stays one
+      // l = frac 2^ex; 2^ref: what frac counts
+      const int ex = min(max((int)(__float_as_uint(l) >> 23) - 127, -100), 120);
+      const float f = __uint_as_float((127 + (int)kSumRef - ex) << 23);
+      const size_t rows = (size_t)a.B * a.Q * a.Hq;
+      const size_t at =
+          g.slot >= 0 ? (size_t)g.slot * kRows + r_unit
+                      : parts.by_row + (g.prefix ? 0 : rows) + row.out;
+      if (row.out >= 0)
+        parts.ml[at] = make_float2(
+            any ? (float)ex - nr - kSumRef : -INFINITY,
+            any ? l * __uint_as_float((127 - ex) << 23) : 0.f);
+      for (int c = 0; c < steps; ++c) {
+        float o[16];
+        tmem_ld_x16(o_col + 16 * c, o);
+        tmem_loaded(o);
+        if (row.out >= 0) {
+          float4* to = reinterpret_cast<float4*>(parts.o + at * a.D + 16 * c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            to[j] = make_float4(o[4 * j] * f, o[4 * j + 1] * f,
+                                o[4 * j + 2] * f, o[4 * j + 3] * f);
+        }
+        __syncwarp();
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 1) tc::tmem_dealloc(tmem, 512);
+  if (tid == 0 && m.abort) raise_error(a.err, kErrTimeout);
+}
+
+// Joins the parts of every row of out: a warp each.
+constexpr int kJoinWarps = 4;
+constexpr int kMostParts = 2 * kMaxCtas;
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    shared_attn_tc_join_kernel(const __grid_constant__ PagedAttnArgs a,
+                               const Shape s, void* ws) {
+  __shared__ int s_at[kJoinWarps][kMostParts];
+  __shared__ float s_w[kJoinWarps][kMostParts];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_trigger();
+  pdl_wait();
+  const int rows = a.B * a.Q * a.Hq;
+  const int row = blockIdx.x * kJoinWarps + warp;
+  if (row >= rows) return;
+  const Parts parts = parts_of(ws, rows, a.D);
+  const int query = row / a.Hq, h = row - query * a.Hq;
+  const int b = query / a.Q, i = query - b * a.Q, hk = h / s.g;
+  const int r_own = i * s.g + h % s.g;
+  bool bad = false;
+  const Lens l = lens_of(a, b, &bad);
+  const int total = parts.where[a.B], G = parts.where[a.B + 1];
+  int n = 0;
+  // the parts of unit u of T tiles that starts at position `first`
+  auto add = [&](int first, int T, int cost, int r, size_t whole) {
+    const int work = work_of(T, cost);
+    if (work == 0) return;
+    const int c0 = cta_of(total, first, G);
+    const int c1 = cta_of(total, first + work - 1, G);
+    for (int c = c0 + lane; c - lane <= c1; c += 32) {
+      int at = -1;
+      if (c <= c1) {
+        const int p0 = max(0, run_start(total, c, G) - first);
+        const int p1 = min(work, run_start(total, c + 1, G) - first);
+        const int t0 = tiles_before(p0, T, cost);
+        const int t1 = tiles_before(p1, T, cost);
+        if (t1 > t0)
+          at = t1 - t0 == T ? (int)whole
+                            : (2 * c + (p0 > 0 ? 0 : 1)) * kRows + r;
+      }
+      const uint32_t have = __ballot_sync(0xffffffffu, at >= 0);
+      if (at >= 0) s_at[warp][n + __popc(have & ((1u << lane) - 1))] = at;
+      n += __popc(have);
+    }
+  };
+  if (i < l.nq) {
+    const int r_all = b * s.own + r_own;
+    const int u = r_all / kRows, v = r_own / kRows;
+    if (s.tiles > 0)
+      add(hk * shared_work(s) + u * work_of(s.tiles, 2), s.tiles,
+          cost_of(s.all, u), r_all % kRows, parts.by_row + row);
+    int first = parts.where[b] + hk * own_work(a, s, l);
+    for (int k = 0; k < v; ++k)
+      first += work_of(tiles_of(a, s, l, k), cost_of(s.own, k));
+    add(first, tiles_of(a, s, l, v), cost_of(s.own, v), r_own % kRows,
+        parts.by_row + rows + row);
+  }
+  __syncwarp();
+  float top = -INFINITY;
+  for (int k = lane; k < n; k += 32)
+    top = fmaxf(top, parts.ml[s_at[warp][k]].x);
+  top = warp_max(top);
+  float sum = 0.f;
+  for (int k = lane; k < n; k += 32) {
+    const float2 v = parts.ml[s_at[warp][k]];
+    const float w = v.x == -INFINITY ? 0.f : exp2f(v.x - top);
+    s_w[warp][k] = w;
+    sum += w * v.y;
+  }
+  sum = warp_sum(sum);
+  __syncwarp();
+  const bool on = sum > 0.f || sum != sum;
+  const float inv = on ? 1.f / sum : 0.f;
+  if (lane == 0 && a.lse)
+    a.lse[row] = on ? (log2f(sum) + top) * 0.6931471805599453f : -INFINITY;
+  if (4 * lane >= a.D) return;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = 0; k < n; ++k) {
+    const float w = s_w[warp][k];
+    if (w == 0.f) continue;
+    const float4 v = *reinterpret_cast<const float4*>(
+        parts.o + (size_t)s_at[warp][k] * a.D + 4 * lane);
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+  }
+  const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+  const __nv_bfloat162 y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+  uint2 v;
+  v.x = *reinterpret_cast<const uint32_t*>(&x);
+  v.y = *reinterpret_cast<const uint32_t*>(&y);
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) +
+                            (size_t)row * a.D + 4 * lane) = v;
+}
+
+Shape shape_of(const PagedAttnArgs& a, int shared) {
+  Shape s;
+  s.g = a.Hq / a.Hkv;
+  s.own = a.Q * s.g;
+  s.all = a.B * s.own;
+  s.own_units = (s.own + kRows - 1) / kRows;
+  s.all_units = (s.all + kRows - 1) / kRows;
+  s.shared = shared;
+  s.tiles = (shared + kTile - 1) / kTile;
+  return s;
+}
+
+}  // namespace
+
+size_t shared_attn_tc_ws(long long B, long long Q, int Hq, int D) {
+  const size_t n = (size_t)2 * kMaxCtas * kRows + 2 * (size_t)(B * Q * Hq);
+  return n * (D * sizeof(float) + sizeof(float2)) + (B + 2) * sizeof(int);
+}
+
+cudaError_t launch_shared_attn_tc(const PagedAttnArgs& a, int shared, int sms,
+                                  void* ws, cudaStream_t stream) {
+  const Shape s = shape_of(a, shared);
+  const long long own_tiles =
+      ((long long)a.max_pages * a.page - shared + kTile - 1) / kTile;
+  const long long most =
+      a.Hkv * (long long)s.all_units * (kUnitCost + 2ll * s.tiles) +
+      (long long)a.B * a.Hkv * s.own_units * (kUnitCost + 2 * own_tiles);
+  const long long rows = (long long)a.B * a.Q * a.Hq;
+  // (and the parts' numbers stay within 32 bits)
+  if (most > 0x7fffffffll || 2 * rows + 2 * kMaxCtas * kRows > 0x7fffffffll)
+    return cudaErrorNotSupported;
+  const int G = std::min(sms, kMaxCtas);
+  CUtensorMap mk, mv;
+  const uint64_t pool = (uint64_t)a.num_pages * a.Hkv * a.page;
+  if (!make_tmap_u8_2d(&mk, a.k_codes, a.D, pool, 128, a.page) ||
+      !make_tmap_u8_2d(&mv, a.v_codes, a.D, pool, 128, a.page))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(
+      shared_attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      kSmem);
+  if (e != cudaSuccess) return e;
+  PdlLaunch L(dim3(G), dim3(kThreads), kSmem, stream);
+  e = cudaLaunchKernelEx(&L.cfg, shared_attn_tc_kernel, mk, mv, a, s, ws);
+  if (e != cudaSuccess) return e;
+  PdlLaunch J(dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)),
+              dim3(32 * kJoinWarps), 0, stream);
+  return cudaLaunchKernelEx(&J.cfg, shared_attn_tc_join_kernel, a, s, ws);
+}
+
+}  // namespace dflash
