@@ -410,6 +410,35 @@ __device__ __forceinline__ float warp_top(float v) {
   return r;
 }
 
+// Pairs of fp32 in one register pair.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// A factor of scores: a masked one (-inf) has to stay that, so it is not 0.
+__device__ __forceinline__ float factor(float f) {
+  return fmaxf(f, 0x1p-126f);
+}
+
 // A row of the segment as its thread sees it.
 struct Row {
   int out;        // row of out and lse, -1: none
@@ -712,13 +741,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* dst = wide + rw.at * kWideBytes + tok * 128;
           // values past the cache's end may be anything: they are 0
           const bool live = left > 0;
+          uint4 w[8];                         // (dimensions past D: zeros)
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            w[c] = *reinterpret_cast<const uint4*>(src +
+                                                   ((c ^ (tok & 7)) << 4));
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            if (c >= steps) break;
-            uint4 w = *reinterpret_cast<const uint4*>(
-                src + ((c ^ (tok & 7)) << 4));
-            if (!live) w = make_uint4(0, 0, 0, 0);
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            if (!live) w[c] = make_uint4(0, 0, 0, 0);
+            const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
             uint32_t y[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -836,7 +867,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&m.q_full[half]);
       const int lim = row.out >= 0 ? row.lim : 0x7fffffff;
-      float l = 0.f, nr = 0.f;                // nr: -reference
+      uint64_t l2 = 0;                        // two sums of weights
+      float nr = 0.f;                         // -reference
       for (int t = 0; t < g.T; ++t, ++tile) {
         ok = wait_for(&m.s_full[half], s_par, abort, a.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
@@ -855,20 +887,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_loaded(x[c & 1]);
           if (c < 3) tmem_ld_x32(s_col + 32 * (c + 1), x[(c + 1) & 1]);
           float (&y)[32] = x[c & 1];
-          if (masked) {
+          if (masked) {                       // for the second reading, too
+            uint32_t w[2][16];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
+            for (int j = 0; j < 32; ++j) {
               if (32 * c + j >= seen) y[j] = -INFINITY;
+              w[j >> 4][j & 15] = __float_as_uint(y[j]);
+            }
+            tmem_st_x16(s_col + 32 * c, w[0]);
+            tmem_st_x16(s_col + 32 * c + 16, w[1]);
           }
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             const float4 i = info[2 * c + b];
-            float big = y[16 * b];
+            float big[4];
 #pragma unroll
-            for (int j = 1; j < 16; ++j) big = fmaxf(big, y[16 * b + j]);
-            if (big > -INFINITY) top = fmaxf(top, fmaf(big, i.x * back, i.y));
+            for (int j = 0; j < 4; ++j)
+              big[j] = fmaxf(fmaxf(y[16 * b + j], y[16 * b + 4 + j]),
+                             fmaxf(y[16 * b + 8 + j], y[16 * b + 12 + j]));
+            big[0] = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
+            top = fmaxf(top, fmaf(big[0], factor(i.x * back), i.y));
           }
         }
+        if (masked) tmem_stored();
         if (__any_sync(0xffffffffu, t == 0 || top + nr > kRaise)) {
           // ---- raise the reference: nothing to raise for a row that sees
           // nothing, and in the first tile nothing to scale
@@ -880,7 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // in two factors: the sum may hold what the weights do not
             const float f = tc::ex2_approx(fmaxf(d, -100.f));
             const float f2 = tc::ex2_approx(fminf(d + 100.f, 0.f));
-            l = l * f * f2;
+            l2 = mul2(mul2(l2, pack2(f, f)), pack2(f2, f2));
             for (int c = 0; c < steps; ++c) {
               float o[16];
               tmem_ld_x16(o_col + 16 * c, o);
@@ -904,31 +945,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             const float4 i = info[2 * c + b];
-            const float f = i.x * back, add = i.y + nr;
+            const float f = factor(i.x * back), add = i.y + nr;
             if (i.z == 0.f) {
+              const float apart = nr + kSumRef;
               float sum = 0.f;
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                if (!masked || 32 * c + 16 * b + j < seen)
-                  sum += tc::ex2_approx(
-                      fmaf(y[16 * b + j], f, nr + kSumRef));
-              l += sum;
+                sum += tc::ex2_approx(fmaf(y[16 * b + j], f, apart));
+              l2 = add2(l2, pack2(sum, 0.f));
             }
-            float sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              float e = tc::ex2_approx(fmaf(y[16 * b + j], f, add));
-              if (masked && 32 * c + 16 * b + j >= seen) e = 0.f;
-              y[16 * b + j] = e;
-              sum += e;
-            }
-            l = fmaf(i.z, sum, l);
+            const uint64_t f2 = pack2(f, f), a2 = pack2(add, add);
+            uint64_t sum[2];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const __half2 h = __floats2half2_rn(y[16 * b + 2 * j],
-                                                  y[16 * b + 2 * j + 1]);
+              float e0, e1;
+              unpack2(fma2(pack2(y[16 * b + 2 * j], y[16 * b + 2 * j + 1]), f2,
+                           a2), e0, e1);
+              e0 = tc::ex2_approx(e0);
+              e1 = tc::ex2_approx(e1);
+              const uint64_t e = pack2(e0, e1);
+              sum[j & 1] = j < 2 ? e : add2(sum[j & 1], e);
+              const __half2 h = __floats2half2_rn(e0, e1);
               w[8 * b + j] = *reinterpret_cast<const uint32_t*>(&h);
             }
+            l2 = fma2(add2(sum[0], sum[1]), pack2(i.z, i.z), l2);
           }
           // (onto scores that have been read)
           tmem_st_x16(s_col + 16 * c, w);
@@ -945,6 +985,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       o_par ^= 1;
       tc::fence_after_sync();
+      float l, l_odd;
+      unpack2(l2, l, l_odd);
+      l += l_odd;
       const bool any = l > 0.f || l != l;     // a NaN stays one
       // l = frac 2^ex; 2^ref: what frac counts
       const int ex = min(max((int)(__float_as_uint(l) >> 23) - 127, -100), 120);
