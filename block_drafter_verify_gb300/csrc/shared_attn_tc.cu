@@ -83,13 +83,15 @@ struct Meta {
   alignas(16) float4 info[kInfo][kTile / 16];
   uint64_t raw_full[kRaw], raw_empty[kRaw], wide_full[kWide], wide_empty[kWide];
   uint64_t s_full[2], p_full[2], q_full[2], o_full[2];
+  uint64_t x_full, x_empty;
+  alignas(8) float2 x[kHalf];  // the second half's sums and references
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t drain;
   uint32_t tmem;
   int abort;
 };
 constexpr int kQBytes = kRows * 128 * 2;
-constexpr int kSmem = 1024 + kQBytes + kWide * kWideBytes + kRaw * kRawBytes +
+constexpr int kSmem = kQBytes + kWide * kWideBytes + kRaw * kRawBytes +
                       ((int)sizeof(Meta) + 15) / 16 * 16;
 static_assert(kSmem <= 232448, "");
 
@@ -152,7 +154,8 @@ __device__ __forceinline__ int tiles_before(int at, int T, int cost) {
   return at <= kUnitCost ? 0 : min(T, (at - kUnitCost + cost - 1) / cost);
 }
 
-// Walks the units from a position in the numbering.
+// Walks the units from a position in the numbering.  (Calls: inlined, the walk
+// took registers that the softmax needs.)
 struct Walk {
   int b, hk, u, at;       // b = -1: the shared tokens; at: position in the unit
   int left;               // positions left in this CTA's run
@@ -160,7 +163,7 @@ struct Walk {
 // Where the run of CTA `cta` of `grid` starts.  A whole warp, each lane with a
 // stretch of the sequences; *bad: some length was out of range.  where [B + 2]
 // (or NULL) gets every sequence's first position, all of them, and G.
-__device__ void walk_start(const PagedAttnArgs& a, const Shape& s, int cta,
+__device__ __noinline__ void walk_start(const PagedAttnArgs& a, const Shape& s, int cta,
                            int grid, Walk& w, int* where, bool* bad) {
   const int lane = threadIdx.x & 31;
   const int per = (a.B + 31) / 32;
@@ -227,7 +230,7 @@ __device__ void walk_start(const PagedAttnArgs& a, const Shape& s, int cta,
   w.at = __shfl_sync(0xffffffffu, o, from);
 }
 // The next segment; false at the end of the run.
-__device__ bool walk_next(const PagedAttnArgs& a, const Shape& s, Walk& w,
+__device__ __noinline__ bool walk_next(const PagedAttnArgs& a, const Shape& s, Walk& w,
                           int cta, Segment& g) {
   bool bad = false;
   while (w.left > 0) {
@@ -308,6 +311,20 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity,
       return false;
     }
   }
+}
+
+// Whether phase `parity` of `bar` is complete, without a wait (which a try_wait
+// is even with a limit of 0).
+__device__ __forceinline__ bool test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(tc::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // Position in a ring of S stages; `phase` flips on every lap.
@@ -439,6 +456,29 @@ __device__ __forceinline__ float factor(float f) {
   return fmaxf(f, 0x1p-126f);
 }
 
+// A value that all lanes have, for a uniform register: an MMA whose operands
+// come from a lane's own registers takes some 90 cycles to issue.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) {
+  return __shfl_sync(0xffffffffu, x, 0);
+}
+
+// How a segment's tiles fall to the halves: with more than 128 rows each has
+// rows of its own and takes every tile; otherwise they share the rows, and take
+// every other tile each (the first half joins both parts in the end).
+struct Halves {
+  int n, T;
+  bool apart;             // rows of their own
+  __device__ __forceinline__ Halves(int rows, int T_)
+      : n(rows > kHalf || T_ > 1 ? 2 : 1), T(T_), apart(rows > kHalf) {}
+  __device__ __forceinline__ int tiles(int h) const {
+    return apart ? T : (T + 1 - h) / 2;
+  }
+  // tile i of half h among the segment's
+  __device__ __forceinline__ int tile(int h, int i) const {
+    return apart ? i : 2 * i + h;
+  }
+};
+
 // A row of the segment as its thread sees it.
 struct Row {
   int out;        // row of out and lse, -1: none
@@ -462,9 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                           const __grid_constant__ CUtensorMap map_v,
                           const __grid_constant__ PagedAttnArgs a,
                           const Shape shape, void* ws) {
-  extern __shared__ uint8_t raw_smem[];
-  uint8_t* base = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
+  // (all there is: no room to align it by hand)
+  extern __shared__ __align__(1024) uint8_t base[];
   uint8_t* sq = base;                         // [2 halves][2][128][128]
   uint8_t* wide = sq + kQBytes;               // [kWide][2][128][128]
   uint8_t* raw = wide + kWide * kWideBytes;   // [kRaw][128][128]
@@ -479,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kWide; ++i) {
       tc::mbar_init(&m.wide_full[i], 4);
-      tc::mbar_init(&m.wide_empty[i], 1);
+      tc::mbar_init(&m.wide_empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&m.s_full[i], 2);
@@ -491,6 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&m.seg_full[i], 1);
       tc::mbar_init(&m.seg_empty[i], 1 + 1 + 4 + 8);
     }
+    tc::mbar_init(&m.x_full, 4);
+    tc::mbar_init(&m.x_empty, 4);
     tc::mbar_init(&m.drain, 1);
     m.abort = 0;
     tc::fence_mbar_init();
@@ -618,77 +659,118 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    // The whole warp waits, one elected thread issues: operands stay in uniform
+    // registers.  Products are issued as what they wait for is there, either
+    // half's: scores go to the columns that weights leave, and products of
+    // different shapes are not ordered, so those with the weights have to be
+    // done before.
+    const uint32_t tm = uniform(tmem);
     constexpr uint32_t id_s = idesc_f16(kTile);
     const uint32_t id_o = idesc_f16_mn(a.D);
     bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t par) {
-      ok = ok && wait_for(bar, par, abort, a.wait_ns);
-      ok = __all_sync(0xffffffffu, ok);
-      return ok;
-    };
-    Ring<kWide> rw;
-    uint32_t q_par[2] = {0, 0}, p_par[2] = {0, 0};
+    uint32_t wide_at = 0;                     // operands before the segment's
+    uint32_t n0 = 0, n1 = 0;                  // the halves' tiles before it
+    uint32_t q_par0 = 0, q_par1 = 0;
     while (ok) {
       if (!next_segment()) break;
       const bool done = m.seg[rg.at].done;
-      const int T = __shfl_sync(0xffffffffu, m.seg[rg.at].T, 0);
-      const int halves =
-          __shfl_sync(0xffffffffu, m.seg[rg.at].rows, 0) > kHalf ? 2 : 1;
+      const int T = uniform(m.seg[rg.at].T);
+      const Halves hv(uniform(m.seg[rg.at].rows), T);
       done_segment();
       if (done) break;
-      // scores of half h with the keys in stage `at`
-      auto scores = [&](int h, int at, bool last) {
-        tc::fence_after_sync();
-        if (elect_one()) {
-          const uint64_t dq =
-              tc::sdesc_k_sw128(tc::smem_u32(sq) + h * (kQBytes / 2));
-          const uint64_t dk =
-              tc::sdesc_k_sw128(tc::smem_u32(wide) + at * kWideBytes);
-          for (int k = 0; k < steps; ++k) {
-            const int off = (k >> 2) * (kRawBytes >> 4) + (k & 3) * 2;
-            tc::mma_bf16(tm + h * kTile, dq + off, dk + off, id_s, k > 0);
-          }
-          if (last) tc::mma_commit(&m.wide_empty[at]);
-          tc::mma_commit(&m.s_full[h]);
-          tc::mbar_arrive(&m.s_full[h]);  // (releases the tile's scales)
-        }
-        __syncwarp();
+      auto ready = [&](uint64_t* bar, uint32_t par) {
+        return __all_sync(0xffffffffu, test_wait(bar, par)) != 0;
       };
-      for (int h = 0; h < halves; ++h) {
-        if (!wait(&m.q_full[h], q_par[h])) break;
-        q_par[h] ^= 1;
-        if (h == 0 && !wait(&m.wide_full[rw.at], rw.phase)) break;
-        scores(h, rw.at, h == halves - 1);
-      }
-      rw.next();
-      for (int t = 0; t < T && ok; ++t) {
-        const Ring<kWide> rv = rw;
-        rw.next();
-        const bool more = t + 1 < T;
-        for (int h = 0; h < halves; ++h) {
-          if (!wait(&m.p_full[h], p_par[h])) break;
-          p_par[h] ^= 1;
-          if (h == 0 && !wait(&m.wide_full[rv.at], rv.phase)) break;
-          tc::fence_after_sync();
-          if (elect_one()) {
-            const uint64_t dv =
-                sdesc_mn_wide(tc::smem_u32(wide) + rv.at * kWideBytes);
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              mma_f16_ts(tm + kRows + h * kTile, tm + h * kTile + 8 * k,
-                         dv + k * (2048 >> 4), id_o, t > 0 || k > 0);
-            if (h == halves - 1) tc::mma_commit(&m.wide_empty[rv.at]);
-            if (!more) tc::mma_commit(&m.o_full[h]);
+      // A stage is free when both halves have used it, or the one that does.
+      auto release = [&](uint32_t at) {
+        tc::mma_commit(&m.wide_empty[at]);
+        if (!hv.apart) tc::mbar_arrive(&m.wide_empty[at]);
+      };
+      // Scores (`next` even) and values (odd) of a half's tiles by turns, the
+      // halves by turns; one piece of code for both.
+      int h = 0, next = 0, next_o = 0;        // this half's, the other's
+      uint32_t n = n0, n_o = n1, q_par = q_par0, q_par_o = q_par1;
+      uint32_t full_to = wide_at;             // operands known to be there
+      uint64_t since = 0;                     // when something was issued last
+      int polls = 0;
+      while (next < 2 * hv.tiles(h) || next_o < 2 * hv.tiles(1 - h)) {
+        const int i = next >> 1;
+        bool go = i < hv.tiles(h);
+        if (go) {
+          const int t = hv.tile(h, i);
+          const uint32_t seq = wide_at + 2 * t + (next & 1), at = seq % kWide;
+          if (next & 1)
+            go = ready(&m.p_full[h], (n + i) & 1);
+          else
+            go = i == 0 ? ready(&m.q_full[h], q_par)
+                        : ready(&m.o_full[h], (n + i - 1) & 1);
+          if (go && seq >= full_to) {         // (they come in order)
+            go = ready(&m.wide_full[at], (seq / kWide) & 1);
+            if (go) full_to = seq + 1;
           }
-          __syncwarp();
-          if (more) {
-            if (h == 0 && !wait(&m.wide_full[rw.at], rw.phase)) break;
-            scores(h, rw.at, h == halves - 1);
+          if (go) {
+            tc::fence_after_sync();
+            const uint32_t src = uniform(tc::smem_u32(wide) + at * kWideBytes);
+            const uint32_t ds = uniform(tm + h * kTile);
+            if (next & 1) {
+              const uint64_t dv = sdesc_mn_wide(src);
+              if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k)
+                  mma_f16_ts(ds + kRows, ds + 8 * k, dv + k * (2048 >> 4),
+                             id_o, i > 0 || k > 0);
+                release(at);
+                tc::mma_commit(&m.o_full[h]);
+              }
+            } else {
+              if (i == 0) q_par ^= 1;
+              const uint64_t dk = tc::sdesc_k_sw128(src);
+              const uint64_t dq = tc::sdesc_k_sw128(
+                  uniform(tc::smem_u32(sq) + h * (kQBytes / 2)));
+              if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const int off = (k >> 2) * (kRawBytes >> 4) + (k & 3) * 2;
+                  if (k < steps)
+                    tc::mma_bf16(ds, dq + off, dk + off, id_s, k > 0);
+                }
+                release(at);
+                tc::mma_commit(&m.s_full[h]);
+                tc::mbar_arrive(&m.s_full[h]);  // (releases the tile's scales)
+              }
+            }
+            __syncwarp();
+            ++next;
+            polls = 0;
+            since = 0;
           }
         }
-        if (more) rw.next();
+        if (!go && ++polls >= (a.wait_ns < 1000000ull ? 2 : 256)) {
+          polls = 0;
+          const uint64_t now = tc::globaltimer_ns();
+          if (since == 0) since = now;
+          if (*abort || now - since > a.wait_ns) {
+            *abort = 1;
+            ok = false;
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
+        h ^= 1;
+        const int k = next;
+        next = next_o;
+        next_o = k;
+        const uint32_t k1 = n, k2 = q_par;
+        n = n_o;
+        n_o = k1;
+        q_par = q_par_o;
+        q_par_o = k2;
       }
+      q_par0 = h ? q_par_o : q_par;
+      q_par1 = h ? q_par : q_par_o;
+      wide_at += 2 * T;
+      n0 += hv.tiles(0);
+      n1 += hv.tiles(1);
     }
     if (elect_one()) tc::mma_commit(&m.drain);
     __syncwarp();
@@ -779,24 +861,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 8) {
     // -------------------------------------------------------------- softmax
     const int half = (warp - 8) >> 2, quarter = warp & 3;
-    const int r_half = quarter * 32 + lane, r_unit = half * kHalf + r_half;
+    const int r_half = quarter * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t s_col = lanes + half * kTile;
     const uint32_t o_col = lanes + kRows + half * kTile;
     uint8_t* qh = sq + half * (kQBytes / 2);
     const Parts parts = parts_of(ws, (size_t)a.B * a.Q * a.Hq, a.D);
-    uint32_t s_par = 0, o_par = 0;
-    int tile = 0;                             // of all segments
+    uint32_t n = 0;                           // tiles of this half
+    uint32_t x_par = 0;
+    bool lent = false;                        // the first half reads this O
+    int tile = 0;                             // tiles before the segment's
     bool ok = true;
     while (ok) {
       if (!next_segment()) break;
       const Segment g = m.seg[rg.at];
       done_segment();
       if (g.done) break;
-      if (half * kHalf >= g.rows) {
-        tile += g.T;
-        continue;
-      }
+      const Halves hv(g.rows, g.T);
+      const int tile0 = tile;
+      tile += g.T;
+      if (half >= hv.n) continue;
+      const int r_unit = r_half + (hv.apart ? half * kHalf : 0);
       const Row row = row_at(a, shape, g, r_unit);
       float back = 0.f;                       // undoes the row's scaling
       // ---- q: eight lanes to a row, 16 dimensions each --------------------
@@ -869,55 +954,64 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lim = row.out >= 0 ? row.lim : 0x7fffffff;
       uint64_t l2 = 0;                        // two sums of weights
       float nr = 0.f;                         // -reference
-      for (int t = 0; t < g.T; ++t, ++tile) {
-        ok = wait_for(&m.s_full[half], s_par, abort, a.wait_ns);
+      for (int i = 0; i < hv.tiles(half); ++i, ++n) {
+        const int t = hv.tile(half, i);
+        // (also says that the products before are done)
+        ok = wait_for(&m.s_full[half], n & 1, abort, a.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        s_par ^= 1;
         tc::fence_after_sync();
-        const float4* info = m.info[tile % kInfo];
+        const float4* info = m.info[(tile0 + t) % kInfo];
         const int seen = lim - (g.tok0 + t * kTile);  // columns [0, seen)
         const bool masked = __any_sync(0xffffffffu, seen < kTile);
+        // Half of the scores at a time, in loops that are not unrolled: two
+        // warps of every scheduler run this code at different places, and
+        // with all of it unrolled they waited for instructions.
+        float y[kTile / 2];
+        auto load = [&](int c0) {
+#pragma unroll
+          for (int c = 0; c < kTile / 2; c += 16)
+            tmem_ld_x16(s_col + c0 + c,
+                        *reinterpret_cast<float (*)[16]>(y + c));
+          tmem_loaded(y);
+        };
         // ---- the largest exponent ------------------------------------------
         float top = -INFINITY;
-        float x[2][32];
-        tmem_ld_x32(s_col, x[0]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_loaded(x[c & 1]);
-          if (c < 3) tmem_ld_x32(s_col + 32 * (c + 1), x[(c + 1) & 1]);
-          float (&y)[32] = x[c & 1];
+        bool far = false;
+#pragma unroll 1
+        for (int c0 = 0; c0 < kTile; c0 += kTile / 2) {
+          load(c0);
           if (masked) {                       // for the second reading, too
-            uint32_t w[2][16];
+            uint32_t w[16];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              if (32 * c + j >= seen) y[j] = -INFINITY;
-              w[j >> 4][j & 15] = __float_as_uint(y[j]);
+            for (int j = 0; j < kTile / 2; ++j) {
+              if (c0 + j >= seen) y[j] = -INFINITY;
+              w[j & 15] = __float_as_uint(y[j]);
+              if ((j & 15) == 15) tmem_st_x16(s_col + c0 + j - 15, w);
             }
-            tmem_st_x16(s_col + 32 * c, w[0]);
-            tmem_st_x16(s_col + 32 * c + 16, w[1]);
           }
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const float4 i = info[2 * c + b];
+          for (int b = 0; b < 4; ++b) {
+            const float4 k = info[c0 / 16 + b];
+            const float* z = y + 16 * b;
             float big[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              big[j] = fmaxf(fmaxf(y[16 * b + j], y[16 * b + 4 + j]),
-                             fmaxf(y[16 * b + 8 + j], y[16 * b + 12 + j]));
+              big[j] = fmaxf(fmaxf(z[j], z[4 + j]), fmaxf(z[8 + j], z[12 + j]));
             big[0] = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3]));
-            top = fmaxf(top, fmaf(big[0], factor(i.x * back), i.y));
+            top = fmaxf(top, fmaf(big[0], factor(k.x * back), k.y));
+            far |= k.z == 0.f;
           }
         }
         if (masked) tmem_stored();
-        if (__any_sync(0xffffffffu, t == 0 || top + nr > kRaise)) {
+        if (__any_sync(0xffffffffu, i == 0 || top + nr > kRaise)) {
           // ---- raise the reference: nothing to raise for a row that sees
           // nothing, and in the first tile nothing to scale
           float d = 0.f;
-          if (top > -INFINITY && (t == 0 || top + nr > kHead))
+          if (top > -INFINITY && (i == 0 || top + nr > kHead))
             d = kHead - ceilf(top + nr);
           nr += d;
-          if (t > 0) {
+          if (i > 0) {
             // in two factors: the sum may hold what the weights do not
             const float f = tc::ex2_approx(fmaxf(d, -100.f));
             const float f2 = tc::ex2_approx(fminf(d + 100.f, 0.f));
@@ -934,64 +1028,110 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        // ---- the weights ---------------------------------------------------
-        tmem_ld_x32(s_col, x[0]);
+        if (far) {                            // (the same in all threads)
+#pragma unroll 1
+          for (int c = 0; c < kTile; c += 16) {
+            const float4 k = info[c / 16];
+            if (k.z != 0.f) continue;
+            float z[16];
+            tmem_ld_x16(s_col + c, z);
+            tmem_loaded(z);
+            const float f = factor(k.x * back), apart = nr + kSumRef;
+            float sum = 0.f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_loaded(x[c & 1]);
-          if (c < 3) tmem_ld_x32(s_col + 32 * (c + 1), x[(c + 1) & 1]);
-          float (&y)[32] = x[c & 1];
-          uint32_t w[16];
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const float4 i = info[2 * c + b];
-            const float f = factor(i.x * back), add = i.y + nr;
-            if (i.z == 0.f) {
-              const float apart = nr + kSumRef;
-              float sum = 0.f;
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                sum += tc::ex2_approx(fmaf(y[16 * b + j], f, apart));
-              l2 = add2(l2, pack2(sum, 0.f));
-            }
-            const uint64_t f2 = pack2(f, f), a2 = pack2(add, add);
-            uint64_t sum[2];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              float e0, e1;
-              unpack2(fma2(pack2(y[16 * b + 2 * j], y[16 * b + 2 * j + 1]), f2,
-                           a2), e0, e1);
-              e0 = tc::ex2_approx(e0);
-              e1 = tc::ex2_approx(e1);
-              const uint64_t e = pack2(e0, e1);
-              sum[j & 1] = j < 2 ? e : add2(sum[j & 1], e);
-              const __half2 h = __floats2half2_rn(e0, e1);
-              w[8 * b + j] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            l2 = fma2(add2(sum[0], sum[1]), pack2(i.z, i.z), l2);
+            for (int j = 0; j < 16; ++j)
+              sum += tc::ex2_approx(fmaf(z[j], f, apart));
+            l2 = add2(l2, pack2(sum, 0.f));
           }
-          // (onto scores that have been read)
-          tmem_st_x16(s_col + 16 * c, w);
+        }
+        // ---- the weights ---------------------------------------------------
+#pragma unroll 1
+        for (int c0 = 0; c0 < kTile; c0 += kTile / 2) {
+          load(c0);
+#pragma unroll
+          for (int c = 0; c < kTile / 2; c += 32) {
+            uint32_t w[16];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const float4 k = info[(c0 + c) / 16 + b];
+              const float* z = y + c + 16 * b;
+              const float f = factor(k.x * back), add = k.y + nr;
+              const uint64_t f2 = pack2(f, f), a2 = pack2(add, add);
+              uint64_t sum[2];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                float e0, e1;
+                unpack2(fma2(pack2(z[2 * j], z[2 * j + 1]), f2, a2), e0, e1);
+                e0 = tc::ex2_approx(e0);
+                e1 = tc::ex2_approx(e1);
+                const uint64_t e = pack2(e0, e1);
+                sum[j & 1] = j < 2 ? e : add2(sum[j & 1], e);
+                const __half2 h = __floats2half2_rn(e0, e1);
+                w[8 * b + j] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              l2 = fma2(add2(sum[0], sum[1]), pack2(k.z, k.z), l2);
+            }
+            // (onto scores that have been read)
+            tmem_st_x16(s_col + (c0 + c) / 2, w);
+          }
         }
         tmem_stored();
+        if (lent) {                           // O may be written again?
+          lent = false;
+          ok = wait_for(&m.x_empty, x_par, abort, a.wait_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          x_par ^= 1;
+        }
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&m.p_full[half]);
       }
       if (!ok) break;
       // ---- the part ----------------------------------------------------------
-      ok = wait_for(&m.o_full[half], o_par, abort, a.wait_ns);
+      ok = wait_for(&m.o_full[half], (n - 1) & 1, abort, a.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      o_par ^= 1;
       tc::fence_after_sync();
       float l, l_odd;
       unpack2(l2, l, l_odd);
       l += l_odd;
+      // The halves' parts of the same rows lie in the same lanes: the first half
+      // reads both, against the larger of the references.
+      const bool both = hv.n == 2 && !hv.apart;
+      float d0 = 0.f, d1 = 0.f;               // to it
+      if (both && half == 1) {
+        m.x[r_half] = make_float2(l, nr);
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&m.x_full);
+        lent = true;
+        continue;
+      }
+      if (both) {
+        ok = wait_for(&m.x_full, x_par, abort, a.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        x_par ^= 1;
+        tc::fence_after_sync();
+        const float2 x = m.x[r_half];
+        const bool on0 = l > 0.f || l != l, on1 = x.x > 0.f || x.x != x.x;
+        const float to = on0 && on1 ? fminf(nr, x.y) : on0 ? nr : x.y;
+        d0 = on0 ? to - nr : -INFINITY;
+        d1 = on1 ? to - x.y : -INFINITY;
+        auto scaled = [](float v, float d) {
+          return d == -INFINITY ? 0.f
+                                : v * tc::ex2_approx(fmaxf(d, -100.f)) *
+                                      tc::ex2_approx(fminf(d + 100.f, 0.f));
+        };
+        l = scaled(l, d0) + scaled(x.x, d1);
+        nr = to;
+      }
       const bool any = l > 0.f || l != l;     // a NaN stays one
       // l = frac 2^ex; 2^ref: what frac counts
       const int ex = min(max((int)(__float_as_uint(l) >> 23) - 127, -100), 120);
-      const float f = __uint_as_float((127 + (int)kSumRef - ex) << 23);
+      const float f0 = tc::ex2_approx(d0 + (kSumRef - (float)ex));
+      const float f1 = tc::ex2_approx(d1 + (kSumRef - (float)ex));
       const size_t rows = (size_t)a.B * a.Q * a.Hq;
       const size_t at =
           g.slot >= 0 ? (size_t)g.slot * kRows + r_unit
@@ -1001,17 +1141,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             any ? (float)ex - nr - kSumRef : -INFINITY,
             any ? l * __uint_as_float((127 - ex) << 23) : 0.f);
       for (int c = 0; c < steps; ++c) {
-        float o[16];
+        float o[16], o1[16];
         tmem_ld_x16(o_col + 16 * c, o);
+        if (both) {
+          tmem_ld_x16(o_col + kTile + 16 * c, o1);
+          tmem_loaded(o1);
+        }
         tmem_loaded(o);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          o[j] *= f0;
+          if (both) o[j] = fmaf(o1[j], f1, o[j]);
+        }
         if (row.out >= 0) {
           float4* to = reinterpret_cast<float4*>(parts.o + at * a.D + 16 * c);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            to[j] = make_float4(o[4 * j] * f, o[4 * j + 1] * f,
-                                o[4 * j + 2] * f, o[4 * j + 3] * f);
+            to[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2],
+                                o[4 * j + 3]);
         }
         __syncwarp();
+      }
+      if (both) {
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&m.x_empty);
       }
     }
   }
