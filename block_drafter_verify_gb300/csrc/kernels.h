@@ -209,7 +209,7 @@ cudaError_t launch_paged_attn_tc(const PagedAttnArgs& a, int sms, float* part,
                                  cudaStream_t s);
 // shared_attn_tc.cu: the tensor-core kernels of a shared prefix, for what
 // paged_attn_tc_takes.
-size_t shared_attn_tc_ws(long long B, long long Q, int Hq, int D);
+size_t shared_attn_tc_ws(long long B, long long Q, int Hq, int Hkv, int D);
 cudaError_t launch_shared_attn_tc(const PagedAttnArgs& a, int shared, int sms,
                                   void* ws, cudaStream_t s);
 // A length from the device clamped to [0, most]; *bad if it was outside.

@@ -102,7 +102,7 @@ size_t dflash_shared_attn_workspace_bytes(int B, int Q, int Hq, int Hkv,
   // an upper bound over both dtypes
   size_t need = simt_ws(B, Q, Hq, Hkv, D);
   if (paged_attn_tc_takes(D, DFLASH_BF16))
-    need = std::max(need, shared_attn_tc_ws(B, Q, Hq, D));
+    need = std::max(need, shared_attn_tc_ws(B, Q, Hq, Hkv, D));
   return (need + 255) & ~(size_t)255;
 }
 

@@ -50,7 +50,7 @@ constexpr int kMaxCtas = 160;
 constexpr int kThreads = 512;
 constexpr int kRawBytes = kTile * 128;      // a tile of codes
 constexpr int kWideBytes = 2 * kRawBytes;   // and as fp16
-constexpr int kRaw = 4, kWide = 3;          // stages: K and V by turns
+constexpr int kRaw = 2, kWide = 4;          // stages: K and V by turns
 constexpr int kInfo = 8;                    // tiles' scales in flight
 constexpr int kSegs = 4;                    // segments handed out ahead
 constexpr float kLog2e = 1.4426950408889634f;
@@ -138,17 +138,18 @@ __host__ __device__ __forceinline__ int shared_work(const Shape& s) {
 __device__ __forceinline__ int own_work(const PagedAttnArgs& a, const Shape& s,
                                         const Lens& l) {
   int w = 0;
+#pragma unroll 1
   for (int u = 0; u < s.own_units; ++u)
     w += work_of(tiles_of(a, s, l, u), cost_of(s.own, u));
   return w;
 }
-// First position of CTA c of the G that work.
-__device__ __forceinline__ int run_start(int total, int c, int G) {
-  return (int)((long long)total * c / G);
-}
-__device__ __forceinline__ int cta_of(int total, int at, int G) {
-  return (int)(((at + 1ll) * G - 1) / total);
-}
+// First position of CTA c of the G that work, which have `total` = q G + r.
+struct Runs {
+  int q, r, G;
+  __device__ __forceinline__ int start(int c) const {
+    return q * c + r * c / G;
+  }
+};
 // Tiles of a unit before position `at` of it.
 __device__ __forceinline__ int tiles_before(int at, int T, int cost) {
   return at <= kUnitCost ? 0 : min(T, (at - kUnitCost + cost - 1) / cost);
@@ -159,16 +160,29 @@ __device__ __forceinline__ int tiles_before(int at, int T, int cost) {
 struct Walk {
   int b, hk, u, at;       // b = -1: the shared tokens; at: position in the unit
   int left;               // positions left in this CTA's run
+  int pos;                // position among all
+  Runs runs;
 };
+// A unit that has tiles, as the CTA that begins it leaves it for the join: its
+// first position, the first and last CTA that have some of it, its tiles.
+struct alignas(16) Begun {
+  int first, c0, c1, T;
+};
+__host__ __device__ __forceinline__ size_t unit_of(const Shape& s, int Hkv,
+                                                   int b, int hk, int u) {
+  return b < 0 ? (size_t)hk * s.all_units + u
+               : (size_t)Hkv * s.all_units +
+                     ((size_t)b * Hkv + hk) * s.own_units + u;
+}
 // Where the run of CTA `cta` of `grid` starts.  A whole warp, each lane with a
-// stretch of the sequences; *bad: some length was out of range.  where [B + 2]
-// (or NULL) gets every sequence's first position, all of them, and G.
+// stretch of the sequences; *bad: some length was out of range.
 __device__ __noinline__ void walk_start(const PagedAttnArgs& a, const Shape& s, int cta,
-                           int grid, Walk& w, int* where, bool* bad) {
+                           int grid, Walk& w, bool* bad) {
   const int lane = threadIdx.x & 31;
   const int per = (a.B + 31) / 32;
   const int b0 = min(a.B, lane * per), b1 = min(a.B, b0 + per);
   int work = 0;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b)
     work += a.Hkv * own_work(a, s, lens_of(a, b, bad));
   int run = work;
@@ -181,21 +195,13 @@ __device__ __noinline__ void walk_start(const PagedAttnArgs& a, const Shape& s, 
   run += first;
   const int total = __shfl_sync(0xffffffffu, run, 31);
   const int G = min(grid, total);
-  if (where) {
-    int at = run - work;
-    for (int b = b0; b < b1; ++b) {
-      where[b] = at;
-      at += a.Hkv * own_work(a, s, lens_of(a, b, bad));
-    }
-    if (lane == 31) {
-      where[a.B] = total;
-      where[a.B + 1] = G;
-    }
-  }
-  w = Walk{0, 0, 0, 0, 0};
+  w = Walk{0, 0, 0, 0, 0, 0, Runs{0, 0, G}};
   if (cta >= G) return;                    // the same in every lane
-  const int p0 = run_start(total, cta, G);
-  w.left = run_start(total, cta + 1, G) - p0;
+  w.runs.q = total / G;
+  w.runs.r = total - w.runs.q * G;
+  const int p0 = w.runs.start(cta);
+  w.left = w.runs.start(cta + 1) - p0;
+  w.pos = p0;
   if (p0 < first) {
     w.b = -1;
     w.hk = p0 / head;
@@ -209,6 +215,7 @@ __device__ __noinline__ void walk_start(const PagedAttnArgs& a, const Shape& s, 
   int o = p0 - (run - work);
   if (mine) {
     int h = 1;
+#pragma unroll 1
     for (w.b = b0; w.b < b1; ++w.b) {
       h = own_work(a, s, lens_of(a, w.b, bad));
       if (o < a.Hkv * h) break;
@@ -217,6 +224,7 @@ __device__ __noinline__ void walk_start(const PagedAttnArgs& a, const Shape& s, 
     w.hk = o / h;
     o -= w.hk * h;
     const Lens l = lens_of(a, w.b, bad);
+#pragma unroll 1
     for (;; ++w.u) {
       const int t = work_of(tiles_of(a, s, l, w.u), cost_of(s.own, w.u));
       if (o < t) break;
@@ -229,9 +237,10 @@ __device__ __noinline__ void walk_start(const PagedAttnArgs& a, const Shape& s, 
   w.u = __shfl_sync(0xffffffffu, w.u, from);
   w.at = __shfl_sync(0xffffffffu, o, from);
 }
-// The next segment; false at the end of the run.
+// The next segment; false at the end of the run.  The units that begin in the
+// run go to `begun`.
 __device__ __noinline__ bool walk_next(const PagedAttnArgs& a, const Shape& s, Walk& w,
-                          int cta, Segment& g) {
+                          int cta, Segment& g, Begun* begun) {
   bool bad = false;
   while (w.left > 0) {
     const bool prefix = w.b < 0;
@@ -242,6 +251,12 @@ __device__ __noinline__ bool walk_next(const PagedAttnArgs& a, const Shape& s, W
     const int from = w.at, end = min(work, from + w.left);
     const int t0 = tiles_before(from, T, cost), t1 = tiles_before(end, T, cost);
     const int b = w.b, hk = w.hk, u = w.u;
+    if (from == 0 && T > 0 && (threadIdx.x & 31) == 0) {
+      int last = cta;                       // CTA of the unit's last position
+      while (w.runs.start(last + 1) < w.pos + work) ++last;
+      begun[unit_of(s, a.Hkv, b, hk, u)] = Begun{w.pos, cta, last, T};
+    }
+    w.pos += end - from;
     w.left -= end - from;
     w.at = end;
     if (end == work) {
@@ -280,7 +295,8 @@ __device__ __noinline__ bool walk_next(const PagedAttnArgs& a, const Shape& s, W
 struct Parts {
   float* o;
   float2* ml;
-  int* where;
+  Runs* runs;
+  Begun* begun;
   size_t by_row;           // first of the parts by row
 };
 __host__ __device__ inline Parts parts_of(void* ws, size_t rows, int D) {
@@ -289,16 +305,17 @@ __host__ __device__ inline Parts parts_of(void* ws, size_t rows, int D) {
   const size_t n = p.by_row + 2 * rows;
   p.o = static_cast<float*>(ws);
   p.ml = reinterpret_cast<float2*>(p.o + n * D);
-  p.where = reinterpret_cast<int*>(p.ml + n);
+  p.runs = reinterpret_cast<Runs*>(p.ml + n);       // (16 bytes)
+  p.begun = reinterpret_cast<Begun*>(
+      reinterpret_cast<uint8_t*>(p.runs) + 16 + (n & 1) * 8);
   return p;
 }
 
 // Wait for phase `parity` of `bar`, at most `limit` ns; false (and *abort set)
 // if it runs out or another role gave up.  The clock and *abort are looked at
 // every 64 polls (every poll with a limit below a millisecond).
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity,
-                                         volatile int* abort, uint64_t limit) {
-  if (tc::mbar_try_wait(bar, parity, 1000)) return true;
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity,
+                                       volatile int* abort, uint64_t limit) {
   const uint64_t t0 = tc::globaltimer_ns();
   const int polls = limit < 1000000ull ? 1 : 64;
   for (;;) {
@@ -311,6 +328,11 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity,
       return false;
     }
   }
+}
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity,
+                                         volatile int* abort, uint64_t limit) {
+  return tc::mbar_try_wait(bar, parity, 1000) ||
+         wait_long(bar, parity, abort, limit);
 }
 
 // Whether phase `parity` of `bar` is complete, without a wait (which a try_wait
@@ -393,10 +415,6 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t addr, float (&v)[16]) {
       : "r"(addr));
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_ld_x32(uint32_t addr, float (&v)[32]) {
-  tmem_ld_x16(addr, *reinterpret_cast<float (*)[16]>(v));
-  tmem_ld_x16(addr + 16, *reinterpret_cast<float (*)[16]>(v + 16));
 }
 // Wait for this thread's TMEM loads; no use of v is scheduled before it.
 template <int M>
@@ -779,20 +797,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 2) {
     // ----------------------------------------------------------- the run
     Walk w;
+    const Parts parts = parts_of(ws, (size_t)a.B * a.Q * a.Hq, a.D);
     {
       bool bad = false;
-      const size_t rows = (size_t)a.B * a.Q * a.Hq;
-      walk_start(a, shape, blockIdx.x, gridDim.x, w,
-                 blockIdx.x == 0 ? parts_of(ws, rows, a.D).where : nullptr,
-                 &bad);
-      if (bad && blockIdx.x == 0) raise_error(a.err, kErrBadIndex);
+      walk_start(a, shape, blockIdx.x, gridDim.x, w, &bad);
+      if (blockIdx.x == 0) {
+        if (bad) raise_error(a.err, kErrBadIndex);
+        if (lane == 0) *parts.runs = w.runs;
+      }
     }
     for (bool more = true; more;) {
       const bool ok = wait_for(&m.seg_empty[rg.at], rg.phase ^ 1, abort,
                                a.wait_ns);
       if (!__all_sync(0xffffffffu, ok)) break;
       Segment g;
-      more = walk_next(a, shape, w, blockIdx.x, g);
+      more = walk_next(a, shape, w, blockIdx.x, g, parts.begun);
       if (lane == 0) {
         m.seg[rg.at] = g;
         tc::mbar_arrive(&m.seg_full[rg.at]);
@@ -1016,6 +1035,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float f = tc::ex2_approx(fmaxf(d, -100.f));
             const float f2 = tc::ex2_approx(fminf(d + 100.f, 0.f));
             l2 = mul2(mul2(l2, pack2(f, f)), pack2(f2, f2));
+#pragma unroll 1
             for (int c = 0; c < steps; ++c) {
               float o[16];
               tmem_ld_x16(o_col + 16 * c, o);
@@ -1140,6 +1160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         parts.ml[at] = make_float2(
             any ? (float)ex - nr - kSumRef : -INFINITY,
             any ? l * __uint_as_float((127 - ex) << 23) : 0.f);
+#pragma unroll 1
       for (int c = 0; c < steps; ++c) {
         float o[16], o1[16];
         tmem_ld_x16(o_col + 16 * c, o);
@@ -1193,27 +1214,24 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   const Parts parts = parts_of(ws, rows, a.D);
   const int query = row / a.Hq, h = row - query * a.Hq;
   const int b = query / a.Q, i = query - b * a.Q, hk = h / s.g;
-  const int r_own = i * s.g + h % s.g;
   bool bad = false;
   const Lens l = lens_of(a, b, &bad);
-  const int total = parts.where[a.B], G = parts.where[a.B + 1];
+  const Runs runs = *parts.runs;
   int n = 0;
-  // the parts of unit u of T tiles that starts at position `first`
-  auto add = [&](int first, int T, int cost, int r, size_t whole) {
-    const int work = work_of(T, cost);
-    if (work == 0) return;
-    const int c0 = cta_of(total, first, G);
-    const int c1 = cta_of(total, first + work - 1, G);
-    for (int c = c0 + lane; c - lane <= c1; c += 32) {
+  // the parts of row r of a unit; whole: where the row's part of all of it is
+  auto add = [&](int at_b, int u, int cost, int r, size_t whole) {
+    const Begun g = parts.begun[unit_of(s, a.Hkv, at_b, hk, u)];
+    const int work = work_of(g.T, cost);
+    for (int c = g.c0 + lane; c - lane <= g.c1; c += 32) {
       int at = -1;
-      if (c <= c1) {
-        const int p0 = max(0, run_start(total, c, G) - first);
-        const int p1 = min(work, run_start(total, c + 1, G) - first);
-        const int t0 = tiles_before(p0, T, cost);
-        const int t1 = tiles_before(p1, T, cost);
+      if (c <= g.c1) {
+        const int p0 = max(0, runs.start(c) - g.first);
+        const int p1 = min(work, runs.start(c + 1) - g.first);
+        const int t0 = tiles_before(p0, g.T, cost);
+        const int t1 = tiles_before(p1, g.T, cost);
         if (t1 > t0)
-          at = t1 - t0 == T ? (int)whole
-                            : (2 * c + (p0 > 0 ? 0 : 1)) * kRows + r;
+          at = t1 - t0 == g.T ? (int)whole
+                              : (2 * c + (p0 > 0 ? 0 : 1)) * kRows + r;
       }
       const uint32_t have = __ballot_sync(0xffffffffu, at >= 0);
       if (at >= 0) s_at[warp][n + __popc(have & ((1u << lane) - 1))] = at;
@@ -1221,16 +1239,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     }
   };
   if (i < l.nq) {
-    const int r_all = b * s.own + r_own;
+    const int r_own = i * s.g + h - hk * s.g, r_all = b * s.own + r_own;
     const int u = r_all / kRows, v = r_own / kRows;
     if (s.tiles > 0)
-      add(hk * shared_work(s) + u * work_of(s.tiles, 2), s.tiles,
-          cost_of(s.all, u), r_all % kRows, parts.by_row + row);
-    int first = parts.where[b] + hk * own_work(a, s, l);
-    for (int k = 0; k < v; ++k)
-      first += work_of(tiles_of(a, s, l, k), cost_of(s.own, k));
-    add(first, tiles_of(a, s, l, v), cost_of(s.own, v), r_own % kRows,
-        parts.by_row + rows + row);
+      add(-1, u, cost_of(s.all, u), r_all % kRows, parts.by_row + row);
+    if (tiles_of(a, s, l, v) > 0)
+      add(b, v, cost_of(s.own, v), r_own % kRows, parts.by_row + rows + row);
   }
   __syncwarp();
   float top = -INFINITY;
@@ -1252,16 +1266,25 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     a.lse[row] = on ? (log2f(sum) + top) * 0.6931471805599453f : -INFINITY;
   if (4 * lane >= a.D) return;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = 0; k < n; ++k) {
-    const float w = s_w[warp][k];
-    if (w == 0.f) continue;
-    const float4 v = *reinterpret_cast<const float4*>(
-        parts.o + (size_t)s_at[warp][k] * a.D + 4 * lane);
-    o.x = fmaf(w, v.x, o.x);
-    o.y = fmaf(w, v.y, o.y);
-    o.z = fmaf(w, v.z, o.z);
-    o.w = fmaf(w, v.w, o.w);
+  constexpr int kAt = 8;                      // parts on their way at once
+  for (int k0 = 0; k0 < n; k0 += kAt) {
+    float4 v[kAt];
+    float w[kAt];
+#pragma unroll
+    for (int j = 0; j < kAt; ++j) {
+      w[j] = k0 + j < n ? s_w[warp][k0 + j] : 0.f;
+      v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (w[j] != 0.f)                        // (a NaN is none)
+        v[j] = *reinterpret_cast<const float4*>(
+            parts.o + (size_t)s_at[warp][k0 + j] * a.D + 4 * lane);
+    }
+#pragma unroll
+    for (int j = 0; j < kAt; ++j) {
+      o.x = fmaf(w[j], v[j].x, o.x);
+      o.y = fmaf(w[j], v[j].y, o.y);
+      o.z = fmaf(w[j], v[j].z, o.z);
+      o.w = fmaf(w[j], v[j].w, o.w);
+    }
   }
   const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv);
   const __nv_bfloat162 y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
@@ -1286,9 +1309,12 @@ Shape shape_of(const PagedAttnArgs& a, int shared) {
 
 }  // namespace
 
-size_t shared_attn_tc_ws(long long B, long long Q, int Hq, int D) {
+size_t shared_attn_tc_ws(long long B, long long Q, int Hq, int Hkv, int D) {
   const size_t n = (size_t)2 * kMaxCtas * kRows + 2 * (size_t)(B * Q * Hq);
-  return n * (D * sizeof(float) + sizeof(float2)) + (B + 2) * sizeof(int);
+  const long long own = Q * (Hq / Hkv);
+  const size_t units = Hkv * ((B * own + kRows - 1) / kRows +
+                              B * ((own + kRows - 1) / kRows));
+  return n * (D * sizeof(float) + sizeof(float2)) + 32 + units * sizeof(Begun);
 }
 
 cudaError_t launch_shared_attn_tc(const PagedAttnArgs& a, int shared, int sms,
