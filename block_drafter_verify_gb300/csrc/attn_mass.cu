@@ -175,8 +175,10 @@ extern "C" dflash_status dflash_attn_mass(
   a.wait_ns = wait_limit_ns();
   if (a.first >= mass_most(a)) return DFLASH_OK;  // no token to take
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = dt == DFLASH_FP32 ? launch_simt<float>(a, s)
-                                          : launch_simt<__nv_bfloat16>(a, s);
+  const cudaError_t e = paged_attn_tc_takes(D, dt)
+                            ? launch_attn_mass_tc(a, sms, s)
+                        : dt == DFLASH_FP32 ? launch_simt<float>(a, s)
+                                            : launch_simt<__nv_bfloat16>(a, s);
   return e == cudaSuccess            ? DFLASH_OK
          : e == cudaErrorNotSupported ? DFLASH_ERR_UNSUPPORTED
                                       : DFLASH_ERR_CUDA;

@@ -1,0 +1,632 @@
+// The attention weight that cached tokens gather, on the tensor cores (tcgen05),
+// for bf16 queries and heads of up to 128 dimensions.
+//
+// The cached codes go from HBM to the MMAs as they are, with q as the sum of two
+// E4M3 numbers side by side in the MMA's N (a row's largest value scaled to
+// [128, 256); the second part holds 2^5 times what the first leaves: all of
+// bf16's bits, down to 2^-17 of that value).  S^T[token, row] = K q^T, so a
+// thread owns a token: its key's scale is one factor, and the sum over the rows
+// is its own.  A row brings its scaling and its logsumexp (in bits).
+//
+// All tiles of 128 tokens of all (sequence, key head) pairs are numbered, and
+// every CTA (one per SM) takes an equal run, counted with the rows that they have.
+// With more than 128 rows the run's tiles are gone through for each 128 rows
+// again (the codes then come from L2) and the tokens' sums kept in shared memory
+// meanwhile: one thread owns a token throughout, nothing is added atomically.
+//
+// Warps: 0 copies tiles (TMA, one box per page), 1 issues the MMAs, 2 hands out
+// the segments, 4-7 lay out q (two buffers), 8-15 take the tiles' weights (a group
+// of four to every other tile).  Every wait is bounded; on a timeout the CTA stops
+// issuing, drains, frees TMEM and flags the error word.
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "attn_roles.cuh"
+#include "kernels.h"
+#include "tc_ptx.cuh"
+
+namespace dflash {
+namespace {
+
+constexpr int kTile = 128;       // tokens of a tile
+constexpr int kRows = 128;       // rows of a segment
+constexpr int kThreads = 512;
+constexpr int kStages = 8;       // tiles in shared memory
+constexpr int kTileBytes = kTile * 128;
+constexpr int kQBytes = 2 * kRows * 128;  // two parts
+constexpr int kSegs = 4;
+constexpr int kKeep = 48;        // tiles whose sums are kept (an even number)
+constexpr int kUnitCost = 2;     // of a pair besides its tiles, in tiles
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Tiles of one pair with (up to) 128 of its rows; without rows: the sums of
+// those tiles are complete.
+struct Segment {
+  int done;
+  int b, hk;
+  int row0, rows;
+  int tok0, T, end;              // first token, tiles, end of the tokens
+  int lone;                      // all rows: sums are complete at once
+  int n, nq;
+};
+struct Row {
+  float rel, nl;                 // undoes the scaling; -logsumexp in bits
+};
+struct Meta {
+  Segment seg[kSegs];
+  alignas(16) Row row[2][kRows];
+  int lim[2][kRows];             // tokens a row sees
+  float ks[kStages][8];          // factors of a tile's pages
+  float keep[kKeep][kTile];
+  uint64_t k_full[kStages], k_empty[kStages];
+  uint64_t s_full[2], s_empty[2], q_full[2], q_empty[2];
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  uint64_t drain;
+  uint32_t tmem;
+  int abort;
+};
+constexpr int kSmem = 2 * kQBytes + kStages * kTileBytes +
+                      ((int)sizeof(Meta) + 15) / 16 * 16;
+static_assert(kSmem <= 232448, "");
+
+struct Shape {
+  int g, first;                  // heads of a key head; first tile's token
+};
+struct Lens {
+  int n, nq;
+};
+__device__ __forceinline__ Lens lens_of(const AttnMassArgs& a, int b,
+                                        bool* bad) {
+  Lens l;
+  l.n = mass_length(a, b, bad);
+  l.nq = attn_clamp(a.q_len ? a.q_len[b] : a.Q, a.Q, bad);
+  return l;
+}
+__device__ __forceinline__ int tiles_of(const Shape& s, const Lens& l) {
+  return (max(0, l.n - s.first) + kTile - 1) / kTile;
+}
+// Of a tile: the times it is gone through.
+__device__ __forceinline__ int cost_of(const Shape& s, const Lens& l) {
+  return max(1, (l.nq * s.g + kRows - 1) / kRows);
+}
+__device__ __noinline__ int work_of(const AttnMassArgs& a, const Shape& s,
+                                    const Lens& l) {
+  const int T = tiles_of(s, l);
+  return T > 0 ? kUnitCost + T * cost_of(s, l) : 0;
+}
+
+// Walks the pairs from a position in the numbering.  Position kUnitCost + t c of
+// a pair whose tiles cost c is its tile t.
+struct Walk {
+  int b, hk, at;                 // at: position in the pair
+  int left;                      // positions left in this CTA's run
+};
+__device__ __noinline__ void walk_start(const AttnMassArgs& a, const Shape& s,
+                                        int cta, int grid, Walk& w,
+                                        bool* bad) {
+  const int lane = threadIdx.x & 31;
+  const int per = (a.B + 31) / 32;
+  const int b0 = min(a.B, lane * per), b1 = min(a.B, b0 + per);
+  int work = 0;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b)
+    work += a.Hkv * work_of(a, s, lens_of(a, b, bad));
+  int run = work;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += v;
+  }
+  const int total = __shfl_sync(0xffffffffu, run, 31);
+  const int p0 = (int)((long long)total * cta / grid);
+  w = Walk{0, 0, 0, (int)((long long)total * (cta + 1) / grid) - p0};
+  if (w.left <= 0) return;                 // the same in every lane
+  const bool mine = p0 >= run - work && p0 < run;
+  int o = p0 - (run - work);
+  if (mine) {
+    int h = 1;
+#pragma unroll 1
+    for (w.b = b0; w.b < b1; ++w.b) {
+      h = work_of(a, s, lens_of(a, w.b, bad));
+      if (o < a.Hkv * h) break;
+      o -= a.Hkv * h;
+    }
+    w.hk = o / h;
+    o -= w.hk * h;
+  }
+  const int from = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+  w.b = __shfl_sync(0xffffffffu, w.b, from);
+  w.hk = __shfl_sync(0xffffffffu, w.hk, from);
+  w.at = __shfl_sync(0xffffffffu, o, from);
+}
+// The next pair's tiles [t0, t0 + T) of the run; false at its end.
+__device__ __noinline__ bool walk_next(const AttnMassArgs& a, const Shape& s,
+                                       Walk& w, Segment& g, int& t0) {
+  bool bad = false;
+  while (w.left > 0) {
+    const Lens l = lens_of(a, w.b, &bad);
+    const int T = tiles_of(s, l), c = cost_of(s, l);
+    const int work = T > 0 ? kUnitCost + T * c : 0;
+    const int end = min(work, w.at + w.left);
+    auto before = [&](int at) {
+      return at <= kUnitCost ? 0 : min(T, (at - kUnitCost + c - 1) / c);
+    };
+    t0 = before(w.at);
+    g.T = before(end) - t0;
+    g.b = w.b;
+    g.hk = w.hk;
+    g.n = g.end = l.n;
+    g.nq = l.nq;
+    w.left -= end - w.at;
+    w.at = end;
+    if (end == work) {
+      w.at = 0;
+      if (++w.hk == a.Hkv) {
+        w.hk = 0;
+        ++w.b;
+      }
+    }
+    if (g.T > 0) return true;
+  }
+  return false;
+}
+
+// kind::f8f6f4, E4M3, fp32 D: N known at run time only.
+__device__ __forceinline__ uint32_t idesc_n(int N) {
+  return tc::idesc_e4m3_f32(kTile, 0) | ((uint32_t)(N >> 3) << 17);
+}
+__device__ __forceinline__ void expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(
+                   tc::smem_u32(bar)),
+               "r"(bytes)
+               : "memory");
+}
+// 16 bytes from global to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src,
+                                       bool read) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+               "l"(src), "r"(read ? 16 : 0)
+               : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_mass_tc_kernel(const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ AttnMassArgs a,
+                        const Shape shape) {
+  extern __shared__ __align__(1024) uint8_t base[];
+  uint8_t* sq = base;                        // [2 buffers][2 parts][rows][128]
+  uint8_t* sk = sq + 2 * kQBytes;            // [kStages][128][128]
+  Meta& m = *reinterpret_cast<Meta*>(sk + kStages * kTileBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort = &m.abort;
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      tc::mbar_init(&m.k_full[i], 1);
+      tc::mbar_init(&m.k_empty[i], 1 + 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&m.s_full[i], 2);
+      tc::mbar_init(&m.s_empty[i], 4);
+      tc::mbar_init(&m.q_full[i], 4);
+      tc::mbar_init(&m.q_empty[i], 1 + 8);
+    }
+    for (int i = 0; i < kSegs; ++i) {
+      tc::mbar_init(&m.seg_full[i], 1);
+      tc::mbar_init(&m.seg_empty[i], 1 + 1 + 4 + 8);
+    }
+    tc::mbar_init(&m.drain, 1);
+    m.abort = 0;
+    tc::fence_mbar_init();
+  }
+  for (int i = tid; i < kKeep * kTile; i += kThreads) (&m.keep[0][0])[i] = 0.f;
+  if (warp == 1) {
+    tc::tmem_alloc(&m.tmem, 512);
+    tc::tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) tc::tma_prefetch_map(&map_k);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = m.tmem;
+  pdl_wait();
+  pdl_trigger();
+
+  Ring<kSegs> rg;
+  auto next_segment = [&] {
+    const bool ok = wait_for(&m.seg_full[rg.at], rg.phase, abort, a.wait_ns);
+    return __all_sync(0xffffffffu, ok) != 0;
+  };
+  auto done_segment = [&] {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&m.seg_empty[rg.at]);
+    rg.next();
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const int pt = kTile / a.page;           // pages of a tile
+    const int oob = a.num_pages * a.Hkv * a.page;  // a row past the pool
+    const uint32_t box = (uint32_t)a.page * 128;
+    const float c = fabsf(a.scale) * kLog2e;
+    Ring<kStages> rk;
+    int in_flight = 0;
+    bool ok = true;
+    while (ok) {
+      if (!next_segment()) break;
+      const Segment g = m.seg[rg.at];
+      done_segment();
+      if (g.done) break;
+      if (g.rows == 0) continue;
+      const int page0 = g.tok0 / a.page;
+      const int last = min((g.end + a.page - 1) / a.page, page0 + g.T * pt);
+      // page ids two chunks of 32 ahead, their scales one ahead
+      int at = page0;
+      auto load_id = [&](int first) {
+        const int pg = first + lane;
+        return pg < last ? a.table[(size_t)g.b * a.max_pages + pg] : -1;
+      };
+      auto load_scale = [&](int pid) {
+        return pid >= 0 && pid < a.num_pages
+                   ? a.k_scale[(size_t)pid * a.Hkv + g.hk] : 0.f;
+      };
+      int id = load_id(at), id1 = load_id(at + 32), id2 = load_id(at + 64);
+      float ks = load_scale(id), ks1 = load_scale(id1);
+#pragma unroll 1
+      for (int t = 0; t < g.T && ok; ++t) {
+        const int pg = page0 + t * pt;       // first page of the tile
+        if (pg - at == 32) {
+          at += 32;
+          id = id1;
+          ks = ks1;
+          id1 = id2;
+          ks1 = load_scale(id1);
+          id2 = load_id(at + 64);
+        }
+        const int from = pg - at + lane;     // lane < pt: its page
+        const int pid = __shfl_sync(0xffffffffu, id, from & 31);
+        const bool have = lane < pt && pg + lane < last;
+        const bool bad = have && (pid < 0 || pid >= a.num_pages);
+        if (bad) raise_error(a.err, kErrBadIndex);
+        const int row = bad ? oob : (pid * a.Hkv + g.hk) * a.page;
+        const uint32_t bytes = box * __popc(__ballot_sync(0xffffffffu, have));
+        ok = wait_for(&m.k_empty[rk.at], rk.phase ^ 1, abort, a.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) expect_tx(&m.k_full[rk.at], bytes);
+        __syncwarp();
+        if (have)                            // (the factors follow)
+          tc::tma_load_2d(sk + rk.at * kTileBytes + lane * box, &map_k,
+                          &m.k_full[rk.at], 0, row);
+        const float pk = __shfl_sync(0xffffffffu, ks, from & 31);
+        if (lane < pt) m.ks[rk.at][lane] = have && !bad ? pk * c : 0.f;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&m.k_full[rk.at]);
+        rk.next();
+        in_flight = min(in_flight + 1, kStages);
+      }
+    }
+    // no copy is in flight when the CTA leaves, whatever the others did
+    int never = 0;
+    for (; in_flight > 0; --in_flight) {
+      Ring<kStages> r = rk;
+      r.at -= in_flight;
+      if (r.at < 0) {
+        r.at += kStages;
+        r.phase ^= 1;
+      }
+      wait_for(&m.k_full[r.at], r.phase, &never, kWaitLimitNs);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    const uint32_t tm = uniform(tmem);
+    const uint32_t sk_u = uniform(tc::smem_u32(sk));
+    const uint32_t sq_u = uniform(tc::smem_u32(sq));
+    const int steps = (a.D + 31) / 32;       // of 32 dimensions
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t par) {
+      ok = ok && wait_for(bar, par, abort, a.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      return ok;
+    };
+    Ring<kStages> rk;
+    Ring<2> rq;
+    uint32_t par0 = 0, par1 = 0;             // of the score buffers
+    while (ok) {
+      if (!next_segment()) break;
+      const bool done = m.seg[rg.at].done;
+      const int T = uniform(m.seg[rg.at].T), rows = uniform(m.seg[rg.at].rows);
+      done_segment();
+      if (done) break;
+      if (rows == 0) continue;
+      const uint32_t idesc = uniform(idesc_n(2 * ((rows + 7) / 8 * 8)));
+      const uint64_t dq =
+          tc::sdesc_k_sw128(uniform(sq_u + rq.at * kQBytes));
+      if (!wait(&m.q_full[rq.at], rq.phase)) break;
+#pragma unroll 1
+      for (int t = 0; t < T && ok; ++t) {
+        const int buf = t & 1;
+        // (a buffer's first use finds it empty)
+        if (!wait(&m.s_empty[buf], (buf ? par1 : par0) ^ 1)) break;
+        if (buf) par1 ^= 1; else par0 ^= 1;
+        if (!wait(&m.k_full[rk.at], rk.phase)) break;
+        tc::fence_after_sync();
+        const uint32_t d = uniform(tm + buf * 256);
+        const uint64_t dk =
+            tc::sdesc_k_sw128(uniform(sk_u + rk.at * kTileBytes));
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < steps)
+              tc::mma_e4m3(d, dk + 2 * k, dq + 2 * k, idesc, k > 0);
+          tc::mma_commit(&m.k_empty[rk.at]);
+          tc::mma_commit(&m.s_full[buf]);
+          tc::mbar_arrive(&m.s_full[buf]);   // (releases the tile's factors)
+          if (t == T - 1) tc::mma_commit(&m.q_empty[rq.at]);
+        }
+        __syncwarp();
+        rk.next();
+      }
+      rq.next();
+    }
+    if (elect_one()) tc::mma_commit(&m.drain);
+    __syncwarp();
+    int never = 0;
+    wait_for(&m.drain, 0, &never, kWaitLimitNs);
+  } else if (warp == 2) {
+    // ------------------------------------------------------------- the run
+    Walk w;
+    bool bad = false;
+    walk_start(a, shape, blockIdx.x, gridDim.x, w, &bad);
+    if (bad && blockIdx.x == 0) raise_error(a.err, kErrBadIndex);
+    bool ok = true;
+    auto put = [&](const Segment& g) {
+      ok = ok && wait_for(&m.seg_empty[rg.at], rg.phase ^ 1, abort, a.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      if (lane == 0) {
+        m.seg[rg.at] = g;
+        tc::mbar_arrive(&m.seg_full[rg.at]);
+      }
+      __syncwarp();
+      rg.next();
+    };
+    Segment g;
+    int t0;
+    g.done = 0;
+#pragma unroll 1
+    while (ok && walk_next(a, shape, w, g, t0)) {
+      const int rows = g.nq * shape.g, all = g.T;
+      g.lone = rows > 0 && rows <= kRows;
+#pragma unroll 1
+      for (int from = 0; from < all && ok; from += g.lone ? all : kKeep) {
+        const int T = g.lone ? all : min(kKeep, all - from);
+        g.tok0 = shape.first + (t0 + from) * kTile;
+#pragma unroll 1
+        for (int r = 0; r < rows && ok; r += kRows) {
+          g.row0 = r;
+          g.rows = min(kRows, rows - r);
+          // tiles that the last of these rows sees
+          const int i = (r + g.rows - 1) / shape.g;
+          const int lim = a.causal ? g.n - g.nq + i + 1 : g.n;
+          g.T = min(T, (max(0, lim - g.tok0) + kTile - 1) / kTile);
+          if (g.T > 0) put(g);
+        }
+        if (!g.lone) {
+          g.rows = 0;
+          g.T = T;
+          put(g);
+        }
+      }
+    }
+    g.done = 1;
+    put(g);
+  } else if (warp >= 4 && warp < 8) {
+    // -------------------------------------------------------------- q's parts
+    const int ch = tid & 7, r16 = (tid - 128) >> 3;  // 16 dimensions of a row
+    Ring<2> rq;
+    bool ok = true;
+    while (ok) {
+      if (!next_segment()) break;
+      const Segment g = m.seg[rg.at];
+      done_segment();
+      if (g.done) break;
+      if (g.rows == 0) continue;
+      ok = wait_for(&m.q_empty[rq.at], rq.phase ^ 1, abort, a.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      uint8_t* q = sq + rq.at * kQBytes;
+      const int np = (g.rows + 7) / 8 * 8;   // rows of a part
+      // All values fly at once, asynchronously, to where their codes will be:
+      // the first 64 dimensions of a row in its first part, the others in its
+      // second.  The lanes of a row read them before one writes.
+      auto raw = [&](int r) {
+        return q + (ch >> 2) * np * 128 + r * 128 + (ch & 3) * 32;
+      };
+      auto out_of = [&](int r) {
+        const int row = g.row0 + r, i = row / shape.g;
+        return (long long)((size_t)g.b * a.Q + i) * a.Hq + g.hk * shape.g +
+               row - i * shape.g;
+      };
+#pragma unroll 1
+      for (int r = r16; r < np; r += 16) {
+        const bool read = r < g.rows && ch * 16 < a.D;
+        const long long out = out_of(r);
+        const uint8_t* src = static_cast<const uint8_t*>(a.q) +
+                             (read ? (out * a.D + ch * 16) * 2 : 0);
+        copy16(tc::smem_u32(raw(r)), src, read);
+        copy16(tc::smem_u32(raw(r) + 16), src + 16, read);
+        if (ch == 0) {
+          const float lse = r < g.rows ? a.lse[out] : -INFINITY;
+          m.row[rq.at][r].nl = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+          m.lim[rq.at][r] =
+              a.causal ? g.n - g.nq + (g.row0 + r) / shape.g + 1 : g.n;
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      // (a warp has four rows: its lanes go together)
+#pragma unroll 1
+      for (int r = r16; r < np; r += 16) {
+        const uint4 u0 = *reinterpret_cast<const uint4*>(raw(r));
+        const uint4 u1 = *reinterpret_cast<const uint4*>(raw(r) + 16);
+        const uint32_t v[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+        float top = 0.f;                     // infinite: a NaN
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float x0 = __uint_as_float(v[k] << 16);
+          const float x1 = __uint_as_float(v[k] & 0xffff0000u);
+          top = x0 == x0 ? fmaxf(top, fabsf(x0)) : INFINITY;
+          top = x1 == x1 ? fmaxf(top, fabsf(x1)) : INFINITY;
+        }
+#pragma unroll
+        for (int o = 4; o; o >>= 1)
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
+        float up = top < INFINITY ? __uint_as_float((134 - e) << 23)
+                                  : __uint_as_float(0x7fffffffu);
+        if (a.scale < 0.f) up = -up;
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float2 y = make_float2(__uint_as_float(v[k] << 16) * up,
+                                       __uint_as_float(v[k] & 0xffff0000u) * up);
+          const uint32_t h =
+              __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+          const float2 f = __half22float2(
+              __half2(__nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3)));
+          const uint32_t l = __nv_cvt_float2_to_fp8x2(
+              make_float2((y.x - f.x) * 32.f, (y.y - f.y) * 32.f),
+              __NV_SATFINITE, __NV_E4M3);
+          if (k & 1) {
+            hi[k >> 1] |= h << 16;
+            lo[k >> 1] |= l << 16;
+          } else {
+            hi[k >> 1] = h;
+            lo[k >> 1] = l;
+          }
+        }
+        // (np is a multiple of 8: the second part's swizzle is the first's)
+        uint8_t* dst = q + r * 128 + ((ch ^ (r & 7)) << 4);
+        __syncwarp();
+        *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(dst + np * 128) =
+            make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        if (ch == 0)
+          m.row[rq.at][r].rel = __uint_as_float((120 + e) << 23);
+      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&m.q_full[rq.at]);
+      rq.next();
+    }
+  } else if (warp >= 8) {
+    // -------------------------------------------------------------- weights
+    const int half = (warp - 8) >> 2, quarter = warp & 3;
+    const int tok = quarter * 32 + lane;
+    const uint32_t s_col =
+        tmem + ((uint32_t)(quarter * 32) << 16) + half * 256;
+    const int page_bits = __ffs(a.page) - 1;
+    Ring<2> rq;
+    int tile = 0;                            // copied before the segment's
+    uint32_t s_par = 0;
+    bool ok = true;
+    while (ok) {
+      if (!next_segment()) break;
+      const Segment g = m.seg[rg.at];
+      done_segment();
+      if (g.done) break;
+      auto store = [&](int t, float sum) {
+        const int at = g.tok0 + t * kTile + tok;
+        if (at >= a.first && at < g.n) mass_store(a, g.b, g.hk, at, sum);
+      };
+      if (g.rows == 0) {                     // the sums are complete
+        for (int t = half; t < g.T; t += 2) {
+          store(t, m.keep[t][tok]);
+          m.keep[t][tok] = 0.f;
+        }
+        continue;
+      }
+      const int np = (g.rows + 7) / 8 * 8;
+      const Row* rows = m.row[rq.at];
+      const int* lims = m.lim[rq.at];
+      ok = wait_for(&m.q_full[rq.at], rq.phase, abort, a.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+#pragma unroll 1
+      for (int t = half; t < g.T; t += 2) {
+        ok = wait_for(&m.s_full[half], s_par, abort, a.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        s_par ^= 1;
+        tc::fence_after_sync();
+        const float ct = m.ks[(tile + t) % kStages][tok >> page_bits];
+        const int at = g.tok0 + t * kTile + tok;
+        // some row does not see all of the tile
+        const bool masked = lims[0] < g.tok0 + (t + 1) * kTile;
+        float sum = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < np; c += 8) {
+          float hi[8], lo[8];
+          tmem_ld_x8(s_col + c, hi);
+          tmem_ld_x8(s_col + np + c, lo);
+          tmem_loaded(hi);
+          tmem_loaded(lo);
+          float part[2] = {0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const Row r = rows[c + j];
+            float x = fmaf(fmaf(lo[j], 1.f / 32, hi[j]) * ct, r.rel, r.nl);
+            if (masked && at >= lims[c + j]) x = -INFINITY;
+            part[j & 1] += tc::ex2_approx(x);
+          }
+          sum += part[0] + part[1];
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(&m.s_empty[half]);
+          tc::mbar_arrive(&m.k_empty[(tile + t) % kStages]);  // (the factors)
+        }
+        if (g.lone)
+          store(t, sum);
+        else
+          m.keep[t][tok] += sum;
+      }
+      if (!ok) break;
+      tile += g.T;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&m.q_empty[rq.at]);
+      rq.next();
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 1) tc::tmem_dealloc(tmem, 512);
+  if (tid == 0 && m.abort) raise_error(a.err, kErrTimeout);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_mass_tc(const AttnMassArgs& a, int sms,
+                                cudaStream_t stream) {
+  Shape s;
+  s.g = a.Hq / a.Hkv;
+  s.first = a.first / kTile * kTile;
+  const long long tiles = (mass_most(a) - s.first + kTile - 1) / kTile;
+  const long long passes = ((long long)a.Q * s.g + kRows - 1) / kRows;
+  if ((long long)a.B * a.Hkv * (kUnitCost + tiles * passes) > 0x7fffffffll)
+    return cudaErrorNotSupported;
+  CUtensorMap mk;
+  const uint64_t pool = (uint64_t)a.num_pages * a.Hkv * a.page;
+  if (!make_tmap_u8_2d(&mk, a.k_codes, a.D, pool, 128, a.page))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(
+      attn_mass_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  PdlLaunch L(dim3(sms), dim3(kThreads), kSmem, stream);
+  return cudaLaunchKernelEx(&L.cfg, attn_mass_tc_kernel, mk, a, s);
+}
+
+}  // namespace dflash

@@ -244,6 +244,9 @@ __device__ __forceinline__ int mass_length(const AttnMassArgs& a, int b,
                                            bool* bad) {
   return attn_clamp(a.kv_len[b], mass_most(a), bad);
 }
+// attn_mass_tc.cu: the tensor-core kernel, for what paged_attn_tc_takes.
+cudaError_t launch_attn_mass_tc(const AttnMassArgs& a, int sms,
+                                cudaStream_t s);
 // The weight that token t of sequence b and key head hk got from this call.
 __device__ __forceinline__ void mass_store(const AttnMassArgs& a, int b,
                                            int hk, int t, float sum) {
