@@ -1,21 +1,22 @@
 // Log probabilities of given tokens, their ranks, the rows' entropies and
 // their most likely tokens.
 //
-// Mathematics.  With x = l / T, m = max l, d = (l - m) / T, w = exp(d):
-//   lse = m / T + ln S,  S = sum w;   ln p_v = d_v - ln S;
-//   entropy = ln S - (sum w d) / S.
-// One pass keeps m, S and U = sum w d of what a thread has seen; when m grows
-// by h / T, U becomes f (U - S h / T) and S f S with f = exp(-h / T), and two
-// threads' sums join likewise.  A token's rank is the number of tokens before it
-// in the order (logit descending, id ascending), so its logit is fetched first
-// and the pass counts.
+// Mathematics, in bits: with c = log2(e) / T and a whole number r near the largest
+// l c, y = l c - r (one rounding), w = 2^y, S = sum w, U = sum w y:
+//   lse = ln2 (r + log2 S);   ln p_v = ln2 (y_v - log2 S);
+//   entropy = ln2 (log2 S - U / S).
+// One pass keeps r, S and U of what a thread has seen; when r grows by h, U becomes
+// 2^-h (U - h S) and S 2^-h S, and two threads' sums join likewise.  A token's rank
+// is the number of tokens before it in the order (logit descending, id ascending),
+// so its logit is fetched first and the pass counts: words before the token those
+// above the next smaller number, words after it those above its logit.
 //
 // The K most likely: the K-th largest maximum of 64 groups of threads bounds
-// the K-th largest logit of the slice from below; only the groups that reach it
-// read their parts again, from L2, for the few more than K candidates, which are
-// ranked by counting.  A cluster of CTAs owns a row; the first of them joins the
-// CTAs' sums and lists.  What overflows the list (ties by the thousand) is found
-// by K searches for the next largest instead.
+// the K-th largest logit of the slice from below; only the threads that reach it
+// have their parts read again, from L2, a warp at a time for each, for the few more
+// than K candidates, which are ranked by counting.  A cluster of CTAs owns a row;
+// the first of them joins the CTAs' sums and lists.  What overflows the list (ties
+// by the thousand) is found by K searches for the next largest instead.
 //
 // What bounds it: bytes in batches, the chain of dependent steps for one row.
 #include <cooperative_groups.h>
@@ -43,6 +44,7 @@ constexpr int kMost = DFLASH_MAX_ALTERNATIVES;
 constexpr int kList = 1024;     // candidates of a CTA
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 static_assert(kMost <= kGroups, "");
 
 struct Args {
@@ -56,19 +58,30 @@ struct Args {
   int* err;
 };
 
-// m: largest logit; s, u: sums of w and of w (l - m), not yet over T.
+// m: largest logit; r: the reference, -inf while there is none; s, u: the sums.
 struct Sums {
-  float m, s, u;
+  float m, r, s, u;
 };
-__device__ __forceinline__ Sums join(const Sums& a, const Sums& b, float c) {
-  if (a.m == -INFINITY) return b;
-  if (b.m == -INFINITY) return a;
-  const Sums& x = a.m >= b.m ? a : b;
-  const Sums& y = a.m >= b.m ? b : a;
-  const float h = y.m - x.m;
-  if (!(h > -INFINITY)) return x;  // x.m is infinite
-  const float f = tc::ex2_approx(h * c);
-  return Sums{x.m, x.s + f * y.s, x.u + f * (y.u + h * y.s)};
+// 2^h u and s of a reference that is h higher.
+__device__ __forceinline__ void lower(float h, float& s, float& u) {
+  const float f = tc::ex2_approx(h);
+  u = f * fmaf(h, s, u);
+  s *= f;
+}
+__device__ __forceinline__ Sums join(Sums a, Sums b) {
+  if (b.r > a.r) {
+    const Sums t = a;
+    a = b;
+    b = t;
+  }
+  a.m = fmaxf(a.m, b.m);
+  const float h = b.r - a.r;         // (no reference, an infinite one: -inf, NaN)
+  if (h > -INFINITY) {
+    lower(h, b.s, b.u);
+    a.s += b.s;
+    a.u += b.u;
+  }
+  return a;
 }
 
 // What the CTAs of a row hand to the first of them.
@@ -117,18 +130,42 @@ struct Words {
   }
 };
 
-// max of two numbers; a NaN if one is.
-__device__ __forceinline__ float max_nan(float a, float b) {
+// max of three numbers; a NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// The next smaller number (of -inf: a NaN, above which nothing is).
+__device__ __forceinline__ float next_below(float x) {
+  const int w = __float_as_int(x);
+  return x == 0.f ? __int_as_float(0x80000001)
+                  : __int_as_float(x > 0.f ? w - 1 : w + 1);
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 
 template <typename T, bool kTop, bool kRank>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     logprobs_kernel(const __grid_constant__ Args a) {
   constexpr int N = Words<T>::N;
-  constexpr int kAhead = 4;          // words in flight
+  constexpr int kAhead = 2;          // words in flight
   extern __shared__ uint4 smem16[];
   Shared& sh = *reinterpret_cast<Shared*>(smem16);
   cg::cluster_group cluster = cg::this_cluster();
@@ -189,8 +226,10 @@ __global__ void __launch_bounds__(kThreads)
     return w;
   };
 
-  Sums acc{-INFINITY, 0.f, 0.f};
+  Sums acc{-INFINITY, -INFINITY, 0.f, 0.f};
   int before = 0;
+  const float below = next_below(mine);
+  const uint64_t c2 = pack2(c, c);
   auto take = [&](const uint4 (&raw)[kAhead], int first, int n) {
     float f[kAhead][N];
     float top = -INFINITY;
@@ -199,7 +238,7 @@ __global__ void __launch_bounds__(kThreads)
       if (k >= n) break;
       Words<T>::get(raw[k], f[k]);
 #pragma unroll
-      for (int j = 0; j < N; ++j) top = max_nan(top, f[k][j]);
+      for (int j = 0; j < N; j += 2) top = max_nan(top, f[k][j], f[k][j + 1]);
     }
     if (top != top) {                // a NaN: left out
       odd = true;
@@ -215,53 +254,101 @@ __global__ void __launch_bounds__(kThreads)
       }
     }
     if (top > acc.m) {
-      const float h = acc.m - top;   // -inf at first, and before +inf
-      const float g = tc::ex2_approx(h * c);
-      acc.u = h > -INFINITY ? g * fmaf(h, acc.s, acc.u) : 0.f;
-      acc.s *= g;
       acc.m = top;
+      const float r = ceilf(top * c);
+      if (r > acc.r) {
+        const float h = acc.r - r;   // -inf at first, and before +inf
+        if (h > -INFINITY) lower(h, acc.s, acc.u);
+        acc.r = r;
+      }
     }
-    const float ref = acc.m == -INFINITY ? 0.f : acc.m;
+    const float ref = acc.r == -INFINITY ? 0.f : -acc.r;
+    const uint64_t ref2 = pack2(ref, ref);
+    uint64_t s2 = 0, u2 = 0;
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       if (k >= n) break;
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        // (-inf: a weight of 0 times a number)
-        const float d = fmaxf(f[k][j] - ref, -1e30f);
-        const float w = tc::ex2_approx(d * c);
-        acc.s += w;
-        acc.u = fmaf(w, d, acc.u);
+      for (int j = 0; j < N; j += 2) {
+        const uint64_t y = fma2(pack2(f[k][j], f[k][j + 1]), c2, ref2);
+        float y0, y1;
+        unpack2(y, y0, y1);
+        const uint64_t w = pack2(tc::ex2_approx(y0), tc::ex2_approx(y1));
+        s2 = add2(s2, w);
+        u2 = fma2(w, y, u2);
       }
-      if constexpr (kRank) {
-        const long long at = ((long long)first + k * kThreads) * N - skew;
+    }
+    float s0, s1, u0, u1;
+    unpack2(s2, s0, s1);
+    unpack2(u2, u0, u1);
+    u0 += u1;
+    if (u0 != u0) {                  // -inf, whose weight is 0: again without
+      u0 = 0.f;
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-          before += f[k][j] > mine ||
-                    (f[k][j] == mine && at + j < token && at + j >= 0);
+      for (int k = 0; k < kAhead; ++k) {
+        if (k >= n) break;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const float y = fmaf(f[k][j], c, ref);
+          if (y > -INFINITY) u0 = fmaf(tc::ex2_approx(y), y, u0);
+        }
+      }
+    }
+    acc.s += s0 + s1;
+    acc.u += u0;
+    if constexpr (kRank) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (k >= n) break;
+        const long long at = ((long long)first + k * kThreads) * N - skew;
+        if (at < 0 || (at <= token && token < at + N) || mine == -INFINITY) {
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            before += f[k][j] > mine ||
+                      (f[k][j] == mine && at + j < token && at + j >= 0);
+        } else {
+          const float than = at < token ? below : mine;
+#pragma unroll
+          for (int j = 0; j < N; ++j) before += f[k][j] > than;
+        }
       }
     }
   };
-  for (int i = w0 + tid; i < w1; i += kAhead * kThreads) {
-    uint4 raw[kAhead];
-    const int n = min(kAhead, (w1 - i + kThreads - 1) / kThreads);
+  {
+    uint4 raw[kAhead], next[kAhead];
+    auto ask = [&](int i, uint4 (&to)[kAhead]) {
+      const int n = min(kAhead, (w1 - i + kThreads - 1) / kThreads);
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (k < n) raw[k] = fetch(i + k * kThreads);
-    take(raw, i, n);
+      for (int k = 0; k < kAhead; ++k)
+        if (k < n) to[k] = fetch(i + k * kThreads);
+      return n;
+    };
+    int i = w0 + tid, n = ask(i, raw);
+#pragma unroll 1
+    while (n > 0) {
+      const int n2 = ask(i + kAhead * kThreads, next);
+      take(raw, i, n);
+      i += kAhead * kThreads;
+      n = n2;
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) raw[k] = next[k];
+    }
   }
 
   // ---- the CTA's sums ------------------------------------------------------
   const float my_max = acc.m;
+  auto fold = [&](Sums& x) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const Sums x{__shfl_xor_sync(0xffffffffu, acc.m, o),
-                 __shfl_xor_sync(0xffffffffu, acc.s, o),
-                 __shfl_xor_sync(0xffffffffu, acc.u, o)};
-    // the lower lane's first in both, so that both lanes get the same bits
-    acc = lane & o ? join(x, acc, c) : join(acc, x, c);
-    if (kRank) before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
+    for (int o = 16; o; o >>= 1) {
+      const Sums y{__shfl_xor_sync(0xffffffffu, x.m, o),
+                   __shfl_xor_sync(0xffffffffu, x.r, o),
+                   __shfl_xor_sync(0xffffffffu, x.s, o),
+                   __shfl_xor_sync(0xffffffffu, x.u, o)};
+      x = join(x, y);                // (both lanes get the same bits)
+    }
+  };
+  fold(acc);
+  if (kRank) before = __reduce_add_sync(0xffffffffu, before);
   odd = __any_sync(0xffffffffu, odd);
   if (lane == 0) {
     sh.warp_sums[warp] = acc;
@@ -279,18 +366,13 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
   Shared* first = cluster.map_shared_rank(&sh, 0);
   if (tid < 32) {
-    Sums x = tid < kWarps ? sh.warp_sums[tid] : Sums{-INFINITY, 0.f, 0.f};
-    int b = tid < kWarps ? sh.warp_before[tid] : 0;
-    int o = tid < kWarps ? sh.warp_odd[tid] : 0;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-      const Sums y{__shfl_xor_sync(0xffffffffu, x.m, d),
-                   __shfl_xor_sync(0xffffffffu, x.s, d),
-                   __shfl_xor_sync(0xffffffffu, x.u, d)};
-      x = tid & d ? join(y, x, c) : join(x, y, c);
-      b += __shfl_xor_sync(0xffffffffu, b, d);
-      o |= __shfl_xor_sync(0xffffffffu, o, d);
-    }
+    Sums x = tid < kWarps ? sh.warp_sums[tid]
+                          : Sums{-INFINITY, -INFINITY, 0.f, 0.f};
+    fold(x);
+    const int b =
+        __reduce_add_sync(0xffffffffu, tid < kWarps ? sh.warp_before[tid] : 0);
+    const int o =
+        __reduce_or_sync(0xffffffffu, tid < kWarps ? sh.warp_odd[tid] : 0);
     // every CTA of the cluster has started
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     if (tid == 0) {
@@ -316,21 +398,39 @@ __global__ void __launch_bounds__(kThreads)
     }
     __syncthreads();
     const float bound = sh.bound;
-    // -inf: fewer than K groups hold any token, so every token above -inf is
-    // a candidate
-    if (sh.group_max[tid / kGroupOf] >= bound && my_max >= bound &&
-        my_max > -INFINITY)
-      for (int i = w0 + tid; i < w1; i += kThreads) {
-        float f[N];
-        Words<T>::get(fetch(i), f);
+    // (-inf: fewer than K groups hold any token; then every token above it is a
+    // candidate)
+    uint32_t reach = __ballot_sync(
+        0xffffffffu, my_max >= bound && my_max > -INFINITY);
+    while (reach) {                  // the whole warp reads one thread's part
+      const int who = __ffs(reach) - 1;
+      reach &= reach - 1;
+      constexpr int kAt = 4;         // words on their way at once
+      for (int i = w0 + warp * 32 + who + lane * kThreads; i < w1;
+           i += kAt * 32 * kThreads) {
+        uint4 raw[kAt];
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-          if (f[j] >= bound && f[j] > -INFINITY) {
-            const int at = atomicAdd(&sh.listed, 1);
-            if (at < kList)
-              sh.list[at] = word_of(f[j], (int)((long long)i * N + j - skew));
-          }
+        for (int k = 0; k < kAt; ++k) {
+          const int at = i + k * 32 * kThreads;
+          raw[k] = make_uint4(0, 0, 0, 0);
+          if (at < w1) raw[k] = fetch(at);
+        }
+#pragma unroll
+        for (int k = 0; k < kAt; ++k) {
+          const int at = i + k * 32 * kThreads;
+          float f[N];
+          Words<T>::get(raw[k], f);
+#pragma unroll
+          for (int j = 0; j < N; ++j)
+            if (at < w1 && f[j] >= bound && f[j] > -INFINITY) {
+              const int to = atomicAdd(&sh.listed, 1);
+              if (to < kList)
+                sh.list[to] =
+                    word_of(f[j], (int)((long long)at * N + j - skew));
+            }
+        }
       }
+    }
     __syncthreads();
     int n = sh.listed;
     if (n <= kList) {
@@ -373,29 +473,35 @@ __global__ void __launch_bounds__(kThreads)
   if (me != 0) return;
 
   // ---- the row -----------------------------------------------------------------
-  Sums x{-INFINITY, 0.f, 0.f};
+  Sums x{-INFINITY, -INFINITY, 0.f, 0.f};
   int rank = 0, any_odd = 0;
   for (int i = 0; i < C; ++i) {
-    x = join(x, sh.sums[i], c);
+    x = join(x, sh.sums[i]);
     rank += sh.before[i];
     any_odd |= sh.odd[i];
   }
-  const bool empty = x.m == -INFINITY, infinite = x.m == INFINITY;
-  const float inv_t = 1.f / t;
-  const float log_s = logf(x.s);
+  // (an x beyond fp32's range counts as infinite)
+  const bool empty = x.m == -INFINITY;
+  const bool infinite = !empty && !(fabsf(x.r) < INFINITY);
+  const float log_s = log2f(x.s);
   const float nan = __int_as_float(0x7fffffff);
+  // (ln p in one rounding of y: exact for the row's likeliest tokens)
+  auto log_p = [&](float l) { return (fmaf(l, c, -x.r) - log_s) * kLn2; };
   if (tid == 0) {
     if (any_odd || empty || infinite) raise_error(a.err, kErrNonfinite);
     if (token >= a.V || token < -1) raise_error(a.err, kErrBadIndex);
     if (a.lse)
-      a.lse[r] = empty || infinite ? x.m : fmaf(x.m, inv_t, log_s);
+      a.lse[r] = empty      ? -INFINITY
+                 : infinite ? x.r
+                            : (x.r + log_s) * kLn2;
     if (a.entropy)
-      a.entropy[r] =
-          empty || infinite ? nan : fmaxf(log_s - x.u / x.s * inv_t, 0.f);
+      a.entropy[r] = empty || infinite
+                         ? nan
+                         : fmaxf((log_s - x.u / x.s) * kLn2, 0.f);
     if (a.logprob)
-      a.logprob[r] = token == -1                    ? 0.f
+      a.logprob[r] = token == -1                   ? 0.f
                      : !given || empty || infinite ? nan
-                                                   : (mine - x.m) / t - log_s;
+                                                   : log_p(mine);
     if (kRank) a.rank[r] = given && mine == mine ? rank : -1;
   }
   if (kTop) {
@@ -419,7 +525,7 @@ __global__ void __launch_bounds__(kThreads)
       if (above < a.K) {
         const float v = value_of(w);
         a.top[(long long)r * a.K + above] =
-            infinite ? nan : (v - x.m) / t - log_s;
+            infinite ? nan : log_p(v);
         a.top_id[(long long)r * a.K + above] = (int)~(uint32_t)w;
       }
     }
@@ -429,10 +535,11 @@ __global__ void __launch_bounds__(kThreads)
 template <typename T>
 cudaError_t launch(const Args& args, int sms, cudaStream_t s) {
   Args a = args;
-  // CTAs of a row: as many as two an SM leave room for, with 4096 tokens each
+  // CTAs of a row: as many as all rows' find room at once, two to an SM (the
+  // chain of steps at a CTA's end is then paid once: 288 rows of 151936 fp32
+  // logits 51 us, with two CTAs each 55 us), with 4096 tokens each
   int C = 1;
-  while (C < kMaxCluster && (long long)a.R * C < 2 * sms &&
-         a.V > 4096 * C)
+  while (C < kMaxCluster && (long long)a.R * C <= sms && a.V > 4096 * C)
     C *= 2;
   const int N = 16 / sizeof(T);
   // (a row may start anywhere in its first word)
