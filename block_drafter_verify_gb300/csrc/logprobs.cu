@@ -405,30 +405,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     while (reach) {                  // the whole warp reads one thread's part
       const int who = __ffs(reach) - 1;
       reach &= reach - 1;
-      constexpr int kAt = 4;         // words on their way at once
+#pragma unroll 2
       for (int i = w0 + warp * 32 + who + lane * kThreads; i < w1;
-           i += kAt * 32 * kThreads) {
-        uint4 raw[kAt];
+           i += 32 * kThreads) {
+        float f[N];
+        Words<T>::get(fetch(i), f);
 #pragma unroll
-        for (int k = 0; k < kAt; ++k) {
-          const int at = i + k * 32 * kThreads;
-          raw[k] = make_uint4(0, 0, 0, 0);
-          if (at < w1) raw[k] = fetch(at);
-        }
-#pragma unroll
-        for (int k = 0; k < kAt; ++k) {
-          const int at = i + k * 32 * kThreads;
-          float f[N];
-          Words<T>::get(raw[k], f);
-#pragma unroll
-          for (int j = 0; j < N; ++j)
-            if (at < w1 && f[j] >= bound && f[j] > -INFINITY) {
-              const int to = atomicAdd(&sh.listed, 1);
-              if (to < kList)
-                sh.list[to] =
-                    word_of(f[j], (int)((long long)at * N + j - skew));
-            }
-        }
+        for (int j = 0; j < N; ++j)
+          if (f[j] >= bound && f[j] > -INFINITY) {
+            const int to = atomicAdd(&sh.listed, 1);
+            if (to < kList)
+              sh.list[to] = word_of(f[j], (int)((long long)i * N + j - skew));
+          }
       }
     }
     __syncthreads();
