@@ -25,8 +25,13 @@
 // 69 us.  Three CTAs to an SM: two 80 us, four (64 registers) 72 us.
 //
 // With positions of several axes a token's angles come from a row of the tables
-// for each axis; a thread's four or eight angles lie in one section, which costs
-// it one more load, or (axes in turn) are gathered one by one.
+// for each axis.  A thread whose four or eight angles lie in one section loads
+// them at once; where a section begins among them, or axes take turns, it looks
+// up the rows of the axes that occur first and gathers angles one by one.  The
+// prompts above: 63 us with one axis or sections that begin at multiples of
+// eight (the wait for a position), 74 us with thirds of 64 angles, 82 us with
+// axes in turn.  16-byte loads of every axis' part of the row, of which each
+// angle takes its own, cost the registers of the values on their way: 87 us.
 #include <cuda_fp8.h>
 
 #include "kernels.h"
@@ -267,13 +272,28 @@ __device__ __forceinline__ void load_angles(const AppendArgs& a, long long row,
       const size_t at = (size_t)row_of(axis) * r2 + first;
       load_n<float, VEC>(a.cos_tab + at, c);
       load_n<float, VEC>(a.sin_tab + at, s);
-    } else {
+    } else {                             // the rows of all axes that occur
+      uint32_t used = 0;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const size_t at =
-            (size_t)row_of(w[i / 4] >> (8 * (i % 4)) & 0xff) * r2 + first + i;
-        c[i] = a.cos_tab[at];
-        s[i] = a.sin_tab[at];
+        const uint32_t x = w[i / 4] >> (8 * (i % 4)) & 0xff;
+        used |= x < (uint32_t)a.axes ? 1u << x : 0x80000001u;
+      }
+      if (used >> 31) raise_error(a.err, kErrBadIndex);
+      uint32_t at[DFLASH_MAX_AXES];
+#pragma unroll
+      for (int x = 0; x < DFLASH_MAX_AXES; ++x)
+        at[x] = used >> x & 1 ? (uint32_t)row_of(x) : x > 0 ? at[0] : 0;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const uint32_t x = w[i / 4] >> (8 * (i % 4)) & 0xff;
+        uint32_t r = at[0];
+#pragma unroll
+        for (int k = 1; k < DFLASH_MAX_AXES; ++k)
+          if (x == k) r = at[k];
+        const size_t to = (size_t)r * r2 + first + i;
+        c[i] = a.cos_tab[to];
+        s[i] = a.sin_tab[to];
       }
     }
   }
