@@ -11,16 +11,20 @@
 // that become subnormal.
 //
 // One launch: a CTA for every sequence and key head, or a cluster of up to eight
-// where there are few.  It finds the cut (a thread holds the keys of 32 slots in
-// registers over the histograms), writes the list of kept slots, and moves their
+// where there are few.  It finds the cut (a thread holds the weights of 16 slots
+// in registers over the histograms), writes the list of kept slots, and moves their
 // codes, in place: slots only move down, so pages are taken in rounds, lower ones
 // first, of as many as the cluster's warps hold in registers.  A round's pages are
 // all read, the cluster meets, and they are written: what a later round reads lies
-// above.  (Pages in any order, each waiting for flags of those that read it: 170 us
-// for the second case below.)
+// above.
 //
-// What bounds it: few heads the chain of a round's loads (kept slots and page ids
-// are asked for a round ahead), many heads bytes.
+// What bounds it: with few heads the chain of steps (three histograms, then the
+// loads of a round; kept slots and page ids are asked for a round ahead), with
+// many bytes.  Eight heads of 128: 2100 to 2048 tokens 20 us, 131072 to 100000
+// tokens 250 us; 32 such sequences of 6000 to 8000 tokens to 6000 at most 129 us
+// (59 us of bytes at the copy's rate), where a launch for the lists, one for the
+// codes and whole histograms took 193 us, and pages in any order, each waiting for
+// flags of those that read it, 170 us.
 #include <cooperative_groups.h>
 #include <cuda_fp8.h>
 
@@ -288,6 +292,8 @@ __global__ void __launch_bounds__(
     }
     key = prefix;
     if (nan) raise_error(a.err, kErrNonfinite);
+  } else if (C > 1) {
+    cluster.sync();                          // (all CTAs have started)
   }
   // ---- the kept slots in their order ---------------------------------------
   // bit (k, j) of gt: the slot stays; of eq: it lies on the cut
