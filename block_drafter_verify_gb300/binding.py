@@ -193,6 +193,13 @@ def _on(stream):
     return stream.cuda_stream
 
 
+def _here(t, name):
+    """Refuse a tensor of another device than the current one, on which the
+    call would run."""
+    if t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is not on the current device")
+
+
 def _run(name, st):
     if st != 0:
         raise DFlashError(name, st)
@@ -564,6 +571,7 @@ def dflash_kv_append_axes(q, k, v, cos, sin, axis_pos, axis_of, pos, n_new,
     axis_of [rot/2] u8 the axis of each angle (None with one axis); pos [B]
     i32 is the slot of a sequence's first new token only."""
     A = axis_pos.shape[0]
+    _here(k, "k")
 
     def axes(rows, rot):
         if axis_pos.numel() != A * rows:
@@ -657,6 +665,7 @@ def dflash_shared_attn(q, k_codes, v_codes, k_scale, v_scale, page_table,
     """dflash_paged_attn for sequences whose first `shared` tokens (whole
     pages) are the first sequence's, read once for all; ws uint8 of
     dflash_shared_attn_workspace_bytes."""
+    _here(q, "q")
     N, Hkv, page, D = _check_cache(k_codes, v_codes, k_scale, v_scale)
     B, Q, Hq, Dq = q.shape
     tB, max_pages = page_table.shape
@@ -694,6 +703,7 @@ def dflash_attn_mass(q, k_codes, k_scale, page_table, kv_len, q_len, lse,
     these queries; fresh [B] i32 or None: slots from there on start at 0,
     those below are multiplied by `decay` first; slots below `first` are left
     as they are.  kv_len, q_len and causal as in dflash_paged_attn."""
+    _here(q, "q")
     N, Hkv, page, D = k_codes.shape
     if k_scale.numel() != N * Hkv:
         raise ValueError("scales must be [num_pages, Hkv]")
@@ -730,6 +740,7 @@ def dflash_kv_evict(mass, k_codes, v_codes, k_scale, v_scale, page_table,
     each key head.  mass_out [B,Hkv,slots] f32 or None: the kept slots' mass
     in their new places; new_len [B] i32 and kept [B,Hkv,budget] i32 (or
     None) outputs; ws uint8 of dflash_kv_evict_workspace_bytes."""
+    _here(mass, "mass")
     N, Hkv, page, D = _check_cache(k_codes, v_codes, k_scale, v_scale)
     B, max_pages = page_table.shape
     if kv_len.numel() != B or new_len.numel() != B:
@@ -756,6 +767,7 @@ def dflash_logprobs(logits, temperature, token, logprob, rank, lse, entropy,
     entropy, and the K most likely tokens: logprob, lse, entropy [R] f32, rank
     [R] i32, top [R,K] f32, top_id [R,K] i32 outputs, each may be None;
     temperature [R] f32 or None."""
+    _here(logits, "logits")
     R, V = logits.shape
     ld, step = logits.stride()
     if (step != 1 and V > 1) or not logits.is_cuda:

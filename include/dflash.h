@@ -702,7 +702,12 @@ size_t dflash_shared_attn_workspace_bytes(int B, int Q, int Hq, int Hkv,
  *   ws >= dflash_shared_attn_workspace_bytes(B, Q, Hq, Hkv, D) bytes, 256-byte
  *      aligned; its contents need no initialisation
  * Requirements, and what is flagged on the device: as dflash_paged_attn;
- * 0 <= shared <= max_pages * page, shared % page == 0.
+ * 0 <= shared <= max_pages * page, shared % page == 0.  Sizes (the page table's
+ * width among them) with which the work, counted in 128 rows times 128 tokens,
+ * could pass 2^31 give DFLASH_ERR_UNSUPPORTED.
+ * With bf16 and D <= 128 the tensor cores compute: q is taken as fp16 relative
+ * to its row's largest value (all of bf16's bits down to 2^-28 of it), a weight
+ * times its value as fp16 (2^-12 relative); sums are fp32.
  */
 dflash_status dflash_shared_attn(
     const void* q, const uint8_t* k_codes, const uint8_t* v_codes,
@@ -731,8 +736,11 @@ dflash_status dflash_shared_attn(
  *         anyway, for example a prefix that sequences share)
  *   mass  [B, Hkv] rows of fp32, ld_mass elements apart, in/out
  * Sums and weights are fp32; their order is fixed, and nothing is added
- * atomically.
- * Requirements: as dflash_paged_attn; first >= 0, ld_mass >= 1, decay finite.
+ * atomically.  (bf16 and D <= 128, the tensor cores: q as two E4M3 numbers, all
+ * of bf16's bits down to 2^-17 of its row's largest value.)
+ * Requirements: as dflash_paged_attn; first >= 0, ld_mass >= 1, decay finite;
+ * work that could pass 2^31 tiles of 128 rows times 128 tokens gives
+ * DFLASH_ERR_UNSUPPORTED.
  * On the device: as dflash_paged_attn; a kv_len beyond ld_mass sets
  * DFLASH_ERR_BAD_INDEX too (the length is clamped).
  */
@@ -805,7 +813,7 @@ dflash_status dflash_kv_evict(
  * Requirements: R >= 1, 1 <= V < 2^31 - 256, ld >= V, 0 <= K <=
  * DFLASH_MAX_ALTERNATIVES.  No workspace.
  * A NaN logit counts as -inf (as a given token: logprob NaN, rank -1).  A row
- * with a +inf logit has lse = +inf, one without any logit above -inf lse =
+ * with a +inf logit (or an x beyond fp32's range) has lse = +inf, one without any logit above -inf lse =
  * -inf; both have NaN for entropy and log probabilities.  Those three, and a T
  * that is below 2^-126 or not finite (taken as 1), set DFLASH_ERR_NONFINITE; a
  * token outside [-1, V) sets DFLASH_ERR_BAD_INDEX (logprob NaN, rank -1).
@@ -841,10 +849,10 @@ dflash_status dflash_profile_stage(int stage, void* begin, void* end);
 
 /* Limit, in nanoseconds, of the bounded waits inside the tensor-core
  * kernels of later launches: the conv, the single-CTA LM head (one row tile,
- * B*K <= 128) and dflash_paged_attn give up on a wait that runs longer, stop
- * issuing work, let their copies and MMAs in flight complete, free their TMEM
- * and set DFLASH_ERR_DEVICE_TIMEOUT in the device error word (their results
- * are then invalid).  dflash_sample's waits for the copies of a row do so too
+ * B*K <= 128), dflash_paged_attn, dflash_shared_attn and dflash_attn_mass give
+ * up on a wait that runs longer, stop issuing work, let their copies and MMAs
+ * in flight complete, free their TMEM and set DFLASH_ERR_DEVICE_TIMEOUT in the
+ * device error word (their results are then invalid).  dflash_sample's waits for the copies of a row do so too
  * (that row's token is then -1).  0 restores the default of 2 s, far beyond
  * any real wait; the CTA-pair LM head always uses it.  Process-wide host state,
  * meant for tests of that failure path ("Failure detection": a wait that
