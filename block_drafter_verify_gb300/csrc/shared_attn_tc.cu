@@ -673,12 +673,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) *parts.runs = w.runs;
       }
     }
+    // (to the end even if something gave up: the join reads what units left)
+    bool ok = true;
     for (bool more = true; more;) {
-      const bool ok = wait_for(&m.seg_empty[rg.at], rg.phase ^ 1, abort,
-                               a.wait_ns);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      ok = ok && wait_for(&m.seg_empty[rg.at], rg.phase ^ 1, abort, a.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
       Segment g;
       more = walk_next(a, shape, w, blockIdx.x, g, parts.begun);
+      if (!ok) continue;
       if (lane == 0) {
         m.seg[rg.at] = g;
         tc::mbar_arrive(&m.seg_full[rg.at]);
@@ -1089,9 +1091,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   auto add = [&](int at_b, int u, int cost, int r, size_t whole) {
     const Begun g = parts.begun[unit_of(s, a.Hkv, at_b, hk, u)];
     const int work = work_of(g.T, cost);
-    for (int c = g.c0 + lane; c - lane <= g.c1; c += 32) {
+    // (in range whatever another call has left in a workspace that is its own
+    // at the same time)
+    const int c1 = min(g.c1, kMaxCtas - 1);
+    for (int c = max(g.c0, 0) + lane; c - lane <= c1; c += 32) {
       int at = -1;
-      if (c <= g.c1) {
+      if (c <= c1) {
         const int p0 = max(0, runs.start(c) - g.first);
         const int p1 = min(work, runs.start(c + 1) - g.first);
         const int t0 = tiles_before(p0, g.T, cost);
