@@ -205,8 +205,18 @@ struct PagedAttnArgs {
 // paged_attn_tc.cu: the tensor-core kernels.
 bool paged_attn_tc_takes(int D, dflash_dtype dt);
 size_t paged_attn_tc_ws(int B, int Q, int Hq, int Hkv);
+// shared: tokens that all sequences begin with, in the pages of the first one's
+// row of the table.  own: of the sequences' other tokens only, out [rows, D]
+// fp32 the sums of weights times values, lse [rows] float2 the {reference, sum
+// of weights}, for units of up to kPagedTcOwnRows rows.
+constexpr int kPagedTcOwnRows = 32;
+struct PagedTcUnits {
+  int N, row_tiles;       // rows of a unit; units of a sequence and key head
+};
+PagedTcUnits paged_attn_tc_units(long long Q, int Hq, int Hkv);
 cudaError_t launch_paged_attn_tc(const PagedAttnArgs& a, int sms, float* part,
-                                 cudaStream_t s);
+                                 cudaStream_t s, int shared = 0,
+                                 bool own = false);
 // shared_attn_tc.cu: the tensor-core kernels of a shared prefix, for what
 // paged_attn_tc_takes.
 size_t shared_attn_tc_ws(long long B, long long Q, int Hq, int Hkv, int D);

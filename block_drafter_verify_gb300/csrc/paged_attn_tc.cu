@@ -150,14 +150,18 @@ static_assert(sizeof(Meta) <= 7 * 1024, "");
 // ---- the numbering of the tiles -------------------------------------------
 struct Shape {
   int N, row_tiles, rows, g;  // rows = Q * g
+  // pages that all sequences have in common; tokens, and their pages, that are
+  // left out at the start of every sequence (dflash_shared_attn)
+  int common, first, first_page;
 };
 struct Lens {
   int n, nq;
 };
-__device__ __forceinline__ Lens lens_of(const PagedAttnArgs& a, int b,
-                                        bool* bad) {
+__device__ __forceinline__ Lens lens_of(const PagedAttnArgs& a,
+                                        const Shape& s, int b, bool* bad) {
   Lens l;
-  l.n = attn_clamp(a.kv_len[b], (long long)a.max_pages * a.page, bad);
+  l.n = max(0, attn_clamp(a.kv_len[b], (long long)a.max_pages * a.page, bad) -
+                   s.first);
   l.nq = attn_clamp(a.q_len ? a.q_len[b] : a.Q, a.Q, bad);
   return l;
 }
@@ -217,7 +221,7 @@ __device__ void walk_start(const PagedAttnArgs& a, const Shape& s, int cta,
   const int b0 = min(a.B, lane * per), b1 = min(a.B, b0 + per);
   int work = 0;
   for (int b = b0; b < b1; ++b)
-    work += a.Hkv * head_work(a, s, lens_of(a, b, bad));
+    work += a.Hkv * head_work(a, s, lens_of(a, s, b, bad));
   int run = work;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -237,13 +241,13 @@ __device__ void walk_start(const PagedAttnArgs& a, const Shape& s, int cta,
   int o = p0 - (run - work), h = 1;
   if (mine) {
     for (w.b = b0; w.b < b1; ++w.b) {
-      h = head_work(a, s, lens_of(a, w.b, bad));
+      h = head_work(a, s, lens_of(a, s, w.b, bad));
       if (o < a.Hkv * h) break;
       o -= a.Hkv * h;
     }
     w.hk = o / h;
     o -= w.hk * h;
-    const Lens l = lens_of(a, w.b, bad);
+    const Lens l = lens_of(a, s, w.b, bad);
     for (;; ++w.rt) {
       const int t = kUnitCost + tiles_of(a, s, l, w.rt);
       if (o < t) break;
@@ -264,7 +268,7 @@ __device__ __forceinline__ Cut cut_at(const PagedAttnArgs& a, const Shape& s,
   bool bad = false;
   const int before = run_start(w.total, cta, w.G) - w.at;  // first position
   const int head = before + kUnitCost;                     // its first tile's
-  const int end = head + tiles_of(a, s, lens_of(a, w.b, &bad), w.rt);
+  const int end = head + tiles_of(a, s, lens_of(a, s, w.b, &bad), w.rt);
   const int c0 = (int)(((head + 1ll) * w.G - 1) / w.total);
   if (c0 != cta - 1) return c;
   const int c1 = (int)(((long long)end * w.G - 1) / w.total);
@@ -282,7 +286,7 @@ __device__ bool walk_next(const PagedAttnArgs& a, const Shape& s, Walk& w,
                           Part& p) {
   bool bad = false;
   while (w.left > 0) {
-    p.l = lens_of(a, w.b, &bad);
+    p.l = lens_of(a, s, w.b, &bad);
     const int t = tiles_of(a, s, p.l, w.rt);
     const int work = kUnitCost + t;
     const int end = min(work, w.at + w.left);
@@ -545,7 +549,9 @@ __device__ __forceinline__ void split(float e0, float e1, float e2, float e3,
   }
 }
 
-template <int N>
+// kPart: out and lse get {sums of weights times values} and {reference, sum of
+// weights} of every row, in fp32.
+template <int N, bool kPart>
 __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
     paged_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k,
                          const __grid_constant__ CUtensorMap map_v,
@@ -625,7 +631,8 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
       auto load_id = [&](int first) {
         const int pg = first + lane;
         return pg < pages && pg < p.t1 * pt
-                   ? a.table[(size_t)p.b * a.max_pages + pg]
+                   ? a.table[(size_t)(pg < shape.common ? 0 : p.b) *
+                                 a.max_pages + shape.first_page + pg]
                    : -1;
       };
       int id = load_id(at), id1 = load_id(at + 32), id2 = load_id(at + 64);
@@ -1259,7 +1266,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
             min(max((int)(__float_as_uint(sum) >> 23) - 127, -100), 120);
         const float frac = sum * __uint_as_float((127 - ex) << 23);
         const float ref = (float)ex - m.neg_ref[r] - kSumRef;
-        if (whole) {
+        if (whole && !kPart) {
           const bool on = seen && g.on[r];
           m.fac[r] = on ? exp2f(kSumRef) / sum : 0.f;
           if (!dry && g.out_row[r] >= 0 && a.lse)
@@ -1269,8 +1276,13 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
           m.fac[r] = __uint_as_float((127 + (int)kSumRef - ex) << 23);
           float2* ml = reinterpret_cast<float2*>(
               part + (size_t)2 * gridDim.x * N * 128);
-          ml[(size_t)g.slot * N + r] =
-              make_float2(seen ? ref : -INFINITY, seen ? frac : 0.f);
+          long long at = (long long)g.slot * N + r;
+          if (kPart && whole) {
+            ml = reinterpret_cast<float2*>(a.lse);
+            at = dry ? -1 : g.out_row[r];
+          }
+          if (!kPart || at >= 0)
+            ml[at] = make_float2(seen ? ref : -INFINITY, seen ? frac : 0.f);
         }
       }
       half_sync(bar);
@@ -1297,9 +1309,13 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
           v *= f;
           if (whole) {
             const int at = dry ? -1 : g.out_row[row];
-            if (at >= 0 && d < a.D)
-              static_cast<__nv_bfloat16*>(a.out)[(size_t)at * a.D + d] =
-                  __float2bfloat16_rn(f == 0.f ? 0.f : v);
+            if (at >= 0 && d < a.D) {
+              if constexpr (kPart)
+                static_cast<float*>(a.out)[(size_t)at * a.D + d] = v;
+              else
+                static_cast<__nv_bfloat16*>(a.out)[(size_t)at * a.D + d] =
+                    __float2bfloat16_rn(f == 0.f ? 0.f : v);
+            }
           } else {
             part[((size_t)g.slot * N + row) * 128 + d] = v;
           }
@@ -1323,6 +1339,7 @@ __global__ void __launch_bounds__(Plan<N>::kThreads, 1)
 // 30 for a prompt of 8192 tokens and 64 heads.)
 constexpr int kJoinRows = 8;
 constexpr int kJoinThreads = 32 * kJoinRows;
+template <bool kPart>
 __global__ void __launch_bounds__(kJoinThreads)
     paged_attn_tc_join_kernel(const __grid_constant__ PagedAttnArgs a,
                               const Shape shape, int grid,
@@ -1361,9 +1378,12 @@ __global__ void __launch_bounds__(kJoinThreads)
       ((size_t)b * a.Q + qi) * a.Hq + hk * shape.g + row % shape.g;
   bool bad = false;
   const bool on =
-      (sum > 0.f || sum != sum) && qi < lens_of(a, b, &bad).nq;
-  const float inv = on ? 1.f / sum : 0.f;
-  if (lane == 0 && a.lse)
+      (sum > 0.f || sum != sum) && qi < lens_of(a, shape, b, &bad).nq;
+  const float inv = kPart ? 1.f : on ? 1.f / sum : 0.f;
+  if (kPart && lane == 0)
+    reinterpret_cast<float2*>(a.lse)[at] =
+        make_float2(on ? top : -INFINITY, on ? sum : 0.f);
+  if (!kPart && lane == 0 && a.lse)
     a.lse[at] = on ? (log2f(sum) + top) * 0.6931471805599453f : -INFINITY;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -1376,7 +1396,10 @@ __global__ void __launch_bounds__(kJoinThreads)
     o.z = fmaf(w, v.z, o.z);
     o.w = fmaf(w, v.w, o.w);
   }
-  if (4 * lane < a.D) {
+  if (kPart && 4 * lane < a.D) {
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at * a.D +
+                               4 * lane) = o;
+  } else if (4 * lane < a.D) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv);
     const __nv_bfloat162 y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
     uint2 v;
@@ -1395,14 +1418,15 @@ Shape shape_of(long long Q, int Hq, int Hkv) {
   const int per = (s.rows + s.row_tiles - 1) / s.row_tiles;
   s.N = (per + 15) / 16 * 16;
   s.row_tiles = (s.rows + s.N - 1) / s.N;
+  s.common = s.first = s.first_page = 0;
   return s;
 }
 
-template <int N>
+template <int N, bool kPart = false>
 cudaError_t launch_n(const CUtensorMap& mk, const CUtensorMap& mv,
                      const PagedAttnArgs& a, const Shape& s, int G,
                      float* part, cudaStream_t stream) {
-  auto* f = paged_attn_tc_kernel<N>;
+  auto* f = paged_attn_tc_kernel<N, kPart>;
   cudaError_t e = cudaFuncSetAttribute(
       f, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<N>::kBytes);
   if (e != cudaSuccess) return e;
@@ -1422,9 +1446,21 @@ size_t paged_attn_tc_ws(int B, int Q, int Hq, int Hkv) {
   return part_words(kMaxCtas, s.N) * sizeof(float) + kMaxCtas * sizeof(Cut);
 }
 
+PagedTcUnits paged_attn_tc_units(long long Q, int Hq, int Hkv) {
+  const Shape s = shape_of(Q, Hq, Hkv);
+  return PagedTcUnits{s.N, s.row_tiles};
+}
+
 cudaError_t launch_paged_attn_tc(const PagedAttnArgs& a, int sms, float* part,
-                                 cudaStream_t stream) {
-  const Shape s = shape_of(a.Q, a.Hq, a.Hkv);
+                                 cudaStream_t stream, int shared, bool own) {
+  Shape s = shape_of(a.Q, a.Hq, a.Hkv);
+  if (own) {
+    if (s.N > kPagedTcOwnRows) return cudaErrorInvalidValue;
+    s.first = shared;
+    s.first_page = shared / a.page;
+  } else {
+    s.common = shared / a.page;
+  }
   const long long most =
       (long long)a.B * a.Hkv * s.row_tiles *
       (((long long)a.max_pages * a.page + kTile - 1) / kTile + kUnitCost);
@@ -1436,21 +1472,28 @@ cudaError_t launch_paged_attn_tc(const PagedAttnArgs& a, int sms, float* part,
       !make_tmap_u8_2d(&mv, a.v_codes, a.D, rows, 128, a.page))
     return cudaErrorInvalidValue;
   cudaError_t e;
-  switch (s.N) {
-    case 16: e = launch_n<16>(mk, mv, a, s, G, part, stream); break;
-    case 32: e = launch_n<32>(mk, mv, a, s, G, part, stream); break;
-    case 48: e = launch_n<48>(mk, mv, a, s, G, part, stream); break;
-    case 64: e = launch_n<64>(mk, mv, a, s, G, part, stream); break;
-    case 80: e = launch_n<80>(mk, mv, a, s, G, part, stream); break;
-    default: e = launch_n<96>(mk, mv, a, s, G, part, stream); break;
-  }
+  static_assert(kPagedTcOwnRows == 32, "");
+  if (own)
+    e = s.N == 16 ? launch_n<16, true>(mk, mv, a, s, G, part, stream)
+                  : launch_n<32, true>(mk, mv, a, s, G, part, stream);
+  else
+    switch (s.N) {
+      case 16: e = launch_n<16>(mk, mv, a, s, G, part, stream); break;
+      case 32: e = launch_n<32>(mk, mv, a, s, G, part, stream); break;
+      case 48: e = launch_n<48>(mk, mv, a, s, G, part, stream); break;
+      case 64: e = launch_n<64>(mk, mv, a, s, G, part, stream); break;
+      case 80: e = launch_n<80>(mk, mv, a, s, G, part, stream); break;
+      default: e = launch_n<96>(mk, mv, a, s, G, part, stream); break;
+    }
   if (e != cudaSuccess) return e;
   if (G < 2) return e;
   const int rows_of = std::min(s.N, s.rows);
   PdlLaunch J(dim3(G - 1, (rows_of + kJoinRows - 1) / kJoinRows),
               dim3(kJoinThreads), 0, stream);
-  return cudaLaunchKernelEx(&J.cfg, paged_attn_tc_join_kernel, a, s, G,
-                            (const float*)part);
+  return cudaLaunchKernelEx(&J.cfg,
+                            own ? paged_attn_tc_join_kernel<true>
+                                : paged_attn_tc_join_kernel<false>,
+                            a, s, G, (const float*)part);
 }
 
 }  // namespace dflash

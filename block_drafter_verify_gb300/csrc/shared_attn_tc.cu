@@ -1115,8 +1115,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     const int u = r_all / kRows, v = r_own / kRows;
     if (s.tiles > 0)
       add(-1, u, cost_of(s.all, u), r_all % kRows, parts.by_row + row);
-    if (tiles_of(a, s, l, v) > 0)
+    if (s.own_units == 0) {                   // another launch's, by row
+      if (lane == 0) s_at[warp][n] = (int)(parts.by_row + rows + row);
+      ++n;
+    } else if (tiles_of(a, s, l, v) > 0) {
       add(b, v, cost_of(s.own, v), r_own % kRows, parts.by_row + rows + row);
+    }
   }
   __syncwarp();
   float top = -INFINITY;
@@ -1179,19 +1183,38 @@ Shape shape_of(const PagedAttnArgs& a, int shared) {
   return s;
 }
 
-}  // namespace
-
-size_t shared_attn_tc_ws(long long B, long long Q, int Hq, int Hkv, int D) {
+// What the parts and tables take.
+size_t tc_ws(long long B, long long Q, int Hq, int Hkv, int D) {
   const size_t n = (size_t)2 * kMaxCtas * kRows + 2 * (size_t)(B * Q * Hq);
   const long long own = Q * (Hq / Hkv);
   const size_t units = Hkv * ((B * own + kRows - 1) / kRows +
                               B * ((own + kRows - 1) / kRows));
-  return n * (D * sizeof(float) + sizeof(float2)) + 32 + units * sizeof(Begun);
+  const size_t need =
+      n * (D * sizeof(float) + sizeof(float2)) + 32 + units * sizeof(Begun);
+  return (need + 255) & ~(size_t)255;
+}
+
+}  // namespace
+
+size_t shared_attn_tc_ws(long long B, long long Q, int Hq, int Hkv, int D) {
+  return tc_ws(B, Q, Hq, Hkv, D) + paged_attn_tc_ws((int)B, (int)Q, Hq, Hkv);
 }
 
 cudaError_t launch_shared_attn_tc(const PagedAttnArgs& a, int shared, int sms,
                                   void* ws, cudaStream_t stream) {
-  const Shape s = shape_of(a, shared);
+  // Few tiles of shared tokens are read for each sequence again by the kernel
+  // whose cost follows the rows.  Each costs it 0.7 us with 16 rows and 1.1 with
+  // 48, and a call 8 us less: up to 28 tiles of 16 rows a CTA.  (32 query and 8
+  // key heads: 4 sequences, 2148 tokens 14.7 against 22.9 us; 2 and 4 sequences,
+  // 16884 tokens, 13 and 27 tiles a CTA 21.7 and 31.0 against 32.4 and 35.1, 8
+  // sequences 51.1 against 38.1; 16 sequences with 9 queries, 2148 tokens, 13
+  // tiles of 48 rows 35.8 against 36.9.)
+  Shape s = shape_of(a, shared);
+  const PagedTcUnits units = paged_attn_tc_units(a.Q, a.Hq, a.Hkv);
+  const long long n_units = (long long)a.B * a.Hkv * units.row_tiles;
+  if (n_units * s.tiles * units.N <= 448ll * sms)
+    return launch_paged_attn_tc(a, sms, static_cast<float*>(ws), stream,
+                                shared);
   const long long own_tiles =
       ((long long)a.max_pages * a.page - shared + kTile - 1) / kTile;
   const long long most =
@@ -1201,6 +1224,15 @@ cudaError_t launch_shared_attn_tc(const PagedAttnArgs& a, int shared, int sms,
   // (and the parts' numbers stay within 32 bits)
   if (most > 0x7fffffffll || 2 * rows + 2 * kMaxCtas * kRows > 0x7fffffffll)
     return cudaErrorNotSupported;
+  // Own tokens of few rows fill a tile of 128 rows badly: where there are many
+  // such units that kernel takes them, in a launch (and a join) more.  (64
+  // sequences, 32 query heads: 16384 shared and 500 to 1000 own tokens 96.6
+  // against 99.2 us, 64 heads and 1000 to 2000 own ones 129 against 150; 256
+  // sequences, 1024 and 50 to 100 tokens 91 against 147.  16 sequences, 16384
+  // and 250 to 500 tokens: 50.0 against 42.8.)
+  const bool apart =
+      units.N <= kPagedTcOwnRows && n_units >= 2 * sms;
+  if (apart) s.own_units = 0;
   const int G = std::min(sms, kMaxCtas);
   CUtensorMap mk, mv;
   const uint64_t pool = (uint64_t)a.num_pages * a.Hkv * a.page;
@@ -1214,6 +1246,18 @@ cudaError_t launch_shared_attn_tc(const PagedAttnArgs& a, int shared, int sms,
   PdlLaunch L(dim3(G), dim3(kThreads), kSmem, stream);
   e = cudaLaunchKernelEx(&L.cfg, shared_attn_tc_kernel, mk, mv, a, s, ws);
   if (e != cudaSuccess) return e;
+  if (apart) {
+    const Parts parts = parts_of(ws, rows, a.D);
+    PagedAttnArgs own = a;
+    own.out = parts.o + (parts.by_row + rows) * a.D;
+    own.lse = reinterpret_cast<float*>(parts.ml + parts.by_row + rows);
+    e = launch_paged_attn_tc(
+        own, sms,
+        reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
+                                 tc_ws(a.B, a.Q, a.Hq, a.Hkv, a.D)),
+        stream, shared, true);
+    if (e != cudaSuccess) return e;
+  }
   PdlLaunch J(dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)),
               dim3(32 * kJoinWarps), 0, stream);
   return cudaLaunchKernelEx(&J.cfg, shared_attn_tc_join_kernel, a, s, ws);
