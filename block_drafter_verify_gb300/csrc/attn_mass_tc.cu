@@ -50,12 +50,13 @@ struct Segment {
   int lone;                      // all rows: sums are complete at once
   int n, nq;
 };
-struct Row {
-  float rel, nl;                 // undoes the scaling; -logsumexp in bits
+// Two rows: what undoes their scaling, and -logsumexp in bits.
+struct alignas(16) Rows {
+  float rel[2], nl[2];
 };
 struct Meta {
   Segment seg[kSegs];
-  alignas(16) Row row[2][kRows];
+  Rows row[2][kRows / 2];
   int lim[2][kRows];             // tokens a row sees
   float ks[kStages][8];          // factors of a tile's pages
   float keep[kKeep][kTile];
@@ -459,7 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         copy16(tc::smem_u32(raw(r) + 16), src + 16, read);
         if (ch == 0) {
           const float lse = r < g.rows ? a.lse[out] : -INFINITY;
-          m.row[rq.at][r].nl = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+          m.row[rq.at][r >> 1].nl[r & 1] =
+              lse == -INFINITY ? -INFINITY : -lse * kLog2e;
           m.lim[rq.at][r] =
               a.causal ? g.n - g.nq + (g.row0 + r) / shape.g + 1 : g.n;
         }
@@ -513,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<uint4*>(dst + np * 128) =
             make_uint4(lo[0], lo[1], lo[2], lo[3]);
         if (ch == 0)
-          m.row[rq.at][r].rel = __uint_as_float((120 + e) << 23);
+          m.row[rq.at][r >> 1].rel[r & 1] = __uint_as_float((120 + e) << 23);
       }
       fence_async();
       __syncwarp();
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       const int np = (g.rows + 7) / 8 * 8;
-      const Row* rows = m.row[rq.at];
+      const Rows* rows = m.row[rq.at];
       const int* lims = m.lim[rq.at];
       ok = wait_for(&m.q_full[rq.at], rq.phase, abort, a.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
@@ -564,24 +566,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int at = g.tok0 + t * kTile + tok;
         // some row does not see all of the tile
         const bool masked = lims[0] < g.tok0 + (t + 1) * kTile;
-        float sum = 0.f;
+        const uint64_t ct2 = pack2(ct, ct);
+        const uint64_t rest2 = pack2(1.f / 32, 1.f / 32);
+        uint64_t sum2[2] = {0, 0};
+        // eight rows from c on, by pairs
+        auto take = [&](int c, const float* hi, const float* lo) {
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            const ulonglong2 r =
+                *reinterpret_cast<const ulonglong2*>(&rows[(c + j) >> 1]);
+            const uint64_t s2 = mul2(
+                fma2(pack2(lo[j], lo[j + 1]), rest2, pack2(hi[j], hi[j + 1])),
+                ct2);
+            float x0, x1;
+            unpack2(fma2(s2, r.x, r.y), x0, x1);
+            if (masked) {
+              if (at >= lims[c + j]) x0 = -INFINITY;
+              if (at >= lims[c + j + 1]) x1 = -INFINITY;
+            }
+            sum2[j >> 1 & 1] =
+                add2(sum2[j >> 1 & 1],
+                     pack2(tc::ex2_approx(x0), tc::ex2_approx(x1)));
+          }
+        };
+        int c = 0;
 #pragma unroll 1
-        for (int c = 0; c < np; c += 8) {
+        for (; c + 16 <= np; c += 16) {
+          float hi[16], lo[16];
+          tmem_ld_x16(s_col + c, hi);
+          tmem_ld_x16(s_col + np + c, lo);
+          tmem_loaded(hi);
+          tmem_loaded(lo);
+          take(c, hi, lo);
+          take(c + 8, hi + 8, lo + 8);
+        }
+        if (c < np) {
           float hi[8], lo[8];
           tmem_ld_x8(s_col + c, hi);
           tmem_ld_x8(s_col + np + c, lo);
           tmem_loaded(hi);
           tmem_loaded(lo);
-          float part[2] = {0.f, 0.f};
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const Row r = rows[c + j];
-            float x = fmaf(fmaf(lo[j], 1.f / 32, hi[j]) * ct, r.rel, r.nl);
-            if (masked && at >= lims[c + j]) x = -INFINITY;
-            part[j & 1] += tc::ex2_approx(x);
-          }
-          sum += part[0] + part[1];
+          take(c, hi, lo);
         }
+        float sum, sum_odd;
+        unpack2(add2(sum2[0], sum2[1]), sum, sum_odd);
+        sum += sum_odd;
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) {
