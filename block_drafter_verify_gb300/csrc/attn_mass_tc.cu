@@ -31,12 +31,13 @@ namespace {
 
 constexpr int kTile = 128;       // tokens of a tile
 constexpr int kRows = 128;       // rows of a segment
-constexpr int kThreads = 512;
+constexpr int kGroups = 4;       // of warps that take weights
+constexpr int kThreads = 256 + 128 * kGroups;
 constexpr int kStages = 8;       // tiles in shared memory
 constexpr int kTileBytes = kTile * 128;
 constexpr int kQBytes = 2 * kRows * 128;  // two parts
 constexpr int kSegs = 4;
-constexpr int kKeep = 48;        // tiles whose sums are kept (an even number)
+constexpr int kKeep = 48;        // tiles whose sums are kept (a multiple of 4)
 constexpr int kUnitCost = 2;     // of a pair besides its tiles, in tiles
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -61,7 +62,7 @@ struct Meta {
   float ks[kStages][8];          // factors of a tile's pages
   float keep[kKeep][kTile];
   uint64_t k_full[kStages], k_empty[kStages];
-  uint64_t s_full[2], s_empty[2], q_full[2], q_empty[2];
+  uint64_t s_full[kGroups], s_empty[kGroups], q_full[2], q_empty[2];
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t drain;
   uint32_t tmem;
@@ -73,6 +74,7 @@ static_assert(kSmem <= 232448, "");
 
 struct Shape {
   int g, first;                  // heads of a key head; first tile's token
+  int groups;                    // that work, each with its columns of TMEM
 };
 struct Lens {
   int n, nq;
@@ -207,15 +209,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::mbar_init(&m.k_full[i], 1);
       tc::mbar_init(&m.k_empty[i], 1 + 4);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kGroups; ++i) {
       tc::mbar_init(&m.s_full[i], 2);
       tc::mbar_init(&m.s_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&m.q_full[i], 4);
-      tc::mbar_init(&m.q_empty[i], 1 + 8);
+      tc::mbar_init(&m.q_empty[i], 1 + 4 * shape.groups);
     }
     for (int i = 0; i < kSegs; ++i) {
       tc::mbar_init(&m.seg_full[i], 1);
-      tc::mbar_init(&m.seg_empty[i], 1 + 1 + 4 + 8);
+      tc::mbar_init(&m.seg_empty[i], 1 + 1 + 4 + 4 * shape.groups);
     }
     tc::mbar_init(&m.drain, 1);
     m.abort = 0;
@@ -333,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     Ring<kStages> rk;
     Ring<2> rq;
-    uint32_t par0 = 0, par1 = 0;             // of the score buffers
+    uint32_t pars = 0;                       // of the score buffers
     while (ok) {
       if (!next_segment()) break;
       const bool done = m.seg[rg.at].done;
@@ -347,13 +351,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(&m.q_full[rq.at], rq.phase)) break;
 #pragma unroll 1
       for (int t = 0; t < T && ok; ++t) {
-        const int buf = t & 1;
+        const int buf = t & (shape.groups - 1);
         // (a buffer's first use finds it empty)
-        if (!wait(&m.s_empty[buf], (buf ? par1 : par0) ^ 1)) break;
-        if (buf) par1 ^= 1; else par0 ^= 1;
+        if (!wait(&m.s_empty[buf], (pars >> buf & 1) ^ 1)) break;
+        pars ^= 1u << buf;
         if (!wait(&m.k_full[rk.at], rk.phase)) break;
         tc::fence_after_sync();
-        const uint32_t d = uniform(tm + buf * 256);
+        const uint32_t d = uniform(tm + buf * (512 / shape.groups));
         const uint64_t dk =
             tc::sdesc_k_sw128(uniform(sk_u + rk.at * kTileBytes));
         if (elect_one()) {
@@ -522,12 +526,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) tc::mbar_arrive(&m.q_full[rq.at]);
       rq.next();
     }
-  } else if (warp >= 8) {
+  } else if (warp >= 8 && warp < 8 + 4 * shape.groups) {
     // -------------------------------------------------------------- weights
-    const int half = (warp - 8) >> 2, quarter = warp & 3;
+    const int group = (warp - 8) >> 2, quarter = warp & 3;
     const int tok = quarter * 32 + lane;
     const uint32_t s_col =
-        tmem + ((uint32_t)(quarter * 32) << 16) + half * 256;
+        tmem + ((uint32_t)(quarter * 32) << 16) + group * (512 / shape.groups);
     const int page_bits = __ffs(a.page) - 1;
     Ring<2> rq;
     int tile = 0;                            // copied before the segment's
@@ -543,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (at >= a.first && at < g.n) mass_store(a, g.b, g.hk, at, sum);
       };
       if (g.rows == 0) {                     // the sums are complete
-        for (int t = half; t < g.T; t += 2) {
+        for (int t = group; t < g.T; t += shape.groups) {
           store(t, m.keep[t][tok]);
           m.keep[t][tok] = 0.f;
         }
@@ -556,8 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
 #pragma unroll 1
-      for (int t = half; t < g.T; t += 2) {
-        ok = wait_for(&m.s_full[half], s_par, abort, a.wait_ns);
+      for (int t = group; t < g.T; t += shape.groups) {
+        ok = wait_for(&m.s_full[group], s_par, abort, a.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         s_par ^= 1;
@@ -614,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) {
-          tc::mbar_arrive(&m.s_empty[half]);
+          tc::mbar_arrive(&m.s_empty[group]);
           tc::mbar_arrive(&m.k_empty[(tile + t) % kStages]);  // (the factors)
         }
         if (g.lone)
@@ -644,6 +648,8 @@ cudaError_t launch_attn_mass_tc(const AttnMassArgs& a, int sms,
   s.g = a.Hq / a.Hkv;
   s.first = a.first / kTile * kTile;
   const long long tiles = (mass_most(a) - s.first + kTile - 1) / kTile;
+  // Two parts of a tile's rows in 128 columns: four groups, else two.
+  s.groups = (long long)a.Q * s.g <= 64 ? 4 : 2;
   const long long passes = ((long long)a.Q * s.g + kRows - 1) / kRows;
   if ((long long)a.B * a.Hkv * (kUnitCost + tiles * passes) > 0x7fffffffll)
     return cudaErrorNotSupported;
