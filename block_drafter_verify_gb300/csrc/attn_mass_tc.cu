@@ -15,8 +15,9 @@
 // meanwhile: one thread owns a token throughout, nothing is added atomically.
 //
 // Warps: 0 copies tiles (TMA, one box per page), 1 issues the MMAs, 2 hands out
-// the segments, 4-7 lay out q (two buffers), 8-15 take the tiles' weights (a group
-// of four to every other tile).  Every wait is bounded; on a timeout the CTA stops
+// the segments, 4-7 lay out q (two buffers), the others take the tiles' weights:
+// groups of four a tile each by turns, four groups with up to 64 rows (whose
+// scores are 128 columns), else two.  Every wait is bounded; on a timeout the CTA stops
 // issuing, drains, frees TMEM and flags the error word.
 #include <cuda_fp8.h>
 
@@ -30,19 +31,14 @@ namespace dflash {
 namespace {
 
 constexpr int kTile = 128;       // tokens of a tile
-constexpr int kRows = 128;       // rows of a segment
-constexpr int kGroups = 4;       // of warps that take weights
-constexpr int kThreads = 256 + 128 * kGroups;
-constexpr int kStages = 8;       // tiles in shared memory
 constexpr int kTileBytes = kTile * 128;
-constexpr int kQBytes = 2 * kRows * 128;  // two parts
+constexpr int kMaxRows = 128;    // of a segment
 constexpr int kSegs = 4;
-constexpr int kKeep = 48;        // tiles whose sums are kept (a multiple of 4)
 constexpr int kUnitCost = 2;     // of a pair besides its tiles, in tiles
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Tiles of one pair with (up to) 128 of its rows; without rows: the sums of
-// those tiles are complete.
+// Tiles of one pair with (up to 64 or 128) of its rows; without rows: the sums
+// of those tiles are complete.
 struct Segment {
   int done;
   int b, hk;
@@ -55,26 +51,40 @@ struct Segment {
 struct alignas(16) Rows {
   float rel[2], nl[2];
 };
-struct Meta {
-  Segment seg[kSegs];
-  Rows row[2][kRows / 2];
-  int lim[2][kRows];             // tokens a row sees
-  float ks[kStages][8];          // factors of a tile's pages
-  float keep[kKeep][kTile];
-  uint64_t k_full[kStages], k_empty[kStages];
-  uint64_t s_full[kGroups], s_empty[kGroups], q_full[2], q_empty[2];
-  uint64_t seg_full[kSegs], seg_empty[kSegs];
-  uint64_t drain;
-  uint32_t tmem;
-  int abort;
+// For segments of up to 64 rows, whose scores leave TMEM room for four tiles, or
+// of up to 128.
+template <int kRows_>
+struct Plan {
+  static constexpr int kRows = kRows_;
+  static constexpr int kGroups = kRows == 64 ? 4 : 2;  // that take weights
+  static constexpr int kThreads = 256 + 128 * kGroups;
+  static constexpr int kColumns = 512 / kGroups;
+  static constexpr int kStages = kRows == 64 ? 11 : 8;  // tiles in shared memory
+  // tiles whose sums are kept (a multiple of kGroups); 64 are all rows
+  static constexpr int kKeep = kRows == 64 ? 8 : 48;
+  static constexpr int kQBytes = 2 * kRows * 128;       // two parts
+
+  struct Meta {
+    Segment seg[kSegs];
+    Rows row[2][kRows / 2];
+    int lim[2][kRows];             // tokens a row sees
+    float ks[kStages][8];          // factors of a tile's pages
+    float keep[kKeep][kTile];
+    uint64_t k_full[kStages], k_empty[kStages];
+    uint64_t s_full[kGroups], s_empty[kGroups], q_full[2], q_empty[2];
+    uint64_t seg_full[kSegs], seg_empty[kSegs];
+    uint64_t drain;
+    uint32_t tmem;
+    int abort;
+  };
+  static constexpr int kSmem = 2 * kQBytes + kStages * kTileBytes +
+                               ((int)sizeof(Meta) + 15) / 16 * 16;
+  static_assert(kSmem <= 232448, "");
 };
-constexpr int kSmem = 2 * kQBytes + kStages * kTileBytes +
-                      ((int)sizeof(Meta) + 15) / 16 * 16;
-static_assert(kSmem <= 232448, "");
 
 struct Shape {
   int g, first;                  // heads of a key head; first tile's token
-  int groups;                    // that work, each with its columns of TMEM
+  int rows;                      // most of a segment
 };
 struct Lens {
   int n, nq;
@@ -91,7 +101,7 @@ __device__ __forceinline__ int tiles_of(const Shape& s, const Lens& l) {
 }
 // Of a tile: the times it is gone through.
 __device__ __forceinline__ int cost_of(const Shape& s, const Lens& l) {
-  return max(1, (l.nq * s.g + kRows - 1) / kRows);
+  return max(1, (l.nq * s.g + s.rows - 1) / s.rows);
 }
 __device__ __noinline__ int work_of(const AttnMassArgs& a, const Shape& s,
                                     const Lens& l) {
@@ -193,10 +203,16 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src,
                : "memory");
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+template <int kRows>
+__global__ void __launch_bounds__(Plan<kRows>::kThreads, 1)
     attn_mass_tc_kernel(const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ AttnMassArgs a,
                         const Shape shape) {
+  using PL = Plan<kRows>;
+  using Meta = typename PL::Meta;
+  constexpr int kThreads = PL::kThreads, kStages = PL::kStages;
+  constexpr int kGroups = PL::kGroups, kQBytes = PL::kQBytes;
+  constexpr int kKeep = PL::kKeep;
   extern __shared__ __align__(1024) uint8_t base[];
   uint8_t* sq = base;                        // [2 buffers][2 parts][rows][128]
   uint8_t* sk = sq + 2 * kQBytes;            // [kStages][128][128]
@@ -215,11 +231,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&m.q_full[i], 4);
-      tc::mbar_init(&m.q_empty[i], 1 + 4 * shape.groups);
+      tc::mbar_init(&m.q_empty[i], 1 + 4 * kGroups);
     }
     for (int i = 0; i < kSegs; ++i) {
       tc::mbar_init(&m.seg_full[i], 1);
-      tc::mbar_init(&m.seg_empty[i], 1 + 1 + 4 + 4 * shape.groups);
+      tc::mbar_init(&m.seg_empty[i], 1 + 1 + 4 + 4 * kGroups);
     }
     tc::mbar_init(&m.drain, 1);
     m.abort = 0;
@@ -351,13 +367,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(&m.q_full[rq.at], rq.phase)) break;
 #pragma unroll 1
       for (int t = 0; t < T && ok; ++t) {
-        const int buf = t & (shape.groups - 1);
+        const int buf = t & (kGroups - 1);
         // (a buffer's first use finds it empty)
         if (!wait(&m.s_empty[buf], (pars >> buf & 1) ^ 1)) break;
         pars ^= 1u << buf;
         if (!wait(&m.k_full[rk.at], rk.phase)) break;
         tc::fence_after_sync();
-        const uint32_t d = uniform(tm + buf * (512 / shape.groups));
+        const uint32_t d = uniform(tm + buf * PL::kColumns);
         const uint64_t dk =
             tc::sdesc_k_sw128(uniform(sk_u + rk.at * kTileBytes));
         if (elect_one()) {
@@ -526,12 +542,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) tc::mbar_arrive(&m.q_full[rq.at]);
       rq.next();
     }
-  } else if (warp >= 8 && warp < 8 + 4 * shape.groups) {
+  } else if (warp >= 8) {
     // -------------------------------------------------------------- weights
     const int group = (warp - 8) >> 2, quarter = warp & 3;
     const int tok = quarter * 32 + lane;
     const uint32_t s_col =
-        tmem + ((uint32_t)(quarter * 32) << 16) + group * (512 / shape.groups);
+        tmem + ((uint32_t)(quarter * 32) << 16) + group * PL::kColumns;
     const int page_bits = __ffs(a.page) - 1;
     Ring<2> rq;
     int tile = 0;                            // copied before the segment's
@@ -547,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (at >= a.first && at < g.n) mass_store(a, g.b, g.hk, at, sum);
       };
       if (g.rows == 0) {                     // the sums are complete
-        for (int t = group; t < g.T; t += shape.groups) {
+        for (int t = group; t < g.T; t += kGroups) {
           store(t, m.keep[t][tok]);
           m.keep[t][tok] = 0.f;
         }
@@ -560,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
 #pragma unroll 1
-      for (int t = group; t < g.T; t += shape.groups) {
+      for (int t = group; t < g.T; t += kGroups) {
         ok = wait_for(&m.s_full[group], s_par, abort, a.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -640,6 +656,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0 && m.abort) raise_error(a.err, kErrTimeout);
 }
 
+template <int kRows>
+cudaError_t launch(const CUtensorMap& mk, const AttnMassArgs& a, const Shape& s,
+                   int sms, cudaStream_t stream) {
+  using PL = Plan<kRows>;
+  auto* f = attn_mass_tc_kernel<kRows>;
+  cudaError_t e = cudaFuncSetAttribute(
+      f, cudaFuncAttributeMaxDynamicSharedMemorySize, PL::kSmem);
+  if (e != cudaSuccess) return e;
+  PdlLaunch L(dim3(sms), dim3(PL::kThreads), PL::kSmem, stream);
+  return cudaLaunchKernelEx(&L.cfg, f, mk, a, s);
+}
+
 }  // namespace
 
 cudaError_t launch_attn_mass_tc(const AttnMassArgs& a, int sms,
@@ -647,21 +675,19 @@ cudaError_t launch_attn_mass_tc(const AttnMassArgs& a, int sms,
   Shape s;
   s.g = a.Hq / a.Hkv;
   s.first = a.first / kTile * kTile;
+  const long long rows = (long long)a.Q * s.g;
+  // (72 rows of 32 sequences: 73 us in one pass of 128, 94 in two of 40)
+  s.rows = rows <= 64 ? 64 : kMaxRows;
   const long long tiles = (mass_most(a) - s.first + kTile - 1) / kTile;
-  // Two parts of a tile's rows in 128 columns: four groups, else two.
-  s.groups = (long long)a.Q * s.g <= 64 ? 4 : 2;
-  const long long passes = ((long long)a.Q * s.g + kRows - 1) / kRows;
+  const long long passes = (rows + s.rows - 1) / s.rows;
   if ((long long)a.B * a.Hkv * (kUnitCost + tiles * passes) > 0x7fffffffll)
     return cudaErrorNotSupported;
   CUtensorMap mk;
   const uint64_t pool = (uint64_t)a.num_pages * a.Hkv * a.page;
   if (!make_tmap_u8_2d(&mk, a.k_codes, a.D, pool, 128, a.page))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(
-      attn_mass_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  PdlLaunch L(dim3(sms), dim3(kThreads), kSmem, stream);
-  return cudaLaunchKernelEx(&L.cfg, attn_mass_tc_kernel, mk, a, s);
+  return s.rows == 64 ? launch<64>(mk, a, s, sms, stream)
+                      : launch<kMaxRows>(mk, a, s, sms, stream);
 }
 
 }  // namespace dflash
