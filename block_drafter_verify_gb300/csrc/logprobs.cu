@@ -12,9 +12,10 @@
 // above the next smaller number, words after it those above its logit.
 //
 // The K most likely: the K-th largest maximum of 64 groups of threads bounds
-// the K-th largest logit of the slice from below; only the threads that reach it
-// have their parts read again, from L2, a warp at a time for each, for the few more
-// than K candidates, which are ranked by counting.  A cluster of CTAs owns a row;
+// the K-th largest logit of the slice from below.  Of the threads that reach it
+// most do so with the words of their maximum alone, which they read again; the
+// others have their whole part read again, from L2, a warp at a time for each.  The
+// few more than K candidates are ranked by counting.  A cluster of CTAs owns a row;
 // the first of them joins the CTAs' sums and lists.  What overflows the list (ties
 // by the thousand) is found by K searches for the next largest instead.
 //
@@ -228,6 +229,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   Sums acc{-INFINITY, -INFINITY, 0.f, 0.f};
   int before = 0;
+  int best = 0;                      // the first word of those with the maximum
+  float others = -INFINITY;          // the largest of all other words
   const float below = next_below(mine);
   const uint64_t c2 = pack2(c, c);
   auto take = [&](const uint4 (&raw)[kAhead], int first, int n) {
@@ -253,8 +256,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
     }
+    if (kTop) others = fmaxf(others, fminf(top, acc.m));
     if (top > acc.m) {
       acc.m = top;
+      best = first;
       const float r = ceilf(top * c);
       if (r > acc.r) {
         const float h = acc.r - r;   // -inf at first, and before +inf
@@ -400,24 +405,32 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float bound = sh.bound;
     // (-inf: fewer than K groups hold any token; then every token above it is a
     // candidate)
-    uint32_t reach = __ballot_sync(
-        0xffffffffu, my_max >= bound && my_max > -INFINITY);
+    auto offer = [&](int i) {
+      float f[N];
+      Words<T>::get(fetch(i), f);
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (f[j] >= bound && f[j] > -INFINITY) {
+          const int to = atomicAdd(&sh.listed, 1);
+          if (to < kList)
+            sh.list[to] = word_of(f[j], (int)((long long)i * N + j - skew));
+        }
+    };
+    const bool reaches = my_max >= bound && my_max > -INFINITY;
+    const bool again = reaches && others >= bound;
+    if (reaches && !again) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (best + k * kThreads < w1) offer(best + k * kThreads);
+    }
+    uint32_t reach = __ballot_sync(0xffffffffu, again);
     while (reach) {                  // the whole warp reads one thread's part
       const int who = __ffs(reach) - 1;
       reach &= reach - 1;
 #pragma unroll 2
       for (int i = w0 + warp * 32 + who + lane * kThreads; i < w1;
-           i += 32 * kThreads) {
-        float f[N];
-        Words<T>::get(fetch(i), f);
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-          if (f[j] >= bound && f[j] > -INFINITY) {
-            const int to = atomicAdd(&sh.listed, 1);
-            if (to < kList)
-              sh.list[to] = word_of(f[j], (int)((long long)i * N + j - skew));
-          }
-      }
+           i += 32 * kThreads)
+        offer(i);
     }
     __syncthreads();
     int n = sh.listed;
