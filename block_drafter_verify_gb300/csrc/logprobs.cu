@@ -228,6 +228,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
 
   Sums acc{-INFINITY, -INFINITY, 0.f, 0.f};
+  // The given token's logit is a good first reference: none is too high that
+  // some logit has.  (It is often the largest, and no thread raises it then.)
+  if (given && fabsf(mine * c) < INFINITY) acc.r = ceilf(mine * c);
+  const int token_at =               // its word
+      given ? (int)(((long long)token + skew) / N) : -1;
   int before = 0;
   int best = 0;                      // the first word of those with the maximum
   float others = -INFINITY;          // the largest of all other words
@@ -256,16 +261,16 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
     }
-    if (kTop) others = fmaxf(others, fminf(top, acc.m));
-    if (top > acc.m) {
-      acc.m = top;
-      best = first;
+    if (kTop) {
+      others = fmaxf(others, fminf(top, acc.m));
+      best = top > acc.m ? first : best;
+    }
+    acc.m = fmaxf(acc.m, top);
+    if (top * c > acc.r) {
       const float r = ceilf(top * c);
-      if (r > acc.r) {
-        const float h = acc.r - r;   // -inf at first, and before +inf
-        if (h > -INFINITY) lower(h, acc.s, acc.u);
-        acc.r = r;
-      }
+      const float h = acc.r - r;     // -inf at first, and before +inf
+      if (h > -INFINITY) lower(h, acc.s, acc.u);
+      acc.r = r;
     }
     const float ref = acc.r == -INFINITY ? 0.f : -acc.r;
     const uint64_t ref2 = pack2(ref, ref);
@@ -305,14 +310,15 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         if (k >= n) break;
-        const long long at = ((long long)first + k * kThreads) * N - skew;
-        if (at < 0 || (at <= token && token < at + N) || mine == -INFINITY) {
+        const int word = first + k * kThreads;
+        if (word == token_at || mine == -INFINITY) {
+          const long long at = (long long)word * N - skew;
 #pragma unroll
           for (int j = 0; j < N; ++j)
             before += f[k][j] > mine ||
                       (f[k][j] == mine && at + j < token && at + j >= 0);
         } else {
-          const float than = at < token ? below : mine;
+          const float than = word < token_at ? below : mine;
 #pragma unroll
           for (int j = 0; j < N; ++j) before += f[k][j] > than;
         }
