@@ -491,6 +491,18 @@ __global__ void __launch_bounds__(
     }
     // all of the round's slots have been read
     if (C > 1) cluster.sync(); else __syncthreads();
+    // the next round's codes on their way to L2
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k)
+      if (from[k] >= 0 && ids[k] >= 0 && ids[k] < a.num_pages) {
+        const int u = t + k * kOfThreads;
+        const long long of =
+            (((long long)ids[k] * a.Hkv + h) * a.page +
+             (from[k] & (a.page - 1))) * a.D +
+            (u - (int)(u * by >> 16) * per_slot) * 16;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.codes[0] + of));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.codes[1] + of));
+      }
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
 #pragma unroll
