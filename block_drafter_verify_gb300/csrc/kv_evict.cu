@@ -489,8 +489,14 @@ __global__ void __launch_bounds__(
         top[kv] = max(top[kv], __shfl_xor_sync(0xffffffffu, top[kv], o));
       if (lane == 0) sh.exp[kv][warp] = top[kv];
     }
-    // all of the round's slots have been read
-    if (C > 1) cluster.sync(); else __syncthreads();
+    // All of the round's slots have been read: their codes are in `top`.  The
+    // cluster only waits, it hands nothing over (nothing that was written is read
+    // again), and needs no fence.
+    __syncthreads();
+    if (C > 1)
+      asm volatile(
+          "barrier.cluster.arrive.relaxed.aligned;\n\t"
+          "barrier.cluster.wait.aligned;" ::: "memory");
     // the next round's codes on their way to L2
 #pragma unroll
     for (int k = 0; k < kUnits; ++k)
