@@ -4,27 +4,28 @@
 // Mathematics.  Of a key head's n > budget slots the first `sink` and the last
 // `recent` stay, and of the others the budget - sink - recent of largest weight
 // (ties: the lower slot).  That is a cut in the order of 32-bit keys, found by
-// three histograms (11, 11 and 10 bits), and the first few of the slots that lie
-// on it.  The kept slots move to slots 0 .. budget - 1 in their order.  A page
-// that gets other tokens gets a scale of its own, the least power of two with
-// max |x| <= 448 s, as an append would give it: codes move exactly but for those
-// that become subnormal.
+// three histograms (11, 11 and 10 bits), and the first few of the slots that
+// lie on it.  The kept slots move to slots 0 .. budget - 1 in their order.  A
+// page that gets other tokens gets a scale of its own, the least power of two
+// with max |x| <= 448 s, as an append would give it: codes move exactly but for
+// those that become subnormal.
 //
-// One launch: a CTA for every sequence and key head, or a cluster of up to eight
-// where there are few.  It finds the cut (a thread holds the weights of 16 slots
-// in registers over the histograms), writes the list of kept slots, and moves their
-// codes, in place: slots only move down, so pages are taken in rounds, lower ones
-// first, of as many as the cluster's warps hold in registers.  A round's pages are
-// all read, the cluster meets, and they are written: what a later round reads lies
-// above.
+// One launch: a CTA for every sequence and key head, or a cluster of up to
+// eight where there are few.  It finds the cut (a thread holds the weights of
+// 16 slots in registers over the histograms), writes the list of kept slots,
+// and moves their codes, in place: slots only move down, so pages are taken in
+// rounds, lower ones first, of as many as the cluster's warps hold in
+// registers.  A round's pages are all read, the cluster meets, and they are
+// written: what a later round reads lies above.
 //
 // What bounds it: with few heads the chain of steps (three histograms, then the
 // loads of a round; kept slots and page ids are asked for a round ahead), with
 // many bytes.  Eight heads of 128: 2100 to 2048 tokens 20 us, 131072 to 100000
-// tokens 250 us; 32 such sequences of 6000 to 8000 tokens to 6000 at most 129 us
-// (59 us of bytes at the copy's rate), where a launch for the lists, one for the
-// codes and whole histograms took 193 us, and pages in any order, each waiting for
-// flags of those that read it, 170 us.
+// tokens 242 us; 32 such sequences of up to 8000 tokens to 6000 at most 120 us
+// (59 us of bytes at the copy's rate; half of the issue slots: some 170
+// instructions for 16 codes, most of them maxima and conversions), where a
+// launch for the lists, one for the codes and whole histograms took 193 us, and
+// pages in any order, each waiting for flags of those that read it, 170 us.
 #include <cooperative_groups.h>
 #include <cuda_fp8.h>
 
@@ -74,7 +75,8 @@ __device__ __forceinline__ int length_of(const EvictArgs& a, int b,
 }
 
 // Exponent of the least power of two s with x <= 448 s, x the value of an E4M3
-// code without its sign: 448 is 1.75 2^8, and a code's largest fraction is 1.875.
+// code without its sign: 448 is 1.75 2^8, and a code's largest fraction is
+// 1.875.
 __device__ __forceinline__ int scale_exponent(uint32_t code) {
   if (code < 8)                              // 0, or 1 to 7 times 2^-9
     return code == 0 ? -1000 : 31 - __clz((int)code) - 17;
@@ -90,8 +92,8 @@ __device__ __forceinline__ uint32_t largest(const uint4& w) {
   return max(m & 0xffffu, m >> 16);
 }
 // Four codes times 2^off, rounded to codes again.  In fp16, which has room for
-// what a code times 2^-11 to 2^7 needs; else in fp32.  (Below 2^-40 a code is 0,
-// above 2^17 all of them are: the scale is made for the largest.)
+// what a code times 2^-11 to 2^7 needs; else in fp32.  (Below 2^-40 a code is
+// 0, above 2^17 all of them are: the scale is made for the largest.)
 __device__ __forceinline__ uint32_t requant4(uint32_t w, int off) {
   uint32_t out = 0;
   if (off >= -11 && off <= 7) {
@@ -132,7 +134,8 @@ struct alignas(16) Shared {
   int exp[2][kWarps];
 };
 
-// kOf warps have a page, kUnits 16-byte units of its keys and of its values a lane.
+// kOf warps have a page, kUnits 16-byte units of its keys and of its values a
+// lane.
 template <int kThreads, int kOf, int kUnits>
 __global__ void __launch_bounds__(
     kThreads, kThreads == 512 ? 1 : kUnits == 4 ? 4 : 2)
@@ -221,9 +224,9 @@ __global__ void __launch_bounds__(
               atomicAdd(&sh.hist[(w >> shift) & ((1 << bits) - 1)], 1);
           }
       }
-      // The bin, counted from the largest, in which the left-th slot lies: first
-      // its group of 32, from the CTAs' sums of groups, then the bin.  (Whole
-      // histograms read from eight CTAs: 9000 cycles.)
+      // The bin, counted from the largest, in which the left-th slot lies:
+      // first its group of 32, from the CTAs' sums of groups, then the bin.
+      // (Whole histograms read from eight CTAs: 9000 cycles.)
       __syncthreads();
       {
         int n_own = 0;
@@ -407,7 +410,8 @@ __global__ void __launch_bounds__(
       be += te;
     }
   }
-  // ---- the codes -----------------------------------------------------------------
+  // ---- the codes
+  // -----------------------------------------------------------------
   if (C > 1) cluster.sync(); else __syncthreads();  // the list is there
   const int page_bits = __ffs(a.page) - 1;
   const int pages = (a.budget + a.page - 1) >> page_bits;
@@ -490,8 +494,8 @@ __global__ void __launch_bounds__(
       if (lane == 0) sh.exp[kv][warp] = top[kv];
     }
     // All of the round's slots have been read: their codes are in `top`.  The
-    // cluster only waits, it hands nothing over (nothing that was written is read
-    // again), and needs no fence.
+    // cluster only waits, it hands nothing over (nothing that was written is
+    // read again), and needs no fence.
     __syncthreads();
     if (C > 1)
       asm volatile(
@@ -637,8 +641,8 @@ dflash_status dflash_kv_evict(
   a.kept = kept ? kept : static_cast<int*>(ws);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // CTAs to a head: as many as make four small ones to an SM, half of the
-  // sequences being shorter than their budget, if there are slots for them; large
-  // ones where the heads leave most SMs without any.
+  // sequences being shorter than their budget, if there are slots for them;
+  // large ones where the heads leave most SMs without any.
   const long long slots =
       std::min<long long>(ld_mass, (long long)max_pages * page);
   int C = 1;

@@ -32,6 +32,15 @@
 // q, do the softmax and write the parts.  While one half's softmax runs, the
 // tensor cores have the other's products.  Every wait is bounded; on a timeout
 // the CTA stops issuing, drains, frees TMEM and flags the error word.
+//
+// What bounds it: the chain of a half's tile (scores, their two readings by the
+// softmax, weights, products) and its handshakes, 5900 cycles for 256 rows by
+// 128 tokens of which the tensor pipe has 2100.  64 sequences of 9 tokens, 64
+// query and 8 key heads, 16384 shared and up to 2000 own tokens: 519 us, 540
+// TFLOP/s, the tensor pipe 33 %, issue slots 41 %.  Tiles of 64 tokens with two
+// score buffers a half and an issuer for each: the same.  The softmax's loops
+// are not unrolled and rare paths are kept short: the roles' code passes the
+// instruction caches, and each step that made it shorter gained 3 to 10 %.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -176,8 +185,9 @@ __host__ __device__ __forceinline__ size_t unit_of(const Shape& s, int Hkv,
 }
 // Where the run of CTA `cta` of `grid` starts.  A whole warp, each lane with a
 // stretch of the sequences; *bad: some length was out of range.
-__device__ __noinline__ void walk_start(const PagedAttnArgs& a, const Shape& s, int cta,
-                           int grid, Walk& w, bool* bad) {
+__device__ __noinline__ void walk_start(const PagedAttnArgs& a,
+                                        const Shape& s, int cta, int grid,
+                                        Walk& w, bool* bad) {
   const int lane = threadIdx.x & 31;
   const int per = (a.B + 31) / 32;
   const int b0 = min(a.B, lane * per), b1 = min(a.B, b0 + per);
@@ -239,8 +249,9 @@ __device__ __noinline__ void walk_start(const PagedAttnArgs& a, const Shape& s, 
 }
 // The next segment; false at the end of the run.  The units that begin in the
 // run go to `begun`.
-__device__ __noinline__ bool walk_next(const PagedAttnArgs& a, const Shape& s, Walk& w,
-                          int cta, Segment& g, Begun* begun) {
+__device__ __noinline__ bool walk_next(const PagedAttnArgs& a, const Shape& s,
+                                       Walk& w, int cta, Segment& g,
+                                       Begun* begun) {
   bool bad = false;
   while (w.left > 0) {
     const bool prefix = w.b < 0;

@@ -813,10 +813,11 @@ dflash_status dflash_kv_evict(
  * Requirements: R >= 1, 1 <= V < 2^31 - 256, ld >= V, 0 <= K <=
  * DFLASH_MAX_ALTERNATIVES.  No workspace.
  * A NaN logit counts as -inf (as a given token: logprob NaN, rank -1).  A row
- * with a +inf logit (or an x beyond fp32's range) has lse = +inf, one without any logit above -inf lse =
- * -inf; both have NaN for entropy and log probabilities.  Those three, and a T
- * that is below 2^-126 or not finite (taken as 1), set DFLASH_ERR_NONFINITE; a
- * token outside [-1, V) sets DFLASH_ERR_BAD_INDEX (logprob NaN, rank -1).
+ * with a +inf logit (or an x beyond fp32's range) has lse = +inf, one without any
+ * logit above -inf lse = -inf; both have NaN for entropy and log probabilities.
+ * Those three, and a T that is below 2^-126 or not finite (taken as 1), set
+ * DFLASH_ERR_NONFINITE; a token outside [-1, V) sets DFLASH_ERR_BAD_INDEX
+ * (logprob NaN, rank -1).
  */
 dflash_status dflash_logprobs(
     const void* logits, int64_t ld, dflash_dtype dt, const float* temperature,
@@ -852,11 +853,12 @@ dflash_status dflash_profile_stage(int stage, void* begin, void* end);
  * B*K <= 128), dflash_paged_attn, dflash_shared_attn and dflash_attn_mass give
  * up on a wait that runs longer, stop issuing work, let their copies and MMAs
  * in flight complete, free their TMEM and set DFLASH_ERR_DEVICE_TIMEOUT in the
- * device error word (their results are then invalid).  dflash_sample's waits for the copies of a row do so too
- * (that row's token is then -1).  0 restores the default of 2 s, far beyond
- * any real wait; the CTA-pair LM head always uses it.  Process-wide host state,
- * meant for tests of that failure path ("Failure detection": a wait that
- * never completes must end in a status the host reads, not a hang).
+ * device error word (their results are then invalid).  dflash_sample's waits
+ * for the copies of a row do so too (that row's token is then -1).  0 restores
+ * the default of 2 s, far beyond any real wait; the CTA-pair LM head always
+ * uses it.  Process-wide host state, meant for tests of that failure path
+ * ("Failure detection": a wait that never completes must end in a status the
+ * host reads, not a hang).
  * Always returns DFLASH_OK. */
 dflash_status dflash_set_wait_limit_ns(uint64_t ns);
 
