@@ -5,13 +5,12 @@
 // largest l c, y = l c - r (one rounding), w = 2^y, S = sum w, U = sum w y:
 //   lse = ln2 (r + log2 S);   ln p_v = ln2 (y_v - log2 S);
 //   entropy = ln2 (log2 S - U / S).
-// One pass keeps r (at first the given token's l c), S and U of what a thread has
-// seen; when r grows by h, U becomes 2^-h (U - h S) and S 2^-h S, and two
-// threads' sums join likewise.  A
-// token's rank is the number of tokens before it in the order (logit
-// descending, id ascending), so its logit is fetched first and the pass counts:
-// words before the token those above the next smaller number, words after it
-// those above its logit.
+// One pass keeps r (at first of the given token's l c), S and U of what a thread
+// has seen; when r grows by h, U becomes 2^-h (U - h S) and S 2^-h S, and two
+// threads' sums join likewise.  A token's rank is the number of tokens before it in
+// the order (logit descending, id ascending), so its logit is fetched first and
+// the pass counts: words before the token those above the next smaller number,
+// words after it those above its logit.
 //
 // The K most likely: the K-th largest maximum of 64 groups of threads bounds
 // the K-th largest logit of the slice from below.  Of the threads that reach it
@@ -25,7 +24,7 @@
 // What bounds it: in batches instructions (26 a logit, 70 % of the issue slots)
 // and the steps at a row's end; for one row the chain of steps.  288 rows of
 // 151936 fp32 logits 45 us with 20 alternatives, 35 us without (4.9 TB/s), one
-// bf16 row 5.7 us. (Words on their way through shared memory, four to twelve of
+// bf16 row 5.7 us.  (Words on their way through shared memory, four to twelve of
 // a thread in flight instead of two: 49 to 51 us.)
 #include <cooperative_groups.h>
 

@@ -19,38 +19,48 @@ namespace {
 
 // Two to an SM of 152.  Not the device's count: the workspace query has none.
 constexpr int kTargetCtas = 304;
+// Of the own tokens, where there are shared ones, too: those of a wave that the
+// longer parts of the shared tokens leave, at least.
+constexpr int kOwnCtas = 100;
 constexpr int kMostSplits = kMaxSplits / 2;  // of the shared tokens, of others
 
-// Parts that `items` CTAs' tokens are cut into.
-int splits_of(long long items) {
-  return (int)std::min<long long>((kTargetCtas + items - 1) / items,
-                                  kMostSplits);
-}
 struct Splits {
   long long own_tiles, shared_tiles;
   int own, shared;
 };
-Splits simt_splits(long long B, long long Q, int Hq, int Hkv) {
+// Parts that tokens are cut into.  The shared tokens' CTAs do not pass a wave.
+// (fp32, 32 query and 8 key heads of 128: 16 sequences, 4096 shared tokens, four
+// parts in 256 CTAs 101 us, five in 320 163, three 142; 5 sequences of 4 queries,
+// 12 heads of 64, 1040 shared tokens 29 us, with 304 CTAs for either 37.)
+Splits simt_splits(long long B, long long Q, int Hq, int Hkv, bool any) {
   Splits s;
   s.own_tiles = (Q * (Hq / Hkv) + kRows - 1) / kRows;
   s.shared_tiles = (B * Q * (Hq / Hkv) + kRows - 1) / kRows;
-  s.own = splits_of(B * Hkv * s.own_tiles);
-  s.shared = splits_of(Hkv * s.shared_tiles);
+  const long long items = B * Hkv * s.own_tiles;
+  const int most = any ? kOwnCtas : kTargetCtas;
+  s.own = (int)std::min<long long>((most + items - 1) / items, kMostSplits);
+  s.shared = !any ? 0
+                  : (int)std::min<long long>(
+                        std::max(1ll, kTargetCtas / (Hkv * s.shared_tiles)),
+                        kMostSplits);
   return s;
 }
 
 size_t simt_ws(long long B, long long Q, int Hq, int Hkv, int D) {
-  const Splits s = simt_splits(B, Q, Hq, Hkv);
-  return (size_t)(s.own + s.shared) * B * Q * Hq * (D + 2) * sizeof(float);
+  int parts = 0;
+  for (const bool any : {false, true}) {
+    const Splits s = simt_splits(B, Q, Hq, Hkv, any);
+    parts = std::max(parts, s.own + s.shared);
+  }
+  return (size_t)parts * B * Q * Hq * (D + 2) * sizeof(float);
 }
 
 template <typename T, int W, int G>
 cudaError_t launch_simt(const PagedAttnArgs& a, int shared, float* part,
                         cudaStream_t s) {
-  const Splits n = simt_splits(a.B, a.Q, a.Hq, a.Hkv);
-  SharedView v{shared, 0, (int)n.shared_tiles, 0};
+  const Splits n = simt_splits(a.B, a.Q, a.Hq, a.Hkv, shared > 0);
+  SharedView v{shared, n.shared, (int)n.shared_tiles, 0};
   if (shared > 0) {
-    v.splits = n.shared;
     const long long items = a.Hkv * n.shared_tiles * n.shared;
     if (items > 0x7fffffffll) return cudaErrorNotSupported;
     v.items = (unsigned)items;
