@@ -15,8 +15,8 @@ import torch
 from oracle import serving_ops as so
 from oracle import target_ops as to
 from parity import np_
-from test_gpu_serving_ops import U, _i32, _mass_args, _status
-from test_gpu_target_ops import DT, _check_attn, _tables
+from test_gpu_serving_ops import U, _check_evict, _i32, _mass_args, _status
+from test_gpu_target_ops import DT, Cache, _check_attn, _tables
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -324,6 +324,27 @@ def test_attention_with_nothing_shared_is_paged_attention(lib):
                                             *extra, 0.1, out, lse, ws)
         lib.dflash_check()
         _check_attn("bf16", D, 700, out, lse, ref)
+
+
+@pytest.mark.parametrize("Hkv,D,page,budget,sink,recent,kv", [
+    # clusters of eight, whose slots do not fit their registers
+    (1, 16, 128, 100001, 5, 1000, [150003]),
+    (1, 32, 16, 66000, 0, 0, [70001, 3]),
+    # many heads: small CTAs, the same for one sequence
+    (8, 16, 64, 12000, 100, 50, [20001] + [90] * 19),
+    # nothing to choose in clusters of several CTAs
+    (2, 64, 32, 2500, 1500, 1000, [3000, 2501, 2500, 7777]),
+    (8, 64, 16, 700, 0, 700, [3000] * 3),
+])
+@pytest.mark.parametrize("ties", [False, True])
+def test_eviction_by_clusters(lib, Hkv, D, page, budget, sink, recent, kv,
+                              ties):
+    rng = np.random.default_rng(budget + ties)
+    cache = Cache(kv, page, Hkv, D, rng)
+    mass = rng.random((len(kv), Hkv, max(kv) + 5)).astype(np.float32)
+    if ties:
+        mass = np.floor(mass * 4) / 4
+    _check_evict(lib, cache, mass, kv, budget, sink, recent)
 
 
 def _limited(lib, call):
