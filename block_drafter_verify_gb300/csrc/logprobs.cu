@@ -69,8 +69,18 @@ struct Args {
 struct Sums {
   float m, r, s, u;
 };
+// Products l c from this size on are rounded by whole bits, and more: there y is
+// what their rounded values differ by, never above 0.
+constexpr float kFar = 0x1p30f;
+constexpr float kLowest = -0x1.fffffep127f;  // instead of a finite l's -inf
+__device__ __forceinline__ float far_bits(float l, float c, float ref) {
+  return l == -INFINITY
+             ? -INFINITY
+             : fminf(fmaxf(__fmul_rn(l, c), kLowest) + ref, 0.f);
+}
 // 2^h u and s of a reference that is h higher.
 __device__ __forceinline__ void lower(float h, float& s, float& u) {
+  h = fmaxf(h, -1024.f);             // (the same 0, and no infinite h s)
   const float f = tc::ex2_approx(h);
   u = f * fmaf(h, s, u);
   s *= f;
@@ -183,13 +193,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   pdl_wait();
   const int r = blockIdx.x / C;
   const T* row = static_cast<const T*>(a.logits) + (long long)r * a.ld;
-  float t = a.temperature ? a.temperature[r] : 1.f;
-  bool odd = false;
-  if (!(t >= 0x1p-126f && t < INFINITY)) {
-    odd = true;
-    t = 1.f;
-  }
-  const float c = kLog2e / t;
+  auto temperature = [&](bool& odd) {
+    const float t = a.temperature ? a.temperature[r] : 1.f;
+    odd = !(t >= 0x1p-126f && t < INFINITY);
+    return odd ? 1.f : t;
+  };
+  bool odd;
+  const float c = kLog2e / temperature(odd);
   const int token = a.token ? a.token[r] : -1;
   const bool given = token >= 0 && token < a.V;
   const float mine = given ? to_f32(row[token]) : 0.f;
@@ -272,13 +282,16 @@ __global__ void __launch_bounds__(kThreads, 2)
       best = top > acc.m ? first : best;
     }
     acc.m = fmaxf(acc.m, top);
-    if (top * c > acc.r) {
-      const float r = ceilf(top * c);
+    const float bits = fmaxf(top * c, kLowest);
+    if (bits > acc.r) {
+      const float r = ceilf(bits);
       const float h = acc.r - r;     // -inf at first, and before +inf
       if (h > -INFINITY) lower(h, acc.s, acc.u);
       acc.r = r;
     }
-    const float ref = acc.r == -INFINITY ? 0.f : -acc.r;
+    // (far: NaNs, which are seen below)
+    const float ref =
+        fabsf(acc.r) < kFar ? -acc.r : __int_as_float(0x7fffffff);
     const uint64_t ref2 = pack2(ref, ref);
     uint64_t s2 = 0, u2 = 0;
 #pragma unroll
@@ -298,15 +311,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     unpack2(s2, s0, s1);
     unpack2(u2, u0, u1);
     u0 += u1;
-    if (u0 != u0) {                  // -inf, whose weight is 0: again without
-      u0 = 0.f;
+    if (u0 != u0) {                  // far, or -inf, whose weight is 0: again
+      s0 = s1 = u0 = 0.f;
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         if (k >= n) break;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-          const float y = fmaf(f[k][j], c, ref);
-          if (y > -INFINITY) u0 = fmaf(tc::ex2_approx(y), y, u0);
+          const float y = ref == ref ? fmaf(f[k][j], c, ref)
+                                     : far_bits(f[k][j], c, -acc.r);
+          const float w = tc::ex2_approx(y);
+          s0 += w;
+          if (y > -INFINITY) u0 = fmaf(w, y, u0);
         }
       }
     }
@@ -498,17 +514,26 @@ __global__ void __launch_bounds__(kThreads, 2)
   // (an x beyond fp32's range counts as infinite)
   const bool empty = x.m == -INFINITY;
   const bool infinite = !empty && !(fabsf(x.r) < INFINITY);
+  const bool far = fabsf(x.r) >= kFar;
   const float log_s = log2f(x.s);
   const float nan = __int_as_float(0x7fffffff);
+  // (read again: held over the pass it cost the registers of something else)
+  bool known;
+  const float t = temperature(known);
+  const float lse = empty      ? -INFINITY
+                    : infinite ? x.r
+                    : far      ? x.m / t + log_s * kLn2
+                               : (x.r + log_s) * kLn2;
   // (ln p in one rounding of y: exact for the row's likeliest tokens)
-  auto log_p = [&](float l) { return (fmaf(l, c, -x.r) - log_s) * kLn2; };
+  auto log_p = [&](float l) {
+    if (far) return (far_bits(l, c, -x.r) - log_s) * kLn2;
+    const float y = fmaf(l, c, -x.r);
+    return y < -kFar ? l / t - lse : (y - log_s) * kLn2;
+  };
   if (tid == 0) {
     if (any_odd || empty || infinite) raise_error(a.err, kErrNonfinite);
     if (token >= a.V || token < -1) raise_error(a.err, kErrBadIndex);
-    if (a.lse)
-      a.lse[r] = empty      ? -INFINITY
-                 : infinite ? x.r
-                            : (x.r + log_s) * kLn2;
+    if (a.lse) a.lse[r] = lse;
     if (a.entropy)
       a.entropy[r] = empty || infinite
                          ? nan

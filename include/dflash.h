@@ -813,11 +813,13 @@ dflash_status dflash_kv_evict(
  * Requirements: R >= 1, 1 <= V < 2^31 - 256, ld >= V, 0 <= K <=
  * DFLASH_MAX_ALTERNATIVES.  No workspace.
  * A NaN logit counts as -inf (as a given token: logprob NaN, rank -1).  A row
- * with a +inf logit (or an x beyond fp32's range) has lse = +inf, one without any
- * logit above -inf lse = -inf; both have NaN for entropy and log probabilities.
- * Those three, and a T that is below 2^-126 or not finite (taken as 1), set
- * DFLASH_ERR_NONFINITE; a token outside [-1, V) sets DFLASH_ERR_BAD_INDEX
- * (logprob NaN, rank -1).
+ * with a +inf logit (or an x above 2.3e38, whose bits pass fp32's range) has lse =
+ * +inf, one without any logit above -inf lse = -inf; both have NaN for entropy and
+ * log probabilities.  Those three, and a T that is below 2^-126 or not finite
+ * (taken as 1), set DFLASH_ERR_NONFINITE; a token outside [-1, V) sets
+ * DFLASH_ERR_BAD_INDEX (logprob NaN, rank -1).  Finite logits, a type's lowest
+ * value among them, are none of these; weights of x beyond 2^29 in size are told
+ * apart as far as their rounded values differ.
  */
 dflash_status dflash_logprobs(
     const void* logits, int64_t ld, dflash_dtype dt, const float* temperature,

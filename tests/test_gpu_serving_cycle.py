@@ -5,6 +5,7 @@ waits' limits; and examples/shared_prompt.py.
 
 Tolerances: those of test_gpu_serving_ops and test_gpu_target_ops, whose
 derivations stand there; everything else is equal bit for bit."""
+import math
 import os
 import sys
 
@@ -15,7 +16,8 @@ import torch
 from oracle import serving_ops as so
 from oracle import target_ops as to
 from parity import np_
-from test_gpu_serving_ops import U, _check_evict, _i32, _mass_args, _status
+from test_gpu_serving_ops import (U, _check_evict, _check_logprobs, _i32,
+                                  _logprobs, _mass_args, _status)
 from test_gpu_target_ops import DT, Cache, _check_attn, _tables
 
 pytestmark = pytest.mark.gpu
@@ -345,6 +347,65 @@ def test_eviction_by_clusters(lib, Hkv, D, page, budget, sink, recent, kv,
     if ties:
         mass = np.floor(mass * 4) / 4
     _check_evict(lib, cache, mass, kv, budget, sink, recent)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T", [0.5, 1.0, 2.0, 7.0])
+def test_log_probabilities_of_masked_rows(lib, dtype, T):
+    """Rows masked by the type's lowest value, in whole stretches: as if those
+    tokens were not there, also if one of them is the given token, whose own log
+    probability is what its logit says."""
+    rng = np.random.default_rng(21)
+    V, K, low = 30011, 8, torch.finfo(DT[dtype]).min
+    l = torch.tensor(rng.standard_normal((4, V)) * 3,
+                     dtype=torch.float32).to(DT[dtype]).cuda()
+    l[0, 100:] = low
+    l[1, :V - 3] = low
+    l[2, ::2] = low
+    l[3, 5:29000] = low
+    token = [3, V - 1, 7, 9]
+    got = _logprobs(lib, l, [T] * 4, token, K)
+    lib.dflash_check()
+    want = l.clone()
+    want[want == low] = -torch.inf
+    # (the oracle's weights of them are 0 either way)
+    seen = {k: v[:3] for k, v in got.items()}
+    seen["top"], seen["top_id"] = got["top"][:3, :3], got["top_id"][:3, :3]
+    _check_logprobs(want[:3], [T] * 3, token[:3], 3, seen)
+    _check_logprobs(want[3:], [T], [0], 4,
+                    {k: v[3:] for k, v in _logprobs(
+                        lib, l, [T] * 4, [0] * 4, 4).items()})
+    # (l / T may pass fp32's range)
+    own = low / T if low / T > -3.5e38 else -np.inf
+    assert got["logprob"][3] == own or abs(
+        got["logprob"][3] / own - 1) <= 4 * U
+    # three tokens only: the others follow in the order of their ids
+    assert got["top_id"][1, 3:].tolist() == list(range(K - 3))
+    assert np.all(got["top"][1, 3:] <= -1e37)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T", [0.5, 1.0, 2.0])
+def test_log_probabilities_of_rows_all_at_one_far_value(lib, dtype, T):
+    """All tokens at the type's lowest value, at a large one of either sign,
+    some at -inf: uniform over what is not -inf."""
+    V = 4099
+    for value in (torch.finfo(DT[dtype]).min, -1e30, 1e30, 3e9, -3e9):
+        l = torch.full((2, V), value, dtype=torch.float32).to(
+            DT[dtype]).cuda()
+        l[1, 10:] = -torch.inf
+        got = _logprobs(lib, l, [T] * 2, [5, 5], 4)
+        lib.dflash_check()
+        for r, n in ((0, V), (1, 10)):
+            x = float(l[0, 0].float()) / T
+            z = -np.inf if x < -3.5e38 else np.float32(x + math.log(n))
+            assert got["lse"][r] == z or abs(got["lse"][r] / z - 1) <= 4 * U
+            tol = (V / 512 + 40) * U + 8 * U * math.log(n)
+            assert abs(got["logprob"][r] + math.log(n)) <= tol
+            assert abs(got["entropy"][r] - math.log(n)) <= tol
+            assert got["rank"][r] == 5
+            assert got["top_id"][r].tolist() == [0, 1, 2, 3]
+            assert np.all(np.abs(got["top"][r] + math.log(n)) <= tol)
 
 
 def _limited(lib, call):
