@@ -285,8 +285,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float bits = fmaxf(top * c, kLowest);
     if (bits > acc.r) {
       const float r = ceilf(bits);
-      const float h = acc.r - r;     // -inf at first, and before +inf
-      if (h > -INFINITY) lower(h, acc.s, acc.u);
+      // (a step of -inf, at first, before +inf or where it passes fp32's range,
+      // leaves nothing)
+      lower(acc.r - r, acc.s, acc.u);
       acc.r = r;
     }
     // (far: NaNs, which are seen below)

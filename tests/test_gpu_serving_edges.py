@@ -1,0 +1,60 @@
+"""The operators around a shared prompt and a bounded cache at calls that their
+documentation allows and the other tests do not make.  Oracle and tolerances as
+in test_gpu_serving_ops, whose derivations stand there."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving_ops as so
+from test_gpu_serving_ops import _logprobs
+from test_gpu_target_ops import DT, U
+
+pytestmark = pytest.mark.gpu
+
+
+# --------------------------------------------------------------------------
+# log probabilities
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,far", [(1e-32, 3.0), (1.0, 1e33), (1.0, 3e37),
+                                   (0.25, 1e31)])
+@pytest.mark.parametrize("given", ["none", "masked", "far"])
+def test_masked_tokens_before_a_far_logit_count_nothing(lib, dtype, T, far,
+                                                        given):
+    """A thread whose first words are all at the type's lowest value and that
+    meets a logit of 1e31 bits or more only then: a step that passes fp32's
+    range.  Every slice of the row is masked but for its end.
+
+    A product l log2(e) / T is rounded (U of itself), and so is its logarithm:
+    alternatives are off by 4 U of the largest x."""
+    V, K = 70001, 4
+    low = torch.finfo(DT[dtype]).min
+    x = torch.full((3, V), low, dtype=torch.float64)
+    x[0, V - 5:] = far * torch.tensor([0.5, 0.25, 1.0, 0.125, -0.5])
+    x[1, 8700] = far                      # the last words of a slice
+    x[1, V - 1] = far / 2
+    x[2, 40000] = -far                    # nothing above 0
+    l = x.to(DT[dtype]).cuda()
+    token = {"none": None, "masked": [3, 5, 7],
+             "far": [V - 3, 8700, 40000]}[given]
+    got = _logprobs(lib, l, [T] * 3, token, K,
+                    None if token else ["lse", "entropy", "top", "top_id"])
+    lib.dflash_check()
+    l = l.double().cpu().numpy()
+    for r, n in ((0, 4), (1, 2), (2, 1)):
+        lp, rank, z, ent, top, ids = so.logprobs_row(
+            l[r], T, token[r] if token else -1, K)
+        assert ent == 0
+        assert abs(got["entropy"][r]) <= 40 * U
+        assert abs(got["lse"][r] - z) <= 4 * U * abs(z) + 40 * U
+        assert np.array_equal(got["top_id"][r, :n], ids[:n])
+        tol = 4 * U * abs(z) + 40 * U
+        assert np.all(np.abs(got["top"][r, :n] - top[:n]) <=
+                      tol + 8 * U * np.abs(top[:n]))
+        assert abs(got["top"][r, 0]) <= 40 * U
+        if token:
+            assert got["rank"][r] == rank
+        if given == "far":
+            assert abs(got["logprob"][r]) <= 40 * U
