@@ -170,6 +170,7 @@ struct Walk {
   int b, hk, u, at;       // b = -1: the shared tokens; at: position in the unit
   int left;               // positions left in this CTA's run
   int pos;                // position among all
+  int shared_end;         // of the shared tokens that some sequence has
   Runs runs;
 };
 // A unit that has tiles, as the CTA that begins it leaves it for the join: its
@@ -191,10 +192,13 @@ __device__ __noinline__ void walk_start(const PagedAttnArgs& a,
   const int lane = threadIdx.x & 31;
   const int per = (a.B + 31) / 32;
   const int b0 = min(a.B, lane * per), b1 = min(a.B, b0 + per);
-  int work = 0;
+  int work = 0, longest = 0;
 #pragma unroll 1
-  for (int b = b0; b < b1; ++b)
-    work += a.Hkv * own_work(a, s, lens_of(a, b, bad));
+  for (int b = b0; b < b1; ++b) {
+    const Lens l = lens_of(a, b, bad);
+    work += a.Hkv * own_work(a, s, l);
+    longest = max(longest, l.n);
+  }
   int run = work;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -205,7 +209,10 @@ __device__ __noinline__ void walk_start(const PagedAttnArgs& a,
   run += first;
   const int total = __shfl_sync(0xffffffffu, run, 31);
   const int G = min(grid, total);
-  w = Walk{0, 0, 0, 0, 0, 0, Runs{0, 0, G}};
+  // (what lies behind the longest sequence may be anything)
+  const int shared_end =
+      min(s.shared, __reduce_max_sync(0xffffffffu, longest));
+  w = Walk{0, 0, 0, 0, 0, 0, shared_end, Runs{0, 0, G}};
   if (cta >= G) return;                    // the same in every lane
   w.runs.q = total / G;
   w.runs.r = total - w.runs.q * G;
@@ -290,7 +297,7 @@ __device__ __noinline__ bool walk_next(const PagedAttnArgs& a, const Shape& s,
       g.rows = min(kRows, (prefix ? s.all : s.own) - u * kRows);
       g.tok0 = tok + t0 * kTile;
       g.T = t1 - t0;
-      g.end = prefix ? s.shared : l.n;
+      g.end = prefix ? w.shared_end : l.n;
       g.slot = t1 - t0 == T ? -1 : 2 * cta + (from > 0 ? 0 : 1);
       return true;
     }

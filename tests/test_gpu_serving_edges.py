@@ -8,8 +8,9 @@ import pytest
 import torch
 
 from oracle import serving_ops as so
-from test_gpu_serving_ops import _logprobs
-from test_gpu_target_ops import DT, U
+from oracle import target_ops as to
+from test_gpu_serving_ops import SharedCache, _logprobs, _share
+from test_gpu_target_ops import DT, U, _check_attn
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +59,62 @@ def test_masked_tokens_before_a_far_logit_count_nothing(lib, dtype, T, far,
             assert got["rank"][r] == rank
         if given == "far":
             assert abs(got["logprob"][r]) <= 40 * U
+
+
+# --------------------------------------------------------------------------
+# attention under a shared prefix
+# --------------------------------------------------------------------------
+def _ends_inside(dtype, B, Q, Hq, Hkv, D, page, shared, most, numbers, rng):
+    """A SharedCache all of whose sequences end at `most` or before, within
+    the prefix; what lies behind holds NaN codes and scales or, without page
+    `numbers`, is in no page."""
+    kv = [int(rng.integers(0, most + 1)) for _ in range(B)]
+    kv[0] = most
+    cache = SharedCache(shared, kv, page, Hkv, D, rng)
+    row = cache.table[0]
+    if most % page:
+        for c in cache.codes:
+            c[row[most // page], :, most % page:] = 0x7F
+    behind = row[-(-most // page):shared // page].copy()
+    for c, s in zip(cache.codes, cache.scale):
+        c[behind] = 0x7F
+        s[behind] = np.nan
+    if not numbers:
+        row[-(-most // page):] = rng.choice([-9, 10 ** 6],
+                                            row.size - -(-most // page))
+    q = torch.tensor(rng.standard_normal((B, Q, Hq, D)) * 2,
+                     dtype=torch.float32).to(DT[dtype]).cuda()
+    return cache, q, kv
+
+
+# dtype, B, Q, Hq, Hkv, D, page, shared, the longest
+INSIDE = [
+    ("bf16", 2, 40, 32, 2, 64, 32, 7040, 7001),       # together
+    ("bf16", 2, 40, 32, 2, 128, 16, 7040, 150),
+    ("bf16", 320, 1, 8, 2, 64, 32, 3840, 3300),       # apart
+    ("bf16", 320, 2, 8, 2, 80, 64, 3840, 64),
+    ("bf16", 3, 1, 8, 2, 64, 16, 320, 100),           # unshared
+    ("fp32", 3, 5, 4, 2, 64, 16, 1600, 777),
+    ("bf16", 3, 5, 4, 2, 256, 64, 640, 129),
+]
+
+
+@pytest.mark.parametrize("dtype,B,Q,Hq,Hkv,D,page,shared,most", INSIDE)
+@pytest.mark.parametrize("causal,numbers", [(True, True), (False, False)])
+def test_prefix_that_no_sequence_has_to_its_end(lib, dtype, B, Q, Hq, Hkv, D,
+                                                page, shared, most, causal,
+                                                numbers):
+    """Slots past every length may hold anything, entries of the page table
+    that no token needs too."""
+    rng = np.random.default_rng(B + most)
+    cache, q, kv = _ends_inside(dtype, B, Q, Hq, Hkv, D, page, shared, most,
+                                numbers, rng)
+    ql = [int(rng.integers(0, Q + 1)) for _ in range(B)]
+    ql[0] = Q
+    out, lse = _share(lib, dtype, cache, q, kv, ql, shared, causal, D ** -0.5)
+    lib.dflash_check()
+    ref = to.paged_attn(q.float().cpu().numpy().astype(np.float64),
+                        *cache.codes, *cache.scale,
+                        so.shared_table(cache.table, shared, page), kv, ql,
+                        D ** -0.5, causal)
+    _check_attn(dtype, D, max(kv), out, lse, ref)
