@@ -273,6 +273,7 @@ __global__ void __launch_bounds__(Plan<kRows>::kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     const int pt = kTile / a.page;           // pages of a tile
+    const int first_page = a.first / a.page;  // (of those below, none is read)
     const int oob = a.num_pages * a.Hkv * a.page;  // a row past the pool
     const uint32_t box = (uint32_t)a.page * 128;
     const float c = fabsf(a.scale) * kLog2e;
@@ -312,7 +313,8 @@ __global__ void __launch_bounds__(Plan<kRows>::kThreads, 1)
         }
         const int from = pg - at + lane;     // lane < pt: its page
         const int pid = __shfl_sync(0xffffffffu, id, from & 31);
-        const bool have = lane < pt && pg + lane < last;
+        const bool have =
+            lane < pt && pg + lane < last && pg + lane >= first_page;
         const bool bad = have && (pid < 0 || pid >= a.num_pages);
         if (bad) raise_error(a.err, kErrBadIndex);
         const int row = bad ? oob : (pid * a.Hkv + g.hk) * a.page;

@@ -732,8 +732,9 @@ dflash_status dflash_shared_attn(
  * queries only.
  *   lse   [B, Q, Hq] fp32;  fresh [B] int32: the slots from which on there is
  *         no weight yet (the length before the block), or NULL: kv_len
- *   first slots below it are not looked at (those that an eviction keeps
- *         anyway, for example a prefix that sequences share)
+ *   first slots below it are not looked at, nor pages that end below it (those
+ *         that an eviction keeps anyway, for example a prefix that sequences
+ *         share, whatever their rows of page_table hold there)
  *   mass  [B, Hkv] rows of fp32, ld_mass elements apart, in/out
  * Sums and weights are fp32; their order is fixed, and nothing is added
  * atomically.  (bf16 and D <= 128, the tensor cores: q as two E4M3 numbers, all

@@ -9,8 +9,10 @@ import torch
 
 from oracle import serving_ops as so
 from oracle import target_ops as to
-from test_gpu_serving_ops import SharedCache, _logprobs, _share
-from test_gpu_target_ops import DT, U, _check_attn
+from parity import np_
+from test_gpu_serving_ops import (SharedCache, _evict, _i32, _logprobs,
+                                  _mass_args, _share)
+from test_gpu_target_ops import DT, U, Cache, _check_attn
 
 pytestmark = pytest.mark.gpu
 
@@ -118,3 +120,73 @@ def test_prefix_that_no_sequence_has_to_its_end(lib, dtype, B, Q, Hq, Hkv, D,
                         so.shared_table(cache.table, shared, page), kv, ql,
                         D ** -0.5, causal)
     _check_attn(dtype, D, max(kv), out, lse, ref)
+
+
+# --------------------------------------------------------------------------
+# gathered attention weight
+# --------------------------------------------------------------------------
+def _check_mass(lib, dtype, cache, q, kv, ql, lse, first, scale=None):
+    Q, Hq, D = q.shape[1:]
+    Hkv = cache.codes[0].shape[1]
+    scale = D ** -0.5 if scale is None else scale
+    (kc, _, ks, _), table = cache.cuda()
+    old = np.zeros((len(kv), Hkv, max(max(kv), 1) + 5), np.float32)
+    mass = torch.from_numpy(old.copy()).cuda()
+    lib.dflash_attn_mass(q, kc, ks, table, _i32(kv), _i32(ql),
+                         torch.from_numpy(lse).cuda(), None, first, scale,
+                         1.0, mass)
+    lib.dflash_check()
+    # (keys past a length are not numbers, and not read)
+    want, size = so.attn_mass(q.float().cpu().numpy().astype(np.float64),
+                              cache.codes[0], cache.scale[0], cache.table, kv,
+                              [Q] * len(kv) if ql is None else ql, lse, None,
+                              first, scale, 1.0, old)
+    tol = (D + 12) * U * size + (Q * Hq // Hkv + 16) * U * np.abs(want)
+    bad = ~(np.abs(np_(mass) - want) <= tol)
+    assert not bad.any(), (np.abs(np_(mass) - want)[bad].max(), bad.sum())
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,page,Q,first", [
+    ("bf16", 8, 2, 64, 16, 3, 80), ("bf16", 8, 1, 128, 64, 9, 192),
+    ("bf16", 32, 1, 64, 32, 5, 32), ("bf16", 4, 2, 64, 32, 1, 1003),
+    ("bf16", 4, 2, 256, 16, 2, 80), ("fp32", 4, 2, 64, 16, 2, 80)])
+def test_mass_below_first_reads_no_pages(lib, dtype, Hq, Hkv, D, page, Q,
+                                         first):
+    """The page numbers of a shared prefix in rows other than the first may be
+    anything, as in dflash_shared_attn; those of the first slot's own page are
+    needed."""
+    rng = np.random.default_rng(first + D)
+    kv = [first + Q, first + 200, max(first - 7, Q)]
+    cache, q, _, nq, lse = _mass_args(rng, dtype, Hq, Hkv, D, page, Q, True,
+                                      kv, None)
+    want_table = cache.table.copy()
+    cache.table[1:, :first // page] = rng.choice(
+        [-9, 10 ** 6], (2, first // page))
+    rest = cache.cuda
+    seen = cache.table
+
+    def cuda():
+        pool, _ = rest()
+        return pool, torch.from_numpy(seen.copy()).cuda()
+    cache.cuda, cache.table = cuda, want_table
+    _check_mass(lib, dtype, cache, q, kv, None, lse, first)
+
+
+@pytest.mark.parametrize("Hkv,page,shared,budget", [(2, 16, 80, 100),
+                                                    (1, 64, 192, 210)])
+def test_eviction_reads_no_pages_of_a_kept_prefix(lib, Hkv, page, shared,
+                                                  budget):
+    """Nor does dflash_kv_evict with a sink that covers them."""
+    rng = np.random.default_rng(page)
+    kv = [shared + 150, shared + 90, shared + 5]
+    cache = Cache(kv, page, Hkv, 64, rng)
+    mass = rng.random((3, Hkv, max(kv))).astype(np.float32)
+    got = []
+    for nonsense in (False, True):
+        if nonsense:
+            cache.table[1:, :shared // page] = rng.choice(
+                [-9, 10 ** 6], (2, shared // page))
+        got.append(_evict(lib, cache, mass, kv, budget, shared, 10))
+        lib.dflash_check()
+    for a, b in zip(*got):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
