@@ -89,8 +89,8 @@ __global__ void __launch_bounds__(kTokens)
       for (int i = 0; i < 8; ++i) {
         const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
             (__nv_fp8x2_storage_t)(x[i >> 1] >> (16 * (i & 1))), __NV_E4M3)));
-        k[2 * i] = f.x * ks;
-        k[2 * i + 1] = f.y * ks;
+        k[2 * i] = f.x;
+        k[2 * i + 1] = f.y;
       }
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(kTokens)
     }
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
-      if (t < s_lim[r] && s_lse[r] != -INFINITY) sum += expf(s[r] - s_lse[r]);
+      if (t < s_lim[r] && s_lse[r] != -INFINITY)
+        sum += expf(s[r] * ks - s_lse[r]);
   }
   if (mine) mass_store(a, b, hk, t, sum);
 }

@@ -41,6 +41,11 @@ constexpr int kMaxRows = 128;    // of a segment
 constexpr int kSegs = 4;
 constexpr int kUnitCost = 2;     // of a pair besides its tiles, in tiles
 constexpr float kLog2e = 1.4426950408889634f;
+// A score is (sum of products) (key's factor) (row's factor), and the first two
+// alone can pass fp32's range: 2^24 times a key's scale of up to 2^120.  So
+// 2^24 goes from the key's factor to the row's, for queries below 2^111 (scores
+// of larger ones pass 2^47 with the smallest scale, where fp32 has no weights).
+constexpr int kToRow = 24;
 
 // Tiles of one pair with (up to 64 or 128) of its rows; without rows: the sums
 // of those tiles are complete.
@@ -276,7 +281,7 @@ __global__ void __launch_bounds__(Plan<kRows>::kThreads, 1)
     const int first_page = a.first / a.page;  // (of those below, none is read)
     const int oob = a.num_pages * a.Hkv * a.page;  // a row past the pool
     const uint32_t box = (uint32_t)a.page * 128;
-    const float c = fabsf(a.scale) * kLog2e;
+    const float c = fabsf(a.scale) * kLog2e * (1.f / (1 << kToRow));
     Ring<kStages> rk;
     int in_flight = 0;
     bool ok = true;
@@ -511,7 +516,7 @@ __global__ void __launch_bounds__(Plan<kRows>::kThreads, 1)
 #pragma unroll
         for (int o = 4; o; o >>= 1)
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const int e = max((int)(__float_as_uint(top) >> 23) - 127, -100);
+        const int e = max((int)(__float_as_uint(top) >> 23) - 127, -119);
         float up = top < INFINITY ? __uint_as_float((134 - e) << 23)
                                   : __uint_as_float(0x7fffffffu);
         if (a.scale < 0.f) up = -up;
@@ -542,7 +547,8 @@ __global__ void __launch_bounds__(Plan<kRows>::kThreads, 1)
         *reinterpret_cast<uint4*>(dst + np * 128) =
             make_uint4(lo[0], lo[1], lo[2], lo[3]);
         if (ch == 0)
-          m.row[rq.at][r >> 1].rel[r & 1] = __uint_as_float((120 + e) << 23);
+          m.row[rq.at][r >> 1].rel[r & 1] =
+              __uint_as_float(min(120 + kToRow + e, 254) << 23);
       }
       fence_async();
       __syncwarp();

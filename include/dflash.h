@@ -738,7 +738,7 @@ dflash_status dflash_shared_attn(
  *   mass  [B, Hkv] rows of fp32, ld_mass elements apart, in/out
  * Sums and weights are fp32; their order is fixed, and nothing is added
  * atomically.  (bf16 and D <= 128, the tensor cores: q as two E4M3 numbers, all
- * of bf16's bits down to 2^-17 of its row's largest value.)
+ * of bf16's bits down to 2^-17 of its row's largest value; queries below 2^111.)
  * Requirements: as dflash_paged_attn; first >= 0, ld_mass >= 1, decay finite;
  * work that could pass 2^31 tiles of 128 rows times 128 tokens gives
  * DFLASH_ERR_UNSUPPORTED.

@@ -172,6 +172,42 @@ def test_mass_below_first_reads_no_pages(lib, dtype, Hq, Hkv, D, page, Q,
     _check_mass(lib, dtype, cache, q, kv, None, lse, first)
 
 
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 128),
+                                     ("bf16", 256), ("fp32", 64)])
+@pytest.mark.parametrize("up,down", [(112, -110), (118, -116), (-60, 62)])
+def test_mass_of_keys_and_queries_far_from_one(lib, dtype, D, up, down):
+    """Key scales up to 2^118 with queries as small, and the other way round:
+    scores of ordinary size, of which no intermediate may overflow."""
+    rng = np.random.default_rng(up + D)
+    Hq, Hkv, page, Q, kv = 8, 2, 32, 3, [300, 77]
+    cache, q, *_ = _mass_args(rng, dtype, Hq, Hkv, D, page, Q, True, kv, None)
+    # (codes below 256: with those above a value may pass fp32's range)
+    cache.codes[0] = np.where((cache.codes[0] & 0x7F) > 0x77,
+                              cache.codes[0] & 0x87, cache.codes[0])
+    N = cache.scale[0].shape[0]
+    cache.scale[0][:] = np.exp2(up - rng.integers(0, 4, (N, Hkv)))
+    q = (q.float() * 2.0 ** (down - 6)).to(DT[dtype])
+    q64 = q.float().cpu().numpy().astype(np.float64)
+    _, lse, _, _ = to.paged_attn(q64, cache.codes[0], cache.codes[0],
+                                 cache.scale[0], cache.scale[0], cache.table,
+                                 kv, [Q] * 2, D ** -0.5, True)
+    _check_mass(lib, dtype, cache, q, kv, None, lse.astype(np.float32), 0)
+
+
+def test_mass_of_a_key_of_zeros_under_large_scores(lib):
+    """Its score is 0, whatever its page's scale and the query's size: a weight
+    of exp(0 - lse)."""
+    rng = np.random.default_rng(17)
+    for dtype in ("bf16", "fp32"):
+        cache, q, _, _, lse = _mass_args(rng, dtype, 8, 2, 64, 16, 1, True,
+                                         [200], None)
+        cache.codes[0][:] = 0
+        cache.scale[0][:] = 2.0 ** 60
+        q *= 2.0 ** 100
+        lse[:] = 3.0
+        _check_mass(lib, dtype, cache, q, [200], None, lse, 0)
+
+
 @pytest.mark.parametrize("Hkv,page,shared,budget", [(2, 16, 80, 100),
                                                     (1, 64, 192, 210)])
 def test_eviction_reads_no_pages_of_a_kept_prefix(lib, Hkv, page, shared,
