@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kTokens)
     }
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
-      if (t < s_lim[r] && s_lse[r] != -INFINITY)
+      if (t < s_lim[r] && fabsf(s_lse[r]) != INFINITY)
         sum += expf(s[r] * ks - s_lse[r]);
   }
   if (mine) mass_store(a, b, hk, t, sum);

@@ -77,7 +77,8 @@ struct Plan {
   struct Meta {
     Segment seg[kSegs];
     Rows row[2][kRows / 2];
-    int lim[2][kRows];             // tokens a row sees
+    int lim[2][kRows];             // tokens a row sees (none without weights)
+    int4 off[2];                   // some row has none: of the warps that say so
     float ks[kStages][8];          // factors of a tile's pages
     float keep[kKeep][kTile];
     uint64_t k_full[kStages], k_empty[kStages];
@@ -482,6 +483,9 @@ __global__ void __launch_bounds__(Plan<kRows>::kThreads, 1)
         return (long long)((size_t)g.b * a.Q + i) * a.Hq + g.hk * shape.g +
                row - i * shape.g;
       };
+      // A row whose logsumexp is infinite has no weights, whatever it holds: its
+      // scores, which may be no numbers, are masked.
+      bool off = false;
 #pragma unroll 1
       for (int r = r16; r < np; r += 16) {
         const bool read = r < g.rows && ch * 16 < a.D;
@@ -492,12 +496,17 @@ __global__ void __launch_bounds__(Plan<kRows>::kThreads, 1)
         copy16(tc::smem_u32(raw(r) + 16), src + 16, read);
         if (ch == 0) {
           const float lse = r < g.rows ? a.lse[out] : -INFINITY;
-          m.row[rq.at][r >> 1].nl[r & 1] =
-              lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+          const bool none = fabsf(lse) == INFINITY;
+          m.row[rq.at][r >> 1].nl[r & 1] = none ? -INFINITY : -lse * kLog2e;
           m.lim[rq.at][r] =
-              a.causal ? g.n - g.nq + (g.row0 + r) / shape.g + 1 : g.n;
+              none       ? 0
+              : a.causal ? g.n - g.nq + (g.row0 + r) / shape.g + 1
+                         : g.n;
+          off |= none && r < g.rows;
         }
       }
+      off = __any_sync(0xffffffffu, off);
+      if (lane == 0) (&m.off[rq.at].x)[warp - 4] = off;
       asm volatile("cp.async.wait_all;" ::: "memory");
       // (a warp has four rows: its lanes go together)
 #pragma unroll 1
@@ -588,6 +597,8 @@ __global__ void __launch_bounds__(Plan<kRows>::kThreads, 1)
       ok = wait_for(&m.q_full[rq.at], rq.phase, abort, a.wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
+      const int4 o4 = m.off[rq.at];
+      const bool off = (o4.x | o4.y | o4.z | o4.w) != 0;
 #pragma unroll 1
       for (int t = group; t < g.T; t += kGroups) {
         ok = wait_for(&m.s_full[group], s_par, abort, a.wait_ns);
@@ -598,7 +609,7 @@ __global__ void __launch_bounds__(Plan<kRows>::kThreads, 1)
         const float ct = m.ks[(tile + t) % kStages][tok >> page_bits];
         const int at = g.tok0 + t * kTile + tok;
         // some row does not see all of the tile
-        const bool masked = lims[0] < g.tok0 + (t + 1) * kTile;
+        const bool masked = off || lims[0] < g.tok0 + (t + 1) * kTile;
         const uint64_t ct2 = pack2(ct, ct);
         const uint64_t rest2 = pack2(1.f / 32, 1.f / 32);
         uint64_t sum2[2] = {0, 0};

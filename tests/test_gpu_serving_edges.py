@@ -208,6 +208,28 @@ def test_mass_of_a_key_of_zeros_under_large_scores(lib):
         _check_mass(lib, dtype, cache, q, [200], None, lse, 0)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_mass_of_rows_with_an_infinite_logsumexp_adds_nothing(lib, dtype):
+    """Whatever those rows hold: queries that are not numbers, infinite ones,
+    ones whose scores pass fp32's range."""
+    rng = np.random.default_rng(31)
+    Hq, Hkv, D, page, Q, kv = 8, 2, 64, 16, 3, [200, 40]
+    cache, q, _, nq, lse = _mass_args(rng, dtype, Hq, Hkv, D, page, Q, True,
+                                      kv, None)
+    cache.scale[0][:] = 2.0 ** 100
+    q *= 2.0 ** -106
+    q64 = q.float().cpu().numpy().astype(np.float64)
+    _, lse, _, _ = to.paged_attn(q64, cache.codes[0], cache.codes[0],
+                                 cache.scale[0], cache.scale[0], cache.table,
+                                 kv, nq, D ** -0.5, True)
+    lse = lse.astype(np.float32)
+    for i, x in enumerate((math.nan, math.inf, -math.inf, 2.0 ** 100)):
+        for b, z in ((0, -np.inf), (1, np.inf)):
+            q[b, i % 3, 2 * i] = x
+            lse[b, i % 3, 2 * i] = z
+    _check_mass(lib, dtype, cache, q, kv, None, lse, 0)
+
+
 @pytest.mark.parametrize("Hkv,page,shared,budget", [(2, 16, 80, 100),
                                                     (1, 64, 192, 210)])
 def test_eviction_reads_no_pages_of_a_kept_prefix(lib, Hkv, page, shared,
