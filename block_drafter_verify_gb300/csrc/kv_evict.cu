@@ -21,7 +21,7 @@
 // What bounds it: with few heads the chain of steps (three histograms, then the
 // loads of a round; kept slots and page ids are asked for a round ahead), with
 // many bytes.  Eight heads of 128: 2100 to 2048 tokens 20 us, 131072 to 100000
-// tokens 242 us; 32 such sequences of up to 8000 tokens to 6000 at most 120 us
+// tokens 255 us; 32 such sequences of up to 8000 tokens to 6000 at most 123 us
 // (59 us of bytes at the copy's rate; half of the issue slots: some 170
 // instructions for 16 codes, most of them maxima and conversions), where a
 // launch for the lists, one for the codes and whole histograms took 193 us, and
@@ -493,14 +493,12 @@ __global__ void __launch_bounds__(
         top[kv] = max(top[kv], __shfl_xor_sync(0xffffffffu, top[kv], o));
       if (lane == 0) sh.exp[kv][warp] = top[kv];
     }
-    // All of the round's slots have been read: their codes are in `top`.  The
-    // cluster only waits, it hands nothing over (nothing that was written is
-    // read again), and needs no fence.
-    __syncthreads();
-    if (C > 1)
-      asm volatile(
-          "barrier.cluster.arrive.relaxed.aligned;\n\t"
-          "barrier.cluster.wait.aligned;" ::: "memory");
+    // All of the round's slots have been read before one is written, by any CTA
+    // of the cluster: its barrier orders the reads before the writes.  (A relaxed
+    // one takes 3 us less for the batch above, and only that every word has its
+    // part in `top` would hold the writes back.  Arriving before the maxima are
+    // taken: 122 us, but 20.4 and 251 to 259.)
+    if (C > 1) cluster.sync(); else __syncthreads();
     // the next round's codes on their way to L2
 #pragma unroll
     for (int k = 0; k < kUnits; ++k)

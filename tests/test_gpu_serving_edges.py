@@ -10,8 +10,8 @@ import torch
 from oracle import serving_ops as so
 from oracle import target_ops as to
 from parity import np_
-from test_gpu_serving_ops import (SharedCache, _evict, _i32, _logprobs,
-                                  _mass_args, _share)
+from test_gpu_serving_ops import (SharedCache, _check_evict, _evict, _i32,
+                                  _logprobs, _mass_args, _share)
 from test_gpu_target_ops import DT, U, Cache, _check_attn
 
 pytestmark = pytest.mark.gpu
@@ -248,3 +248,24 @@ def test_eviction_reads_no_pages_of_a_kept_prefix(lib, Hkv, page, shared,
         lib.dflash_check()
     for a, b in zip(*got):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("Hkv,D,page,shift", [(1, 128, 16, 1), (4, 64, 32, 40),
+                                              (2, 16, 128, 300)])
+def test_rounds_of_a_cluster_read_before_they_write(lib, Hkv, D, page, shift):
+    """Every page takes tokens of the next ones, which other CTAs of the
+    cluster write in the same round; many rounds, over and over."""
+    rng = np.random.default_rng(shift)
+    kv = [20000, 9000]
+    cache = Cache(kv, page, Hkv, D, rng, spread=20)
+    mass = np.ones((2, Hkv, kv[0]), np.float32)
+    for b in range(2):
+        mass[b, :, 3 + b:3 + b + shift] = 0
+    budget = kv[1] - shift
+    _check_evict(lib, cache, mass, kv, budget, 0, 0)
+    first = _evict(lib, cache, mass, kv, budget, 0, 0)
+    for _ in range(10):
+        again = _evict(lib, cache, mass, kv, budget, 0, 0)
+        for a, b in zip(again, first):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    lib.dflash_check()
