@@ -1,12 +1,13 @@
 // The attention weight that cached tokens gather, on the tensor cores
 // (tcgen05), for bf16 queries and heads of up to 128 dimensions.
 //
-// The cached codes go from HBM to the MMAs as they are, with q as the sum of
-// two E4M3 numbers side by side in the MMA's N (a row's largest value scaled to
-// [128, 256); the second part holds 2^5 times what the first leaves: all of
-// bf16's bits, down to 2^-17 of that value).  S^T[token, row] = K q^T, so a
-// thread owns a token: its key's scale is one factor, and the sum over the rows
-// is its own.  A row brings its scaling and its logsumexp (in bits).
+// The cached codes go from HBM to the MMAs as they are, with q as the sum of two
+// E4M3 numbers side by side in the MMA's N (a row's largest value scaled to
+// [128, 256); the second part holds 2^5 times what the first leaves, in steps of
+// 2^-14: all of bf16's bits of values from 2^-7 on, 2^-14 of the largest, and
+// smaller ones to 2^-15, 2^-22 of it).  S^T[token, row] = K q^T, so a thread
+// owns a token: its key's scale is one factor, and the sum over the rows is its
+// own.  A row brings its scaling and its logsumexp (in bits).
 //
 // All tiles of 128 tokens of all (sequence, key head) pairs are numbered, and
 // every CTA (one per SM) takes an equal run, counted with the rows that they
@@ -16,12 +17,14 @@
 // atomically.
 //
 // Warps: 0 copies tiles (TMA, one box per page), 1 issues the MMAs, 2 hands out
-// the segments, 4-7 lay out q (two buffers), the others take the tiles'
-// weights: groups of four a tile each by turns, four groups with up to 64 rows
-// (whose scores are 128 columns), else two.  What bounds it: the latencies of a
-// tile's way through TMEM and these warps; HBM at 53 %.  32 sequences of up to
-// 8000 tokens with 36 rows 49 us (4.4 TB/s), 72 rows 73 us; one row of 20000
-// tokens 10.6 us, the chain of one tile.  (Two groups for 36 rows: 59 us.)
+// the segments, 4-7 lay out q (two buffers), the others take the tiles' weights:
+// groups of four a tile each by turns, four groups with up to 64 rows (whose
+// scores are 128 columns), else two.  What bounds it: the latencies of a tile's
+// way through TMEM and these warps; HBM at 54 %.  32 sequences of up to 8000
+// tokens with 36 rows 48 us (4.4 TB/s), 72 rows 73 us; one row of 20000 tokens
+// 10.7 us, the chain of one tile; a prompt of 2048 tokens, four heads to a key
+// head, 320 us (its rows are laid out 128 at a time, for one tile a CTA). (Two
+// groups for 36 rows: 59 us.)
 // Every wait is bounded; on a timeout the CTA stops issuing, drains, frees TMEM
 // and flags the error word.
 #include <cuda_fp8.h>

@@ -494,10 +494,10 @@ __global__ void __launch_bounds__(
       if (lane == 0) sh.exp[kv][warp] = top[kv];
     }
     // All of the round's slots have been read before one is written, by any CTA
-    // of the cluster: its barrier orders the reads before the writes.  (A relaxed
-    // one takes 3 us less for the batch above, and only that every word has its
-    // part in `top` would hold the writes back.  Arriving before the maxima are
-    // taken: 122 us, but 20.4 and 251 to 259.)
+    // of the cluster: its barrier orders the reads before the writes.  (A
+    // relaxed one takes 3 us less for the batch above, and only that every word
+    // has its part in `top` would hold the writes back.  Arriving before the
+    // maxima are taken: 122 us, but 20.4 and 251 to 259.)
     if (C > 1) cluster.sync(); else __syncthreads();
     // the next round's codes on their way to L2
 #pragma unroll

@@ -12,20 +12,21 @@
 // the pass counts: words before the token those above the next smaller number,
 // words after it those above its logit.
 //
-// The K most likely: the K-th largest maximum of 64 groups of threads bounds
-// the K-th largest logit of the slice from below.  Of the threads that reach it
-// most do so with the words of their maximum alone, which they read again; the
-// others have their whole part read again, from L2, a warp at a time for each.
-// The few more than K candidates are ranked by counting.  A cluster of CTAs
-// owns a row; the first of them joins the CTAs' sums and lists.  What overflows
-// the list (ties by the thousand) is found by K searches for the next largest
-// instead.
+// The K most likely: the K-th largest maximum of 64 groups of threads bounds the
+// K-th largest logit of the slice from below.  Of the threads that reach it most
+// do so with the words of their maximum alone, which they read again; the others
+// have their whole part read again, from L2, a warp at a time for each. The few
+// more than K candidates are ranked by counting.  A cluster of CTAs owns a row;
+// the first of them joins the CTAs' sums and lists.  What overflows the list
+// (ties by the thousand, or a row masked by the type's lowest value whose other
+// tokens lie in fewer than K groups: 288 such rows 1140 us, masked by -inf 55)
+// is found by K searches for the next largest instead.
 //
-// What bounds it: in batches instructions (26 a logit, 70 % of the issue slots)
+// What bounds it: in batches instructions (25 a logit, 70 % of the issue slots)
 // and the steps at a row's end; for one row the chain of steps.  288 rows of
-// 151936 fp32 logits 45 us with 20 alternatives, 35 us without (4.9 TB/s), one
-// bf16 row 5.7 us.  (Words on their way through shared memory, four to twelve of
-// a thread in flight instead of two: 49 to 51 us.)
+// 151936 fp32 logits 45 us with 20 alternatives, 35 us without (4.9 TB/s), bf16
+// 38 us, one bf16 row 5.9 us.  (Words on their way through shared memory, four
+// to twelve of a thread in flight instead of two: 49 to 51 us.)
 #include <cooperative_groups.h>
 
 #include <algorithm>

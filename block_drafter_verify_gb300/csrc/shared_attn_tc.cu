@@ -15,8 +15,9 @@
 //   q        is scaled by a power of two for each row, its largest value to
 //            [2^14, 2^15): fp16 then holds all of bf16's bits down to 2^-28 of
 //            that value.
-//   P        fp16: 2^-12 of a weight, or 2^-35 of the row's largest.  The sum
-//            counts weights as they are in fp32.
+//   P        fp16: to 2^-11 of a weight, or 2^-34 of the row's largest
+//            (which is 2^9 or more).  The sum counts weights as they are in
+//            fp32.
 // The page's scales are one factor and one addend of the exponent for 16 columns:
 // weights carry their value's scale, the row's sum is taken without it (see
 // kSumRef).  The running maximum is lazy: weights are taken against a reference

@@ -707,7 +707,8 @@ size_t dflash_shared_attn_workspace_bytes(int B, int Q, int Hq, int Hkv,
  * could pass 2^31 give DFLASH_ERR_UNSUPPORTED.
  * With bf16 and D <= 128 the tensor cores compute: q is taken as fp16 relative
  * to its row's largest value (all of bf16's bits down to 2^-28 of it), a weight
- * times its value as fp16 (2^-12 relative); sums are fp32.
+ * times its value's scale as fp16 (to 2^-11 of itself or 2^-34 of its row's
+ * largest, whichever is more); sums are fp32.
  */
 dflash_status dflash_shared_attn(
     const void* q, const uint8_t* k_codes, const uint8_t* v_codes,
@@ -738,7 +739,8 @@ dflash_status dflash_shared_attn(
  *   mass  [B, Hkv] rows of fp32, ld_mass elements apart, in/out
  * Sums and weights are fp32; their order is fixed, and nothing is added
  * atomically.  (bf16 and D <= 128, the tensor cores: q as two E4M3 numbers, all
- * of bf16's bits down to 2^-17 of its row's largest value; queries below 2^111.)
+ * of bf16's bits down to 2^-14 of its row's largest value, smaller values to
+ * 2^-22 of that; queries below 2^111.)
  * Requirements: as dflash_paged_attn; first >= 0, ld_mass >= 1, decay finite;
  * work that could pass 2^31 tiles of 128 rows times 128 tokens gives
  * DFLASH_ERR_UNSUPPORTED.
